@@ -400,6 +400,17 @@ __device__ __forceinline__ uint32_t e4m3x2(float a, float b) {
   return (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
 }
 
+// The value 2^(byte - 127) of an E8M0 scale (NaN for 0xFF; byte 0 is the
+// subnormal 2^-127).
+__device__ __forceinline__ float e8m0_value(uint32_t sbyte) {
+  return __uint_as_float(sbyte == 0xFFu ? 0x7FFFFFFFu : sbyte == 0u ? 0x00400000u : sbyte << 23);
+}
+// The two E4M3 values of a 16-bit word (low byte first); exact.
+__device__ __forceinline__ float2 e4m3x2_value(uint32_t w) {
+  const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)w, __NV_E4M3);
+  return __half22float2(*reinterpret_cast<const __half2*>(&h));
+}
+
 __device__ __forceinline__ uint32_t pack_bf16x2(float a, float b) {
   const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);  // a -> low half
   return *reinterpret_cast<const uint32_t*>(&h);

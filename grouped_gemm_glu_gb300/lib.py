@@ -57,6 +57,20 @@ def glu_params(act: str = "swiglu", alpha: float = 1.0, up_offset: float = 0.0,
     return GluParams(ACT[act], alpha, up_offset, gate_lo, gate_hi, up_lo, up_hi)
 
 
+class RouterParams(C.Structure):
+    _fields_ = [("score", C.c_int32), ("renorm", C.c_int32), ("n_group", C.c_int32), ("topk_group", C.c_int32),
+                ("group_top", C.c_int32), ("scale", C.c_float)]
+
+
+SCORE = {"softmax": 0, "sigmoid": 1}
+
+
+def router_params(score: str = "softmax", renorm: bool = False, scale: float = 1.0, n_group: int = 1,
+                  topk_group: int = 1, group_top: int = 1) -> RouterParams:
+    """How a router chooses experts (see moe_router_params_t)."""
+    return RouterParams(SCORE[score], int(renorm), n_group, topk_group, group_top, scale)
+
+
 P, I, U64, SZ, F32 = C.c_void_p, C.c_int, C.c_uint64, C.c_size_t, C.c_float
 
 _SIGS = {
@@ -95,6 +109,12 @@ _SIGS = {
     "moe_dglu_act": [P, P, P, P, I, I, I, C.POINTER(GluParams), P, P],
     "moe_route_permute_noalloc": [P, P, P, I, I, I, I, I, I, P, P, P, P, P, P, P, P, P, P],
     "moe_route_noalloc_max_scratch_bytes": ([], SZ),
+    "moe_rmsnorm_fwd": [P, P, P, F32, I, I, P, P, P, P, P, P],
+    "moe_rmsnorm_bwd_workspace_size": ([I, I], SZ),
+    "moe_rmsnorm_bwd": [P, P, P, P, P, I, I, P, P, P, SZ, P],
+    "moe_dequantize_mxfp8": [P, P, SZ, P, P],
+    "moe_router_fwd": [P, I, P, P, I, I, I, C.POINTER(RouterParams), P, P, P, P],
+    "moe_router_bwd": [P, I, P, P, I, I, I, C.POINTER(RouterParams), P, P],
     "moe_get_status": [P, P, P],
     "moe_set_wait_limit_ns": ([U64], None),
     "moe_wait_selftest": [I, P, P, P],

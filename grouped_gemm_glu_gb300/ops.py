@@ -496,3 +496,133 @@ def dglu_act(da, pre, counts, offsets, F: int, params: L.GluParams):
     L.check(lib.moe_dglu_act(_p(da), _p(pre), _p(counts), _p(offsets), counts.shape[0], F, R_cap, C.byref(params),
                              _p(d), _s()), "moe_dglu_act")
     return d
+
+
+def _need(t, dtype, shape, what):
+    """A dense CUDA tensor of this type and shape (None in shape: any), or ValueError."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError(f"{what}: a CUDA tensor is needed")
+    if t.dtype != dtype:
+        raise ValueError(f"{what}: {dtype} is needed, got {t.dtype}")
+    if t.dim() != len(shape) or any(n is not None and n != m for n, m in zip(shape, t.shape)):
+        raise ValueError(f"{what}: shape {tuple(shape)} is needed, got {tuple(t.shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{what}: a contiguous tensor is needed")
+    return t
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+def rmsnorm(x, gamma, eps: float = 1e-5, residual=None, bf16: bool = True, mxfp8: bool = False,
+            with_rstd: bool = True) -> dict:
+    """Residual addition and RMS norm of x [T, H] bf16 with the weight gamma
+    [H]: y = h * rstd * gamma with h = bf16(x + residual).  Returns h (with a
+    residual), y (bf16=True), q [T, H] and s [T, H/32] (mxfp8=True: the
+    row-wise MXFP8 of y, what an MXFP8 FC1 reads) and rstd [T]."""
+    bf = torch.bfloat16
+    _need(x, bf, (None, None), "x")
+    T, H = x.shape
+    _need(gamma, bf, (H,), "gamma")
+    o = {}
+    new, dev = torch.empty, x.device
+    h = y = q = s = r = None
+    if residual is not None:
+        _need(residual, bf, (T, H), "residual")
+        h = o["h"] = torch.empty_like(x)
+    if bf16:
+        y = o["y"] = torch.empty_like(x)
+    if mxfp8:
+        q = o["q"] = new(T, H, dtype=torch.uint8, device=dev)
+        s = o["s"] = new(T, H // 32, dtype=torch.uint8, device=dev)
+    if with_rstd:
+        r = o["rstd"] = new(T, dtype=torch.float32, device=dev)
+    L.check(L.load().moe_rmsnorm_fwd(x.data_ptr(), _ptr(residual), gamma.data_ptr(), eps, T, H, _ptr(h), _ptr(y),
+                                     _ptr(q), _ptr(s), _ptr(r), _s()), "moe_rmsnorm_fwd")
+    return o
+
+
+def rmsnorm_bwd(dy, h, gamma, rstd, dres=None, with_dgamma: bool = True):
+    """Backward of rmsnorm: (dx [T, H] bf16, dgamma [H] f32 or None).  h is the
+    forward's h (its x where there was no residual), dres the gradient that
+    arrives at h from the rest of the residual stream; dx is the gradient of x
+    and of the residual alike."""
+    bf = torch.bfloat16
+    _need(dy, bf, (None, None), "dy")
+    T, H = dy.shape
+    _need(h, bf, (T, H), "h")
+    _need(gamma, bf, (H,), "gamma")
+    _need(rstd, torch.float32, (T,), "rstd")
+    if dres is not None:
+        _need(dres, bf, (T, H), "dres")
+    lib = L.load()
+    dx = torch.empty_like(dy)
+    dgamma = ws = None
+    nbytes = 0
+    if with_dgamma:
+        dgamma = torch.empty(H, dtype=torch.float32, device=dy.device)
+        nbytes = lib.moe_rmsnorm_bwd_workspace_size(T, H)
+        ws = torch.empty(nbytes, dtype=torch.uint8, device=dy.device)
+    L.check(lib.moe_rmsnorm_bwd(dy.data_ptr(), _ptr(dres), h.data_ptr(), gamma.data_ptr(), rstd.data_ptr(), T, H,
+                                dx.data_ptr(), _ptr(dgamma), _ptr(ws), nbytes, _s()), "moe_rmsnorm_bwd")
+    return dx, dgamma
+
+
+def dequantize_mxfp8(q, s, out=None):
+    """The bf16 values of MXFP8 codes q [..., C] with scales s [..., C/32]."""
+    _need(q, torch.uint8, q.shape, "q")
+    if q.shape[-1] % 32:
+        raise ValueError("q: the last dimension must be a multiple of 32")
+    _need(s, torch.uint8, (*q.shape[:-1], q.shape[-1] // 32), "s")
+    o = _need(out, torch.bfloat16, q.shape, "out") if out is not None else torch.empty(
+        q.shape, dtype=torch.bfloat16, device=q.device)
+    L.check(L.load().moe_dequantize_mxfp8(q.data_ptr(), s.data_ptr(), s.numel(), o.data_ptr(), _s()),
+            "moe_dequantize_mxfp8")
+    return o
+
+
+def _logits(logits):
+    if logits.dtype not in (torch.float32, torch.bfloat16):
+        raise ValueError(f"logits: float32 or bfloat16 is needed, got {logits.dtype}")
+    _need(logits, logits.dtype, (None, None), "logits")
+    return int(logits.dtype == torch.bfloat16)
+
+
+def router(logits, k: int, params: L.RouterParams, bias=None, token_mask=None, with_load: bool = True) -> dict:
+    """Expert choice from logits [T, n] (f32 or bf16): idx [T, k] int32 and
+    prob [T, k] f32 (route_permute's topk_idx and topk_prob; slots without an
+    expert hold -1 and 0) and load [n] int32, the tokens of each expert.
+    bias [n] f32 takes part in the choice only; token_mask [T] uint8 or bool:
+    tokens with 0 choose nothing."""
+    b16 = _logits(logits)
+    T, n = logits.shape
+    if bias is not None:
+        _need(bias, torch.float32, (n,), "bias")
+    if token_mask is not None:
+        if token_mask.dtype == torch.bool:
+            token_mask = token_mask.view(torch.uint8)
+        _need(token_mask, torch.uint8, (T,), "token_mask")
+    dev = logits.device
+    o = {"idx": torch.empty(T, k, dtype=torch.int32, device=dev),
+         "prob": torch.empty(T, k, dtype=torch.float32, device=dev)}
+    load = None
+    if with_load:
+        load = o["load"] = torch.empty(n, dtype=torch.int32, device=dev)
+    L.check(L.load().moe_router_fwd(logits.data_ptr(), b16, _ptr(bias), _ptr(token_mask), T, n, k, C.byref(params),
+                                    o["idx"].data_ptr(), o["prob"].data_ptr(), _ptr(load), _s()), "moe_router_fwd")
+    return o
+
+
+def router_bwd(logits, idx, dprob, params: L.RouterParams):
+    """dlogits [T, n] (in the logits' type) from dprob [T, k] f32, the gradient
+    of the weights that router returned with idx [T, k]."""
+    b16 = _logits(logits)
+    T, n = logits.shape
+    _need(idx, torch.int32, (T, None), "idx")
+    k = idx.shape[1]
+    _need(dprob, torch.float32, (T, k), "dprob")
+    d = torch.empty_like(logits)
+    L.check(L.load().moe_router_bwd(logits.data_ptr(), b16, idx.data_ptr(), dprob.data_ptr(), T, n, k,
+                                    C.byref(params), d.data_ptr(), _s()), "moe_router_bwd")
+    return d

@@ -560,6 +560,91 @@ MOE_API moe_status_t moe_dglu_act(const moe_bf16* da, const moe_bf16* pre, const
                                   const int32_t* offsets, int E, int F, int R_cap,
                                   const moe_glu_params_t* params, moe_bf16* dfc1, moe_stream_t stream);
 
+/* ---------------------------------------------------------------------- */
+/* In front of the expert MLP: residual + RMS norm, and the router.         */
+
+/* Residual addition and RMS norm.  Per token of x [T][H] bf16:
+ *   h = bf16(x + residual)   (x itself when residual is NULL)
+ *   r = 1 / sqrt(mean(h^2) + eps),  y = h r gamma        (fp32)
+ * Outputs: h [T][H] bf16 (with a residual, and only then; may be x or
+ * residual itself), y [T][H] bf16 and / or the row-wise MXFP8 of the fp32 y
+ * (q [T][H] E4M3, s [T][H/32] E8M0; both or neither), at least one of the
+ * two forms; rstd [T] f32 = r (nullable; the backward reads it).
+ * gamma [H] bf16.  H % 8 == 0 (H % 32 == 0 with q), H <= 16384 (else
+ * MOE_ERR_UNSUPPORTED); bf16 buffers 16-byte, q 8-byte aligned.  T == 0
+ * launches nothing. */
+MOE_API moe_status_t moe_rmsnorm_fwd(const moe_bf16* x, const moe_bf16* residual, const moe_bf16* gamma, float eps,
+                                     int T, int H, moe_bf16* h, moe_bf16* y, uint8_t* q, uint8_t* s, float* rstd,
+                                     moe_stream_t stream);
+
+/* Bytes of device workspace moe_rmsnorm_bwd needs for dgamma. */
+MOE_API size_t moe_rmsnorm_bwd_workspace_size(int T, int H);
+
+/* Backward of moe_rmsnorm_fwd: dy [T][H] bf16 the gradient at y, dres [T][H]
+ * bf16 (nullable) the gradient arriving at h from the rest of the residual
+ * stream, h (x where there was no residual) and rstd as the forward wrote
+ * them.  With t = dy gamma:
+ *   dx = bf16(rstd (t - h rstd^2 mean(t h)) + dres)  [T][H], the gradient at
+ *        x and at the residual alike (may be dy or dres itself)
+ *   dgamma[c] = sum over tokens of dy h rstd          [H] f32, nullable
+ * dgamma is summed in fp32 in a fixed order (partial lines in ws, then one
+ * ordered sum): the same inputs give the same bits.  ws:
+ * moe_rmsnorm_bwd_workspace_size(T, H) bytes, 16-byte aligned (nullable
+ * without dgamma).  Shapes and alignment as the forward; T == 0 writes
+ * dgamma = 0. */
+MOE_API moe_status_t moe_rmsnorm_bwd(const moe_bf16* dy, const moe_bf16* dres, const moe_bf16* h,
+                                     const moe_bf16* gamma, const float* rstd, int T, int H, moe_bf16* dx,
+                                     float* dgamma, void* ws, size_t ws_bytes, moe_stream_t stream);
+
+/* MXFP8 rows back to values: out = e4m3 * 2^(s - 127) for `blocks` blocks of
+ * 32 consecutive codes (q [32 blocks], s [blocks]), bf16 (exact while the
+ * value is in bf16's range; scale 0xFF gives NaN).  q and out 16-byte
+ * aligned. */
+MOE_API moe_status_t moe_dequantize_mxfp8(const uint8_t* q, const uint8_t* s, size_t blocks, moe_bf16* out,
+                                          moe_stream_t stream);
+
+typedef enum { MOE_SCORE_SOFTMAX = 0, MOE_SCORE_SIGMOID = 1 } moe_score_t;
+
+/* How a router chooses experts ([MegaMoE] 2.1: the top-k experts and their
+ * probabilities). */
+typedef struct {
+  int32_t score;      /* moe_score_t: softmax over the n experts, or a sigmoid of each logit */
+  int32_t renorm;     /* != 0: the weights are divided by their sum over the chosen experts (softmax: the
+                         softmax over the chosen logits; sigmoid: s / (sum s + 1e-20)) */
+  int32_t n_group;    /* the experts form n_group groups of n / n_group neighbours (1: no groups) */
+  int32_t topk_group; /* experts are chosen from the topk_group best groups only */
+  int32_t group_top;  /* a group's score is the sum of its group_top (1 or 2) best keys */
+  float scale;        /* factor on the weights */
+} moe_router_params_t;
+
+/* Expert choice.  logits [T][n], f32 or (logits_bf16 != 0) bf16; bias [n]
+ * f32 (nullable) is added to the scores for the choice only; token_mask [T]
+ * (nullable): a token with mask 0 chooses nothing.
+ * The choice is made on fp32 keys: score + bias with a bias, the logits
+ * themselves without one (the same order); group scores for group_top = 2
+ * without a bias sum the scores.  Ties go to the lowest index, of experts and
+ * of groups.  An expert whose logit (or key) is -inf is never chosen: a slot
+ * that finds no expert gets index -1 and weight 0, which moe_route_permute
+ * drops.  A NaN logit ranks first, so that it shows in the weights; softmax
+ * weights of a row holding NaN or +inf are NaN.
+ * Out: topk_idx [T][k] int32 (best first), topk_prob [T][k] f32 (scale *
+ * weight), load [n] int32 (nullable; the number of tokens that chose each
+ * expert, overwritten): moe_route_permute's inputs.
+ * 1 <= n <= 1024, 1 <= k <= 32, n % n_group == 0, n_group <= 32,
+ * k <= n / n_group * topk_group; else MOE_ERR_ARG. */
+MOE_API moe_status_t moe_router_fwd(const void* logits, int logits_bf16, const float* bias,
+                                    const uint8_t* token_mask, int T, int n, int k,
+                                    const moe_router_params_t* params, int32_t* topk_idx, float* topk_prob,
+                                    int32_t* load, moe_stream_t stream);
+
+/* Gradient of the weights: from dprob [T][k] f32 (moe_combine_bwd's) and the
+ * choice, dlogits [T][n] in the logits' type, every element written.  The
+ * choice itself and the bias carry no gradient; slots with an index outside
+ * [0, n) contribute nothing.  dlogits may not alias logits. */
+MOE_API moe_status_t moe_router_bwd(const void* logits, int logits_bf16, const int32_t* topk_idx,
+                                    const float* dprob, int T, int n, int k, const moe_router_params_t* params,
+                                    void* dlogits, moe_stream_t stream);
+
 /* Copies the device status word to *host_out (synchronises `stream`; not
  * for use inside a graph capture). */
 MOE_API moe_status_t moe_get_status(const int32_t* status, int32_t* host_out, moe_stream_t stream);
