@@ -19,6 +19,16 @@
 // and writes dx (8 bytes per element).  A row is held in registers by its
 // threads (packed bf16) between the reduction and the output, so every byte
 // crosses HBM once.
+//
+// One CTA per SM walks the rows in G groups of wpr warps, one row per group
+// at a time.  A reduction and its barrier stand between a row's loads and its
+// stores, so loads issued row by row leave HBM idle; each thread therefore
+// copies the columns it owns of the next rows into its own slots of shared
+// memory (cp.async, `stages` rows ahead: about 170 KB in flight per SM).  The
+// slots are private to the thread: no barrier guards them.  A call of few
+// rows (at most FEW_ROWS) takes one CTA per row instead, spread over as many
+// warps as it has vectors for, because there one row's latency is the call's
+// time.
 #include "common.cuh"
 #include "host_common.h"
 
@@ -29,6 +39,9 @@ constexpr int MAX_H = 16384;  // 16 warps x 4 vectors of 8 columns a lane
 // threads per CTA: with more than one vector a thread's registers allow 16 warps
 template <int V>
 constexpr int max_threads() { return V == 1 ? 1024 : 512; }
+constexpr int MAX_T = 1 << 30;  // row indexes stay in 32 bits a few grids past the end
+constexpr int FEW_ROWS = 256;
+constexpr int RING_BYTES = 200 * 1024;  // of the 227 KB a CTA may have
 
 __device__ __forceinline__ void unpack8(const uint4 q, float* v) {
   v[0] = bf16_lo(q.x);
@@ -44,170 +57,264 @@ __device__ __forceinline__ uint4 pack8(const float* v) {
   return make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
 }
 
-// Sum over the `wpr` warps of a row (a CTA holds whole rows).  red: one float
-// per warp of the CTA.  Every thread gets the sum, added in the same order.
-__device__ __forceinline__ float row_sum(float v, float* red, int wpr) {
+__device__ __forceinline__ void cp_async16(void* dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// Waits until at most `ahead` (0..3) of the thread's newest groups are in flight.
+__device__ __forceinline__ void cp_async_wait(int ahead) {
+  if (ahead == 0)
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
+  else if (ahead == 1)
+    asm volatile("cp.async.wait_group 1;" ::: "memory");
+  else if (ahead == 2)
+    asm volatile("cp.async.wait_group 2;" ::: "memory");
+  else
+    asm volatile("cp.async.wait_group 3;" ::: "memory");
+}
+
+// A float and the rounding error of the sum it came from.
+struct Pair {
+  float hi, lo;
+};
+__device__ __forceinline__ Pair two_sum(float a, float b) {  // a + b = hi + lo exactly (Knuth)
+  const float s = a + b, bb = s - a;
+  return {s, (a - (s - bb)) + (b - bb)};
+}
+
+// Sum over a group's wpr warps, in the same order for every thread: within a
+// warp in fp32, across warps with the rounding errors kept.  red: two sets
+// of one float per warp of the CTA, used in turn (par), so that one barrier
+// per row is enough: a warp writes a set again only after the barrier of the
+// row between.
+__device__ __forceinline__ Pair row_sum(float v, float* red, int par, int group, int wpr) {
 #pragma unroll
   for (int d = 16; d > 0; d >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, d);
-  if (wpr == 1) return v;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  if (lane == 0) red[warp] = v;
-  __syncthreads();
-  const int first = warp / wpr * wpr;
-  float s = lane < wpr ? red[first + lane] : 0.0f;
+  if (wpr == 1) return {v, 0.0f};
+  const int lane = threadIdx.x & 31;
+  red += par * 32;
+  if (lane == 0) red[threadIdx.x >> 5] = v;
+  asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "r"(32 * wpr) : "memory");
+  Pair s{lane < wpr ? red[group * wpr + lane] : 0.0f, 0.0f};
 #pragma unroll
-  for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, d);
-  __syncthreads();  // red is free again
+  for (int d = 16; d > 0; d >>= 1) {
+    if (d >= 2 * wpr) continue;
+    const float oh = __shfl_xor_sync(0xFFFFFFFFu, s.hi, d), ol = __shfl_xor_sync(0xFFFFFFFFu, s.lo, d);
+    const Pair q = two_sum(s.hi, oh);
+    s = {q.hi, q.lo + (s.lo + ol)};
+  }
+  // lanes past the last warp's hold other sums when 2 wpr is not above 31
+  s.hi = __shfl_sync(0xFFFFFFFFu, s.hi, 0);
+  s.lo = __shfl_sync(0xFFFFFFFFu, s.lo, 0);
   return s;
 }
 
-// V: 16-byte vectors of a row per thread.  A row belongs to wpr warps, a CTA
-// to blockDim / (32 wpr) rows; vector j of a thread is column group
-// t + j * 32 wpr of the row.
+// 1 / sqrt(ss / n + eps) as hi + lo, good to about 2^-30: the quantised
+// outputs round y on a coarse grid, where an error of y of one fp32 step
+// already moves some value of a large batch across a rounding boundary.
+__device__ __forceinline__ Pair inv_rms(Pair ss, float n, float eps) {
+  const float q = ss.hi / n;
+  const float q_lo = (fmaf(-q, n, ss.hi) + ss.lo) / n;
+  Pair w = two_sum(q, eps);
+  w.lo += q_lo;
+  const float r = 1.0f / sqrtf(w.hi);
+  const float a = w.hi * r;                       // Newton: r (1 + e / 2), e = 1 - w r^2
+  const float a_lo = fmaf(w.hi, r, -a);
+  const float e = fmaf(-a, r, 1.0f) - fmaf(w.lo, r, a_lo) * r;
+  return {r, fabsf(e) < 1e-3f ? 0.5f * r * e : 0.0f};  // (no correction for 0, Inf, NaN)
+}
+
+// V: 16-byte vectors of a row per thread; vector j of a thread is column
+// group t + j * 32 wpr of the row.
 template <int V>
-__global__ void __launch_bounds__(max_threads<V>()) k_rmsnorm_fwd(const uint4* __restrict__ x, const uint4* __restrict__ res,
-                              const uint4* __restrict__ gamma, float eps, int T, int H8, int wpr,
-                              uint4* __restrict__ h_out, uint4* __restrict__ y, uint8_t* __restrict__ q,
-                              uint8_t* __restrict__ s, float* __restrict__ rstd) {
-  __shared__ float red[32];
-  const int tpr = 32 * wpr, t = threadIdx.x % tpr, rows = blockDim.x / tpr;
-  const int row = blockIdx.x * rows + threadIdx.x / tpr;
-  const bool on = row < T;
-  const size_t base = (size_t)row * H8;
-  uint4 hv[V];
-  float ss = 0.0f;
+__global__ void __launch_bounds__(max_threads<V>()) k_rmsnorm_fwd(
+    const uint4* __restrict__ x, const uint4* __restrict__ res, const uint4* __restrict__ gamma, float eps, int T,
+    int H8, int wpr, int groups, int stages, uint4* __restrict__ h_out, uint4* __restrict__ y, uint8_t* __restrict__ q,
+    uint8_t* __restrict__ s, float* __restrict__ rstd) {
+  extern __shared__ __align__(16) uint4 ring[];  // [stages][inputs][V][threads]
+  __shared__ float red[64];
+  const int tpr = 32 * wpr, group = threadIdx.x / tpr, t = threadIdx.x - group * tpr;
+  const int nin = res != nullptr ? 2 : 1, nthr = blockDim.x;
+  const int slot0 = blockIdx.x * groups + group, slots = gridDim.x * groups;
+  auto fetch = [&](int row, int stage) {  // always one group, so that the counts of groups match
+    if (row < T) {
+      const size_t base = (size_t)row * H8;
+      uint4* d = ring + (size_t)stage * nin * V * nthr + threadIdx.x;
 #pragma unroll
-  for (int j = 0; j < V; ++j) {
-    const int c = t + j * tpr;
-    hv[j] = make_uint4(0, 0, 0, 0);
-    if (on && c < H8) {
-      hv[j] = __ldg(x + base + c);
-      if (res != nullptr) {
-        float a[8], b[8];
-        unpack8(hv[j], a);
-        unpack8(__ldg(res + base + c), b);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) a[i] += b[i];
-        hv[j] = pack8(a);
-        h_out[base + c] = hv[j];
+      for (int j = 0; j < V; ++j) {
+        const int c = t + j * tpr;
+        if (c < H8) {
+          cp_async16(d + j * nthr, x + base + c);
+          if (nin == 2) cp_async16(d + (V + j) * nthr, res + base + c);
+        }
       }
     }
-    float v[8];
-    unpack8(hv[j], v);
+    cp_async_commit();
+  };
+  uint4 gm[V];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) ss = fmaf(v[i], v[i], ss);
-  }
-  ss = row_sum(ss, red, wpr);
-  const float r = 1.0f / sqrtf(ss / (float)(8 * H8) + eps);
-  if (on && rstd != nullptr && t == 0) rstd[row] = r;
+  for (int j = 0; j < V; ++j) gm[j] = t + j * tpr < H8 ? __ldg(gamma + t + j * tpr) : make_uint4(0, 0, 0, 0);
+  for (int st = 0; st < stages; ++st) fetch(slot0 + st * slots, st);
+  int stage = 0, par = 0;
+  for (int row = slot0; row < T; row += slots) {
+    const size_t base = (size_t)row * H8;
+    cp_async_wait(stages - 1);
+    const uint4* d = ring + (size_t)stage * nin * V * nthr + threadIdx.x;
+    uint4 hv[V];
+    float ss = 0.0f;
 #pragma unroll
-  for (int j = 0; j < V; ++j) {
-    const int c = t + j * tpr;
-    const bool in = on && c < H8;
-    float v[8], g[8];
-    unpack8(hv[j], v);
-    unpack8(in ? __ldg(gamma + c) : make_uint4(0, 0, 0, 0), g);
+    for (int j = 0; j < V; ++j) {
+      const int c = t + j * tpr;
+      hv[j] = make_uint4(0, 0, 0, 0);
+      if (c < H8) {
+        hv[j] = d[j * nthr];
+        if (nin == 2) {
+          float a[8], b[8];
+          unpack8(hv[j], a);
+          unpack8(d[(V + j) * nthr], b);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = v[i] * r * g[i];
-    if (in && y != nullptr) y[base + c] = pack8(v);
-    if (q != nullptr) {
-      // a 32-column block is four consecutive lanes (H % 32 == 0: all four are in range, or none)
-      uint32_t m = 0;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) m = max(m, abs_bits(v[i]));
-      m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
-      m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
-      const uint32_t sb = e8m0_from_amax_bits(m);
-      uint2 code = make_uint2(0x7F7F7F7Fu, 0x7F7F7F7Fu);
-      if (sb != 0xFFu) {
-        const float inv = mx_inv_scale(sb);
-        code.x = e4m3x2(v[0] * inv, v[1] * inv) | (e4m3x2(v[2] * inv, v[3] * inv) << 16);
-        code.y = e4m3x2(v[4] * inv, v[5] * inv) | (e4m3x2(v[6] * inv, v[7] * inv) << 16);
+          for (int i = 0; i < 8; ++i) a[i] += b[i];
+          hv[j] = pack8(a);
+          h_out[base + c] = hv[j];
+        }
       }
-      if (in) {
-        reinterpret_cast<uint2*>(q)[base + c] = code;
-        if ((c & 3) == 0) s[(base + c) >> 2] = (uint8_t)sb;
+      float v[8];
+      unpack8(hv[j], v);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) ss = fmaf(v[i], v[i], ss);
+    }
+    const Pair sum = row_sum(ss, red, par, group, wpr);  // (the row's slots have been read)
+    fetch(row + stages * slots, stage);
+    if (++stage == stages) stage = 0;
+    par ^= 1;
+    const Pair r = inv_rms(sum, (float)(8 * H8), eps);
+    if (rstd != nullptr && t == 0) rstd[row] = r.hi + r.lo;
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      const int c = t + j * tpr;
+      const bool in = c < H8;
+      float v[8], g[8];
+      unpack8(hv[j], v);
+      unpack8(gm[j], g);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float p = v[i] * g[i];  // exact: two 8-bit significands
+        v[i] = fmaf(p, r.hi, p * r.lo);
+      }
+      if (in && y != nullptr) y[base + c] = pack8(v);
+      if (q != nullptr) {
+        // a 32-column block is four consecutive lanes (H % 32 == 0: all four are in range, or none)
+        uint32_t m = 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) m = max(m, abs_bits(v[i]));
+        m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
+        m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
+        const uint32_t sb = e8m0_from_amax_bits(m);
+        uint2 code = make_uint2(0x7F7F7F7Fu, 0x7F7F7F7Fu);
+        if (sb != 0xFFu) {
+          const float inv = mx_inv_scale(sb);
+          code.x = e4m3x2(v[0] * inv, v[1] * inv) | (e4m3x2(v[2] * inv, v[3] * inv) << 16);
+          code.y = e4m3x2(v[4] * inv, v[5] * inv) | (e4m3x2(v[6] * inv, v[7] * inv) << 16);
+        }
+        if (in) {
+          reinterpret_cast<uint2*>(q)[base + c] = code;
+          if ((c & 3) == 0) s[(base + c) >> 2] = (uint8_t)sb;
+        }
       }
     }
   }
 }
 
-// Backward.  A CTA walks rows blockIdx.x * rows + ..., and every thread keeps
-// the dgamma sums of its own columns over the rows it sees (fp32, in row
-// order); they leave as one line per row slot of the CTA, part[slot][H], and
-// k_dgamma_sum adds the lines in slot order: the result does not depend on
-// timing.
+// Backward.  Every thread keeps the dgamma sums of its own columns over the
+// rows it sees (fp32, in row order); they leave as one line per group,
+// part[slot][H], and k_dgamma_sum adds the lines in slot order: the result
+// does not depend on timing.
 template <int V>
-__global__ void __launch_bounds__(max_threads<V>()) k_rmsnorm_bwd(const uint4* __restrict__ dy, const uint4* __restrict__ dres,
-                              const uint4* __restrict__ h, const uint4* __restrict__ gamma,
-                              const float* __restrict__ rstd, int T, int H8, int wpr, uint4* __restrict__ dx,
-                              float* __restrict__ part) {
-  __shared__ float red[32];
-  const int tpr = 32 * wpr, t = threadIdx.x % tpr, rows = blockDim.x / tpr;
-  const int slot = blockIdx.x * rows + threadIdx.x / tpr, slots = gridDim.x * rows;
+__global__ void __launch_bounds__(max_threads<V>()) k_rmsnorm_bwd(
+    const uint4* __restrict__ dy, const uint4* __restrict__ dres, const uint4* __restrict__ h,
+    const uint4* __restrict__ gamma, const float* __restrict__ rstd, int T, int H8, int wpr, int groups, int stages,
+    uint4* __restrict__ dx, float* __restrict__ part) {
+  extern __shared__ __align__(16) uint4 ring[];  // [stages][inputs][V][threads]
+  __shared__ float red[64];
+  const int tpr = 32 * wpr, group = threadIdx.x / tpr, t = threadIdx.x - group * tpr;
+  const int nin = dres != nullptr ? 3 : 2, nthr = blockDim.x;
+  const int slot0 = blockIdx.x * groups + group, slots = gridDim.x * groups;
   const float inv_h = 1.0f / (float)(8 * H8);
+  auto fetch = [&](int row, int stage) {
+    if (row < T) {
+      const size_t base = (size_t)row * H8;
+      uint4* d = ring + (size_t)stage * nin * V * nthr + threadIdx.x;
+#pragma unroll
+      for (int j = 0; j < V; ++j) {
+        const int c = t + j * tpr;
+        if (c < H8) {
+          cp_async16(d + j * nthr, dy + base + c);
+          cp_async16(d + (V + j) * nthr, h + base + c);
+          if (nin == 3) cp_async16(d + (2 * V + j) * nthr, dres + base + c);
+        }
+      }
+    }
+    cp_async_commit();
+  };
   float acc[V][8];
 #pragma unroll
   for (int j = 0; j < V; ++j)
 #pragma unroll
     for (int i = 0; i < 8; ++i) acc[j][i] = 0.0f;
-  const int steps = (T + slots - 1) / slots;  // the same for every thread: the row sum has barriers
-  for (int st = 0; st < steps; ++st) {
-    const int row = slot + st * slots;
-    const bool on = row < T;
+  for (int st = 0; st < stages; ++st) fetch(slot0 + st * slots, st);
+  int stage = 0, par = 0;
+  float r = slot0 < T ? __ldg(rstd + slot0) : 0.0f;
+  for (int row = slot0; row < T; row += slots) {
     const size_t base = (size_t)row * H8;
-    uint4 dv[V], hv[V];
+    const float r_next = row + slots < T ? __ldg(rstd + row + slots) : 0.0f;
+    cp_async_wait(stages - 1);
+    const uint4* b = ring + (size_t)stage * nin * V * nthr + threadIdx.x;
+    uint4 dv[V], hv[V], ev[V];
     float dot = 0.0f;
-    const float r = on ? __ldg(rstd + row) : 0.0f;
 #pragma unroll
     for (int j = 0; j < V; ++j) {
       const int c = t + j * tpr;
-      dv[j] = hv[j] = make_uint4(0, 0, 0, 0);
-      if (on && c < H8) {
-        dv[j] = __ldg(dy + base + c);
-        hv[j] = __ldg(h + base + c);
-      }
-    }
-#pragma unroll
-    for (int j = 0; j < V; ++j) {
-      const int c = t + j * tpr;
+      dv[j] = hv[j] = ev[j] = make_uint4(0, 0, 0, 0);
+      if (c >= H8) continue;
+      dv[j] = b[j * nthr];
+      hv[j] = b[(V + j) * nthr];
+      if (nin == 3) ev[j] = b[(2 * V + j) * nthr];
       float d[8], v[8], g[8];
       unpack8(dv[j], d);
       unpack8(hv[j], v);
-      unpack8(c < H8 ? __ldg(gamma + c) : make_uint4(0, 0, 0, 0), g);
+      unpack8(__ldg(gamma + c), g);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         dot = fmaf(d[i] * g[i], v[i], dot);
         acc[j][i] = fmaf(d[i], v[i] * r, acc[j][i]);
       }
     }
-    dot = row_sum(dot, red, wpr);
+    dot = row_sum(dot, red, par, group, wpr).hi;
+    fetch(row + stages * slots, stage);
+    if (++stage == stages) stage = 0;
+    par ^= 1;
     const float k = r * r * (dot * inv_h);
 #pragma unroll
     for (int j = 0; j < V; ++j) {
       const int c = t + j * tpr;
-      if (!on || c >= H8) continue;
-      float d[8], v[8], g[8], o[8];
+      if (c >= H8) continue;
+      float d[8], v[8], g[8], e[8], o[8];
       unpack8(dv[j], d);
       unpack8(hv[j], v);
+      unpack8(ev[j], e);
       unpack8(__ldg(gamma + c), g);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) o[i] = r * (d[i] * g[i] - v[i] * k);
-      if (dres != nullptr) {
-        float e[8];
-        unpack8(__ldg(dres + base + c), e);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) o[i] += e[i];
-      }
+      for (int i = 0; i < 8; ++i) o[i] = fmaf(r, fmaf(-v[i], k, d[i] * g[i]), e[i]);
       dx[base + c] = pack8(o);
     }
+    r = r_next;
   }
   if (part != nullptr) {
 #pragma unroll
     for (int j = 0; j < V; ++j) {
       const int c = t + j * tpr;
       if (c >= H8) continue;
-      float4* d = reinterpret_cast<float4*>(part + (size_t)slot * H8 * 8) + 2 * c;
+      float4* d = reinterpret_cast<float4*>(part + (size_t)slot0 * H8 * 8) + 2 * c;
       d[0] = make_float4(acc[j][0], acc[j][1], acc[j][2], acc[j][3]);
       d[1] = make_float4(acc[j][4], acc[j][5], acc[j][6], acc[j][7]);
     }
@@ -223,6 +330,7 @@ __global__ void __launch_bounds__(256) k_dgamma_sum(const float* __restrict__ pa
   const int c = blockIdx.x * 32 + lane;
   float a = 0.0f;
   if (c < H)
+#pragma unroll 8
     for (int sl = warp; sl < slots; sl += 8) a += __ldg(part + (size_t)sl * H + c);
   sm[warp][lane] = a;
   __syncthreads();
@@ -258,35 +366,34 @@ __global__ void __launch_bounds__(256) k_dequant_mxfp8(const uint4* __restrict__
   }
 }
 
-// How a row is split: V vectors per thread and wpr warps per row.  Rows wide
-// enough take four vectors per thread, so that a thread has four 16-byte
-// loads of each input in flight; a call of few rows spreads each over as many
-// warps as it has vectors for, because then one row's latency is the call's
-// time.
-constexpr int FEW_ROWS = 256;
+// How the rows are laid over the GPU (see the head of the file).
 struct Split {
-  int V, wpr, threads, rows;  // rows per CTA
+  int V, wpr, groups, threads;
 };
 static Split split(int H8, int T) {
   const int lanes = (H8 + 31) / 32;  // warps needed at one vector per thread (<= 64)
   Split p{};
-  p.V = T <= FEW_ROWS ? (lanes > 32 ? 4 : 1) : lanes >= 8 ? 4 : lanes >= 4 ? 2 : 1;
-  const int need = (lanes + p.V - 1) / p.V;
-  p.wpr = 1;
-  while (p.wpr < need) p.wpr *= 2;
-  p.threads = p.wpr >= 8 ? 32 * p.wpr : 256;
-  p.rows = p.threads / (32 * p.wpr);
+  const bool few = T <= FEW_ROWS;
+  // four vectors of each input per thread where the row is wide enough for two warps of them
+  p.V = few ? (lanes > 32 ? 4 : 1) : lanes >= 8 ? 4 : lanes >= 4 ? 2 : 1;
+  p.wpr = (lanes + p.V - 1) / p.V;
+  p.groups = few ? 1 : 16 / p.wpr;
+  if (p.wpr > 1 && p.groups > 15) p.groups = 15;  // one named barrier per group
+  p.threads = 32 * p.wpr * p.groups;
   return p;
 }
+static int ring_stage(const Split& p, int inputs) { return inputs * p.V * p.threads * 16; }
+static int ring_stages(const Split& p, int inputs, int T) {
+  if (T <= FEW_ROWS) return 1;
+  const int n = RING_BYTES / ring_stage(p, inputs);
+  return n < 1 ? 1 : n > 4 ? 4 : n;
+}
 
-// CTAs of the backward: a few per SM, so that each walks many rows and the
-// partial sums stay a small share of the traffic; never more than BWD_CTAS
-constexpr int BWD_CTAS = 1024;
-static int bwd_ctas(int T, int sms, const Split& p) {
-  const int need = (T + p.rows - 1) / p.rows;
-  int c = sms * (p.threads > 256 ? 2 : 4);
-  if (c > BWD_CTAS) c = BWD_CTAS;
-  return need < c ? need : c;
+constexpr int SM_BOUND = 256;  // workspace bound: one CTA per SM of the largest device
+static int ctas(int T, int sms, const Split& p) {
+  const int need = (T + p.groups - 1) / p.groups;
+  const int most = T <= FEW_ROWS ? FEW_ROWS : sms < SM_BOUND ? sms : SM_BOUND;
+  return need < most ? need : most;
 }
 
 }  // namespace norm
@@ -298,7 +405,7 @@ extern "C" moe_status_t moe_rmsnorm_fwd(const moe_bf16* x, const moe_bf16* resid
                                         int T, int H, moe_bf16* h, moe_bf16* y, uint8_t* q, uint8_t* s, float* rstd,
                                         moe_stream_t stream) {
   using namespace norm;
-  if (T < 0 || H <= 0 || (H & 7) || !(eps >= 0.0f)) return MOE_ERR_ARG;
+  if (T < 0 || T > MAX_T || H <= 0 || (H & 7) || !(eps >= 0.0f)) return MOE_ERR_ARG;
   if (T == 0) return MOE_OK;
   if (!x || !gamma || (residual != nullptr) != (h != nullptr) || (q == nullptr) != (s == nullptr)) return MOE_ERR_ARG;
   if (!y && !q) return MOE_ERR_ARG;
@@ -307,39 +414,36 @@ extern "C" moe_status_t moe_rmsnorm_fwd(const moe_bf16* x, const moe_bf16* resid
   if (!aligned16(x) || !aligned16(gamma) || (residual && (!aligned16(residual) || !aligned16(h))) ||
       (y && !aligned16(y)) || (q && (reinterpret_cast<uintptr_t>(q) & 7)))
     return MOE_ERR_ARG;
-  const int H8 = H / 8;
+  const int sms = sm_count();
+  if (sms <= 0) return MOE_ERR_CUDA;
+  const int H8 = H / 8, inputs = residual ? 2 : 1;
   const Split p = split(H8, T);
-  const int grid = (T + p.rows - 1) / p.rows;
+  const int stages = ring_stages(p, inputs, T), smem = stages * ring_stage(p, inputs);
   auto run = [&](auto kernel) {
-    kernel<<<grid, p.threads, 0, as_stream(stream)>>>(
+    if (!set_smem_limit((const void*)kernel, RING_BYTES)) return MOE_ERR_CUDA;
+    kernel<<<ctas(T, sms, p), p.threads, smem, as_stream(stream)>>>(
         reinterpret_cast<const uint4*>(x), reinterpret_cast<const uint4*>(residual),
-        reinterpret_cast<const uint4*>(gamma), eps, T, H8, p.wpr, reinterpret_cast<uint4*>(h),
+        reinterpret_cast<const uint4*>(gamma), eps, T, H8, p.wpr, p.groups, stages, reinterpret_cast<uint4*>(h),
         reinterpret_cast<uint4*>(y), q, s, rstd);
+    count_launch();
+    return launch_status();
   };
-  if (p.V == 1)
-    run(k_rmsnorm_fwd<1>);
-  else if (p.V == 2)
-    run(k_rmsnorm_fwd<2>);
-  else
-    run(k_rmsnorm_fwd<4>);
-  count_launch();
-  return launch_status();
+  return p.V == 1 ? run(k_rmsnorm_fwd<1>) : p.V == 2 ? run(k_rmsnorm_fwd<2>) : run(k_rmsnorm_fwd<4>);
 }
 
 extern "C" size_t moe_rmsnorm_bwd_workspace_size(int T, int H) {
   using namespace norm;
   if (T <= 0 || H <= 0 || (H & 7) || H > MAX_H) return 0;
-  // one line of dgamma sums per row slot of the largest grid
+  // one line of dgamma sums per row group of the largest grid
   const Split p = split(H / 8, T);
-  const int need = (T + p.rows - 1) / p.rows;
-  return (size_t)(need < BWD_CTAS ? need : BWD_CTAS) * p.rows * (size_t)H * sizeof(float);
+  return (size_t)ctas(T, SM_BOUND, p) * p.groups * (size_t)H * sizeof(float);
 }
 
 extern "C" moe_status_t moe_rmsnorm_bwd(const moe_bf16* dy, const moe_bf16* dres, const moe_bf16* h,
                                         const moe_bf16* gamma, const float* rstd, int T, int H, moe_bf16* dx,
                                         float* dgamma, void* ws, size_t ws_bytes, moe_stream_t stream) {
   using namespace norm;
-  if (T < 0 || H <= 0 || (H & 7)) return MOE_ERR_ARG;
+  if (T < 0 || T > MAX_T || H <= 0 || (H & 7)) return MOE_ERR_ARG;
   if (T == 0) {
     if (dgamma && cudaMemsetAsync(dgamma, 0, (size_t)H * sizeof(float), as_stream(stream)) != cudaSuccess)
       return MOE_ERR_CUDA;
@@ -352,26 +456,24 @@ extern "C" moe_status_t moe_rmsnorm_bwd(const moe_bf16* dy, const moe_bf16* dres
   if (dgamma && (!ws || !aligned16(ws) || ws_bytes < moe_rmsnorm_bwd_workspace_size(T, H))) return MOE_ERR_ARG;
   const int sms = sm_count();
   if (sms <= 0) return MOE_ERR_CUDA;
-  const int H8 = H / 8;
+  const int H8 = H / 8, inputs = dres ? 3 : 2;
   const Split p = split(H8, T);
-  const int ctas = bwd_ctas(T, sms, p);
+  const int grid = ctas(T, sms, p);
+  const int stages = ring_stages(p, inputs, T), smem = stages * ring_stage(p, inputs);
   float* part = dgamma ? static_cast<float*>(ws) : nullptr;
   auto run = [&](auto kernel) {
-    kernel<<<ctas, p.threads, 0, as_stream(stream)>>>(
+    if (!set_smem_limit((const void*)kernel, RING_BYTES)) return MOE_ERR_CUDA;
+    kernel<<<grid, p.threads, smem, as_stream(stream)>>>(
         reinterpret_cast<const uint4*>(dy), reinterpret_cast<const uint4*>(dres), reinterpret_cast<const uint4*>(h),
-        reinterpret_cast<const uint4*>(gamma), rstd, T, H8, p.wpr, reinterpret_cast<uint4*>(dx), part);
-  };
-  if (p.V == 1)
-    run(k_rmsnorm_bwd<1>);
-  else if (p.V == 2)
-    run(k_rmsnorm_bwd<2>);
-  else
-    run(k_rmsnorm_bwd<4>);
-  count_launch();
-  if (dgamma) {
-    k_dgamma_sum<<<(H + 31) / 32, 256, 0, as_stream(stream)>>>(part, ctas * p.rows, H, dgamma);
+        reinterpret_cast<const uint4*>(gamma), rstd, T, H8, p.wpr, p.groups, stages, reinterpret_cast<uint4*>(dx),
+        part);
     count_launch();
-  }
+    return launch_status();
+  };
+  const moe_status_t rc = p.V == 1 ? run(k_rmsnorm_bwd<1>) : p.V == 2 ? run(k_rmsnorm_bwd<2>) : run(k_rmsnorm_bwd<4>);
+  if (rc != MOE_OK || !dgamma) return rc;
+  k_dgamma_sum<<<(H + 31) / 32, 256, 0, as_stream(stream)>>>(part, grid * p.groups, H, dgamma);
+  count_launch();
   return launch_status();
 }
 

@@ -10,15 +10,19 @@
 //   the k largest keys, ties to the lowest index; weight = the score,
 //   renormalised over the chosen experts if asked, times scale
 //
-// One warp per token, lane l holding experts l, l + 32, ...: keys are the
-// floats' bits mapped to unsigned integers of the same order, so that a
-// round of the choice is a max over the lane's registers and two warp
-// reductions (redux.sync): the largest key, then the lowest index that has
-// it.  An expert with a logit (or bias) of -inf is never chosen.
+// One warp per token; lane l holds the VL neighbouring experts l VL .. l VL +
+// VL - 1 (VL = 1, 2, 4, ... with 32 VL >= n), so that a row is read in one or
+// two vector loads per lane, a group of experts is a run of lanes whose best
+// keys meet in a few shuffles, and the lowest lane among equal keys holds the
+// lowest index.  Keys are the floats' bits mapped to unsigned integers of the
+// same order: a round of the choice is one warp reduction (redux.sync) and a
+// ballot; the lane that held the best key drops it and looks for its next.
+// Lane j then computes the weight of the j-th expert from its logit.  An
+// expert with a logit (or bias) of -inf is never chosen.
 //
 // Memory: each logit is read once (4 or 2 bytes), 8 bytes leave per chosen
-// expert.  A batch of 8192 x 256 fp32 logits is 8.4 MB, so the instructions
-// of the k rounds bound the kernel, not HBM.
+// expert; at 8192 x 256 that is 1.3 us of HBM time, so the instructions of
+// the scores and the k rounds bound the kernel.
 #include <type_traits>
 
 #include "common.cuh"
@@ -47,9 +51,67 @@ __device__ __forceinline__ float key_value(uint32_t k) {
   return __uint_as_float((k & 0x80000000u) ? (k ^ 0x80000000u) : ~k);
 }
 
-__device__ __forceinline__ float load_logit(const void* p, size_t i, int bf16) {
-  return bf16 ? __uint_as_float((uint32_t)__ldg(static_cast<const uint16_t*>(p) + i) << 16)
+template <bool BF16>
+__device__ __forceinline__ float load_logit(const void* p, size_t i) {
+  return BF16 ? __uint_as_float((uint32_t)__ldg(static_cast<const uint16_t*>(p) + i) << 16)
               : __ldg(static_cast<const float*>(p) + i);
+}
+
+// The lane's VL logits of row t, -inf past n.  vec: rows start on the
+// alignment of one lane's vector, and n is a multiple of VL.
+template <int VL, bool BF16>
+__device__ __forceinline__ void load_row(const void* p, size_t t, int n, int lane, bool vec, float* x) {
+  const int e0 = lane * VL;
+  if (vec) {
+#pragma unroll
+    for (int i = 0; i < VL; ++i) x[i] = -INFINITY;
+    if (e0 >= n) return;
+    if (BF16) {
+      const uint16_t* s = static_cast<const uint16_t*>(p) + t * n + e0;
+      if (VL == 1) {
+        x[0] = __uint_as_float((uint32_t)__ldg(s) << 16);
+      } else if (VL == 2) {
+        const uint32_t w = __ldg(reinterpret_cast<const uint32_t*>(s));
+        x[0] = bf16_lo(w);
+        x[VL - 1] = bf16_hi(w);
+      } else if (VL == 4) {
+        const uint2 w = __ldg(reinterpret_cast<const uint2*>(s));
+        x[0] = bf16_lo(w.x);
+        x[1 % VL] = bf16_hi(w.x);
+        x[2 % VL] = bf16_lo(w.y);
+        x[3 % VL] = bf16_hi(w.y);
+      } else {
+#pragma unroll
+        for (int c = 0; c < VL / 8; ++c) {
+          const uint4 w = __ldg(reinterpret_cast<const uint4*>(s) + c);
+          const uint32_t v[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+          for (int i = 0; i < 8; ++i) x[(8 * c + i) % VL] = (i & 1) ? bf16_hi(v[i / 2]) : bf16_lo(v[i / 2]);
+        }
+      }
+    } else {
+      const float* s = static_cast<const float*>(p) + t * n + e0;
+      if (VL == 1) {
+        x[0] = __ldg(s);
+      } else if (VL == 2) {
+        const float2 w = __ldg(reinterpret_cast<const float2*>(s));
+        x[0] = w.x;
+        x[VL - 1] = w.y;
+      } else {
+#pragma unroll
+        for (int c = 0; c < VL / 4; ++c) {
+          const float4 w = __ldg(reinterpret_cast<const float4*>(s) + c);
+          x[(4 * c) % VL] = w.x;
+          x[(4 * c + 1) % VL] = w.y;
+          x[(4 * c + 2) % VL] = w.z;
+          x[(4 * c + 3) % VL] = w.w;
+        }
+      }
+    }
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < VL; ++i) x[i] = e0 + i < n ? load_logit<BF16>(p, t * n + e0 + i) : -INFINITY;
 }
 
 __device__ __forceinline__ float warp_sum(float v) {
@@ -63,163 +125,229 @@ __device__ __forceinline__ float warp_max(float v) {
   return v;
 }
 
-// Scores of the lane's VL logits (x, -inf past n), and for softmax the row's
-// sums; every form rounds as the formula written out in fp32 does.
+// Each rounds as the formula 1 / (1 + exp(-x)) in fp32 does (a correctly
+// rounded reciprocal is the quotient of 1).
+__device__ __forceinline__ float sigmoid(float x) { return __frcp_rn(1.0f + expf(-x)); }
+
+// Softmax of the row: its largest logit (0 for a row without experts) and
+// the sum of the exponentials; a score is expf(x - m) / d.
+struct Soft {
+  float m, d;
+};
 template <int VL>
-__device__ __forceinline__ void scores(const float* x, int score, float* s) {
-  if (score == MOE_SCORE_SIGMOID) {
-#pragma unroll
-    for (int i = 0; i < VL; ++i) s[i] = 1.0f / (1.0f + expf(-x[i]));
-    return;
-  }
+__device__ __forceinline__ Soft softmax_of(const float* x) {
   float m = x[0];
 #pragma unroll
   for (int i = 1; i < VL; ++i) m = fmaxf(m, x[i]);
   m = warp_max(m);
-  if (m == -INFINITY) m = 0.0f;  // a row without experts: every score is 0
+  if (m == -INFINITY) m = 0.0f;
   float sum = 0.0f;
 #pragma unroll
-  for (int i = 0; i < VL; ++i) {
-    s[i] = expf(x[i] - m);
-    sum += s[i];
-  }
+  for (int i = 0; i < VL; ++i) sum += expf(x[i] - m);
   sum = warp_sum(sum);
-  const float d = fmaxf(sum, 1e-38f);
-#pragma unroll
-  for (int i = 0; i < VL; ++i) s[i] = sum != sum ? sum : s[i] / d;
+  return {m, sum != sum ? sum : fmaxf(sum, 1e-38f)};
 }
+__device__ __forceinline__ float soft_score(const Soft& s, float x) { return expf(x - s.m) / s.d; }
 
-template <int VL>
-__global__ void __launch_bounds__(32 * WARPS) k_router_fwd(const void* __restrict__ logits, int bf16,
+template <int VL, bool BF16>
+__global__ void __launch_bounds__(32 * WARPS) k_router_fwd(const void* __restrict__ logits, int vec,
                                                            const float* __restrict__ bias,
                                                            const uint8_t* __restrict__ mask, int T, const Params p,
                                                            int32_t* __restrict__ idx, float* __restrict__ prob,
                                                            int32_t* __restrict__ load) {
-  extern __shared__ int32_t hist[];  // [n] when load is counted
+  extern __shared__ int32_t hist[];           // [n] when load is counted
+  __shared__ int32_t chosen[WARPS][K_MAX];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int n = p.n, e0 = lane * VL;
   if (load != nullptr) {
-    for (int e = threadIdx.x; e < p.n; e += blockDim.x) hist[e] = 0;
+    for (int e = threadIdx.x; e < n; e += blockDim.x) hist[e] = 0;
     __syncthreads();
   }
-  const int n = p.n;
+  const bool sig = p.score == MOE_SCORE_SIGMOID;
+  // scores of all experts are needed for a bias and for sums of group scores only
+  const bool by_score = bias != nullptr || (p.G > 1 && p.gtop > 1);
+  // groups that are whole runs of 2^j lanes
+  const int gs = n / p.G, seg = gs / VL;
+  const bool runs = gs % VL == 0 && (seg & (seg - 1)) == 0 && p.G * seg <= 32;
   for (int t = blockIdx.x * WARPS + warp; t < T; t += gridDim.x * WARPS) {
-    const bool live = mask == nullptr || __ldg(mask + t) != 0;
-    float x[VL], s[VL];
-    uint32_t key[VL];
-#pragma unroll
-    for (int i = 0; i < VL; ++i) {
-      const int e = lane + 32 * i;
-      x[i] = e < n ? load_logit(logits, (size_t)t * n + e, bf16) : -INFINITY;
-    }
-    // scores are needed for the weights (unless they are the softmax of the
-    // chosen logits alone), for a bias and for sums of group scores
-    const bool need_s = p.score == MOE_SCORE_SIGMOID || !p.renorm || bias != nullptr || p.gtop > 1;
-    if (need_s) scores<VL>(x, p.score, s);
-#pragma unroll
-    for (int i = 0; i < VL; ++i) {
-      const int e = lane + 32 * i;
-      float f = x[i];
-      if (bias != nullptr && e < n && f != -INFINITY) f = s[i] + __ldg(bias + e);
-      key[i] = e < n ? ordered_key(f) : 0u;
-    }
-    if (p.G > 1) {
-      // group scores: lane g ends with the score of group g
-      const int gs = n / p.G;
-      float mine = -INFINITY;
-      for (int g = 0; g < p.G; ++g) {
-        const int lo = g * gs, hi = lo + gs;
-        uint32_t b1 = 0, b2 = 0;  // the lane's best two of the group
-#pragma unroll
-        for (int i = 0; i < VL; ++i) {
-          const int e = lane + 32 * i;
-          if (e >= lo && e < hi) {
-            uint32_t kk = key[i];
-            if (p.gtop > 1 && bias == nullptr) kk = x[i] == -INFINITY ? KEY_NEG_INF : ordered_key(s[i]);
-            b2 = max(b2, min(b1, kk));
-            b1 = max(b1, kk);
-          }
-        }
-        const uint32_t m1 = __reduce_max_sync(0xFFFFFFFFu, b1);
-        float sc = key_value(m1);
-        if (p.gtop > 1 && gs > 1) {
-          const unsigned who = __ballot_sync(0xFFFFFFFFu, b1 == m1);
-          const uint32_t rest = (lane == __ffs(who) - 1) ? b2 : b1;
-          sc += key_value(__reduce_max_sync(0xFFFFFFFFu, rest));
-        }
-        if (lane == g) mine = sc;
-      }
-      // keep the topk_group best: lane g counts the groups that come before it
-      const uint32_t gk = lane < p.G ? ordered_key(mine) : 0u;
-      int before = 0;
-      for (int g = 0; g < p.G; ++g) {
-        const uint32_t o = __shfl_sync(0xFFFFFFFFu, gk, g);
-        before += (o > gk || (o == gk && g < lane)) ? 1 : 0;
-      }
-      const unsigned kept = __ballot_sync(0xFFFFFFFFu, lane < p.G && before < p.keep);
+    int mine = -1;  // the lane's chosen expert (lane j: the j-th)
+    Soft sm{0.0f, 1.0f};
+    if (mask == nullptr || __ldg(mask + t) != 0) {
+      float x[VL];
+      uint32_t key[VL];
+      load_row<VL, BF16>(logits, t, n, lane, vec != 0, x);
+      if (!sig && (by_score || !p.renorm)) sm = softmax_of<VL>(x);
+      uint32_t g1 = 0, g2 = 0;  // the lane's best two keys (of the group choice)
 #pragma unroll
       for (int i = 0; i < VL; ++i) {
-        const int e = lane + 32 * i;
-        if (e < n && !((kept >> (e / gs)) & 1u)) key[i] = 0u;
+        key[i] = ordered_key(x[i]);
+        uint32_t gk = key[i];
+        if (by_score) {
+          const float s = sig ? sigmoid(x[i]) : soft_score(sm, x[i]);
+          if (bias != nullptr) {
+            key[i] = gk = x[i] == -INFINITY ? KEY_NEG_INF : ordered_key(s + (e0 + i < n ? __ldg(bias + e0 + i) : 0.0f));
+          } else {
+            gk = x[i] == -INFINITY ? KEY_NEG_INF : ordered_key(s);
+          }
+        }
+        if (p.G > 1 && runs) {
+          g2 = max(g2, min(g1, gk));
+          g1 = max(g1, gk);
+        }
+        if (p.G > 1 && !runs) x[i] = key_value(gk);  // the other path reads the group keys back
       }
-    }
-    // the choice: lane j keeps the j-th expert
-    int my_idx = -1;
-    float my_val = 0.0f;
-    if (live) {
-      for (int j = 0; j < p.k; ++j) {
-        uint32_t b = key[0];
-        int bi = 0;
-#pragma unroll
-        for (int i = 1; i < VL; ++i)
-          if (key[i] > b) {
-            b = key[i];
-            bi = i;
+      if (p.G > 1) {
+        float score = -INFINITY;  // lane g: the score of group g
+        if (runs) {
+          for (int d = 1; d < seg; d <<= 1) {
+            const uint32_t o1 = __shfl_xor_sync(0xFFFFFFFFu, g1, d), o2 = __shfl_xor_sync(0xFFFFFFFFu, g2, d);
+            g2 = max(max(g2, o2), min(g1, o1));
+            g1 = max(g1, o1);
           }
-        const uint32_t m = __reduce_max_sync(0xFFFFFFFFu, b);
-        if (m <= KEY_NEG_INF) break;
-        const uint32_t e = __reduce_min_sync(0xFFFFFFFFu, b == m ? (uint32_t)(lane + 32 * bi) : 0xFFFFFFFFu);
-        float v = 0.0f;
+          float mineg = key_value(g1);
+          if (p.gtop > 1 && gs > 1) mineg += key_value(g2);
+          score = __shfl_sync(0xFFFFFFFFu, mineg, (lane * seg) & 31);
+        } else {
+          for (int g = 0; g < p.G; ++g) {
+            const int lo = g * gs, hi = lo + gs;
+            uint32_t b1 = 0, b2 = 0;
 #pragma unroll
-        for (int i = 0; i < VL; ++i)
-          if (e == (uint32_t)(lane + 32 * i)) {
-            key[i] = 0u;
-            v = need_s && !(p.renorm && p.score == MOE_SCORE_SOFTMAX) ? s[i] : x[i];
+            for (int i = 0; i < VL; ++i) {
+              if (e0 + i >= lo && e0 + i < hi) {
+                const uint32_t kk = ordered_key(x[i]);
+                b2 = max(b2, min(b1, kk));
+                b1 = max(b1, kk);
+              }
+            }
+            const uint32_t m1 = __reduce_max_sync(0xFFFFFFFFu, b1);
+            float sc = key_value(m1);
+            if (p.gtop > 1 && gs > 1) {
+              const unsigned who = __ballot_sync(0xFFFFFFFFu, b1 == m1);
+              sc += key_value(__reduce_max_sync(0xFFFFFFFFu, lane == __ffs(who) - 1 ? b2 : b1));
+            }
+            if (lane == g) score = sc;
           }
-        v = __shfl_sync(0xFFFFFFFFu, v, e & 31u);
-        if (lane == j) {
-          my_idx = (int)e;
-          my_val = v;
+        }
+        // keep the topk_group best: lane g counts the groups that come before its own
+        const uint32_t gk = lane < p.G ? ordered_key(score) : 0u;
+        int before = 0;
+        for (int g = 0; g < p.G; ++g) {
+          const uint32_t o = __shfl_sync(0xFFFFFFFFu, gk, g);
+          before += (o > gk || (o == gk && g < lane)) ? 1 : 0;
+        }
+        const unsigned kept = __ballot_sync(0xFFFFFFFFu, lane < p.G && before < p.keep);
+        if (runs) {
+          if (!((kept >> (e0 / gs & 31)) & 1u)) {
+#pragma unroll
+            for (int i = 0; i < VL; ++i) key[i] = 0u;
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < VL; ++i)
+            if (e0 + i < n && !((kept >> ((e0 + i) / gs)) & 1u)) key[i] = 0u;
         }
       }
-    }
-    if (p.renorm) {
-      if (p.score == MOE_SCORE_SOFTMAX) {
-        const float m = warp_max(my_idx >= 0 ? my_val : -INFINITY);
-        const float ex = my_idx >= 0 ? expf(my_val - m) : 0.0f;
-        const float sum = warp_sum(ex);
-        my_val = my_idx >= 0 ? ex / sum : 0.0f;
-      } else {
-        my_val = my_val / (warp_sum(my_val) + 1e-20f);
+      // the choice
+      uint32_t b = key[0];
+      int bi = 0;
+#pragma unroll
+      for (int i = 1; i < VL; ++i)
+        if (key[i] > b) {
+          b = key[i];
+          bi = i;
+        }
+      int j = 0;
+      for (; j < p.k; ++j) {
+        const uint32_t m = __reduce_max_sync(0xFFFFFFFFu, b);
+        if (m <= KEY_NEG_INF) break;
+        const unsigned who = __ballot_sync(0xFFFFFFFFu, b == m);
+        if (lane == __ffs(who) - 1) {
+          chosen[warp][j] = e0 + bi;
+          b = 0u;
+          int nb = 0;
+#pragma unroll
+          for (int i = 0; i < VL; ++i) {
+            if (i == bi) key[i] = 0u;
+            if (key[i] > b) {
+              b = key[i];
+              nb = i;
+            }
+          }
+          bi = nb;
+        }
       }
+      __syncwarp();
+      if (lane < j) mine = chosen[warp][lane];
+      __syncwarp();
+    }
+    float w = 0.0f;
+    if (p.renorm && !sig) {
+      // the softmax over the chosen logits (the largest chosen logit is the first one's without a bias,
+      // but not with one)
+      const float xe = mine >= 0 ? load_logit<BF16>(logits, (size_t)t * n + mine) : -INFINITY;
+      const float m = warp_max(xe);
+      const float ex = mine >= 0 ? expf(xe - m) : 0.0f;
+      const float sum = warp_sum(ex);
+      if (mine >= 0) w = ex / sum;
+    } else {
+      if (mine >= 0) {
+        const float xe = load_logit<BF16>(logits, (size_t)t * n + mine);
+        w = sig ? sigmoid(xe) : soft_score(sm, xe);
+      }
+      if (p.renorm) w = w / (warp_sum(w) + 1e-20f);
     }
     if (lane < p.k) {
-      idx[(size_t)t * p.k + lane] = my_idx;
-      prob[(size_t)t * p.k + lane] = my_val * p.scale;
-      if (load != nullptr && my_idx >= 0) atomicAdd(&hist[my_idx], 1);
+      idx[(size_t)t * p.k + lane] = mine;
+      prob[(size_t)t * p.k + lane] = w * p.scale;
+      if (load != nullptr && mine >= 0) atomicAdd(&hist[mine], 1);
     }
   }
   if (load != nullptr) {
     __syncthreads();
-    for (int e = threadIdx.x; e < n; e += blockDim.x)
-      if (hist[e] != 0) atomicAdd(load + e, hist[e]);  // integers: the order does not matter
+    // integers: the order does not matter.  A lone CTA has every count.
+    for (int e = threadIdx.x; e < n; e += blockDim.x) {
+      if (gridDim.x == 1)
+        load[e] = hist[e];
+      else if (hist[e] != 0)
+        atomicAdd(load + e, hist[e]);
+    }
   }
 }
 
-__device__ __forceinline__ void store_logit(void* p, size_t i, float v, int bf16) {
-  if (bf16)
+template <bool BF16>
+__device__ __forceinline__ void store_logit(void* p, size_t i, float v) {
+  if (BF16)
     static_cast<uint16_t*>(p)[i] = __bfloat16_as_ushort(__float2bfloat16_rn(v));
   else
     static_cast<float*>(p)[i] = v;
+}
+// The lane's VL values of row t (see load_row).
+template <int VL, bool BF16>
+__device__ __forceinline__ void store_row(void* p, size_t t, int n, int lane, bool vec, const float* v) {
+  const int e0 = lane * VL;
+  if (!vec || VL == 1) {
+#pragma unroll
+    for (int i = 0; i < VL; ++i)
+      if (e0 + i < n) store_logit<BF16>(p, t * n + e0 + i, v[i]);
+    return;
+  }
+  if (e0 >= n) return;
+  constexpr int W = BF16 ? VL / 2 : VL;  // 32-bit words
+  uint32_t w[W > 0 ? W : 1];
+#pragma unroll
+  for (int i = 0; i < W; ++i)
+    w[i] = BF16 ? pack_bf16x2(v[(2 * i) % VL], v[(2 * i + 1) % VL]) : __float_as_uint(v[i % VL]);
+  uint32_t* d = reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(p) + (t * n + e0) * (BF16 ? 2 : 4));
+  if (W >= 4) {
+#pragma unroll
+    for (int c = 0; c < W / 4; ++c)
+      reinterpret_cast<uint4*>(d)[c] =
+          make_uint4(w[(4 * c) % W], w[(4 * c + 1) % W], w[(4 * c + 2) % W], w[(4 * c + 3) % W]);
+  } else if (W == 2) {
+    *reinterpret_cast<uint2*>(d) = make_uint2(w[0], w[1 % W]);
+  } else {
+    *d = w[0];
+  }
 }
 
 // Backward, one warp per token; lane j < k holds the j-th chosen expert with
@@ -229,8 +357,9 @@ __device__ __forceinline__ void store_logit(void* p, size_t i, float v, int bf16
 //   sigmoid, renormalised:   dx_j = (g_j - sum g w) / D * s_j (1 - s_j),  D = sum s + 1e-20
 //   sigmoid:                 dx_j = g_j s_j (1 - s_j)
 // Experts without a gradient get 0; only the plain softmax reads every logit.
-template <int VL>
-__global__ void __launch_bounds__(32 * WARPS) k_router_bwd(const void* __restrict__ logits, int bf16,
+// The row is written whole, then lane j writes its expert's element over it.
+template <int VL, bool BF16>
+__global__ void __launch_bounds__(32 * WARPS) k_router_bwd(const void* __restrict__ logits, int vec,
                                                            const int32_t* __restrict__ idx,
                                                            const float* __restrict__ dprob, int T, const Params p,
                                                            void* __restrict__ dlogits) {
@@ -244,7 +373,7 @@ __global__ void __launch_bounds__(32 * WARPS) k_router_bwd(const void* __restric
       if (e < 0 || e >= n) e = -1;
       if (e >= 0) {
         g = p.scale * __ldg(dprob + (size_t)t * p.k + lane);
-        xe = load_logit(logits, (size_t)t * n + e, bf16);
+        xe = load_logit<BF16>(logits, (size_t)t * n + e);
       }
     }
     float out[VL];
@@ -252,8 +381,8 @@ __global__ void __launch_bounds__(32 * WARPS) k_router_bwd(const void* __restric
     for (int i = 0; i < VL; ++i) out[i] = 0.0f;
     float d;  // gradient of the lane's chosen logit
     if (p.score == MOE_SCORE_SIGMOID) {
-      const float s = e >= 0 ? 1.0f / (1.0f + expf(-xe)) : 0.0f;
-      const float s1 = 1.0f / (1.0f + expf(xe));  // 1 - s without the cancellation
+      const float s = e >= 0 ? sigmoid(xe) : 0.0f;
+      const float s1 = sigmoid(-xe);  // 1 - s without the cancellation
       if (p.renorm) {
         const float D = warp_sum(s) + 1e-20f;
         const float in = warp_sum(g * (s / D));
@@ -266,43 +395,21 @@ __global__ void __launch_bounds__(32 * WARPS) k_router_bwd(const void* __restric
       const float ex = e >= 0 ? expf(xe - m) : 0.0f;
       const float w = ex / fmaxf(warp_sum(ex), 1e-38f);
       d = w * (g - warp_sum(g * w));
+    } else if (!__any_sync(0xFFFFFFFFu, e >= 0)) {
+      d = 0.0f;  // a token that chose nothing: its logits (masked, perhaps not finite) are not looked at
     } else {
-      float x[VL], s[VL];
+      load_row<VL, BF16>(logits, t, n, lane, vec != 0, out);
+      const Soft sm = softmax_of<VL>(out);
+      const float se = e >= 0 ? soft_score(sm, xe) : 0.0f;
+      const float in = warp_sum(g * se);
+      d = se * (g - in);
+      const float scale = -in / sm.d;
 #pragma unroll
-      for (int i = 0; i < VL; ++i) {
-        const int c = lane + 32 * i;
-        x[i] = c < n ? load_logit(logits, (size_t)t * n + c, bf16) : -INFINITY;
-      }
-      scores<VL>(x, p.score, s);
-      float se = 0.0f;  // the score of the lane's chosen expert
-      for (int j = 0; j < p.k; ++j) {
-        const int ej = __shfl_sync(0xFFFFFFFFu, e, j);
-        if (ej < 0) continue;
-        float v = 0.0f;
-#pragma unroll
-        for (int i = 0; i < VL; ++i)
-          if (ej == lane + 32 * i) v = s[i];
-        v = __shfl_sync(0xFFFFFFFFu, v, ej & 31);
-        if (lane == j) se = v;
-      }
-      d = g * se;
-      const float in = warp_sum(d);
-#pragma unroll
-      for (int i = 0; i < VL; ++i) out[i] = -s[i] * in;
+      for (int i = 0; i < VL; ++i) out[i] = expf(out[i] - sm.m) * scale;
     }
-    for (int j = 0; j < p.k; ++j) {
-      const int ej = __shfl_sync(0xFFFFFFFFu, e, j);
-      const float dj = __shfl_sync(0xFFFFFFFFu, d, j);
-      if (ej < 0) continue;
-#pragma unroll
-      for (int i = 0; i < VL; ++i)
-        if (ej == lane + 32 * i) out[i] += dj;
-    }
-#pragma unroll
-    for (int i = 0; i < VL; ++i) {
-      const int c = lane + 32 * i;
-      if (c < n) store_logit(dlogits, (size_t)t * n + c, out[i], bf16);
-    }
+    store_row<VL, BF16>(dlogits, t, n, lane, vec != 0, out);
+    __syncwarp();  // orders the row's stores before the chosen experts'
+    if (e >= 0) store_logit<BF16>(dlogits, (size_t)t * n + e, d);
   }
 }
 
@@ -318,22 +425,33 @@ static int grid_of(int T) {
   return (int)(need < cap ? need : cap);
 }
 
-// lane registers for n experts: the next power of two of n / 32
+// Experts per lane: the power of two that covers n / 32; rows are read in
+// vectors where every row starts on a vector's boundary.
 template <class F>
-static void dispatch(int n, F&& f) {
-  const int vl = (n + 31) / 32;
-  if (vl <= 1)
-    f(std::integral_constant<int, 1>{});
-  else if (vl <= 2)
-    f(std::integral_constant<int, 2>{});
-  else if (vl <= 4)
-    f(std::integral_constant<int, 4>{});
-  else if (vl <= 8)
-    f(std::integral_constant<int, 8>{});
-  else if (vl <= 16)
-    f(std::integral_constant<int, 16>{});
+static void dispatch(int n, int bf16, const void* a, const void* b, F&& f) {
+  int vl = 1;
+  while (32 * vl < n) vl *= 2;
+  const int es = bf16 ? 2 : 4, unit = vl * es < 16 ? vl * es : 16;
+  const int vec = n % vl == 0 && ((size_t)n * es) % unit == 0 &&
+                  ((reinterpret_cast<uintptr_t>(a) | reinterpret_cast<uintptr_t>(b)) & (unit - 1)) == 0;
+  auto typed = [&](auto v) {
+    if (bf16)
+      f(v, std::true_type{}, vec);
+    else
+      f(v, std::false_type{}, vec);
+  };
+  if (vl == 1)
+    typed(std::integral_constant<int, 1>{});
+  else if (vl == 2)
+    typed(std::integral_constant<int, 2>{});
+  else if (vl == 4)
+    typed(std::integral_constant<int, 4>{});
+  else if (vl == 8)
+    typed(std::integral_constant<int, 8>{});
+  else if (vl == 16)
+    typed(std::integral_constant<int, 16>{});
   else
-    f(std::integral_constant<int, 32>{});
+    typed(std::integral_constant<int, 32>{});
 }
 
 }  // namespace router
@@ -350,15 +468,16 @@ extern "C" moe_status_t moe_router_fwd(const void* logits, int logits_bf16, cons
   if ((int64_t)T * k > (int64_t)INT32_MAX / 2) return MOE_ERR_ARG;
   if (T > 0 && (!logits || !topk_idx || !topk_prob)) return MOE_ERR_ARG;
   cudaStream_t st = as_stream(stream);
-  if (load && cudaMemsetAsync(load, 0, (size_t)n * sizeof(int32_t), st) != cudaSuccess) return MOE_ERR_CUDA;
+  const int grid = T > 0 ? grid_of(T) : 0;
+  if (T > 0 && grid <= 0) return MOE_ERR_CUDA;
+  if (load && grid != 1 && cudaMemsetAsync(load, 0, (size_t)n * sizeof(int32_t), st) != cudaSuccess)
+    return MOE_ERR_CUDA;
   if (T == 0) return MOE_OK;
   const Params p{n, k, params->score, params->renorm ? 1 : 0, params->n_group, params->topk_group, params->group_top,
                  params->scale};
-  const int grid = grid_of(T);
-  if (grid <= 0) return MOE_ERR_CUDA;
-  dispatch(n, [&](auto vl) {
-    k_router_fwd<decltype(vl)::value><<<grid, 32 * WARPS, load ? n * sizeof(int32_t) : 0, st>>>(
-        logits, logits_bf16 ? 1 : 0, bias, token_mask, T, p, topk_idx, topk_prob, load);
+  dispatch(n, logits_bf16, logits, nullptr, [&](auto vl, auto bf16, int vec) {
+    k_router_fwd<decltype(vl)::value, decltype(bf16)::value><<<grid, 32 * WARPS, load ? n * sizeof(int32_t) : 0, st>>>(
+        logits, vec, bias, token_mask, T, p, topk_idx, topk_prob, load);
   });
   count_launch();
   return launch_status();
@@ -376,9 +495,9 @@ extern "C" moe_status_t moe_router_bwd(const void* logits, int logits_bf16, cons
                  params->scale};
   const int grid = grid_of(T);
   if (grid <= 0) return MOE_ERR_CUDA;
-  dispatch(n, [&](auto vl) {
-    k_router_bwd<decltype(vl)::value><<<grid, 32 * WARPS, 0, as_stream(stream)>>>(
-        logits, logits_bf16 ? 1 : 0, topk_idx, dprob, T, p, dlogits);
+  dispatch(n, logits_bf16, logits, dlogits, [&](auto vl, auto bf16, int vec) {
+    k_router_bwd<decltype(vl)::value, decltype(bf16)::value><<<grid, 32 * WARPS, 0, as_stream(stream)>>>(
+        logits, vec, topk_idx, dprob, T, p, dlogits);
   });
   count_launch();
   return launch_status();

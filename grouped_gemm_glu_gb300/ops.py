@@ -499,16 +499,30 @@ def dglu_act(da, pre, counts, offsets, F: int, params: L.GluParams):
 
 
 def _need(t, dtype, shape, what):
-    """A dense CUDA tensor of this type and shape (None in shape: any), or ValueError."""
+    """A dense CUDA tensor of this type and shape (None: any shape), or ValueError."""
+    if isinstance(t, torch.Tensor) and t.is_cuda and t.dtype == dtype and t.is_contiguous() and (
+            shape is None or t.shape == shape):
+        return t
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise ValueError(f"{what}: a CUDA tensor is needed")
     if t.dtype != dtype:
         raise ValueError(f"{what}: {dtype} is needed, got {t.dtype}")
-    if t.dim() != len(shape) or any(n is not None and n != m for n, m in zip(shape, t.shape)):
+    if shape is not None and t.shape != shape:
         raise ValueError(f"{what}: shape {tuple(shape)} is needed, got {tuple(t.shape)}")
-    if not t.is_contiguous():
-        raise ValueError(f"{what}: a contiguous tensor is needed")
-    return t
+    raise ValueError(f"{what}: a contiguous tensor is needed")
+
+
+def _need2(t, dtype, what):
+    """_need for a matrix of any size; returns its two extents."""
+    _need(t, dtype, None, what)
+    if t.dim() != 2:
+        raise ValueError(f"{what}: two dimensions are needed, got {tuple(t.shape)}")
+    return t.shape
+
+
+def _cur(t) -> int:
+    """The current stream's handle on t's device."""
+    return torch._C._cuda_getCurrentRawStream(t.get_device())
 
 
 def _ptr(t):
@@ -522,8 +536,7 @@ def rmsnorm(x, gamma, eps: float = 1e-5, residual=None, bf16: bool = True, mxfp8
     residual), y (bf16=True), q [T, H] and s [T, H/32] (mxfp8=True: the
     row-wise MXFP8 of y, what an MXFP8 FC1 reads) and rstd [T]."""
     bf = torch.bfloat16
-    _need(x, bf, (None, None), "x")
-    T, H = x.shape
+    T, H = _need2(x, bf, "x")
     _need(gamma, bf, (H,), "gamma")
     o = {}
     new, dev = torch.empty, x.device
@@ -539,7 +552,7 @@ def rmsnorm(x, gamma, eps: float = 1e-5, residual=None, bf16: bool = True, mxfp8
     if with_rstd:
         r = o["rstd"] = new(T, dtype=torch.float32, device=dev)
     L.check(L.load().moe_rmsnorm_fwd(x.data_ptr(), _ptr(residual), gamma.data_ptr(), eps, T, H, _ptr(h), _ptr(y),
-                                     _ptr(q), _ptr(s), _ptr(r), _s()), "moe_rmsnorm_fwd")
+                                     _ptr(q), _ptr(s), _ptr(r), _cur(x)), "moe_rmsnorm_fwd")
     return o
 
 
@@ -549,8 +562,7 @@ def rmsnorm_bwd(dy, h, gamma, rstd, dres=None, with_dgamma: bool = True):
     arrives at h from the rest of the residual stream; dx is the gradient of x
     and of the residual alike."""
     bf = torch.bfloat16
-    _need(dy, bf, (None, None), "dy")
-    T, H = dy.shape
+    T, H = _need2(dy, bf, "dy")
     _need(h, bf, (T, H), "h")
     _need(gamma, bf, (H,), "gamma")
     _need(rstd, torch.float32, (T,), "rstd")
@@ -565,28 +577,29 @@ def rmsnorm_bwd(dy, h, gamma, rstd, dres=None, with_dgamma: bool = True):
         nbytes = lib.moe_rmsnorm_bwd_workspace_size(T, H)
         ws = torch.empty(nbytes, dtype=torch.uint8, device=dy.device)
     L.check(lib.moe_rmsnorm_bwd(dy.data_ptr(), _ptr(dres), h.data_ptr(), gamma.data_ptr(), rstd.data_ptr(), T, H,
-                                dx.data_ptr(), _ptr(dgamma), _ptr(ws), nbytes, _s()), "moe_rmsnorm_bwd")
+                                dx.data_ptr(), _ptr(dgamma), _ptr(ws), nbytes, _cur(dy)), "moe_rmsnorm_bwd")
     return dx, dgamma
 
 
 def dequantize_mxfp8(q, s, out=None):
     """The bf16 values of MXFP8 codes q [..., C] with scales s [..., C/32]."""
-    _need(q, torch.uint8, q.shape, "q")
+    _need(q, torch.uint8, None, "q")
     if q.shape[-1] % 32:
         raise ValueError("q: the last dimension must be a multiple of 32")
     _need(s, torch.uint8, (*q.shape[:-1], q.shape[-1] // 32), "s")
     o = _need(out, torch.bfloat16, q.shape, "out") if out is not None else torch.empty(
         q.shape, dtype=torch.bfloat16, device=q.device)
-    L.check(L.load().moe_dequantize_mxfp8(q.data_ptr(), s.data_ptr(), s.numel(), o.data_ptr(), _s()),
+    L.check(L.load().moe_dequantize_mxfp8(q.data_ptr(), s.data_ptr(), s.numel(), o.data_ptr(), _cur(q)),
             "moe_dequantize_mxfp8")
     return o
 
 
 def _logits(logits):
-    if logits.dtype not in (torch.float32, torch.bfloat16):
-        raise ValueError(f"logits: float32 or bfloat16 is needed, got {logits.dtype}")
-    _need(logits, logits.dtype, (None, None), "logits")
-    return int(logits.dtype == torch.bfloat16)
+    dt = logits.dtype
+    if dt != torch.float32 and dt != torch.bfloat16:
+        raise ValueError(f"logits: float32 or bfloat16 is needed, got {dt}")
+    _need2(logits, dt, "logits")
+    return 1 if dt == torch.bfloat16 else 0
 
 
 def router(logits, k: int, params: L.RouterParams, bias=None, token_mask=None, with_load: bool = True) -> dict:
@@ -610,7 +623,7 @@ def router(logits, k: int, params: L.RouterParams, bias=None, token_mask=None, w
     if with_load:
         load = o["load"] = torch.empty(n, dtype=torch.int32, device=dev)
     L.check(L.load().moe_router_fwd(logits.data_ptr(), b16, _ptr(bias), _ptr(token_mask), T, n, k, C.byref(params),
-                                    o["idx"].data_ptr(), o["prob"].data_ptr(), _ptr(load), _s()), "moe_router_fwd")
+                                    o["idx"].data_ptr(), o["prob"].data_ptr(), _ptr(load), _cur(logits)), "moe_router_fwd")
     return o
 
 
@@ -619,10 +632,10 @@ def router_bwd(logits, idx, dprob, params: L.RouterParams):
     of the weights that router returned with idx [T, k]."""
     b16 = _logits(logits)
     T, n = logits.shape
-    _need(idx, torch.int32, (T, None), "idx")
-    k = idx.shape[1]
+    k = _need2(idx, torch.int32, "idx")[1]
+    _need(idx, torch.int32, (T, k), "idx")
     _need(dprob, torch.float32, (T, k), "dprob")
     d = torch.empty_like(logits)
     L.check(L.load().moe_router_bwd(logits.data_ptr(), b16, idx.data_ptr(), dprob.data_ptr(), T, n, k,
-                                    C.byref(params), d.data_ptr(), _s()), "moe_router_bwd")
+                                    C.byref(params), d.data_ptr(), _cur(logits)), "moe_router_bwd")
     return d

@@ -197,6 +197,8 @@ def test_ties_empty_rows_and_nonfinite():
     m[3] = False
     o = ops.router(x, 3, prm, token_mask=m)
     assert np_(o["idx"])[3].tolist() == [-1] * 3 and np.all(np_(o["prob"])[3] == 0)
+    for kind, rn in (("softmax", False), ("softmax", True), ("sigmoid", False), ("sigmoid", True)):
+        assert np.all(np_(ops.router_bwd(x, o["idx"], torch.ones(6, 3, device=DEV), L.router_params(kind, rn)))[3] == 0)
     assert int(o["load"].sum()) == 10  # three, one, three and three experts of rows 0, 2, 4, 5
     # sigmoids that underflow: the renormalised weights are 0, not NaN
     y = torch.full((1, 8), -200.0, device=DEV)
