@@ -15,9 +15,12 @@
 // two vector loads per lane, a group of experts is a run of lanes whose best
 // keys meet in a few shuffles, and the lowest lane among equal keys holds the
 // lowest index.  Keys are the floats' bits mapped to unsigned integers of the
-// same order: a round of the choice is one warp reduction (redux.sync) and a
-// ballot; the lane that held the best key drops it and looks for its next.
-// Lane j then computes the weight of the j-th expert from its logit.  An
+// same order, sorted within each lane by min / max: a round of the choice is
+// one warp reduction (redux.sync) over the lanes' best keys and a ballot, and
+// the lane that held the winner moves its list up.  Which of that lane's
+// experts had the key is settled once, after the rounds, by lane j for the
+// j-th choice from a copy of the keys in shared memory; lane j then computes
+// the weight from the expert's logit.  An
 // expert with a logit (or bias) of -inf is never chosen.
 //
 // Memory: each logit is read once (4 or 2 bytes), 8 bytes leave per chosen
@@ -32,20 +35,24 @@ namespace moeglu {
 namespace router {
 
 constexpr int N_MAX = 1024, K_MAX = 32, G_MAX = 32;
-constexpr int WARPS = 8;
+template <int VL>
+constexpr int max_warps() { return VL < 32 ? 16 : 8; }  // per CTA: registers, and 32 KB of keys
 constexpr uint32_t KEY_NEG_INF = 0x007FFFFFu;  // ordered_key(-inf): keys at or below it are not chosen
 
 struct Params {
   int n, k, score, renorm, G, keep, gtop;
   float scale;
+  // set by dispatch(): experts per group; log2 of the lanes per group where
+  // groups are whole runs of 2^j lanes, else -1; whether the logits' and the
+  // bias's rows start on a lane's vector
+  int gs, seg_log, vec, vec_bias;
 };
 
 // Unsigned integers in the order of the floats: -inf < ... < -0 = +0 < ... <
 // +inf < NaN (a NaN is chosen first, so that it shows in the weights).
 __device__ __forceinline__ uint32_t ordered_key(float f) {
-  if (f != f) return 0xFFFFFFFFu;
   const uint32_t b = __float_as_uint(f + 0.0f);  // -0 + 0 = +0
-  return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
+  return f != f ? 0xFFFFFFFFu : b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u);
 }
 __device__ __forceinline__ float key_value(uint32_t k) {
   return __uint_as_float((k & 0x80000000u) ? (k ^ 0x80000000u) : ~k);
@@ -149,151 +156,175 @@ __device__ __forceinline__ Soft softmax_of(const float* x) {
 }
 __device__ __forceinline__ float soft_score(const Soft& s, float x) { return expf(x - s.m) / s.d; }
 
+// Descending order of VL keys (Batcher's odd-even merge sort, unrolled).
+template <int VL>
+__device__ __forceinline__ void sort_desc(uint32_t* v) {
+#pragma unroll
+  for (int p = 1; p < VL; p *= 2) {
+#pragma unroll
+    for (int k = p; k >= 1; k /= 2) {
+#pragma unroll
+      for (int j = k % p; j + k < VL; j += 2 * k) {
+#pragma unroll
+        for (int i = 0; i < k; ++i) {
+          if (i + j + k < VL && (i + j) / (2 * p) == (i + j + k) / (2 * p)) {
+            const uint32_t hi = max(v[i + j], v[i + j + k]), lo = min(v[i + j], v[i + j + k]);
+            v[i + j] = hi;
+            v[i + j + k] = lo;
+          }
+        }
+      }
+    }
+  }
+}
+
+// Dynamic shared memory: the keys of the warps' rows ([warps][32 VL]), then
+// the histogram [n] when load is counted.
 template <int VL, bool BF16>
-__global__ void __launch_bounds__(32 * WARPS) k_router_fwd(const void* __restrict__ logits, int vec,
+__global__ void __launch_bounds__(32 * max_warps<VL>()) k_router_fwd(const void* __restrict__ logits,
                                                            const float* __restrict__ bias,
                                                            const uint8_t* __restrict__ mask, int T, const Params p,
                                                            int32_t* __restrict__ idx, float* __restrict__ prob,
                                                            int32_t* __restrict__ load) {
-  extern __shared__ int32_t hist[];           // [n] when load is counted
-  __shared__ int32_t chosen[WARPS][K_MAX];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  extern __shared__ __align__(16) uint32_t keys_all[];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+  int32_t* hist = reinterpret_cast<int32_t*>(keys_all + warps * 32 * VL);
+  uint32_t* keys = keys_all + warp * 32 * VL;
   const int n = p.n, e0 = lane * VL;
   if (load != nullptr) {
     for (int e = threadIdx.x; e < n; e += blockDim.x) hist[e] = 0;
     __syncthreads();
   }
   const bool sig = p.score == MOE_SCORE_SIGMOID;
-  // scores of all experts are needed for a bias and for sums of group scores only
-  const bool by_score = bias != nullptr || (p.G > 1 && p.gtop > 1);
-  // groups that are whole runs of 2^j lanes
-  const int gs = n / p.G, seg = gs / VL;
-  const bool runs = gs % VL == 0 && (seg & (seg - 1)) == 0 && p.G * seg <= 32;
-  for (int t = blockIdx.x * WARPS + warp; t < T; t += gridDim.x * WARPS) {
+  // scores of all experts are needed for a bias only; sums of group scores
+  // without one are made from the logits that the best keys are
+  const bool sums = p.G > 1 && p.gtop > 1;
+  const int gs = p.gs;
+  const bool runs = p.seg_log >= 0;
+  for (int t = blockIdx.x * warps + warp; t < T; t += gridDim.x * warps) {
     int mine = -1;  // the lane's chosen expert (lane j: the j-th)
     Soft sm{0.0f, 1.0f};
     if (mask == nullptr || __ldg(mask + t) != 0) {
       float x[VL];
       uint32_t key[VL];
-      load_row<VL, BF16>(logits, t, n, lane, vec != 0, x);
-      if (!sig && (by_score || !p.renorm)) sm = softmax_of<VL>(x);
-      uint32_t g1 = 0, g2 = 0;  // the lane's best two keys (of the group choice)
+      load_row<VL, BF16>(logits, t, n, lane, p.vec != 0, x);
+      if (!sig && (bias != nullptr || sums || !p.renorm)) sm = softmax_of<VL>(x);
+      // the key of a group sum: the score behind a key that is a logit
+      auto group_key = [&](uint32_t k) {
+        if (bias != nullptr || !sums || k <= KEY_NEG_INF) return k;
+        const float f = key_value(k);
+        return ordered_key(sig ? sigmoid(f) : soft_score(sm, f));
+      };
+      if (bias != nullptr) {
+        float b[VL];
+        load_row<VL, false>(bias, 0, n, lane, p.vec_bias != 0, b);  // -inf past n, as the logits
+        if (sig) {
 #pragma unroll
-      for (int i = 0; i < VL; ++i) {
-        key[i] = ordered_key(x[i]);
-        uint32_t gk = key[i];
-        if (by_score) {
-          const float s = sig ? sigmoid(x[i]) : soft_score(sm, x[i]);
-          if (bias != nullptr) {
-            key[i] = gk = x[i] == -INFINITY ? KEY_NEG_INF : ordered_key(s + (e0 + i < n ? __ldg(bias + e0 + i) : 0.0f));
-          } else {
-            gk = x[i] == -INFINITY ? KEY_NEG_INF : ordered_key(s);
-          }
-        }
-        if (p.G > 1 && runs) {
-          g2 = max(g2, min(g1, gk));
-          g1 = max(g1, gk);
-        }
-        if (p.G > 1 && !runs) x[i] = key_value(gk);  // the other path reads the group keys back
-      }
-      if (p.G > 1) {
-        float score = -INFINITY;  // lane g: the score of group g
-        if (runs) {
-          for (int d = 1; d < seg; d <<= 1) {
-            const uint32_t o1 = __shfl_xor_sync(0xFFFFFFFFu, g1, d), o2 = __shfl_xor_sync(0xFFFFFFFFu, g2, d);
-            g2 = max(max(g2, o2), min(g1, o1));
-            g1 = max(g1, o1);
-          }
-          float mineg = key_value(g1);
-          if (p.gtop > 1 && gs > 1) mineg += key_value(g2);
-          score = __shfl_sync(0xFFFFFFFFu, mineg, (lane * seg) & 31);
+          for (int i = 0; i < VL; ++i) key[i] = ordered_key(x[i] == -INFINITY ? x[i] : sigmoid(x[i]) + b[i]);
         } else {
-          for (int g = 0; g < p.G; ++g) {
-            const int lo = g * gs, hi = lo + gs;
-            uint32_t b1 = 0, b2 = 0;
 #pragma unroll
-            for (int i = 0; i < VL; ++i) {
-              if (e0 + i >= lo && e0 + i < hi) {
-                const uint32_t kk = ordered_key(x[i]);
-                b2 = max(b2, min(b1, kk));
-                b1 = max(b1, kk);
-              }
-            }
-            const uint32_t m1 = __reduce_max_sync(0xFFFFFFFFu, b1);
-            float sc = key_value(m1);
-            if (p.gtop > 1 && gs > 1) {
-              const unsigned who = __ballot_sync(0xFFFFFFFFu, b1 == m1);
-              sc += key_value(__reduce_max_sync(0xFFFFFFFFu, lane == __ffs(who) - 1 ? b2 : b1));
-            }
-            if (lane == g) score = sc;
-          }
+          for (int i = 0; i < VL; ++i) key[i] = ordered_key(x[i] == -INFINITY ? x[i] : soft_score(sm, x[i]) + b[i]);
         }
-        // keep the topk_group best: lane g counts the groups that come before its own
+      } else {
+#pragma unroll
+        for (int i = 0; i < VL; ++i) key[i] = ordered_key(x[i]);
+      }
+      // keep the topk_group best groups: lane g, holding the score of group
+      // g, counts the groups that come before it
+      auto kept_groups = [&](float score) {
         const uint32_t gk = lane < p.G ? ordered_key(score) : 0u;
         int before = 0;
         for (int g = 0; g < p.G; ++g) {
           const uint32_t o = __shfl_sync(0xFFFFFFFFu, gk, g);
           before += (o > gk || (o == gk && g < lane)) ? 1 : 0;
         }
-        const unsigned kept = __ballot_sync(0xFFFFFFFFu, lane < p.G && before < p.keep);
-        if (runs) {
-          if (!((kept >> (e0 / gs & 31)) & 1u)) {
-#pragma unroll
-            for (int i = 0; i < VL; ++i) key[i] = 0u;
-          }
-        } else {
-#pragma unroll
-          for (int i = 0; i < VL; ++i)
-            if (e0 + i < n && !((kept >> ((e0 + i) / gs)) & 1u)) key[i] = 0u;
-        }
-      }
-      // the choice
-      uint32_t b = key[0];
-      int bi = 0;
-#pragma unroll
-      for (int i = 1; i < VL; ++i)
-        if (key[i] > b) {
-          b = key[i];
-          bi = i;
-        }
-      int j = 0;
-      for (; j < p.k; ++j) {
-        const uint32_t m = __reduce_max_sync(0xFFFFFFFFu, b);
-        if (m <= KEY_NEG_INF) break;
-        const unsigned who = __ballot_sync(0xFFFFFFFFu, b == m);
-        if (lane == __ffs(who) - 1) {
-          chosen[warp][j] = e0 + bi;
-          b = 0u;
-          int nb = 0;
+        return __ballot_sync(0xFFFFFFFFu, lane < p.G && before < p.keep);
+      };
+      if (p.G > 1 && !runs) {
+        float score = -INFINITY;
+        for (int g = 0; g < p.G; ++g) {
+          const int lo = g * gs, hi = lo + gs;
+          uint32_t b1 = 0, b2 = 0;  // the lane's best two of the group
 #pragma unroll
           for (int i = 0; i < VL; ++i) {
-            if (i == bi) key[i] = 0u;
-            if (key[i] > b) {
-              b = key[i];
-              nb = i;
+            if (e0 + i >= lo && e0 + i < hi) {
+              b2 = max(b2, min(b1, key[i]));
+              b1 = max(b1, key[i]);
             }
           }
-          bi = nb;
+          const uint32_t m1 = __reduce_max_sync(0xFFFFFFFFu, b1);
+          float sc = key_value(group_key(m1));
+          if (p.gtop > 1 && gs > 1) {
+            const unsigned who = __ballot_sync(0xFFFFFFFFu, b1 == m1);
+            sc += key_value(group_key(__reduce_max_sync(0xFFFFFFFFu, lane == __ffs(who) - 1 ? b2 : b1)));
+          }
+          if (lane == g) score = sc;
+        }
+        const unsigned kept = kept_groups(score);
+        int g = e0 / gs, left = gs - (e0 - g * gs);  // the group of expert e0 + i, and what is left of it
+#pragma unroll
+        for (int i = 0; i < VL; ++i) {
+          if (e0 + i < n && !((kept >> g) & 1u)) key[i] = 0u;
+          if (--left == 0) {
+            ++g;
+            left = gs;
+          }
         }
       }
-      __syncwarp();
-      if (lane < j) mine = chosen[warp][lane];
-      __syncwarp();
+#pragma unroll
+      for (int i = 0; i < VL; ++i) keys[e0 + i] = key[i];
+      sort_desc<VL>(key);
+      if (p.G > 1 && runs) {
+        uint32_t g1 = key[0], g2 = VL > 1 ? key[1 % VL] : 0u;
+        for (int d = 1; d < (1 << p.seg_log); d <<= 1) {
+          const uint32_t o1 = __shfl_xor_sync(0xFFFFFFFFu, g1, d), o2 = __shfl_xor_sync(0xFFFFFFFFu, g2, d);
+          g2 = max(max(g2, o2), min(g1, o1));
+          g1 = max(g1, o1);
+        }
+        float score = key_value(group_key(g1));
+        if (p.gtop > 1 && gs > 1) score += key_value(group_key(g2));
+        const unsigned kept = kept_groups(__shfl_sync(0xFFFFFFFFu, score, (lane << p.seg_log) & 31));
+        if (!((kept >> (lane >> p.seg_log)) & 1u)) key[0] = 0u;  // (nothing below it is looked at)
+      }
+      // the choice: lane j keeps the j-th key and the lane it came from
+      uint32_t my_key = 0u;
+      int my_src = -1, j = 0;
+      for (; j < p.k; ++j) {
+        const uint32_t m = __reduce_max_sync(0xFFFFFFFFu, key[0]);
+        if (m <= KEY_NEG_INF) break;
+        const int src = __ffs(__ballot_sync(0xFFFFFFFFu, key[0] == m)) - 1;
+        if (lane == j) {
+          my_key = m;
+          my_src = src;
+        }
+        if (lane == src) {
+#pragma unroll
+          for (int i = 0; i + 1 < VL; ++i) key[i] = key[i + 1];
+          key[VL - 1] = 0u;
+        }
+      }
+      // its index: the c-th of the source's experts with that key, c the
+      // number of earlier choices of the same key from the same lane
+      const unsigned same = __match_any_sync(0xFFFFFFFFu, my_key) & __match_any_sync(0xFFFFFFFFu, my_src);
+      int c = __popc(same & ((1u << lane) - 1u));
+      if (lane < j) {
+        const uint32_t* src = keys + my_src * VL;
+#pragma unroll
+        for (int i = 0; i < VL; ++i)
+          if (src[i] == my_key && c-- == 0) mine = my_src * VL + i;
+      }
+      __syncwarp();  // the keys have been read
     }
     float w = 0.0f;
+    const float xe = mine >= 0 ? load_logit<BF16>(logits, (size_t)t * n + mine) : -INFINITY;
     if (p.renorm && !sig) {
-      // the softmax over the chosen logits (the largest chosen logit is the first one's without a bias,
-      // but not with one)
-      const float xe = mine >= 0 ? load_logit<BF16>(logits, (size_t)t * n + mine) : -INFINITY;
+      // the softmax over the chosen logits
       const float m = warp_max(xe);
       const float ex = mine >= 0 ? expf(xe - m) : 0.0f;
       const float sum = warp_sum(ex);
       if (mine >= 0) w = ex / sum;
     } else {
-      if (mine >= 0) {
-        const float xe = load_logit<BF16>(logits, (size_t)t * n + mine);
-        w = sig ? sigmoid(xe) : soft_score(sm, xe);
-      }
+      if (mine >= 0) w = sig ? sigmoid(xe) : soft_score(sm, xe);
       if (p.renorm) w = w / (warp_sum(w) + 1e-20f);
     }
     if (lane < p.k) {
@@ -359,13 +390,13 @@ __device__ __forceinline__ void store_row(void* p, size_t t, int n, int lane, bo
 // Experts without a gradient get 0; only the plain softmax reads every logit.
 // The row is written whole, then lane j writes its expert's element over it.
 template <int VL, bool BF16>
-__global__ void __launch_bounds__(32 * WARPS) k_router_bwd(const void* __restrict__ logits, int vec,
+__global__ void __launch_bounds__(32 * max_warps<VL>()) k_router_bwd(const void* __restrict__ logits,
                                                            const int32_t* __restrict__ idx,
                                                            const float* __restrict__ dprob, int T, const Params p,
                                                            void* __restrict__ dlogits) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31, warps = blockDim.x >> 5;
   const int n = p.n;
-  for (int t = blockIdx.x * WARPS + warp; t < T; t += gridDim.x * WARPS) {
+  for (int t = blockIdx.x * warps + (threadIdx.x >> 5); t < T; t += gridDim.x * warps) {
     int e = -1;
     float g = 0.0f, xe = -INFINITY;
     if (lane < p.k) {
@@ -398,7 +429,7 @@ __global__ void __launch_bounds__(32 * WARPS) k_router_bwd(const void* __restric
     } else if (!__any_sync(0xFFFFFFFFu, e >= 0)) {
       d = 0.0f;  // a token that chose nothing: its logits (masked, perhaps not finite) are not looked at
     } else {
-      load_row<VL, BF16>(logits, t, n, lane, vec != 0, out);
+      load_row<VL, BF16>(logits, t, n, lane, p.vec != 0, out);
       const Soft sm = softmax_of<VL>(out);
       const float se = e >= 0 ? soft_score(sm, xe) : 0.0f;
       const float in = warp_sum(g * se);
@@ -407,7 +438,7 @@ __global__ void __launch_bounds__(32 * WARPS) k_router_bwd(const void* __restric
 #pragma unroll
       for (int i = 0; i < VL; ++i) out[i] = expf(out[i] - sm.m) * scale;
     }
-    store_row<VL, BF16>(dlogits, t, n, lane, vec != 0, out);
+    store_row<VL, BF16>(dlogits, t, n, lane, p.vec != 0, out);
     __syncwarp();  // orders the row's stores before the chosen experts'
     if (e >= 0) store_logit<BF16>(dlogits, (size_t)t * n + e, d);
   }
@@ -420,25 +451,48 @@ static bool params_ok(const moe_router_params_t* q, int n, int k) {
          k <= n / q->n_group * q->topk_group && q->scale == q->scale;
 }
 
-static int grid_of(int T) {
-  const long long need = ((long long)T + WARPS - 1) / WARPS, cap = (long long)sm_count() * 8;
-  return (int)(need < cap ? need : cap);
+// CTAs and warps per CTA.  Few tokens fit one CTA, which then holds every
+// count of the load and needs no cleared buffer and no atomics; otherwise the
+// warps spread over two CTAs per SM (`ctas` per SM), as few as fill it: every
+// CTA adds its n counts to the same n addresses, and 2432 small CTAs spent
+// 12 us on that where 304 large ones do not show it (32768 tokens, 64 experts).
+struct Grid {
+  int ctas, warps;
+};
+static Grid grid_of(int T, int max_warps, int ctas_per_sm) {
+  if (T <= 16) return {1, T < max_warps ? T : max_warps};
+  const int most = sm_count() * ctas_per_sm;
+  if (most <= 0) return {0, 0};
+  int w = (T + most - 1) / most;
+  if (w > max_warps) w = max_warps;
+  const int need = (T + w - 1) / w;
+  return {need < most ? need : most, w};
 }
 
 // Experts per lane: the power of two that covers n / 32; rows are read in
-// vectors where every row starts on a vector's boundary.
+// vectors where every row starts on a vector's boundary (n a multiple of the
+// lane's experts, aligned bases).
 template <class F>
-static void dispatch(int n, int bf16, const void* a, const void* b, F&& f) {
+static void dispatch(const moe_router_params_t* q, int n, int k, int bf16, const void* a, const void* b,
+                     const float* bias, F&& f) {
   int vl = 1;
   while (32 * vl < n) vl *= 2;
-  const int es = bf16 ? 2 : 4, unit = vl * es < 16 ? vl * es : 16;
-  const int vec = n % vl == 0 && ((size_t)n * es) % unit == 0 &&
-                  ((reinterpret_cast<uintptr_t>(a) | reinterpret_cast<uintptr_t>(b)) & (unit - 1)) == 0;
+  auto fits = [&](int es, uintptr_t bases) {
+    const int unit = vl * es < 16 ? vl * es : 16;
+    return n % vl == 0 && ((size_t)n * es) % unit == 0 && (bases & (unit - 1)) == 0;
+  };
+  Params p{n, k, q->score, q->renorm ? 1 : 0, q->n_group, q->topk_group, q->group_top, q->scale};
+  p.gs = n / q->n_group;
+  p.seg_log = -1;
+  if (p.gs % vl == 0 && (p.gs / vl & (p.gs / vl - 1)) == 0)
+    for (p.seg_log = 0; (1 << p.seg_log) < p.gs / vl;) ++p.seg_log;
+  p.vec = fits(bf16 ? 2 : 4, reinterpret_cast<uintptr_t>(a) | reinterpret_cast<uintptr_t>(b));
+  p.vec_bias = fits(4, reinterpret_cast<uintptr_t>(bias));
   auto typed = [&](auto v) {
     if (bf16)
-      f(v, std::true_type{}, vec);
+      f(v, std::true_type{}, p);
     else
-      f(v, std::false_type{}, vec);
+      f(v, std::false_type{}, p);
   };
   if (vl == 1)
     typed(std::integral_constant<int, 1>{});
@@ -468,16 +522,16 @@ extern "C" moe_status_t moe_router_fwd(const void* logits, int logits_bf16, cons
   if ((int64_t)T * k > (int64_t)INT32_MAX / 2) return MOE_ERR_ARG;
   if (T > 0 && (!logits || !topk_idx || !topk_prob)) return MOE_ERR_ARG;
   cudaStream_t st = as_stream(stream);
-  const int grid = T > 0 ? grid_of(T) : 0;
-  if (T > 0 && grid <= 0) return MOE_ERR_CUDA;
-  if (load && grid != 1 && cudaMemsetAsync(load, 0, (size_t)n * sizeof(int32_t), st) != cudaSuccess)
+  const Grid g = T > 0 ? grid_of(T, n <= 512 ? max_warps<1>() : max_warps<32>(), 2) : Grid{0, 0};
+  if (T > 0 && g.ctas <= 0) return MOE_ERR_CUDA;
+  if (load && g.ctas != 1 && cudaMemsetAsync(load, 0, (size_t)n * sizeof(int32_t), st) != cudaSuccess)
     return MOE_ERR_CUDA;
   if (T == 0) return MOE_OK;
-  const Params p{n, k, params->score, params->renorm ? 1 : 0, params->n_group, params->topk_group, params->group_top,
-                 params->scale};
-  dispatch(n, logits_bf16, logits, nullptr, [&](auto vl, auto bf16, int vec) {
-    k_router_fwd<decltype(vl)::value, decltype(bf16)::value><<<grid, 32 * WARPS, load ? n * sizeof(int32_t) : 0, st>>>(
-        logits, vec, bias, token_mask, T, p, topk_idx, topk_prob, load);
+  dispatch(params, n, k, logits_bf16, logits, nullptr, bias, [&](auto vl, auto bf16, const Params& p) {
+    constexpr int VL = decltype(vl)::value;
+    const size_t smem = (size_t)g.warps * 32 * VL * 4 + (load ? (size_t)n * 4 : 0);  // at most 36 KB
+    k_router_fwd<VL, decltype(bf16)::value><<<g.ctas, 32 * g.warps, smem, st>>>(
+        logits, bias, token_mask, T, p, topk_idx, topk_prob, load);
   });
   count_launch();
   return launch_status();
@@ -491,13 +545,11 @@ extern "C" moe_status_t moe_router_bwd(const void* logits, int logits_bf16, cons
   if ((int64_t)T * k > (int64_t)INT32_MAX / 2) return MOE_ERR_ARG;
   if (T == 0) return MOE_OK;
   if (!logits || !topk_idx || !dprob || !dlogits) return MOE_ERR_ARG;
-  const Params p{n, k, params->score, params->renorm ? 1 : 0, params->n_group, params->topk_group, params->group_top,
-                 params->scale};
-  const int grid = grid_of(T);
-  if (grid <= 0) return MOE_ERR_CUDA;
-  dispatch(n, logits_bf16, logits, dlogits, [&](auto vl, auto bf16, int vec) {
-    k_router_bwd<decltype(vl)::value, decltype(bf16)::value><<<grid, 32 * WARPS, 0, as_stream(stream)>>>(
-        logits, vec, topk_idx, dprob, T, p, dlogits);
+  const Grid g = grid_of(T, 8, 8);
+  if (g.ctas <= 0) return MOE_ERR_CUDA;
+  dispatch(params, n, k, logits_bf16, logits, dlogits, nullptr, [&](auto vl, auto bf16, const Params& p) {
+    k_router_bwd<decltype(vl)::value, decltype(bf16)::value><<<g.ctas, 32 * g.warps, 0, as_stream(stream)>>>(
+        logits, topk_idx, dprob, T, p, dlogits);
   });
   count_launch();
   return launch_status();
