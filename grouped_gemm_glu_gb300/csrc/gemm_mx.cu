@@ -688,20 +688,24 @@ __global__ void __launch_bounds__(THREADS, 1)
           }
           const int p0 = ti.n0 + h * 128 + half * 64;  // first GEMM column of the block
           if (!live || p0 >= a.N) continue;
+          // without a gate N is a multiple of 32 only: the last block may be half a block
+          const bool both = epi_glu(EPI) || p0 + 32 < a.N;
           if (a.bias != nullptr) {
             float b[32];
             const uint16_t* bp = a.bias + (size_t)ti.e * a.N + p0;
             load_bf16x32(bp, b);
 #pragma unroll
             for (int i = 0; i < 32; ++i) v[i] += b[i];
-            load_bf16x32(bp + 32, b);
+            if (both) {
+              load_bf16x32(bp + 32, b);
 #pragma unroll
-            for (int i = 0; i < 32; ++i) v[32 + i] += b[i];
+              for (int i = 0; i < 32; ++i) v[32 + i] += b[i];
+            }
           }
           if (a.pre_out != nullptr && row_ok) {
             uint16_t* pp = a.pre_out + (size_t)row * a.N + p0;
             store_bf16x32(pp, v, !real);
-            store_bf16x32(pp + 32, v + 32, !real);
+            if (both) store_bf16x32(pp + 32, v + 32, !real);
           }
           if (epi_glu(EPI)) {
             float yv[32];
@@ -722,6 +726,7 @@ __global__ void __launch_bounds__(THREADS, 1)
           } else {
 #pragma unroll
             for (int bk = 0; bk < 2; ++bk) {
+              if (bk == 1 && !both) break;
               float yv[32];
 #pragma unroll
               for (int i = 0; i < 32; ++i) yv[i] = real ? act_fwd(a.prm, v[32 * bk + i], 0.0f) * rs : 0.0f;
