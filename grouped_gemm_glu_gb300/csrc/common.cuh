@@ -258,6 +258,8 @@ __host__ __device__ constexpr uint32_t idesc_bf16_f32(int M, int N) {
 __host__ __device__ constexpr uint32_t idesc_mxf8_e8m0(int M, int N) {
   return ((uint32_t)(N >> 3) << 17) | (1u << 23) | ((uint32_t)(M >> 4) << 24);
 }
+// kind::mxf8f6f4: operand B holds E2M1 elements (format code 5, bits 10-12) next to an A of another type
+constexpr uint32_t IDESC_B_E2M1 = 5u << 10;
 // kind::mxf4nvf4: E2M1 operands (format code 1 of that kind), E4M3 scales
 // (scale-format bit 23 clear), fp32 accumulate, both operands K-major.
 __host__ __device__ constexpr uint32_t idesc_nvf4_e4m3(int M, int N) {
@@ -438,6 +440,31 @@ __device__ __forceinline__ uint32_t mx_quant_block32(const float* v, uint32_t* c
     codes[w] = lo | (hi << 16);
   }
   return sb;
+}
+
+// Eight fp32 values (a.x, a.y, b.x, ... d.y) to E2M1, round to nearest even
+// with saturation, packed element 2i in the low nibble of byte i: each
+// cvt...e2m1x2 puts its first source operand in the high nibble, and the
+// four bytes are joined by one vector move.
+__device__ __forceinline__ uint32_t e2m1x8(float2 a, float2 b, float2 c, float2 d) {
+  uint32_t r;
+  asm("{\n\t.reg .b8 q0, q1, q2, q3;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 q0, %2, %1;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 q1, %4, %3;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 q2, %6, %5;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 q3, %8, %7;\n\t"
+      "mov.b32 %0, {q0, q1, q2, q3};\n\t}"
+      : "=r"(r)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y), "f"(d.x), "f"(d.y));
+  return r;
+}
+
+// E8M0 scale byte of an MXFP4 block: shared exponent floor(log2 amax) - 2
+// (E2M1's largest exponent), clamped to the E8M0 range; 0xFF for a non-finite
+// amax.
+__device__ __forceinline__ uint32_t e8m0_fp4_from_amax_bits(uint32_t amax_bits) {
+  const uint32_t ex = amax_bits >> 23;
+  return ex == 0xFFu ? 0xFFu : (ex > 2u ? ex - 2u : 0u);
 }
 
 // ---------------------------------------------------------------------------

@@ -89,6 +89,7 @@ struct Args {
   const int32_t* offsets;
   int E, M, N, K, R_cap;   // K: fixed contraction (M-grouped); M: rows of A (K-grouped)
   int kgrouped;            // 0: FC2 / dX, 1: weight gradient
+  uint32_t b_fmt;          // element type of B in the MMA's instruction descriptor (0: as A)
   int b_pretiled;          // M-grouped: Bs is already in the tensor-core order (sfb_t = Bs; nothing to re-tile)
   int n_tiles_n, m_tiles;  // tiles along N; along M (K-grouped)
   int KB;                  // M-grouped: k-blocks per row tile (K / 128)
@@ -492,6 +493,8 @@ __global__ void __launch_bounds__(THREADS, 1)
 
   if (warp == PRODUCER_WARP) {
     if (lane == 0) {
+      // an unpacking load of 4-bit elements counts the bytes it copies, not the gaps it leaves
+      const uint32_t stage_tx = STAGE_BYTES + SF_ST - (a.b_fmt == IDESC_B_E2M1 ? B_TILE / 2 : 0);
       int stage = 0;
       uint32_t phase = 0, issued = 0, issued_parity = 0;
       for (int t = blockIdx.x; t < total; t += gridDim.x) {
@@ -504,7 +507,7 @@ __global__ void __launch_bounds__(THREADS, 1)
           }
           uint8_t* dst = tiles + stage * STAGE_BYTES;
           uint8_t* sdst = sf + stage * SF_ST;
-          mbar_arrive_expect_tx(full + stage, STAGE_BYTES + SF_ST);
+          mbar_arrive_expect_tx(full + stage, stage_tx);
           if (!a.kgrouped) {
             tma_load_2d(dst, &tmA, full + stage, kb * BK, ti.m0);
             tma_load_3d(dst + A_TILE, &tmB, full + stage, kb * BK, ti.n0, ti.e);
@@ -536,7 +539,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     }
   } else if (warp == MMA_WARP) {
     if (lane == 0) {
-      const uint32_t idesc = NV4 ? idesc_nvf4_e4m3(BM, BN) : idesc_mxf8_e8m0(BM, BN);
+      const uint32_t idesc = (NV4 ? idesc_nvf4_e4m3(BM, BN) : idesc_mxf8_e8m0(BM, BN)) | a.b_fmt;
       int stage = 0;
       uint32_t phase = 0;
       int lt = 0;
@@ -844,6 +847,23 @@ static moe_status_t launch(const CUtensorMap& tmA, const CUtensorMap& tmB, const
   return launch_status();
 }
 
+// Weight operand [E][N][K] of an M-grouped call: MXFP8 codes, or packed MXFP4
+// codes [E][N][Kp / 2] (Kp = K rounded up to 128), which the TMA unpacks on
+// the way: every 16 elements become 16 bytes of shared memory (8 of codes, 8
+// unused), the 4-bit form that kind::mxf8f6f4 reads next to 8-bit elements,
+// so a tile has the size and the swizzle of an 8-bit one while 4 bits per
+// element cross HBM and L2.  (That load wants whole 128-element boxes and
+// 32-byte row pitches: hence Kp.)
+static bool encode_weight(CUtensorMap* tm, const void* W, int E, int N, int K, bool w4) {
+  const uint64_t cols = w4 ? (uint64_t)(K + BK - 1) / BK * BK : (uint64_t)K;
+  const uint64_t pitch = w4 ? cols / 2 : cols;
+  const uint64_t dims[3] = {cols, (uint64_t)N, (uint64_t)E};
+  const uint64_t strides[2] = {pitch, (uint64_t)N * pitch};
+  const uint32_t box[3] = {BK, BN, 1};
+  return encode_tmap(tm, w4 ? CU_TENSOR_MAP_DATA_TYPE_16U4_ALIGN16B : CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, W, dims,
+                     strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
 static size_t align_up(size_t x) { return (x + 255) & ~size_t(255); }
 
 static int n_tiles(int N) { return (N + BN - 1) / BN; }
@@ -902,8 +922,10 @@ extern "C" moe_status_t moe_grouped_fc2_fwd(const moe_in_t* A, const moe_in_t* W
   if (!A || !W || !A->data || !W->data || !counts || !offsets || !out) return MOE_ERR_ARG;
   if (E <= 0 || E > E_MAX || K <= 0 || (K % 32) || N <= 0 || (N % 32) || R_cap <= 0 || (R_cap % BM))
     return MOE_ERR_ARG;
-  // one operand type per MMA (an MXFP8 or NVFP4 weight may carry pre-tiled scales)
-  const bool w_tiled = (A->dtype == MOE_IN_MXFP8 && W->dtype == MOE_IN_MXFP8_TILED) ||
+  // one operand type per MMA (an MXFP8 or NVFP4 weight may carry pre-tiled scales), but for an MXFP4 weight
+  // next to MXFP8 rows
+  const bool w4 = A->dtype == MOE_IN_MXFP8 && W->dtype == MOE_IN_MXFP4;
+  const bool w_tiled = w4 || (A->dtype == MOE_IN_MXFP8 && W->dtype == MOE_IN_MXFP8_TILED) ||
                        (A->dtype == MOE_IN_NVFP4 && W->dtype == MOE_IN_NVFP4_TILED);
   if (sm_margin < 0 || (A->dtype != W->dtype && !w_tiled)) return MOE_ERR_ARG;
   if (out_mode != MOE_OUT_BF16 && out_mode != MOE_OUT_MXFP8 && out_mode != MOE_OUT_NVFP4) return MOE_ERR_ARG;
@@ -981,6 +1003,7 @@ extern "C" moe_status_t moe_grouped_fc2_fwd(const moe_in_t* A, const moe_in_t* W
       (reinterpret_cast<uintptr_t>(Ws) & 3) || (reinterpret_cast<uintptr_t>(ws) & 255))
     return MOE_ERR_ARG;
   if (w_tiled && (reinterpret_cast<uintptr_t>(Ws) & 15)) return MOE_ERR_ARG;  // 16-byte bulk copies
+  if (w4 && (reinterpret_cast<uintptr_t>(Wq) & 31)) return MOE_ERR_ARG;       // the unpacking load
   if (out_mode == MOE_OUT_MXFP8) {
     if (!out->q_row || !out->s_row || (out->q_col == nullptr) != (out->s_col == nullptr)) return MOE_ERR_ARG;
     if (!aligned16(out->q_row) || (out->q_col && !aligned16(out->q_col))) return MOE_ERR_ARG;
@@ -999,13 +1022,7 @@ extern "C" moe_status_t moe_grouped_fc2_fwd(const moe_in_t* A, const moe_in_t* W
     if (!encode_tmap(&tmA, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, Aq, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B))
       return MOE_ERR_CUDA;
   }
-  {
-    const uint64_t dims[3] = {(uint64_t)K, (uint64_t)N, (uint64_t)E};
-    const uint64_t strides[2] = {(uint64_t)K, (uint64_t)N * K};
-    const uint32_t box[3] = {BK, BN, 1};
-    if (!encode_tmap(&tmB, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, Wq, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B))
-      return MOE_ERR_CUDA;
-  }
+  if (!encode_weight(&tmB, Wq, E, N, K, w4)) return MOE_ERR_CUDA;
   Args a{};
   a.counts = counts;
   a.offsets = offsets;
@@ -1026,6 +1043,7 @@ extern "C" moe_status_t moe_grouped_fc2_fwd(const moe_in_t* A, const moe_in_t* W
   a.sfa_t = static_cast<uint8_t*>(ws);
   a.sfb_t = w_tiled ? const_cast<uint8_t*>(Ws) : static_cast<uint8_t*>(ws) + a_bytes;
   a.b_pretiled = w_tiled ? 1 : 0;
+  a.b_fmt = w4 ? IDESC_B_E2M1 : 0u;
   a.out = out->y;
   a.out_f32 = 0;
   a.status = status;
@@ -1044,8 +1062,9 @@ extern "C" moe_status_t moe_grouped_fc2_fwd(const moe_in_t* A, const moe_in_t* W
   return launch(tmA, tmB, nullptr, a, bound, sf_items, sm_margin, as_stream(stream));
 }
 
-extern "C" moe_status_t moe_grouped_fc1_glu_quant_fwd_mxfp8(
-    const uint8_t* xq, const uint8_t* xs, const uint8_t* W1q, const uint8_t* W1s, const moe_bf16* b1p,
+// FC1 on MXFP8 rows; w4: the weight is MXFP4 (scales in the tensor-core order)
+static moe_status_t fc1_mx(
+    const bool w4, const uint8_t* xq, const uint8_t* xs, const uint8_t* W1q, const uint8_t* W1s, const moe_bf16* b1p,
     const float* row_scale, const int32_t* counts, const int32_t* offsets, int E, int H, int F, int R_cap,
     const moe_glu_params_t* params, int out_mode, const moe_act_out_t* out, void* ws, size_t ws_bytes, int sm_margin,
     int32_t* status, moe_stream_t stream) {
@@ -1060,6 +1079,7 @@ extern "C" moe_status_t moe_grouped_fc1_glu_quant_fwd_mxfp8(
   if (!aligned16(xq) || !aligned16(W1q) || (reinterpret_cast<uintptr_t>(xs) & 3) ||
       (reinterpret_cast<uintptr_t>(W1s) & 3) || (reinterpret_cast<uintptr_t>(ws) & 255) || (b1p && !aligned16(b1p)))
     return MOE_ERR_ARG;
+  if (w4 && ((reinterpret_cast<uintptr_t>(W1q) & 31) || !aligned16(W1s))) return MOE_ERR_ARG;  // unpacking load, bulk copies
   if (out->row_dot || out->rht_amax) return MOE_ERR_ARG;
   if (out->pre && !aligned16(out->pre)) return MOE_ERR_ARG;
   if (out_mode == MOE_OUT_MXFP8) {
@@ -1082,13 +1102,7 @@ extern "C" moe_status_t moe_grouped_fc1_glu_quant_fwd_mxfp8(
     if (!encode_tmap(&tmA, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, xq, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B))
       return MOE_ERR_CUDA;
   }
-  {
-    const uint64_t dims[3] = {(uint64_t)H, (uint64_t)N1, (uint64_t)E};
-    const uint64_t strides[2] = {(uint64_t)H, (uint64_t)N1 * H};
-    const uint32_t box[3] = {BK, BN, 1};
-    if (!encode_tmap(&tmB, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, W1q, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B))
-      return MOE_ERR_CUDA;
-  }
+  if (!encode_weight(&tmB, W1q, E, N1, H, w4)) return MOE_ERR_CUDA;
   Args a{};
   a.counts = counts;
   a.offsets = offsets;
@@ -1104,7 +1118,9 @@ extern "C" moe_status_t moe_grouped_fc1_glu_quant_fwd_mxfp8(
   a.As = xs;
   a.Bs = W1s;
   a.sfa_t = static_cast<uint8_t*>(ws);
-  a.sfb_t = static_cast<uint8_t*>(ws) + a_bytes;
+  a.sfb_t = w4 ? const_cast<uint8_t*>(W1s) : static_cast<uint8_t*>(ws) + a_bytes;
+  a.b_pretiled = w4 ? 1 : 0;
+  a.b_fmt = w4 ? IDESC_B_E2M1 : 0u;
   a.status = status;
   a.wait_ns = g_wait_limit_ns.load();
   a.out_mode = out_mode;
@@ -1127,8 +1143,26 @@ extern "C" moe_status_t moe_grouped_fc1_glu_quant_fwd_mxfp8(
   }
   const long long mt_bound = (long long)R_cap / BM + E;
   const long long bound = mt_bound * a.n_tiles_n;
-  const long long sf_items = mt_bound * a.KB + (long long)E * 2 * a.n_tiles_n * a.KB;
+  const long long sf_items = mt_bound * a.KB + (w4 ? 0 : (long long)E * 2 * a.n_tiles_n * a.KB);
   return launch(tmA, tmB, nullptr, a, bound, sf_items, sm_margin, as_stream(stream), epi);
+}
+
+extern "C" moe_status_t moe_grouped_fc1_glu_quant_fwd_mxfp8(
+    const uint8_t* xq, const uint8_t* xs, const uint8_t* W1q, const uint8_t* W1s, const moe_bf16* b1p,
+    const float* row_scale, const int32_t* counts, const int32_t* offsets, int E, int H, int F, int R_cap,
+    const moe_glu_params_t* params, int out_mode, const moe_act_out_t* out, void* ws, size_t ws_bytes, int sm_margin,
+    int32_t* status, moe_stream_t stream) {
+  return fc1_mx(false, xq, xs, W1q, W1s, b1p, row_scale, counts, offsets, E, H, F, R_cap, params, out_mode, out, ws,
+                ws_bytes, sm_margin, status, stream);
+}
+
+extern "C" moe_status_t moe_grouped_fc1_glu_quant_fwd_mxfp4(
+    const uint8_t* xq, const uint8_t* xs, const uint8_t* W1q, const uint8_t* W1s, const moe_bf16* b1p,
+    const float* row_scale, const int32_t* counts, const int32_t* offsets, int E, int H, int F, int R_cap,
+    const moe_glu_params_t* params, int out_mode, const moe_act_out_t* out, void* ws, size_t ws_bytes, int sm_margin,
+    int32_t* status, moe_stream_t stream) {
+  return fc1_mx(true, xq, xs, W1q, W1s, b1p, row_scale, counts, offsets, E, H, F, R_cap, params, out_mode, out, ws,
+                ws_bytes, sm_margin, status, stream);
 }
 
 extern "C" moe_status_t moe_grouped_wgrad(const uint8_t* Aq, const uint8_t* As, const uint8_t* Bq, const uint8_t* Bs,

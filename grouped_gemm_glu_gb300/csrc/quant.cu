@@ -317,23 +317,6 @@ __global__ void __launch_bounds__(256) k_quant_cols(const __grid_constant__ CUte
   }
 }
 
-// Eight fp32 values (a.x, a.y, b.x, ... d.y) to E2M1, round to nearest even
-// with saturation, packed element 2i in the low nibble of byte i: each
-// cvt...e2m1x2 puts its first source operand in the high nibble, and the
-// four bytes are joined by one vector move.
-__device__ __forceinline__ uint32_t e2m1x8(float2 a, float2 b, float2 c, float2 d) {
-  uint32_t r;
-  asm("{\n\t.reg .b8 q0, q1, q2, q3;\n\t"
-      "cvt.rn.satfinite.e2m1x2.f32 q0, %2, %1;\n\t"
-      "cvt.rn.satfinite.e2m1x2.f32 q1, %4, %3;\n\t"
-      "cvt.rn.satfinite.e2m1x2.f32 q2, %6, %5;\n\t"
-      "cvt.rn.satfinite.e2m1x2.f32 q3, %8, %7;\n\t"
-      "mov.b32 %0, {q0, q1, q2, q3};\n\t}"
-      : "=r"(r)
-      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y), "f"(d.x), "f"(d.y));
-  return r;
-}
-
 // One NVFP4 block of 16 values under the per-tensor scale sg: returns the
 // E4M3 block-scale byte and writes the 16 E2M1 codes (element 2i in the low
 // nibble of byte i) to w[0..1].  s_b = E4M3(fp32(amax_b / 6) * sg),

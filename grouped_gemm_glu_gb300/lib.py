@@ -31,7 +31,7 @@ class ActOut(C.Structure):
                 ("rht_amax", C.c_void_p), ("rht_signs", C.c_uint32)]
 
 
-IN_BF16, IN_MXFP8, IN_NVFP4, IN_MXFP8_TILED, IN_NVFP4_TILED = 0, 1, 2, 3, 4
+IN_BF16, IN_MXFP8, IN_NVFP4, IN_MXFP8_TILED, IN_NVFP4_TILED, IN_MXFP4 = 0, 1, 2, 3, 4, 5
 
 
 class InT(C.Structure):
@@ -88,6 +88,12 @@ _SIGS = {
     "moe_mxfp8_tiled_scale_bytes": ([I, I, I], SZ),
     "moe_grouped_fc1_glu_quant_fwd_mxfp8": [P, P, P, P, P, P, P, P, I, I, I, I, C.POINTER(GluParams), I,
                                             C.POINTER(ActOut), P, SZ, I, P, P],
+    "moe_grouped_fc1_glu_quant_fwd_mxfp4": [P, P, P, P, P, P, P, P, I, I, I, I, C.POINTER(GluParams), I,
+                                            C.POINTER(ActOut), P, SZ, I, P, P],
+    "moe_mxfp4_code_bytes": ([I, I, I], SZ),
+    "moe_mxfp4_scale_bytes": ([I, I, I], SZ),
+    "moe_quantize_mxfp4": [P, I, I, I, I, P, P, P, P],
+    "moe_dequantize_mxfp4": [P, P, I, I, I, P, P],
     "moe_grouped_fc2_workspace_size": ([I, I, I, I], SZ),
     "moe_grouped_fc2_fwd": [C.POINTER(InT), C.POINTER(InT), P, P, I, I, I, I, I, C.POINTER(ActOut), P, SZ, I, P, P],
     "moe_grouped_wgrad_workspace_size": ([I, I, I, I], SZ),

@@ -639,3 +639,117 @@ def router_bwd(logits, idx, dprob, params: L.RouterParams):
     L.check(L.load().moe_router_bwd(logits.data_ptr(), b16, idx.data_ptr(), dprob.data_ptr(), T, n, k,
                                     C.byref(params), d.data_ptr(), _cur(logits)), "moe_router_bwd")
     return d
+
+
+def quantize_mxfp4(src, col: bool = False, status=None):
+    """MXFP4 form of a weight src [G, R, C] bf16: (q, s) with q [G, N, Kp/2]
+    uint8 (packed codes, Kp = K rounded up to 128) and s the E8M0 scales in the
+    tensor-core order (flat uint8).  Blocks run along C (N = R, K = C), or with
+    col=True along R (N = C, K = R; the transposed form)."""
+    lib = L.load()
+    _need(src, torch.bfloat16, None, "src")
+    if src.dim() != 3:
+        raise ValueError(f"src: [G, R, C] is needed, got {tuple(src.shape)}")
+    G, R, Cc = src.shape
+    N, K = (Cc, R) if col else (R, Cc)
+    q = torch.empty(G, N, (K + 127) // 128 * 64, dtype=torch.uint8, device=src.device)
+    s = torch.empty(lib.moe_mxfp4_scale_bytes(G, N, K), dtype=torch.uint8, device=src.device)
+    L.check(lib.moe_quantize_mxfp4(src.data_ptr(), G, R, Cc, int(col), q.data_ptr(), s.data_ptr(), _ptr(status),
+                                   _cur(src)), "moe_quantize_mxfp4")
+    return q, s
+
+
+def _mxfp4(q, s, K, what):
+    """Checks an MXFP4 weight of contraction length K; returns (G, N)."""
+    _need(q, torch.uint8, None, what)
+    if q.dim() != 3 or q.shape[2] != (K + 127) // 128 * 64:
+        raise ValueError(f"{what}: [G, N, {(K + 127) // 128 * 64}] codes are needed, got {tuple(q.shape)}")
+    G, N = q.shape[0], q.shape[1]
+    _need(s, torch.uint8, (L.load().moe_mxfp4_scale_bytes(G, N, K),), what + " scales")
+    return G, N
+
+
+def dequantize_mxfp4(q, s, K: int):
+    """The bf16 values [G, N, K] of an MXFP4 weight (q, s)."""
+    G, N = _mxfp4(q, s, K, "q")
+    o = torch.empty(G, N, K, dtype=torch.bfloat16, device=q.device)
+    L.check(L.load().moe_dequantize_mxfp4(q.data_ptr(), s.data_ptr(), G, N, K, o.data_ptr(), _cur(q)),
+            "moe_dequantize_mxfp4")
+    return o
+
+
+def _rows_mxfp8(xq, xs, what):
+    R, K = _need2(xq, torch.uint8, what)
+    _need(xs, torch.uint8, (R, K // 32), what + " scales")
+    return R, K
+
+
+def _groups(counts, offsets, E):
+    _need(counts, torch.int32, (E,), "counts")
+    _need(offsets, torch.int32, (E + 1,), "offsets")
+
+
+def fc2_fwd_mxfp4(Aq, As, Wq, Ws, counts, offsets, sm_margin: int = 0, status=None, out=None):
+    """GroupGemm on MXFP8 rows and an MXFP4 weight: y [R_cap, N] bf16 =
+    A [R_cap, K] . W[e]^T per expert, A as codes and scales [R_cap, K/32], W
+    [E, N, K] as quantize_mxfp4 writes it."""
+    lib = L.load()
+    R_cap, K = _rows_mxfp8(Aq, As, "A")
+    E, N = _mxfp4(Wq, Ws, K, "W")
+    _groups(counts, offsets, E)
+    dev = Aq.device
+    y = torch.empty(R_cap, N, dtype=torch.bfloat16, device=dev) if out is None else _need(
+        out, torch.bfloat16, (R_cap, N), "out")
+    st = status if status is not None else new_status(dev)
+    a_in = L.InT(L.IN_MXFP8, Aq.data_ptr(), As.data_ptr(), None)
+    w_in = L.InT(L.IN_MXFP4, Wq.data_ptr(), Ws.data_ptr(), None)
+    nbytes = lib.moe_grouped_fc2_workspace_size(E, K, N, R_cap)
+    ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+    ao = L.ActOut(y=y.data_ptr())
+    L.check(lib.moe_grouped_fc2_fwd(C.byref(a_in), C.byref(w_in), counts.data_ptr(), offsets.data_ptr(), E, K, N, R_cap,
+                                    L.OUT_BF16, C.byref(ao), ws.data_ptr(), nbytes, sm_margin, st.data_ptr(), _cur(Aq)),
+            "moe_grouped_fc2_fwd (MXFP4)")
+    return y
+
+
+def fc1_fwd_mxfp4(xq, xs, W1q, W1s, counts, offsets, F: int, params: L.GluParams, out_mode: int = L.OUT_MXFP8,
+                  b1p=None, row_scale=None, save_pre: bool = True, with_col: bool = True, sm_margin: int = 0,
+                  status=None) -> dict:
+    """fc1_fwd_mxfp8 with an MXFP4 weight: W1q, W1s the MXFP4 form of the
+    packed W1p [E, N1, H] (quantize_mxfp4)."""
+    lib = L.load()
+    R_cap, H = _rows_mxfp8(xq, xs, "x")
+    E, N1 = _mxfp4(W1q, W1s, H, "W1")
+    _groups(counts, offsets, E)
+    if N1 != (F if params.act == L.ACT["srelu"] else 2 * F):
+        raise ValueError(f"W1: {N1} rows do not match F = {F}")
+    if b1p is not None:
+        _need(b1p, torch.bfloat16, (E, N1), "b1p")
+    if row_scale is not None:
+        _need(row_scale, torch.float32, (R_cap,), "row_scale")
+    dev, u8, new = xq.device, torch.uint8, torch.empty
+    o = {}
+    if out_mode == L.OUT_MXFP8:
+        o["q_row"] = new(R_cap, F, dtype=u8, device=dev)
+        o["s_row"] = new(R_cap, F // 32, dtype=u8, device=dev)
+        if with_col:
+            o["q_col"] = new(F, R_cap, dtype=u8, device=dev)
+            o["s_col"] = new(F, R_cap // 32, dtype=u8, device=dev)
+    else:
+        o["y"] = new(R_cap, F, dtype=torch.bfloat16, device=dev)
+        if out_mode == L.OUT_NVFP4:
+            o["amax"] = torch.zeros(1, dtype=torch.float32, device=dev)
+    if save_pre:
+        o["pre"] = new(R_cap, N1, dtype=torch.bfloat16, device=dev)
+    st = status if status is not None else new_status(dev)
+    nbytes = lib.moe_grouped_fc2_workspace_size(E, H, N1, R_cap)
+    ws = new(nbytes, dtype=u8, device=dev)
+    g = o.get
+    ao = L.ActOut(_ptr(g("q_row")), _ptr(g("s_row")), _ptr(g("q_col")), _ptr(g("s_col")), _ptr(g("y")),
+                  _ptr(g("amax")), _ptr(g("pre")))
+    L.check(lib.moe_grouped_fc1_glu_quant_fwd_mxfp4(
+        xq.data_ptr(), xs.data_ptr(), W1q.data_ptr(), W1s.data_ptr(), _ptr(b1p), _ptr(row_scale), counts.data_ptr(),
+        offsets.data_ptr(), E, H, F, R_cap, C.byref(params), out_mode, C.byref(ao), ws.data_ptr(), nbytes, sm_margin,
+        st.data_ptr(), _cur(xq)), "moe_grouped_fc1_glu_quant_fwd_mxfp4")
+    o["status"] = st
+    return o

@@ -137,8 +137,12 @@ typedef enum {
                              MXFP8 A) whose scales are already in the order the tensor cores copy
                              them, as written by moe_quantize_mxfp8 with col = 2: the call skips
                              their re-tiling.  Scales 16-byte aligned. */
-  MOE_IN_NVFP4_TILED = 4  /* the same for an NVFP4 weight next to an NVFP4 A: scales as written by
+  MOE_IN_NVFP4_TILED = 4, /* the same for an NVFP4 weight next to an NVFP4 A: scales as written by
                              moe_nvfp4_cast_cols_tiled.  Scales 16-byte aligned. */
+  MOE_IN_MXFP4 = 5        /* an MXFP4 weight (the W operand, next to an MXFP8 A): packed E2M1 codes
+                             [E][N][Kp/2] (Kp = K rounded up to 128, zero codes past K; 32-byte
+                             aligned) with E8M0 scales per 32 elements in the tensor-core order, as
+                             written by moe_quantize_mxfp4.  Scales 16-byte aligned. */
 } moe_in_dtype_t;
 
 typedef struct {
@@ -308,7 +312,9 @@ MOE_API size_t moe_grouped_fc2_workspace_size(int E, int K, int N, int R_cap);
  * Operands: A [R_cap][K], W [E][N][K] (K contiguous in both), the same
  * dtype for both (the tensor cores take one operand type per MMA; a W of
  * MOE_IN_MXFP8_TILED / MOE_IN_NVFP4_TILED counts as MXFP8 / NVFP4 and
- * carries its scales in the tensor-core order):
+ * carries its scales in the tensor-core order; the one mixed pair is MXFP8
+ * rows with an MXFP4 weight, which one block-scaled MMA multiplies as they
+ * are):
  *   MOE_IN_MXFP8: E4M3 codes, scale = E8M0 [R_cap][K/32] / [E][N][K/32]
  *                 (4-byte aligned); block-scaled MMA (kind::mxf8f6f4);
  *                 ws = moe_grouped_fc2_workspace_size() bytes, 256-byte
@@ -354,6 +360,44 @@ MOE_API moe_status_t moe_grouped_fc1_glu_quant_fwd_mxfp8(const uint8_t* xq, cons
                                                  const moe_glu_params_t* params, int out_mode,
                                                  const moe_act_out_t* out, void* ws, size_t ws_bytes,
                                                  int sm_margin, int32_t* status, moe_stream_t stream);
+
+/* moe_grouped_fc1_glu_quant_fwd_mxfp8 with an MXFP4 weight: W1q, W1s the
+ * MXFP4 form of the packed W1p [E][N1][H] (moe_quantize_mxfp4, col = 0; W1q
+ * 32-byte, W1s 16-byte aligned).  Same epilogue, outputs and workspace. */
+MOE_API moe_status_t moe_grouped_fc1_glu_quant_fwd_mxfp4(const uint8_t* xq, const uint8_t* xs,
+                                                 const uint8_t* W1q, const uint8_t* W1s,
+                                                 const moe_bf16* b1p, const float* row_scale,
+                                                 const int32_t* counts, const int32_t* offsets,
+                                                 int E, int H, int F, int R_cap,
+                                                 const moe_glu_params_t* params, int out_mode,
+                                                 const moe_act_out_t* out, void* ws, size_t ws_bytes,
+                                                 int sm_margin, int32_t* status, moe_stream_t stream);
+
+/* Bytes of the MXFP4 form of a weight W [G][N][K] (contraction along K):
+ * packed codes, rows of K rounded up to 128 elements; and scales. */
+MOE_API size_t moe_mxfp4_code_bytes(int G, int N, int K);
+MOE_API size_t moe_mxfp4_scale_bytes(int G, int N, int K);
+
+/* MXFP4 cast of a weight (OCP microscaling: E2M1 elements, one E8M0 scale per
+ * 32 along the contraction; scale byte floor(log2 amax) - 2 + 127 clamped to
+ * [0, 254], elements rounded to nearest even and saturated at 6; a block
+ * holding NaN or Inf gets scale 0xFF and codes 7).  src [G][R][C] bf16:
+ *   col == 0: N = R, K = C (blocks along the rows; e.g. W1p [E][N1][H])
+ *   col != 0: N = C, K = R (transposed; e.g. W2 [E][F][H], contracted over F)
+ * q [G][N][Kp/2] (element 2i in the low nibble of byte i, zero codes from K
+ * to Kp), s [G][ceil(N/256)][ceil(K/128)][2][512] bytes: byte 16 l + 4 j + i
+ * of the 512 of (128-row group g of N, 128-element k-block b) = the scale of
+ * row 128 g + 32 j + l, elements 128 b + 32 i .. + 31 (0 past N and K).
+ * R % 32 == 0, C % 32 == 0; src, q and s 16-byte aligned.  status (nullable)
+ * receives MOE_ERR_TIMEOUT if a staged tile never arrives. */
+MOE_API moe_status_t moe_quantize_mxfp4(const moe_bf16* src, int G, int R, int C, int col, uint8_t* q, uint8_t* s,
+                                        int32_t* status, moe_stream_t stream);
+
+/* The values of an MXFP4 weight: out [G][N][K] bf16 = e2m1 * 2^(scale - 127)
+ * (exact while the value is in bf16's range).  K % 32 == 0; q and out 16-byte
+ * aligned. */
+MOE_API moe_status_t moe_dequantize_mxfp4(const uint8_t* q, const uint8_t* s, int G, int N, int K, moe_bf16* out,
+                                          moe_stream_t stream);
 
 /* Bytes of device workspace moe_grouped_wgrad (and moe_grouped_wgrad_nvfp4) needs. */
 MOE_API size_t moe_grouped_wgrad_workspace_size(int E, int M, int N, int R_cap);
