@@ -345,24 +345,41 @@ __global__ void __launch_bounds__(256) k_dgamma_sum(const float* __restrict__ pa
 // MXFP8 rows back to bf16: e4m3 * 2^(s - 127) has at most 4 significant bits,
 // so the result is exact (unless it leaves bf16's range).  One thread per 16
 // codes (16 bytes in, 32 out).
+constexpr int DQ_UNROLL = 4;  // 16-byte loads in flight per thread
 __global__ void __launch_bounds__(256) k_dequant_mxfp8(const uint4* __restrict__ q, const uint8_t* __restrict__ s,
                                                        size_t n16, uint4* __restrict__ out) {
-  for (size_t i = (size_t)blockIdx.x * blockDim.x + threadIdx.x; i < n16; i += (size_t)gridDim.x * blockDim.x) {
-    const uint4 w = __ldg(q + i);
-    const uint32_t sb = __ldg(s + (i >> 1));
-    const float sc = e8m0_value(sb);
-    const uint32_t c[4] = {w.x, w.y, w.z, w.w};
-    float v[16];
+  const size_t step = (size_t)gridDim.x * blockDim.x;
+  for (size_t i0 = (size_t)blockIdx.x * blockDim.x + threadIdx.x; i0 < n16; i0 += DQ_UNROLL * step) {
+    uint4 w[DQ_UNROLL];
+    uint32_t sb[DQ_UNROLL];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const float2 a = e4m3x2_value(c[j] & 0xFFFFu), b = e4m3x2_value(c[j] >> 16);
-      v[4 * j] = a.x * sc;
-      v[4 * j + 1] = a.y * sc;
-      v[4 * j + 2] = b.x * sc;
-      v[4 * j + 3] = b.y * sc;
+    for (int u = 0; u < DQ_UNROLL; ++u) {
+      const size_t i = i0 + u * step;
+      w[u] = make_uint4(0, 0, 0, 0);
+      sb[u] = 0;
+      if (i < n16) {
+        w[u] = __ldg(q + i);
+        sb[u] = __ldg(s + (i >> 1));
+      }
     }
-    out[2 * i] = pack8(v);
-    out[2 * i + 1] = pack8(v + 8);
+#pragma unroll
+    for (int u = 0; u < DQ_UNROLL; ++u) {
+      const size_t i = i0 + u * step;
+      if (i >= n16) break;
+      const float sc = e8m0_value(sb[u]);
+      const uint32_t c[4] = {w[u].x, w[u].y, w[u].z, w[u].w};
+      float v[16];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float2 a = e4m3x2_value(c[j] & 0xFFFFu), b = e4m3x2_value(c[j] >> 16);
+        v[4 * j] = a.x * sc;
+        v[4 * j + 1] = a.y * sc;
+        v[4 * j + 2] = b.x * sc;
+        v[4 * j + 3] = b.y * sc;
+      }
+      out[2 * i] = pack8(v);
+      out[2 * i + 1] = pack8(v + 8);
+    }
   }
 }
 
@@ -484,7 +501,7 @@ extern "C" moe_status_t moe_dequantize_mxfp8(const uint8_t* q, const uint8_t* s,
   if (!q || !s || !out || !aligned16(q) || !aligned16(out)) return MOE_ERR_ARG;
   const size_t n16 = 2 * blocks;
   size_t grid = (n16 + 255) / 256;
-  const size_t cap = (size_t)sm_count() * 16;
+  const size_t cap = (size_t)sm_count() * 8;
   if (cap == 0) return MOE_ERR_CUDA;
   if (grid > cap) grid = cap;
   k_dequant_mxfp8<<<(int)grid, 256, 0, as_stream(stream)>>>(reinterpret_cast<const uint4*>(q), s, n16,

@@ -4,6 +4,7 @@ method is computed here."""
 from __future__ import annotations
 
 import ctypes as C
+import functools
 
 import torch
 
@@ -574,7 +575,7 @@ def rmsnorm_bwd(dy, h, gamma, rstd, dres=None, with_dgamma: bool = True):
     nbytes = 0
     if with_dgamma:
         dgamma = torch.empty(H, dtype=torch.float32, device=dy.device)
-        nbytes = lib.moe_rmsnorm_bwd_workspace_size(T, H)
+        nbytes = _size("moe_rmsnorm_bwd_workspace_size", T, H)
         ws = torch.empty(nbytes, dtype=torch.uint8, device=dy.device)
     L.check(lib.moe_rmsnorm_bwd(dy.data_ptr(), _ptr(dres), h.data_ptr(), gamma.data_ptr(), rstd.data_ptr(), T, H,
                                 dx.data_ptr(), _ptr(dgamma), _ptr(ws), nbytes, _cur(dy)), "moe_rmsnorm_bwd")
@@ -653,19 +654,26 @@ def quantize_mxfp4(src, col: bool = False, status=None):
     G, R, Cc = src.shape
     N, K = (Cc, R) if col else (R, Cc)
     q = torch.empty(G, N, (K + 127) // 128 * 64, dtype=torch.uint8, device=src.device)
-    s = torch.empty(lib.moe_mxfp4_scale_bytes(G, N, K), dtype=torch.uint8, device=src.device)
+    s = torch.empty(_size("moe_mxfp4_scale_bytes", G, N, K), dtype=torch.uint8, device=src.device)
     L.check(lib.moe_quantize_mxfp4(src.data_ptr(), G, R, Cc, int(col), q.data_ptr(), s.data_ptr(), _ptr(status),
                                    _cur(src)), "moe_quantize_mxfp4")
     return q, s
 
 
+@functools.lru_cache(maxsize=1024)
+def _size(name: str, *dims) -> int:
+    """A *_bytes / *_workspace_size entry point: host arithmetic on the shape, asked once per shape."""
+    return getattr(L.load(), name)(*dims)
+
+
 def _mxfp4(q, s, K, what):
     """Checks an MXFP4 weight of contraction length K; returns (G, N)."""
     _need(q, torch.uint8, None, what)
-    if q.dim() != 3 or q.shape[2] != (K + 127) // 128 * 64:
-        raise ValueError(f"{what}: [G, N, {(K + 127) // 128 * 64}] codes are needed, got {tuple(q.shape)}")
-    G, N = q.shape[0], q.shape[1]
-    _need(s, torch.uint8, (L.load().moe_mxfp4_scale_bytes(G, N, K),), what + " scales")
+    shape = q.shape
+    if len(shape) != 3 or shape[2] != (K + 127) // 128 * 64:
+        raise ValueError(f"{what}: [G, N, {(K + 127) // 128 * 64}] codes are needed, got {tuple(shape)}")
+    G, N = shape[0], shape[1]
+    _need(s, torch.uint8, (_size("moe_mxfp4_scale_bytes", G, N, K),), what)
     return G, N
 
 
@@ -680,7 +688,7 @@ def dequantize_mxfp4(q, s, K: int):
 
 def _rows_mxfp8(xq, xs, what):
     R, K = _need2(xq, torch.uint8, what)
-    _need(xs, torch.uint8, (R, K // 32), what + " scales")
+    _need(xs, torch.uint8, (R, K // 32), what)
     return R, K
 
 
@@ -703,7 +711,7 @@ def fc2_fwd_mxfp4(Aq, As, Wq, Ws, counts, offsets, sm_margin: int = 0, status=No
     st = status if status is not None else new_status(dev)
     a_in = L.InT(L.IN_MXFP8, Aq.data_ptr(), As.data_ptr(), None)
     w_in = L.InT(L.IN_MXFP4, Wq.data_ptr(), Ws.data_ptr(), None)
-    nbytes = lib.moe_grouped_fc2_workspace_size(E, K, N, R_cap)
+    nbytes = _size("moe_grouped_fc2_workspace_size", E, K, N, R_cap)
     ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
     ao = L.ActOut(y=y.data_ptr())
     L.check(lib.moe_grouped_fc2_fwd(C.byref(a_in), C.byref(w_in), counts.data_ptr(), offsets.data_ptr(), E, K, N, R_cap,
@@ -728,7 +736,7 @@ def fc1_fwd_mxfp4(xq, xs, W1q, W1s, counts, offsets, F: int, params: L.GluParams
     if row_scale is not None:
         _need(row_scale, torch.float32, (R_cap,), "row_scale")
     dev, u8, new = xq.device, torch.uint8, torch.empty
-    o = {}
+    o, ao = {}, L.ActOut()
     if out_mode == L.OUT_MXFP8:
         o["q_row"] = new(R_cap, F, dtype=u8, device=dev)
         o["s_row"] = new(R_cap, F // 32, dtype=u8, device=dev)
@@ -742,11 +750,10 @@ def fc1_fwd_mxfp4(xq, xs, W1q, W1s, counts, offsets, F: int, params: L.GluParams
     if save_pre:
         o["pre"] = new(R_cap, N1, dtype=torch.bfloat16, device=dev)
     st = status if status is not None else new_status(dev)
-    nbytes = lib.moe_grouped_fc2_workspace_size(E, H, N1, R_cap)
+    nbytes = _size("moe_grouped_fc2_workspace_size", E, H, N1, R_cap)
     ws = new(nbytes, dtype=u8, device=dev)
-    g = o.get
-    ao = L.ActOut(_ptr(g("q_row")), _ptr(g("s_row")), _ptr(g("q_col")), _ptr(g("s_col")), _ptr(g("y")),
-                  _ptr(g("amax")), _ptr(g("pre")))
+    for k, v in o.items():
+        setattr(ao, k, v.data_ptr())
     L.check(lib.moe_grouped_fc1_glu_quant_fwd_mxfp4(
         xq.data_ptr(), xs.data_ptr(), W1q.data_ptr(), W1s.data_ptr(), _ptr(b1p), _ptr(row_scale), counts.data_ptr(),
         offsets.data_ptr(), E, H, F, R_cap, C.byref(params), out_mode, C.byref(ao), ws.data_ptr(), nbytes, sm_margin,
