@@ -258,8 +258,8 @@ __host__ __device__ constexpr uint32_t idesc_bf16_f32(int M, int N) {
 __host__ __device__ constexpr uint32_t idesc_mxf8_e8m0(int M, int N) {
   return ((uint32_t)(N >> 3) << 17) | (1u << 23) | ((uint32_t)(M >> 4) << 24);
 }
-// kind::mxf8f6f4: operand B holds E2M1 elements (format code 5, bits 10-12) next to an A of another type
-constexpr uint32_t IDESC_B_E2M1 = 5u << 10;
+// kind::mxf8f6f4: operand A holds E2M1 elements (format code 5, bits 7-9) next to an E4M3 B
+constexpr uint32_t IDESC_A_E2M1 = 5u << 7;
 // kind::mxf4nvf4: E2M1 operands (format code 1 of that kind), E4M3 scales
 // (scale-format bit 23 clear), fp32 accumulate, both operands K-major.
 __host__ __device__ constexpr uint32_t idesc_nvf4_e4m3(int M, int N) {

@@ -89,7 +89,6 @@ struct Args {
   const int32_t* offsets;
   int E, M, N, K, R_cap;   // K: fixed contraction (M-grouped); M: rows of A (K-grouped)
   int kgrouped;            // 0: FC2 / dX, 1: weight gradient
-  uint32_t b_fmt;          // element type of B in the MMA's instruction descriptor (0: as A)
   int b_pretiled;          // M-grouped: Bs is already in the tensor-core order (sfb_t = Bs; nothing to re-tile)
   int n_tiles_n, m_tiles;  // tiles along N; along M (K-grouped)
   int KB;                  // M-grouped: k-blocks per row tile (K / 128)
@@ -493,8 +492,6 @@ __global__ void __launch_bounds__(THREADS, 1)
 
   if (warp == PRODUCER_WARP) {
     if (lane == 0) {
-      // an unpacking load of 4-bit elements counts the bytes it copies, not the gaps it leaves
-      const uint32_t stage_tx = STAGE_BYTES + SF_ST - (a.b_fmt == IDESC_B_E2M1 ? B_TILE / 2 : 0);
       int stage = 0;
       uint32_t phase = 0, issued = 0, issued_parity = 0;
       for (int t = blockIdx.x; t < total; t += gridDim.x) {
@@ -507,7 +504,7 @@ __global__ void __launch_bounds__(THREADS, 1)
           }
           uint8_t* dst = tiles + stage * STAGE_BYTES;
           uint8_t* sdst = sf + stage * SF_ST;
-          mbar_arrive_expect_tx(full + stage, stage_tx);
+          mbar_arrive_expect_tx(full + stage, STAGE_BYTES + SF_ST);
           if (!a.kgrouped) {
             tma_load_2d(dst, &tmA, full + stage, kb * BK, ti.m0);
             tma_load_3d(dst + A_TILE, &tmB, full + stage, kb * BK, ti.n0, ti.e);
@@ -539,7 +536,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     }
   } else if (warp == MMA_WARP) {
     if (lane == 0) {
-      const uint32_t idesc = (NV4 ? idesc_nvf4_e4m3(BM, BN) : idesc_mxf8_e8m0(BM, BN)) | a.b_fmt;
+      const uint32_t idesc = NV4 ? idesc_nvf4_e4m3(BM, BN) : idesc_mxf8_e8m0(BM, BN);
       int stage = 0;
       uint32_t phase = 0;
       int lt = 0;
@@ -847,23 +844,6 @@ static moe_status_t launch(const CUtensorMap& tmA, const CUtensorMap& tmB, const
   return launch_status();
 }
 
-// Weight operand [E][N][K] of an M-grouped call: MXFP8 codes, or packed MXFP4
-// codes [E][N][Kp / 2] (Kp = K rounded up to 128), which the TMA unpacks on
-// the way: every 16 elements become 16 bytes of shared memory (8 of codes, 8
-// unused), the 4-bit form that kind::mxf8f6f4 reads next to 8-bit elements,
-// so a tile has the size and the swizzle of an 8-bit one while 4 bits per
-// element cross HBM and L2.  (That load wants whole 128-element boxes and
-// 32-byte row pitches: hence Kp.)
-static bool encode_weight(CUtensorMap* tm, const void* W, int E, int N, int K, bool w4) {
-  const uint64_t cols = w4 ? (uint64_t)(K + BK - 1) / BK * BK : (uint64_t)K;
-  const uint64_t pitch = w4 ? cols / 2 : cols;
-  const uint64_t dims[3] = {cols, (uint64_t)N, (uint64_t)E};
-  const uint64_t strides[2] = {pitch, (uint64_t)N * pitch};
-  const uint32_t box[3] = {BK, BN, 1};
-  return encode_tmap(tm, w4 ? CU_TENSOR_MAP_DATA_TYPE_16U4_ALIGN16B : CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, W, dims,
-                     strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
-}
-
 static size_t align_up(size_t x) { return (x + 255) & ~size_t(255); }
 
 static int n_tiles(int N) { return (N + BN - 1) / BN; }
@@ -1011,6 +991,9 @@ extern "C" moe_status_t moe_grouped_fc2_fwd(const moe_in_t* A, const moe_in_t* W
     if (!out->y || !aligned16(out->y)) return MOE_ERR_ARG;
     if (out_mode == MOE_OUT_NVFP4 && !out->amax) return MOE_ERR_ARG;
   }
+  if (w4)
+    return grouped_gemm_mxfp4(Aq, As, Wq, Ws, counts, offsets, E, K, N, R_cap, nullptr, nullptr, nullptr, out_mode, out,
+                              ws, ws_bytes, sm_margin, status, as_stream(stream));
   size_t a_bytes, b_bytes;
   fc2_ws_parts(E, K, N, R_cap, &a_bytes, &b_bytes);
   if (ws_bytes < a_bytes + b_bytes) return MOE_ERR_ARG;
@@ -1022,7 +1005,13 @@ extern "C" moe_status_t moe_grouped_fc2_fwd(const moe_in_t* A, const moe_in_t* W
     if (!encode_tmap(&tmA, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, Aq, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B))
       return MOE_ERR_CUDA;
   }
-  if (!encode_weight(&tmB, Wq, E, N, K, w4)) return MOE_ERR_CUDA;
+  {
+    const uint64_t dims[3] = {(uint64_t)K, (uint64_t)N, (uint64_t)E};
+    const uint64_t strides[2] = {(uint64_t)K, (uint64_t)N * K};
+    const uint32_t box[3] = {BK, BN, 1};
+    if (!encode_tmap(&tmB, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, Wq, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B))
+      return MOE_ERR_CUDA;
+  }
   Args a{};
   a.counts = counts;
   a.offsets = offsets;
@@ -1043,7 +1032,6 @@ extern "C" moe_status_t moe_grouped_fc2_fwd(const moe_in_t* A, const moe_in_t* W
   a.sfa_t = static_cast<uint8_t*>(ws);
   a.sfb_t = w_tiled ? const_cast<uint8_t*>(Ws) : static_cast<uint8_t*>(ws) + a_bytes;
   a.b_pretiled = w_tiled ? 1 : 0;
-  a.b_fmt = w4 ? IDESC_B_E2M1 : 0u;
   a.out = out->y;
   a.out_f32 = 0;
   a.status = status;
@@ -1091,6 +1079,9 @@ static moe_status_t fc1_mx(
   } else {
     return MOE_ERR_ARG;
   }
+  if (w4)
+    return grouped_gemm_mxfp4(xq, xs, W1q, W1s, counts, offsets, E, H, N1, R_cap, params, b1p, row_scale, out_mode, out,
+                              ws, ws_bytes, sm_margin, status, as_stream(stream));
   size_t a_bytes, b_bytes;
   fc2_ws_parts(E, H, N1, R_cap, &a_bytes, &b_bytes);
   if (ws_bytes < a_bytes + b_bytes) return MOE_ERR_ARG;
@@ -1102,7 +1093,13 @@ static moe_status_t fc1_mx(
     if (!encode_tmap(&tmA, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, xq, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B))
       return MOE_ERR_CUDA;
   }
-  if (!encode_weight(&tmB, W1q, E, N1, H, w4)) return MOE_ERR_CUDA;
+  {
+    const uint64_t dims[3] = {(uint64_t)H, (uint64_t)N1, (uint64_t)E};
+    const uint64_t strides[2] = {(uint64_t)H, (uint64_t)N1 * H};
+    const uint32_t box[3] = {BK, BN, 1};
+    if (!encode_tmap(&tmB, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, W1q, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B))
+      return MOE_ERR_CUDA;
+  }
   Args a{};
   a.counts = counts;
   a.offsets = offsets;
@@ -1118,9 +1115,7 @@ static moe_status_t fc1_mx(
   a.As = xs;
   a.Bs = W1s;
   a.sfa_t = static_cast<uint8_t*>(ws);
-  a.sfb_t = w4 ? const_cast<uint8_t*>(W1s) : static_cast<uint8_t*>(ws) + a_bytes;
-  a.b_pretiled = w4 ? 1 : 0;
-  a.b_fmt = w4 ? IDESC_B_E2M1 : 0u;
+  a.sfb_t = static_cast<uint8_t*>(ws) + a_bytes;
   a.status = status;
   a.wait_ns = g_wait_limit_ns.load();
   a.out_mode = out_mode;
@@ -1143,7 +1138,7 @@ static moe_status_t fc1_mx(
   }
   const long long mt_bound = (long long)R_cap / BM + E;
   const long long bound = mt_bound * a.n_tiles_n;
-  const long long sf_items = mt_bound * a.KB + (w4 ? 0 : (long long)E * 2 * a.n_tiles_n * a.KB);
+  const long long sf_items = mt_bound * a.KB + (long long)E * 2 * a.n_tiles_n * a.KB;
   return launch(tmA, tmB, nullptr, a, bound, sf_items, sm_margin, as_stream(stream), epi);
 }
 

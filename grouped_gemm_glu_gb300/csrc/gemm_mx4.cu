@@ -1,0 +1,628 @@
+// Grouped products of MXFP8 rows with MXFP4 weights on tcgen05 CTA pairs:
+//   y[rows of e] = a[rows] . W[e]^T   (FC2, or FC1 with the fused activation)
+// kind::mxf8f6f4 with E2M1 x E4M3 operands, one E8M0 scale per 32 elements of
+// K on each side, fp32 accumulators in tensor memory.
+//
+// The weight is the MMA's M operand and the rows are its N operand, because
+// the weight is what has to be read: an expert with one row costs an N of 32,
+// one with hundreds an N of up to 224.  A pair (cluster of two CTAs,
+// cta_group::2) computes 256 weight rows x N rows: each CTA holds 128 weight
+// rows and half of the N rows in its shared memory, so a 128-wide step of K
+// moves 16 + 16 KB into and out of an SM's shared memory where one CTA on a
+// 128 x 256 tile moves 16 + 32 KB; the shared-memory port (128 bytes a clock),
+// not the tensor core, bounds the latter.
+//
+// Weights cross HBM and L2 as 4 bits: the TMA unpacks every 16 elements into
+// 16 bytes of shared memory (8 of codes, 8 unused), the form in which this MMA
+// kind reads 4-bit elements next to 8-bit ones.
+//
+// An expert's rows (padded to 32) are cut into ceil(blocks / 7) tiles of
+// nearly equal numbers of 32-row blocks, so no tile is a sliver.  Two
+// accumulators of 224 columns and the scales fill the 512 columns of tensor
+// memory: a tile is written out while the next one is multiplied.
+//
+// Two launches: k_mx4_scales gathers the rows' scales of every row tile into
+// the order tcgen05.cp consumes (byte 16 l + 4 j + i of 512 = row 32 j + l,
+// k sub-block i; [row tile][k-block][2][512]), k_grouped_mx4 multiplies.  The
+// second is launched as a programmatic dependent of the first: its prologue
+// runs meanwhile, and only its producer waits.  (Gathering inside the second
+// kernel, by a warp that wrote the stage's scales itself, took 1 to 2 us per
+// k-block: four times the MMAs.)
+//
+// Warps (10 per CTA, one CTA per SM, persistent over the tiles):
+//   0-7  epilogue: warp (q, h) takes the 32 weight rows of lane quarter q and
+//        the 32-row groups h, h + 2, ...; a thread owns one output column and
+//        32 rows.  GLU: quarters 2i / 2i + 1 hold the input / gate halves of
+//        one packed block of 64, the gate warp hands its values over through
+//        shared memory
+//   8    TMA producer: weight tile, row tile and both scale blocks of each
+//        k-block; all complete on the even CTA's stage barrier
+//   9    tensor-memory owner; in the even CTA the MMA issuer: scales into
+//        tensor memory (tcgen05.cp), then 4 MMAs of K = 32
+// Every wait is bounded (MOE_ERR_TIMEOUT + early exit, never a trap).
+#include "common.cuh"
+#include "epilogue.cuh"
+#include "host_common.h"
+
+namespace moeglu {
+namespace gmx4 {
+
+constexpr int BW = 128;             // weight rows per CTA
+constexpr int BK = 128;             // elements of K per k-block
+constexpr int NB_MAX = 7;           // 32-row blocks per tile
+constexpr int NT_MAX = 32 * NB_MAX;
+constexpr int EPI_WARPS = 8;
+constexpr int PRODUCER_WARP = 8, MMA_WARP = 9;
+constexpr int THREADS = 10 * 32;
+constexpr int W_TILE = BW * BK;                // unpacked
+constexpr int W_TX = BW * BK / 2;              // bytes the unpacking load counts
+constexpr int X_TILE = NT_MAX / 2 * BK;
+constexpr int STAGE_BYTES = W_TILE + (X_TILE + 1023) / 1024 * 1024;
+constexpr int SF_STAGE = 512 + 1024;           // weight block, two blocks of rows
+constexpr int STAGES = 6;
+constexpr int SCRATCH = 1024;                  // per epilogue warp
+constexpr int E_MAX = 1024;
+constexpr int OFF_SF = STAGES * STAGE_BYTES;
+constexpr int OFF_SCRATCH = OFF_SF + STAGES * SF_STAGE;
+constexpr int OFF_PREF = OFF_SCRATCH + EPI_WARPS * SCRATCH;
+constexpr int OFF_BARS = OFF_PREF + (E_MAX + 2) * 4;
+constexpr int NUM_BARS = 2 * STAGES + 5;
+constexpr int OFF_MISC = OFF_BARS + NUM_BARS * 8;
+constexpr int SMEM_BYTES = 1024 + OFF_MISC + 64;
+static_assert(SMEM_BYTES <= 232448, "shared memory budget");
+static_assert(OFF_BARS % 8 == 0 && OFF_SF % 1024 == 0 && OFF_SCRATCH % 16 == 0, "alignment");
+constexpr uint32_t TMEM_COLS = 512;
+constexpr uint32_t SFW_COL = 2 * NT_MAX, SFX_COL = SFW_COL + 4;  // 4 + 8 columns of scales
+static_assert(SFX_COL + 8 <= TMEM_COLS, "tensor memory");
+
+struct Args {
+  const int32_t* counts;
+  const int32_t* offsets;
+  int E, N, K, R_cap, n_tiles, num_kb;
+  const uint8_t* xs;  // scales of the rows, [R_cap][K/32]
+  uint8_t* xs_tiled;  // [row tile][num_kb][2][512]
+  int mt_cap;         // row tiles that fit xs_tiled
+  int32_t* status;
+  uint64_t wait_ns;
+  const uint16_t* bias;    // [E][N] bf16 or null
+  const float* row_scale;  // [R_cap] or null
+  uint16_t* pre_out;       // [R_cap][N] bf16 or null
+  GluParams prm;
+  // outputs (emit_block_t)
+  int out_mode, out_N;
+  uint8_t* q_row;
+  uint8_t* s_row;
+  uint8_t* q_col;
+  uint8_t* s_col;
+  uint16_t* y;
+  float* amax;
+  float* rht_amax;  // null: the rotated amax belongs to the backward
+  uint32_t rht_signs;
+};
+
+enum Epi { PLAIN = 0, GLU = 1, GLU_L1 = 2, GLU_L2 = 3, GLU_L3 = 4, ELT = 5 };
+
+__device__ __forceinline__ void umma_mxf8_pair(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                               uint32_t sfa_tmem, uint32_t sfb_tmem, uint32_t accumulate) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %6, 0;\n"
+      " tcgen05.mma.cta_group::2.kind::mxf8f6f4.block_scale [%0], %1, %2, %3, [%4], [%5], p;\n}\n" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(sfa_tmem), "r"(sfb_tmem), "r"(accumulate)
+      : "memory");
+}
+// In each CTA of the pair: 32 rows x 16 bytes of its own shared memory into 4
+// columns of each 32-lane sub-partition of its tensor memory.
+__device__ __forceinline__ void tc_cp_32x128b_x4_pair(uint32_t taddr, uint64_t sdesc) {
+  asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(sdesc) : "memory");
+}
+
+struct Tile {
+  int e, n0;      // expert, first weight row of the pair's tile
+  int mt;         // row tile (over all experts)
+  int row0;       // first row
+  int nb, valid;  // 32-row blocks, real rows
+};
+
+__device__ __forceinline__ int row_blocks(int count) { return (max(count, 0) + 31) / 32; }
+
+// Row tile m of expert e, which has mt of them.
+__device__ __forceinline__ void row_tile(const Args& a, int e, int m, int mt, Tile& ti) {
+  const int cnt = __ldg(a.counts + e), off = __ldg(a.offsets + e);
+  const int blocks = row_blocks(cnt);
+  const int b0 = (int)((long long)m * blocks / mt), b1 = (int)((long long)(m + 1) * blocks / mt);
+  ti.e = e;
+  ti.row0 = off + 32 * b0;
+  // (offsets and counts are device data: a tile never reaches past the buffers)
+  ti.nb = off < 0 ? 0 : max(0, min(b1 - b0, (a.R_cap - ti.row0) / 32));
+  ti.valid = min(cnt - 32 * b0, 32 * ti.nb);
+}
+
+__device__ __forceinline__ int find_expert(const int32_t* pref, int E, int x, int mul) {
+  int lo = 0, hi = E - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (pref[mid] * mul <= x) lo = mid; else hi = mid - 1;
+  }
+  return lo;
+}
+
+__device__ __forceinline__ Tile decode(int t, const int32_t* pref, const Args& a) {
+  const int e = find_expert(pref, a.E, t, a.n_tiles);
+  const int mt = pref[e + 1] - pref[e];
+  const int local = t - pref[e] * a.n_tiles;
+  const int n = local / mt, m = local - n * mt;  // row tiles of one weight tile follow each other (the weight stays in L2)
+  Tile ti;
+  row_tile(a, e, m, mt, ti);
+  ti.n0 = n * 2 * BW;
+  ti.mt = pref[e] + m;
+  if (ti.mt >= a.mt_cap) ti.nb = 0;  // (only with counts that exceed the buffers)
+  return ti;
+}
+
+// Row tiles per expert -> exclusive prefix pref[0..E] (whole CTA).
+__device__ __forceinline__ void build_prefix(const Args& a, int32_t* pref) {
+  const int E = a.E, lane = threadIdx.x & 31;
+  for (int e = threadIdx.x; e < E; e += blockDim.x)
+    pref[e + 1] = (row_blocks(__ldg(a.counts + e)) + NB_MAX - 1) / NB_MAX;
+  if (threadIdx.x == 0) pref[0] = 0;
+  __syncthreads();
+  if (threadIdx.x < 32) {
+    const int per = (E + 31) / 32;
+    const int beg = 1 + lane * per, end = min(E + 1, beg + per);
+    int sum = 0;
+    for (int i = beg; i < end; ++i) sum += pref[i];
+    int incl = sum;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int v = __shfl_up_sync(0xFFFFFFFFu, incl, d);
+      if (lane >= d) incl += v;
+    }
+    int run = incl - sum;
+    for (int i = beg; i < end; ++i) {
+      run += pref[i];
+      pref[i] = run;
+    }
+  }
+  __syncthreads();
+}
+
+__device__ __forceinline__ void launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void wait_for_primary() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+__device__ __forceinline__ void warp_pair_sync(int id) { asm volatile("bar.sync %0, 64;" ::"r"(id) : "memory"); }
+
+template <int EPI>
+__device__ __forceinline__ float activate(const GluParams& p, float u, float g) {
+  if (EPI == GLU_L1) return swiglu_fwd_lean(p, u, g);
+  if (EPI == GLU_L2) return swiglu_fwd_lean_clamped(p, u, g);
+  if (EPI == GLU_L3) return geglu_fwd_lean(p, u, g);
+  return act_fwd(p, u, g);
+}
+
+// One tile of this CTA: accumulator lane i is weight row n0 + 128 rank + i,
+// column j is row row0 + j.
+template <int EPI>
+__device__ __forceinline__ void epilogue(const Args& a, const Tile& ti, uint32_t tacc, int q, int h, int lane, int rank,
+                                         uint8_t* scratch, Amax& amax_bits) {
+  const int colbase = ti.n0 + rank * BW + q * 32;
+  if (colbase >= a.N) return;  // N is a multiple of 64 (gated) or 32: warps that share a block drop out together
+  const int col = colbase + lane;
+  const float bias = a.bias != nullptr ? bf16_lo(__ldg(a.bias + (size_t)ti.e * a.N + col)) : 0.0f;
+  constexpr bool GATED = EPI >= GLU && EPI <= GLU_L3;
+#pragma unroll 1
+  for (int g = h; g < ti.nb; g += 2) {
+    const int rb = ti.row0 + 32 * g;
+    const int nvalid = max(0, min(32, ti.valid - 32 * g));
+    float v[32];
+    tmem_ld32(tacc + 32 * g, v);
+#pragma unroll
+    for (int j = 0; j < 32; ++j) v[j] = j < nvalid ? v[j] + bias : 0.0f;
+    if (EPI != PLAIN && a.pre_out != nullptr) {
+#pragma unroll
+      for (int j = 0; j < 32; ++j)
+        a.pre_out[(size_t)(rb + j) * a.N + col] = __bfloat16_as_ushort(__float2bfloat16_rn(v[j]));
+    }
+    if (GATED) {
+      // the two warps' 2 KB of scratch: 16 rows x 32 lanes at a time
+      float* xs = reinterpret_cast<float*>(scratch);
+      const bool gate_warp = (q & 1) != 0;
+      const int id = 1 + h * 2 + (q >> 1);
+      float gate[32];
+#pragma unroll
+      for (int hf = 0; hf < 2; ++hf) {
+        warp_pair_sync(id);  // the input warp has read what was there
+        if (gate_warp) {
+#pragma unroll
+          for (int j = 0; j < 16; ++j) xs[j * 32 + lane] = v[16 * hf + j];
+        }
+        warp_pair_sync(id);
+        if (!gate_warp) {
+#pragma unroll
+          for (int j = 0; j < 16; ++j) gate[16 * hf + j] = xs[j * 32 + lane];
+        }
+      }
+      if (gate_warp) continue;
+#pragma unroll
+      for (int j = 0; j < 32; ++j) {
+        const float rs = (a.row_scale != nullptr && j < nvalid) ? __ldg(a.row_scale + rb + j) : 1.0f;
+        v[j] = j < nvalid ? activate<EPI>(a.prm, v[j], gate[j]) * rs : 0.0f;
+      }
+      emit_block_t(a, v, (colbase / 64) * 32 + lane, rb, lane, amax_bits);
+    } else {
+      if (EPI == ELT) {
+#pragma unroll
+        for (int j = 0; j < 32; ++j) {
+          const float rs = (a.row_scale != nullptr && j < nvalid) ? __ldg(a.row_scale + rb + j) : 1.0f;
+          v[j] = j < nvalid ? act_fwd(a.prm, v[j], 0.0f) * rs : 0.0f;
+        }
+      }
+      emit_block_t(a, v, col, rb, lane, amax_bits);
+    }
+  }
+}
+
+// The four scale bytes that start `at` bytes into the rows' scales (4-byte
+// aligned base, `total` bytes, a multiple of 4).  At a row's end, bytes of
+// the next row may fill the word: no MMA reads them.
+__device__ __forceinline__ uint32_t row_scales(const uint8_t* base, size_t at, size_t total) {
+  const size_t w = at & ~(size_t)3;
+  const int sh = (int)(at & 3) * 8;
+  const uint32_t lo = __ldg(reinterpret_cast<const uint32_t*>(base + w));
+  if (sh == 0) return lo;
+  const uint32_t hi = w + 4 < total ? __ldg(reinterpret_cast<const uint32_t*>(base + w + 4)) : 0u;
+  return __funnelshift_r(lo, hi, sh);
+}
+
+// One warp per (row tile, k-block).
+__global__ void __launch_bounds__(256) k_mx4_scales(const Args a) {
+  __shared__ int32_t pref[E_MAX + 2];
+  launch_dependents();
+  build_prefix(a, pref);
+  if (__ldg(a.offsets + a.E) > a.R_cap) return;
+  const int lane = threadIdx.x & 31, warps = blockDim.x >> 5;
+  const int ks = a.K / 32;
+  const size_t total = (size_t)a.R_cap * ks;
+  const int items = min(pref[a.E], a.mt_cap) * a.num_kb;
+  for (int it = blockIdx.x * warps + (threadIdx.x >> 5); it < items; it += gridDim.x * warps) {
+    const int mt = it / a.num_kb, kb = it - mt * a.num_kb;
+    const int e = find_expert(pref, a.E, mt, 1);
+    Tile ti;
+    row_tile(a, e, mt - pref[e], pref[e + 1] - pref[e], ti);
+    uint32_t v[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      v[j] = j < ti.nb ? row_scales(a.xs, (size_t)(ti.row0 + 32 * j + lane) * ks + 4 * kb, total) : 0u;
+    uint4* dst = reinterpret_cast<uint4*>(a.xs_tiled + (size_t)it * 1024);
+    dst[lane] = make_uint4(v[0], v[1], v[2], v[3]);
+    if (ti.nb > 4) dst[32 + lane] = make_uint4(v[4], v[5], v[6], v[7]);
+  }
+}
+
+template <int EPI>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
+    k_grouped_mx4(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX64,
+                  const __grid_constant__ CUtensorMap tmX32, const __grid_constant__ CUtensorMap tmX16,
+                  const __grid_constant__ CUtensorMap tmWs, const __grid_constant__ CUtensorMap tmXs, const Args a) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* sf = smem + OFF_SF;
+  uint8_t* scratch_all = smem + OFF_SCRATCH;
+  int32_t* pref = reinterpret_cast<int32_t*>(smem + OFF_PREF);
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + OFF_BARS);
+  uint64_t* empty = full + STAGES;
+  uint64_t* acc_full = full + 2 * STAGES;
+  uint64_t* acc_empty = acc_full + 2;
+  uint64_t* mma_done = acc_empty + 2;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + OFF_MISC);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + OFF_MISC + 4);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int E = a.E;
+  const int rank = (int)cluster_ctarank();
+  const int cl = blockIdx.x >> 1, ncl = gridDim.x >> 1;
+
+  if (warp == PRODUCER_WARP && lane == 0) {
+    for (int s = 0; s < STAGES; ++s) {
+      mbar_init(full + s, 1);
+      mbar_init(empty + s, 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(acc_full + b, 1);
+      mbar_init(acc_empty + b, 2 * EPI_WARPS);
+    }
+    mbar_init(mma_done, 1);
+    *abort_flag = 0;
+    fence_barrier_init();
+    fence_async_shared();
+    tma_prefetch_desc(&tmW);
+    tma_prefetch_desc(&tmX64);
+    tma_prefetch_desc(&tmX32);
+    tma_prefetch_desc(&tmX16);
+    tma_prefetch_desc(&tmWs);
+    tma_prefetch_desc(&tmXs);
+  }
+  if (warp == MMA_WARP) {
+    tmem_alloc_pair(tmem_slot, TMEM_COLS);
+    tmem_relinquish_pair();
+  }
+  build_prefix(a, pref);
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();  // both CTAs' barriers and tensor memory exist before any cross-CTA use
+  tc_fence_after();
+  const uint32_t tmem_base = *tmem_slot;
+  const bool over = __ldg(a.offsets + E) > a.R_cap;
+  if (over && threadIdx.x == 0) set_status(a.status, MOE_ERR_CAPACITY);
+  const int total = over ? 0 : pref[E] * a.n_tiles;
+  WaitGuard guard{abort_flag, a.status, a.wait_ns};
+
+  if (warp == PRODUCER_WARP) {
+    if (lane == 0) {
+      int stage = 0;
+      uint32_t phase = 0, issued = 0, issued_parity = 0;
+      wait_for_primary();  // the tiled scales of the rows (in every CTA: the grid ends after its primary)
+      for (int t = cl; t < total; t += ncl) {
+        const Tile ti = decode(t, pref, a);
+        if (ti.nb == 0) continue;
+        const uint32_t tx = 2u * (W_TX + SF_STAGE) + (uint32_t)ti.nb * 32 * BK;  // both CTAs' bytes
+        const int xrow = ti.row0 + rank * 16 * ti.nb;
+        const int ws_row = (ti.e * a.n_tiles + ti.n0 / (2 * BW)) * a.num_kb * 2 + rank, xs_row = ti.mt * a.num_kb * 2;
+        bool ok = true;
+        for (int kb = 0; kb < a.num_kb; ++kb) {
+          if (!mbar_wait(empty + stage, phase ^ 1u, guard)) {
+            ok = false;
+            break;
+          }
+          uint8_t* dst = smem + stage * STAGE_BYTES;
+          const uint32_t bar = mapa_shared(smem_u32(full + stage), 0);
+          if (rank == 0) mbar_arrive_expect_tx(full + stage, tx);
+          tma_load_3d_pair(dst, &tmW, bar, kb * BK, ti.n0 + rank * BW, ti.e);
+          // this CTA's 16 nb rows in boxes of 64, 32 and 16
+          uint8_t* xd = dst + W_TILE;
+          int r = 0;
+          if (ti.nb & 4) {
+            tma_load_2d_pair(xd, &tmX64, bar, kb * BK, xrow);
+            r = 64;
+          }
+          if (ti.nb & 2) {
+            tma_load_2d_pair(xd + r * BK, &tmX32, bar, kb * BK, xrow + r);
+            r += 32;
+          }
+          if (ti.nb & 1) tma_load_2d_pair(xd + r * BK, &tmX16, bar, kb * BK, xrow + r);
+          uint8_t* sd = sf + stage * SF_STAGE;
+          tma_load_2d_pair(sd, &tmWs, bar, 0, ws_row + 2 * kb);
+          tma_load_2d_pair(sd + 512, &tmXs, bar, 0, xs_row + 2 * kb);
+          issued |= 1u << stage;
+          issued_parity = (issued_parity & ~(1u << stage)) | (phase << stage);
+          if (++stage == STAGES) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+        if (!ok) break;
+      }
+      if (rank == 0 && *abort_flag) {  // let the copies in flight land (they complete on this CTA's barriers)
+        volatile int never = 0;
+        WaitGuard drain{&never, a.status, 100000000ull};
+        for (int s = 0; s < STAGES; ++s)
+          if (issued & (1u << s)) mbar_wait(full + s, (issued_parity >> s) & 1u, drain);
+      }
+    }
+  } else if (warp == MMA_WARP) {
+    if (lane == 0 && rank == 0) {
+      int stage = 0, lt = 0;
+      uint32_t phase = 0;
+      for (int t = cl; t < total; t += ncl) {
+        const Tile ti = decode(t, pref, a);
+        if (ti.nb == 0) continue;
+        const int buf = lt & 1;
+        const uint32_t aph = (uint32_t)(lt >> 1) & 1u;
+        ++lt;
+        if (!mbar_wait_cluster(acc_empty + buf, aph ^ 1u, guard)) break;
+        tc_fence_after();
+        const uint32_t idesc = idesc_mxf8_e8m0(2 * BW, 32 * ti.nb) | IDESC_A_E2M1;
+        const uint32_t d_tmem = tmem_base + (uint32_t)(buf * NT_MAX);
+        bool ok = true;
+        for (int kb = 0; kb < a.num_kb; ++kb) {
+          if (!mbar_wait_cluster(full + stage, phase, guard)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t w_addr = smem_u32(smem + stage * STAGE_BYTES);
+          const uint32_t sf_addr = smem_u32(sf + stage * SF_STAGE);
+          tc_cp_32x128b_x4_pair(tmem_base + SFW_COL, sdesc_noswizzle(sf_addr, 128));
+          tc_cp_32x128b_x4_pair(tmem_base + SFX_COL, sdesc_noswizzle(sf_addr + 512, 128));
+          if (ti.nb > 4) tc_cp_32x128b_x4_pair(tmem_base + SFX_COL + 4, sdesc_noswizzle(sf_addr + 1024, 128));
+          const uint64_t wd = sdesc_kmajor_sw128(w_addr), xd = sdesc_kmajor_sw128(w_addr + W_TILE);
+          const int nsub = min(4, (a.K - kb * BK) / 32);
+          if (nsub == 4) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              umma_mxf8_pair(d_tmem, wd + 2 * k, xd + 2 * k, idesc_with_sf_ids(idesc, (uint32_t)k, (uint32_t)k),
+                             tmem_base + SFW_COL, tmem_base + SFX_COL, (kb | k) != 0 ? 1u : 0u);
+          } else {
+            for (int k = 0; k < nsub; ++k)
+              umma_mxf8_pair(d_tmem, wd + 2 * k, xd + 2 * k, idesc_with_sf_ids(idesc, (uint32_t)k, (uint32_t)k),
+                             tmem_base + SFW_COL, tmem_base + SFX_COL, (kb | k) != 0 ? 1u : 0u);
+          }
+          tc_commit_pair_mc(empty + stage, 0x3);
+          if (++stage == STAGES) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+        if (!ok) break;
+        tc_commit_pair_mc(acc_full + buf, 0x3);
+      }
+      tc_commit_pair_mc(mma_done, 0x1);
+      volatile int never = 0;
+      WaitGuard drain{&never, a.status, 100000000ull};
+      mbar_wait(mma_done, 0, drain);
+    }
+  } else {
+    const int q = warp & 3, h = warp >> 2;
+    Amax amax_bits{0u, 0u};
+    int lt = 0;
+    for (int t = cl; t < total; t += ncl) {
+      const Tile ti = decode(t, pref, a);
+      if (ti.nb == 0) continue;
+      const int buf = lt & 1;
+      const uint32_t aph = (uint32_t)(lt >> 1) & 1u;
+      ++lt;
+      int ok = 1;
+      if (lane == 0) ok = mbar_wait(acc_full + buf, aph, guard) ? 1 : 0;
+      if (!__shfl_sync(0xFFFFFFFFu, ok, 0)) break;
+      tc_fence_after();
+      epilogue<EPI>(a, ti, tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(buf * NT_MAX), q, h, lane, rank,
+                    scratch_all + (warp & ~1) * SCRATCH, amax_bits);
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(acc_empty + buf), 0));
+    }
+    if (a.out_mode == MOE_OUT_NVFP4 && a.amax != nullptr) {
+      const uint32_t m = __reduce_max_sync(0xFFFFFFFFu, amax_bits.plain);
+      if (lane == 0 && m != 0) atomicMax(reinterpret_cast<int*>(a.amax), (int)m);
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();  // no CTA leaves while its peer may still touch its memory
+  if (warp == MMA_WARP) {
+    tc_fence_after();
+    tmem_dealloc_pair(tmem_base, TMEM_COLS);
+  }
+}
+
+struct Maps {
+  CUtensorMap w, x64, x32, x16, ws, xs;
+};
+
+template <int EPI>
+static moe_status_t launch(const Maps& m, const Args& a, int sm_margin, cudaStream_t stream) {
+  const void* kfn = (const void*)k_grouped_mx4<EPI>;
+  if (!set_smem_limit(kfn, SMEM_BYTES)) return MOE_ERR_CUDA;
+  const int sms = sm_count();
+  int clusters = max_active_pairs(kfn, THREADS, SMEM_BYTES);
+  if (clusters <= 0 || sms <= 0) return MOE_ERR_CUDA;
+  const int by_margin = (sms - sm_margin) / 2;
+  if (clusters > by_margin) clusters = by_margin;
+  const long long tiles_bound = (long long)a.mt_cap * a.n_tiles;
+  if (clusters > tiles_bound) clusters = (int)tiles_bound;
+  if (clusters < 1) clusters = 1;
+  const long long items = ((long long)a.mt_cap * a.num_kb + 7) / 8;
+  k_mx4_scales<<<(int)(items < 8ll * sms ? items : 8ll * sms), 256, 0, stream>>>(a);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(2 * clusters);
+  cfg.blockDim = dim3(THREADS);
+  cfg.dynamicSmemBytes = SMEM_BYTES;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, k_grouped_mx4<EPI>, m.w, m.x64, m.x32, m.x16, m.ws, m.xs, a) != cudaSuccess)
+    return MOE_ERR_CUDA;
+  count_launch(2);
+  return launch_status();
+}
+
+// Row tiles a call can have: at most one partly filled tile per expert.
+static int row_tiles_cap(int E, int R_cap) { return R_cap / NT_MAX + E; }
+
+}  // namespace gmx4
+
+size_t grouped_gemm_mxfp4_workspace(int E, int K, int R_cap) {
+  return (size_t)gmx4::row_tiles_cap(E, R_cap) * ((K + gmx4::BK - 1) / gmx4::BK) * 1024;
+}
+
+// See host_common.h.  The entry points (gemm_mx.cu) have checked the arguments.
+moe_status_t grouped_gemm_mxfp4(const uint8_t* xq, const uint8_t* xs, const uint8_t* wq, const uint8_t* ws,
+                                const int32_t* counts, const int32_t* offsets, int E, int K, int N, int R_cap,
+                                const moe_glu_params_t* params, const moe_bf16* bias, const float* row_scale,
+                                int out_mode, const moe_act_out_t* out, void* work, size_t work_bytes, int sm_margin,
+                                int32_t* status, cudaStream_t stream) {
+  using namespace gmx4;
+  const int n_tiles = (N + 2 * BW - 1) / (2 * BW), num_kb = (K + BK - 1) / BK, mt_cap = row_tiles_cap(E, R_cap);
+  if (!work || (reinterpret_cast<uintptr_t>(work) & 255) || work_bytes < grouped_gemm_mxfp4_workspace(E, K, R_cap))
+    return MOE_ERR_ARG;
+  if ((long long)E * n_tiles * num_kb * 2 > INT32_MAX || (long long)mt_cap * num_kb * 2 > INT32_MAX ||
+      (long long)mt_cap * n_tiles > INT32_MAX)
+    return MOE_ERR_ARG;
+  Maps m;
+  {
+    // the unpacking load wants whole 128-element boxes and 32-byte row pitches
+    const uint64_t kp = (uint64_t)(K + BK - 1) / BK * BK;
+    const uint64_t dims[3] = {kp, (uint64_t)N, (uint64_t)E};
+    const uint64_t strides[2] = {kp / 2, (uint64_t)N * (kp / 2)};
+    const uint32_t box[3] = {BK, BW, 1};
+    if (!encode_tmap(&m.w, CU_TENSOR_MAP_DATA_TYPE_16U4_ALIGN16B, 3, wq, dims, strides, box,
+                     CU_TENSOR_MAP_SWIZZLE_128B))
+      return MOE_ERR_CUDA;
+  }
+  CUtensorMap* xmaps[3] = {&m.x64, &m.x32, &m.x16};
+  for (int i = 0; i < 3; ++i) {
+    const uint64_t dims[2] = {(uint64_t)K, (uint64_t)R_cap};
+    const uint64_t strides[1] = {(uint64_t)K};
+    const uint32_t box[2] = {BK, 64u >> i};
+    if (!encode_tmap(xmaps[i], CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, xq, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B))
+      return MOE_ERR_CUDA;
+  }
+  for (int i = 0; i < 2; ++i) {  // scale blocks as rows of 128 words: one of the weight's, two of the rows'
+    const uint64_t dims[2] = {128, 2 * (i == 0 ? (uint64_t)E * n_tiles * num_kb : (uint64_t)mt_cap * num_kb)};
+    const uint64_t strides[1] = {512};
+    const uint32_t box[2] = {128, i == 0 ? 1u : 2u};
+    if (!encode_tmap(i == 0 ? &m.ws : &m.xs, CU_TENSOR_MAP_DATA_TYPE_UINT32, 2, i == 0 ? (const void*)ws : work, dims,
+                     strides, box, CU_TENSOR_MAP_SWIZZLE_NONE))
+      return MOE_ERR_CUDA;
+  }
+  Args a{};
+  a.counts = counts;
+  a.offsets = offsets;
+  a.E = E;
+  a.N = N;
+  a.K = K;
+  a.R_cap = R_cap;
+  a.n_tiles = n_tiles;
+  a.num_kb = num_kb;
+  a.xs = xs;
+  a.xs_tiled = static_cast<uint8_t*>(work);
+  a.mt_cap = mt_cap;
+  a.status = status;
+  a.wait_ns = g_wait_limit_ns.load();
+  a.bias = reinterpret_cast<const uint16_t*>(bias);
+  a.row_scale = row_scale;
+  a.pre_out = reinterpret_cast<uint16_t*>(out->pre);
+  a.out_mode = out_mode;
+  a.q_row = out->q_row;
+  a.s_row = out->s_row;
+  a.q_col = out->q_col;
+  a.s_col = out->s_col;
+  a.y = reinterpret_cast<uint16_t*>(out->y);
+  a.amax = out->amax;
+  if (out_mode == MOE_OUT_NVFP4 && a.amax && cudaMemsetAsync(a.amax, 0, sizeof(float), stream) != cudaSuccess)
+    return MOE_ERR_CUDA;
+  if (!params) {
+    a.out_N = N;
+    return launch<PLAIN>(m, a, sm_margin, stream);
+  }
+  const int lean = glu_lean_kind(params);
+  a.prm = GluParams{params->act,   params->alpha, params->up_offset, params->gate_lo, params->gate_hi,
+                    params->up_lo, params->up_hi, lean,              -params->alpha * 1.4426950408889634f};
+  if (params->act == MOE_ACT_SRELU) {
+    a.out_N = N;
+    return launch<ELT>(m, a, sm_margin, stream);
+  }
+  a.out_N = N / 2;
+  return lean == 1   ? launch<GLU_L1>(m, a, sm_margin, stream)
+         : lean == 2 ? launch<GLU_L2>(m, a, sm_margin, stream)
+         : lean == 3 ? launch<GLU_L3>(m, a, sm_margin, stream)
+                     : launch<GLU>(m, a, sm_margin, stream);
+}
+
+}  // namespace moeglu
+
+extern "C" size_t moe_grouped_mxfp4_workspace_size(int E, int K, int R_cap) {
+  if (E <= 0 || K <= 0 || R_cap <= 0) return 0;
+  return moeglu::grouped_gemm_mxfp4_workspace(E, K, R_cap);
+}

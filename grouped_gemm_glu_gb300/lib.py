@@ -90,6 +90,7 @@ _SIGS = {
                                             C.POINTER(ActOut), P, SZ, I, P, P],
     "moe_grouped_fc1_glu_quant_fwd_mxfp4": [P, P, P, P, P, P, P, P, I, I, I, I, C.POINTER(GluParams), I,
                                             C.POINTER(ActOut), P, SZ, I, P, P],
+    "moe_grouped_mxfp4_workspace_size": ([I, I, I], SZ),
     "moe_mxfp4_code_bytes": ([I, I, I], SZ),
     "moe_mxfp4_scale_bytes": ([I, I, I], SZ),
     "moe_quantize_mxfp4": [P, I, I, I, I, P, P, P, P],

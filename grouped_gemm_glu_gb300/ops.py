@@ -701,7 +701,6 @@ def fc2_fwd_mxfp4(Aq, As, Wq, Ws, counts, offsets, sm_margin: int = 0, status=No
     """GroupGemm on MXFP8 rows and an MXFP4 weight: y [R_cap, N] bf16 =
     A [R_cap, K] . W[e]^T per expert, A as codes and scales [R_cap, K/32], W
     [E, N, K] as quantize_mxfp4 writes it."""
-    lib = L.load()
     R_cap, K = _rows_mxfp8(Aq, As, "A")
     E, N = _mxfp4(Wq, Ws, K, "W")
     _groups(counts, offsets, E)
@@ -711,12 +710,12 @@ def fc2_fwd_mxfp4(Aq, As, Wq, Ws, counts, offsets, sm_margin: int = 0, status=No
     st = status if status is not None else new_status(dev)
     a_in = L.InT(L.IN_MXFP8, Aq.data_ptr(), As.data_ptr(), None)
     w_in = L.InT(L.IN_MXFP4, Wq.data_ptr(), Ws.data_ptr(), None)
-    nbytes = _size("moe_grouped_fc2_workspace_size", E, K, N, R_cap)
-    ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
     ao = L.ActOut(y=y.data_ptr())
-    L.check(lib.moe_grouped_fc2_fwd(C.byref(a_in), C.byref(w_in), counts.data_ptr(), offsets.data_ptr(), E, K, N, R_cap,
-                                    L.OUT_BF16, C.byref(ao), ws.data_ptr(), nbytes, sm_margin, st.data_ptr(), _cur(Aq)),
-            "moe_grouped_fc2_fwd (MXFP4)")
+    nbytes = _size("moe_grouped_mxfp4_workspace_size", E, K, R_cap)
+    ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+    L.check(L.load().moe_grouped_fc2_fwd(C.byref(a_in), C.byref(w_in), counts.data_ptr(), offsets.data_ptr(), E, K, N,
+                                         R_cap, L.OUT_BF16, C.byref(ao), ws.data_ptr(), nbytes, sm_margin,
+                                         st.data_ptr(), _cur(Aq)), "moe_grouped_fc2_fwd (MXFP4)")
     return y
 
 
@@ -725,7 +724,6 @@ def fc1_fwd_mxfp4(xq, xs, W1q, W1s, counts, offsets, F: int, params: L.GluParams
                   status=None) -> dict:
     """fc1_fwd_mxfp8 with an MXFP4 weight: W1q, W1s the MXFP4 form of the
     packed W1p [E, N1, H] (quantize_mxfp4)."""
-    lib = L.load()
     R_cap, H = _rows_mxfp8(xq, xs, "x")
     E, N1 = _mxfp4(W1q, W1s, H, "W1")
     _groups(counts, offsets, E)
@@ -750,11 +748,11 @@ def fc1_fwd_mxfp4(xq, xs, W1q, W1s, counts, offsets, F: int, params: L.GluParams
     if save_pre:
         o["pre"] = new(R_cap, N1, dtype=torch.bfloat16, device=dev)
     st = status if status is not None else new_status(dev)
-    nbytes = _size("moe_grouped_fc2_workspace_size", E, H, N1, R_cap)
+    nbytes = _size("moe_grouped_mxfp4_workspace_size", E, H, R_cap)
     ws = new(nbytes, dtype=u8, device=dev)
     for k, v in o.items():
         setattr(ao, k, v.data_ptr())
-    L.check(lib.moe_grouped_fc1_glu_quant_fwd_mxfp4(
+    L.check(L.load().moe_grouped_fc1_glu_quant_fwd_mxfp4(
         xq.data_ptr(), xs.data_ptr(), W1q.data_ptr(), W1s.data_ptr(), _ptr(b1p), _ptr(row_scale), counts.data_ptr(),
         offsets.data_ptr(), E, H, F, R_cap, C.byref(params), out_mode, C.byref(ao), ws.data_ptr(), nbytes, sm_margin,
         st.data_ptr(), _cur(xq)), "moe_grouped_fc1_glu_quant_fwd_mxfp4")

@@ -328,6 +328,10 @@ MOE_API size_t moe_grouped_fc2_workspace_size(int E, int K, int N, int R_cap);
  *                 out_mode must be MOE_OUT_BF16 (else MOE_ERR_UNSUPPORTED).
  *                 ([MoE-Fusion] "Fusing MXFP8 and NVFP4 quantisation": the
  *                 consumer of the forward's NVFP4 cast.)
+ *   MOE_IN_MXFP4: (W only) next to an MXFP8 A; ws =
+ *                 moe_grouped_mxfp4_workspace_size(E, K, R_cap) bytes,
+ *                 256-byte aligned (the rows' scales, re-tiled).
+ *                 K % 32 == 0, N % 32 == 0.
  *   MOE_IN_BF16:  bf16, scale unused; kind::f16 MMA on CTA pairs; ws
  *                 nullable: with >= 256 bytes (16-byte aligned) it holds the
  *                 dynamic tile scheduler's counter, as for the fused FC1.
@@ -363,7 +367,8 @@ MOE_API moe_status_t moe_grouped_fc1_glu_quant_fwd_mxfp8(const uint8_t* xq, cons
 
 /* moe_grouped_fc1_glu_quant_fwd_mxfp8 with an MXFP4 weight: W1q, W1s the
  * MXFP4 form of the packed W1p [E][N1][H] (moe_quantize_mxfp4, col = 0; W1q
- * 32-byte, W1s 16-byte aligned).  Same epilogue, outputs and workspace. */
+ * 32-byte, W1s 16-byte aligned).  Same epilogue and outputs;
+ * ws: moe_grouped_mxfp4_workspace_size(E, H, R_cap) bytes, 256-byte aligned. */
 MOE_API moe_status_t moe_grouped_fc1_glu_quant_fwd_mxfp4(const uint8_t* xq, const uint8_t* xs,
                                                  const uint8_t* W1q, const uint8_t* W1s,
                                                  const moe_bf16* b1p, const float* row_scale,
@@ -372,6 +377,10 @@ MOE_API moe_status_t moe_grouped_fc1_glu_quant_fwd_mxfp4(const uint8_t* xq, cons
                                                  const moe_glu_params_t* params, int out_mode,
                                                  const moe_act_out_t* out, void* ws, size_t ws_bytes,
                                                  int sm_margin, int32_t* status, moe_stream_t stream);
+
+/* Bytes of device workspace a grouped product with an MXFP4 weight needs
+ * (contraction length K). */
+MOE_API size_t moe_grouped_mxfp4_workspace_size(int E, int K, int R_cap);
 
 /* Bytes of the MXFP4 form of a weight W [G][N][K] (contraction along K):
  * packed codes, rows of K rounded up to 128 elements; and scales. */
