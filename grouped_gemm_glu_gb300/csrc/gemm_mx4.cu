@@ -159,6 +159,23 @@ __device__ __forceinline__ Tile decode(int t, const int32_t* pref, const Args& a
   return ti;
 }
 
+// The same in every lane, known as such to the compiler.
+__device__ __forceinline__ Tile uniform(Tile t) {
+  t.e = __shfl_sync(0xFFFFFFFFu, t.e, 0);
+  t.n0 = __shfl_sync(0xFFFFFFFFu, t.n0, 0);
+  t.mt = __shfl_sync(0xFFFFFFFFu, t.mt, 0);
+  t.row0 = __shfl_sync(0xFFFFFFFFu, t.row0, 0);
+  t.nb = __shfl_sync(0xFFFFFFFFu, t.nb, 0);
+  t.valid = __shfl_sync(0xFFFFFFFFu, t.valid, 0);
+  return t;
+}
+// True in one lane of a converged warp (the same one every time).
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xFFFFFFFF;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(p));
+  return p != 0;
+}
+
 // Row tiles per expert -> exclusive prefix pref[0..E] (whole CTA).
 __device__ __forceinline__ void build_prefix(const Args& a, int32_t* pref) {
   const int E = a.E, lane = threadIdx.x & 31;
@@ -315,7 +332,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
   uint64_t* mma_done = acc_empty + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + OFF_MISC);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + OFF_MISC + 4);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xFFFFFFFFu, (int)(threadIdx.x >> 5), 0);  // warp-uniform for the compiler
   const int E = a.E;
   const int rank = (int)cluster_ctarank();
   const int cl = blockIdx.x >> 1, ncl = gridDim.x >> 1;
@@ -349,112 +367,114 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
   __syncthreads();
   cluster_sync();  // both CTAs' barriers and tensor memory exist before any cross-CTA use
   tc_fence_after();
-  const uint32_t tmem_base = *tmem_slot;
+  const uint32_t tmem_base = __shfl_sync(0xFFFFFFFFu, *tmem_slot, 0);
   const bool over = __ldg(a.offsets + E) > a.R_cap;
   if (over && threadIdx.x == 0) set_status(a.status, MOE_ERR_CAPACITY);
   const int total = over ? 0 : pref[E] * a.n_tiles;
   WaitGuard guard{abort_flag, a.status, a.wait_ns};
 
+  // The producer's and the MMA issuer's loops are run by their whole warps, in
+  // step, and one elected lane issues: the operands of TMA and tcgen05
+  // instructions are uniform registers, and in a loop that only one lane runs
+  // each of them is moved there one by one (110 to 140 cycles per
+  // instruction, 1000 per k-block, measured with the clock).
   if (warp == PRODUCER_WARP) {
-    if (lane == 0) {
-      int stage = 0;
-      uint32_t phase = 0, issued = 0, issued_parity = 0;
-      wait_for_primary();  // the tiled scales of the rows (in every CTA: the grid ends after its primary)
-      for (int t = cl; t < total; t += ncl) {
-        const Tile ti = decode(t, pref, a);
-        if (ti.nb == 0) continue;
-        const uint32_t tx = 2u * (W_TX + SF_STAGE) + (uint32_t)ti.nb * 32 * BK;  // both CTAs' bytes
-        const int xrow = ti.row0 + rank * 16 * ti.nb;
-        const int ws_row = (ti.e * a.n_tiles + ti.n0 / (2 * BW)) * a.num_kb * 2 + rank, xs_row = ti.mt * a.num_kb * 2;
-        bool ok = true;
-        for (int kb = 0; kb < a.num_kb; ++kb) {
-          if (!mbar_wait(empty + stage, phase ^ 1u, guard)) {
-            ok = false;
-            break;
-          }
-          uint8_t* dst = smem + stage * STAGE_BYTES;
-          const uint32_t bar = mapa_shared(smem_u32(full + stage), 0);
+    int stage = 0;
+    uint32_t phase = 0, issued = 0, issued_parity = 0;
+    wait_for_primary();  // the tiled scales of the rows (in every CTA: the grid ends after its primary)
+    for (int t = cl; t < total; t += ncl) {
+      const Tile ti = uniform(decode(t, pref, a));
+      if (ti.nb == 0) continue;
+      const uint32_t tx = 2u * (W_TX + SF_STAGE) + (uint32_t)ti.nb * 32 * BK;  // both CTAs' bytes
+      const int xrow = ti.row0 + rank * 16 * ti.nb, wrow = ti.n0 + rank * BW;
+      const int ws_row = (ti.e * a.n_tiles + ti.n0 / (2 * BW)) * a.num_kb * 2 + rank, xs_row = ti.mt * a.num_kb * 2;
+      bool ok = true;
+      for (int kb = 0; kb < a.num_kb; ++kb) {
+        if (!__all_sync(0xFFFFFFFFu, mbar_wait(empty + stage, phase ^ 1u, guard))) {
+          ok = false;
+          break;
+        }
+        uint8_t* dst = smem + stage * STAGE_BYTES;
+        uint8_t* sd = sf + stage * SF_STAGE;
+        const uint32_t bar = mapa_shared(smem_u32(full + stage), 0);
+        if (elect_one()) {
           if (rank == 0) mbar_arrive_expect_tx(full + stage, tx);
-          tma_load_3d_pair(dst, &tmW, bar, kb * BK, ti.n0 + rank * BW, ti.e);
+          tma_load_3d_pair(dst, &tmW, bar, kb * BK, wrow, ti.e);
           // this CTA's 16 nb rows in boxes of 64, 32 and 16
           uint8_t* xd = dst + W_TILE;
-          int r = 0;
-          if (ti.nb & 4) {
-            tma_load_2d_pair(xd, &tmX64, bar, kb * BK, xrow);
-            r = 64;
-          }
-          if (ti.nb & 2) {
-            tma_load_2d_pair(xd + r * BK, &tmX32, bar, kb * BK, xrow + r);
-            r += 32;
-          }
-          if (ti.nb & 1) tma_load_2d_pair(xd + r * BK, &tmX16, bar, kb * BK, xrow + r);
-          uint8_t* sd = sf + stage * SF_STAGE;
+          if (ti.nb & 4) tma_load_2d_pair(xd, &tmX64, bar, kb * BK, xrow);
+          const int r2 = (ti.nb & 4) * 16, r1 = (ti.nb & 6) * 16;
+          if (ti.nb & 2) tma_load_2d_pair(xd + r2 * BK, &tmX32, bar, kb * BK, xrow + r2);
+          if (ti.nb & 1) tma_load_2d_pair(xd + r1 * BK, &tmX16, bar, kb * BK, xrow + r1);
           tma_load_2d_pair(sd, &tmWs, bar, 0, ws_row + 2 * kb);
           tma_load_2d_pair(sd + 512, &tmXs, bar, 0, xs_row + 2 * kb);
-          issued |= 1u << stage;
-          issued_parity = (issued_parity & ~(1u << stage)) | (phase << stage);
-          if (++stage == STAGES) {
-            stage = 0;
-            phase ^= 1u;
-          }
         }
-        if (!ok) break;
+        __syncwarp();
+        issued |= 1u << stage;
+        issued_parity = (issued_parity & ~(1u << stage)) | (phase << stage);
+        if (++stage == STAGES) {
+          stage = 0;
+          phase ^= 1u;
+        }
       }
-      if (rank == 0 && *abort_flag) {  // let the copies in flight land (they complete on this CTA's barriers)
-        volatile int never = 0;
-        WaitGuard drain{&never, a.status, 100000000ull};
-        for (int s = 0; s < STAGES; ++s)
-          if (issued & (1u << s)) mbar_wait(full + s, (issued_parity >> s) & 1u, drain);
-      }
+      if (!ok) break;
+    }
+    if (rank == 0 && lane == 0 && *abort_flag) {  // let the copies in flight land (they complete on these barriers)
+      volatile int never = 0;
+      WaitGuard drain{&never, a.status, 100000000ull};
+      for (int s = 0; s < STAGES; ++s)
+        if (issued & (1u << s)) mbar_wait(full + s, (issued_parity >> s) & 1u, drain);
     }
   } else if (warp == MMA_WARP) {
-    if (lane == 0 && rank == 0) {
+    if (rank == 0) {
       int stage = 0, lt = 0;
       uint32_t phase = 0;
       for (int t = cl; t < total; t += ncl) {
-        const Tile ti = decode(t, pref, a);
+        const Tile ti = uniform(decode(t, pref, a));
         if (ti.nb == 0) continue;
         const int buf = lt & 1;
         const uint32_t aph = (uint32_t)(lt >> 1) & 1u;
         ++lt;
-        if (!mbar_wait_cluster(acc_empty + buf, aph ^ 1u, guard)) break;
+        if (!__all_sync(0xFFFFFFFFu, mbar_wait(acc_empty + buf, aph ^ 1u, guard))) break;
         tc_fence_after();
         const uint32_t idesc = idesc_mxf8_e8m0(2 * BW, 32 * ti.nb) | IDESC_A_E2M1;
         const uint32_t d_tmem = tmem_base + (uint32_t)(buf * NT_MAX);
         bool ok = true;
         for (int kb = 0; kb < a.num_kb; ++kb) {
-          if (!mbar_wait_cluster(full + stage, phase, guard)) {
+          if (!__all_sync(0xFFFFFFFFu, mbar_wait(full + stage, phase, guard))) {
             ok = false;
             break;
           }
           tc_fence_after();
-          const uint32_t w_addr = smem_u32(smem + stage * STAGE_BYTES);
-          const uint32_t sf_addr = smem_u32(sf + stage * SF_STAGE);
-          tc_cp_32x128b_x4_pair(tmem_base + SFW_COL, sdesc_noswizzle(sf_addr, 128));
-          tc_cp_32x128b_x4_pair(tmem_base + SFX_COL, sdesc_noswizzle(sf_addr + 512, 128));
-          if (ti.nb > 4) tc_cp_32x128b_x4_pair(tmem_base + SFX_COL + 4, sdesc_noswizzle(sf_addr + 1024, 128));
+          const uint32_t w_addr = smem_u32(smem) + stage * STAGE_BYTES;
+          const uint32_t sf_addr = smem_u32(sf) + stage * SF_STAGE;
           const uint64_t wd = sdesc_kmajor_sw128(w_addr), xd = sdesc_kmajor_sw128(w_addr + W_TILE);
+          const uint64_t sd = sdesc_noswizzle(sf_addr, 128);
           const int nsub = min(4, (a.K - kb * BK) / 32);
-          if (nsub == 4) {
+          if (elect_one()) {
+            tc_cp_32x128b_x4_pair(tmem_base + SFW_COL, sd);
+            tc_cp_32x128b_x4_pair(tmem_base + SFX_COL, sd + (512 >> 4));
+            if (ti.nb > 4) tc_cp_32x128b_x4_pair(tmem_base + SFX_COL + 4, sd + (1024 >> 4));
 #pragma unroll
             for (int k = 0; k < 4; ++k)
-              umma_mxf8_pair(d_tmem, wd + 2 * k, xd + 2 * k, idesc_with_sf_ids(idesc, (uint32_t)k, (uint32_t)k),
-                             tmem_base + SFW_COL, tmem_base + SFX_COL, (kb | k) != 0 ? 1u : 0u);
-          } else {
-            for (int k = 0; k < nsub; ++k)
-              umma_mxf8_pair(d_tmem, wd + 2 * k, xd + 2 * k, idesc_with_sf_ids(idesc, (uint32_t)k, (uint32_t)k),
-                             tmem_base + SFW_COL, tmem_base + SFX_COL, (kb | k) != 0 ? 1u : 0u);
+              if (k < nsub)
+                umma_mxf8_pair(d_tmem, wd + 2 * k, xd + 2 * k, idesc_with_sf_ids(idesc, (uint32_t)k, (uint32_t)k),
+                               tmem_base + SFW_COL, tmem_base + SFX_COL, (kb | k) != 0 ? 1u : 0u);
+            tc_commit_pair_mc(empty + stage, 0x3);
           }
-          tc_commit_pair_mc(empty + stage, 0x3);
+          __syncwarp();
           if (++stage == STAGES) {
             stage = 0;
             phase ^= 1u;
           }
         }
         if (!ok) break;
-        tc_commit_pair_mc(acc_full + buf, 0x3);
+        if (elect_one()) tc_commit_pair_mc(acc_full + buf, 0x3);
+        __syncwarp();
       }
-      tc_commit_pair_mc(mma_done, 0x1);
+      // (the same lane is elected throughout: its commit covers everything issued)
+      if (elect_one()) tc_commit_pair_mc(mma_done, 0x1);
+      __syncwarp();
       volatile int never = 0;
       WaitGuard drain{&never, a.status, 100000000ull};
       mbar_wait(mma_done, 0, drain);
