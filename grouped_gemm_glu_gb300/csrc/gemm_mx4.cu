@@ -60,7 +60,7 @@ constexpr int X_TILE = NT_MAX / 2 * BK;
 constexpr int STAGE_BYTES = W_TILE + (X_TILE + 1023) / 1024 * 1024;
 constexpr int SF_STAGE = 512 + 1024;           // weight block, two blocks of rows
 constexpr int STAGES = 6;
-constexpr int SCRATCH = 1024;                  // per epilogue warp
+constexpr int SCRATCH = 2048;                  // per epilogue warp
 constexpr int E_MAX = 1024;
 constexpr int OFF_SF = STAGES * STAGE_BYTES;
 constexpr int OFF_SCRATCH = OFF_SF + STAGES * SF_STAGE;
@@ -169,6 +169,16 @@ __device__ __forceinline__ Tile uniform(Tile t) {
   t.valid = __shfl_sync(0xFFFFFFFFu, t.valid, 0);
   return t;
 }
+// Whether the phase is over, without waiting for it.
+__device__ __forceinline__ uint32_t mbar_peek(uint64_t* b, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
+      : "=r"(ok)
+      : "r"(smem_u32(b)), "r"(parity)
+      : "memory");
+  return ok;
+}
 // True in one lane of a converged warp (the same one every time).
 __device__ __forceinline__ bool elect_one() {
   uint32_t p;
@@ -216,8 +226,36 @@ __device__ __forceinline__ float activate(const GluParams& p, float u, float g) 
   return act_fwd(p, u, g);
 }
 
+// Rows r0 .. r0 + 15 of one output column per lane (a warp: 32 neighbouring
+// columns) as bf16, bf16 plus amax, or MXFP8 rows.
+__device__ __forceinline__ void emit_rows16(const Args& a, const float* o, int col, int r0, int lane, Amax& amax_bits) {
+  const size_t N = (size_t)a.out_N;
+  if (a.out_mode == MOE_OUT_MXFP8) {
+    uint8_t* q = a.q_row + (size_t)r0 * N + col;
+    uint8_t* s = a.s_row + (size_t)r0 * (N / 32) + col / 32;
+#pragma unroll
+    for (int j = 0; j < 16; ++j) {
+      const uint32_t sb = e8m0_from_amax_bits(__reduce_max_sync(0xFFFFFFFFu, abs_bits(o[j])));
+      q[j * N] = (uint8_t)(sb == 0xFFu ? 0x7Fu : e4m3x2(o[j] * mx_inv_scale(sb), 0.0f) & 0xFFu);
+      if (lane == 0) s[j * (N / 32)] = (uint8_t)sb;
+    }
+    return;
+  }
+  uint16_t* y = a.y + (size_t)r0 * N + col;
+#pragma unroll
+  for (int j = 0; j < 16; ++j) y[j * N] = __bfloat16_as_ushort(__float2bfloat16_rn(o[j]));
+  if (a.out_mode == MOE_OUT_NVFP4) {
+#pragma unroll
+    for (int j = 0; j < 16; ++j) amax_bits.plain = max(amax_bits.plain, abs_bits(o[j]));
+  }
+}
+
 // One tile of this CTA: accumulator lane i is weight row n0 + 128 rank + i,
-// column j is row row0 + j.
+// column j is row row0 + j.  GLU: lane quarters 2i and 2i + 1 hold the input
+// and the gate half of one packed block of 64; the two warps swap halves
+// through 4 KB of shared memory, so that each computes 16 of the 32 rows.
+// (The column-wise MXFP8 copy needs a column's 32 rows in one thread: with it
+// the input warp takes the gate warp's rows as well.)
 template <int EPI>
 __device__ __forceinline__ void epilogue(const Args& a, const Tile& ti, uint32_t tacc, int q, int h, int lane, int rank,
                                          uint8_t* scratch, Amax& amax_bits) {
@@ -233,38 +271,64 @@ __device__ __forceinline__ void epilogue(const Args& a, const Tile& ti, uint32_t
     float v[32];
     tmem_ld32(tacc + 32 * g, v);
 #pragma unroll
-    for (int j = 0; j < 32; ++j) v[j] = j < nvalid ? v[j] + bias : 0.0f;
-    if (EPI != PLAIN && a.pre_out != nullptr) {
+    for (int j = 0; j < 32; ++j) v[j] += bias;
+    if (nvalid < 32) {
 #pragma unroll
-      for (int j = 0; j < 32; ++j)
-        a.pre_out[(size_t)(rb + j) * a.N + col] = __bfloat16_as_ushort(__float2bfloat16_rn(v[j]));
+      for (int j = 0; j < 32; ++j) v[j] = j < nvalid ? v[j] : 0.0f;
+    }
+    if (EPI != PLAIN && a.pre_out != nullptr) {
+      uint16_t* pp = a.pre_out + (size_t)rb * a.N + col;
+#pragma unroll
+      for (int j = 0; j < 32; ++j) pp[(size_t)j * a.N] = __bfloat16_as_ushort(__float2bfloat16_rn(v[j]));
     }
     if (GATED) {
-      // the two warps' 2 KB of scratch: 16 rows x 32 lanes at a time
-      float* xs = reinterpret_cast<float*>(scratch);
+      float* xs = reinterpret_cast<float*>(scratch);  // [2][16 rows][32 lanes]: to the gate warp, to the input warp
       const bool gate_warp = (q & 1) != 0;
-      const int id = 1 + h * 2 + (q >> 1);
-      float gate[32];
+      const bool both = a.q_col != nullptr && a.out_mode == MOE_OUT_MXFP8;
+      const int id = 1 + h * 2 + (q >> 1), f = (colbase / 64) * 32 + lane;
+      float x[32];
+      warp_pair_sync(id);  // both warps have read what was there
+      if (gate_warp) {
 #pragma unroll
-      for (int hf = 0; hf < 2; ++hf) {
-        warp_pair_sync(id);  // the input warp has read what was there
-        if (gate_warp) {
+        for (int j = 0; j < 16; ++j) xs[(16 + j) * 32 + lane] = v[j];
+        if (both) {
 #pragma unroll
-          for (int j = 0; j < 16; ++j) xs[j * 32 + lane] = v[16 * hf + j];
+          for (int j = 0; j < 16; ++j) xs[j * 32 + lane] = v[16 + j];
         }
-        warp_pair_sync(id);
-        if (!gate_warp) {
+      } else if (!both) {
 #pragma unroll
-          for (int j = 0; j < 16; ++j) gate[16 * hf + j] = xs[j * 32 + lane];
+        for (int j = 0; j < 16; ++j) xs[j * 32 + lane] = v[16 + j];
+      }
+      warp_pair_sync(id);
+      if (!both) {
+        float o[16];
+        const int r0 = rb + (gate_warp ? 16 : 0), live = nvalid - (gate_warp ? 16 : 0);
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+          const float m = xs[((gate_warp ? 0 : 16) + j) * 32 + lane];
+          o[j] = activate<EPI>(a.prm, gate_warp ? m : v[j], gate_warp ? v[16 + j] : m);
         }
+        if (a.row_scale != nullptr) {
+#pragma unroll
+          for (int j = 0; j < 16; ++j)
+            if (j < live) o[j] *= __ldg(a.row_scale + r0 + j);
+        }
+        if (live < 16) {
+#pragma unroll
+          for (int j = 0; j < 16; ++j) o[j] = j < live ? o[j] : 0.0f;
+        }
+        emit_rows16(a, o, f, r0, lane, amax_bits);
+        continue;
       }
       if (gate_warp) continue;
 #pragma unroll
+      for (int j = 0; j < 32; ++j) x[j] = xs[(j < 16 ? 16 + j : j - 16) * 32 + lane];
+#pragma unroll
       for (int j = 0; j < 32; ++j) {
         const float rs = (a.row_scale != nullptr && j < nvalid) ? __ldg(a.row_scale + rb + j) : 1.0f;
-        v[j] = j < nvalid ? activate<EPI>(a.prm, v[j], gate[j]) * rs : 0.0f;
+        v[j] = j < nvalid ? activate<EPI>(a.prm, v[j], x[j]) * rs : 0.0f;
       }
-      emit_block_t(a, v, (colbase / 64) * 32 + lane, rb, lane, amax_bits);
+      emit_block_t(a, v, f, rb, lane, amax_bits);
     } else {
       if (EPI == ELT) {
 #pragma unroll
@@ -273,7 +337,12 @@ __device__ __forceinline__ void epilogue(const Args& a, const Tile& ti, uint32_t
           v[j] = j < nvalid ? act_fwd(a.prm, v[j], 0.0f) * rs : 0.0f;
         }
       }
-      emit_block_t(a, v, col, rb, lane, amax_bits);
+      if (a.q_col != nullptr && a.out_mode == MOE_OUT_MXFP8) {
+        emit_block_t(a, v, col, rb, lane, amax_bits);
+      } else {
+        emit_rows16(a, v, col, rb, lane, amax_bits);
+        emit_rows16(a, v + 16, col, rb + 16, lane, amax_bits);
+      }
     }
   }
 }
@@ -440,8 +509,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         const uint32_t idesc = idesc_mxf8_e8m0(2 * BW, 32 * ti.nb) | IDESC_A_E2M1;
         const uint32_t d_tmem = tmem_base + (uint32_t)(buf * NT_MAX);
         bool ok = true;
+        uint32_t ready = mbar_peek(full + stage, phase);
         for (int kb = 0; kb < a.num_kb; ++kb) {
-          if (!__all_sync(0xFFFFFFFFu, mbar_wait(full + stage, phase, guard))) {
+          if (!__all_sync(0xFFFFFFFFu, ready) && !__all_sync(0xFFFFFFFFu, mbar_wait(full + stage, phase, guard))) {
             ok = false;
             break;
           }
@@ -467,6 +537,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
             stage = 0;
             phase ^= 1u;
           }
+          ready = mbar_peek(full + stage, phase);  // the next stage, while this one is multiplied
         }
         if (!ok) break;
         if (elect_one()) tc_commit_pair_mc(acc_full + buf, 0x3);
