@@ -16,10 +16,10 @@
 // 16 bytes of shared memory (8 of codes, 8 unused), the form in which this MMA
 // kind reads 4-bit elements next to 8-bit ones.
 //
-// An expert's rows (padded to 32) are cut into ceil(blocks / 7) tiles of
-// nearly equal numbers of 32-row blocks, so no tile is a sliver.  Two
-// accumulators of 224 columns and the scales fill the 512 columns of tensor
-// memory: a tile is written out while the next one is multiplied.
+// An expert's rows (padded to 32) are cut into ceil(blocks / NB) tiles of
+// nearly equal numbers of 32-row blocks, so no tile is a sliver.  With NB = 7
+// two accumulators of 224 columns and the scales fill the 512 columns of
+// tensor memory: a tile is written out while the next one is multiplied.
 //
 // Two launches: k_mx4_scales gathers the rows' scales of every row tile into
 // the order tcgen05.cp consumes (byte 16 l + 4 j + i of 512 = row 32 j + l,
@@ -29,14 +29,16 @@
 // kernel, by a warp that wrote the stage's scales itself, took 1 to 2 us per
 // k-block: four times the MMAs.)
 //
-// Warps (10 per CTA, one CTA per SM, persistent over the tiles):
+// Warps (11 per CTA, one CTA per SM, persistent over the tiles):
 //   0-7  epilogue: warp (q, h) takes the 32 weight rows of lane quarter q and
 //        the 32-row groups h, h + 2, ...; a thread owns one output column and
 //        32 rows.  GLU: quarters 2i / 2i + 1 hold the input / gate halves of
 //        one packed block of 64, the gate warp hands its values over through
 //        shared memory
-//   8    TMA producer: weight tile, row tile and both scale blocks of each
-//        k-block; all complete on the even CTA's stage barrier
+//   8    TMA producer of the weight: tile and scales of each k-block
+//   10   TMA producer of the rows (two issuers, because four to six copies a
+//        k-block from one thread took longer than the MMAs); all copies of
+//        both CTAs complete on the even CTA's stage barrier
 //   9    tensor-memory owner; in the even CTA the MMA issuer: scales into
 //        tensor memory (tcgen05.cp), then 4 MMAs of K = 32
 // Every wait is bounded (MOE_ERR_TIMEOUT + early exit, never a trap).
@@ -49,38 +51,45 @@ namespace gmx4 {
 
 constexpr int BW = 128;             // weight rows per CTA
 constexpr int BK = 128;             // elements of K per k-block
-constexpr int NB_MAX = 7;           // 32-row blocks per tile
-constexpr int NT_MAX = 32 * NB_MAX;
 constexpr int EPI_WARPS = 8;
-constexpr int PRODUCER_WARP = 8, MMA_WARP = 9;
-constexpr int THREADS = 10 * 32;
+constexpr int PRODUCER_WARP = 8, MMA_WARP = 9, ROWS_WARP = 10;
+constexpr int THREADS = 11 * 32;
 constexpr int W_TILE = BW * BK;                // unpacked
 constexpr int W_TX = BW * BK / 2;              // bytes the unpacking load counts
-constexpr int X_TILE = NT_MAX / 2 * BK;
-constexpr int STAGE_BYTES = W_TILE + (X_TILE + 1023) / 1024 * 1024;
-constexpr int SF_STAGE = 512 + 1024;           // weight block, two blocks of rows
-constexpr int STAGES = 6;
 constexpr int SCRATCH = 2048;                  // per epilogue warp
 constexpr int E_MAX = 1024;
-constexpr int OFF_SF = STAGES * STAGE_BYTES;
-constexpr int OFF_SCRATCH = OFF_SF + STAGES * SF_STAGE;
-constexpr int OFF_PREF = OFF_SCRATCH + EPI_WARPS * SCRATCH;
-constexpr int OFF_BARS = OFF_PREF + (E_MAX + 2) * 4;
-constexpr int NUM_BARS = 2 * STAGES + 5;
-constexpr int OFF_MISC = OFF_BARS + NUM_BARS * 8;
-constexpr int SMEM_BYTES = 1024 + OFF_MISC + 64;
-static_assert(SMEM_BYTES <= 232448, "shared memory budget");
-static_assert(OFF_BARS % 8 == 0 && OFF_SF % 1024 == 0 && OFF_SCRATCH % 16 == 0, "alignment");
 constexpr uint32_t TMEM_COLS = 512;
-constexpr uint32_t SFW_COL = 2 * NT_MAX, SFX_COL = SFW_COL + 4;  // 4 + 8 columns of scales
-static_assert(SFX_COL + 8 <= TMEM_COLS, "tensor memory");
+
+// NB: 32-row blocks per tile, at most.  7 is what tensor memory takes twice;
+// 2 leaves shared memory for 9 stages instead of 6: where an expert has few
+// rows the weights stream from HBM, and the bytes in flight (8 KB per stage
+// and SM) bound the rate.
+template <int NB>
+struct Lay {
+  static constexpr int NT = 32 * NB;  // rows per tile
+  static constexpr int XB = NB > 4 ? 2 : 1;                      // 512-byte scale blocks of the rows
+  static constexpr int STAGES = NB > 4 ? 6 : 9;
+  static constexpr int STAGE_BYTES = W_TILE + (NT / 2 * BK + 1023) / 1024 * 1024;
+  static constexpr int SF_STAGE = 512 + 512 * XB;
+  static constexpr int OFF_SF = STAGES * STAGE_BYTES;
+  static constexpr int OFF_SCRATCH = OFF_SF + STAGES * SF_STAGE;
+  static constexpr int OFF_PREF = OFF_SCRATCH + EPI_WARPS * SCRATCH;
+  static constexpr int OFF_BARS = OFF_PREF + (E_MAX + 2) * 4;
+  static constexpr int NUM_BARS = 2 * STAGES + 5;
+  static constexpr int OFF_MISC = OFF_BARS + NUM_BARS * 8;
+  static constexpr int SMEM_BYTES = 1024 + OFF_MISC + 64;
+  static_assert(SMEM_BYTES <= 232448, "shared memory budget");
+  static_assert(OFF_BARS % 8 == 0 && OFF_SF % 1024 == 0 && OFF_SCRATCH % 16 == 0, "alignment");
+  static constexpr uint32_t SFW_COL = 2 * NT, SFX_COL = SFW_COL + 4;  // 4 + 4 XB columns of scales
+  static_assert(SFX_COL + 4 * XB <= TMEM_COLS, "tensor memory");
+};
 
 struct Args {
   const int32_t* counts;
   const int32_t* offsets;
   int E, N, K, R_cap, n_tiles, num_kb;
   const uint8_t* xs;  // scales of the rows, [R_cap][K/32]
-  uint8_t* xs_tiled;  // [row tile][num_kb][2][512]
+  uint8_t* xs_tiled;  // [row tile][num_kb][XB][512]
   int mt_cap;         // row tiles that fit xs_tiled
   int32_t* status;
   uint64_t wait_ns;
@@ -125,7 +134,7 @@ struct Tile {
 
 __device__ __forceinline__ int row_blocks(int count) { return (max(count, 0) + 31) / 32; }
 
-// Row tile m of expert e, which has mt of them.
+// Row tile m of expert e, which has mt of them (see build_prefix).
 __device__ __forceinline__ void row_tile(const Args& a, int e, int m, int mt, Tile& ti) {
   const int cnt = __ldg(a.counts + e), off = __ldg(a.offsets + e);
   const int blocks = row_blocks(cnt);
@@ -186,11 +195,13 @@ __device__ __forceinline__ bool elect_one() {
   return p != 0;
 }
 
-// Row tiles per expert -> exclusive prefix pref[0..E] (whole CTA).
+// Row tiles per expert, of at most NB blocks -> exclusive prefix pref[0..E]
+// (whole CTA).
+template <int NB>
 __device__ __forceinline__ void build_prefix(const Args& a, int32_t* pref) {
   const int E = a.E, lane = threadIdx.x & 31;
   for (int e = threadIdx.x; e < E; e += blockDim.x)
-    pref[e + 1] = (row_blocks(__ldg(a.counts + e)) + NB_MAX - 1) / NB_MAX;
+    pref[e + 1] = (row_blocks(__ldg(a.counts + e)) + NB - 1) / NB;
   if (threadIdx.x == 0) pref[0] = 0;
   __syncthreads();
   if (threadIdx.x < 32) {
@@ -360,10 +371,12 @@ __device__ __forceinline__ uint32_t row_scales(const uint8_t* base, size_t at, s
 }
 
 // One warp per (row tile, k-block).
+template <int NB>
 __global__ void __launch_bounds__(256) k_mx4_scales(const Args a) {
+  constexpr int XB = Lay<NB>::XB;
   __shared__ int32_t pref[E_MAX + 2];
   launch_dependents();
-  build_prefix(a, pref);
+  build_prefix<NB>(a, pref);
   if (__ldg(a.offsets + a.E) > a.R_cap) return;
   const int lane = threadIdx.x & 31, warps = blockDim.x >> 5;
   const int ks = a.K / 32;
@@ -374,33 +387,37 @@ __global__ void __launch_bounds__(256) k_mx4_scales(const Args a) {
     const int e = find_expert(pref, a.E, mt, 1);
     Tile ti;
     row_tile(a, e, mt - pref[e], pref[e + 1] - pref[e], ti);
-    uint32_t v[8];
+    uint32_t v[4 * XB];
 #pragma unroll
-    for (int j = 0; j < 8; ++j)
+    for (int j = 0; j < 4 * XB; ++j)
       v[j] = j < ti.nb ? row_scales(a.xs, (size_t)(ti.row0 + 32 * j + lane) * ks + 4 * kb, total) : 0u;
-    uint4* dst = reinterpret_cast<uint4*>(a.xs_tiled + (size_t)it * 1024);
-    dst[lane] = make_uint4(v[0], v[1], v[2], v[3]);
-    if (ti.nb > 4) dst[32 + lane] = make_uint4(v[4], v[5], v[6], v[7]);
+    uint4* dst = reinterpret_cast<uint4*>(a.xs_tiled + (size_t)it * (512 * XB));
+#pragma unroll
+    for (int b = 0; b < XB; ++b)
+      if (ti.nb > 4 * b) dst[32 * b + lane] = make_uint4(v[4 * b], v[4 * b + 1], v[4 * b + 2], v[4 * b + 3]);
   }
 }
 
-template <int EPI>
+template <int EPI, int NB>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     k_grouped_mx4(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX64,
                   const __grid_constant__ CUtensorMap tmX32, const __grid_constant__ CUtensorMap tmX16,
                   const __grid_constant__ CUtensorMap tmWs, const __grid_constant__ CUtensorMap tmXs, const Args a) {
+  using L = Lay<NB>;
+  constexpr int STAGES = L::STAGES, STAGE_BYTES = L::STAGE_BYTES, SF_STAGE = L::SF_STAGE;
+  constexpr uint32_t SFW_COL = L::SFW_COL, SFX_COL = L::SFX_COL;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint8_t* sf = smem + OFF_SF;
-  uint8_t* scratch_all = smem + OFF_SCRATCH;
-  int32_t* pref = reinterpret_cast<int32_t*>(smem + OFF_PREF);
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + OFF_BARS);
+  uint8_t* sf = smem + L::OFF_SF;
+  uint8_t* scratch_all = smem + L::OFF_SCRATCH;
+  int32_t* pref = reinterpret_cast<int32_t*>(smem + L::OFF_PREF);
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + L::OFF_BARS);
   uint64_t* empty = full + STAGES;
   uint64_t* acc_full = full + 2 * STAGES;
   uint64_t* acc_empty = acc_full + 2;
   uint64_t* mma_done = acc_empty + 2;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + OFF_MISC);
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + OFF_MISC + 4);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::OFF_MISC);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::OFF_MISC + 4);
   const int lane = threadIdx.x & 31;
   const int warp = __shfl_sync(0xFFFFFFFFu, (int)(threadIdx.x >> 5), 0);  // warp-uniform for the compiler
   const int E = a.E;
@@ -431,7 +448,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     tmem_alloc_pair(tmem_slot, TMEM_COLS);
     tmem_relinquish_pair();
   }
-  build_prefix(a, pref);
+  build_prefix<NB>(a, pref);
   tc_fence_before();
   __syncthreads();
   cluster_sync();  // both CTAs' barriers and tensor memory exist before any cross-CTA use
@@ -447,36 +464,42 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
   // instructions are uniform registers, and in a loop that only one lane runs
   // each of them is moved there one by one (110 to 140 cycles per
   // instruction, 1000 per k-block, measured with the clock).
-  if (warp == PRODUCER_WARP) {
+  if (warp == PRODUCER_WARP || warp == ROWS_WARP) {
+    const bool weight = warp == PRODUCER_WARP;
     int stage = 0;
     uint32_t phase = 0, issued = 0, issued_parity = 0;
-    wait_for_primary();  // the tiled scales of the rows (in every CTA: the grid ends after its primary)
+    const uint32_t full0 = mapa_shared(smem_u32(full), 0);
+    if (!weight) wait_for_primary();  // the tiled scales of the rows (in every CTA: the grid ends after its primary)
     for (int t = cl; t < total; t += ncl) {
       const Tile ti = uniform(decode(t, pref, a));
       if (ti.nb == 0) continue;
       const uint32_t tx = 2u * (W_TX + SF_STAGE) + (uint32_t)ti.nb * 32 * BK;  // both CTAs' bytes
       const int xrow = ti.row0 + rank * 16 * ti.nb, wrow = ti.n0 + rank * BW;
-      const int ws_row = (ti.e * a.n_tiles + ti.n0 / (2 * BW)) * a.num_kb * 2 + rank, xs_row = ti.mt * a.num_kb * 2;
+      const int ws_row = (ti.e * a.n_tiles + ti.n0 / (2 * BW)) * a.num_kb * 2 + rank, xs_row = ti.mt * a.num_kb * L::XB;
+      const int r2 = (ti.nb & 4) * 16, r1 = (ti.nb & 6) * 16;
       bool ok = true;
       for (int kb = 0; kb < a.num_kb; ++kb) {
-        if (!__all_sync(0xFFFFFFFFu, mbar_wait(empty + stage, phase ^ 1u, guard))) {
+        if (!__all_sync(0xFFFFFFFFu, mbar_peek(empty + stage, phase ^ 1u)) &&
+            !__all_sync(0xFFFFFFFFu, mbar_wait(empty + stage, phase ^ 1u, guard))) {
           ok = false;
           break;
         }
         uint8_t* dst = smem + stage * STAGE_BYTES;
         uint8_t* sd = sf + stage * SF_STAGE;
-        const uint32_t bar = mapa_shared(smem_u32(full + stage), 0);
+        const uint32_t bar = full0 + 8 * stage;
         if (elect_one()) {
-          if (rank == 0) mbar_arrive_expect_tx(full + stage, tx);
-          tma_load_3d_pair(dst, &tmW, bar, kb * BK, wrow, ti.e);
-          // this CTA's 16 nb rows in boxes of 64, 32 and 16
-          uint8_t* xd = dst + W_TILE;
-          if (ti.nb & 4) tma_load_2d_pair(xd, &tmX64, bar, kb * BK, xrow);
-          const int r2 = (ti.nb & 4) * 16, r1 = (ti.nb & 6) * 16;
-          if (ti.nb & 2) tma_load_2d_pair(xd + r2 * BK, &tmX32, bar, kb * BK, xrow + r2);
-          if (ti.nb & 1) tma_load_2d_pair(xd + r1 * BK, &tmX16, bar, kb * BK, xrow + r1);
-          tma_load_2d_pair(sd, &tmWs, bar, 0, ws_row + 2 * kb);
-          tma_load_2d_pair(sd + 512, &tmXs, bar, 0, xs_row + 2 * kb);
+          if (weight) {
+            if (rank == 0) mbar_arrive_expect_tx(full + stage, tx);
+            tma_load_3d_pair(dst, &tmW, bar, kb * BK, wrow, ti.e);
+            tma_load_2d_pair(sd, &tmWs, bar, 0, ws_row + 2 * kb);
+          } else {
+            // this CTA's 16 nb rows in boxes of 64, 32 and 16
+            uint8_t* xd = dst + W_TILE;
+            if (NB >= 4 && (ti.nb & 4)) tma_load_2d_pair(xd, &tmX64, bar, kb * BK, xrow);
+            if (ti.nb & 2) tma_load_2d_pair(xd + r2 * BK, &tmX32, bar, kb * BK, xrow + r2);
+            if (ti.nb & 1) tma_load_2d_pair(xd + r1 * BK, &tmX16, bar, kb * BK, xrow + r1);
+            tma_load_2d_pair(sd + 512, &tmXs, bar, 0, xs_row + L::XB * kb);
+          }
         }
         __syncwarp();
         issued |= 1u << stage;
@@ -507,7 +530,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         if (!__all_sync(0xFFFFFFFFu, mbar_wait(acc_empty + buf, aph ^ 1u, guard))) break;
         tc_fence_after();
         const uint32_t idesc = idesc_mxf8_e8m0(2 * BW, 32 * ti.nb) | IDESC_A_E2M1;
-        const uint32_t d_tmem = tmem_base + (uint32_t)(buf * NT_MAX);
+        const uint32_t d_tmem = tmem_base + (uint32_t)(buf * L::NT);
         bool ok = true;
         uint32_t ready = mbar_peek(full + stage, phase);
         for (int kb = 0; kb < a.num_kb; ++kb) {
@@ -524,7 +547,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
           if (elect_one()) {
             tc_cp_32x128b_x4_pair(tmem_base + SFW_COL, sd);
             tc_cp_32x128b_x4_pair(tmem_base + SFX_COL, sd + (512 >> 4));
-            if (ti.nb > 4) tc_cp_32x128b_x4_pair(tmem_base + SFX_COL + 4, sd + (1024 >> 4));
+            if (NB > 4 && ti.nb > 4) tc_cp_32x128b_x4_pair(tmem_base + SFX_COL + 4, sd + (1024 >> 4));
 #pragma unroll
             for (int k = 0; k < 4; ++k)
               if (k < nsub)
@@ -564,7 +587,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       if (lane == 0) ok = mbar_wait(acc_full + buf, aph, guard) ? 1 : 0;
       if (!__shfl_sync(0xFFFFFFFFu, ok, 0)) break;
       tc_fence_after();
-      epilogue<EPI>(a, ti, tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(buf * NT_MAX), q, h, lane, rank,
+      epilogue<EPI>(a, ti, tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(buf * L::NT), q, h, lane, rank,
                     scratch_all + (warp & ~1) * SCRATCH, amax_bits);
       tc_fence_before();
       __syncwarp();
@@ -588,12 +611,13 @@ struct Maps {
   CUtensorMap w, x64, x32, x16, ws, xs;
 };
 
-template <int EPI>
-static moe_status_t launch(const Maps& m, const Args& a, int sm_margin, cudaStream_t stream) {
-  const void* kfn = (const void*)k_grouped_mx4<EPI>;
-  if (!set_smem_limit(kfn, SMEM_BYTES)) return MOE_ERR_CUDA;
+template <int EPI, int NB>
+static moe_status_t launch_nb(const Maps& m, const Args& a, int sm_margin, cudaStream_t stream) {
+  using L = Lay<NB>;
+  const void* kfn = (const void*)k_grouped_mx4<EPI, NB>;
+  if (!set_smem_limit(kfn, L::SMEM_BYTES)) return MOE_ERR_CUDA;
   const int sms = sm_count();
-  int clusters = max_active_pairs(kfn, THREADS, SMEM_BYTES);
+  int clusters = max_active_pairs(kfn, THREADS, L::SMEM_BYTES);
   if (clusters <= 0 || sms <= 0) return MOE_ERR_CUDA;
   const int by_margin = (sms - sm_margin) / 2;
   if (clusters > by_margin) clusters = by_margin;
@@ -601,30 +625,40 @@ static moe_status_t launch(const Maps& m, const Args& a, int sm_margin, cudaStre
   if (clusters > tiles_bound) clusters = (int)tiles_bound;
   if (clusters < 1) clusters = 1;
   const long long items = ((long long)a.mt_cap * a.num_kb + 7) / 8;
-  k_mx4_scales<<<(int)(items < 8ll * sms ? items : 8ll * sms), 256, 0, stream>>>(a);
+  k_mx4_scales<NB><<<(int)(items < 8ll * sms ? items : 8ll * sms), 256, 0, stream>>>(a);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(2 * clusters);
   cfg.blockDim = dim3(THREADS);
-  cfg.dynamicSmemBytes = SMEM_BYTES;
+  cfg.dynamicSmemBytes = L::SMEM_BYTES;
   cfg.stream = stream;
   cudaLaunchAttribute attr;
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, k_grouped_mx4<EPI>, m.w, m.x64, m.x32, m.x16, m.ws, m.xs, a) != cudaSuccess)
+  if (cudaLaunchKernelEx(&cfg, k_grouped_mx4<EPI, NB>, m.w, m.x64, m.x32, m.x16, m.ws, m.xs, a) != cudaSuccess)
     return MOE_ERR_CUDA;
   count_launch(2);
   return launch_status();
 }
 
+// Few rows per expert: at most FEW of them on average over the buffers.
+constexpr int FEW = 96;
+static bool few_rows(int E, int R_cap) { return R_cap <= (long long)FEW * E; }
+
+template <int EPI>
+static moe_status_t launch(const Maps& m, const Args& a, int sm_margin, cudaStream_t stream) {
+  return few_rows(a.E, a.R_cap) ? launch_nb<EPI, 2>(m, a, sm_margin, stream) : launch_nb<EPI, 7>(m, a, sm_margin, stream);
+}
+
 // Row tiles a call can have: at most one partly filled tile per expert.
-static int row_tiles_cap(int E, int R_cap) { return R_cap / NT_MAX + E; }
+static int row_tiles_cap(int E, int R_cap) { return R_cap / (few_rows(E, R_cap) ? Lay<2>::NT : Lay<7>::NT) + E; }
+static int scale_blocks(int E, int R_cap) { return few_rows(E, R_cap) ? Lay<2>::XB : Lay<7>::XB; }
 
 }  // namespace gmx4
 
 size_t grouped_gemm_mxfp4_workspace(int E, int K, int R_cap) {
-  return (size_t)gmx4::row_tiles_cap(E, R_cap) * ((K + gmx4::BK - 1) / gmx4::BK) * 1024;
+  return (size_t)gmx4::row_tiles_cap(E, R_cap) * ((K + gmx4::BK - 1) / gmx4::BK) * gmx4::scale_blocks(E, R_cap) * 512;
 }
 
 // See host_common.h.  The entry points (gemm_mx.cu) have checked the arguments.
@@ -635,6 +669,7 @@ moe_status_t grouped_gemm_mxfp4(const uint8_t* xq, const uint8_t* xs, const uint
                                 int32_t* status, cudaStream_t stream) {
   using namespace gmx4;
   const int n_tiles = (N + 2 * BW - 1) / (2 * BW), num_kb = (K + BK - 1) / BK, mt_cap = row_tiles_cap(E, R_cap);
+  const int xb = scale_blocks(E, R_cap);
   if (!work || (reinterpret_cast<uintptr_t>(work) & 255) || work_bytes < grouped_gemm_mxfp4_workspace(E, K, R_cap))
     return MOE_ERR_ARG;
   if ((long long)E * n_tiles * num_kb * 2 > INT32_MAX || (long long)mt_cap * num_kb * 2 > INT32_MAX ||
@@ -659,10 +694,10 @@ moe_status_t grouped_gemm_mxfp4(const uint8_t* xq, const uint8_t* xs, const uint
     if (!encode_tmap(xmaps[i], CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, xq, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B))
       return MOE_ERR_CUDA;
   }
-  for (int i = 0; i < 2; ++i) {  // scale blocks as rows of 128 words: one of the weight's, two of the rows'
-    const uint64_t dims[2] = {128, 2 * (i == 0 ? (uint64_t)E * n_tiles * num_kb : (uint64_t)mt_cap * num_kb)};
+  for (int i = 0; i < 2; ++i) {  // scale blocks as rows of 128 words: one of the weight's, xb of the rows'
+    const uint64_t dims[2] = {128, i == 0 ? (uint64_t)E * n_tiles * num_kb * 2 : (uint64_t)mt_cap * num_kb * xb};
     const uint64_t strides[1] = {512};
-    const uint32_t box[2] = {128, i == 0 ? 1u : 2u};
+    const uint32_t box[2] = {128, i == 0 ? 1u : (uint32_t)xb};
     if (!encode_tmap(i == 0 ? &m.ws : &m.xs, CU_TENSOR_MAP_DATA_TYPE_UINT32, 2, i == 0 ? (const void*)ws : work, dims,
                      strides, box, CU_TENSOR_MAP_SWIZZLE_NONE))
       return MOE_ERR_CUDA;
