@@ -74,7 +74,7 @@ struct Lay {
   static constexpr int OFF_SF = STAGES * STAGE_BYTES;
   static constexpr int OFF_SCRATCH = OFF_SF + STAGES * SF_STAGE;
   static constexpr int OFF_PREF = OFF_SCRATCH + EPI_WARPS * SCRATCH;
-  static constexpr int OFF_BARS = OFF_PREF + (E_MAX + 2) * 4;
+  static constexpr int OFF_BARS = OFF_PREF + (3 * E_MAX + 4) * 4;  // prefix, counts, offsets
   static constexpr int NUM_BARS = 2 * STAGES + 5;
   static constexpr int OFF_MISC = OFF_BARS + NUM_BARS * 8;
   static constexpr int SMEM_BYTES = 1024 + OFF_MISC + 64;
@@ -134,9 +134,15 @@ struct Tile {
 
 __device__ __forceinline__ int row_blocks(int count) { return (max(count, 0) + 31) / 32; }
 
-// Row tile m of expert e, which has mt of them (see build_prefix).
-__device__ __forceinline__ void row_tile(const Args& a, int e, int m, int mt, Tile& ti) {
-  const int cnt = __ldg(a.counts + e), off = __ldg(a.offsets + e);
+// The experts' row tiles in shared memory: pref[0..E] their exclusive prefix,
+// cnt[0..E-1] and off[0..E-1] the counts and offsets.
+struct Rows {
+  int32_t *pref, *cnt, *off;
+};
+
+// Row tile m of expert e, which has mt of them.
+__device__ __forceinline__ void row_tile(const Args& a, const Rows& r, int e, int m, int mt, Tile& ti) {
+  const int cnt = r.cnt[e], off = r.off[e];
   const int blocks = row_blocks(cnt);
   const int b0 = (int)((long long)m * blocks / mt), b1 = (int)((long long)(m + 1) * blocks / mt);
   ti.e = e;
@@ -155,15 +161,15 @@ __device__ __forceinline__ int find_expert(const int32_t* pref, int E, int x, in
   return lo;
 }
 
-__device__ __forceinline__ Tile decode(int t, const int32_t* pref, const Args& a) {
-  const int e = find_expert(pref, a.E, t, a.n_tiles);
-  const int mt = pref[e + 1] - pref[e];
-  const int local = t - pref[e] * a.n_tiles;
+__device__ __forceinline__ Tile decode(int t, const Rows& r, const Args& a) {
+  const int e = find_expert(r.pref, a.E, t, a.n_tiles);
+  const int mt = r.pref[e + 1] - r.pref[e];
+  const int local = t - r.pref[e] * a.n_tiles;
   const int n = local / mt, m = local - n * mt;  // row tiles of one weight tile follow each other (the weight stays in L2)
   Tile ti;
-  row_tile(a, e, m, mt, ti);
+  row_tile(a, r, e, m, mt, ti);
   ti.n0 = n * 2 * BW;
-  ti.mt = pref[e] + m;
+  ti.mt = r.pref[e] + m;
   if (ti.mt >= a.mt_cap) ti.nb = 0;  // (only with counts that exceed the buffers)
   return ti;
 }
@@ -195,20 +201,24 @@ __device__ __forceinline__ bool elect_one() {
   return p != 0;
 }
 
-// Row tiles per expert, of at most NB blocks -> exclusive prefix pref[0..E]
-// (whole CTA).
+// Fills Rows with tiles of at most NB blocks (whole CTA); returns offsets[E].
 template <int NB>
-__device__ __forceinline__ void build_prefix(const Args& a, int32_t* pref) {
+__device__ __forceinline__ int build_rows(const Args& a, const Rows& r) {
   const int E = a.E, lane = threadIdx.x & 31;
-  for (int e = threadIdx.x; e < E; e += blockDim.x)
-    pref[e + 1] = (row_blocks(__ldg(a.counts + e)) + NB - 1) / NB;
-  if (threadIdx.x == 0) pref[0] = 0;
+  const int end_row = __ldg(a.offsets + E);
+  for (int e = threadIdx.x; e < E; e += blockDim.x) {
+    const int c = __ldg(a.counts + e);
+    r.cnt[e] = c;
+    r.off[e] = __ldg(a.offsets + e);
+    r.pref[e + 1] = (row_blocks(c) + NB - 1) / NB;
+  }
+  if (threadIdx.x == 0) r.pref[0] = 0;
   __syncthreads();
   if (threadIdx.x < 32) {
     const int per = (E + 31) / 32;
     const int beg = 1 + lane * per, end = min(E + 1, beg + per);
     int sum = 0;
-    for (int i = beg; i < end; ++i) sum += pref[i];
+    for (int i = beg; i < end; ++i) sum += r.pref[i];
     int incl = sum;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
@@ -217,11 +227,12 @@ __device__ __forceinline__ void build_prefix(const Args& a, int32_t* pref) {
     }
     int run = incl - sum;
     for (int i = beg; i < end; ++i) {
-      run += pref[i];
-      pref[i] = run;
+      run += r.pref[i];
+      r.pref[i] = run;
     }
   }
   __syncthreads();
+  return end_row;
 }
 
 __device__ __forceinline__ void launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
@@ -374,19 +385,19 @@ __device__ __forceinline__ uint32_t row_scales(const uint8_t* base, size_t at, s
 template <int NB>
 __global__ void __launch_bounds__(256) k_mx4_scales(const Args a) {
   constexpr int XB = Lay<NB>::XB;
-  __shared__ int32_t pref[E_MAX + 2];
+  __shared__ int32_t sm[3 * E_MAX + 1];
+  const Rows r{sm, sm + E_MAX + 1, sm + 2 * E_MAX + 1};
   launch_dependents();
-  build_prefix<NB>(a, pref);
-  if (__ldg(a.offsets + a.E) > a.R_cap) return;
+  if (build_rows<NB>(a, r) > a.R_cap) return;
   const int lane = threadIdx.x & 31, warps = blockDim.x >> 5;
   const int ks = a.K / 32;
   const size_t total = (size_t)a.R_cap * ks;
-  const int items = min(pref[a.E], a.mt_cap) * a.num_kb;
+  const int items = min(r.pref[a.E], a.mt_cap) * a.num_kb;
   for (int it = blockIdx.x * warps + (threadIdx.x >> 5); it < items; it += gridDim.x * warps) {
     const int mt = it / a.num_kb, kb = it - mt * a.num_kb;
-    const int e = find_expert(pref, a.E, mt, 1);
+    const int e = find_expert(r.pref, a.E, mt, 1);
     Tile ti;
-    row_tile(a, e, mt - pref[e], pref[e + 1] - pref[e], ti);
+    row_tile(a, r, e, mt - r.pref[e], r.pref[e + 1] - r.pref[e], ti);
     uint32_t v[4 * XB];
 #pragma unroll
     for (int j = 0; j < 4 * XB; ++j)
@@ -410,7 +421,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* sf = smem + L::OFF_SF;
   uint8_t* scratch_all = smem + L::OFF_SCRATCH;
-  int32_t* pref = reinterpret_cast<int32_t*>(smem + L::OFF_PREF);
+  int32_t* rows_sm = reinterpret_cast<int32_t*>(smem + L::OFF_PREF);
+  const Rows rows{rows_sm, rows_sm + E_MAX + 1, rows_sm + 2 * E_MAX + 1};
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + L::OFF_BARS);
   uint64_t* empty = full + STAGES;
   uint64_t* acc_full = full + 2 * STAGES;
@@ -448,15 +460,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     tmem_alloc_pair(tmem_slot, TMEM_COLS);
     tmem_relinquish_pair();
   }
-  build_prefix<NB>(a, pref);
+  const int end_row = build_rows<NB>(a, rows);
   tc_fence_before();
   __syncthreads();
   cluster_sync();  // both CTAs' barriers and tensor memory exist before any cross-CTA use
   tc_fence_after();
   const uint32_t tmem_base = __shfl_sync(0xFFFFFFFFu, *tmem_slot, 0);
-  const bool over = __ldg(a.offsets + E) > a.R_cap;
+  const bool over = end_row > a.R_cap;
   if (over && threadIdx.x == 0) set_status(a.status, MOE_ERR_CAPACITY);
-  const int total = over ? 0 : pref[E] * a.n_tiles;
+  const int total = over ? 0 : rows.pref[E] * a.n_tiles;
   WaitGuard guard{abort_flag, a.status, a.wait_ns};
 
   // The producer's and the MMA issuer's loops are run by their whole warps, in
@@ -471,7 +483,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     const uint32_t full0 = mapa_shared(smem_u32(full), 0);
     if (!weight) wait_for_primary();  // the tiled scales of the rows (in every CTA: the grid ends after its primary)
     for (int t = cl; t < total; t += ncl) {
-      const Tile ti = uniform(decode(t, pref, a));
+      const Tile ti = uniform(decode(t, rows, a));
       if (ti.nb == 0) continue;
       const uint32_t tx = 2u * (W_TX + SF_STAGE) + (uint32_t)ti.nb * 32 * BK;  // both CTAs' bytes
       const int xrow = ti.row0 + rank * 16 * ti.nb, wrow = ti.n0 + rank * BW;
@@ -522,7 +534,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       int stage = 0, lt = 0;
       uint32_t phase = 0;
       for (int t = cl; t < total; t += ncl) {
-        const Tile ti = uniform(decode(t, pref, a));
+        const Tile ti = uniform(decode(t, rows, a));
         if (ti.nb == 0) continue;
         const int buf = lt & 1;
         const uint32_t aph = (uint32_t)(lt >> 1) & 1u;
@@ -578,7 +590,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     Amax amax_bits{0u, 0u};
     int lt = 0;
     for (int t = cl; t < total; t += ncl) {
-      const Tile ti = decode(t, pref, a);
+      const Tile ti = decode(t, rows, a);
       if (ti.nb == 0) continue;
       const int buf = lt & 1;
       const uint32_t aph = (uint32_t)(lt >> 1) & 1u;
