@@ -243,6 +243,61 @@ __global__ void __launch_bounds__(256, 1) k_permute_gather(const uint4* __restri
   }
 }
 
+// The same gather for rows that are already MXFP8 (H codes and H / 32 scales
+// per row: about half the bytes of bf16 rows).  A block of 32 columns lies in
+// one row, so the codes need no change.  Pad rows get zero codes and scales.
+__global__ void __launch_bounds__(256, 1) k_permute_gather_mx(const uint4* __restrict__ xq,
+                                                           const uint8_t* __restrict__ xs, int H, int E,
+                                                           const int32_t* __restrict__ counts,
+                                                           const int32_t* __restrict__ offsets,
+                                                           const int32_t* __restrict__ overflow,
+                                                           int32_t* __restrict__ tok_of, float* __restrict__ prob_perm,
+                                                           uint4* __restrict__ q_perm, uint8_t* __restrict__ s_perm) {
+  __shared__ int32_t s_off[ROUTE_E_MAX + 1];
+  __shared__ int32_t s_cnt[ROUTE_E_MAX];
+  for (int e = threadIdx.x; e <= E; e += blockDim.x) {
+    s_off[e] = offsets[e];
+    if (e < E) s_cnt[e] = counts[e];
+  }
+  __syncthreads();
+  if (*overflow) return;
+  const int R = s_off[E], H16 = H / 16, S = H / 32;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int wpb = blockDim.x >> 5;
+  for (int r = blockIdx.x * wpb + warp; r < R; r += gridDim.x * wpb) {
+    // expert of row r: last e with s_off[e] <= r
+    int lo = 0, hi = E - 1;
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (s_off[mid] <= r) lo = mid; else hi = mid - 1;
+    }
+    uint4* dst = q_perm + (size_t)r * H16;
+    uint8_t* sdst = s_perm + (size_t)r * S;
+    if (r < s_off[lo] + s_cnt[lo]) {
+      const int t = tok_of[r];
+      const uint4* src = xq + (size_t)t * H16;
+      const uint8_t* ssrc = xs + (size_t)t * S;
+      // four 16-byte loads in flight per lane before the stores
+      for (int v = lane; v < H16; v += 128) {
+        uint4 c[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) c[u] = v + 32 * u < H16 ? __ldg(src + v + 32 * u) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+          if (v + 32 * u < H16) dst[v + 32 * u] = c[u];
+      }
+      for (int v = lane; v < S; v += 32) sdst[v] = __ldg(ssrc + v);
+    } else {
+      for (int v = lane; v < H16; v += 32) dst[v] = make_uint4(0, 0, 0, 0);
+      for (int v = lane; v < S; v += 32) sdst[v] = 0;
+      if (lane == 0) {
+        tok_of[r] = -1;
+        prob_perm[r] = 0.0f;
+      }
+    }
+  }
+}
+
 // Column-wise MXFP8 of the permuted rows, fused into the kernels that write
 // them (the weight gradient's operands x_perm and dY_perm; [MoE-Fusion]
 // "Fusing MXFP8 and NVFP4 quantisation": MXFP8 = row-wise output plus a
@@ -693,6 +748,24 @@ extern "C" size_t moe_route_workspace_size(int T, int k, int E) {
   return ((size_t)route_chunks(T, k) * E + 64) * sizeof(int32_t);
 }
 
+// The three routing launches: counts, offsets and the stable permutation.
+static moe_status_t launch_route(const int32_t* topk_idx, const float* topk_prob, int T, int k, int expert_begin, int E,
+                                 int R_cap, int32_t* row_of, int32_t* tok_of, float* prob_perm, int32_t* counts,
+                                 int32_t* offsets, void* ws, int32_t* status, cudaStream_t s) {
+  const int n_assign = T * k;
+  const int n_chunks = route_chunks(T, k);
+  int32_t* chunk_counts = static_cast<int32_t*>(ws);
+  int32_t* overflow = chunk_counts + (size_t)n_chunks * E;
+  k_route_count<<<n_chunks, ROUTE_THREADS, 0, s>>>(topk_idx, n_assign, expert_begin, E, chunk_counts);
+  k_route_scan<<<1, 1024, 0, s>>>(chunk_counts, n_chunks, E, R_cap, counts, offsets, overflow, status);
+  const int scatter_smem = ROUTE_WARPS * E * (int)sizeof(int32_t);
+  if (scatter_smem > 48 * 1024 && !set_smem_limit((const void*)k_route_scatter, scatter_smem)) return MOE_ERR_CUDA;
+  k_route_scatter<<<n_chunks, ROUTE_THREADS, scatter_smem, s>>>(topk_idx, topk_prob, n_assign, k, expert_begin, E,
+                                                                 chunk_counts, offsets, overflow, row_of, tok_of,
+                                                                 prob_perm);
+  return MOE_OK;
+}
+
 extern "C" moe_status_t moe_route_permute(const moe_bf16* x, const int32_t* topk_idx, const float* topk_prob, int T,
                                           int H, int k, int expert_begin, int E, int R_cap, moe_bf16* x_perm,
                                           int32_t* row_of, int32_t* tok_of, float* prob_perm, int32_t* counts,
@@ -707,17 +780,10 @@ extern "C" moe_status_t moe_route_permute(const moe_bf16* x, const int32_t* topk
   if (!aligned16(x) || !aligned16(x_perm)) return MOE_ERR_ARG;
   if (ws_bytes < moe_route_workspace_size(T, k, E)) return MOE_ERR_ARG;
   cudaStream_t s = as_stream(stream);
-  const int n_assign = T * k;
-  const int n_chunks = route_chunks(T, k);
-  int32_t* chunk_counts = static_cast<int32_t*>(ws);
-  int32_t* overflow = chunk_counts + (size_t)n_chunks * E;
-  k_route_count<<<n_chunks, ROUTE_THREADS, 0, s>>>(topk_idx, n_assign, expert_begin, E, chunk_counts);
-  k_route_scan<<<1, 1024, 0, s>>>(chunk_counts, n_chunks, E, R_cap, counts, offsets, overflow, status);
-  const int scatter_smem = ROUTE_WARPS * E * (int)sizeof(int32_t);
-  if (scatter_smem > 48 * 1024 && !set_smem_limit((const void*)k_route_scatter, scatter_smem)) return MOE_ERR_CUDA;
-  k_route_scatter<<<n_chunks, ROUTE_THREADS, scatter_smem, s>>>(topk_idx, topk_prob, n_assign, k, expert_begin, E,
-                                                                 chunk_counts, offsets, overflow, row_of, tok_of,
-                                                                 prob_perm);
+  const moe_status_t rc = launch_route(topk_idx, topk_prob, T, k, expert_begin, E, R_cap, row_of, tok_of, prob_perm,
+                                       counts, offsets, ws, status, s);
+  if (rc != MOE_OK) return rc;
+  const int32_t* overflow = static_cast<int32_t*>(ws) + (size_t)route_chunks(T, k) * E;
   if (xq_col) {
     if (!set_smem_limit((const void*)k_permute_gather_qcol, Qf<1024>::SMEM)) return MOE_ERR_CUDA;
     k_permute_gather_qcol<<<R_cap / 32, QF_THREADS, Qf<1024>::SMEM, s>>>(
@@ -732,6 +798,32 @@ extern "C" moe_status_t moe_route_permute(const moe_bf16* x, const int32_t* topk
     k_permute_gather<<<grid, 256, 0, s>>>(reinterpret_cast<const uint4*>(x), H / 8, E, counts, offsets, overflow,
                                           tok_of, prob_perm, reinterpret_cast<uint4*>(x_perm));
   }
+  count_launch(4);
+  return launch_status();
+}
+
+extern "C" moe_status_t moe_route_permute_mxfp8(const uint8_t* xq, const uint8_t* xs, const int32_t* topk_idx,
+                                                const float* topk_prob, int T, int H, int k, int expert_begin, int E,
+                                                int R_cap, uint8_t* xq_perm, uint8_t* xs_perm, int32_t* row_of,
+                                                int32_t* tok_of, float* prob_perm, int32_t* counts, int32_t* offsets,
+                                                void* ws, size_t ws_bytes, int32_t* status, moe_stream_t stream) {
+  if (!xq || !xs || !topk_idx || !topk_prob || !xq_perm || !xs_perm || !row_of || !tok_of || !prob_perm || !counts ||
+      !offsets || !ws)
+    return MOE_ERR_ARG;
+  if (T <= 0 || H <= 0 || (H & 31) || k <= 0 || k > 64 || E <= 0 || E > ROUTE_E_MAX || R_cap <= 0 || (R_cap & 31))
+    return MOE_ERR_ARG;
+  if ((int64_t)T * k > (int64_t)INT32_MAX / 2) return MOE_ERR_ARG;
+  if (!aligned16(xq) || !aligned16(xq_perm) || ws_bytes < moe_route_workspace_size(T, k, E)) return MOE_ERR_ARG;
+  cudaStream_t s = as_stream(stream);
+  const moe_status_t rc = launch_route(topk_idx, topk_prob, T, k, expert_begin, E, R_cap, row_of, tok_of, prob_perm,
+                                       counts, offsets, ws, status, s);
+  if (rc != MOE_OK) return rc;
+  const int32_t* overflow = static_cast<int32_t*>(ws) + (size_t)route_chunks(T, k) * E;
+  int grid = (R_cap + 7) / 8;
+  if (grid > sm_count() * 8) grid = sm_count() * 8;
+  if (grid < 1) grid = 1;
+  k_permute_gather_mx<<<grid, 256, 0, s>>>(reinterpret_cast<const uint4*>(xq), xs, H, E, counts, offsets, overflow,
+                                           tok_of, prob_perm, reinterpret_cast<uint4*>(xq_perm), xs_perm);
   count_launch(4);
   return launch_status();
 }

@@ -758,3 +758,32 @@ def fc1_fwd_mxfp4(xq, xs, W1q, W1s, counts, offsets, F: int, params: L.GluParams
         st.data_ptr(), _cur(xq)), "moe_grouped_fc1_glu_quant_fwd_mxfp4")
     o["status"] = st
     return o
+
+
+def route_permute_mxfp8(xq, xs, topk_idx, topk_prob, E: int, R_cap: int, expert_begin: int = 0, status=None) -> dict:
+    """route_permute for MXFP8 rows xq [T, H], xs [T, H/32]: the routing tensors
+    and xq_perm [R_cap, H], xs_perm [R_cap, H/32]."""
+    T, H = _rows_mxfp8(xq, xs, "x")
+    k = _need2(topk_idx, torch.int32, "topk_idx")[1]
+    _need(topk_idx, torch.int32, (T, k), "topk_idx")
+    _need(topk_prob, torch.float32, (T, k), "topk_prob")
+    dev, i32, u8 = xq.device, torch.int32, torch.uint8
+    o = {
+        "xq_perm": torch.empty(R_cap, H, dtype=u8, device=dev),
+        "xs_perm": torch.empty(R_cap, H // 32, dtype=u8, device=dev),
+        "row_of": torch.empty(T * k, dtype=i32, device=dev),
+        "tok_of": torch.empty(R_cap, dtype=i32, device=dev),
+        "prob_perm": torch.empty(R_cap, dtype=torch.float32, device=dev),
+        "counts": torch.empty(E, dtype=i32, device=dev),
+        "offsets": torch.empty(E + 1, dtype=i32, device=dev),
+    }
+    n = _size("moe_route_workspace_size", T, k, E)
+    ws = torch.empty(n, dtype=u8, device=dev)
+    st = status if status is not None else new_status(dev)
+    L.check(L.load().moe_route_permute_mxfp8(
+        xq.data_ptr(), xs.data_ptr(), topk_idx.data_ptr(), topk_prob.data_ptr(), T, H, k, expert_begin, E, R_cap,
+        o["xq_perm"].data_ptr(), o["xs_perm"].data_ptr(), o["row_of"].data_ptr(), o["tok_of"].data_ptr(),
+        o["prob_perm"].data_ptr(), o["counts"].data_ptr(), o["offsets"].data_ptr(), ws.data_ptr(), n, st.data_ptr(),
+        _cur(xq)), "moe_route_permute_mxfp8")
+    o["status"] = st
+    return o

@@ -191,6 +191,17 @@ MOE_API moe_status_t moe_route_permute(const moe_bf16* x, const int32_t* topk_id
                                int32_t* counts, int32_t* offsets, uint8_t* xq_col, uint8_t* xs_col,
                                void* ws, size_t ws_bytes, int32_t* status, moe_stream_t stream);
 
+/* moe_route_permute for rows that are already MXFP8 (the norm's row-wise
+ * output, moe_rmsnorm_fwd): xq [T][H] E4M3 with xs [T][H/32] E8M0 ->
+ * xq_perm [R_cap][H], xs_perm [R_cap][H/32] (pad rows zero), what an
+ * MXFP8-input FC1 reads.  The other outputs, the workspace and the status as
+ * moe_route_permute.  H % 32 == 0; xq and xq_perm 16-byte aligned. */
+MOE_API moe_status_t moe_route_permute_mxfp8(const uint8_t* xq, const uint8_t* xs, const int32_t* topk_idx,
+                                             const float* topk_prob, int T, int H, int k, int expert_begin, int E,
+                                             int R_cap, uint8_t* xq_perm, uint8_t* xs_perm, int32_t* row_of,
+                                             int32_t* tok_of, float* prob_perm, int32_t* counts, int32_t* offsets,
+                                             void* ws, size_t ws_bytes, int32_t* status, moe_stream_t stream);
+
 /* GroupGemm + Activation + Quantize/Transpose, forward ([MoE-Fusion]).
  * pre = x_perm[rows of e] . W1p[e]^T + b1p[e]  (bf16 in, fp32 accumulate in
  * tensor memory); the epilogue pairs input/gate columns of the packed tile,
