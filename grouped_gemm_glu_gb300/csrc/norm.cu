@@ -43,18 +43,25 @@ constexpr int MAX_T = 1 << 30;  // row indexes stay in 32 bits a few grids past 
 constexpr int FEW_ROWS = 256;
 constexpr int RING_BYTES = 200 * 1024;  // of the 227 KB a CTA may have
 
-__device__ __forceinline__ void unpack8(const uint4 q, float* v) {
-  v[0] = bf16_lo(q.x);
-  v[1] = bf16_hi(q.x);
-  v[2] = bf16_lo(q.y);
-  v[3] = bf16_hi(q.y);
-  v[4] = bf16_lo(q.z);
-  v[5] = bf16_hi(q.z);
-  v[6] = bf16_lo(q.w);
-  v[7] = bf16_hi(q.w);
+// Eight bf16 values as four float pairs (the packed fp32 instructions of
+// sm_100 work on pairs).
+__device__ __forceinline__ void unpack8(const uint4 q, float2* v) {
+  v[0] = make_float2(bf16_lo(q.x), bf16_hi(q.x));
+  v[1] = make_float2(bf16_lo(q.y), bf16_hi(q.y));
+  v[2] = make_float2(bf16_lo(q.z), bf16_hi(q.z));
+  v[3] = make_float2(bf16_lo(q.w), bf16_hi(q.w));
 }
-__device__ __forceinline__ uint4 pack8(const float* v) {
-  return make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
+__device__ __forceinline__ uint4 pack8(const float2* v) {
+  return make_uint4(pack_bf16x2(v[0].x, v[0].y), pack_bf16x2(v[1].x, v[1].y), pack_bf16x2(v[2].x, v[2].y),
+                    pack_bf16x2(v[3].x, v[3].y));
+}
+__device__ __forceinline__ float2 pair_of(float a) { return make_float2(a, a); }
+__device__ __forceinline__ float2 neg2(float2 a) { return make_float2(-a.x, -a.y); }
+// The larger magnitude, NaN if either is.
+__device__ __forceinline__ float max_abs(float m, float v) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(m), "f"(fabsf(v)));
+  return r;
 }
 
 __device__ __forceinline__ void cp_async16(void* dst, const void* src) {
@@ -82,36 +89,53 @@ __device__ __forceinline__ Pair two_sum(float a, float b) {  // a + b = hi + lo 
   return {s, (a - (s - bb)) + (b - bb)};
 }
 
-// Sum over a group's wpr warps, in the same order for every thread: within a
-// warp in fp32, across warps with the rounding errors kept.  red: two sets
-// of one float per warp of the CTA, used in turn (par), so that one barrier
-// per row is enough: a warp writes a set again only after the barrier of the
-// row between.
-__device__ __forceinline__ Pair row_sum(float v, float* red, int par, int group, int wpr) {
+// Adds the squares of v to the sums hi + lo of the two halves, keeping the
+// rounding errors (a square of a bf16 value is exact in fp32).
+__device__ __forceinline__ void add_squares(float2 v, float2& hi, float2& lo) {
+  const float2 q = __fmul2_rn(v, v);
+  const float2 s = __fadd2_rn(hi, q), bb = __fadd2_rn(s, neg2(hi));
+  lo = __fadd2_rn(lo, __fadd2_rn(__fadd2_rn(hi, neg2(__fadd2_rn(s, neg2(bb)))), __fadd2_rn(q, neg2(bb))));
+  hi = s;
+}
+
+// Adds another lane's pair; EXACT keeps the rounding errors of the sums.
+template <bool EXACT>
+__device__ __forceinline__ Pair lane_add(Pair s, int d) {
+  const float oh = __shfl_xor_sync(0xFFFFFFFFu, s.hi, d);
+  if (!EXACT) return {s.hi + oh, 0.0f};
+  const float ol = __shfl_xor_sync(0xFFFFFFFFu, s.lo, d);
+  const Pair q = two_sum(s.hi, oh);
+  return {q.hi, q.lo + (s.lo + ol)};
+}
+
+// Sum over a group's wpr warps, in the same order for every thread.  red: two
+// sets of one pair per warp of the CTA, used in turn (par), so that one
+// barrier per row is enough: a warp writes a set again only after the barrier
+// of the row between.
+template <bool EXACT>
+__device__ __forceinline__ Pair row_sum(Pair s, float2* red, int par, int group, int wpr) {
 #pragma unroll
-  for (int d = 16; d > 0; d >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, d);
-  if (wpr == 1) return {v, 0.0f};
+  for (int d = 16; d > 0; d >>= 1) s = lane_add<EXACT>(s, d);
+  if (wpr == 1) return s;
   const int lane = threadIdx.x & 31;
   red += par * 32;
-  if (lane == 0) red[threadIdx.x >> 5] = v;
+  if (lane == 0) red[threadIdx.x >> 5] = make_float2(s.hi, s.lo);
   asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "r"(32 * wpr) : "memory");
-  Pair s{lane < wpr ? red[group * wpr + lane] : 0.0f, 0.0f};
+  const float2 o = lane < wpr ? red[group * wpr + lane] : make_float2(0.0f, 0.0f);
+  s = {o.x, o.y};
 #pragma unroll
-  for (int d = 16; d > 0; d >>= 1) {
-    if (d >= 2 * wpr) continue;
-    const float oh = __shfl_xor_sync(0xFFFFFFFFu, s.hi, d), ol = __shfl_xor_sync(0xFFFFFFFFu, s.lo, d);
-    const Pair q = two_sum(s.hi, oh);
-    s = {q.hi, q.lo + (s.lo + ol)};
-  }
-  // lanes past the last warp's hold other sums when 2 wpr is not above 31
+  for (int d = 16; d > 0; d >>= 1)
+    if (d < 2 * wpr) s = lane_add<EXACT>(s, d);
+  // (lane 0's is the sum of lanes 0 .. 2^j - 1 with 2^j >= wpr)
   s.hi = __shfl_sync(0xFFFFFFFFu, s.hi, 0);
   s.lo = __shfl_sync(0xFFFFFFFFu, s.lo, 0);
   return s;
 }
 
-// 1 / sqrt(ss / n + eps) as hi + lo, good to about 2^-30: the quantised
+// 1 / sqrt(ss / n + eps) as hi + lo, good to about 2^-29: the quantised
 // outputs round y on a coarse grid, where an error of y of one fp32 step
-// already moves some value of a large batch across a rounding boundary.
+// already moves some value of a large batch across a rounding boundary (36
+// of 58.7 million codes with everything in fp32).
 __device__ __forceinline__ Pair inv_rms(Pair ss, float n, float eps) {
   const float q = ss.hi / n;
   const float q_lo = (fmaf(-q, n, ss.hi) + ss.lo) / n;
@@ -124,6 +148,15 @@ __device__ __forceinline__ Pair inv_rms(Pair ss, float n, float eps) {
   return {r, fabsf(e) < 1e-3f ? 0.5f * r * e : 0.0f};  // (no correction for 0, Inf, NaN)
 }
 
+// y = p (r.hi + r.lo) rounded to fp32; if it sits on the middle of two E4M3
+// values and the rounding dropped something, the neighbour on that side.
+__device__ __forceinline__ float off_middle(float y, float p, Pair r) {
+  if ((__float_as_uint(y) & 0xFFFFFu) != 0x80000u) return y;
+  const float rest = fmaf(p, r.hi, -y) + p * r.lo;
+  if (rest == 0.0f || rest != rest) return y;
+  return __uint_as_float(__float_as_uint(y) + ((rest > 0.0f) == (y > 0.0f) ? 1u : 0xFFFFFFFFu));
+}
+
 // V: 16-byte vectors of a row per thread; vector j of a thread is column
 // group t + j * 32 wpr of the row.
 template <int V>
@@ -132,7 +165,7 @@ __global__ void __launch_bounds__(max_threads<V>()) k_rmsnorm_fwd(
     int H8, int wpr, int groups, int stages, uint4* __restrict__ h_out, uint4* __restrict__ y, uint8_t* __restrict__ q,
     uint8_t* __restrict__ s, float* __restrict__ rstd) {
   extern __shared__ __align__(16) uint4 ring[];  // [stages][inputs][V][threads]
-  __shared__ float red[64];
+  __shared__ float2 red[64];
   const int tpr = 32 * wpr, group = threadIdx.x / tpr, t = threadIdx.x - group * tpr;
   const int nin = res != nullptr ? 2 : 1, nthr = blockDim.x;
   const int slot0 = blockIdx.x * groups + group, slots = gridDim.x * groups;
@@ -161,60 +194,76 @@ __global__ void __launch_bounds__(max_threads<V>()) k_rmsnorm_fwd(
     cp_async_wait(stages - 1);
     const uint4* d = ring + (size_t)stage * nin * V * nthr + threadIdx.x;
     uint4 hv[V];
-    float ss = 0.0f;
+    float2 hi = pair_of(0.0f), lo = pair_of(0.0f);
 #pragma unroll
     for (int j = 0; j < V; ++j) {
       const int c = t + j * tpr;
       hv[j] = make_uint4(0, 0, 0, 0);
+      float2 v[4];
       if (c < H8) {
         hv[j] = d[j * nthr];
         if (nin == 2) {
-          float a[8], b[8];
-          unpack8(hv[j], a);
+          float2 b[4];
+          unpack8(hv[j], v);
           unpack8(d[(V + j) * nthr], b);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) a[i] += b[i];
-          hv[j] = pack8(a);
+          for (int i = 0; i < 4; ++i) v[i] = __fadd2_rn(v[i], b[i]);
+          hv[j] = pack8(v);
           h_out[base + c] = hv[j];
         }
       }
-      float v[8];
       unpack8(hv[j], v);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) ss = fmaf(v[i], v[i], ss);
+      for (int i = 0; i < 4; ++i) add_squares(v[i], hi, lo);
     }
-    const Pair sum = row_sum(ss, red, par, group, wpr);  // (the row's slots have been read)
+    Pair part = two_sum(hi.x, hi.y);
+    part.lo += lo.x + lo.y;
+    const Pair sum = row_sum<true>(part, red, par, group, wpr);  // (the row's slots have been read)
     fetch(row + stages * slots, stage);
     if (++stage == stages) stage = 0;
     par ^= 1;
     const Pair r = inv_rms(sum, (float)(8 * H8), eps);
+    const float2 rhi = pair_of(r.hi), rlo = pair_of(r.lo);
     if (rstd != nullptr && t == 0) rstd[row] = r.hi + r.lo;
 #pragma unroll
     for (int j = 0; j < V; ++j) {
       const int c = t + j * tpr;
       const bool in = c < H8;
-      float v[8], g[8];
+      float2 v[4], g[4];
       unpack8(hv[j], v);
       unpack8(gm[j], g);
+      uint32_t mid = 0xFFFFFFFFu;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float p = v[i] * g[i];  // exact: two 8-bit significands
-        v[i] = fmaf(p, r.hi, p * r.lo);
+      for (int i = 0; i < 4; ++i) {
+        g[i] = __fmul2_rn(v[i], g[i]);  // exact: two 8-bit significands
+        v[i] = __ffma2_rn(g[i], rhi, __fmul2_rn(g[i], rlo));
+        mid = min(mid, min((__float_as_uint(v[i].x) ^ 0x80000u) & 0xFFFFFu, (__float_as_uint(v[i].y) ^ 0x80000u) & 0xFFFFFu));
+      }
+      // a y that was rounded onto the middle of two codes (20 bits below E4M3's three: a 1 and zeros): what
+      // the rounding dropped decides the code
+      if (q != nullptr && mid == 0u) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          v[i].x = off_middle(v[i].x, g[i].x, r);
+          v[i].y = off_middle(v[i].y, g[i].y, r);
+        }
       }
       if (in && y != nullptr) y[base + c] = pack8(v);
       if (q != nullptr) {
         // a 32-column block is four consecutive lanes (H % 32 == 0: all four are in range, or none)
-        uint32_t m = 0;
+        float m = 0.0f;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) m = max(m, abs_bits(v[i]));
-        m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
-        m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
-        const uint32_t sb = e8m0_from_amax_bits(m);
+        for (int i = 0; i < 4; ++i) m = max_abs(max_abs(m, v[i].x), v[i].y);
+        m = max_abs(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
+        m = max_abs(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
+        const uint32_t sb = e8m0_from_amax_bits(abs_bits(m));
         uint2 code = make_uint2(0x7F7F7F7Fu, 0x7F7F7F7Fu);
         if (sb != 0xFFu) {
-          const float inv = mx_inv_scale(sb);
-          code.x = e4m3x2(v[0] * inv, v[1] * inv) | (e4m3x2(v[2] * inv, v[3] * inv) << 16);
-          code.y = e4m3x2(v[4] * inv, v[5] * inv) | (e4m3x2(v[6] * inv, v[7] * inv) << 16);
+          const float2 inv = pair_of(mx_inv_scale(sb));
+#pragma unroll
+          for (int i = 0; i < 4; ++i) v[i] = __fmul2_rn(v[i], inv);
+          code.x = e4m3x2(v[0].x, v[0].y) | (e4m3x2(v[1].x, v[1].y) << 16);
+          code.y = e4m3x2(v[2].x, v[2].y) | (e4m3x2(v[3].x, v[3].y) << 16);
         }
         if (in) {
           reinterpret_cast<uint2*>(q)[base + c] = code;
@@ -235,7 +284,7 @@ __global__ void __launch_bounds__(max_threads<V>()) k_rmsnorm_bwd(
     const uint4* __restrict__ gamma, const float* __restrict__ rstd, int T, int H8, int wpr, int groups, int stages,
     uint4* __restrict__ dx, float* __restrict__ part) {
   extern __shared__ __align__(16) uint4 ring[];  // [stages][inputs][V][threads]
-  __shared__ float red[64];
+  __shared__ float2 red[64];
   const int tpr = 32 * wpr, group = threadIdx.x / tpr, t = threadIdx.x - group * tpr;
   const int nin = dres != nullptr ? 3 : 2, nthr = blockDim.x;
   const int slot0 = blockIdx.x * groups + group, slots = gridDim.x * groups;
@@ -256,11 +305,11 @@ __global__ void __launch_bounds__(max_threads<V>()) k_rmsnorm_bwd(
     }
     cp_async_commit();
   };
-  float acc[V][8];
+  float2 acc[V][4];
 #pragma unroll
   for (int j = 0; j < V; ++j)
 #pragma unroll
-    for (int i = 0; i < 8; ++i) acc[j][i] = 0.0f;
+    for (int i = 0; i < 4; ++i) acc[j][i] = pair_of(0.0f);
   for (int st = 0; st < stages; ++st) fetch(slot0 + st * slots, st);
   int stage = 0, par = 0;
   float r = slot0 < T ? __ldg(rstd + slot0) : 0.0f;
@@ -270,7 +319,8 @@ __global__ void __launch_bounds__(max_threads<V>()) k_rmsnorm_bwd(
     cp_async_wait(stages - 1);
     const uint4* b = ring + (size_t)stage * nin * V * nthr + threadIdx.x;
     uint4 dv[V], hv[V], ev[V];
-    float dot = 0.0f;
+    float2 dot2 = pair_of(0.0f);
+    const float2 r2 = pair_of(r);
 #pragma unroll
     for (int j = 0; j < V; ++j) {
       const int c = t + j * tpr;
@@ -279,33 +329,33 @@ __global__ void __launch_bounds__(max_threads<V>()) k_rmsnorm_bwd(
       dv[j] = b[j * nthr];
       hv[j] = b[(V + j) * nthr];
       if (nin == 3) ev[j] = b[(2 * V + j) * nthr];
-      float d[8], v[8], g[8];
+      float2 d[4], v[4], g[4];
       unpack8(dv[j], d);
       unpack8(hv[j], v);
       unpack8(__ldg(gamma + c), g);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        dot = fmaf(d[i] * g[i], v[i], dot);
-        acc[j][i] = fmaf(d[i], v[i] * r, acc[j][i]);
+      for (int i = 0; i < 4; ++i) {
+        dot2 = __ffma2_rn(__fmul2_rn(d[i], g[i]), v[i], dot2);
+        acc[j][i] = __ffma2_rn(d[i], __fmul2_rn(v[i], r2), acc[j][i]);
       }
     }
-    dot = row_sum(dot, red, par, group, wpr).hi;
+    const float dot = row_sum<false>(Pair{dot2.x + dot2.y, 0.0f}, red, par, group, wpr).hi;
     fetch(row + stages * slots, stage);
     if (++stage == stages) stage = 0;
     par ^= 1;
-    const float k = r * r * (dot * inv_h);
+    const float2 k = pair_of(-(r * r * (dot * inv_h)));
 #pragma unroll
     for (int j = 0; j < V; ++j) {
       const int c = t + j * tpr;
       if (c >= H8) continue;
-      float d[8], v[8], g[8], e[8], o[8];
+      float2 d[4], v[4], g[4], e[4];
       unpack8(dv[j], d);
       unpack8(hv[j], v);
       unpack8(ev[j], e);
       unpack8(__ldg(gamma + c), g);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) o[i] = fmaf(r, fmaf(-v[i], k, d[i] * g[i]), e[i]);
-      dx[base + c] = pack8(o);
+      for (int i = 0; i < 4; ++i) d[i] = __ffma2_rn(r2, __ffma2_rn(v[i], k, __fmul2_rn(d[i], g[i])), e[i]);
+      dx[base + c] = pack8(d);
     }
     r = r_next;
   }
@@ -315,8 +365,8 @@ __global__ void __launch_bounds__(max_threads<V>()) k_rmsnorm_bwd(
       const int c = t + j * tpr;
       if (c >= H8) continue;
       float4* d = reinterpret_cast<float4*>(part + (size_t)slot0 * H8 * 8) + 2 * c;
-      d[0] = make_float4(acc[j][0], acc[j][1], acc[j][2], acc[j][3]);
-      d[1] = make_float4(acc[j][4], acc[j][5], acc[j][6], acc[j][7]);
+      d[0] = make_float4(acc[j][0].x, acc[j][0].y, acc[j][1].x, acc[j][1].y);
+      d[1] = make_float4(acc[j][2].x, acc[j][2].y, acc[j][3].x, acc[j][3].y);
     }
   }
 }
@@ -366,19 +416,16 @@ __global__ void __launch_bounds__(256) k_dequant_mxfp8(const uint4* __restrict__
     for (int u = 0; u < DQ_UNROLL; ++u) {
       const size_t i = i0 + u * step;
       if (i >= n16) break;
-      const float sc = e8m0_value(sb[u]);
+      const float2 sc = pair_of(e8m0_value(sb[u]));
       const uint32_t c[4] = {w[u].x, w[u].y, w[u].z, w[u].w};
-      float v[16];
+      float2 v[8];
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const float2 a = e4m3x2_value(c[j] & 0xFFFFu), b = e4m3x2_value(c[j] >> 16);
-        v[4 * j] = a.x * sc;
-        v[4 * j + 1] = a.y * sc;
-        v[4 * j + 2] = b.x * sc;
-        v[4 * j + 3] = b.y * sc;
+        v[2 * j] = __fmul2_rn(e4m3x2_value(c[j] & 0xFFFFu), sc);
+        v[2 * j + 1] = __fmul2_rn(e4m3x2_value(c[j] >> 16), sc);
       }
       out[2 * i] = pack8(v);
-      out[2 * i + 1] = pack8(v + 8);
+      out[2 * i + 1] = pack8(v + 4);
     }
   }
 }
