@@ -371,61 +371,59 @@ __global__ void __launch_bounds__(max_threads<V>()) k_rmsnorm_bwd(
   }
 }
 
-// dgamma[c] = sum over the slots of part[slot][c], in a fixed order: 8 warps
-// take every eighth line of 32 columns, then their sums are added in warp order.
-__global__ void __launch_bounds__(256) k_dgamma_sum(const float* __restrict__ part, int slots, int H,
-                                                    float* __restrict__ dgamma) {
-  __shared__ float sm[8][32];
+// dgamma[c] = sum over the slots of part[slot][c], in a fixed order: warp w
+// of 32 takes lines w, w + 32, ... of 32 columns (a few loads each, all in
+// flight: a launch of this size is latency), then the warps' sums are added
+// in warp order.
+__global__ void __launch_bounds__(1024) k_dgamma_sum(const float* __restrict__ part, int slots, int H,
+                                                     float* __restrict__ dgamma) {
+  __shared__ float sm[32][32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int c = blockIdx.x * 32 + lane;
   float a = 0.0f;
-  if (c < H)
+  if (c < H) {
 #pragma unroll 8
-    for (int sl = warp; sl < slots; sl += 8) a += __ldg(part + (size_t)sl * H + c);
+    for (int sl = warp; sl < slots; sl += 32) a += __ldg(part + (size_t)sl * H + c);
+  }
   sm[warp][lane] = a;
   __syncthreads();
   if (warp == 0 && c < H) {
     a = sm[0][lane];
 #pragma unroll
-    for (int w = 1; w < 8; ++w) a += sm[w][lane];
+    for (int w = 1; w < 32; ++w) a += sm[w][lane];
     dgamma[c] = a;
   }
 }
 
 // MXFP8 rows back to bf16: e4m3 * 2^(s - 127) has at most 4 significant bits,
-// so the result is exact (unless it leaves bf16's range).  One thread per 16
-// codes (16 bytes in, 32 out).
-constexpr int DQ_UNROLL = 4;  // 16-byte loads in flight per thread
-__global__ void __launch_bounds__(256) k_dequant_mxfp8(const uint4* __restrict__ q, const uint8_t* __restrict__ s,
-                                                       size_t n16, uint4* __restrict__ out) {
+// so the result is exact (unless it leaves bf16's range).  A thread converts 8
+// codes at a time (8 bytes in, 16 out, neighbouring threads neighbouring
+// codes).
+constexpr int DQ_UNROLL = 8;  // loads in flight per thread
+__global__ void __launch_bounds__(256) k_dequant_mxfp8(const uint2* __restrict__ q, const uint8_t* __restrict__ s,
+                                                       size_t n8, uint4* __restrict__ out) {
   const size_t step = (size_t)gridDim.x * blockDim.x;
-  for (size_t i0 = (size_t)blockIdx.x * blockDim.x + threadIdx.x; i0 < n16; i0 += DQ_UNROLL * step) {
-    uint4 w[DQ_UNROLL];
+  for (size_t i0 = (size_t)blockIdx.x * blockDim.x + threadIdx.x; i0 < n8; i0 += DQ_UNROLL * step) {
+    uint2 w[DQ_UNROLL];
     uint32_t sb[DQ_UNROLL];
 #pragma unroll
     for (int u = 0; u < DQ_UNROLL; ++u) {
       const size_t i = i0 + u * step;
-      w[u] = make_uint4(0, 0, 0, 0);
+      w[u] = make_uint2(0, 0);
       sb[u] = 0;
-      if (i < n16) {
+      if (i < n8) {
         w[u] = __ldg(q + i);
-        sb[u] = __ldg(s + (i >> 1));
+        sb[u] = __ldg(s + (i >> 2));
       }
     }
 #pragma unroll
     for (int u = 0; u < DQ_UNROLL; ++u) {
       const size_t i = i0 + u * step;
-      if (i >= n16) break;
+      if (i >= n8) break;
       const float2 sc = pair_of(e8m0_value(sb[u]));
-      const uint32_t c[4] = {w[u].x, w[u].y, w[u].z, w[u].w};
-      float2 v[8];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        v[2 * j] = __fmul2_rn(e4m3x2_value(c[j] & 0xFFFFu), sc);
-        v[2 * j + 1] = __fmul2_rn(e4m3x2_value(c[j] >> 16), sc);
-      }
-      out[2 * i] = pack8(v);
-      out[2 * i + 1] = pack8(v + 4);
+      const float2 v[4] = {__fmul2_rn(e4m3x2_value(w[u].x & 0xFFFFu), sc), __fmul2_rn(e4m3x2_value(w[u].x >> 16), sc),
+                           __fmul2_rn(e4m3x2_value(w[u].y & 0xFFFFu), sc), __fmul2_rn(e4m3x2_value(w[u].y >> 16), sc)};
+      out[i] = pack8(v);
     }
   }
 }
@@ -536,7 +534,7 @@ extern "C" moe_status_t moe_rmsnorm_bwd(const moe_bf16* dy, const moe_bf16* dres
   };
   const moe_status_t rc = p.V == 1 ? run(k_rmsnorm_bwd<1>) : p.V == 2 ? run(k_rmsnorm_bwd<2>) : run(k_rmsnorm_bwd<4>);
   if (rc != MOE_OK || !dgamma) return rc;
-  k_dgamma_sum<<<(H + 31) / 32, 256, 0, as_stream(stream)>>>(part, grid * p.groups, H, dgamma);
+  k_dgamma_sum<<<(H + 31) / 32, 1024, 0, as_stream(stream)>>>(part, grid * p.groups, H, dgamma);
   count_launch();
   return launch_status();
 }
@@ -546,12 +544,12 @@ extern "C" moe_status_t moe_dequantize_mxfp8(const uint8_t* q, const uint8_t* s,
   using namespace norm;
   if (blocks == 0) return MOE_OK;
   if (!q || !s || !out || !aligned16(q) || !aligned16(out)) return MOE_ERR_ARG;
-  const size_t n16 = 2 * blocks;
-  size_t grid = (n16 + 255) / 256;
+  const size_t n8 = 4 * blocks;
+  size_t grid = (n8 + 255) / 256;
   const size_t cap = (size_t)sm_count() * 8;
   if (cap == 0) return MOE_ERR_CUDA;
   if (grid > cap) grid = cap;
-  k_dequant_mxfp8<<<(int)grid, 256, 0, as_stream(stream)>>>(reinterpret_cast<const uint4*>(q), s, n16,
+  k_dequant_mxfp8<<<(int)grid, 256, 0, as_stream(stream)>>>(reinterpret_cast<const uint2*>(q), s, n8,
                                                            reinterpret_cast<uint4*>(out));
   count_launch();
   return launch_status();
