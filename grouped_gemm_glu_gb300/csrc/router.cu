@@ -345,6 +345,137 @@ __global__ void __launch_bounds__(32 * max_warps<VL>()) k_router_fwd(const void*
   }
 }
 
+// The same choice for few experts without groups (n <= LPT VL, k <= LPT):
+// LPT lanes per token, 32 / LPT tokens per warp, so that no lane idles and a
+// round serves all of them: with 64 experts on 8 lanes a warp spends about
+// the instructions on four tokens that it spent on one.  The reductions are
+// shuffles inside the token's lanes.
+template <int LPT, int VL, bool BF16>
+__global__ void __launch_bounds__(32 * max_warps<VL>()) k_router_small(const void* __restrict__ logits,
+                                                                       const float* __restrict__ bias,
+                                                                       const uint8_t* __restrict__ mask, int T,
+                                                                       const Params p, int32_t* __restrict__ idx,
+                                                                       float* __restrict__ prob,
+                                                                       int32_t* __restrict__ load) {
+  constexpr int TPW = 32 / LPT;
+  extern __shared__ __align__(16) uint32_t keys_all[];  // [warps][32 VL] keys, [warps][32] choices (two words), hist
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+  uint32_t* keys = keys_all + warp * 32 * VL;
+  uint2* picks = reinterpret_cast<uint2*>(keys_all + warps * 32 * VL) + warp * 32;
+  int32_t* hist = reinterpret_cast<int32_t*>(keys_all + warps * (32 * VL + 64));
+  const int n = p.n, sub = lane & (LPT - 1), first = lane - sub;  // the token's first lane
+  const unsigned seg = (LPT == 32 ? 0xFFFFFFFFu : (1u << LPT) - 1u) << first;
+  if (load != nullptr) {
+    for (int e = threadIdx.x; e < n; e += blockDim.x) hist[e] = 0;
+    __syncthreads();
+  }
+  const bool sig = p.score == MOE_SCORE_SIGMOID;
+  auto seg_sum = [&](float v) {
+#pragma unroll
+    for (int d = LPT / 2; d > 0; d >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, d);
+    return v;
+  };
+  auto seg_max = [&](float v) {
+#pragma unroll
+    for (int d = LPT / 2; d > 0; d >>= 1) v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, d));
+    return v;
+  };
+  for (int t0 = (blockIdx.x * warps + warp) * TPW; t0 < T; t0 += gridDim.x * warps * TPW) {
+    const int t = t0 + lane / LPT;
+    const bool on = t < T && (mask == nullptr || __ldg(mask + t) != 0);
+    float x[VL];
+    uint32_t key[VL];
+    if (on) {
+      load_row<VL, BF16>(logits, t, n, sub, p.vec != 0, x);
+    } else {
+#pragma unroll
+      for (int i = 0; i < VL; ++i) x[i] = -INFINITY;
+    }
+    Soft sm{0.0f, 1.0f};
+    if (!sig && (bias != nullptr || !p.renorm)) {
+      float m = x[0];
+#pragma unroll
+      for (int i = 1; i < VL; ++i) m = fmaxf(m, x[i]);
+      m = seg_max(m);
+      if (m == -INFINITY) m = 0.0f;
+      float sum = 0.0f;
+#pragma unroll
+      for (int i = 0; i < VL; ++i) sum += expf(x[i] - m);
+      sum = seg_sum(sum);
+      sm = {m, sum != sum ? sum : fmaxf(sum, 1e-38f)};
+    }
+    if (bias != nullptr) {
+      float b[VL];
+      load_row<VL, false>(bias, 0, n, sub, p.vec_bias != 0, b);
+#pragma unroll
+      for (int i = 0; i < VL; ++i)
+        key[i] = ordered_key(x[i] == -INFINITY ? x[i] : (sig ? sigmoid(x[i]) : soft_score(sm, x[i])) + b[i]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < VL; ++i) key[i] = ordered_key(x[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < VL; ++i) keys[lane * VL + i] = key[i];
+    sort_desc<VL>(key);
+    uint32_t last = 0u;
+    int again = 0, chosen = 0;  // how often this lane's last winning key has won; choices of the token
+    for (int j = 0; j < p.k; ++j) {
+      uint32_t m = key[0];
+#pragma unroll
+      for (int d = LPT / 2; d > 0; d >>= 1) m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, d));
+      const bool got = m > KEY_NEG_INF;
+      const unsigned who = __ballot_sync(0xFFFFFFFFu, got && key[0] == m);
+      if (who == 0u) break;  // no token of the warp finds another expert
+      chosen += got ? 1 : 0;
+      if (got && lane == __ffs(who & seg) - 1) {
+        again = m == last ? again + 1 : 0;
+        last = m;
+        picks[first + j] = make_uint2(m, (uint32_t)lane | ((uint32_t)again << 8));
+#pragma unroll
+        for (int i = 0; i + 1 < VL; ++i) key[i] = key[i + 1];
+        key[VL - 1] = 0u;
+      }
+    }
+    __syncwarp();
+    // lane `sub` of the token settles its sub-th choice: the c-th of the source lane's experts with that key
+    int mine = -1;
+    if (sub < chosen) {
+      const uint2 pk = picks[first + sub];
+      const uint32_t* src = keys + (pk.y & 0xFFu) * VL;
+      int c = (int)(pk.y >> 8);
+#pragma unroll
+      for (int i = 0; i < VL; ++i)
+        if (src[i] == pk.x && c-- == 0) mine = (int)((pk.y & (LPT - 1)) * VL) + i;
+    }
+    __syncwarp();  // keys and picks have been read
+    float w = 0.0f;
+    const float xe = mine >= 0 ? load_logit<BF16>(logits, (size_t)t * n + mine) : -INFINITY;
+    if (p.renorm && !sig) {
+      const float m = seg_max(xe);
+      const float ex = mine >= 0 ? expf(xe - m) : 0.0f;
+      const float sum = seg_sum(ex);
+      if (mine >= 0) w = ex / sum;
+    } else {
+      if (mine >= 0) w = sig ? sigmoid(xe) : soft_score(sm, xe);
+      if (p.renorm) w = w / (seg_sum(w) + 1e-20f);
+    }
+    if (t < T && sub < p.k) {
+      idx[(size_t)t * p.k + sub] = mine;
+      prob[(size_t)t * p.k + sub] = w * p.scale;
+      if (load != nullptr && mine >= 0) atomicAdd(&hist[mine], 1);
+    }
+  }
+  if (load != nullptr) {
+    __syncthreads();
+    for (int e = threadIdx.x; e < n; e += blockDim.x) {
+      if (gridDim.x == 1)
+        load[e] = hist[e];
+      else if (hist[e] != 0)
+        atomicAdd(load + e, hist[e]);
+    }
+  }
+}
+
 template <bool BF16>
 __device__ __forceinline__ void store_logit(void* p, size_t i, float v) {
   if (BF16)
@@ -472,11 +603,8 @@ static Grid grid_of(int T, int max_warps, int ctas_per_sm) {
 // Experts per lane: the power of two that covers n / 32; rows are read in
 // vectors where every row starts on a vector's boundary (n a multiple of the
 // lane's experts, aligned bases).
-template <class F>
-static void dispatch(const moe_router_params_t* q, int n, int k, int bf16, const void* a, const void* b,
-                     const float* bias, F&& f) {
-  int vl = 1;
-  while (32 * vl < n) vl *= 2;
+static Params make_params(const moe_router_params_t* q, int n, int k, int vl, int bf16, const void* a, const void* b,
+                          const float* bias) {
   auto fits = [&](int es, uintptr_t bases) {
     const int unit = vl * es < 16 ? vl * es : 16;
     return n % vl == 0 && ((size_t)n * es) % unit == 0 && (bases & (unit - 1)) == 0;
@@ -488,6 +616,14 @@ static void dispatch(const moe_router_params_t* q, int n, int k, int bf16, const
     for (p.seg_log = 0; (1 << p.seg_log) < p.gs / vl;) ++p.seg_log;
   p.vec = fits(bf16 ? 2 : 4, reinterpret_cast<uintptr_t>(a) | reinterpret_cast<uintptr_t>(b));
   p.vec_bias = fits(4, reinterpret_cast<uintptr_t>(bias));
+  return p;
+}
+template <class F>
+static void dispatch(const moe_router_params_t* q, int n, int k, int bf16, const void* a, const void* b,
+                     const float* bias, F&& f) {
+  int vl = 1;
+  while (32 * vl < n) vl *= 2;
+  const Params p = make_params(q, n, k, vl, bf16, a, b, bias);
   auto typed = [&](auto v) {
     if (bf16)
       f(v, std::true_type{}, p);
@@ -522,11 +658,30 @@ extern "C" moe_status_t moe_router_fwd(const void* logits, int logits_bf16, cons
   if ((int64_t)T * k > (int64_t)INT32_MAX / 2) return MOE_ERR_ARG;
   if (T > 0 && (!logits || !topk_idx || !topk_prob)) return MOE_ERR_ARG;
   cudaStream_t st = as_stream(stream);
-  const Grid g = T > 0 ? grid_of(T, n <= 512 ? max_warps<1>() : max_warps<32>(), 2) : Grid{0, 0};
+  // few experts without groups: several tokens per warp (lanes per token and experts per lane by n)
+  const int lpt = n <= 64 ? 8 : 16, small_vl = n <= 32 ? 4 : 8;
+  const bool small = params->n_group == 1 && n <= 128 && k <= lpt;
+  const int units = small ? (T + 32 / lpt - 1) / (32 / lpt) : T;  // warps' worth of work
+  const Grid g = T > 0 ? grid_of(units, n <= 512 ? max_warps<1>() : max_warps<32>(), 2) : Grid{0, 0};
   if (T > 0 && g.ctas <= 0) return MOE_ERR_CUDA;
   if (load && g.ctas != 1 && cudaMemsetAsync(load, 0, (size_t)n * sizeof(int32_t), st) != cudaSuccess)
     return MOE_ERR_CUDA;
   if (T == 0) return MOE_OK;
+  if (small) {
+    const Params p = make_params(params, n, k, small_vl, logits_bf16, logits, nullptr, bias);
+    const size_t smem = (size_t)g.warps * (32 * small_vl + 64) * 4 + (load ? (size_t)n * 4 : 0);
+    auto run = [&](auto kernel) {
+      kernel<<<g.ctas, 32 * g.warps, smem, st>>>(logits, bias, token_mask, T, p, topk_idx, topk_prob, load);
+    };
+    if (n <= 32)
+      logits_bf16 ? run(k_router_small<8, 4, true>) : run(k_router_small<8, 4, false>);
+    else if (n <= 64)
+      logits_bf16 ? run(k_router_small<8, 8, true>) : run(k_router_small<8, 8, false>);
+    else
+      logits_bf16 ? run(k_router_small<16, 8, true>) : run(k_router_small<16, 8, false>);
+    count_launch();
+    return launch_status();
+  }
   dispatch(params, n, k, logits_bf16, logits, nullptr, bias, [&](auto vl, auto bf16, const Params& p) {
     constexpr int VL = decltype(vl)::value;
     const size_t smem = (size_t)g.warps * 32 * VL * 4 + (load ? (size_t)n * 4 : 0);  // at most 36 KB

@@ -243,3 +243,33 @@ def test_refusals():
             ops.router(x, k, prm)
     with pytest.raises(L.MoeError):
         ops.router(torch.zeros(2, 1025, device=DEV), 2, ok)
+
+
+@pytest.mark.parametrize("T,n,k,score,bias,renorm,dt", [
+    (1, 5, 3, "softmax", False, True, "f32"), (3, 32, 8, "sigmoid", True, True, "bf16"),
+    (1001, 8, 2, "softmax", False, False, "f32"), (4100, 61, 7, "softmax", False, False, "f32"),
+    (259, 64, 8, "sigmoid", True, False, "bf16"), (515, 100, 16, "softmax", True, True, "f32"),
+    (130, 128, 9, "sigmoid", False, True, "f32"), (33, 64, 9, "softmax", False, True, "f32"),
+    (70, 33, 8, "softmax", False, True, "bf16"), (2, 24, 8, "sigmoid", True, True, "f32")])
+def test_few_experts(T, n, k, score, bias, renorm, dt):
+    """Sizes at which a token has part of a warp (and one, k = 9 of 64, that
+    does not): rows past T in the last warp, masked tokens beside live ones,
+    rows with fewer live experts than slots, coarse logits with many ties."""
+    rng = np.random.default_rng(T * n)
+    x = np.round(4 * rng.standard_normal((T, n))).astype(np.float32) / 4
+    x[rng.random((T, n)) < 0.1] = NINF
+    x[:: 7, k // 2:] = NINF
+    xt = torch.from_numpy(x).to(torch.bfloat16 if dt == "bf16" else torch.float32)
+    b = (np.round(64 * 0.1 * rng.standard_normal(n)) / 64).astype(np.float32) if bias else None
+    mask = (rng.random(T) > 0.2).astype(np.uint8)
+    prm = L.router_params(score, renorm=renorm, scale=0.5)
+    o = ops.router(xt.to(DEV), k, prm, bias=None if b is None else torch.from_numpy(b).to(DEV),
+                   token_mask=torch.from_numpy(mask).to(DEV))
+    x = np_(xt).astype(np.float64)
+    ref, unsafe = _choose(x, k, score, b, 1, 1, 1, mask)
+    idx = np_(o["idx"])
+    assert unsafe.mean() <= 0.02
+    assert np.array_equal(idx[~unsafe], ref[~unsafe])
+    w = 0.5 * _weights(x, idx, score, renorm)
+    assert np.all(np.abs(np_(o["prob"]) - w) <= 128 * U * w)
+    assert np.array_equal(np_(o["load"]), np.bincount(idx[idx >= 0], minlength=n))
