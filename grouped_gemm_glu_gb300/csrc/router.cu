@@ -36,7 +36,7 @@ namespace router {
 
 constexpr int N_MAX = 1024, K_MAX = 32, G_MAX = 32;
 template <int VL>
-constexpr int max_warps() { return VL < 32 ? 16 : 8; }  // per CTA: registers, and 32 KB of keys
+constexpr int max_warps() { return VL <= 8 ? 32 : VL < 32 ? 16 : 8; }  // per CTA: registers, and 32 KB of keys
 constexpr uint32_t KEY_NEG_INF = 0x007FFFFFu;  // ordered_key(-inf): keys at or below it are not chosen
 
 struct Params {
@@ -155,6 +155,24 @@ __device__ __forceinline__ Soft softmax_of(const float* x) {
   return {m, sum != sum ? sum : fmaxf(sum, 1e-38f)};
 }
 __device__ __forceinline__ float soft_score(const Soft& s, float x) { return expf(x - s.m) / s.d; }
+
+// The counts of this CTA into load (whole CTA).  A lone CTA has every count;
+// otherwise load was cleared by the kernel before this one, which the launch
+// overlaps with this one up to here (programmatic dependent launch).
+__device__ __forceinline__ void flush_load(const int32_t* hist, int n, int32_t* load) {
+  __syncthreads();
+  if (gridDim.x > 1) asm volatile("griddepcontrol.wait;" ::: "memory");
+  for (int e = threadIdx.x; e < n; e += blockDim.x) {
+    if (gridDim.x == 1)
+      load[e] = hist[e];
+    else if (hist[e] != 0)
+      atomicAdd(load + e, hist[e]);  // integers: the order does not matter
+  }
+}
+__global__ void k_router_clear(int32_t* __restrict__ load, int n) {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  for (int e = threadIdx.x; e < n; e += blockDim.x) load[e] = 0;
+}
 
 // Descending order of VL keys (Batcher's odd-even merge sort, unrolled).
 template <int VL>
@@ -333,16 +351,7 @@ __global__ void __launch_bounds__(32 * max_warps<VL>()) k_router_fwd(const void*
       if (load != nullptr && mine >= 0) atomicAdd(&hist[mine], 1);
     }
   }
-  if (load != nullptr) {
-    __syncthreads();
-    // integers: the order does not matter.  A lone CTA has every count.
-    for (int e = threadIdx.x; e < n; e += blockDim.x) {
-      if (gridDim.x == 1)
-        load[e] = hist[e];
-      else if (hist[e] != 0)
-        atomicAdd(load + e, hist[e]);
-    }
-  }
+  if (load != nullptr) flush_load(hist, n, load);
 }
 
 // The same choice for few experts without groups (n <= LPT VL, k <= LPT):
@@ -465,15 +474,7 @@ __global__ void __launch_bounds__(32 * max_warps<VL>()) k_router_small(const voi
       if (load != nullptr && mine >= 0) atomicAdd(&hist[mine], 1);
     }
   }
-  if (load != nullptr) {
-    __syncthreads();
-    for (int e = threadIdx.x; e < n; e += blockDim.x) {
-      if (gridDim.x == 1)
-        load[e] = hist[e];
-      else if (hist[e] != 0)
-        atomicAdd(load + e, hist[e]);
-    }
-  }
+  if (load != nullptr) flush_load(hist, n, load);
 }
 
 template <bool BF16>
@@ -583,10 +584,10 @@ static bool params_ok(const moe_router_params_t* q, int n, int k) {
 }
 
 // CTAs and warps per CTA.  Few tokens fit one CTA, which then holds every
-// count of the load and needs no cleared buffer and no atomics; otherwise the
-// warps spread over two CTAs per SM (`ctas` per SM), as few as fill it: every
-// CTA adds its n counts to the same n addresses, and 2432 small CTAs spent
-// 12 us on that where 304 large ones do not show it (32768 tokens, 64 experts).
+// count of the load and needs no cleared buffer and no atomics; otherwise
+// `ctas_per_sm` CTAs per SM of as many warps as there is work for: every CTA
+// adds its n counts to the same n addresses, and 2432 small CTAs took 12 us
+// longer over that than 304 large ones (32768 tokens, 64 experts).
 struct Grid {
   int ctas, warps;
 };
@@ -662,16 +663,34 @@ extern "C" moe_status_t moe_router_fwd(const void* logits, int logits_bf16, cons
   const int lpt = n <= 64 ? 8 : 16, small_vl = n <= 32 ? 4 : 8;
   const bool small = params->n_group == 1 && n <= 128 && k <= lpt;
   const int units = small ? (T + 32 / lpt - 1) / (32 / lpt) : T;  // warps' worth of work
-  const Grid g = T > 0 ? grid_of(units, n <= 512 ? max_warps<1>() : max_warps<32>(), 2) : Grid{0, 0};
+  const Grid g = T > 0 ? (n <= 256   ? grid_of(units, max_warps<8>(), 1)
+                          : n <= 512 ? grid_of(units, max_warps<16>(), 2)
+                                     : grid_of(units, max_warps<32>(), 2))
+                       : Grid{0, 0};
   if (T > 0 && g.ctas <= 0) return MOE_ERR_CUDA;
-  if (load && g.ctas != 1 && cudaMemsetAsync(load, 0, (size_t)n * sizeof(int32_t), st) != cudaSuccess)
-    return MOE_ERR_CUDA;
-  if (T == 0) return MOE_OK;
+  if (T == 0) {
+    if (load && cudaMemsetAsync(load, 0, (size_t)n * sizeof(int32_t), st) != cudaSuccess) return MOE_ERR_CUDA;
+    return MOE_OK;
+  }
+  const bool clear = load && g.ctas > 1;
+  if (clear) {
+    k_router_clear<<<1, 256, 0, st>>>(load, n);
+    count_launch();
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(g.ctas);
+  cfg.blockDim = dim3(32 * g.warps);
+  cfg.stream = st;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = clear ? 1 : 0;
   if (small) {
     const Params p = make_params(params, n, k, small_vl, logits_bf16, logits, nullptr, bias);
-    const size_t smem = (size_t)g.warps * (32 * small_vl + 64) * 4 + (load ? (size_t)n * 4 : 0);
+    cfg.dynamicSmemBytes = (size_t)g.warps * (32 * small_vl + 64) * 4 + (load ? (size_t)n * 4 : 0);  // < 48 KB
     auto run = [&](auto kernel) {
-      kernel<<<g.ctas, 32 * g.warps, smem, st>>>(logits, bias, token_mask, T, p, topk_idx, topk_prob, load);
+      cudaLaunchKernelEx(&cfg, kernel, logits, bias, token_mask, T, p, topk_idx, topk_prob, load);
     };
     if (n <= 32)
       logits_bf16 ? run(k_router_small<8, 4, true>) : run(k_router_small<8, 4, false>);
@@ -684,9 +703,9 @@ extern "C" moe_status_t moe_router_fwd(const void* logits, int logits_bf16, cons
   }
   dispatch(params, n, k, logits_bf16, logits, nullptr, bias, [&](auto vl, auto bf16, const Params& p) {
     constexpr int VL = decltype(vl)::value;
-    const size_t smem = (size_t)g.warps * 32 * VL * 4 + (load ? (size_t)n * 4 : 0);  // at most 36 KB
-    k_router_fwd<VL, decltype(bf16)::value><<<g.ctas, 32 * g.warps, smem, st>>>(
-        logits, bias, token_mask, T, p, topk_idx, topk_prob, load);
+    cfg.dynamicSmemBytes = (size_t)g.warps * 32 * VL * 4 + (load ? (size_t)n * 4 : 0);  // at most 36 KB
+    cudaLaunchKernelEx(&cfg, k_router_fwd<VL, decltype(bf16)::value>, logits, bias, token_mask, T, p, topk_idx,
+                       topk_prob, load);
   });
   count_launch();
   return launch_status();
