@@ -247,16 +247,18 @@ __global__ void __launch_bounds__(32 * max_warps<VL>()) k_router_fwd(const void*
 #pragma unroll
         for (int i = 0; i < VL; ++i) key[i] = ordered_key(x[i]);
       }
-      // keep the topk_group best groups: lane g, holding the score of group
-      // g, counts the groups that come before it
+      // the topk_group best groups, lane g holding the score of group g
       auto kept_groups = [&](float score) {
-        const uint32_t gk = lane < p.G ? ordered_key(score) : 0u;
-        int before = 0;
-        for (int g = 0; g < p.G; ++g) {
-          const uint32_t o = __shfl_sync(0xFFFFFFFFu, gk, g);
-          before += (o > gk || (o == gk && g < lane)) ? 1 : 0;
+        uint32_t gk = lane < p.G ? max(ordered_key(score), 1u) : 0u;
+        unsigned kept = 0u;
+        for (int r = 0; r < p.keep; ++r) {
+          const uint32_t m = __reduce_max_sync(0xFFFFFFFFu, gk);
+          const unsigned who = __ballot_sync(0xFFFFFFFFu, gk == m);
+          const unsigned best = who & (0u - who);  // the lowest index among equals
+          kept |= best;
+          if ((best >> lane) & 1u) gk = 0u;
         }
-        return __ballot_sync(0xFFFFFFFFu, lane < p.G && before < p.keep);
+        return kept;
       };
       if (p.G > 1 && !runs) {
         float score = -INFINITY;

@@ -697,26 +697,48 @@ def _groups(counts, offsets, E):
     _need(offsets, torch.int32, (E + 1,), "offsets")
 
 
-def fc2_fwd_mxfp4(Aq, As, Wq, Ws, counts, offsets, sm_margin: int = 0, status=None, out=None):
-    """GroupGemm on MXFP8 rows and an MXFP4 weight: y [R_cap, N] bf16 =
+def _outputs(out_mode, R_cap, N, dev, with_col):
+    """Output tensors of a fused epilogue and the moe_act_out_t that names them."""
+    o, ao, new, u8 = {}, L.ActOut(), torch.empty, torch.uint8
+    if out_mode == L.OUT_MXFP8:
+        o["q_row"] = new(R_cap, N, dtype=u8, device=dev)
+        o["s_row"] = new(R_cap, N // 32, dtype=u8, device=dev)
+        if with_col:
+            o["q_col"] = new(N, R_cap, dtype=u8, device=dev)
+            o["s_col"] = new(N, R_cap // 32, dtype=u8, device=dev)
+    else:
+        o["y"] = new(R_cap, N, dtype=torch.bfloat16, device=dev)
+        if out_mode == L.OUT_NVFP4:
+            o["amax"] = torch.empty(1, dtype=torch.float32, device=dev)
+    for k, v in o.items():
+        setattr(ao, k, v.data_ptr())
+    return o, ao
+
+
+def fc2_fwd_mxfp4(Aq, As, Wq, Ws, counts, offsets, sm_margin: int = 0, status=None, out=None,
+                  out_mode: int = L.OUT_BF16, with_col: bool = True):
+    """GroupGemm on MXFP8 rows and an MXFP4 weight: y [R_cap, N] =
     A [R_cap, K] . W[e]^T per expert, A as codes and scales [R_cap, K/32], W
-    [E, N, K] as quantize_mxfp4 writes it."""
+    [E, N, K] as quantize_mxfp4 writes it.  Returns the bf16 tensor y, or (out_mode) the
+    dict of MXFP8 or NVFP4-mode outputs as fc2_fwd does."""
     R_cap, K = _rows_mxfp8(Aq, As, "A")
     E, N = _mxfp4(Wq, Ws, K, "W")
     _groups(counts, offsets, E)
     dev = Aq.device
-    y = torch.empty(R_cap, N, dtype=torch.bfloat16, device=dev) if out is None else _need(
-        out, torch.bfloat16, (R_cap, N), "out")
+    if out is not None:
+        o, ao = {"y": _need(out, torch.bfloat16, (R_cap, N), "out")}, L.ActOut(y=out.data_ptr())
+    else:
+        o, ao = _outputs(out_mode, R_cap, N, dev, with_col)
     st = status if status is not None else new_status(dev)
     a_in = L.InT(L.IN_MXFP8, Aq.data_ptr(), As.data_ptr(), None)
     w_in = L.InT(L.IN_MXFP4, Wq.data_ptr(), Ws.data_ptr(), None)
-    ao = L.ActOut(y=y.data_ptr())
     nbytes = _size("moe_grouped_mxfp4_workspace_size", E, K, R_cap)
     ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
     L.check(L.load().moe_grouped_fc2_fwd(C.byref(a_in), C.byref(w_in), counts.data_ptr(), offsets.data_ptr(), E, K, N,
-                                         R_cap, L.OUT_BF16, C.byref(ao), ws.data_ptr(), nbytes, sm_margin,
+                                         R_cap, out_mode, C.byref(ao), ws.data_ptr(), nbytes, sm_margin,
                                          st.data_ptr(), _cur(Aq)), "moe_grouped_fc2_fwd (MXFP4)")
-    return y
+    o["status"] = st
+    return o["y"] if out_mode == L.OUT_BF16 else o
 
 
 def fc1_fwd_mxfp4(xq, xs, W1q, W1s, counts, offsets, F: int, params: L.GluParams, out_mode: int = L.OUT_MXFP8,
@@ -733,25 +755,14 @@ def fc1_fwd_mxfp4(xq, xs, W1q, W1s, counts, offsets, F: int, params: L.GluParams
         _need(b1p, torch.bfloat16, (E, N1), "b1p")
     if row_scale is not None:
         _need(row_scale, torch.float32, (R_cap,), "row_scale")
-    dev, u8, new = xq.device, torch.uint8, torch.empty
-    o, ao = {}, L.ActOut()
-    if out_mode == L.OUT_MXFP8:
-        o["q_row"] = new(R_cap, F, dtype=u8, device=dev)
-        o["s_row"] = new(R_cap, F // 32, dtype=u8, device=dev)
-        if with_col:
-            o["q_col"] = new(F, R_cap, dtype=u8, device=dev)
-            o["s_col"] = new(F, R_cap // 32, dtype=u8, device=dev)
-    else:
-        o["y"] = new(R_cap, F, dtype=torch.bfloat16, device=dev)
-        if out_mode == L.OUT_NVFP4:
-            o["amax"] = torch.zeros(1, dtype=torch.float32, device=dev)
+    dev = xq.device
+    o, ao = _outputs(out_mode, R_cap, F, dev, with_col)
     if save_pre:
-        o["pre"] = new(R_cap, N1, dtype=torch.bfloat16, device=dev)
+        o["pre"] = torch.empty(R_cap, N1, dtype=torch.bfloat16, device=dev)
+        ao.pre = o["pre"].data_ptr()
     st = status if status is not None else new_status(dev)
     nbytes = _size("moe_grouped_mxfp4_workspace_size", E, H, R_cap)
-    ws = new(nbytes, dtype=u8, device=dev)
-    for k, v in o.items():
-        setattr(ao, k, v.data_ptr())
+    ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
     L.check(L.load().moe_grouped_fc1_glu_quant_fwd_mxfp4(
         xq.data_ptr(), xs.data_ptr(), W1q.data_ptr(), W1s.data_ptr(), _ptr(b1p), _ptr(row_scale), counts.data_ptr(),
         offsets.data_ptr(), E, H, F, R_cap, C.byref(params), out_mode, C.byref(ao), ws.data_ptr(), nbytes, sm_margin,

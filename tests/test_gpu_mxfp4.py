@@ -254,3 +254,68 @@ def test_refusals():
         ops.quantize_mxfp4(torch.zeros(1, 48, 64, dtype=torch.bfloat16, device=DEV))
     with pytest.raises(L.MoeError):  # R_cap % 128
         ops.fc2_fwd_mxfp4(z[:64].contiguous(), s[:64].contiguous(), q4, s4, c, o)
+
+
+@pytest.mark.parametrize("counts,K,N", [([0, 3, 0, 1], 256, 96), ([130, 1, 300], 416, 544), ([40] * 5, 96, 288)])
+def test_product_output_forms(counts, K, N):
+    """MXFP8 outputs are the fp32 accumulator's (as the bf16 output rounds it),
+    row-wise and column-wise; NVFP4 mode is the bf16 output with its amax."""
+    rng = np.random.default_rng(K)
+    xq, xs, cnt, off, xv, cap = _rows(rng, counts, K)
+    q, s, wv = _weight(rng, len(counts), N, K)
+    y = np_(ops.fc2_fwd_mxfp4(xq, xs, q, s, cnt, off))
+    n4 = ops.fc2_fwd_mxfp4(xq, xs, q, s, cnt, off, out_mode=L.OUT_NVFP4)
+    m = ops.fc2_fwd_mxfp4(xq, xs, q, s, cnt, off, out_mode=L.OUT_MXFP8)
+    r = ops.fc2_fwd_mxfp4(xq, xs, q, s, cnt, off, out_mode=L.OUT_MXFP8, with_col=False)
+    o = np_(off)
+    R = int(o[-1])
+    assert np.array_equal(np_(n4["y"])[:R], y[:R])
+    real = np.concatenate([np.arange(o[e], o[e] + c) for e, c in enumerate(counts)])
+    ref = np.zeros((R, N))
+    for e, c in enumerate(counts):
+        ref[o[e]:o[e] + c] = xv[o[e]:o[e] + c] @ wv[e].T
+    # the largest magnitude, within the accumulator's error and (nothing) of rounding
+    a = float(n4["amax"])
+    assert abs(a - np.abs(ref).max()) <= (K / 32 + 8) * 2.0 ** -22 * 8 * np.abs(ref).max()
+    assert torch.equal(m["q_row"][:R], r["q_row"][:R]) and torch.equal(m["s_row"][:R], r["s_row"][:R])
+    for d in (O.mx_dequantize(np_(m["q_row"])[:R], np_(m["s_row"])[:R]),
+              O.mx_dequantize(np_(m["q_col"])[:, :R].copy(), np_(m["s_col"])[:, :R // 32].copy()).T):
+        # a step of E4M3 at a value is 2^-3 of it, and a block's smallest steps are 2^-9 2^-8 of its largest element
+        blk = np.abs(ref).max()
+        assert np.all(np.abs(d - ref)[real] <= 0.13 * np.abs(ref)[real] + 2.0 ** -16 * blk + 0.13 * 2.0 ** -3 * blk * (np.abs(ref)[real] < 2.0 ** -6 * blk))
+        assert np.all(np.delete(d, real, axis=0) == 0)
+
+
+def test_many_experts():
+    """E = 1000 experts with 0 to 3 rows each."""
+    rng = np.random.default_rng(8)
+    counts = rng.integers(0, 4, 1000).tolist()
+    xq, xs, cnt, off, xv, cap = _rows(rng, counts, 64)
+    q, s, wv = _weight(rng, 1000, 32, 64)
+    y, o = np_(ops.fc2_fwd_mxfp4(xq, xs, q, s, cnt, off)), np_(off)
+    for e, c in enumerate(counts):
+        r = slice(o[e], o[e] + c)
+        ref = xv[r] @ wv[e].T
+        lim = 2.0 ** -8 * np.abs(ref) + 10 * 2.0 ** -22 * (np.abs(xv[r]) @ np.abs(wv[e]).T) + 1e-30
+        assert np.all(np.abs(y[r] - ref) <= lim), e
+
+
+def test_past_32_bits():
+    """4.3 billion weights: cast, read-back and product of the last expert."""
+    E, N, K = 66, 8192, 8192
+    w = torch.zeros(E, N, K, dtype=torch.bfloat16, device=DEV)
+    g = torch.Generator(device=DEV).manual_seed(1)
+    w[-1] = torch.randn(N, K, generator=g, device=DEV).to(torch.bfloat16)
+    q, s = ops.quantize_mxfp4(w)
+    q1, s1 = ops.quantize_mxfp4(w[-1:].contiguous())
+    assert torch.equal(q[-1:], q1) and torch.equal(s[-s1.numel():], s1)
+    del w
+    v = ops.dequantize_mxfp4(q, s, K)
+    assert torch.equal(v[-1:], ops.dequantize_mxfp4(q1, s1, K)) and not v[:-1].any()
+    del v
+    rng = np.random.default_rng(0)
+    counts = [0] * (E - 1) + [2]
+    xq, xs, cnt, off, xv, cap = _rows(rng, counts, K)
+    y = ops.fc2_fwd_mxfp4(xq, xs, q, s, cnt, off)
+    one = torch.tensor([2], dtype=torch.int32, device=DEV), torch.tensor([0, 32], dtype=torch.int32, device=DEV)
+    assert torch.equal(y[:32], ops.fc2_fwd_mxfp4(xq, xs, q1, s1, *one)[:32]) and y[:2].any()

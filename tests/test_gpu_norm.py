@@ -184,3 +184,23 @@ def test_refusals():
         ops.rmsnorm(odd, g)
     with pytest.raises(L.MoeError):  # eps < 0
         ops.rmsnorm(x, g, -1.0)
+
+
+def test_past_32_bits():
+    """2.2 billion elements: the last rows are those of a small call."""
+    T, H = 270_000, 8192
+    g = torch.Generator(device=DEV).manual_seed(1)
+    x = torch.zeros(T, H, dtype=torch.bfloat16, device=DEV)
+    x[-300:] = torch.randn(300, H, generator=g, device=DEV).to(torch.bfloat16)
+    gm = torch.ones(H, dtype=torch.bfloat16, device=DEV)
+    o, w = ops.rmsnorm(x, gm, residual=x, mxfp8=True), ops.rmsnorm(x[-300:], gm, residual=x[-300:], mxfp8=True)
+    for k in w:
+        assert torch.equal(o[k][-300:], w[k]), k
+    v = ops.dequantize_mxfp8(o["q"], o["s"])
+    assert torch.equal(v[-300:], ops.dequantize_mxfp8(w["q"], w["s"]))
+    del v
+    dx, dg = ops.rmsnorm_bwd(x, o["h"], gm, o["rstd"])
+    wx, wg = ops.rmsnorm_bwd(x[-300:], w["h"], gm, w["rstd"])
+    assert torch.equal(dx[-300:], wx)
+    # the rows of zeros add nothing; the order of the sums differs
+    assert torch.all((dg - wg).abs() <= 300 * U * (x[-300:].float() * w["h"].float() * w["rstd"][:, None]).abs().sum(0))

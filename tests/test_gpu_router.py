@@ -273,3 +273,18 @@ def test_few_experts(T, n, k, score, bias, renorm, dt):
     w = 0.5 * _weights(x, idx, score, renorm)
     assert np.all(np.abs(np_(o["prob"]) - w) <= 128 * U * w)
     assert np.array_equal(np_(o["load"]), np.bincount(idx[idx >= 0], minlength=n))
+
+
+@pytest.mark.parametrize("n", [64, 512])
+def test_past_32_bits(n):
+    """More than 2^31 logits: the last tokens are those of a small call."""
+    T = (1 << 31) // n + 1000
+    x = torch.full((T, n), -1.0, dtype=torch.bfloat16, device=DEV)
+    g = torch.Generator(device=DEV).manual_seed(1)
+    x[-500:] = torch.randn(500, n, generator=g, device=DEV).to(torch.bfloat16)
+    prm = L.router_params("softmax")
+    o, w = ops.router(x, 3, prm), ops.router(x[-500:].contiguous(), 3, prm)
+    assert torch.equal(o["idx"][-500:], w["idx"]) and torch.equal(o["prob"][-500:], w["prob"])
+    assert int(o["load"].sum()) == 3 * T
+    d = ops.router_bwd(x, o["idx"], o["prob"], prm)
+    assert torch.equal(d[-500:], ops.router_bwd(x[-500:].contiguous(), w["idx"], w["prob"], prm))
