@@ -56,21 +56,26 @@ constexpr int PRODUCER_WARP = 8, MMA_WARP = 9, ROWS_WARP = 10;
 constexpr int THREADS = 11 * 32;
 constexpr int W_TILE = BW * BK;                // unpacked
 constexpr int W_TX = BW * BK / 2;              // bytes the unpacking load counts
+constexpr int KS = 2;                          // k-blocks per stage
 constexpr int SCRATCH = 2048;                  // per epilogue warp
 constexpr int E_MAX = 1024;
 constexpr uint32_t TMEM_COLS = 512;
 
 // NB: 32-row blocks per tile, at most.  7 is what tensor memory takes twice;
-// 2 leaves shared memory for 9 stages instead of 6: where an expert has few
-// rows the weights stream from HBM, and the bytes in flight (8 KB per stage
-// and SM) bound the rate.
+// 2 leaves shared memory for 8 k-blocks instead of 6, for calls whose experts
+// have few rows: there the weights stream from HBM (64 tokens, top-8 of 32
+// experts, 2048 x 7168: 60.5 us with NB = 7, 54.9 with NB = 2).  A stage holds
+// KS = 2 k-blocks, so that a barrier round trip, a commit and the scales' two
+// copies are paid once for both (one per stage: 54.4 us against 51.8 there,
+// and 730 us against 712 for 16384 tokens, top-4, 2880 x 5760, in one run).
 template <int NB>
 struct Lay {
   static constexpr int NT = 32 * NB;  // rows per tile
   static constexpr int XB = NB > 4 ? 2 : 1;                      // 512-byte scale blocks of the rows
-  static constexpr int STAGES = NB > 4 ? 6 : 9;
-  static constexpr int STAGE_BYTES = W_TILE + (NT / 2 * BK + 1023) / 1024 * 1024;
-  static constexpr int SF_STAGE = 512 + 512 * XB;
+  static constexpr int STAGES = NB > 4 ? 3 : 4;
+  static constexpr int X_TILE = (NT / 2 * BK + 1023) / 1024 * 1024;
+  static constexpr int STAGE_BYTES = KS * (W_TILE + X_TILE);     // the k-blocks' weight tiles, then their row tiles
+  static constexpr int SF_STAGE = KS * (512 + 512 * XB);         // likewise their scales
   static constexpr int OFF_SF = STAGES * STAGE_BYTES;
   static constexpr int OFF_SCRATCH = OFF_SF + STAGES * SF_STAGE;
   static constexpr int OFF_PREF = OFF_SCRATCH + EPI_WARPS * SCRATCH;
@@ -80,8 +85,9 @@ struct Lay {
   static constexpr int SMEM_BYTES = 1024 + OFF_MISC + 64;
   static_assert(SMEM_BYTES <= 232448, "shared memory budget");
   static_assert(OFF_BARS % 8 == 0 && OFF_SF % 1024 == 0 && OFF_SCRATCH % 16 == 0, "alignment");
-  static constexpr uint32_t SFW_COL = 2 * NT, SFX_COL = SFW_COL + 4;  // 4 + 4 XB columns of scales
-  static_assert(SFX_COL + 4 * XB <= TMEM_COLS, "tensor memory");
+  // scale columns of tensor memory: 4 of the weight and 4 XB of the rows per k-block of a stage
+  static constexpr uint32_t SFW_COL = 2 * NT, SFX_COL = SFW_COL + 4 * KS;
+  static_assert(SFX_COL + 4 * XB * KS <= TMEM_COLS, "tensor memory");
 };
 
 struct Args {
@@ -485,12 +491,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     for (int t = cl; t < total; t += ncl) {
       const Tile ti = uniform(decode(t, rows, a));
       if (ti.nb == 0) continue;
-      const uint32_t tx = 2u * (W_TX + SF_STAGE) + (uint32_t)ti.nb * 32 * BK;  // both CTAs' bytes
-      const int xrow = ti.row0 + rank * 16 * ti.nb, wrow = ti.n0 + rank * BW;
-      const int ws_row = (ti.e * a.n_tiles + ti.n0 / (2 * BW)) * a.num_kb * 2 + rank, xs_row = ti.mt * a.num_kb * L::XB;
+      const uint32_t tx = 2u * (KS * W_TX + SF_STAGE) + (uint32_t)(KS * ti.nb * 32 * BK);  // both CTAs' bytes
+      const int xrow = ti.row0 + rank * 16 * ti.nb, wrow = ti.e * a.N + ti.n0 + rank * BW;
+      const int ws_blk = (ti.e * a.n_tiles + ti.n0 / (2 * BW)) * a.num_kb, xs_row = ti.mt * a.num_kb * L::XB;
       const int r2 = (ti.nb & 4) * 16, r1 = (ti.nb & 6) * 16;
       bool ok = true;
-      for (int kb = 0; kb < a.num_kb; ++kb) {
+      // (a last stage of fewer k-blocks is filled up with zeros or with blocks that no MMA reads)
+      for (int kb = 0; kb < a.num_kb; kb += KS) {
         if (!__all_sync(0xFFFFFFFFu, mbar_peek(empty + stage, phase ^ 1u)) &&
             !__all_sync(0xFFFFFFFFu, mbar_wait(empty + stage, phase ^ 1u, guard))) {
           ok = false;
@@ -502,15 +509,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         if (elect_one()) {
           if (weight) {
             if (rank == 0) mbar_arrive_expect_tx(full + stage, tx);
-            tma_load_3d_pair(dst, &tmW, bar, kb * BK, wrow, ti.e);
-            tma_load_2d_pair(sd, &tmWs, bar, 0, ws_row + 2 * kb);
+            tma_load_3d_pair(dst, &tmW, bar, 0, wrow, kb);
+            tma_load_3d_pair(sd, &tmWs, bar, 0, rank, ws_blk + kb);
           } else {
             // this CTA's 16 nb rows in boxes of 64, 32 and 16
-            uint8_t* xd = dst + W_TILE;
-            if (NB >= 4 && (ti.nb & 4)) tma_load_2d_pair(xd, &tmX64, bar, kb * BK, xrow);
-            if (ti.nb & 2) tma_load_2d_pair(xd + r2 * BK, &tmX32, bar, kb * BK, xrow + r2);
-            if (ti.nb & 1) tma_load_2d_pair(xd + r1 * BK, &tmX16, bar, kb * BK, xrow + r1);
-            tma_load_2d_pair(sd + 512, &tmXs, bar, 0, xs_row + L::XB * kb);
+#pragma unroll
+            for (int kk = 0; kk < KS; ++kk) {
+              uint8_t* xd = dst + KS * W_TILE + kk * L::X_TILE;
+              const int c = (kb + kk) * BK;
+              if (NB >= 4 && (ti.nb & 4)) tma_load_2d_pair(xd, &tmX64, bar, c, xrow);
+              if (ti.nb & 2) tma_load_2d_pair(xd + r2 * BK, &tmX32, bar, c, xrow + r2);
+              if (ti.nb & 1) tma_load_2d_pair(xd + r1 * BK, &tmX16, bar, c, xrow + r1);
+            }
+            tma_load_2d_pair(sd + KS * 512, &tmXs, bar, 0, xs_row + L::XB * kb);
           }
         }
         __syncwarp();
@@ -545,7 +556,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         const uint32_t d_tmem = tmem_base + (uint32_t)(buf * L::NT);
         bool ok = true;
         uint32_t ready = mbar_peek(full + stage, phase);
-        for (int kb = 0; kb < a.num_kb; ++kb) {
+        for (int kb = 0; kb < a.num_kb; kb += KS) {
           if (!__all_sync(0xFFFFFFFFu, ready) && !__all_sync(0xFFFFFFFFu, mbar_wait(full + stage, phase, guard))) {
             ok = false;
             break;
@@ -553,18 +564,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
           tc_fence_after();
           const uint32_t w_addr = smem_u32(smem) + stage * STAGE_BYTES;
           const uint32_t sf_addr = smem_u32(sf) + stage * SF_STAGE;
-          const uint64_t wd = sdesc_kmajor_sw128(w_addr), xd = sdesc_kmajor_sw128(w_addr + W_TILE);
+          const uint64_t wd = sdesc_kmajor_sw128(w_addr), xd = sdesc_kmajor_sw128(w_addr + KS * W_TILE);
           const uint64_t sd = sdesc_noswizzle(sf_addr, 128);
-          const int nsub = min(4, (a.K - kb * BK) / 32);
+          const int ksub = (a.K - kb * BK) / 32;  // MMAs of K = 32 left
           if (elect_one()) {
-            tc_cp_32x128b_x4_pair(tmem_base + SFW_COL, sd);
-            tc_cp_32x128b_x4_pair(tmem_base + SFX_COL, sd + (512 >> 4));
-            if (NB > 4 && ti.nb > 4) tc_cp_32x128b_x4_pair(tmem_base + SFX_COL + 4, sd + (1024 >> 4));
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-              if (k < nsub)
-                umma_mxf8_pair(d_tmem, wd + 2 * k, xd + 2 * k, idesc_with_sf_ids(idesc, (uint32_t)k, (uint32_t)k),
-                               tmem_base + SFW_COL, tmem_base + SFX_COL, (kb | k) != 0 ? 1u : 0u);
+            for (int kk = 0; kk < KS; ++kk) {
+              tc_cp_32x128b_x4_pair(tmem_base + SFW_COL + 4 * kk, sd + (512 >> 4) * kk);
+              tc_cp_32x128b_x4_pair(tmem_base + SFX_COL + 4 * L::XB * kk, sd + (512 >> 4) * (KS + L::XB * kk));
+              if (NB > 4 && ti.nb > 4)
+                tc_cp_32x128b_x4_pair(tmem_base + SFX_COL + 4 * L::XB * kk + 4, sd + (512 >> 4) * (KS + L::XB * kk + 1));
+            }
+#pragma unroll
+            for (int k = 0; k < 4 * KS; ++k)
+              if (k < ksub)
+                umma_mxf8_pair(d_tmem, wd + (W_TILE >> 4) * (k / 4) + 2 * (k % 4), xd + (L::X_TILE >> 4) * (k / 4) + 2 * (k % 4),
+                               idesc_with_sf_ids(idesc, (uint32_t)(k % 4), (uint32_t)(k % 4)),
+                               tmem_base + SFW_COL + 4 * (k / 4), tmem_base + SFX_COL + 4 * L::XB * (k / 4),
+                               (kb | k) != 0 ? 1u : 0u);
             tc_commit_pair_mc(empty + stage, 0x3);
           }
           __syncwarp();
@@ -684,16 +701,18 @@ moe_status_t grouped_gemm_mxfp4(const uint8_t* xq, const uint8_t* xs, const uint
   const int xb = scale_blocks(E, R_cap);
   if (!work || (reinterpret_cast<uintptr_t>(work) & 255) || work_bytes < grouped_gemm_mxfp4_workspace(E, K, R_cap))
     return MOE_ERR_ARG;
-  if ((long long)E * n_tiles * num_kb * 2 > INT32_MAX || (long long)mt_cap * num_kb * 2 > INT32_MAX ||
+  if ((long long)E * n_tiles * num_kb * 2 > INT32_MAX || (long long)E * N > INT32_MAX - 256 || (long long)mt_cap * num_kb * 2 > INT32_MAX ||
       (long long)mt_cap * n_tiles > INT32_MAX)
     return MOE_ERR_ARG;
   Maps m;
   {
     // the unpacking load wants whole 128-element boxes and 32-byte row pitches
     const uint64_t kp = (uint64_t)(K + BK - 1) / BK * BK;
-    const uint64_t dims[3] = {kp, (uint64_t)N, (uint64_t)E};
-    const uint64_t strides[2] = {kp / 2, (uint64_t)N * (kp / 2)};
-    const uint32_t box[3] = {BK, BW, 1};
+    // as [k-block][row of any expert][128 elements]: rows past an expert's last are the next one's (or zeros),
+    // and no output is stored for them
+    const uint64_t dims[3] = {BK, (uint64_t)E * N, kp / BK};
+    const uint64_t strides[2] = {kp / 2, BK / 2};
+    const uint32_t box[3] = {BK, BW, (uint32_t)KS};
     if (!encode_tmap(&m.w, CU_TENSOR_MAP_DATA_TYPE_16U4_ALIGN16B, 3, wq, dims, strides, box,
                      CU_TENSOR_MAP_SWIZZLE_128B))
       return MOE_ERR_CUDA;
@@ -706,12 +725,16 @@ moe_status_t grouped_gemm_mxfp4(const uint8_t* xq, const uint8_t* xs, const uint
     if (!encode_tmap(xmaps[i], CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, xq, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B))
       return MOE_ERR_CUDA;
   }
-  for (int i = 0; i < 2; ++i) {  // scale blocks as rows of 128 words: one of the weight's, xb of the rows'
-    const uint64_t dims[2] = {128, i == 0 ? (uint64_t)E * n_tiles * num_kb * 2 : (uint64_t)mt_cap * num_kb * xb};
-    const uint64_t strides[1] = {512};
-    const uint32_t box[2] = {128, i == 0 ? 1u : (uint32_t)xb};
-    if (!encode_tmap(i == 0 ? &m.ws : &m.xs, CU_TENSOR_MAP_DATA_TYPE_UINT32, 2, i == 0 ? (const void*)ws : work, dims,
-                     strides, box, CU_TENSOR_MAP_SWIZZLE_NONE))
+  {  // scale blocks as rows of 128 words: the weight's [expert, tile and k-block][half], the rows' in one run
+    const uint64_t dims[3] = {128, 2, (uint64_t)E * n_tiles * num_kb};
+    const uint64_t strides[2] = {512, 1024};
+    const uint32_t box[3] = {128, 1, (uint32_t)KS};
+    if (!encode_tmap(&m.ws, CU_TENSOR_MAP_DATA_TYPE_UINT32, 3, ws, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_NONE))
+      return MOE_ERR_CUDA;
+    const uint64_t xdims[2] = {128, (uint64_t)mt_cap * num_kb * xb};
+    const uint64_t xstrides[1] = {512};
+    const uint32_t xbox[2] = {128, (uint32_t)(xb * KS)};
+    if (!encode_tmap(&m.xs, CU_TENSOR_MAP_DATA_TYPE_UINT32, 2, work, xdims, xstrides, xbox, CU_TENSOR_MAP_SWIZZLE_NONE))
       return MOE_ERR_CUDA;
   }
   Args a{};
