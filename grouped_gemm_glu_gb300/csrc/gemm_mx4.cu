@@ -9,8 +9,10 @@
 // cta_group::2) computes 256 weight rows x N rows: each CTA holds 128 weight
 // rows and half of the N rows in its shared memory, so a 128-wide step of K
 // moves 16 + 16 KB into and out of an SM's shared memory where one CTA on a
-// 128 x 256 tile moves 16 + 32 KB; the shared-memory port (128 bytes a clock),
-// not the tensor core, bounds the latter.
+// 128 x 256 tile moves 16 + 32 KB: at 128 bytes a clock each way more clocks
+// than its MMAs take.  (Cutting the tiles of a call of few tiles along K as
+// well, with partial sums joined by the last part to arrive, made one token's
+// 16 us 31: a part's store, fence and count take longer than its share of K.)
 //
 // Weights cross HBM and L2 as 4 bits: the TMA unpacks every 16 elements into
 // 16 bytes of shared memory (8 of codes, 8 unused), the form in which this MMA
@@ -23,11 +25,11 @@
 //
 // Two launches: k_mx4_scales gathers the rows' scales of every row tile into
 // the order tcgen05.cp consumes (byte 16 l + 4 j + i of 512 = row 32 j + l,
-// k sub-block i; [row tile][k-block][2][512]), k_grouped_mx4 multiplies.  The
+// k sub-block i; [row tile][k-block][XB][512]), k_grouped_mx4 multiplies.  The
 // second is launched as a programmatic dependent of the first: its prologue
-// runs meanwhile, and only its producer waits.  (Gathering inside the second
-// kernel, by a warp that wrote the stage's scales itself, took 1 to 2 us per
-// k-block: four times the MMAs.)
+// runs meanwhile, and only its rows' producer waits (one token 19.1 -> 16.9
+// us).  Gathering inside the second kernel, by a warp that wrote each stage's
+// scales itself, was several times slower.
 //
 // Warps (11 per CTA, one CTA per SM, persistent over the tiles):
 //   0-7  epilogue: warp (q, h) takes the 32 weight rows of lane quarter q and
@@ -35,10 +37,10 @@
 //        32 rows.  GLU: quarters 2i / 2i + 1 hold the input / gate halves of
 //        one packed block of 64, the gate warp hands its values over through
 //        shared memory
-//   8    TMA producer of the weight: tile and scales of each k-block
-//   10   TMA producer of the rows (two issuers, because four to six copies a
-//        k-block from one thread took longer than the MMAs); all copies of
-//        both CTAs complete on the even CTA's stage barrier
+//   8    TMA producer of the weight: tiles and scales of each stage
+//   10   TMA producer of the rows: likewise (two issuing warps: the 64-token
+//        batch below 61.5 -> 60.5 us); all copies of both CTAs complete on
+//        the even CTA's stage barrier
 //   9    tensor-memory owner; in the even CTA the MMA issuer: scales into
 //        tensor memory (tcgen05.cp), then 4 MMAs of K = 32
 // Every wait is bounded (MOE_ERR_TIMEOUT + early exit, never a trap).
@@ -245,6 +247,16 @@ __device__ __forceinline__ void launch_dependents() { asm volatile("griddepcontr
 __device__ __forceinline__ void wait_for_primary() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 __device__ __forceinline__ void warp_pair_sync(int id) { asm volatile("bar.sync %0, 64;" ::"r"(id) : "memory"); }
+
+// Whether ok holds in both warps of a pair (which both call this).
+__device__ __forceinline__ int both_warps(int ok, int id) {
+  int r;
+  asm volatile("{\n .reg .pred p, q;\n setp.ne.s32 p, %1, 0;\n bar.red.and.pred q, %2, 64, p;\n selp.s32 %0, 1, 0, q;\n}\n"
+               : "=r"(r)
+               : "r"(ok), "r"(id)
+               : "memory");
+  return r;
+}
 
 template <int EPI>
 __device__ __forceinline__ float activate(const GluParams& p, float u, float g) {
@@ -614,7 +626,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       ++lt;
       int ok = 1;
       if (lane == 0) ok = mbar_wait(acc_full + buf, aph, guard) ? 1 : 0;
-      if (!__shfl_sync(0xFFFFFFFFu, ok, 0)) break;
+      ok = __shfl_sync(0xFFFFFFFFu, ok, 0);
+      // the two warps that share a block meet at barriers below: both go on or neither does
+      if (EPI >= GLU && EPI <= GLU_L3) ok = both_warps(ok, 1 + h * 2 + (q >> 1));
+      if (!ok) break;
       tc_fence_after();
       epilogue<EPI>(a, ti, tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(buf * L::NT), q, h, lane, rank,
                     scratch_all + (warp & ~1) * SCRATCH, amax_bits);
