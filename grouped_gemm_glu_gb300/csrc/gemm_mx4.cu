@@ -148,36 +148,43 @@ struct Rows {
   int32_t *pref, *cnt, *off;
 };
 
-// Row tile m of expert e, which has mt of them.
+// Row tile m of expert e, which has mt of them: the first blocks % mt tiles
+// have one block more than the others.
 __device__ __forceinline__ void row_tile(const Args& a, const Rows& r, int e, int m, int mt, Tile& ti) {
   const int cnt = r.cnt[e], off = r.off[e];
-  const int blocks = row_blocks(cnt);
-  const int b0 = (int)((long long)m * blocks / mt), b1 = (int)((long long)(m + 1) * blocks / mt);
+  const unsigned blocks = (unsigned)row_blocks(cnt), base = blocks / (unsigned)mt, more = blocks - base * (unsigned)mt;
+  const int b0 = (int)((unsigned)m * base + min((unsigned)m, more));
+  const int nb = (int)base + ((unsigned)m < more ? 1 : 0);
   ti.e = e;
   ti.row0 = off + 32 * b0;
   // (offsets and counts are device data: a tile never reaches past the buffers)
-  ti.nb = off < 0 ? 0 : max(0, min(b1 - b0, (a.R_cap - ti.row0) / 32));
+  ti.nb = off < 0 ? 0 : max(0, min(nb, (a.R_cap - ti.row0) / 32));
   ti.valid = min(cnt - 32 * b0, 32 * ti.nb);
 }
 
-__device__ __forceinline__ int find_expert(const int32_t* pref, int E, int x, int mul) {
+__device__ __forceinline__ int find_expert(const int32_t* pref, int E, int x) {
   int lo = 0, hi = E - 1;
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
-    if (pref[mid] * mul <= x) lo = mid; else hi = mid - 1;
+    if (pref[mid] <= x) lo = mid; else hi = mid - 1;
   }
   return lo;
 }
 
-__device__ __forceinline__ Tile decode(int t, const Rows& r, const Args& a) {
-  const int e = find_expert(r.pref, a.E, t, a.n_tiles);
-  const int mt = r.pref[e + 1] - r.pref[e];
-  const int local = t - r.pref[e] * a.n_tiles;
-  const int n = local / mt, m = local - n * mt;  // row tiles of one weight tile follow each other (the weight stays in L2)
+// Tile t of the sequence; e: the expert of a tile before it (every role goes
+// through its tiles in order).  A search from scratch and 64-bit divisions
+// took each role 2000 to 3000 cycles per tile, a quarter of a tile's time at
+// K = 2880.
+__device__ __forceinline__ Tile decode(int t, int& e, const Rows& r, const Args& a) {
+  while (e + 1 < a.E && r.pref[e + 1] * a.n_tiles <= t) ++e;
+  const int first = r.pref[e], mt = r.pref[e + 1] - first;
+  const int local = t - first * a.n_tiles;
+  // row tiles of one weight tile follow each other (the weight stays in L2)
+  const int n = mt == 1 ? local : (int)((unsigned)local / (unsigned)mt), m = local - n * mt;
   Tile ti;
   row_tile(a, r, e, m, mt, ti);
   ti.n0 = n * 2 * BW;
-  ti.mt = r.pref[e] + m;
+  ti.mt = first + m;
   if (ti.mt >= a.mt_cap) ti.nb = 0;  // (only with counts that exceed the buffers)
   return ti;
 }
@@ -441,7 +448,7 @@ __global__ void __launch_bounds__(256) k_mx4_scales(const Args a) {
   const int items = min(r.pref[a.E], a.mt_cap) * a.num_kb;
   for (int it = blockIdx.x * warps + (threadIdx.x >> 5); it < items; it += gridDim.x * warps) {
     const int mt = it / a.num_kb, kb = it - mt * a.num_kb;
-    const int e = find_expert(r.pref, a.E, mt, 1);
+    const int e = find_expert(r.pref, a.E, mt);
     Tile ti;
     row_tile(a, r, e, mt - r.pref[e], r.pref[e + 1] - r.pref[e], ti);
     uint32_t v[4 * XB];
@@ -524,12 +531,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
   // instruction, 1000 per k-block, measured with the clock).
   if (warp == PRODUCER_WARP || warp == ROWS_WARP) {
     const bool weight = warp == PRODUCER_WARP;
-    int stage = 0;
+    int stage = 0, e = 0;
     uint32_t phase = 0, issued = 0, issued_parity = 0;
     const uint32_t full0 = mapa_shared(smem_u32(full), 0);
     if (!weight) wait_for_primary();  // the tiled scales of the rows (in every CTA: the grid ends after its primary)
     for (int t = cl; t < total; t += ncl) {
-      const Tile ti = uniform(decode(t, rows, a));
+      const Tile ti = uniform(decode(t, e, rows, a));
       if (ti.nb == 0) continue;
       const uint32_t tx = 2u * (KS * W_TX + SF_STAGE) + (uint32_t)(KS * ti.nb * 32 * BK);  // both CTAs' bytes
       const int xrow = ti.row0 + rank * 16 * ti.nb, wrow = ti.e * a.N + ti.n0 + rank * BW;
@@ -582,10 +589,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     }
   } else if (warp == MMA_WARP) {
     if (rank == 0) {
-      int stage = 0, lt = 0;
+      int stage = 0, lt = 0, e = 0;
       uint32_t phase = 0;
       for (int t = cl; t < total; t += ncl) {
-        const Tile ti = uniform(decode(t, rows, a));
+        const Tile ti = uniform(decode(t, e, rows, a));
         if (ti.nb == 0) continue;
         const int buf = lt & 1;
         const uint32_t aph = (uint32_t)(lt >> 1) & 1u;
@@ -645,9 +652,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
   } else {
     const int q = warp & 3, h = warp >> 2;
     Amax amax_bits{0u, 0u};
-    int lt = 0;
+    int lt = 0, e = 0;
     for (int t = cl; t < total; t += ncl) {
-      const Tile ti = decode(t, rows, a);
+      const Tile ti = decode(t, e, rows, a);
       if (ti.nb == 0) continue;
       const int buf = lt & 1;
       const uint32_t aph = (uint32_t)(lt >> 1) & 1u;
