@@ -105,7 +105,7 @@ struct Args {
   const float* row_scale;  // [R_cap] or null
   uint16_t* pre_out;       // [R_cap][N] bf16 or null
   GluParams prm;
-  // outputs (emit_block_t)
+  // outputs
   int out_mode, out_N;
   uint8_t* q_row;
   uint8_t* s_row;
@@ -113,8 +113,6 @@ struct Args {
   uint8_t* s_col;
   uint16_t* y;
   float* amax;
-  float* rht_amax;  // null: the rotated amax belongs to the backward
-  uint32_t rht_signs;
 };
 
 enum Epi { PLAIN = 0, GLU = 1, GLU_L1 = 2, GLU_L2 = 3, GLU_L3 = 4, ELT = 5 };
@@ -273,35 +271,69 @@ __device__ __forceinline__ float activate(const GluParams& p, float u, float g) 
   return act_fwd(p, u, g);
 }
 
-// Rows r0 .. r0 + R - 1 (R = 16 or 32) of one output column per lane (a warp:
-// 32 neighbouring columns, `col` the first) as bf16, bf16 plus amax, or MXFP8
-// rows.  The block is turned over in the warp's 64 R bytes of shared memory,
-// so that it leaves in 16-byte stores: 2-byte stores, 32 per 32 x 32 block,
-// held outputs with a short K at 2.4 TB/s (11957 tokens, top-4, 224 x 4032:
-// 159 us).  The caller's reads of `stage` are complete.
+// 16 values of a block on its scale, as E4M3 codes.
+__device__ __forceinline__ uint4 codes16(const float* v, uint32_t sb) {
+  const float inv = mx_inv_scale(sb);
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    w[i] = sb == 0xFFu ? 0x7F7F7F7Fu
+                       : e4m3x2(v[4 * i] * inv, v[4 * i + 1] * inv) |
+                             (e4m3x2(v[4 * i + 2] * inv, v[4 * i + 3] * inv) << 16);
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+template <int R>
+__device__ __forceinline__ uint32_t amax_bits_of(const float* v) {
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < R; ++i) m = max(m, abs_bits(v[i]));
+  return m;
+}
+
+// 16 rows from r0 of one output column per lane (a warp: 32 neighbouring
+// columns, one scale per row, `col` the first) as MXFP8 rows, turned over in
+// the warp's 2 KB of shared memory: afterwards a lane has half a row, so a
+// row's amax is 16 maxima and one shuffle and its scale is found once (11957
+// tokens, top-4, 224 x 4032: 186 us with a warp-wide reduction and the scale
+// found in every lane, row by row, 151 like this).
+// (A row's 16-byte chunks are permuted by its number: no bank conflicts.)
+__device__ __forceinline__ void emit_mx_rows16(const Args& a, const float* o, int col, int r0, int lane,
+                                               uint8_t* stage) {
+  const size_t N = (size_t)a.out_N;
+  __syncwarp();
+#pragma unroll
+  for (int j = 0; j < 16; ++j)
+    reinterpret_cast<float*>(stage)[j * 32 + (((lane >> 2) ^ (j & 7)) << 2) + (lane & 3)] = o[j];
+  __syncwarp();
+  const int row = lane >> 1, half = lane & 1;
+  float v[16];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float4 x = reinterpret_cast<const float4*>(stage)[row * 8 + ((4 * half + i) ^ (row & 7))];
+    v[4 * i] = x.x, v[4 * i + 1] = x.y, v[4 * i + 2] = x.z, v[4 * i + 3] = x.w;
+  }
+  uint32_t m = amax_bits_of<16>(v);
+  m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
+  const uint32_t sb = e8m0_from_amax_bits(m);
+  *reinterpret_cast<uint4*>(a.q_row + (size_t)(r0 + row) * N + col + 16 * half) = codes16(v, sb);
+  if (half == 0) a.s_row[(size_t)(r0 + row) * (N / 32) + col / 32] = (uint8_t)sb;
+}
+
+// Rows r0 .. r0 + R - 1 (R = 16 or 32) of one output column per lane as bf16,
+// bf16 plus amax, or MXFP8 rows.  The block is turned over in the warp's 2 KB
+// of shared memory, so that it leaves in 16-byte stores (gated 4160 x 960,
+// 12283 tokens, bf16: 217 us with 2-byte stores, 211 like this; without a gate
+// both take 102 us at 4032 x 224).  The caller's reads of `stage` are complete.
 template <int R>
 __device__ __forceinline__ void emit_rows(const Args& a, const float* o, int col, int r0, int lane, uint8_t* stage,
                                           Amax& amax_bits) {
   const size_t N = (size_t)a.out_N;
-  __syncwarp();
   if (a.out_mode == MOE_OUT_MXFP8) {
-    uint32_t mine = 0;  // lane j: the scale of row j
 #pragma unroll
-    for (int j = 0; j < R; ++j) {
-      const uint32_t sb = e8m0_from_amax_bits(__reduce_max_sync(0xFFFFFFFFu, abs_bits(o[j])));
-      stage[j * 32 + lane] = (uint8_t)(sb == 0xFFu ? 0x7Fu : e4m3x2(o[j] * mx_inv_scale(sb), 0.0f) & 0xFFu);
-      if (lane == j) mine = sb;
-    }
-    __syncwarp();
-#pragma unroll
-    for (int i = 0; i < R / 16; ++i) {
-      const int c = lane + 32 * i;  // 16-byte chunk c: row c / 2
-      *reinterpret_cast<uint4*>(a.q_row + (size_t)(r0 + c / 2) * N + col + 16 * (c & 1)) =
-          reinterpret_cast<const uint4*>(stage)[c];
-    }
-    if (lane < R) a.s_row[(size_t)(r0 + lane) * (N / 32) + col / 32] = (uint8_t)mine;
+    for (int i = 0; i < R / 16; ++i) emit_mx_rows16(a, o + 16 * i, col, r0 + 16 * i, lane, stage);
     return;
   }
+  __syncwarp();
   // words of two rows of a column: [row pair][32 columns]
   uint32_t* w = reinterpret_cast<uint32_t*>(stage);
 #pragma unroll
@@ -325,6 +357,19 @@ __device__ __forceinline__ void emit_rows(const Args& a, const float* o, int col
   }
 }
 
+// R rows from r0 of the lane's output column c as (part of) one 32-row block
+// of the column-wise MXFP8 copy, whose amax is m.  (The two warps of a gated
+// block quantise their own 16 rows; with the input warp doing all 32 rows,
+// 16384 tokens, top-4, 2880 x 5760 took 1457 us with both copies, 800 like this.)
+template <int R>
+__device__ __forceinline__ void emit_col(const Args& a, const float* o, int c, int r0, uint32_t m) {
+  const uint32_t sb = e8m0_from_amax_bits(m);
+  uint4* dst = reinterpret_cast<uint4*>(a.q_col + (size_t)c * a.R_cap + r0);
+#pragma unroll
+  for (int i = 0; i < R / 16; ++i) dst[i] = codes16(o + 16 * i, sb);
+  if (r0 % 32 == 0) a.s_col[(size_t)c * (a.R_cap / 32) + r0 / 32] = (uint8_t)sb;
+}
+
 // Hands an accumulator back to the MMA issuer (a barrier's cluster address).
 // Relaxed: what has to come first is this warp's reads of tensor memory, which
 // tcgen05.wait::ld and the fence order; a release would wait for the warp's
@@ -339,8 +384,6 @@ __device__ __forceinline__ void release_accumulator(uint32_t bar, int lane) {
 // column j is row row0 + j.  GLU: lane quarters 2i and 2i + 1 hold the input
 // and the gate half of one packed block of 64; the two warps swap halves
 // through 4 KB of shared memory, so that each computes 16 of the 32 rows.
-// (The column-wise MXFP8 copy needs a column's 32 rows in one thread: with it
-// the input warp takes the gate warp's rows as well.)
 template <int EPI>
 __device__ __forceinline__ void epilogue(const Args& a, const Tile& ti, uint32_t tacc, int q, int h, int lane, int rank,
                                          uint8_t* scratch, Amax& amax_bits) {
@@ -369,52 +412,37 @@ __device__ __forceinline__ void epilogue(const Args& a, const Tile& ti, uint32_t
     if (GATED) {
       float* xs = reinterpret_cast<float*>(scratch);  // [2][16 rows][32 lanes]: to the gate warp, to the input warp
       const bool gate_warp = (q & 1) != 0;
-      const bool both = a.q_col != nullptr && a.out_mode == MOE_OUT_MXFP8;
       const int id = 1 + h * 2 + (q >> 1), f = (colbase / 64) * 32;
-      float x[32];
       warp_pair_sync(id);  // both warps have read what was there
-      if (gate_warp) {
 #pragma unroll
-        for (int j = 0; j < 16; ++j) xs[(16 + j) * 32 + lane] = v[j];
-        if (both) {
-#pragma unroll
-          for (int j = 0; j < 16; ++j) xs[j * 32 + lane] = v[16 + j];
-        }
-      } else if (!both) {
-#pragma unroll
-        for (int j = 0; j < 16; ++j) xs[j * 32 + lane] = v[16 + j];
-      }
+      for (int j = 0; j < 16; ++j) xs[((gate_warp ? 16 : 0) + j) * 32 + lane] = v[gate_warp ? j : 16 + j];
       warp_pair_sync(id);
-      if (!both) {
-        float o[16];
-        const int r0 = rb + (gate_warp ? 16 : 0), live = nvalid - (gate_warp ? 16 : 0);
+      float o[16];
+      const int r0 = rb + (gate_warp ? 16 : 0), live = nvalid - (gate_warp ? 16 : 0);
 #pragma unroll
-        for (int j = 0; j < 16; ++j) {
-          const float m = xs[((gate_warp ? 0 : 16) + j) * 32 + lane];
-          o[j] = activate<EPI>(a.prm, gate_warp ? m : v[j], gate_warp ? v[16 + j] : m);
-        }
-        if (a.row_scale != nullptr) {
-#pragma unroll
-          for (int j = 0; j < 16; ++j)
-            if (j < live) o[j] *= __ldg(a.row_scale + r0 + j);
-        }
-        if (live < 16) {
-#pragma unroll
-          for (int j = 0; j < 16; ++j) o[j] = j < live ? o[j] : 0.0f;
-        }
-        // (each warp turns its rows over in the half of the scratch that it has read)
-        emit_rows<16>(a, o, f, r0, lane, scratch + (gate_warp ? 0 : 2048), amax_bits);
-        continue;
+      for (int j = 0; j < 16; ++j) {
+        const float m = xs[((gate_warp ? 0 : 16) + j) * 32 + lane];
+        o[j] = activate<EPI>(a.prm, gate_warp ? m : v[j], gate_warp ? v[16 + j] : m);
       }
-      if (gate_warp) continue;
+      if (a.row_scale != nullptr) {
 #pragma unroll
-      for (int j = 0; j < 32; ++j) x[j] = xs[(j < 16 ? 16 + j : j - 16) * 32 + lane];
-#pragma unroll
-      for (int j = 0; j < 32; ++j) {
-        const float rs = (a.row_scale != nullptr && j < nvalid) ? __ldg(a.row_scale + rb + j) : 1.0f;
-        v[j] = j < nvalid ? activate<EPI>(a.prm, v[j], x[j]) * rs : 0.0f;
+        for (int j = 0; j < 16; ++j)
+          if (j < live) o[j] *= __ldg(a.row_scale + r0 + j);
       }
-      emit_block_t(a, v, f + lane, rb, lane, amax_bits);
+      if (live < 16) {
+#pragma unroll
+        for (int j = 0; j < 16; ++j) o[j] = j < live ? o[j] : 0.0f;
+      }
+      // (each warp turns its rows over in the half of the scratch that it has read)
+      uint8_t* mine = scratch + (gate_warp ? 0 : 2048);
+      emit_rows<16>(a, o, f, r0, lane, mine, amax_bits);
+      if (a.q_col != nullptr && a.out_mode == MOE_OUT_MXFP8) {  // the column's other 16 rows are with the other warp
+        const uint32_t m = amax_bits_of<16>(o);
+        __syncwarp();
+        reinterpret_cast<uint32_t*>(mine)[lane] = m;
+        warp_pair_sync(id);
+        emit_col<16>(a, o, f + lane, r0, max(m, reinterpret_cast<const uint32_t*>(scratch + (gate_warp ? 2048 : 0))[lane]));
+      }
     } else {
       if (EPI == ELT) {
 #pragma unroll
@@ -423,11 +451,8 @@ __device__ __forceinline__ void epilogue(const Args& a, const Tile& ti, uint32_t
           v[j] = j < nvalid ? act_fwd(a.prm, v[j], 0.0f) * rs : 0.0f;
         }
       }
-      if (a.q_col != nullptr && a.out_mode == MOE_OUT_MXFP8) {
-        emit_block_t(a, v, col, rb, lane, amax_bits);
-      } else {
-        emit_rows<32>(a, v, colbase, rb, lane, scratch + (q & 1) * SCRATCH, amax_bits);
-      }
+      emit_rows<32>(a, v, colbase, rb, lane, scratch + (q & 1) * SCRATCH, amax_bits);
+      if (a.q_col != nullptr && a.out_mode == MOE_OUT_MXFP8) emit_col<32>(a, v, col, rb, amax_bits_of<32>(v));
     }
   }
 }
