@@ -40,7 +40,7 @@ constexpr int MAX_H = 16384;  // 16 warps x 4 vectors of 8 columns a lane
 template <int V>
 constexpr int max_threads() { return V == 1 ? 1024 : 512; }
 constexpr int MAX_T = 1 << 30;  // row indexes stay in 32 bits a few grids past the end
-constexpr int FEW_ROWS = 256;
+constexpr int FEW_ROWS = 512, FEW_WARPS = 152 * 32;  // of a call of few rows, at most
 constexpr int RING_BYTES = 200 * 1024;  // of the 227 KB a CTA may have
 
 // Eight bf16 values as four float pairs (the packed fp32 instructions of
@@ -430,12 +430,18 @@ __global__ void __launch_bounds__(256) k_dequant_mxfp8(const uint2* __restrict__
 
 // How the rows are laid over the GPU (see the head of the file).
 struct Split {
+  bool few;
   int V, wpr, groups, threads;
 };
 static Split split(int H8, int T) {
   const int lanes = (H8 + 31) / 32;  // warps needed at one vector per thread (<= 64)
   Split p{};
-  const bool few = T <= FEW_ROWS;
+  // Few rows: what runs in one wave.  Two warps' columns of H = 512: 2.3 us
+  // against 2.6 at 512 rows (forward), 3.6 against 2.7 at 1024; 2880: 4.0
+  // against 4.4 at 320 rows, 4.9 against 4.4 at 512; 7168: 3.6 against 4.4 at
+  // 128 rows, 6.1 against 4.4 at 256.  (The backward's crossings are the same.)
+  const bool few = T <= FEW_ROWS && T * (lanes < 32 ? lanes : 32) <= FEW_WARPS;
+  p.few = few;
   // four vectors of each input per thread where the row is wide enough for two warps of them
   p.V = few ? (lanes > 32 ? 4 : 1) : lanes >= 8 ? 4 : lanes >= 4 ? 2 : 1;
   p.wpr = (lanes + p.V - 1) / p.V;
@@ -445,8 +451,8 @@ static Split split(int H8, int T) {
   return p;
 }
 static int ring_stage(const Split& p, int inputs) { return inputs * p.V * p.threads * 16; }
-static int ring_stages(const Split& p, int inputs, int T) {
-  if (T <= FEW_ROWS) return 1;
+static int ring_stages(const Split& p, int inputs) {
+  if (p.few) return 1;
   const int n = RING_BYTES / ring_stage(p, inputs);
   return n < 1 ? 1 : n > 4 ? 4 : n;
 }
@@ -454,7 +460,7 @@ static int ring_stages(const Split& p, int inputs, int T) {
 constexpr int SM_BOUND = 256;  // workspace bound: one CTA per SM of the largest device
 static int ctas(int T, int sms, const Split& p) {
   const int need = (T + p.groups - 1) / p.groups;
-  const int most = T <= FEW_ROWS ? FEW_ROWS : sms < SM_BOUND ? sms : SM_BOUND;
+  const int most = p.few ? FEW_ROWS : sms < SM_BOUND ? sms : SM_BOUND;
   return need < most ? need : most;
 }
 
@@ -480,7 +486,7 @@ extern "C" moe_status_t moe_rmsnorm_fwd(const moe_bf16* x, const moe_bf16* resid
   if (sms <= 0) return MOE_ERR_CUDA;
   const int H8 = H / 8, inputs = residual ? 2 : 1;
   const Split p = split(H8, T);
-  const int stages = ring_stages(p, inputs, T), smem = stages * ring_stage(p, inputs);
+  const int stages = ring_stages(p, inputs), smem = stages * ring_stage(p, inputs);
   auto run = [&](auto kernel) {
     if (!set_smem_limit((const void*)kernel, RING_BYTES)) return MOE_ERR_CUDA;
     kernel<<<ctas(T, sms, p), p.threads, smem, as_stream(stream)>>>(
@@ -521,7 +527,7 @@ extern "C" moe_status_t moe_rmsnorm_bwd(const moe_bf16* dy, const moe_bf16* dres
   const int H8 = H / 8, inputs = dres ? 3 : 2;
   const Split p = split(H8, T);
   const int grid = ctas(T, sms, p);
-  const int stages = ring_stages(p, inputs, T), smem = stages * ring_stage(p, inputs);
+  const int stages = ring_stages(p, inputs), smem = stages * ring_stage(p, inputs);
   float* part = dgamma ? static_cast<float*>(ws) : nullptr;
   auto run = [&](auto kernel) {
     if (!set_smem_limit((const void*)kernel, RING_BYTES)) return MOE_ERR_CUDA;
