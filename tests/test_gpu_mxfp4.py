@@ -319,3 +319,50 @@ def test_past_32_bits():
     y = ops.fc2_fwd_mxfp4(xq, xs, q, s, cnt, off)
     one = torch.tensor([2], dtype=torch.int32, device=DEV), torch.tensor([0, 32], dtype=torch.int32, device=DEV)
     assert torch.equal(y[:32], ops.fc2_fwd_mxfp4(xq, xs, q1, s1, *one)[:32]) and y[:2].any()
+
+
+@pytest.mark.parametrize("counts,K,F", [([1], 32, 32), ([5, 33, 0, 64], 160, 160), ([130, 1, 300], 416, 544),
+                                        ([700, 0, 450], 96, 96)])
+@pytest.mark.parametrize("act", ["gptoss", "swiglu", "geglu", "srelu"])
+def test_up_projection_column_copy(counts, K, F, act):
+    """The column-wise MXFP8 copy of the activation's output: blocks of 32 rows
+    of one column, the padding rows zeros.  Its values and the row-wise copy's
+    come from one fp32 value v that is within lim of the formula's (fp32 sums of
+    exact products, as for the product itself; the activation's slope is below
+    4 (1 + max |z|) in its pre-activations); E4M3 steps are at most 2^-3 of a
+    block's largest element, half a step of rounding and at most one of
+    saturation (448 to 512) below 0.13 of it."""
+    rng = np.random.default_rng(K + F + 1)
+    E, gated = len(counts), act != "srelu"
+    N = 2 * F if gated else F
+    prm = L.glu_params("swiglu", alpha=1.702, up_offset=1.0, gate_lo=-7.0, gate_hi=7.0) if act == "gptoss" else \
+        L.glu_params(act)
+    op = {"gptoss": O.ActParams(O.ACT_SWIGLU, alpha=1.702, up_offset=1.0, gate_lo=-7.0, gate_hi=7.0),
+          "swiglu": O.ActParams(O.ACT_SWIGLU), "geglu": O.ActParams(O.ACT_GEGLU), "srelu": O.ActParams(O.ACT_SRELU)}[act]
+    xq, xs, cnt, off, xv, cap = _rows(rng, counts, K)
+    q, s, wv = _weight(rng, E, N, K)
+    m = ops.fc1_fwd_mxfp4(xq, xs, q, s, cnt, off, F, prm, out_mode=L.OUT_MXFP8, save_pre=False)
+    r = ops.fc1_fwd_mxfp4(xq, xs, q, s, cnt, off, F, prm, out_mode=L.OUT_MXFP8, save_pre=False, with_col=False)
+    assert ops.read_status(m["status"]) == 0
+    of = np_(off)
+    end = int(of[-1])
+    assert torch.equal(m["q_row"][:end], r["q_row"][:end]) and torch.equal(m["s_row"][:end], r["s_row"][:end])
+    col = O.mx_dequantize(np_(m["q_col"])[:, :end].copy(), np_(m["s_col"])[:, :end // 32].copy()).T
+    for e, c in enumerate(counts):
+        if not c:
+            continue
+        rows = slice(of[e], of[e] + c)
+        z = xv[rows] @ wv[e].T
+        mag = np.abs(xv[rows]) @ np.abs(wv[e]).T + np.abs(z)
+        if gated:
+            ref, slack = O.act_fwd(*O.unpack_glu_cols(z), op), np.maximum(*O.unpack_glu_cols(mag))
+        else:
+            ref, slack = O.act_fwd(z, None, op), mag
+        lim = 2.0 ** -18 * np.abs(ref) + 16 * (K / 32 + 8) * 2.0 ** -22 * slack * (1 + np.abs(z).max()) + 1e-30
+        pad = int(of[e + 1] - of[e]) - c
+        full = np.pad(ref, ((0, pad), (0, 0)))
+        lim = np.pad(lim, ((0, pad), (0, 0)))
+        blk = np.abs(full).reshape(-1, 32, F).max(1, keepdims=True)
+        d = col[of[e]:of[e + 1]]
+        assert np.all(np.abs(d - full).reshape(-1, 32, F) <= 0.13 * blk + lim.reshape(-1, 32, F).max(1, keepdims=True))
+        assert not d[c:].any()

@@ -204,3 +204,27 @@ def test_past_32_bits():
     assert torch.equal(dx[-300:], wx)
     # the rows of zeros add nothing; the order of the sums differs
     assert torch.all((dg - wg).abs() <= 300 * U * (x[-300:].float() * w["h"].float() * w["rstd"][:, None]).abs().sum(0))
+
+
+@pytest.mark.parametrize("T,H", [(152, 8192), (153, 8192), (173, 7168), (174, 7168), (405, 2880), (406, 2880),
+                                 (512, 64), (513, 64)])
+def test_both_sides_of_the_few_rows_rule(T, H):
+    """The last size that gets a CTA per row and the first that does not: rstd
+    within 64 u, y and dx as above, dgamma's sum over either split's lines."""
+    rng = np.random.default_rng(T + H)
+    x, res, g, dy = _bf(rng, T, H), _bf(rng, T, H), _bf(rng, H), _bf(rng, T, H)
+    o = ops.rmsnorm(x.to(DEV), g.to(DEV), residual=res.to(DEV))
+    h = (x.float() + res.float()).to(torch.bfloat16)
+    assert torch.equal(o["h"].cpu(), h)
+    h64, g64, dy64 = np_(h), np_(g), np_(dy)
+    r = 1.0 / np.sqrt((h64 ** 2).mean(1) + 1e-5)
+    assert np.all(np.abs(np_(o["rstd"]) - r) <= 64 * U * r)
+    r = np_(o["rstd"]).astype(np.float64)[:, None]
+    _bf16_ok(np_(o["y"]), h64 * r * g64, 128 * U * np.abs(h64 * r * g64))
+    dx, dg = ops.rmsnorm_bwd(dy.to(DEV), o["h"], g.to(DEV), o["rstd"])
+    t = dy64 * g64
+    ref = r * (t - h64 * r * r * (t * h64).mean(1, keepdims=True))
+    mag = r * (np.abs(t) + np.abs(h64) * r * r * np.abs(t * h64).mean(1, keepdims=True))
+    _bf16_ok(np_(dx), ref, 2.0 ** -17 * mag)
+    term = dy64 * h64 * r
+    assert np.all(np.abs(np_(dg) - term.sum(0)) <= (T + 32) * U * np.abs(term).sum(0) + 1e-37)
