@@ -21,17 +21,27 @@ from . import lib as L
 from . import ops
 
 
+def _need_router(gamma, Wr, H: int):
+    ops._need(gamma, torch.bfloat16, (H,), "gamma")
+    if not Wr.is_cuda or Wr.dtype != torch.bfloat16 or Wr.dim() != 2 or Wr.shape[1] != H:  # (strides are torch's to follow)
+        raise ValueError(f"Wr: [n, {H}] bf16 on a CUDA device is needed, got {tuple(Wr.shape)} {Wr.dtype}")
+
+
 class MoeBlock:
     def __init__(self, layer, gamma, Wr, router: L.RouterParams, bias=None, eps: float = 1e-5):
         """layer: a MoeLayer; gamma [H] and Wr [n, H] bf16; router: how experts
         are chosen; bias [n] f32: the balance bias of the choice."""
+        _need_router(gamma, Wr, layer.H)
         self.layer, self.gamma, self.Wr, self.router, self.bias, self.eps = layer, gamma, Wr, router, bias, eps
 
     def forward(self, x, residual=None, token_mask=None):
         """x [T, H] bf16 (the previous sublayer's output), residual [T, H] the
-        stream it is added to.  Returns (out [T, H], h [T, H]): the experts'
-        output and the new stream, the next sublayer's x and residual."""
+        stream it is added to; T is the layer's, other sizes are refused.
+        Returns (out [T, H], h [T, H]): the experts' output and the new stream,
+        the next sublayer's x and residual.  out is the layer's own buffer: the
+        next forward overwrites it."""
         ly = self.layer
+        ops._need(x, torch.bfloat16, (ly.T, ly.H), "x")
         n = ops.rmsnorm(x, self.gamma, self.eps, residual=residual)
         self.h = n["h"] if residual is not None else x
         self.y, self.rstd = n["y"], n["rstd"]
@@ -44,8 +54,12 @@ class MoeBlock:
     def backward(self, dout, dh=None) -> dict:
         """dout, dh: the gradients arriving at forward's two outputs.  Returns
         dx (the gradient of x and of the residual alike), dgamma, dWr, dW1
-        (packed rows), dW2 and, with an FC1 bias, db1 (packed)."""
+        (packed rows), dW2 and, with an FC1 bias, db1 (packed).  dW1, dW2 and db1
+        are the layer's own buffers: the next backward overwrites them."""
         ly = self.layer
+        ops._need(dout, torch.bfloat16, (ly.T, ly.H), "dout")
+        if dh is not None:
+            ops._need(dh, torch.bfloat16, (ly.T, ly.H), "dh")
         ly.run(ly.backward_calls(dout))
         dlogits = ops.router_bwd(self.logits, self.idx, ly.dprob, self.router)
         dy = torch.addmm(ly.dx, dlogits, self.Wr)  # the two uses of y: the experts' rows and the logits
@@ -59,8 +73,16 @@ class MoeServer:
         """W1 [E, 2F, H] (rows: input | gate) and W2 [E, F, H] bf16 are cast to
         MXFP4 here, once; b1 [E, 2F] bf16; gamma, Wr, router, bias and eps as
         for MoeBlock."""
+        bf = torch.bfloat16
+        for w, what in ((W1, "W1"), (W2, "W2")):
+            if ops._need(w, bf, None, what).dim() != 3:
+                raise ValueError(f"{what}: three dimensions are needed, got {tuple(w.shape)}")
         self.E, N1, self.H = W1.shape
         self.F, self.k = W2.shape[1], k
+        ops._need(W2, bf, (self.E, self.F, self.H), "W2")
+        if b1 is not None:
+            ops._need(b1, bf, (self.E, N1), "b1")
+        _need_router(gamma, Wr, self.H)
         if N1 != 2 * self.F or params.act in (L.ACT["srelu"], L.ACT["none"]):
             raise ValueError("a gated activation and W1 [E, 2F, H] are needed")
         self.gamma, self.Wr, self.router, self.params, self.bias, self.eps = gamma, Wr, router, params, bias, eps
