@@ -162,11 +162,13 @@ __device__ __forceinline__ float off_middle(float y, float p, Pair r) {
 }
 
 // V: 16-byte vectors of a row per thread; vector j of a thread is column
-// group t + j * 32 wpr of the row.
+// group t + j * 32 wpr of the row.  h_out may be x or res: a thread stores
+// only the columns that it alone reads, after it has read them (so those three
+// are not __restrict__; the backward's dy, dres and dx likewise).
 template <int V>
 __global__ void __launch_bounds__(max_threads<V>()) k_rmsnorm_fwd(
-    const uint4* __restrict__ x, const uint4* __restrict__ res, const uint4* __restrict__ gamma, float eps, int T,
-    int H8, int wpr, int groups, int stages, uint4* __restrict__ h_out, uint4* __restrict__ y, uint8_t* __restrict__ q,
+    const uint4* x, const uint4* res, const uint4* __restrict__ gamma, float eps, int T,
+    int H8, int wpr, int groups, int stages, uint4* h_out, uint4* __restrict__ y, uint8_t* __restrict__ q,
     uint8_t* __restrict__ s, float* __restrict__ rstd) {
   extern __shared__ __align__(16) uint4 ring[];  // [stages][inputs][V][threads]
   __shared__ float2 red[64];
@@ -284,9 +286,9 @@ __global__ void __launch_bounds__(max_threads<V>()) k_rmsnorm_fwd(
 // does not depend on timing.
 template <int V>
 __global__ void __launch_bounds__(max_threads<V>()) k_rmsnorm_bwd(
-    const uint4* __restrict__ dy, const uint4* __restrict__ dres, const uint4* __restrict__ h,
+    const uint4* dy, const uint4* dres, const uint4* __restrict__ h,
     const uint4* __restrict__ gamma, const float* __restrict__ rstd, int T, int H8, int wpr, int groups, int stages,
-    uint4* __restrict__ dx, float* __restrict__ part) {
+    uint4* dx, float* __restrict__ part) {
   extern __shared__ __align__(16) uint4 ring[];  // [stages][inputs][V][threads]
   __shared__ float2 red[64];
   const int tpr = 32 * wpr, group = threadIdx.x / tpr, t = threadIdx.x - group * tpr;
