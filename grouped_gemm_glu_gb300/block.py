@@ -11,7 +11,9 @@ norm, the router's product and choice, then the experts.
 Both issue library calls on the current stream and read nothing back, so a
 step can be captured in a CUDA graph.  The router's product (logits =
 y . Wr^T and its gradients) is a plain matrix product of a small weight and is
-left to torch.
+left to torch.  The logits keep the product's 32 bits: rounded to bf16,
+neighbouring logits of hundreds of experts become equal and the lower index
+wins.  (8192 x 7168 with 256 experts: 25.9 us against 25.6 with bf16 logits.)
 """
 from __future__ import annotations
 
@@ -25,6 +27,11 @@ def _need_router(gamma, Wr, H: int):
     ops._need(gamma, torch.bfloat16, (H,), "gamma")
     if not Wr.is_cuda or Wr.dtype != torch.bfloat16 or Wr.dim() != 2 or Wr.shape[1] != H:  # (strides are torch's to follow)
         raise ValueError(f"Wr: [n, {H}] bf16 on a CUDA device is needed, got {tuple(Wr.shape)} {Wr.dtype}")
+
+
+def _logits(y, Wr):
+    """y . Wr^T, f32: the factors are bf16, their products exact, the sums f32."""
+    return torch.mm(y, Wr.t(), out_dtype=torch.float32)
 
 
 class MoeBlock:
@@ -45,7 +52,7 @@ class MoeBlock:
         n = ops.rmsnorm(x, self.gamma, self.eps, residual=residual)
         self.h = n["h"] if residual is not None else x
         self.y, self.rstd = n["y"], n["rstd"]
-        self.logits = self.y @ self.Wr.t()
+        self.logits = _logits(self.y, self.Wr)
         r = ops.router(self.logits, ly.k, self.router, bias=self.bias, token_mask=token_mask)
         self.idx, self.prob, self.load = r["idx"], r["prob"], r["load"]
         ly.run(ly.forward_calls(self.y, self.idx, self.prob))
@@ -61,7 +68,9 @@ class MoeBlock:
         if dh is not None:
             ops._need(dh, torch.bfloat16, (ly.T, ly.H), "dh")
         ly.run(ly.backward_calls(dout))
-        dlogits = ops.router_bwd(self.logits, self.idx, ly.dprob, self.router)
+        # f32 up to its products, there an operand in bf16 like y and Wr: an error of 2^-9 of each element,
+        # independent from one to the next, beside the 3.6% of the experts' MXFP8 operands behind dprob
+        dlogits = ops.router_bwd(self.logits, self.idx, ly.dprob, self.router).to(torch.bfloat16)
         dy = torch.addmm(ly.dx, dlogits, self.Wr)  # the two uses of y: the experts' rows and the logits
         dx, dgamma = ops.rmsnorm_bwd(dy, self.h, self.gamma, self.rstd, dres=dh)
         return {"dx": dx, "dgamma": dgamma, "dWr": dlogits.t() @ self.y, "dW1": ly.dW1, "dW2": ly.dW2, "db1": ly.db1}
@@ -103,7 +112,7 @@ class MoeServer:
         T = x.shape[0]
         n = ops.rmsnorm(x, self.gamma, self.eps, residual=residual, mxfp8=True, with_rstd=False)
         h = n["h"] if residual is not None else x
-        r = ops.router(n["y"] @ self.Wr.t(), self.k, self.router, bias=self.bias, token_mask=token_mask,
+        r = ops.router(_logits(n["y"], self.Wr), self.k, self.router, bias=self.bias, token_mask=token_mask,
                        with_load=False)
         p = ops.route_permute_mxfp8(n["q"], n["s"], r["idx"], r["prob"], self.E, self.rows(T), status=self.status)
         a = ops.fc1_fwd_mxfp4(p["xq_perm"], p["xs_perm"], self.W1q, self.W1s, p["counts"], p["offsets"], self.F,
