@@ -78,10 +78,11 @@ class MoeBlock:
 
 class MoeServer:
     def __init__(self, W1, W2, gamma, Wr, k: int, router: L.RouterParams, params: L.GluParams, b1=None, bias=None,
-                 eps: float = 1e-5):
+                 eps: float = 1e-5, expert_begin: int = 0):
         """W1 [E, 2F, H] (rows: input | gate) and W2 [E, F, H] bf16 are cast to
         MXFP4 here, once; b1 [E, 2F] bf16; gamma, Wr, router, bias and eps as
-        for MoeBlock."""
+        for MoeBlock.  A shard: W1, W2 and b1 hold E of Wr's n experts, from
+        expert_begin on; the others' part of the output is left to their shards."""
         bf = torch.bfloat16
         for w, what in ((W1, "W1"), (W2, "W2")):
             if ops._need(w, bf, None, what).dim() != 3:
@@ -94,7 +95,10 @@ class MoeServer:
         _need_router(gamma, Wr, self.H)
         if N1 != 2 * self.F or params.act in (L.ACT["srelu"], L.ACT["none"]):
             raise ValueError("a gated activation and W1 [E, 2F, H] are needed")
+        if not 0 <= expert_begin < Wr.shape[0]:
+            raise ValueError(f"expert_begin: one of the {Wr.shape[0]} experts is needed, got {expert_begin}")
         self.gamma, self.Wr, self.router, self.params, self.bias, self.eps = gamma, Wr, router, params, bias, eps
+        self.expert_begin = expert_begin
         self.b1p = ops.repack_fc1(b1.unsqueeze(2)).squeeze(2).contiguous() if b1 is not None else None
         self.W1q, self.W1s = ops.quantize_mxfp4(ops.repack_fc1(W1))
         self.W2q, self.W2s = ops.quantize_mxfp4(W2, col=True)
@@ -114,7 +118,8 @@ class MoeServer:
         h = n["h"] if residual is not None else x
         r = ops.router(_logits(n["y"], self.Wr), self.k, self.router, bias=self.bias, token_mask=token_mask,
                        with_load=False)
-        p = ops.route_permute_mxfp8(n["q"], n["s"], r["idx"], r["prob"], self.E, self.rows(T), status=self.status)
+        p = ops.route_permute_mxfp8(n["q"], n["s"], r["idx"], r["prob"], self.E, self.rows(T),
+                                    expert_begin=self.expert_begin, status=self.status)
         a = ops.fc1_fwd_mxfp4(p["xq_perm"], p["xs_perm"], self.W1q, self.W1s, p["counts"], p["offsets"], self.F,
                               self.params, b1p=self.b1p, save_pre=False, with_col=False, status=self.status)
         y = ops.fc2_fwd_mxfp4(a["q_row"], a["s_row"], self.W2q, self.W2s, p["counts"], p["offsets"],
