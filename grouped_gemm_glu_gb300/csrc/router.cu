@@ -5,8 +5,8 @@
 //   key  = s_e + bias_e; without a bias the logit itself, which orders the
 //          experts as the scores do
 //   group score = sum of the group_top best keys of a group (its best key, or
-//          its two best scores); experts outside the topk_group best groups
-//          are out
+//          its two best scores; -inf where fewer are left); experts outside
+//          the topk_group best groups are out
 //   the k largest keys, ties to the lowest index; weight = the score,
 //   renormalised over the chosen experts if asked, times scale
 //

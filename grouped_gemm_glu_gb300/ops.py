@@ -608,7 +608,8 @@ def router(logits, k: int, params: L.RouterParams, bias=None, token_mask=None, w
     prob [T, k] f32 (route_permute's topk_idx and topk_prob; slots without an
     expert hold -1 and 0) and load [n] int32, the tokens of each expert.
     bias [n] f32 takes part in the choice only; token_mask [T] uint8 or bool:
-    tokens with 0 choose nothing."""
+    tokens with 0 choose nothing.  With group_top = 2 a group that has fewer
+    than two experts left (logit or bias not -inf) ranks behind all others."""
     b16 = _logits(logits)
     T, n = logits.shape
     if bias is not None:

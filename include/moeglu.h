@@ -687,7 +687,11 @@ typedef struct {
  * The choice is made on fp32 keys: score + bias with a bias, the logits
  * themselves without one (the same order); group scores for group_top = 2
  * without a bias sum the scores.  Ties go to the lowest index, of experts and
- * of groups.  An expert whose logit (or key) is -inf is never chosen: a slot
+ * of groups.  A group's score takes its keys as they are, -inf among them: with
+ * group_top = 2 a group with fewer than two experts left scores -inf, ranks
+ * behind every group with two, and by index among the groups of that kind,
+ * empty ones included, so that its last expert may not be chosen; with
+ * group_top = 1 it counts while one expert is left.  An expert whose logit (or key) is -inf is never chosen: a slot
  * that finds no expert gets index -1 and weight 0, which moe_route_permute
  * drops.  A NaN logit ranks first, so that it shows in the weights; softmax
  * weights of a row holding NaN or +inf are NaN.
