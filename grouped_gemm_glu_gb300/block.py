@@ -100,9 +100,9 @@ class MoeServer:
         self.gamma, self.Wr, self.router, self.params, self.bias, self.eps = gamma, Wr, router, params, bias, eps
         self.expert_begin = expert_begin
         self.b1p = ops.repack_fc1(b1.unsqueeze(2)).squeeze(2).contiguous() if b1 is not None else None
-        self.W1q, self.W1s = ops.quantize_mxfp4(ops.repack_fc1(W1))
-        self.W2q, self.W2s = ops.quantize_mxfp4(W2, col=True)
         self.status = ops.new_status(W1.device)
+        self.W1q, self.W1s = ops.quantize_mxfp4(ops.repack_fc1(W1), status=self.status)
+        self.W2q, self.W2s = ops.quantize_mxfp4(W2, col=True, status=self.status)
 
     def rows(self, T: int) -> int:
         """Rows the permuted buffers of T tokens need: every assignment and up

@@ -4,6 +4,7 @@ would misread are errors of the host, before anything is launched."""
 import pytest
 import torch
 
+from grouped_gemm_glu_gb300 import block
 from grouped_gemm_glu_gb300 import lib as L
 from grouped_gemm_glu_gb300.block import MoeBlock, MoeServer
 from grouped_gemm_glu_gb300.layer import MoeLayer
@@ -73,3 +74,11 @@ def test_strided_router_weight_is_taken():
     # (the products may add in another order)
     assert torch.allclose(a.logits.float(), b.logits.float(), rtol=2.0 ** -7, atol=2.0 ** -7)
     assert a.backward(x, x)["dWr"].shape == (E, H)
+
+
+def test_server_casts_report_to_its_status(monkeypatch):
+    """A tile of a weight that never arrives shows in the server's status word."""
+    seen, cast = [], block.ops.quantize_mxfp4
+    monkeypatch.setattr(block.ops, "quantize_mxfp4", lambda *a, **kw: (seen.append(kw.get("status")), cast(*a, **kw))[1])
+    s = _server()
+    assert len(seen) == 2 and all(t is s.status for t in seen)
