@@ -47,8 +47,10 @@
 // Every wait is bounded (MOE_ERR_TIMEOUT + early exit, never a trap).
 //
 // Bound: with many rows by the tensor pipe (16384 tokens, top-4, 2880 x 5760
-// with bias and clamped SwiGLU: 661 us, 3290 TFLOP/s, a k-block of 224 rows in
-// about 460 cycles where its MMAs take 448), with few by reading the live
+// with bias and clamped SwiGLU: 661 us, 3290 TFLOP/s, in bursts of some tens of
+// milliseconds, a k-block of 224 rows in about 460 cycles where its MMAs take
+// 448; 760 us, 2860 TFLOP/s, in passes that go on for seconds under the power
+// cap), with few by reading the live
 // experts' weights (64 tokens, top-8 of 32 experts, 2048 x 7168: 49.8 us, 5.2
 // TB/s), with one token by the two launches and one tile's latency (15.6 us,
 // where the weights' bytes take 5.2).
@@ -696,7 +698,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     Amax amax_bits{0u, 0u};
     int lt = 0, e = 0;
     // With few rows the next tile and its bias are fetched before a tile is
-    // written out (one token 16.0 -> 15.5 us; with NB = 7 the same made products
+    // written out (one token 16.0 -> 15.6 us; with NB = 7 the same made products
     // with a short K 4% slower).
     constexpr bool AHEAD = NB <= 4;
     Tile next;
@@ -782,7 +784,13 @@ static moe_status_t launch_nb(const Maps& m, const Args& a, int sm_margin, cudaS
 // Few rows per expert: at most FEW of them on average over the buffers, which
 // hold up to 31 rows of padding per expert.  32 experts, 2880 x 5760 gated: 61
 // us with NB = 2 against 70 with 7 at 64 rows each, 94 against 73 at 96; 2048 x
-// 7168: 51 against 57 and 79 against 60.
+// 7168: 51 against 57 and 79 against 60.  The counts are device data, so
+// R_cap has to stand for them.  Where one expert has a quarter of the rows, its
+// many low tiles read the weight again: 64 experts, 2048 x 7168, 32 rows each on
+// average 108 us with NB = 2 against 111, 48 121 against 117, 64 132 against
+// 122; 32 experts, 2880 x 5760 gated 67 against 70, 75 against 77, 83 against
+// 78.  Buffers larger than the rows need take NB = 7 and lose the first
+// figures' 12 to 15%.
 constexpr int FEW = 96;
 static bool few_rows(int E, int R_cap) { return R_cap <= (long long)FEW * E; }
 

@@ -65,8 +65,7 @@ moe_status_t grouped_gemm_bf16_out(const void* A, const void* W, const int32_t* 
 
 // Grouped product of MXFP8 rows with an MXFP4 weight (gemm_mx4.cu; the
 // MXFP4 cases of moe_grouped_fc2_fwd and the FC1).  params null: no
-// activation.  work: grouped_gemm_mxfp4_workspace() bytes, 256-byte aligned
-//.
+// activation.  work: grouped_gemm_mxfp4_workspace() bytes, 256-byte aligned.
 size_t grouped_gemm_mxfp4_workspace(int E, int K, int R_cap);
 moe_status_t grouped_gemm_mxfp4(const uint8_t* xq, const uint8_t* xs, const uint8_t* wq, const uint8_t* ws,
                                 const int32_t* counts, const int32_t* offsets, int E, int K, int N, int R_cap,

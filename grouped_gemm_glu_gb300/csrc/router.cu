@@ -24,10 +24,12 @@
 // expert with a logit (or bias) of -inf is never chosen.
 //
 // Memory: each logit is read once (4 or 2 bytes), 8 bytes leave per chosen
-// expert; at 8192 x 256 that is 1.3 us of HBM time, so the instructions of
-// the scores and the k rounds bound the kernel: 12.6 us with 8 groups, bias
-// and top-8 (issue slots 71% busy), 9.6 us for 32768 x 64 top-6, 4.4 us for
-// one token; backward of the latter 8.7 us.
+// expert; at 8192 x 256 that is 1.3 us of HBM time.  What bounds the kernel is
+// the latency of the chain from the loads over the scores and the k rounds:
+// 12.6 us with 8 groups, bias and top-8 (issue slots 45% busy, half of the
+// warps resident on average: 8192 tokens are 1.7 rounds of 152 x 32 warps), 9.6
+// us for 32768 x 64 top-6 (41%), 4.4 us for one token.  Backward of 32768 x 64
+// 8.7 us (46%; half of the stalls wait for its loads).
 #include <type_traits>
 
 #include "common.cuh"
