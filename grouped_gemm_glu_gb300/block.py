@@ -112,10 +112,12 @@ class MoeServer:
 
     def step(self, x, residual=None, token_mask=None):
         """(out [T, H], h [T, H]) as MoeBlock.forward, for one decoded token per
-        sequence or a whole prompt."""
+        sequence or a whole prompt; an empty batch gives empty results."""
         T = x.shape[0]
         n = ops.rmsnorm(x, self.gamma, self.eps, residual=residual, mxfp8=True, with_rstd=False)
         h = n["h"] if residual is not None else x
+        if T == 0:
+            return torch.empty_like(x), h  # (the routing takes no empty batch)
         r = ops.router(_logits(n["y"], self.Wr), self.k, self.router, bias=self.bias, token_mask=token_mask,
                        with_load=False)
         p = ops.route_permute_mxfp8(n["q"], n["s"], r["idx"], r["prob"], self.E, self.rows(T),

@@ -82,3 +82,12 @@ def test_server_casts_report_to_its_status(monkeypatch):
     monkeypatch.setattr(block.ops, "quantize_mxfp4", lambda *a, **kw: (seen.append(kw.get("status")), cast(*a, **kw))[1])
     s = _server()
     assert len(seen) == 2 and all(t is s.status for t in seen)
+
+
+def test_server_takes_an_empty_batch():
+    s, x = _server(), _z(0, H)
+    for res in (None, x):
+        out, h = s.step(x, res)
+        assert out.shape == h.shape == (0, H) and out.dtype == h.dtype == torch.bfloat16
+    with pytest.raises(ValueError):
+        s.step(_z(0, H // 2))
