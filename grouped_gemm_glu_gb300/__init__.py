@@ -6,4 +6,4 @@ marshals torch tensors into it.  Importing this package does not load the
 library; ``grouped_gemm_glu_gb300.lib.load()`` does, and raises if it is
 missing.
 """
-__all__ = ["synth", "lib", "ops", "layer", "block"]
+__all__ = ["synth", "lib", "ops", "layer", "block", "optim"]

@@ -71,6 +71,20 @@ def router_params(score: str = "softmax", renorm: bool = False, scale: float = 1
     return RouterParams(SCORE[score], int(renorm), n_group, topk_group, group_top, scale)
 
 
+class AdamwTensor(C.Structure):
+    _fields_ = [("w", C.c_void_p), ("master", C.c_void_p), ("m", C.c_void_p), ("v", C.c_void_p),
+                ("m_scale", C.c_void_p), ("v_scale", C.c_void_p), ("n", C.c_int64), ("weight_decay", C.c_float),
+                ("w_bf16", C.c_int32), ("grad_bf16", C.c_int32), ("reserved", C.c_int32)]
+
+
+class AdamwParams(C.Structure):
+    _fields_ = [("beta1", C.c_double), ("beta2", C.c_double), ("eps", C.c_double), ("max_norm", C.c_double),
+                ("state", C.c_int32), ("seed", C.c_uint32)]
+
+
+MOMENTS = {"f32": 0, "mxfp8": 1}
+
+
 P, I, U64, SZ, F32 = C.c_void_p, C.c_int, C.c_uint64, C.c_size_t, C.c_float
 
 _SIGS = {
@@ -123,6 +137,10 @@ _SIGS = {
     "moe_dequantize_mxfp8": [P, P, SZ, P, P],
     "moe_router_fwd": [P, I, P, P, I, I, I, C.POINTER(RouterParams), P, P, P, P],
     "moe_router_bwd": [P, I, P, P, I, I, I, C.POINTER(RouterParams), P, P],
+    "moe_adamw_plan_size": ([P, I], SZ),
+    "moe_adamw_plan": [P, I, I, P, SZ],
+    "moe_adamw_workspace_size": ([I], SZ),
+    "moe_adamw_step": [P, P, I, P, C.POINTER(AdamwParams), P, P, P, P, SZ, P],
     "moe_get_status": [P, P, P],
     "moe_set_wait_limit_ns": ([U64], None),
     "moe_wait_selftest": [I, P, P, P],

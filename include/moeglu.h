@@ -715,6 +715,73 @@ MOE_API moe_status_t moe_router_bwd(const void* logits, int logits_bf16, const i
                                     const float* dprob, int T, int n, int k, const moe_router_params_t* params,
                                     void* dlogits, moe_stream_t stream);
 
+/* ---------------------------------------------------------------------- */
+/* The weights' update.                                                     */
+
+typedef enum { MOE_MOMENTS_F32 = 0, MOE_MOMENTS_MXFP8 = 1 } moe_moments_t;
+
+/* One tensor of an AdamW step: n consecutive elements.  f32 weights: w, no
+ * master.  bf16 weights (w_bf16 != 0): master holds their f32 values and w gets
+ * the rounding.  MOE_MOMENTS_F32: m and v f32 [n].  MOE_MOMENTS_MXFP8: m and v
+ * hold E4M3 codes of m and of sqrt(v) (n rounded up to 32 bytes, 8-byte
+ * aligned), m_scale and v_scale one E8M0 byte per 32 elements; zeros are the
+ * state before the first step in both forms.  Weights, masters, moments and
+ * gradients may start at any element (whole vectors are used where f32 data
+ * are 32-byte and bf16 data 16-byte aligned).  No two tensors may overlap. */
+typedef struct {
+  void* w;
+  float* master;
+  void* m;
+  void* v;
+  uint8_t* m_scale;
+  uint8_t* v_scale;
+  int64_t n;
+  float weight_decay; /* >= 0 */
+  int32_t w_bf16;
+  int32_t grad_bf16;
+  int32_t reserved;
+} moe_adamw_tensor_t;
+
+typedef struct {
+  double beta1, beta2; /* in [0, 1) */
+  double eps;
+  double max_norm;     /* 0: the gradients are neither measured nor clipped */
+  int32_t state;       /* moe_moments_t */
+  uint32_t seed;       /* of the random bits that round 8-bit moments */
+} moe_adamw_params_t;
+
+/* The device's copy of a list of tensors: moe_adamw_plan writes its
+ * moe_adamw_plan_size bytes into host memory, the caller copies them to the
+ * device once (8-byte aligned) and passes them to every step. */
+MOE_API size_t moe_adamw_plan_size(const moe_adamw_tensor_t* tensors, int n);
+MOE_API moe_status_t moe_adamw_plan(const moe_adamw_tensor_t* tensors, int n, int state, void* host_plan, size_t bytes);
+MOE_API size_t moe_adamw_workspace_size(int n);
+
+/* One AdamW step over n tensors:
+ *   t += 1;  c = min(1, max_norm / (|g| + 1e-6)) (c = 1 without max_norm), g' = c g
+ *   m = b1 m + (1 - b1) g',  v = b2 v + (1 - b2) g'^2
+ *   w = w (1 - lr wd) - lr (m / (1 - b1^t)) / (sqrt(v / (1 - b2^t)) + eps)
+ * |g| is the 2-norm over all tensors, its squares added in fp32 by eights and
+ * these sums exactly (a gradient past 1.8e19 counts as infinite).  8-bit
+ * moments are written with the smallest scale 2^e (e >= -127) that keeps a
+ * block's largest value at or below 448 2^e; a value between two codes goes up
+ * if its distance above the lower one, as a fraction of theirs, and 16 random
+ * bits over 65536 reach 1 together, and a sqrt(v) > 0 keeps at least the
+ * smallest code.  Random bits of element i of tensor j: with the 32-bit hash
+ * f(x): x ^= x >> 16, x *= 0x7FEB352D, x ^= x >> 15, x *= 0x846CA68B, x ^= x >> 16,
+ * f(f(f(f(f(t) ^ seed) + j) + (i >> 32)) + i), high half for m and low half for
+ * sqrt(v).  A block that holds NaN or an infinity becomes NaN (scale 0xFF).
+ * With max_norm a step whose norm is not finite changes nothing, t included.
+ * tensors, grads (n device addresses) are host arrays, read before the call
+ * returns; plan the device copy of the same tensors; lr (f32), t (int64, the
+ * number of steps taken) and norm (f32, nullable, written with max_norm only)
+ * are in device memory, so that a captured step takes the learning rate and the
+ * count of its replay.  ws: moe_adamw_workspace_size(n) bytes, 16-byte aligned; steps that may run at the same
+ * time need separate ones. */
+MOE_API moe_status_t moe_adamw_step(const moe_adamw_tensor_t* tensors, const void* const* grads, int n, const void* plan,
+                                    const moe_adamw_params_t* p, const float* lr, int64_t* t, float* norm, void* ws,
+                                    size_t ws_bytes, moe_stream_t stream);
+
 /* Copies the device status word to *host_out (synchronises `stream`; not
  * for use inside a graph capture). */
 MOE_API moe_status_t moe_get_status(const int32_t* status, int32_t* host_out, moe_stream_t stream);
