@@ -799,3 +799,74 @@ def route_permute_mxfp8(xq, xs, topk_idx, topk_prob, E: int, R_cap: int, expert_
         _cur(xq)), "moe_route_permute_mxfp8")
     o["status"] = st
     return o
+
+
+def _lora_args(x, A, B, idx, scale):
+    """Checks an adapter call's common arguments; returns (T, K, N, r, G)."""
+    bf = torch.bfloat16
+    T, K = _need2(x, bf, "x")
+    for w, what in ((A, "A"), (B, "B")):
+        if _need(w, bf, None, what).dim() != 3:
+            raise ValueError(f"{what}: three dimensions are needed, got {tuple(w.shape)}")
+    G, r, N = B.shape
+    _need(A, bf, (G, r, K), "A")
+    _need(idx, torch.int32, (T,), "idx")
+    _need(scale, torch.float32, (G,), "scale")
+    d = x.get_device()
+    if A.get_device() != d or B.get_device() != d or idx.get_device() != d or scale.get_device() != d:
+        raise ValueError("x, A, B, idx and scale must lie on one device")
+    if d != torch.cuda.current_device():
+        raise ValueError(f"the tensors lie on cuda:{d}, which is not the current device")
+    if G == 0 or r == 0 or r % 8 or K % 8 or N % 8 or not K or not N:
+        raise ValueError(f"r, K and N must be positive multiples of 8, got r = {r}, K = {K}, N = {N}")
+    if r > 128 or G > 32767:
+        raise ValueError(f"at most rank 128 and 32767 adapters are supported, got {r} and {G}")
+    return T, K, N, r, G
+
+
+def _on(t, dtype, shape, what, like):
+    """_need on the device of `like`."""
+    if _need(t, dtype, shape, what).get_device() != like.get_device():
+        raise ValueError(f"{what}: lies on {t.device}, x on {like.device}")
+    return t
+
+
+def lora(x, A, B, idx, scale, base=None, out=None, with_h: bool = True, status=None) -> dict:
+    """Low-rank adapters beside a shared projection: for row t of x [T, K] with
+    adapter a = idx[t] (int32; rows with an index outside [0, G) have none)
+    h = scale[a] (A_a x) and y = base + B_a^T h.  A [G, r, K] and B [G, r, N]
+    bf16, scale [G] f32, base [T, N] bf16 the projection's output (None: zero),
+    out where y goes (may be base).  Returns y [T, N] and, with_h, h [T, r] bf16,
+    which lora_bwd reads."""
+    T, K, N, r, G = _lora_args(x, A, B, idx, scale)
+    bf = torch.bfloat16
+    if base is not None:
+        _on(base, bf, (T, N), "base", x)
+    y = _on(out, bf, (T, N), "out", x) if out is not None else torch.empty(T, N, dtype=bf, device=x.device)
+    h = torch.empty(T, r, dtype=bf, device=x.device) if with_h else None
+    n = _size("moe_lora_workspace_size", T, r, G)
+    ws = torch.empty(n, dtype=torch.uint8, device=x.device)
+    L.check(L.load().moe_lora_fwd(x.data_ptr(), A.data_ptr(), B.data_ptr(), idx.data_ptr(), scale.data_ptr(), _ptr(base),
+                                  T, K, N, r, G, y.data_ptr(), _ptr(h), ws.data_ptr(), n, _ptr(status), _cur(x)),
+            "moe_lora_fwd")
+    return {"y": y, "h": h} if with_h else {"y": y}
+
+
+def lora_bwd(dy, x, h, A, B, idx, scale, base=None, out=None, status=None):
+    """Backward of lora: (dx [T, K], dA [G, r, K], dB [G, r, N]) bf16 from dy
+    [T, N] and the forward's x and h.  base [T, K] is the gradient that reaches x
+    elsewhere, added to dx (None: zero); out where dx goes (may be base)."""
+    T, K, N, r, G = _lora_args(x, A, B, idx, scale)
+    bf = torch.bfloat16
+    _on(dy, bf, (T, N), "dy", x)
+    _on(h, bf, (T, r), "h", x)
+    if base is not None:
+        _on(base, bf, (T, K), "base", x)
+    dx = _on(out, bf, (T, K), "out", x) if out is not None else torch.empty_like(x)
+    dA, dB = torch.empty_like(A), torch.empty_like(B)
+    n = _size("moe_lora_workspace_size", T, r, G)
+    ws = torch.empty(n, dtype=torch.uint8, device=x.device)
+    L.check(L.load().moe_lora_bwd(dy.data_ptr(), x.data_ptr(), h.data_ptr(), A.data_ptr(), B.data_ptr(), idx.data_ptr(),
+                                  scale.data_ptr(), _ptr(base), T, K, N, r, G, dx.data_ptr(), dA.data_ptr(), dB.data_ptr(),
+                                  ws.data_ptr(), n, _ptr(status), _cur(x)), "moe_lora_bwd")
+    return dx, dA, dB
