@@ -16,12 +16,16 @@
 //   k_wgrad   D[128 columns][r] = X^T U, contracted over an adapter's rows
 // A first kernel (k_group) sorts the row indexes by adapter, stably, and cuts
 // each adapter's rows into tiles of 128; the rows themselves stay where they
-// are and are gathered by 16-byte asynchronous copies straight into the
-// swizzled operand layout, so that any order of rows takes the same path, no
-// tile mixes adapters and no work is done for absent ones.
+// are.  Each warp that loads or stores looks at its 32 rows: neighbours in
+// memory (a request's tokens, mostly) move as one box by TMA, others row by row
+// (16-byte asynchronous copies into the same swizzled layout), so that every
+// order of rows is served, no tile mixes adapters and no work is done for
+// absent ones.  h and u are also kept in the grouped order (an adapter's rows
+// from a multiple of 16 on, zeros up to the next one), where the products
+// behind them read them by TMA.
 // k_shrink and k_wgrad produce little from much: the CTAs of a cluster share
-// a tile's contraction and add their sums through distributed shared memory,
-// always in the same order, so equal inputs give equal bits.
+// a contraction and add their sums through distributed shared memory, always
+// in the same order, so equal inputs give equal bits.
 // Few rows (decoding) take k_rows instead: one cluster per row, one launch.
 #include "common.cuh"
 #include "host_common.h"
@@ -29,21 +33,25 @@
 namespace moeglu {
 namespace lora {
 
-constexpr int TILE = 128;      // rows of one adapter per tile
+constexpr int TILE = 128;  // rows of one adapter per tile, columns per unit
+constexpr int SLAB = 32;   // rows that a warp moves
 constexpr int MAX_R = 128;
-constexpr int KB = 64;         // contraction per stage (128-byte operand rows)
-constexpr int LOADERS = 128;   // threads that copy
-constexpr int THREADS = 160;   // + the MMA warp
+constexpr int KB = 64;     // contraction per stage (128-byte operand rows)
+constexpr int ALIGN = 16;  // an adapter's first place in the grouped order: the MMA's contraction
+constexpr int MIN_BOX = 8; // fewer neighbours than this are copied row by row
 
 struct Tile {
-  int adapter, start, count, pad;
+  int adapter, start, count;  // -1: rows without an adapter; first place in the grouped order
+  int cost;                   // of the tiles before it (see tile_cost)
 };
-// Workspace: the rows by adapter, each adapter's first place, the tiles.
+__host__ __device__ __forceinline__ int tile_cost(int count) { return 1 + (count + SLAB - 1) / SLAB; }
+
+// Workspace: the grouped order.
 struct Plan {
-  int* n_tiles;
-  int* first;  // [G + 2]: adapters, then the rows without one
+  int* sums;    // tiles with an adapter, all tiles, cost of all tiles
+  int* first;   // [G + 2]: each adapter's first place; the rows without one; the end
   Tile* tiles;
-  int* rows;   // [T]
+  int* rows;    // row of each place, -1 where there is none
 };
 
 __device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool ok) {
@@ -55,17 +63,54 @@ template <int N>
 __device__ __forceinline__ void cp_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
+// Arrives on the barrier when the thread's copies so far have landed.
+__device__ __forceinline__ void cp_arrive(uint64_t* bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+__device__ __forceinline__ void mbar_expect_tx(uint64_t* bar, uint32_t bytes) {
+  asm volatile("mbarrier.expect_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(bar)), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void tma_store_2d(const CUtensorMap* m, uint32_t src, int32_t c0, int32_t c1) {
+  asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%2, %3}], [%1];" ::"l"(
+                   reinterpret_cast<uint64_t>(m)),
+               "r"(src), "r"(c0), "r"(c1)
+               : "memory");
+}
+__device__ __forceinline__ void tma_2d(uint32_t dst, const CUtensorMap* m, uint64_t* bar, int32_t c0, int32_t c1) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], [%2];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(m)), "r"(smem_u32(bar)), "r"(c0), "r"(c1)
+      : "memory");
+}
+__device__ __forceinline__ void tma_3d(uint32_t dst, const CUtensorMap* m, uint64_t* bar, int32_t c0, int32_t c1, int32_t c2) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(m)), "r"(smem_u32(bar)), "r"(c0), "r"(c1), "r"(c2)
+      : "memory");
+}
 // 16-byte piece c of 128-byte row `row` of a tile in the 128-byte swizzle
 __device__ __forceinline__ uint32_t piece(uint32_t tile, int row, int c) {
   return tile + row * 128 + ((c ^ (row & 7)) << 4);
 }
-// Operand tile with the contraction across its 128-byte rows (64 elements of
-// the kept dimension per row): `block` bytes between blocks of 64 of them.
-__device__ __forceinline__ uint64_t sdesc_mnmajor_sw128(uint32_t saddr, uint32_t block) {
-  return (uint64_t)((saddr & 0x3FFFFu) >> 4) | ((uint64_t)(block >> 4) << 16) | ((uint64_t)(1024u >> 4) << 32) |
-         (1ull << 46) | (2ull << 61);
+
+// The rank's operands (rows of r elements in the grouped order) have rows of
+// 32, 64 or 128 bytes, by the rank: 16, 32 or blocks of 64 elements, each
+// swizzled over its row's length.
+__host__ __device__ constexpr int rank_cols(int rp) { return rp <= 16 ? 16 : rp <= 32 ? 32 : 64; }
+__host__ __device__ constexpr int rank_bytes(int rp) { return rp <= 64 ? rank_cols(rp) * 2 : 256; }
+__device__ __forceinline__ uint64_t swizzle_bits(uint32_t row_bytes) {
+  return (uint64_t)(row_bytes == 128 ? 2u : row_bytes == 64 ? 4u : 6u) << 61;
 }
-constexpr uint32_t A_MN = 1u << 15, B_MN = 1u << 16;  // instruction descriptor: that operand's layout
+// Operand tiles: rows of row_bytes along the contraction (kmajor) or across it
+// (mnmajor: the rows are steps of the contraction, `block` bytes between
+// blocks of 64 elements of the kept dimension).
+__device__ __forceinline__ uint64_t sdesc_kmajor(uint32_t saddr, uint32_t row_bytes) {
+  return (uint64_t)((saddr & 0x3FFFFu) >> 4) | ((uint64_t)(row_bytes >> 1) << 32) | (1ull << 46) | swizzle_bits(row_bytes);
+}
+__device__ __forceinline__ uint64_t sdesc_mnmajor(uint32_t saddr, uint32_t row_bytes, uint32_t block) {
+  return sdesc_kmajor(saddr, row_bytes) | ((uint64_t)(block >> 4) << 16);
+}
+constexpr uint32_t A_MN = 1u << 15, B_MN = 1u << 16;  // instruction descriptor: that operand lies across the contraction
 
 __device__ __forceinline__ void wait_for_primary() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
@@ -75,406 +120,386 @@ __device__ __forceinline__ float4 ld_cluster(uint32_t addr) {
   asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr));
   return v;
 }
+__device__ __forceinline__ int ld_cluster_int(uint32_t addr) {
+  int v;
+  asm volatile("ld.shared::cluster.b32 %0, [%1];" : "=r"(v) : "r"(addr));
+  return v;
+}
 __device__ __forceinline__ uint32_t cluster_size() {
   uint32_t n;
   asm volatile("mov.u32 %0, %%cluster_nctaid.x;" : "=r"(n));
   return n;
+}
+// The dynamic shared memory from its first multiple of 1024 bytes on (the
+// swizzle's period; 1024 bytes more are asked for).
+__device__ __forceinline__ unsigned char* aligned_smem(unsigned char* p) { return p + ((0u - smem_u32(p)) & 1023u); }
+
+// After an abort: gives the TMA copies of the last steps issued a millisecond
+// to land before the CTA's shared memory is given up.
+__device__ __forceinline__ void settle(uint64_t* full, int stages, int issued, int* never) {
+  for (int k = max(0, issued - stages); k < issued; ++k)
+    mbar_wait(&full[k % stages], (k / stages) & 1, WaitGuard{never, nullptr, 1000000});
+}
+
+// A warp's 32 places: the row of each lane (-1: none), and whether they are
+// neighbours in memory, as far as there are any (the first lanes').
+struct Slab {
+  int row, first, count;
+  bool box;
+};
+__device__ __forceinline__ Slab slab_of(int row) {
+  Slab s;
+  s.row = row;
+  s.count = __popc(__ballot_sync(0xFFFFFFFFu, row >= 0));
+  s.first = __shfl_sync(0xFFFFFFFFu, row, 0);
+  s.box = __all_sync(0xFFFFFFFFu, row < 0 || row == s.first + (int)(threadIdx.x & 31));
+  return s;
 }
 
 // ---------------------------------------------------------------------------
 // Grouping: one CTA; warp w counts and places its stretch of rows
 // ---------------------------------------------------------------------------
 constexpr int GROUP_THREADS = 1024, GROUP_SMEM = 128 * 1024, MAX_G = GROUP_SMEM / 4 - 1;
+constexpr int HELD = 8;  // indexes that a lane keeps between the two passes
+
+__device__ __forceinline__ int warp_scan(int v) {  // inclusive
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const int o = __shfl_up_sync(0xFFFFFFFFu, v, d);
+    if ((int)(threadIdx.x & 31) >= d) v += o;
+  }
+  return v;
+}
 
 __global__ void __launch_bounds__(GROUP_THREADS) k_group(const int32_t* __restrict__ idx, int T, int G, int warps, Plan p) {
   launch_dependents();
-  extern __shared__ int hist[];  // [warps][G + 1]
-  __shared__ int part[2][32];
+  extern __shared__ int hist[];  // [G + 1][warps]
+  __shared__ int part[4][32];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, groups = G + 1;
+  const int per = ((T + warps - 1) / warps + 31) & ~31;
+  const int lo = min(T, warp * per), hi = warp < warps ? min(T, lo + per) : lo;
+  int held[HELD];
+#pragma unroll
+  for (int i = 0; i < HELD; ++i) held[i] = lo + 32 * i + lane < hi ? idx[lo + 32 * i + lane] : 0;
   for (int i = tid; i < warps * groups; i += GROUP_THREADS) hist[i] = 0;
   __syncthreads();
-  const int per = ((T + warps - 1) / warps + 31) & ~31;
-  const int lo = warp * per, hi = warp < warps ? min(T, lo + per) : lo;
-  int* mine = hist + warp * groups;
-  auto group_of = [&](int row) {
-    const int a = idx[row];
-    return (unsigned)a < (unsigned)G ? a : G;
+  // f(row, group, lanes of the same group) for the warp's rows, 32 at a time
+  auto each = [&](auto f) {
+    auto one = [&](int b, int a) {
+      const bool ok = b + lane < hi;
+      a = !ok ? -1 : (unsigned)a < (unsigned)G ? a : G;  // (-1: a group of its own, not counted)
+      const uint32_t same = __match_any_sync(0xFFFFFFFFu, a);
+      f(b + lane, a, same);
+    };
+#pragma unroll
+    for (int i = 0; i < HELD; ++i)
+      if (lo + 32 * i < hi) one(lo + 32 * i, held[i]);
+    for (int b = lo + 32 * HELD; b < hi; b += 32) one(b, b + lane < hi ? idx[b + lane] : 0);
   };
-  for (int b = lo; b < hi; b += 32) {
-    const bool ok = b + lane < hi;
-    const uint32_t act = __ballot_sync(0xFFFFFFFFu, ok);
-    if (ok) {
-      const int a = group_of(b + lane);
-      const uint32_t same = __match_any_sync(act, a);
-      if ((same & ((1u << lane) - 1)) == 0) mine[a] += __popc(same);
-    }
+  const uint32_t below = (1u << lane) - 1;
+  each([&](int, int a, uint32_t same) {
+    if (a >= 0 && (same & below) == 0) hist[a * warps + warp] += __popc(same);
     __syncwarp();
+  });
+  __syncthreads();
+  // per group: its rows before each warp's (in hist) and in all (first, for now)
+  for (int g = warp; g < groups; g += GROUP_THREADS / 32) {
+    const int n = lane < warps ? hist[g * warps + lane] : 0, s = warp_scan(n);
+    if (lane < warps) hist[g * warps + lane] = s - n;
+    if (lane == 31) p.first[g] = s;
   }
   __syncthreads();
-  // places: exclusive sums over the groups (rows, tiles), 1024 groups at a time
-  int rows0 = 0, tiles0 = 0;
+  // places: sums over the groups before (rows up to whole ALIGNs, tiles, cost), 1024 groups at a time
+  int rows0 = 0, tiles0 = 0, cost0 = 0;
   for (int g0 = 0; g0 < groups; g0 += GROUP_THREADS) {
     const int g = g0 + tid;
-    int n = 0;
-    if (g < groups)
-      for (int w = 0; w < warps; ++w) {
-        const int k = hist[w * groups + g];
-        hist[w * groups + g] = n;
-        n += k;
-      }
-    const int tiles = (n + TILE - 1) / TILE;
-    int rs = n, ts = tiles;
-    for (int d = 1; d < 32; d <<= 1) {
-      const int r = __shfl_up_sync(0xFFFFFFFFu, rs, d), t = __shfl_up_sync(0xFFFFFFFFu, ts, d);
-      if (lane >= d) rs += r, ts += t;
-    }
-    if (lane == 31) part[0][warp] = rs, part[1][warp] = ts;
+    const int n = g < groups ? p.first[g] : 0;
+    const int full = n / TILE, rest = n - full * TILE;
+    const int up = (n + ALIGN - 1) / ALIGN * ALIGN, tiles = full + (rest > 0);
+    const int cost = full * tile_cost(TILE) + (rest > 0 ? tile_cost(rest) : 0);
+    int rs = warp_scan(up), ts = warp_scan(tiles), cs = warp_scan(cost);
+    if (lane == 31) part[0][warp] = rs, part[1][warp] = ts, part[2][warp] = cs;
     __syncthreads();
-    if (warp == 0) {
-      int r = part[0][lane], t = part[1][lane];
-      for (int d = 1; d < 32; d <<= 1) {
-        const int a = __shfl_up_sync(0xFFFFFFFFu, r, d), b = __shfl_up_sync(0xFFFFFFFFu, t, d);
-        if (lane >= d) r += a, t += b;
-      }
-      part[0][lane] = r, part[1][lane] = t;
-    }
+    if (warp < 3) part[warp][lane] = warp_scan(part[warp][lane]);
     __syncthreads();
-    const int r0 = rows0 + (warp ? part[0][warp - 1] : 0) + rs - n, t0 = tiles0 + (warp ? part[1][warp - 1] : 0) + ts - tiles;
+    if (warp) rs += part[0][warp - 1], ts += part[1][warp - 1], cs += part[2][warp - 1];
     if (g < groups) {
-      for (int w = 0; w < warps; ++w) hist[w * groups + g] += r0;
+      const int r0 = rows0 + rs - up, t0 = tiles0 + ts - tiles, c0 = cost0 + cs - cost;
       p.first[g] = r0;
-      for (int i = 0; i < tiles; ++i) p.tiles[t0 + i] = {g < G ? g : -1, r0 + i * TILE, min(TILE, n - i * TILE), 0};
+      for (int w = 0; w < warps; ++w) hist[g * warps + w] += r0;
+      for (int i = 0; i < tiles; ++i)
+        p.tiles[t0 + i] = {g < G ? g : -1, r0 + i * TILE, min(TILE, n - i * TILE), c0 + i * tile_cost(TILE)};
+      for (int i = n; i < up; ++i) p.rows[r0 + i] = -1;
+      if (g == G) {
+        p.first[groups] = r0 + up;
+        p.sums[0] = t0;
+        p.sums[1] = t0 + tiles;
+        p.sums[2] = c0 + cost;
+      }
     }
     rows0 += part[0][31];
     tiles0 += part[1][31];
+    cost0 += part[2][31];
     __syncthreads();
   }
-  if (tid == 0) {
-    p.first[groups] = rows0;
-    *p.n_tiles = tiles0;
-  }
-  for (int b = lo; b < hi; b += 32) {
-    const bool ok = b + lane < hi;
-    const uint32_t act = __ballot_sync(0xFFFFFFFFu, ok);
-    int a = 0, at = 0;
-    uint32_t same = 0;
-    if (ok) {
-      a = group_of(b + lane);
-      same = __match_any_sync(act, a);
-      at = mine[a];
-      p.rows[at + __popc(same & ((1u << lane) - 1))] = b + lane;
+  each([&](int row, int a, uint32_t same) {
+    int at = 0;
+    if (a >= 0) {
+      at = hist[a * warps + warp];
+      p.rows[at + __popc(same & below)] = row;
     }
     __syncwarp();
-    if (ok && (same & ((1u << lane) - 1)) == 0) mine[a] = at + __popc(same);
+    if (a >= 0 && (same & below) == 0) hist[a * warps + warp] = at + __popc(same);
     __syncwarp();
-  }
+  });
 }
 
 // ---------------------------------------------------------------------------
-// k_shrink and k_wgrad: the common pipeline
+// k_shrink: cluster (tile), its CTAs share K.  Warps 0 to 3 load 32 rows each
+// and write out, warp 4 issues the MMAs.
 // ---------------------------------------------------------------------------
-// RB: the rank's operand rows (64 or 128) that a stage has room for.
-template <int RB>
-struct Ring {
-  static constexpr int STAGES = RB == 64 ? 4 : 3;
-  static constexpr int A_BYTES = TILE * 128, B_BYTES = RB * 128, STAGE = A_BYTES + B_BYTES;
-  static constexpr int BYTES = STAGES * STAGE + 1024;
-};
+constexpr int SHRINK_THREADS = 160, SHRINK_STAGES = 3;
+__host__ __device__ constexpr int shrink_stage(int rp) { return TILE * 128 + rp * 128; }
+constexpr int shrink_bytes(int rp) {  // (the ring holds the sums in the end: 512 rp bytes)
+  return (SHRINK_STAGES * shrink_stage(rp) > 512 * rp ? SHRINK_STAGES * shrink_stage(rp) : 512 * rp) + 1024;
+}
 struct Bars {
   uint64_t full[4], empty[4], done;
-  int abort;
+  int abort, never;  // (never raised: for the waits that go on after an abort)
   uint32_t tmem;
 };
-
 // Columns of tensor memory for an accumulator of rp columns (a power of two, at least 32).
 __device__ __forceinline__ uint32_t tmem_cols(int rp) { return rp <= 32 ? 32 : rp <= 64 ? 64 : 128; }
 
-// The loaders' side: fill(i, stage address) issues the copies of step i.
-template <int STAGES, class Fill>
-__device__ __forceinline__ void produce(Bars& b, uint32_t ring, int stage_bytes, int steps, const WaitGuard& g, Fill fill) {
-  constexpr int LAG = STAGES - 1;
-  int i = 0;
-  for (; i < steps; ++i) {
-    const int st = i % STAGES;
-    if (i >= STAGES && !mbar_wait(&b.empty[st], (i / STAGES - 1) & 1, g)) break;
-    fill(i, ring + st * stage_bytes);
-    cp_commit();
-    if (i >= LAG) {
-      cp_wait<LAG>();
-      fence_async_shared();
-      mbar_arrive(&b.full[(i - LAG) % STAGES]);
-    }
-  }
-  cp_wait<0>();
-  fence_async_shared();
-  if (i == steps)
-    for (int k = max(0, steps - LAG); k < steps; ++k) mbar_arrive(&b.full[k % STAGES]);
+__device__ __forceinline__ uint2 pack4(float4 s, float f) {
+  return make_uint2(pack_bf16x2(s.x * f, s.y * f), pack_bf16x2(s.z * f, s.w * f));
 }
 
-// Adds the cluster's accumulators [128][rp] (partial: this CTA's copy, as
-// float4 [rp/4][128]) and hands each sum of four neighbouring rank elements to
-// put(lane of the tile, first rank element, sum).
-template <class Put>
-__device__ __forceinline__ void cluster_reduce(uint32_t partial, int rp, Put put) {
+// X [T][K] (and as a tensor map, boxes of 64 columns x 32 rows), P as a map
+// of boxes 64 x rp.  h [T][r] (nullable) by row, hs in the grouped order; also
+// (other, nullable [T][r]) copied into that order as others.
+__global__ void __launch_bounds__(SHRINK_THREADS) k_shrink(const __grid_constant__ CUtensorMap mx,
+                                                           const __grid_constant__ CUtensorMap mp,
+                                                           const __nv_bfloat16* __restrict__ X,
+                                                           const float* __restrict__ scale, int K, int r, int rp, Plan plan,
+                                                           __nv_bfloat16* __restrict__ h, __nv_bfloat16* __restrict__ hs,
+                                                           const __nv_bfloat16* __restrict__ other,
+                                                           __nv_bfloat16* __restrict__ others, uint64_t limit_ns,
+                                                           int32_t* status) {
+  extern __shared__ unsigned char smem_[];
+  unsigned char* smem = aligned_smem(smem_);
+  __shared__ Bars b;
+  __shared__ int rows[TILE];
   const uint32_t size = cluster_size(), rank = cluster_ctarank();
-  const int lanes = TILE / size;
-  for (int i = threadIdx.x; i < lanes * (rp / 4); i += LOADERS) {
-    const int l = rank * lanes + i % lanes, q = i / lanes;
-    const uint32_t at = partial + (q * TILE + l) * 16;
-    float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    for (uint32_t c = 0; c < size; ++c) {
-      const float4 v = ld_cluster(mapa_shared(at, c));
-      s.x += v.x, s.y += v.y, s.z += v.z, s.w += v.w;
-    }
-    put(l, q * 4, s);
+  const int tile = blockIdx.x / size, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  launch_dependents();
+  wait_for_primary();
+  if (tile >= plan.sums[1]) return;  // (the whole cluster)
+  const Tile t = plan.tiles[tile];
+  const int up = (t.count + ALIGN - 1) / ALIGN * ALIGN;
+  if (threadIdx.x < TILE) rows[threadIdx.x] = threadIdx.x < up ? plan.rows[t.start + threadIdx.x] : -1;
+  if (t.adapter < 0) {  // rows without an adapter
+    __syncthreads();
+    if (h)
+      for (int i = threadIdx.x + rank * SHRINK_THREADS; i < t.count * (r / 8); i += SHRINK_THREADS * size)
+        *reinterpret_cast<uint4*>(h + (size_t)rows[i / (r / 8)] * r + (i % (r / 8)) * 8) = make_uint4(0, 0, 0, 0);
+    return;
   }
-}
-
-// The accumulator to shared memory, by the four loader warps.
-__device__ __forceinline__ void spill(uint32_t tmem, unsigned char* partial, int rp, bool any) {
-  const int lane = threadIdx.x;  // the accumulator's lane of this thread (warp w holds 32 w ..)
-  for (int c = 0; c < rp; c += 32) {
-    float v[32];
-    if (any) {
-      tmem_ld32(tmem + ((uint32_t)(threadIdx.x & 96) << 16) + c, v);
-    } else {
-#pragma unroll
-      for (int i = 0; i < 32; ++i) v[i] = 0.0f;
-    }
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (c + 4 * i < rp)
-        *reinterpret_cast<float4*>(partial + (((c >> 2) + i) * TILE + lane) * 16) =
-            make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
-  }
-}
-
-// The dynamic shared memory from its first multiple of 1024 bytes on (the
-// swizzle's period; 1024 bytes more are asked for).
-__device__ __forceinline__ unsigned char* aligned_smem(unsigned char* p) { return p + ((0u - smem_u32(p)) & 1023u); }
-
-template <int RB>
-__device__ __forceinline__ void begin(Bars& b, int rp) {
   if (threadIdx.x == 0) {
-    for (int i = 0; i < Ring<RB>::STAGES; ++i) {
-      mbar_init(&b.full[i], LOADERS);
+    for (int i = 0; i < SHRINK_STAGES; ++i) {
+      mbar_init(&b.full[i], 4);
       mbar_init(&b.empty[i], 1);
     }
     mbar_init(&b.done, 1);
-    b.abort = 0;
+    b.abort = b.never = 0;
     fence_barrier_init();
   }
-  if (threadIdx.x >= LOADERS) {
+  if (warp == 4) {
     tmem_alloc(&b.tmem, tmem_cols(rp));
     tmem_relinquish();
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-}
-
-// The MMA warp's side; step(i, stage address, accumulate) issues step i.
-template <int STAGES, class Step>
-__device__ __forceinline__ void consume(Bars& b, uint32_t ring, int stage_bytes, int steps, const WaitGuard& g, Step step) {
-  if ((threadIdx.x & 31) == 0) {
-    for (int i = 0; i < steps; ++i) {
-      const int st = i % STAGES;
-      if (!mbar_wait(&b.full[st], (i / STAGES) & 1, g)) break;
-      tc_fence_after();
-      step(i, ring + st * stage_bytes);
-      tc_commit(&b.empty[st]);
-    }
-    tc_commit(&b.done);
-  }
-  __syncwarp();
-}
-
-__device__ __forceinline__ uint2 pack4(float4 s, float f) {
-  return make_uint2(pack_bf16x2(s.x * f, s.y * f), pack_bf16x2(s.z * f, s.w * f));
-}
-
-// Cluster (tile): h rows of one tile.  X [T][K], P [G][r][K].
-template <int RB>
-__global__ void __launch_bounds__(THREADS) k_shrink(const __nv_bfloat16* __restrict__ X, const __nv_bfloat16* __restrict__ P,
-                                                    const float* __restrict__ scale, int K, int r, int rp, Plan plan,
-                                                    __nv_bfloat16* __restrict__ h, uint64_t limit_ns, int32_t* status) {
-  extern __shared__ unsigned char smem_[];
-  unsigned char* smem = aligned_smem(smem_);
-  __shared__ Bars b;
-  __shared__ int rows[TILE];
-  const uint32_t size = cluster_size(), rank = cluster_ctarank();
-  const int tile = blockIdx.x / size;
-  launch_dependents();
-  wait_for_primary();
-  if (tile >= *plan.n_tiles) return;  // (the whole cluster)
-  const Tile t = plan.tiles[tile];
-  if (threadIdx.x < TILE) rows[threadIdx.x] = threadIdx.x < t.count ? plan.rows[t.start + threadIdx.x] : 0;
-  if (t.adapter < 0) {  // rows without an adapter
-    __syncthreads();
-    for (int i = threadIdx.x + rank * THREADS; i < t.count * (r / 8); i += THREADS * size)
-      *reinterpret_cast<uint4*>(h + (size_t)rows[i / (r / 8)] * r + (i % (r / 8)) * 8) = make_uint4(0, 0, 0, 0);
-    return;
-  }
-  begin<RB>(b, rp);
   const WaitGuard g{&b.abort, status, limit_ns};
-  const uint32_t ring = smem_u32(smem);
+  const uint32_t ring = smem_u32(smem), stage = shrink_stage(rp);
   const int blocks = (K + KB - 1) / KB;
   const int k0 = (int)((int64_t)blocks * rank / size), steps = (int)((int64_t)blocks * (rank + 1) / size) - k0;
-  using R = Ring<RB>;
-  if (threadIdx.x < LOADERS) {
-    const int c = threadIdx.x & 7, row0 = threadIdx.x >> 3;
-    const __nv_bfloat16* src[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) src[i] = X + (size_t)rows[row0 + 16 * i] * K + c * 8;
-    const __nv_bfloat16* p = P + (size_t)t.adapter * r * K + c * 8;
-    produce<R::STAGES>(b, ring, R::STAGE, steps, g, [&](int i, uint32_t at) {
-      const int k = (k0 + i) * KB;
-      const bool in = k + c * 8 < K;
-#pragma unroll
-      for (int j = 0; j < 8; ++j)
-        if (row0 + 16 * j < t.count) cp16(piece(at, row0 + 16 * j, c), in ? src[j] + k : X, in);
-      for (int j = row0; j < r; j += 16) cp16(piece(at + R::A_BYTES, j, c), in ? p + (size_t)j * K + k : P, in);
-    });
-  } else {
-    const uint32_t idesc = idesc_bf16_f32(TILE, rp);
-    consume<R::STAGES>(b, ring, R::STAGE, steps, g, [&](int i, uint32_t at) {
-#pragma unroll
-      for (int k = 0; k < KB / 16; ++k)
-        umma_bf16(b.tmem, sdesc_kmajor_sw128(at + 32 * k), sdesc_kmajor_sw128(at + R::A_BYTES + 32 * k), idesc, i + k > 0);
-    });
-  }
-  mbar_wait(&b.done, 0, g);
-  tc_fence_after();
-  __syncthreads();  // (every copy has landed and every MMA has read: the ring is free)
-  if (threadIdx.x < LOADERS) spill(b.tmem, smem, rp, steps > 0);
-  tc_fence_before();
-  cluster_sync();
-  if (threadIdx.x < LOADERS && !b.abort) {
-    const float s = scale[t.adapter];
-    cluster_reduce(ring, rp, [&](int l, int q, float4 v) {
-      if (l < t.count && q < r) *reinterpret_cast<uint2*>(h + (size_t)rows[l] * r + q) = pack4(v, s);
-    });
-  }
-  cluster_sync();  // (the other CTAs have read this one's sums)
-  if (threadIdx.x >= LOADERS) {
-    tc_fence_after();
-    tmem_dealloc(b.tmem, tmem_cols(rp));
-  }
-}
-
-// Cluster (adapter, 128 columns of X [T][C]): dP [G][r][C] = U^T X over the
-// adapter's rows, U [T][r].
-template <int RB>
-__global__ void __launch_bounds__(THREADS) k_wgrad(const __nv_bfloat16* __restrict__ X, const __nv_bfloat16* __restrict__ U,
-                                                   int C, int r, int rp, Plan plan, __nv_bfloat16* __restrict__ dP,
-                                                   uint64_t limit_ns, int32_t* status) {
-  extern __shared__ unsigned char smem_[];
-  unsigned char* smem = aligned_smem(smem_);
-  __shared__ Bars b;
-  const uint32_t size = cluster_size(), rank = cluster_ctarank();
-  const int chunks = (C + TILE - 1) / TILE, unit = blockIdx.x / size, adapter = unit / chunks;
-  const int c0 = (unit - adapter * chunks) * TILE;
-  launch_dependents();
-  wait_for_primary();
-  const int first = plan.first[adapter], n = plan.first[adapter + 1] - first;
-  begin<RB>(b, rp);
-  const WaitGuard g{&b.abort, status, limit_ns};
-  const uint32_t ring = smem_u32(smem);
-  const int blocks = (n + KB - 1) / KB;
-  const int k0 = (int)((int64_t)blocks * rank / size), steps = (int)((int64_t)blocks * (rank + 1) / size) - k0;
-  using R = Ring<RB>;
-  if (threadIdx.x < LOADERS) {
-    const int c = threadIdx.x & 15, row0 = threadIdx.x >> 4;
-    const bool col = c0 + c * 8 < C;
-    const int pieces = rp / 8;
-    produce<R::STAGES>(b, ring, R::STAGE, steps, g, [&](int i, uint32_t at) {
-      const int base = (k0 + i) * KB;
+  if (warp < 4) {
+    const Slab s = slab_of(rows[threadIdx.x]);
+    const uint32_t slab = warp * SLAB * 128;
+    int issued = 0;
+    if (s.count == 0 || (s.box && s.count >= MIN_BOX)) {
+      if (lane == 0)
+        for (int i = 0; i < steps; ++i) {
+          const int st = i % SHRINK_STAGES;
+          if (i >= SHRINK_STAGES && !mbar_wait(&b.empty[st], (i / SHRINK_STAGES - 1) & 1, g)) break;
+          const uint32_t at = ring + st * stage;
+          mbar_arrive_expect_tx(&b.full[st], (s.count ? SLAB * 128 : 0) + (warp == 0 ? rp * 128 : 0));
+          if (s.count) tma_2d(at + slab, &mx, &b.full[st], (k0 + i) * KB, s.first);
+          if (warp == 0) tma_3d(at + TILE * 128, &mp, &b.full[st], (k0 + i) * KB, 0, t.adapter);
+          ++issued;
+        }
+    } else {
+      // row by row: eight lanes copy a row's 128 bytes, and arrive two steps later, when they have landed
+      const int c = lane & 7;
+      const __nv_bfloat16* src[8];
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        const int row = row0 + 8 * j;
-        const bool in = col && base + row < n;
-        const __nv_bfloat16* s = in ? X + (size_t)plan.rows[first + base + row] * C + c0 + c * 8 : X;
-        cp16(piece(at + (c >> 3) * (KB * 128), row, c & 7), s, in);
+        const int row = __shfl_sync(0xFFFFFFFFu, s.row, (lane >> 3) + 4 * j);
+        src[j] = row >= 0 ? X + (size_t)row * K + c * 8 : nullptr;
       }
-      for (int j = threadIdx.x; j < KB * pieces; j += LOADERS) {
-        const int row = j / pieces, q = j - row * pieces;
-        const bool in = base + row < n && q * 8 < r;
-        const __nv_bfloat16* s = in ? U + (size_t)plan.rows[first + base + row] * r + q * 8 : U;
-        cp16(piece(at + R::A_BYTES + (q >> 3) * (KB * 128), row, q & 7), s, in);
-      }
-    });
-  } else {
-    const uint32_t idesc = idesc_bf16_f32(TILE, rp) | A_MN | B_MN;
-    consume<R::STAGES>(b, ring, R::STAGE, steps, g, [&](int i, uint32_t at) {
+      constexpr int LAG = SHRINK_STAGES - 1;
+      int i = 0;
+      for (; i < steps; ++i) {
+        const int st = i % SHRINK_STAGES;
+        if (i >= SHRINK_STAGES && !mbar_wait(&b.empty[st], (i / SHRINK_STAGES - 1) & 1, g)) break;
+        const uint32_t at = ring + st * stage;
+        const int k = (k0 + i) * KB;
+        if (warp == 0 && lane == 0) {
+          mbar_expect_tx(&b.full[st], rp * 128);
+          tma_3d(at + TILE * 128, &mp, &b.full[st], k, 0, t.adapter);
+          ++issued;
+        }
+        const bool in = k + c * 8 < K;
 #pragma unroll
-      for (int k = 0; k < KB / 16; ++k)
-        umma_bf16(b.tmem, sdesc_mnmajor_sw128(at + 2048 * k, KB * 128),
-                  sdesc_mnmajor_sw128(at + R::A_BYTES + 2048 * k, KB * 128), idesc, i + k > 0);
-    });
+        for (int j = 0; j < 8; ++j)
+          if (src[j]) cp16(piece(at + slab, (lane >> 3) + 4 * j, c), in ? src[j] + k : X, in);
+        cp_commit();
+        if (i >= LAG) {
+          cp_wait<LAG>();
+          fence_async_shared();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&b.full[(i - LAG) % SHRINK_STAGES]);
+        }
+      }
+      cp_wait<0>();
+      fence_async_shared();
+      __syncwarp();
+      if (lane == 0 && i == steps)
+        for (int k = max(0, steps - LAG); k < steps; ++k) mbar_arrive(&b.full[k % SHRINK_STAGES]);
+    }
+    if (b.abort && lane == 0) settle(b.full, SHRINK_STAGES, issued, &b.never);
+    __syncwarp();
+  } else {
+    if (lane == 0) {
+      const uint32_t idesc = idesc_bf16_f32(TILE, rp);
+      for (int i = 0; i < steps; ++i) {
+        const int st = i % SHRINK_STAGES;
+        if (!mbar_wait(&b.full[st], (i / SHRINK_STAGES) & 1, g)) break;
+        tc_fence_after();
+        const uint32_t at = ring + st * stage;
+#pragma unroll
+        for (int k = 0; k < KB / 16; ++k)
+          umma_bf16(b.tmem, sdesc_kmajor(at + 32 * k, 128), sdesc_kmajor(at + TILE * 128 + 32 * k, 128), idesc, i + k > 0);
+        tc_commit(&b.empty[st]);
+      }
+      tc_commit(&b.done);
+    }
+    __syncwarp();
   }
-  mbar_wait(&b.done, 0, g);
+  if (warp == 4) mbar_wait(&b.done, 0, WaitGuard{&b.never, status, limit_ns});
+  tc_fence_before();
+  __syncthreads();  // (every copy has landed and every MMA has read: the ring is free)
   tc_fence_after();
-  __syncthreads();
-  if (threadIdx.x < LOADERS) spill(b.tmem, smem, rp, steps > 0);
+  // the sums to shared memory, as float4 [rp / 4][128]
+  if (warp < 4 && !b.abort) {
+    for (int c = 0; c < rp; c += 32) {
+      float v[32];
+      if (steps > 0) {
+        tmem_ld32(b.tmem + ((uint32_t)(32 * warp) << 16) + c, v);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 32; ++i) v[i] = 0.0f;
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (c + 4 * i < rp)
+          *reinterpret_cast<float4*>(smem + (((c >> 2) + i) * TILE + threadIdx.x) * 16) =
+              make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+    }
+  }
   tc_fence_before();
   cluster_sync();
-  if (threadIdx.x < LOADERS && !b.abort) {
-    __nv_bfloat16* out = dP + (size_t)adapter * r * C + c0;
-    cluster_reduce(ring, rp, [&](int l, int q, float4 v) {
-      if (c0 + l >= C) return;
-      const float w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-        if (q + j < r) out[(size_t)(q + j) * C + l] = __float2bfloat16_rn(w[j]);
-    });
+  if (!b.abort) {
+    const float f = scale[t.adapter];
+    const int quads = r / 4, items = up * quads;
+    for (int i = threadIdx.x + rank * SHRINK_THREADS; i < items; i += SHRINK_THREADS * size) {
+      const int q = i / up, l = i - q * up;
+      const uint32_t at = ring + (q * TILE + l) * 16;
+      float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      if (l < t.count)
+        for (uint32_t c = 0; c < size; ++c) {
+          const float4 v = ld_cluster(mapa_shared(at, c));
+          s.x += v.x, s.y += v.y, s.z += v.z, s.w += v.w;
+        }
+      const uint2 o = pack4(s, l < t.count ? f : 0.0f);
+      if (h && l < t.count) *reinterpret_cast<uint2*>(h + (size_t)rows[l] * r + q * 4) = o;
+      *reinterpret_cast<uint2*>(hs + (size_t)(t.start + l) * r + q * 4) = l < t.count ? o : make_uint2(0, 0);
+      if (other)
+        *reinterpret_cast<uint2*>(others + (size_t)(t.start + l) * r + q * 4) =
+            l < t.count ? *reinterpret_cast<const uint2*>(other + (size_t)rows[l] * r + q * 4) : make_uint2(0, 0);
+    }
   }
-  cluster_sync();
-  if (threadIdx.x >= LOADERS) {
+  cluster_sync();  // (the other CTAs have read this one's sums)
+  if (warp == 4) {
     tc_fence_after();
     tmem_dealloc(b.tmem, tmem_cols(rp));
   }
 }
 
 // ---------------------------------------------------------------------------
-// k_expand: y = base + h Q, persistent over (tile, 128 columns)
+// k_wgrad: cluster (128 columns of X [T][C]), its CTAs share the grouped rows,
+// all adapters: dP [G][r][C] = U^T X over each adapter's rows, U in the
+// grouped order.  The rows of an adapter that cross from one CTA's share into
+// the next ones' are summed by the CTA in which they begin.
+// Warps 0 to 3 load (32 rows x 64 columns each), 4 issues the MMAs, 5 to 8
+// write out; two accumulators.
 // ---------------------------------------------------------------------------
-template <int RB>
-struct Wide {
-  static constexpr int STAGES = RB == 32 ? 4 : RB == 64 ? 3 : 2;
-  static constexpr int BASE = TILE * 256, Q_BYTES = RB * 256, H_BYTES = TILE * 128 * (RB > 64 ? 2 : 1);
-  static constexpr int STAGE = BASE + Q_BYTES + H_BYTES, BYTES = STAGES * STAGE + 1024;
-};
-struct WideBars {
-  uint64_t full[4], empty[4], acc_full[2], acc_empty[2];
-  int abort;
-  uint32_t tmem;
-};
-constexpr int WIDE_THREADS = 288;  // 4 warps copy, 4 write out, 1 issues the MMAs
+constexpr int WGRAD_THREADS = 288, BATCH = 128;  // steps whose descriptions are looked up together
+__host__ __device__ constexpr int wgrad_stages(int rp) { return rp <= 16 ? 3 : rp <= 32 ? 4 : rp <= 64 ? 3 : 4; }
+__host__ __device__ constexpr int wgrad_stage(int rp) { return KB * 256 + KB * rank_bytes(rp); }
+constexpr int wgrad_bytes(int rp) { return wgrad_stages(rp) * wgrad_stage(rp) + 512 * rp + 1024; }
 
-template <int RB>
-__global__ void __launch_bounds__(WIDE_THREADS) k_expand(const __nv_bfloat16* __restrict__ H,
-                                                         const __nv_bfloat16* __restrict__ Q, const __nv_bfloat16* base,
-                                                         int N, int r, int rp, Plan plan, __nv_bfloat16* y,
-                                                         uint64_t limit_ns, int32_t* status) {
+struct Step {
+  int start, count, adapter;  // up to 64 places of one adapter; a count of 0: no step
+  int flags;
+};
+// the first / last step of a run of one adapter in this CTA; the run began before it / goes on behind it
+enum { RUN_BEGINS = 1, RUN_ENDS = 2, FROM_BEFORE = 4, GOES_ON = 8 };
+
+__global__ void __launch_bounds__(WGRAD_THREADS) k_wgrad(const __grid_constant__ CUtensorMap mx,
+                                                         const __grid_constant__ CUtensorMap mu,
+                                                         const __nv_bfloat16* __restrict__ X, int C, int r, int rp, int G,
+                                                         Plan plan, __nv_bfloat16* __restrict__ dP, uint64_t limit_ns,
+                                                         int32_t* status) {
   extern __shared__ unsigned char smem_[];
   unsigned char* smem = aligned_smem(smem_);
-  __shared__ WideBars b;
-  using R = Wide<RB>;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  __shared__ uint64_t full[4], empty[4], acc_full[2], acc_empty[2], done;
+  __shared__ int abort_, never, head_adapter, head_through, tail_adapter;
+  __shared__ uint32_t tmem_;
+  __shared__ Step steps[BATCH];
+  const uint32_t size = cluster_size(), rank = cluster_ctarank();
+  const int c0 = (int)(blockIdx.x / size) * TILE, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int stages = wgrad_stages(rp);
+  const uint32_t ring = smem_u32(smem), stage = wgrad_stage(rp), acc_cols = tmem_cols(rp);
+  unsigned char* head = smem + stages * stage;  // float4 [rp / 4][128]: the run from before, for its owner
   if (threadIdx.x == 0) {
-    for (int i = 0; i < R::STAGES; ++i) {
-      mbar_init(&b.full[i], LOADERS);
-      mbar_init(&b.empty[i], 4);
+    for (int i = 0; i < stages; ++i) {
+      mbar_init(&full[i], 4);
+      mbar_init(&empty[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&b.acc_full[i], 1);
-      mbar_init(&b.acc_empty[i], 4);
+      mbar_init(&acc_full[i], 1);
+      mbar_init(&acc_empty[i], 4);
     }
-    b.abort = 0;
+    mbar_init(&done, 1);
+    abort_ = never = head_through = 0;
+    head_adapter = tail_adapter = -1;
     fence_barrier_init();
   }
-  if (warp == 8) {
-    tmem_alloc(&b.tmem, 256);
+  if (warp == 4) {
+    tmem_alloc(&tmem_, 2 * acc_cols);
     tmem_relinquish();
   }
   tc_fence_before();
@@ -482,136 +507,427 @@ __global__ void __launch_bounds__(WIDE_THREADS) k_expand(const __nv_bfloat16* __
   tc_fence_after();
   launch_dependents();
   wait_for_primary();
-  const WaitGuard g{&b.abort, status, limit_ns};
-  const uint32_t ring = smem_u32(smem);
-  const int chunks = (N + TILE - 1) / TILE, tiles = *plan.n_tiles;
-  const int64_t units = (int64_t)tiles * chunks;
-  const int n = units > blockIdx.x ? (int)((units - blockIdx.x + gridDim.x - 1) / gridDim.x) : 0;
-  // unit i of this CTA: neighbours in time on the GPU are tiles of the same columns
-  auto unit = [&](int i, Tile& t, int& c0) {
-    const int64_t u = blockIdx.x + (int64_t)i * gridDim.x;
-    const int chunk = (int)(u / tiles);
-    t = plan.tiles[u - (int64_t)chunk * tiles];
-    c0 = chunk * TILE;
-  };
-  if (warp < 4) {
-    constexpr int LAG = R::STAGES - 1;
-    const int c = threadIdx.x & 15, row0 = threadIdx.x >> 4;
-    const int pieces = rp / 8;
-    int i = 0;
-    for (; i < n; ++i) {
-      const int st = i % R::STAGES;
-      const uint32_t at = ring + st * R::STAGE;
-      if (i >= R::STAGES && !mbar_wait(&b.empty[st], (i / R::STAGES - 1) & 1, g)) break;
-      Tile t;
-      int c0;
-      unit(i, t, c0);
-      const int* rows = plan.rows + t.start;
-      const bool col = c0 + c * 8 < N;
-      if (t.adapter >= 0) {
-        for (int j = threadIdx.x; j < t.count * pieces; j += LOADERS) {
-          const int row = j / pieces, q = j - row * pieces;
-          const bool in = q * 8 < r;
-          cp16(piece(at + R::BASE + R::Q_BYTES + (q >> 3) * (TILE * 128), row, q & 7),
-               in ? H + (size_t)rows[row] * r + q * 8 : H, in);
+  const WaitGuard g{&abort_, status, limit_ns};
+  const uint32_t tmem = tmem_;
+  const int tiles = plan.sums[0];
+  auto share = [&](int c) { return (int)((int64_t)2 * tiles * c / (int)size); };  // halves of tiles before CTA c's
+  const int lo = share(rank), hi = share(rank + 1);
+  if (warp >= 5 && c0 + 4 * lane < C)  // adapters without rows
+    for (int a = rank + size * (warp - 5); a < G; a += 4 * size)
+      if (plan.first[a] == plan.first[a + 1])
+        for (int j = 0; j < r; ++j) *reinterpret_cast<uint2*>(dP + ((size_t)a * r + j) * C + c0 + 4 * lane) = make_uint2(0, 0);
+  __syncwarp();
+  int i = 0, run = 0;  // steps and runs so far, counted by every role for itself
+  bool before = false, alive = true;
+  for (int b0 = lo; b0 < hi; b0 += BATCH) {
+    const int m = min(BATCH, hi - b0);
+    __syncthreads();
+    if ((int)threadIdx.x < m) {
+      const int hh = b0 + threadIdx.x, ti = hh >> 1, second = hh & 1;
+      const Tile t = plan.tiles[ti];
+      Step s;
+      s.start = t.start + second * KB;
+      s.count = max(0, min(KB, t.count - second * KB));
+      s.adapter = t.adapter;
+      const bool begins = !second && (ti == 0 || plan.tiles[ti - 1].adapter != t.adapter);
+      const bool ends = (second || t.count <= KB) && (ti + 1 == tiles || plan.tiles[ti + 1].adapter != t.adapter);
+      s.flags = (begins || hh == lo ? RUN_BEGINS : 0) | (ends || hh + 1 == hi ? RUN_ENDS : 0) |
+                (!begins && hh == lo ? FROM_BEFORE : 0) | (!ends && hh + 1 == hi ? GOES_ON : 0);
+      steps[threadIdx.x] = s;
+    }
+    __syncthreads();
+    if (warp < 4) {
+      const int slab = warp & 1, block = warp >> 1, c = lane & 7;
+      const bool cols = c0 + 64 * block < C;
+      auto row_at = [&](int j) {  // this lane's row of step j
+        const int at = SLAB * slab + lane;
+        return j < m && at < steps[j].count ? plan.rows[steps[j].start + at] : -1;
+      };
+      int row = row_at(0);
+      for (int j = 0; j < m && alive; ++j) {
+        const Step s = steps[j];
+        const Slab q = slab_of(row);
+        row = row_at(j + 1);
+        if (s.count == 0) continue;
+        const int st = i % stages;
+        if (i >= stages) alive = __all_sync(0xFFFFFFFFu, mbar_wait(&empty[st], (i / stages - 1) & 1, g));
+        if (!alive) break;
+        const uint32_t at = ring + st * stage, dst = at + block * (KB * 128) + slab * (SLAB * 128);
+        const int up = (s.count + ALIGN - 1) / ALIGN * ALIGN - SLAB * slab;  // rows of the slab that the MMAs read
+        const bool box = cols && q.box && q.count == SLAB;
+        if (lane == 0) {
+          const uint32_t bytes = (box ? SLAB * 128 : 0) + (warp == 0 ? KB * rank_bytes(rp) : 0);
+          if (bytes) mbar_expect_tx(&full[st], bytes);
+          if (box) tma_2d(dst, &mx, &full[st], c0 + 64 * block, q.first);
+          if (warp == 0) {
+            tma_2d(at + KB * 256, &mu, &full[st], 0, s.start);
+            if (rp > 64) tma_2d(at + KB * 256 + KB * 128, &mu, &full[st], 64, s.start);
+          }
         }
-        const __nv_bfloat16* q = Q + (size_t)t.adapter * r * N + c0 + c * 8;
-        for (int j = row0; j < rp; j += 8)
-          cp16(piece(at + R::BASE + (c >> 3) * (rp * 128), j, c & 7), col && j < r ? q + (size_t)j * N : Q, col && j < r);
+        if (!box) {
+          // row by row, with zeros where there is no row or no column
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            const int l = (lane >> 3) + 4 * k, id = __shfl_sync(0xFFFFFFFFu, q.row, l), col = c0 + 64 * block + c * 8;
+            const bool in = id >= 0 && col < C;
+            if (l < up) cp16(piece(dst, l, c), in ? X + (size_t)id * C + col : X, in);
+          }
+          cp_commit();
+          cp_wait<0>();
+          fence_async_shared();
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&full[st]);
+        ++i;
       }
-      if (base)
-        for (int j = row0; j < t.count; j += 8)
-          if (col) cp16(piece(at + (c >> 3) * (TILE * 128), j, c & 7), base + (size_t)rows[j] * N + c0 + c * 8, true);
-      cp_commit();
-      if (i >= LAG) {
-        cp_wait<LAG>();
-        fence_async_shared();
-        mbar_arrive(&b.full[(i - LAG) % R::STAGES]);
+    } else if (warp == 4) {
+      if (lane == 0) {
+        const uint32_t urow = rp > 64 ? 128 : rank_bytes(rp), idesc = idesc_bf16_f32(TILE, rp) | A_MN | B_MN;
+        for (int j = 0; j < m && alive; ++j) {
+          const Step s = steps[j];
+          if (s.count == 0) continue;
+          const int st = i % stages, acc = run & 1;
+          alive = mbar_wait(&full[st], (i / stages) & 1, g);
+          if (alive && (s.flags & RUN_BEGINS) && run >= 2) alive = mbar_wait(&acc_empty[acc], (run / 2 - 1) & 1, g);
+          if (!alive) break;
+          tc_fence_after();
+          const uint32_t at = ring + st * stage;
+          const int ks = (s.count + ALIGN - 1) / ALIGN;
+          for (int k = 0; k < ks; ++k)
+            umma_bf16(tmem + acc * acc_cols, sdesc_mnmajor(at + 2048 * k, 128, KB * 128),
+                      sdesc_mnmajor(at + KB * 256 + ALIGN * urow * k, urow, KB * 128), idesc,
+                      k > 0 || !(s.flags & RUN_BEGINS));
+          tc_commit(&empty[st]);
+          if (s.flags & RUN_ENDS) {
+            tc_commit(&acc_full[acc]);
+            ++run;
+          }
+          ++i;
+        }
+      }
+      __syncwarp();
+    } else {
+      const int quad = warp & 3, l = 32 * quad + lane;  // (a warp reads the tensor-memory lanes of its number modulo 4)
+      for (int j = 0; j < m && alive; ++j) {
+        const Step s = steps[j];
+        if (s.count == 0) continue;
+        if (s.flags & RUN_BEGINS) before = (s.flags & FROM_BEFORE) != 0;
+        if (!(s.flags & RUN_ENDS)) continue;
+        const int acc = run & 1;
+        alive = __all_sync(0xFFFFFFFFu, mbar_wait(&acc_full[acc], (run / 2) & 1, g));
+        if (!alive) break;
+        tc_fence_after();
+        // to the gradient, or to shared memory: head for the CTA in which the run began, the ring (nothing uses it
+        // behind the last step) for this CTA's own last run
+        const bool goes_on = (s.flags & GOES_ON) != 0;
+        unsigned char* keep = before ? head : goes_on ? smem : nullptr;
+        for (int cc = 0; cc < rp; cc += 32) {
+          float v[32];
+          tmem_ld32(tmem + acc * acc_cols + ((uint32_t)(32 * quad) << 16) + cc, v);
+          if (keep) {
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+              if (cc + 4 * k < rp)
+                *reinterpret_cast<float4*>(keep + (((cc >> 2) + k) * TILE + l) * 16) =
+                    make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
+          } else if (c0 + l < C) {
+            __nv_bfloat16* out = dP + ((size_t)s.adapter * r + cc) * C + c0 + l;
+#pragma unroll
+            for (int k = 0; k < 32; ++k)
+              if (cc + k < r) out[(size_t)k * C] = __float2bfloat16_rn(v[k]);
+          }
+        }
+        if (l == 0) {
+          if (before) head_adapter = s.adapter, head_through = goes_on;
+          if (!before && goes_on) tail_adapter = s.adapter;
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&acc_empty[acc]);
+        ++run;
+      }
+    }
+  }
+  if (warp == 4) {
+    if (lane == 0) {
+      tc_commit(&done);
+      mbar_wait(&done, 0, WaitGuard{&never, status, limit_ns});
+    }
+  } else if (warp < 4 && lane == 0 && abort_) {
+    settle(full, stages, i, &never);
+  }
+  __syncwarp();
+  cluster_sync();
+  if (tail_adapter >= 0 && !abort_) {
+    const int a = tail_adapter;
+    int last = rank;  // the last CTA with a part of the run
+    for (int c = rank + 1; c < (int)size; ++c) {
+      if (share(c) == share(c + 1)) continue;
+      if (ld_cluster_int(mapa_shared(smem_u32(&head_adapter), c)) != a) break;
+      last = c;
+      if (!ld_cluster_int(mapa_shared(smem_u32(&head_through), c))) break;
+    }
+    for (int k = threadIdx.x; k < TILE * (r / 4); k += WGRAD_THREADS) {
+      const int l = k % TILE, q = k / TILE;
+      float4 s = *reinterpret_cast<const float4*>(smem + (q * TILE + l) * 16);
+      for (int c = rank + 1; c <= last; ++c) {
+        if (share(c) == share(c + 1)) continue;
+        const float4 v = ld_cluster(mapa_shared(smem_u32(head) + (q * TILE + l) * 16, c));
+        s.x += v.x, s.y += v.y, s.z += v.z, s.w += v.w;
+      }
+      if (c0 + l < C) {
+        __nv_bfloat16* out = dP + ((size_t)a * r + 4 * q) * C + c0 + l;
+        out[0] = __float2bfloat16_rn(s.x);
+        out[(size_t)C] = __float2bfloat16_rn(s.y);
+        out[(size_t)2 * C] = __float2bfloat16_rn(s.z);
+        out[(size_t)3 * C] = __float2bfloat16_rn(s.w);
+      }
+    }
+  }
+  tc_fence_before();
+  cluster_sync();  // (the others have read this CTA's sums)
+  if (warp == 4) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 2 * acc_cols);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// k_expand: y = base + h Q, persistent over units of (tile, 128 columns); a CTA
+// takes neighbouring units, about the same number of 32-row slabs each.
+// Warps 0 to 3 load 32 rows each, 4 to 11 write out 32 rows x 64 columns each,
+// 12 issues the MMAs; two accumulators.
+// ---------------------------------------------------------------------------
+constexpr int EXPAND_THREADS = 416;
+__host__ __device__ constexpr int expand_stages(int rp) { return rp <= 32 ? 4 : rp <= 64 ? 3 : 2; }
+__host__ __device__ constexpr int expand_q(int rp) { return rp * 256; }
+__host__ __device__ constexpr int expand_stage(int rp) { return TILE * 256 + expand_q(rp) + TILE * rank_bytes(rp); }
+constexpr int expand_bytes(int rp) { return expand_stages(rp) * expand_stage(rp) + 1024; }
+
+__global__ void __launch_bounds__(EXPAND_THREADS) k_expand(const __grid_constant__ CUtensorMap mh,
+                                                           const __grid_constant__ CUtensorMap mq,
+                                                           const __grid_constant__ CUtensorMap mb,
+                                                           const __grid_constant__ CUtensorMap my,
+                                                           const __nv_bfloat16* base, int N, int r, int rp, Plan plan,
+                                                           __nv_bfloat16* y, uint64_t limit_ns, int32_t* status) {
+  extern __shared__ unsigned char smem_[];
+  unsigned char* smem = aligned_smem(smem_);
+  __shared__ uint64_t full[4], empty[4], acc_full[2], acc_empty[2], done;
+  __shared__ int abort_, never, begin_tile, begin_chunk;
+  __shared__ uint32_t tmem_;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int stages = expand_stages(rp);
+  const uint32_t ring = smem_u32(smem), stage = expand_stage(rp), q_at = TILE * 256, h_at = q_at + expand_q(rp);
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < stages; ++i) {
+      mbar_init(&full[i], 4 * 32);
+      mbar_init(&empty[i], 8);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&acc_full[i], 1);
+      mbar_init(&acc_empty[i], 8);
+    }
+    mbar_init(&done, 1);
+    abort_ = never = 0;
+    fence_barrier_init();
+  }
+  if (warp == 12) {
+    tmem_alloc(&tmem_, 2 * TILE);
+    tmem_relinquish();
+  }
+  launch_dependents();
+  wait_for_primary();
+  // units in the order (tile, chunk); this CTA's are those whose cost begins in its share of all
+  const int chunks = (N + TILE - 1) / TILE, tiles = plan.sums[1];
+  const int64_t all = (int64_t)plan.sums[2] * chunks;
+  const int64_t lo = all * blockIdx.x / gridDim.x, hi = all * (blockIdx.x + 1) / gridDim.x;
+  for (int i = threadIdx.x; i < tiles; i += EXPAND_THREADS) {
+    const Tile t = plan.tiles[i];
+    const int64_t from = (int64_t)t.cost * chunks, each = tile_cost(t.count);
+    // (the first unit that begins at or behind lo lies in this tile, or at the start of the next)
+    if (from <= lo && lo < from + each * chunks) {
+      const int c = (int)((lo - from + each - 1) / each);
+      begin_tile = c < chunks ? i : i + 1;
+      begin_chunk = c < chunks ? c : 0;
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const WaitGuard g{&abort_, status, limit_ns};
+  const uint32_t tmem = tmem_;
+  struct Walk {  // this CTA's units in turn
+    Tile t, next;
+    int tile, chunk;
+  } w{{}, {}, tiles, 0};
+  auto fetch = [&](int tile) { return tile < tiles ? plan.tiles[tile] : Tile{-1, 0, 0, 0}; };
+  auto more = [&] { return w.tile < tiles && (int64_t)w.t.cost * chunks + (int64_t)w.chunk * tile_cost(w.t.count) < hi; };
+  auto advance = [&] {
+    if (++w.chunk < chunks) return false;
+    w.chunk = 0;
+    w.t = w.next;
+    w.next = fetch(++w.tile + 1);
+    return true;  // another tile
+  };
+  w.tile = lo < hi ? begin_tile : tiles;
+  w.chunk = begin_chunk;
+  w.t = fetch(w.tile);
+  w.next = fetch(w.tile + 1);
+  auto places = [&](const Tile& t, int slab) {  // this lane's row in a slab of the tile
+    const int at = SLAB * slab + lane;
+    return at < t.count ? plan.rows[t.start + at] : -1;
+  };
+  int i = 0;
+  bool alive = true;
+  if (warp < 4) {
+    Slab s = slab_of(places(w.t, warp));
+    int ahead = places(w.next, warp);
+    while (more()) {
+      const int st = i % stages;
+      if (i >= stages) alive = __all_sync(0xFFFFFFFFu, mbar_wait(&empty[st], (i / stages - 1) & 1, g));
+      if (!alive) break;
+      const uint32_t at = ring + st * stage;
+      const int c0 = w.chunk * TILE;
+      const bool two = c0 + 64 < N;  // (the second block of 64 columns has some)
+      const bool product = warp == 0 && w.t.adapter >= 0;
+      const bool box = base && s.count > 0 && s.box && s.count >= MIN_BOX;
+      if (lane == 0) {
+        const uint32_t bytes = (box ? SLAB * 128 * (two ? 2 : 1) : 0) +
+                               (product ? rp * 128 * (two ? 2 : 1) + TILE * rank_bytes(rp) : 0);
+        if (bytes) mbar_expect_tx(&full[st], bytes);
+        if (box) {
+          tma_2d(at + warp * (SLAB * 128), &mb, &full[st], c0, s.first);
+          if (two) tma_2d(at + TILE * 128 + warp * (SLAB * 128), &mb, &full[st], c0 + 64, s.first);
+        }
+        if (product) {
+          tma_2d(at + h_at, &mh, &full[st], 0, w.t.start);
+          if (rp > 64) tma_2d(at + h_at + TILE * 128, &mh, &full[st], 64, w.t.start);
+          tma_3d(at + q_at, &mq, &full[st], c0, 0, w.t.adapter);
+          if (two) tma_3d(at + q_at + rp * 128, &mq, &full[st], c0 + 64, 0, w.t.adapter);
+        }
+      }
+      if (base && !box && s.count > 0) {
+        const int c = lane & 15;
+        for (int l = lane >> 4; l < SLAB; l += 2) {
+          const int id = __shfl_sync(0xFFFFFFFFu, s.row, l);
+          if (id >= 0 && c0 + c * 8 < N)
+            cp16(piece(at + (c >> 3) * (TILE * 128), warp * SLAB + l, c & 7), base + (size_t)id * N + c0 + c * 8, true);
+        }
+        __syncwarp();
+        cp_arrive(&full[st]);
+      } else {
+        __syncwarp();
+        mbar_arrive(&full[st]);
+      }
+      ++i;
+      if (advance()) {
+        s = slab_of(ahead);
+        ahead = places(w.next, warp);
       }
     }
     cp_wait<0>();
-    fence_async_shared();
-    if (i == n)
-      for (int k = max(0, n - LAG); k < n; ++k) mbar_arrive(&b.full[k % R::STAGES]);
-  } else if (warp == 8) {
+    if (lane == 0 && abort_) settle(full, stages, i, &never);
+  } else if (warp == 12) {
     if (lane == 0) {
-      const uint32_t idesc = idesc_bf16_f32(TILE, TILE) | B_MN;
-      for (int i = 0; i < n; ++i) {
-        const int st = i % R::STAGES, acc = i & 1;
-        const uint32_t at = ring + st * R::STAGE;
-        if (!mbar_wait(&b.full[st], (i / R::STAGES) & 1, g)) break;
-        if (i >= 2 && !mbar_wait(&b.acc_empty[acc], (i / 2 - 1) & 1, g)) break;
+      const uint32_t idesc = idesc_bf16_f32(TILE, TILE) | B_MN, hrow = rp > 64 ? 128 : rank_bytes(rp);
+      while (more()) {
+        const int st = i % stages, acc = i & 1;
+        alive = mbar_wait(&full[st], (i / stages) & 1, g);
+        if (alive && i >= 2) alive = mbar_wait(&acc_empty[acc], (i / 2 - 1) & 1, g);
+        if (!alive) break;
         tc_fence_after();
-        Tile t;
-        int c0;
-        unit(i, t, c0);
-        if (t.adapter >= 0)
+        const uint32_t at = ring + st * stage;
+        if (w.t.adapter >= 0)
           for (int k = 0; k < rp / 16; ++k)
-            umma_bf16(b.tmem + acc * TILE,
-                      sdesc_kmajor_sw128(at + R::BASE + R::Q_BYTES + (k >> 2) * (TILE * 128) + 32 * (k & 3)),
-                      sdesc_mnmajor_sw128(at + R::BASE + 2048 * k, rp * 128), idesc, k > 0);
-        tc_commit(&b.acc_full[acc]);
+            umma_bf16(tmem + acc * TILE, sdesc_kmajor(at + h_at + (k >> 2) * (TILE * 128) + 32 * (k & 3), hrow),
+                      sdesc_mnmajor(at + q_at + 2048 * k, 128, rp * 128), idesc, k > 0);
+        tc_commit(&acc_full[acc]);
+        ++i;
+        advance();
       }
+      tc_commit(&done);
+      mbar_wait(&done, 0, WaitGuard{&never, status, limit_ns});
     }
-    __syncwarp();
   } else {
-    const int w = warp - 4, quad = w;  // (warps 4..7: tensor-memory lanes 32 w ..)
-    for (int i = 0; i < n; ++i) {
-      const int st = i % R::STAGES, acc = i & 1;
-      Tile t;
-      int c0;
-      unit(i, t, c0);
-      const int mine = t.count - 32 * w;  // rows of this warp
-      const int row_id = lane < mine ? plan.rows[t.start + 32 * w + lane] : 0;
-      if (!mbar_wait(&b.full[st], (i / R::STAGES) & 1, g)) break;
-      if (!mbar_wait(&b.acc_full[acc], (i / 2) & 1, g)) break;
+    const int slab = warp & 3, block = (warp - 4) >> 2;  // (a warp reads the tensor-memory lanes of its number modulo 4)
+    Slab s = slab_of(places(w.t, slab));
+    int ahead = places(w.next, slab);
+    int stored = -1;  // the stage whose box is on its way out
+    while (more()) {
+      const int st = i % stages, acc = i & 1, c0 = w.chunk * TILE + 64 * block;
+      alive = __all_sync(0xFFFFFFFFu, mbar_wait(&full[st], (i / stages) & 1, g) && mbar_wait(&acc_full[acc], (i / 2) & 1, g));
+      if (!alive) break;
       tc_fence_after();
-      const uint32_t at = ring + st * R::STAGE;
-      unsigned char* stage = smem + st * R::STAGE;
-      if (mine > 0) {
-        for (int q = 0; q < 4; ++q) {
+      const uint32_t at = ring + st * stage + block * (TILE * 128) + slab * (SLAB * 128);
+      unsigned char* mine = smem + (at - ring);
+      if (s.count > 0 && c0 < N) {
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
           float v[32];
-          if (t.adapter >= 0) {
-            tmem_ld32(b.tmem + acc * TILE + ((uint32_t)(32 * quad) << 16) + 32 * q, v);
+          if (w.t.adapter >= 0) {
+            tmem_ld32(tmem + acc * TILE + ((uint32_t)(32 * slab) << 16) + 64 * block + 32 * half, v);
           } else {
 #pragma unroll
             for (int k = 0; k < 32; ++k) v[k] = 0.0f;
           }
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
-            uint4* at16 = reinterpret_cast<uint4*>(stage + (piece(at + (q >> 1) * (TILE * 128), 32 * w + lane, (q & 1) * 4 + k) - at));
-            uint4 o = base ? *at16 : make_uint4(0, 0, 0, 0);
-            const float* s = v + 8 * k;
-            o.x = pack_bf16x2(bf16_lo(o.x) + s[0], bf16_hi(o.x) + s[1]);
-            o.y = pack_bf16x2(bf16_lo(o.y) + s[2], bf16_hi(o.y) + s[3]);
-            o.z = pack_bf16x2(bf16_lo(o.z) + s[4], bf16_hi(o.z) + s[5]);
-            o.w = pack_bf16x2(bf16_lo(o.w) + s[6], bf16_hi(o.w) + s[7]);
-            *at16 = o;
+            uint4* p = reinterpret_cast<uint4*>(mine + (piece(0, lane, 4 * half + k)));
+            uint4 o = base ? *p : make_uint4(0, 0, 0, 0);
+            const float* a = v + 8 * k;
+            o.x = pack_bf16x2(bf16_lo(o.x) + a[0], bf16_hi(o.x) + a[1]);
+            o.y = pack_bf16x2(bf16_lo(o.y) + a[2], bf16_hi(o.y) + a[3]);
+            o.z = pack_bf16x2(bf16_lo(o.z) + a[4], bf16_hi(o.z) + a[5]);
+            o.w = pack_bf16x2(bf16_lo(o.w) + a[6], bf16_hi(o.w) + a[7]);
+            *p = o;
           }
         }
-        tc_fence_before();
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&acc_empty[acc]);
+      // the stage before this one is free once its box has been read
+      const bool box = s.box && s.count == SLAB && c0 < N;
+      if (box) {
+        fence_async_shared();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&b.acc_empty[acc]);
-        const int c = lane & 15;
-        const bool col = c0 + c * 8 < N;
-        for (int j = 0; j < 32 && j < mine; j += 2) {
-          const int row = j + (lane >> 4);
-          const int id = __shfl_sync(0xFFFFFFFFu, row_id, row);
-          if (col && row < mine)
-            *reinterpret_cast<uint4*>(y + (size_t)id * N + c0 + c * 8) = *reinterpret_cast<const uint4*>(
-                stage + (piece(at + (c >> 3) * (TILE * 128), 32 * w + row, c & 7) - at));
+        if (lane == 0) {
+          tma_store_2d(&my, at, c0, s.first);
+          bulk_commit();
         }
-      } else if (lane == 0) {
-        mbar_arrive(&b.acc_empty[acc]);
+      } else if (s.count > 0 && c0 < N) {
+        const int c = lane & 7;
+        for (int l = lane >> 3; l < SLAB; l += 4) {
+          const int id = __shfl_sync(0xFFFFFFFFu, s.row, l);
+          if (id >= 0 && c0 + c * 8 < N)
+            *reinterpret_cast<uint4*>(y + (size_t)id * N + c0 + c * 8) = *reinterpret_cast<const uint4*>(mine + piece(0, l, c));
+        }
       }
       __syncwarp();
-      if (lane == 0) mbar_arrive(&b.empty[st]);
+      if (lane == 0) {
+        if (stored >= 0) {
+          if (box)
+            asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+          else
+            bulk_wait_read_all();
+          mbar_arrive(&empty[stored]);
+        }
+        if (!box) mbar_arrive(&empty[st]);
+      }
+      stored = box ? st : -1;
+      ++i;
+      if (advance()) {
+        s = slab_of(ahead);
+        ahead = places(w.next, slab);
+      }
     }
+    if (lane == 0) bulk_wait_read_all();
   }
+  tc_fence_before();
   __syncthreads();
-  if (warp == 8) {
+  if (warp == 12) {
     tc_fence_after();
-    tmem_dealloc(b.tmem, 256);
+    tmem_dealloc(tmem, 2 * TILE);
   }
 }
 
@@ -700,16 +1016,19 @@ __global__ void __launch_bounds__(ROW_THREADS) k_rows(const __nv_bfloat16* __res
 constexpr int FEW_ROWS = 64;
 
 size_t up256(size_t n) { return (n + 255) & ~(size_t)255; }
-int max_tiles(int T, int G) { return T / TILE + (G + 1 < T ? G + 1 : T); }
+int used_groups(int T, int G) { return G + 1 < T ? G + 1 : T; }             // at most, the rows without one among them
+int max_tiles(int T, int G) { return T / TILE + used_groups(T, G); }
+int places(int T, int G) { return (T / ALIGN + used_groups(T, G)) * ALIGN; }  // of the grouped order, at most
 
 size_t plan_bytes(int T, int G) {
-  return 256 + up256((size_t)(G + 2) * 4) + up256((size_t)max_tiles(T, G) * sizeof(Tile)) + up256((size_t)T * 4);
+  return 256 + up256((size_t)(G + 2) * 4) + up256((size_t)max_tiles(T, G) * sizeof(Tile)) + up256((size_t)places(T, G) * 4);
 }
+size_t sorted_bytes(int T, int r, int G) { return up256((size_t)places(T, G) * r * 2); }
 
 Plan plan_at(void* ws, int T, int G) {
   char* p = static_cast<char*>(ws);
   Plan q;
-  q.n_tiles = reinterpret_cast<int*>(p);
+  q.sums = reinterpret_cast<int*>(p);
   p += 256;
   q.first = reinterpret_cast<int*>(p);
   p += up256((size_t)(G + 2) * 4);
@@ -721,7 +1040,7 @@ Plan plan_at(void* ws, int T, int G) {
 
 template <class... A, class... B>
 moe_status_t launch(void (*k)(A...), int ctas, int cluster, int threads, int smem, int smem_limit, bool dependent,
-                    cudaStream_t stream, B... args) {
+                    cudaStream_t stream, const B&... args) {
   if (smem_limit && !set_smem_limit((const void*)k, smem_limit)) return MOE_ERR_CUDA;  // (one limit per kernel)
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(ctas);
@@ -751,55 +1070,73 @@ moe_status_t launch(void (*k)(A...), int ctas, int cluster, int threads, int sme
 using bf = __nv_bfloat16;
 const bf* in(const moe_bf16* p) { return reinterpret_cast<const bf*>(p); }
 bf* out(moe_bf16* p) { return reinterpret_cast<bf*>(p); }
-
 int pad16(int r) { return (r + 15) & ~15; }
+
+// Tensor maps of a [rows][cols] bf16 matrix in boxes of box_cols x box_rows,
+// swizzled over the box's row, and of an adapters' weight [G][r][C].
+bool map_rows(CUtensorMap* m, const void* p, int rows, int cols, int box_cols, int box_rows) {
+  const uint64_t dims[2] = {(uint64_t)cols, (uint64_t)rows}, strides[1] = {(uint64_t)cols * 2};
+  const uint32_t box[2] = {(uint32_t)box_cols, (uint32_t)box_rows};
+  return encode_tmap(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, p, dims, strides, box,
+                     box_cols == 64   ? CU_TENSOR_MAP_SWIZZLE_128B
+                     : box_cols == 32 ? CU_TENSOR_MAP_SWIZZLE_64B
+                                      : CU_TENSOR_MAP_SWIZZLE_32B);
+}
+bool map_weight(CUtensorMap* m, const void* p, int G, int r, int C, int rp) {
+  const uint64_t dims[3] = {(uint64_t)C, (uint64_t)r, (uint64_t)G}, strides[2] = {(uint64_t)C * 2, (uint64_t)C * 2 * r};
+  const uint32_t box[3] = {64, (uint32_t)rp, 1};
+  return encode_tmap(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, p, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
+}
 
 moe_status_t group(const int32_t* idx, int T, int G, const Plan& p, cudaStream_t s) {
   const int most = GROUP_SMEM / 4 / (G + 1), warps = most < 32 ? most : 32;
   return launch(k_group, 1, 0, GROUP_THREADS, warps * (G + 1) * 4, GROUP_SMEM, false, s, idx, T, G, warps, p);
 }
 
-// CTAs per cluster that share a contraction of `blocks` stages: enough to
-// occupy the SMs with `clusters` of them, and two stages each at least.
-int split_of(int clusters, int blocks) {
-  int s = 1;
-  while (s < 8 && clusters * s < 2 * 152 && blocks >= 4 * s) s *= 2;
-  return s;
+// CTAs per cluster that share a contraction of `blocks` stages: as many as the
+// SMs hold at once with `clusters` of them, and two stages each at least.
+int split_of(const void* kernel, int threads, int smem, int clusters, int blocks) {
+  const int slots = sm_count() * max_active_blocks(kernel, threads, smem);
+  int s = slots / (clusters > 0 ? clusters : 1);
+  if (s > blocks / 2) s = blocks / 2;
+  return s < 1 ? 1 : s > 8 ? 8 : s;
 }
 
 moe_status_t shrink(const moe_bf16* x, const moe_bf16* P, const float* scale, int T, int K, int r, int G, const Plan& p,
-                    moe_bf16* h, int32_t* st, cudaStream_t s) {
-  const int rp = pad16(r), tiles = max_tiles(T, G), split = split_of((T + TILE - 1) / TILE, (K + KB - 1) / KB);
-  const uint64_t lim = g_wait_limit_ns.load();
-  return rp <= 64 ? launch(k_shrink<64>, tiles * split, split, THREADS, Ring<64>::BYTES, Ring<64>::BYTES, true, s, in(x), in(P), scale, K, r,
-                           rp, p, out(h), lim, st)
-                  : launch(k_shrink<128>, tiles * split, split, THREADS, Ring<128>::BYTES, Ring<128>::BYTES, true, s, in(x), in(P), scale, K,
-                           r, rp, p, out(h), lim, st);
+                    moe_bf16* h, moe_bf16* hs, const moe_bf16* other, moe_bf16* others, int32_t* st, cudaStream_t s) {
+  const int rp = pad16(r), tiles = max_tiles(T, G), bytes = shrink_bytes(rp);
+  if (!set_smem_limit((const void*)k_shrink, shrink_bytes(MAX_R))) return MOE_ERR_CUDA;
+  const int split = split_of((const void*)k_shrink, SHRINK_THREADS, bytes, tiles, (K + KB - 1) / KB);
+  CUtensorMap mx, mp;
+  if (!map_rows(&mx, x, T, K, 64, SLAB) || !map_weight(&mp, P, G, r, K, rp)) return MOE_ERR_CUDA;
+  return launch(k_shrink, tiles * split, split, SHRINK_THREADS, bytes, shrink_bytes(MAX_R), true, s, mx, mp, in(x), scale, K,
+                r, rp, p, out(h), out(hs), in(other), out(others), g_wait_limit_ns.load(), st);
 }
 
-moe_status_t wgrad(const moe_bf16* x, const moe_bf16* u, int T, int C, int r, int G, const Plan& p, moe_bf16* dP,
+moe_status_t wgrad(const moe_bf16* x, const moe_bf16* us, int T, int C, int r, int G, const Plan& p, moe_bf16* dP,
                    int32_t* st, cudaStream_t s) {
-  const int rp = pad16(r), units = G * ((C + TILE - 1) / TILE), split = split_of(units, (T + KB - 1) / KB);
-  const uint64_t lim = g_wait_limit_ns.load();
-  return rp <= 64 ? launch(k_wgrad<64>, units * split, split, THREADS, Ring<64>::BYTES, Ring<64>::BYTES, true, s, in(x), in(u), C, r, rp, p,
-                           out(dP), lim, st)
-                  : launch(k_wgrad<128>, units * split, split, THREADS, Ring<128>::BYTES, Ring<128>::BYTES, true, s, in(x), in(u), C, r, rp, p,
-                           out(dP), lim, st);
+  const int rp = pad16(r), units = (C + TILE - 1) / TILE, bytes = wgrad_bytes(rp);
+  if (!set_smem_limit((const void*)k_wgrad, wgrad_bytes(MAX_R))) return MOE_ERR_CUDA;
+  const int split = split_of((const void*)k_wgrad, WGRAD_THREADS, bytes, units, T / KB);
+  CUtensorMap mx, mu;
+  if (!map_rows(&mx, x, T, C, 64, SLAB) || !map_rows(&mu, us, places(T, G), r, rank_cols(rp), KB)) return MOE_ERR_CUDA;
+  return launch(k_wgrad, units * split, split, WGRAD_THREADS, bytes, wgrad_bytes(MAX_R), true, s, mx, mu, in(x), C, r, rp, G,
+                p, out(dP), g_wait_limit_ns.load(), st);
 }
 
-moe_status_t expand(const moe_bf16* h, const moe_bf16* Q, const moe_bf16* base, int T, int N, int r, int G, const Plan& p,
+moe_status_t expand(const moe_bf16* hs, const moe_bf16* Q, const moe_bf16* base, int T, int N, int r, int G, const Plan& p,
                     moe_bf16* y, int32_t* st, cudaStream_t s) {
-  const int rp = pad16(r), sms = sm_count();
+  const int rp = pad16(r), sms = sm_count(), bytes = expand_bytes(rp);
   if (sms < 1) return MOE_ERR_CUDA;
   const int64_t units = (int64_t)max_tiles(T, G) * ((N + TILE - 1) / TILE);
   const int grid = units < sms ? (int)units : sms;
-  const uint64_t lim = g_wait_limit_ns.load();
-  auto go = [&](auto k, int bytes) {
-    return launch(k, grid, 0, WIDE_THREADS, bytes, bytes, true, s, in(h), in(Q), in(base), N, r, rp, p, out(y), lim, st);
-  };
-  return rp <= 32   ? go(k_expand<32>, Wide<32>::BYTES)
-         : rp <= 64 ? go(k_expand<64>, Wide<64>::BYTES)
-                    : go(k_expand<128>, Wide<128>::BYTES);
+  CUtensorMap mh, mq, mb, my;
+  if (!map_rows(&mh, hs, places(T, G), r, rank_cols(rp), TILE) || !map_weight(&mq, Q, G, r, N, rp) ||
+      !map_rows(&mb, base ? base : y, T, N, 64, SLAB) || !map_rows(&my, y, T, N, 64, SLAB))
+    return MOE_ERR_CUDA;
+  constexpr int most = expand_bytes(32) > expand_bytes(MAX_R) ? expand_bytes(32) : expand_bytes(MAX_R);
+  return launch(k_expand, grid, 0, EXPAND_THREADS, bytes, most, true, s, mh, mq, mb, my, in(base), N, r, rp, p, out(y),
+                g_wait_limit_ns.load(), st);
 }
 
 bool sizes_ok(int T, int K, int N, int r, int G) {
@@ -820,7 +1157,7 @@ using namespace moeglu::lora;
 
 extern "C" size_t moe_lora_workspace_size(int T, int r, int G) {
   if (T < 0 || r <= 0 || G <= 0) return 0;
-  return plan_bytes(T, G) + up256((size_t)T * r * 2);
+  return plan_bytes(T, G) + 2 * sorted_bytes(T, r, G);
 }
 
 extern "C" moe_status_t moe_lora_fwd(const moe_bf16* x, const moe_bf16* A, const moe_bf16* B, const int32_t* idx,
@@ -843,10 +1180,10 @@ extern "C" moe_status_t moe_lora_fwd(const moe_bf16* x, const moe_bf16* A, const
     return launch(k_rows, T * ROW_CTAS, ROW_CTAS, ROW_THREADS, 0, 0, false, s, in(x), in(A), in(B), idx, scale, in(base), K, N,
                   r, G, out(y), out(h));
   const Plan p = plan_at(ws, T, G);
-  if (!h) h = reinterpret_cast<moe_bf16*>(static_cast<char*>(ws) + plan_bytes(T, G));
+  auto* hs = reinterpret_cast<moe_bf16*>(static_cast<char*>(ws) + plan_bytes(T, G));
   if (const moe_status_t e = group(idx, T, G, p, s)) return e;
-  if (const moe_status_t e = shrink(x, A, scale, T, K, r, G, p, h, status, s)) return e;
-  return expand(h, B, base, T, N, r, G, p, y, status, s);
+  if (const moe_status_t e = shrink(x, A, scale, T, K, r, G, p, h, hs, nullptr, nullptr, status, s)) return e;
+  return expand(hs, B, base, T, N, r, G, p, y, status, s);
 }
 
 extern "C" moe_status_t moe_lora_bwd(const moe_bf16* dy, const moe_bf16* x, const moe_bf16* h, const moe_bf16* A,
@@ -873,10 +1210,11 @@ extern "C" moe_status_t moe_lora_bwd(const moe_bf16* dy, const moe_bf16* x, cons
       overlap(dx, xn, h, (size_t)T * r * 2) || overlap(dx, xn, A, an) || overlap(dA, an, A, an) || overlap(dB, bn, B, bn))
     return MOE_ERR_ARG;
   const Plan p = plan_at(ws, T, G);
-  auto* u = reinterpret_cast<moe_bf16*>(static_cast<char*>(ws) + plan_bytes(T, G));
+  auto* us = reinterpret_cast<moe_bf16*>(static_cast<char*>(ws) + plan_bytes(T, G));
+  auto* hs = us + sorted_bytes(T, r, G) / 2;
   if (const moe_status_t e = group(idx, T, G, p, s)) return e;
-  if (const moe_status_t e = shrink(dy, B, scale, T, N, r, G, p, u, status, s)) return e;
-  if (const moe_status_t e = expand(u, A, base, T, K, r, G, p, dx, status, s)) return e;
-  if (const moe_status_t e = wgrad(x, u, T, K, r, G, p, dA, status, s)) return e;
-  return wgrad(dy, h, T, N, r, G, p, dB, status, s);
+  if (const moe_status_t e = shrink(dy, B, scale, T, N, r, G, p, nullptr, us, h, hs, status, s)) return e;
+  if (const moe_status_t e = expand(us, A, base, T, K, r, G, p, dx, status, s)) return e;
+  if (const moe_status_t e = wgrad(x, us, T, K, r, G, p, dA, status, s)) return e;
+  return wgrad(dy, hs, T, N, r, G, p, dB, status, s);
 }
