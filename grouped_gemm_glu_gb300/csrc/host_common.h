@@ -38,6 +38,11 @@ int max_active_blocks(const void* kernel, int threads, int smem_bytes);
 // device; returns false on failure).
 bool set_smem_limit(const void* kernel, int bytes);
 
+// Asks for the largest share of an SM's memory as shared memory, so that
+// several CTAs of a kernel with much of it are resident (the default is sized
+// for one; once per kernel and device; false on failure).
+bool prefer_shared(const void* kernel);
+
 // Encodes a tiled TMA descriptor for a row-major tensor with dims[0] the
 // contiguous dimension.  rank 2 or 3; strides_bytes has rank-1 entries.
 bool encode_tmap(CUtensorMap* map, CUtensorMapDataType dtype, int rank, const void* base,

@@ -44,7 +44,9 @@ struct Tile {
   int adapter, start, count;  // -1: rows without an adapter; first place in the grouped order
   int cost;                   // of the tiles before it (see tile_cost)
 };
-__host__ __device__ __forceinline__ int tile_cost(int count) { return 1 + (count + SLAB - 1) / SLAB; }
+// What a unit of k_expand costs: its chain of waits more than its rows (1 + slabs took 73 us, 3 + slabs 55, 5 + slabs 49
+// and this 47 us at 8192 x 7168, rank 32, 8 adapters).
+__host__ __device__ __forceinline__ int tile_cost(int count) { return 8 + (count + SLAB - 1) / SLAB; }
 
 // Workspace: the grouped order.
 struct Plan {
@@ -66,6 +68,10 @@ __device__ __forceinline__ void cp_wait() {
 // Arrives on the barrier when the thread's copies so far have landed.
 __device__ __forceinline__ void cp_arrive(uint64_t* bar) {
   asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+// The arrivals of a warp's 32 threads by one of them (they are served one after the other).
+__device__ __forceinline__ void mbar_arrive_warp(uint64_t* bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], 32;" ::"r"(smem_u32(bar)) : "memory");
 }
 __device__ __forceinline__ void mbar_expect_tx(uint64_t* bar, uint32_t bytes) {
   asm volatile("mbarrier.expect_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(bar)), "r"(bytes) : "memory");
@@ -134,11 +140,48 @@ __device__ __forceinline__ uint32_t cluster_size() {
 // swizzle's period; 1024 bytes more are asked for).
 __device__ __forceinline__ unsigned char* aligned_smem(unsigned char* p) { return p + ((0u - smem_u32(p)) & 1023u); }
 
+// mbar_wait for waits that mostly last a few hundred cycles: the clock and the
+// abort flag are read at every 256th look only, the first time included.
+__device__ __forceinline__ bool wait_on(uint64_t* bar, uint32_t parity, const WaitGuard& g) {
+  uint64_t t0 = 0;
+  for (uint32_t it = 1;; ++it) {
+    if (mbar_test(bar, parity)) return true;
+    if ((it & 255u) == 0) {
+      if (*g.abort) return false;
+      const uint64_t now = globaltimer_ns();
+      if (t0 == 0) {
+        t0 = now;
+      } else if (now - t0 > g.limit_ns) {
+        *g.abort = 1;
+        set_status(g.status, MOE_ERR_TIMEOUT);
+        return false;
+      }
+    }
+  }
+}
+
 // After an abort: gives the TMA copies of the last steps issued a millisecond
 // to land before the CTA's shared memory is given up.
 __device__ __forceinline__ void settle(uint64_t* full, int stages, int issued, int* never) {
   for (int k = max(0, issued - stages); k < issued; ++k)
-    mbar_wait(&full[k % stages], (k / stages) & 1, WaitGuard{never, nullptr, 1000000});
+    wait_on(&full[k % stages], (k / stages) & 1, WaitGuard{never, nullptr, 1000000});
+}
+
+// The operands of TMA and tcgen05 instructions are uniform registers.  Loops
+// that issue them are run by whole warps with one elected lane, on values made
+// uniform here: where a single lane runs the loop, each operand is moved there
+// on its own (k_wgrad's four MMAs and a commit took 1190 cycles a step).
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xFFFFFFFF;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(p));
+  return p != 0;
+}
+template <class T>
+__device__ __forceinline__ T uniform(T v) {
+  return __shfl_sync(0xFFFFFFFFu, v, 0);
+}
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, const WaitGuard& g) {
+  return __all_sync(0xFFFFFFFFu, wait_on(bar, parity, g));
 }
 
 // A warp's 32 places: the row of each lane (-1: none), and whether they are
@@ -146,6 +189,8 @@ __device__ __forceinline__ void settle(uint64_t* full, int stages, int issued, i
 struct Slab {
   int row, first, count;
   bool box;
+  // bit l: lane l's group of eight lanes has neighbours too, as far as it has rows / has eight of them
+  uint32_t near, whole;
 };
 __device__ __forceinline__ Slab slab_of(int row) {
   Slab s;
@@ -153,6 +198,12 @@ __device__ __forceinline__ Slab slab_of(int row) {
   s.count = __popc(__ballot_sync(0xFFFFFFFFu, row >= 0));
   s.first = __shfl_sync(0xFFFFFFFFu, row, 0);
   s.box = __all_sync(0xFFFFFFFFu, row < 0 || row == s.first + (int)(threadIdx.x & 31));
+  const int head = __shfl_sync(0xFFFFFFFFu, row, threadIdx.x & 24);
+  const uint32_t next = __ballot_sync(0xFFFFFFFFu, row < 0 || row == head + (int)(threadIdx.x & 7));
+  const uint32_t some = __ballot_sync(0xFFFFFFFFu, row >= 0);
+  auto all8 = [](uint32_t m) { return m & (m >> 1) & (m >> 2) & (m >> 3) & (m >> 4) & (m >> 5) & (m >> 6) & (m >> 7) & 0x01010101u; };
+  s.near = all8(next) * 0xFFu;
+  s.whole = all8(next & some) * 0xFFu;
   return s;
 }
 
@@ -174,7 +225,7 @@ __device__ __forceinline__ int warp_scan(int v) {  // inclusive
 __global__ void __launch_bounds__(GROUP_THREADS) k_group(const int32_t* __restrict__ idx, int T, int G, int warps, Plan p) {
   launch_dependents();
   extern __shared__ int hist[];  // [G + 1][warps]
-  __shared__ int part[4][32];
+  __shared__ int part[3][32], count[GROUP_THREADS], begin[GROUP_THREADS], tile_at[GROUP_THREADS], cost_at[GROUP_THREADS];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, groups = G + 1;
   const int per = ((T + warps - 1) / warps + 31) & ~31;
   const int lo = min(T, warp * per), hi = warp < warps ? min(T, lo + per) : lo;
@@ -202,18 +253,18 @@ __global__ void __launch_bounds__(GROUP_THREADS) k_group(const int32_t* __restri
     __syncwarp();
   });
   __syncthreads();
-  // per group: its rows before each warp's (in hist) and in all (first, for now)
-  for (int g = warp; g < groups; g += GROUP_THREADS / 32) {
-    const int n = lane < warps ? hist[g * warps + lane] : 0, s = warp_scan(n);
-    if (lane < warps) hist[g * warps + lane] = s - n;
-    if (lane == 31) p.first[g] = s;
-  }
-  __syncthreads();
-  // places: sums over the groups before (rows up to whole ALIGNs, tiles, cost), 1024 groups at a time
+  // 1024 groups at a time: the rows of each before each warp's, and the sums over the groups before it (rows up to
+  // whole ALIGNs, tiles, cost)
   int rows0 = 0, tiles0 = 0, cost0 = 0;
+  const bool few = groups <= GROUP_THREADS;  // (then `begin` still holds every group's first place in the end)
   for (int g0 = 0; g0 < groups; g0 += GROUP_THREADS) {
-    const int g = g0 + tid;
-    const int n = g < groups ? p.first[g] : 0;
+    for (int g = g0 + warp; g < min(groups, g0 + GROUP_THREADS); g += GROUP_THREADS / 32) {
+      const int n = lane < warps ? hist[g * warps + lane] : 0, s = warp_scan(n);
+      if (lane < warps) hist[g * warps + lane] = s - n;
+      if (lane == 31) count[g - g0] = s;
+    }
+    __syncthreads();
+    const int g = g0 + tid, n = g < groups ? count[tid] : 0;
     const int full = n / TILE, rest = n - full * TILE;
     const int up = (n + ALIGN - 1) / ALIGN * ALIGN, tiles = full + (rest > 0);
     const int cost = full * tile_cost(TILE) + (rest > 0 ? tile_cost(rest) : 0);
@@ -223,30 +274,34 @@ __global__ void __launch_bounds__(GROUP_THREADS) k_group(const int32_t* __restri
     if (warp < 3) part[warp][lane] = warp_scan(part[warp][lane]);
     __syncthreads();
     if (warp) rs += part[0][warp - 1], ts += part[1][warp - 1], cs += part[2][warp - 1];
-    if (g < groups) {
-      const int r0 = rows0 + rs - up, t0 = tiles0 + ts - tiles, c0 = cost0 + cs - cost;
-      p.first[g] = r0;
-      for (int w = 0; w < warps; ++w) hist[g * warps + w] += r0;
-      for (int i = 0; i < tiles; ++i)
-        p.tiles[t0 + i] = {g < G ? g : -1, r0 + i * TILE, min(TILE, n - i * TILE), c0 + i * tile_cost(TILE)};
-      for (int i = n; i < up; ++i) p.rows[r0 + i] = -1;
-      if (g == G) {
-        p.first[groups] = r0 + up;
-        p.sums[0] = t0;
-        p.sums[1] = t0 + tiles;
-        p.sums[2] = c0 + cost;
-      }
+    begin[tid] = rows0 + rs - up;
+    tile_at[tid] = tiles0 + ts - tiles;
+    cost_at[tid] = cost0 + cs - cost;
+    if (g < groups) p.first[g] = begin[tid];
+    if (g == G) {
+      p.first[groups] = begin[tid] + up;
+      p.sums[0] = tile_at[tid];
+      p.sums[1] = tile_at[tid] + tiles;
+      p.sums[2] = cost_at[tid] + cost;
     }
     rows0 += part[0][31];
     tiles0 += part[1][31];
     cost0 += part[2][31];
+    __syncthreads();
+    for (int k = warp; k < min(groups - g0, GROUP_THREADS); k += GROUP_THREADS / 32) {
+      const int c = count[k], r0 = begin[k], a = g0 + k;
+      for (int i = lane; i * TILE < c; i += 32)
+        p.tiles[tile_at[k] + i] = {a < G ? a : -1, r0 + i * TILE, min(TILE, c - i * TILE), cost_at[k] + i * tile_cost(TILE)};
+      if (c + lane < (c + ALIGN - 1) / ALIGN * ALIGN) p.rows[r0 + c + lane] = -1;
+      if (!few && lane < warps) hist[a * warps + lane] += r0;
+    }
     __syncthreads();
   }
   each([&](int row, int a, uint32_t same) {
     int at = 0;
     if (a >= 0) {
       at = hist[a * warps + warp];
-      p.rows[at + __popc(same & below)] = row;
+      p.rows[at + (few ? begin[a] : 0) + __popc(same & below)] = row;
     }
     __syncwarp();
     if (a >= 0 && (same & below) == 0) hist[a * warps + warp] = at + __popc(same);
@@ -291,7 +346,7 @@ __global__ void __launch_bounds__(SHRINK_THREADS) k_shrink(const __grid_constant
   __shared__ Bars b;
   __shared__ int rows[TILE];
   const uint32_t size = cluster_size(), rank = cluster_ctarank();
-  const int tile = blockIdx.x / size, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int tile = blockIdx.x / size, warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
   launch_dependents();
   wait_for_primary();
   if (tile >= plan.sums[1]) return;  // (the whole cluster)
@@ -329,17 +384,20 @@ __global__ void __launch_bounds__(SHRINK_THREADS) k_shrink(const __grid_constant
     const Slab s = slab_of(rows[threadIdx.x]);
     const uint32_t slab = warp * SLAB * 128;
     int issued = 0;
-    if (s.count == 0 || (s.box && s.count >= MIN_BOX)) {
-      if (lane == 0)
-        for (int i = 0; i < steps; ++i) {
-          const int st = i % SHRINK_STAGES;
-          if (i >= SHRINK_STAGES && !mbar_wait(&b.empty[st], (i / SHRINK_STAGES - 1) & 1, g)) break;
-          const uint32_t at = ring + st * stage;
-          mbar_arrive_expect_tx(&b.full[st], (s.count ? SLAB * 128 : 0) + (warp == 0 ? rp * 128 : 0));
-          if (s.count) tma_2d(at + slab, &mx, &b.full[st], (k0 + i) * KB, s.first);
-          if (warp == 0) tma_3d(at + TILE * 128, &mp, &b.full[st], (k0 + i) * KB, 0, t.adapter);
-          ++issued;
+    const int adapter = uniform(t.adapter), first = uniform(s.first), count = uniform(s.count);
+    if (count == 0 || (s.box && count >= MIN_BOX)) {
+      for (int i = 0; i < steps; ++i) {
+        const int st = i % SHRINK_STAGES;
+        if (i >= SHRINK_STAGES && !warp_wait(&b.empty[st], (i / SHRINK_STAGES - 1) & 1, g)) break;
+        const uint32_t at = ring + st * stage;
+        if (elect_one()) {
+          mbar_arrive_expect_tx(&b.full[st], (count ? SLAB * 128 : 0) + (warp == 0 ? rp * 128 : 0));
+          if (count) tma_2d(at + slab, &mx, &b.full[st], (k0 + i) * KB, first);
+          if (warp == 0) tma_3d(at + TILE * 128, &mp, &b.full[st], (k0 + i) * KB, 0, adapter);
         }
+        __syncwarp();
+        ++issued;
+      }
     } else {
       // row by row: eight lanes copy a row's 128 bytes, and arrive two steps later, when they have landed
       const int c = lane & 7;
@@ -353,14 +411,15 @@ __global__ void __launch_bounds__(SHRINK_THREADS) k_shrink(const __grid_constant
       int i = 0;
       for (; i < steps; ++i) {
         const int st = i % SHRINK_STAGES;
-        if (i >= SHRINK_STAGES && !mbar_wait(&b.empty[st], (i / SHRINK_STAGES - 1) & 1, g)) break;
+        if (i >= SHRINK_STAGES && !warp_wait(&b.empty[st], (i / SHRINK_STAGES - 1) & 1, g)) break;
         const uint32_t at = ring + st * stage;
         const int k = (k0 + i) * KB;
-        if (warp == 0 && lane == 0) {
+        if (warp == 0 && elect_one()) {
           mbar_expect_tx(&b.full[st], rp * 128);
-          tma_3d(at + TILE * 128, &mp, &b.full[st], k, 0, t.adapter);
-          ++issued;
+          tma_3d(at + TILE * 128, &mp, &b.full[st], k, 0, adapter);
         }
+        __syncwarp();
+        ++issued;
         const bool in = k + c * 8 < K;
 #pragma unroll
         for (int j = 0; j < 8; ++j)
@@ -382,23 +441,23 @@ __global__ void __launch_bounds__(SHRINK_THREADS) k_shrink(const __grid_constant
     if (b.abort && lane == 0) settle(b.full, SHRINK_STAGES, issued, &b.never);
     __syncwarp();
   } else {
-    if (lane == 0) {
-      const uint32_t idesc = idesc_bf16_f32(TILE, rp);
-      for (int i = 0; i < steps; ++i) {
-        const int st = i % SHRINK_STAGES;
-        if (!mbar_wait(&b.full[st], (i / SHRINK_STAGES) & 1, g)) break;
-        tc_fence_after();
-        const uint32_t at = ring + st * stage;
+    const uint32_t idesc = idesc_bf16_f32(TILE, rp), tmem = uniform(b.tmem);
+    for (int i = 0; i < steps; ++i) {
+      const int st = i % SHRINK_STAGES;
+      if (!warp_wait(&b.full[st], (i / SHRINK_STAGES) & 1, g)) break;
+      tc_fence_after();
+      const uint64_t a = sdesc_kmajor(ring + st * stage, 128), w = sdesc_kmajor(ring + st * stage + TILE * 128, 128);
+      if (elect_one()) {
 #pragma unroll
-        for (int k = 0; k < KB / 16; ++k)
-          umma_bf16(b.tmem, sdesc_kmajor(at + 32 * k, 128), sdesc_kmajor(at + TILE * 128 + 32 * k, 128), idesc, i + k > 0);
+        for (int k = 0; k < KB / 16; ++k) umma_bf16(tmem, a + 2 * k, w + 2 * k, idesc, (i | k) != 0);
         tc_commit(&b.empty[st]);
       }
-      tc_commit(&b.done);
+      __syncwarp();
     }
+    if (elect_one()) tc_commit(&b.done);
     __syncwarp();
   }
-  if (warp == 4) mbar_wait(&b.done, 0, WaitGuard{&b.never, status, limit_ns});
+  if (warp == 4) wait_on(&b.done, 0, WaitGuard{&b.never, status, limit_ns});
   tc_fence_before();
   __syncthreads();  // (every copy has landed and every MMA has read: the ring is free)
   tc_fence_after();
@@ -427,12 +486,11 @@ __global__ void __launch_bounds__(SHRINK_THREADS) k_shrink(const __grid_constant
     for (int i = threadIdx.x + rank * SHRINK_THREADS; i < items; i += SHRINK_THREADS * size) {
       const int q = i / up, l = i - q * up;
       const uint32_t at = ring + (q * TILE + l) * 16;
-      float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-      if (l < t.count)
-        for (uint32_t c = 0; c < size; ++c) {
-          const float4 v = ld_cluster(mapa_shared(at, c));
-          s.x += v.x, s.y += v.y, s.z += v.z, s.w += v.w;
-        }
+      float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f), v[8];
+#pragma unroll
+      for (uint32_t c = 0; c < 8; ++c) v[c] = c < size && l < t.count ? ld_cluster(mapa_shared(at, c)) : s;
+#pragma unroll
+      for (uint32_t c = 0; c < 8; ++c) s.x += v[c].x, s.y += v[c].y, s.z += v[c].z, s.w += v[c].w;
       const uint2 o = pack4(s, l < t.count ? f : 0.0f);
       if (h && l < t.count) *reinterpret_cast<uint2*>(h + (size_t)rows[l] * r + q * 4) = o;
       *reinterpret_cast<uint2*>(hs + (size_t)(t.start + l) * r + q * 4) = l < t.count ? o : make_uint2(0, 0);
@@ -449,23 +507,19 @@ __global__ void __launch_bounds__(SHRINK_THREADS) k_shrink(const __grid_constant
 }
 
 // ---------------------------------------------------------------------------
-// k_wgrad: cluster (128 columns of X [T][C]), its CTAs share the grouped rows,
-// all adapters: dP [G][r][C] = U^T X over each adapter's rows, U in the
-// grouped order.  The rows of an adapter that cross from one CTA's share into
-// the next ones' are summed by the CTA in which they begin.
-// Warps 0 to 3 load (32 rows x 64 columns each), 4 issues the MMAs, 5 to 8
-// write out; two accumulators.
+// k_wgrad: cluster (128 columns of X [T][C]), its CTAs share the tiles of all
+// adapters: dP [G][r][C] = U^T X over each adapter's rows, U in the grouped
+// order.  An adapter's tiles that cross from one CTA's share into the next
+// ones' are summed by the whole cluster in the end.
+// Warps 0 to 3 load 32 rows each, 4 issues the MMAs, 5 to 8 write out; two
+// accumulators.
 // ---------------------------------------------------------------------------
-constexpr int WGRAD_THREADS = 288, BATCH = 128;  // steps whose descriptions are looked up together
-__host__ __device__ constexpr int wgrad_stages(int rp) { return rp <= 16 ? 3 : rp <= 32 ? 4 : rp <= 64 ? 3 : 4; }
-__host__ __device__ constexpr int wgrad_stage(int rp) { return KB * 256 + KB * rank_bytes(rp); }
+constexpr int WGRAD_THREADS = 288, BATCH = 16;  // tiles whose rows are looked up together
+__host__ __device__ constexpr int wgrad_stages(int rp) { return rp <= 32 ? 2 : rp <= 64 ? 3 : 2; }
+__host__ __device__ constexpr int wgrad_stage(int rp) { return TILE * 256 + TILE * rank_bytes(rp); }
 constexpr int wgrad_bytes(int rp) { return wgrad_stages(rp) * wgrad_stage(rp) + 512 * rp + 1024; }
 
-struct Step {
-  int start, count, adapter;  // up to 64 places of one adapter; a count of 0: no step
-  int flags;
-};
-// the first / last step of a run of one adapter in this CTA; the run began before it / goes on behind it
+// of a step (a tile) in this CTA: the first / last of its run of one adapter; the run began before / goes on behind it
 enum { RUN_BEGINS = 1, RUN_ENDS = 2, FROM_BEFORE = 4, GOES_ON = 8 };
 
 __global__ void __launch_bounds__(WGRAD_THREADS) k_wgrad(const __grid_constant__ CUtensorMap mx,
@@ -475,15 +529,16 @@ __global__ void __launch_bounds__(WGRAD_THREADS) k_wgrad(const __grid_constant__
                                                          int32_t* status) {
   extern __shared__ unsigned char smem_[];
   unsigned char* smem = aligned_smem(smem_);
-  __shared__ uint64_t full[4], empty[4], acc_full[2], acc_empty[2], done;
-  __shared__ int abort_, never, head_adapter, head_through, tail_adapter;
+  __shared__ uint64_t full[3], empty[3], acc_full[2], acc_empty[2], done;
+  __shared__ int abort_, never, head_through, tail_adapter;
   __shared__ uint32_t tmem_;
-  __shared__ Step steps[BATCH];
+  __shared__ int4 steps[BATCH];                        // first place, rows, adapter, flags
+  __shared__ int row_of[BATCH][TILE], box_of[BATCH][4];  // rows of each step; the first one of 32 neighbours, or -1
   const uint32_t size = cluster_size(), rank = cluster_ctarank();
-  const int c0 = (int)(blockIdx.x / size) * TILE, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int c0 = (int)(blockIdx.x / size) * TILE, warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
   const int stages = wgrad_stages(rp);
   const uint32_t ring = smem_u32(smem), stage = wgrad_stage(rp), acc_cols = tmem_cols(rp);
-  unsigned char* head = smem + stages * stage;  // float4 [rp / 4][128]: the run from before, for its owner
+  unsigned char* head = smem + stages * stage;  // float4 [rp / 4][128]: the run from before
   if (threadIdx.x == 0) {
     for (int i = 0; i < stages; ++i) {
       mbar_init(&full[i], 4);
@@ -495,7 +550,7 @@ __global__ void __launch_bounds__(WGRAD_THREADS) k_wgrad(const __grid_constant__
     }
     mbar_init(&done, 1);
     abort_ = never = head_through = 0;
-    head_adapter = tail_adapter = -1;
+    tail_adapter = -1;
     fence_barrier_init();
   }
   if (warp == 4) {
@@ -508,118 +563,152 @@ __global__ void __launch_bounds__(WGRAD_THREADS) k_wgrad(const __grid_constant__
   launch_dependents();
   wait_for_primary();
   const WaitGuard g{&abort_, status, limit_ns};
-  const uint32_t tmem = tmem_;
+  const uint32_t tmem = uniform(tmem_);
   const int tiles = plan.sums[0];
-  auto share = [&](int c) { return (int)((int64_t)2 * tiles * c / (int)size); };  // halves of tiles before CTA c's
+  auto share = [&](int c) { return (int)((int64_t)tiles * c / (int)size); };  // tiles before CTA c's
   const int lo = share(rank), hi = share(rank + 1);
-  if (warp >= 5 && c0 + 4 * lane < C)  // adapters without rows
-    for (int a = rank + size * (warp - 5); a < G; a += 4 * size)
-      if (plan.first[a] == plan.first[a + 1])
-        for (int j = 0; j < r; ++j) *reinterpret_cast<uint2*>(dP + ((size_t)a * r + j) * C + c0 + 4 * lane) = make_uint2(0, 0);
-  __syncwarp();
-  int i = 0, run = 0;  // steps and runs so far, counted by every role for itself
+  // steps and runs so far, counted by every role for itself; the step's stage, and its turn of the ring (counted on:
+  // a division by the number of stages cost more than the rest of a step)
+  int i = 0, run = 0, st = 0;
+  uint32_t turn = 0;
+  auto next_stage = [&] {
+    ++i;
+    if (++st == stages) st = 0, ++turn;
+  };
   bool before = false, alive = true;
   for (int b0 = lo; b0 < hi; b0 += BATCH) {
     const int m = min(BATCH, hi - b0);
-    __syncthreads();
-    if ((int)threadIdx.x < m) {
-      const int hh = b0 + threadIdx.x, ti = hh >> 1, second = hh & 1;
-      const Tile t = plan.tiles[ti];
-      Step s;
-      s.start = t.start + second * KB;
-      s.count = max(0, min(KB, t.count - second * KB));
-      s.adapter = t.adapter;
-      const bool begins = !second && (ti == 0 || plan.tiles[ti - 1].adapter != t.adapter);
-      const bool ends = (second || t.count <= KB) && (ti + 1 == tiles || plan.tiles[ti + 1].adapter != t.adapter);
-      s.flags = (begins || hh == lo ? RUN_BEGINS : 0) | (ends || hh + 1 == hi ? RUN_ENDS : 0) |
-                (!begins && hh == lo ? FROM_BEFORE : 0) | (!ends && hh + 1 == hi ? GOES_ON : 0);
-      steps[threadIdx.x] = s;
+    if (b0 > lo) __syncthreads();
+    {
+      constexpr int WARPS = WGRAD_THREADS / 32, MORE = (BATCH + WARPS - 1) / WARPS;
+      int4 s[MORE];
+      int row[MORE][4];
+#pragma unroll
+      for (int q = 0; q < MORE; ++q) {
+        const int j = warp + q * WARPS, ti = b0 + j;
+        if (j < m) {
+          const Tile t = plan.tiles[ti];
+          const bool begins = ti == 0 || plan.tiles[ti - 1].adapter != t.adapter;
+          const bool ends = ti + 1 == tiles || plan.tiles[ti + 1].adapter != t.adapter;
+          s[q] = make_int4(t.start, t.count, t.adapter,
+                           (begins || ti == lo ? RUN_BEGINS : 0) | (ends || ti + 1 == hi ? RUN_ENDS : 0) |
+                               (!begins && ti == lo ? FROM_BEFORE : 0) | (!ends && ti + 1 == hi ? GOES_ON : 0));
+        }
+      }
+#pragma unroll
+      for (int q = 0; q < MORE; ++q)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {  // (all loads before the first use)
+          const int l = SLAB * k + lane;
+          row[q][k] = warp + q * WARPS < m && l < s[q].y ? plan.rows[s[q].x + l] : -1;
+        }
+#pragma unroll
+      for (int q = 0; q < MORE; ++q) {
+        const int j = warp + q * WARPS;
+        if (j >= m) break;
+        if (lane == 0) steps[j] = s[q];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int first_row = __shfl_sync(0xFFFFFFFFu, row[q][k], 0);
+          const bool box = __all_sync(0xFFFFFFFFu, row[q][k] >= 0 && row[q][k] == first_row + lane);
+          row_of[j][SLAB * k + lane] = row[q][k];
+          if (lane == 0) box_of[j][k] = box ? first_row : -1;
+        }
+      }
     }
     __syncthreads();
     if (warp < 4) {
-      const int slab = warp & 1, block = warp >> 1, c = lane & 7;
-      const bool cols = c0 + 64 * block < C;
-      auto row_at = [&](int j) {  // this lane's row of step j
-        const int at = SLAB * slab + lane;
-        return j < m && at < steps[j].count ? plan.rows[steps[j].start + at] : -1;
-      };
-      int row = row_at(0);
-      for (int j = 0; j < m && alive; ++j) {
-        const Step s = steps[j];
-        const Slab q = slab_of(row);
-        row = row_at(j + 1);
-        if (s.count == 0) continue;
-        const int st = i % stages;
-        if (i >= stages) alive = __all_sync(0xFFFFFFFFu, mbar_wait(&empty[st], (i / stages - 1) & 1, g));
-        if (!alive) break;
-        const uint32_t at = ring + st * stage, dst = at + block * (KB * 128) + slab * (SLAB * 128);
-        const int up = (s.count + ALIGN - 1) / ALIGN * ALIGN - SLAB * slab;  // rows of the slab that the MMAs read
-        const bool box = cols && q.box && q.count == SLAB;
-        if (lane == 0) {
-          const uint32_t bytes = (box ? SLAB * 128 : 0) + (warp == 0 ? KB * rank_bytes(rp) : 0);
-          if (bytes) mbar_expect_tx(&full[st], bytes);
-          if (box) tma_2d(dst, &mx, &full[st], c0 + 64 * block, q.first);
-          if (warp == 0) {
-            tma_2d(at + KB * 256, &mu, &full[st], 0, s.start);
-            if (rp > 64) tma_2d(at + KB * 256 + KB * 128, &mu, &full[st], 64, s.start);
-          }
-        }
-        if (!box) {
-          // row by row, with zeros where there is no row or no column
-#pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            const int l = (lane >> 3) + 4 * k, id = __shfl_sync(0xFFFFFFFFu, q.row, l), col = c0 + 64 * block + c * 8;
-            const bool in = id >= 0 && col < C;
-            if (l < up) cp16(piece(dst, l, c), in ? X + (size_t)id * C + col : X, in);
-          }
-          cp_commit();
+      const int c = lane & 7;
+      const bool two = c0 + 64 < C;  // (the second block of 64 columns has some)
+      int landing = -1;              // the stage of a step whose rows are still being copied one by one
+      auto landed = [&](bool behind) {  // (behind: another step's copies have been issued since)
+        if (behind)
+          cp_wait<1>();
+        else
           cp_wait<0>();
-          fence_async_shared();
+        fence_async_shared();
+        __syncwarp();
+        if (elect_one()) mbar_arrive(&full[landing]);
+        __syncwarp();
+        landing = -1;
+      };
+      int start = uniform(steps[0].x), count = uniform(steps[0].y), box = uniform(box_of[0][warp]);
+      for (int j = 0; j < m; ++j) {
+        const int from = start, now = count, first = box;
+        if (j + 1 < m) start = uniform(steps[j + 1].x), count = uniform(steps[j + 1].y), box = uniform(box_of[j + 1][warp]);
+        const uint32_t at = ring + st * stage, dst = at + warp * (SLAB * 128);
+        if (turn > 0) alive = alive && warp_wait(&empty[st], (turn - 1) & 1, g);
+        if (!alive) break;
+        const uint32_t extra = warp == 0 ? TILE * rank_bytes(rp) : 0;
+        if (first >= 0) {
+          if (elect_one()) {
+            mbar_arrive_expect_tx(&full[st], SLAB * 128 * (two ? 2 : 1) + extra);
+            tma_2d(dst, &mx, &full[st], c0, first);
+            if (two) tma_2d(dst + TILE * 128, &mx, &full[st], c0 + 64, first);
+          }
+        } else if (extra) {
+          if (elect_one()) mbar_expect_tx(&full[st], extra);
+        }
+        if (extra) {
+          if (elect_one()) {
+            tma_2d(at + TILE * 256, &mu, &full[st], 0, from);
+            if (rp > 64) tma_2d(at + TILE * 256 + TILE * 128, &mu, &full[st], 64, from);
+          }
         }
         __syncwarp();
-        if (lane == 0) mbar_arrive(&full[st]);
-        ++i;
-      }
-    } else if (warp == 4) {
-      if (lane == 0) {
-        const uint32_t urow = rp > 64 ? 128 : rank_bytes(rp), idesc = idesc_bf16_f32(TILE, rp) | A_MN | B_MN;
-        for (int j = 0; j < m && alive; ++j) {
-          const Step s = steps[j];
-          if (s.count == 0) continue;
-          const int st = i % stages, acc = run & 1;
-          alive = mbar_wait(&full[st], (i / stages) & 1, g);
-          if (alive && (s.flags & RUN_BEGINS) && run >= 2) alive = mbar_wait(&acc_empty[acc], (run / 2 - 1) & 1, g);
-          if (!alive) break;
-          tc_fence_after();
-          const uint32_t at = ring + st * stage;
-          const int ks = (s.count + ALIGN - 1) / ALIGN;
-          for (int k = 0; k < ks; ++k)
-            umma_bf16(tmem + acc * acc_cols, sdesc_mnmajor(at + 2048 * k, 128, KB * 128),
-                      sdesc_mnmajor(at + KB * 256 + ALIGN * urow * k, urow, KB * 128), idesc,
-                      k > 0 || !(s.flags & RUN_BEGINS));
-          tc_commit(&empty[st]);
-          if (s.flags & RUN_ENDS) {
-            tc_commit(&acc_full[acc]);
-            ++run;
-          }
-          ++i;
+        if (first < 0) {
+          // row by row, with zeros where there is no row (columns past the last are products that nobody reads)
+          const int up = (now + ALIGN - 1) / ALIGN * ALIGN - SLAB * warp;  // rows of the slab that the MMAs read
+          for (int k = 0; k < 2; ++k)
+#pragma unroll
+            for (int q = 0; q < 8; ++q) {
+              const int l = (lane >> 3) + 4 * q, id = row_of[j][SLAB * warp + l], col = c0 + 64 * k + c * 8;
+              const bool in = id >= 0 && col < C;
+              if (l < up) cp16(piece(dst + k * (TILE * 128), l, c), in ? X + (size_t)id * C + col : X, in);
+            }
+          cp_commit();
         }
+        if (landing >= 0) landed(first < 0);
+        if (first < 0) landing = st;
+        next_stage();
       }
-      __syncwarp();
+      if (landing >= 0) landed(false);
+    } else if (warp == 4) {
+      const uint32_t urow = rp > 64 ? 128 : rank_bytes(rp), idesc = idesc_bf16_f32(TILE, rp) | A_MN | B_MN;
+      for (int j = 0; j < m; ++j) {
+        const int count = uniform(steps[j].y), flags = uniform(steps[j].w), acc = run & 1;
+        alive = alive && warp_wait(&full[st], turn & 1, g);
+        if (alive && (flags & RUN_BEGINS) && run >= 2) alive = warp_wait(&acc_empty[acc], (run / 2 - 1) & 1, g);
+        if (!alive) break;
+        tc_fence_after();
+        const uint64_t x = sdesc_mnmajor(ring + st * stage, 128, TILE * 128);
+        const uint64_t u = sdesc_mnmajor(ring + st * stage + TILE * 256, urow, TILE * 128);
+        const uint32_t keep = (flags & RUN_BEGINS) ? 0u : 1u;
+        if (elect_one()) {
+#pragma unroll
+          for (int k = 0; k < TILE / ALIGN; ++k)
+            if (k * ALIGN < count)
+              umma_bf16(tmem + acc * acc_cols, x + (2048 >> 4) * k, u + urow * k, idesc, k > 0 ? 1u : keep);
+          tc_commit(&empty[st]);
+          if (flags & RUN_ENDS) tc_commit(&acc_full[acc]);
+        }
+        __syncwarp();
+        if (flags & RUN_ENDS) ++run;
+        next_stage();
+      }
     } else {
       const int quad = warp & 3, l = 32 * quad + lane;  // (a warp reads the tensor-memory lanes of its number modulo 4)
       for (int j = 0; j < m && alive; ++j) {
-        const Step s = steps[j];
-        if (s.count == 0) continue;
-        if (s.flags & RUN_BEGINS) before = (s.flags & FROM_BEFORE) != 0;
-        if (!(s.flags & RUN_ENDS)) continue;
+        const int adapter = steps[j].z, flags = steps[j].w;
+        if (flags & RUN_BEGINS) before = (flags & FROM_BEFORE) != 0;
+        if (!(flags & RUN_ENDS)) continue;
         const int acc = run & 1;
-        alive = __all_sync(0xFFFFFFFFu, mbar_wait(&acc_full[acc], (run / 2) & 1, g));
+        alive = warp_wait(&acc_full[acc], (run / 2) & 1, g);
         if (!alive) break;
         tc_fence_after();
-        // to the gradient, or to shared memory: head for the CTA in which the run began, the ring (nothing uses it
-        // behind the last step) for this CTA's own last run
-        const bool goes_on = (s.flags & GOES_ON) != 0;
+        // to the gradient, or to shared memory for the cluster: head for a run from before, the ring (nothing uses it
+        // behind the last step) for one that begins here and goes on
+        const bool goes_on = (flags & GOES_ON) != 0;
         unsigned char* keep = before ? head : goes_on ? smem : nullptr;
         for (int cc = 0; cc < rp; cc += 32) {
           float v[32];
@@ -631,15 +720,15 @@ __global__ void __launch_bounds__(WGRAD_THREADS) k_wgrad(const __grid_constant__
                 *reinterpret_cast<float4*>(keep + (((cc >> 2) + k) * TILE + l) * 16) =
                     make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
           } else if (c0 + l < C) {
-            __nv_bfloat16* out = dP + ((size_t)s.adapter * r + cc) * C + c0 + l;
+            __nv_bfloat16* out = dP + ((size_t)adapter * r + cc) * C + c0 + l;
 #pragma unroll
             for (int k = 0; k < 32; ++k)
               if (cc + k < r) out[(size_t)k * C] = __float2bfloat16_rn(v[k]);
           }
         }
         if (l == 0) {
-          if (before) head_adapter = s.adapter, head_through = goes_on;
-          if (!before && goes_on) tail_adapter = s.adapter;
+          if (before) head_through = goes_on;
+          if (!before && goes_on) tail_adapter = adapter;
         }
         tc_fence_before();
         __syncwarp();
@@ -648,39 +737,56 @@ __global__ void __launch_bounds__(WGRAD_THREADS) k_wgrad(const __grid_constant__
       }
     }
   }
+  if (warp >= 5 && c0 + 4 * lane < C)  // adapters without rows
+    for (int a = rank + size * (warp - 5); a < G; a += 4 * size)
+      if (plan.first[a] == plan.first[a + 1])
+        for (int j = 0; j < r; ++j) *reinterpret_cast<uint2*>(dP + ((size_t)a * r + j) * C + c0 + 4 * lane) = make_uint2(0, 0);
   if (warp == 4) {
-    if (lane == 0) {
-      tc_commit(&done);
-      mbar_wait(&done, 0, WaitGuard{&never, status, limit_ns});
-    }
+    if (elect_one()) tc_commit(&done);  // (the same lane is elected throughout: its commit covers all that was issued)
+    __syncwarp();
+    wait_on(&done, 0, WaitGuard{&never, status, limit_ns});
   } else if (warp < 4 && lane == 0 && abort_) {
     settle(full, stages, i, &never);
   }
   __syncwarp();
   cluster_sync();
-  if (tail_adapter >= 0 && !abort_) {
-    const int a = tail_adapter;
-    int last = rank;  // the last CTA with a part of the run
-    for (int c = rank + 1; c < (int)size; ++c) {
-      if (share(c) == share(c + 1)) continue;
-      if (ld_cluster_int(mapa_shared(smem_u32(&head_adapter), c)) != a) break;
-      last = c;
-      if (!ld_cluster_int(mapa_shared(smem_u32(&head_through), c))) break;
-    }
-    for (int k = threadIdx.x; k < TILE * (r / 4); k += WGRAD_THREADS) {
-      const int l = k % TILE, q = k / TILE;
-      float4 s = *reinterpret_cast<const float4*>(smem + (q * TILE + l) * 16);
-      for (int c = rank + 1; c <= last; ++c) {
-        if (share(c) == share(c + 1)) continue;
-        const float4 v = ld_cluster(mapa_shared(smem_u32(head) + (q * TILE + l) * 16, c));
-        s.x += v.x, s.y += v.y, s.z += v.z, s.w += v.w;
+  if (size > 1 && !abort_) {
+    // the runs that cross shares: the one that begins in CTA c, its heads in the next ones up to where it ends
+    int adapter[8], through[8];
+#pragma unroll
+    for (int c = 0; c < 8; ++c)
+      if (c < (int)size) {
+        adapter[c] = ld_cluster_int(mapa_shared(smem_u32(&tail_adapter), c));
+        through[c] = ld_cluster_int(mapa_shared(smem_u32(&head_through), c));
       }
-      if (c0 + l < C) {
-        __nv_bfloat16* out = dP + ((size_t)a * r + 4 * q) * C + c0 + l;
-        out[0] = __float2bfloat16_rn(s.x);
-        out[(size_t)C] = __float2bfloat16_rn(s.y);
-        out[(size_t)2 * C] = __float2bfloat16_rn(s.z);
-        out[(size_t)3 * C] = __float2bfloat16_rn(s.w);
+#pragma unroll
+    for (int c = 0; c < 8; ++c) {
+      if (c >= (int)size || adapter[c] < 0) continue;
+      uint32_t parts = 0;  // bit d: CTA d holds a head of the run
+      bool open = true;
+#pragma unroll
+      for (int d = 0; d < 8; ++d)
+        if (d > c && d < (int)size && open && share(d) < share(d + 1)) {
+          parts |= 1u << d;
+          open = through[d] != 0;
+        }
+      const int items = TILE * (r / 4);
+      for (int k = threadIdx.x + rank * WGRAD_THREADS; k < items; k += WGRAD_THREADS * size) {
+        const int l = k % TILE, q = k / TILE;
+        const uint32_t at = (q * TILE + l) * 16;
+        float4 s = ld_cluster(mapa_shared(ring + at, c)), v[8];
+#pragma unroll
+        for (int d = 1; d < 8; ++d)
+          v[d] = (parts >> d) & 1 ? ld_cluster(mapa_shared(smem_u32(head) + at, d)) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+        for (int d = 1; d < 8; ++d) s.x += v[d].x, s.y += v[d].y, s.z += v[d].z, s.w += v[d].w;
+        if (c0 + l < C) {
+          __nv_bfloat16* out = dP + ((size_t)adapter[c] * r + 4 * q) * C + c0 + l;
+          out[0] = __float2bfloat16_rn(s.x);
+          out[(size_t)C] = __float2bfloat16_rn(s.y);
+          out[(size_t)2 * C] = __float2bfloat16_rn(s.z);
+          out[(size_t)3 * C] = __float2bfloat16_rn(s.w);
+        }
       }
     }
   }
@@ -693,46 +799,47 @@ __global__ void __launch_bounds__(WGRAD_THREADS) k_wgrad(const __grid_constant__
 }
 
 // ---------------------------------------------------------------------------
-// k_expand: y = base + h Q, persistent over units of (tile, 128 columns); a CTA
-// takes neighbouring units, about the same number of 32-row slabs each.
-// Warps 0 to 3 load 32 rows each, 4 to 11 write out 32 rows x 64 columns each,
-// 12 issues the MMAs; two accumulators.
+// k_expand: y = base + h Q over units of (tile, 128 columns).  Several CTAs per
+// SM, each with a stretch of neighbouring units that cost about the same
+// together.  A CTA multiplies, adds and stores one unit at a time while the
+// next one's rows of base are on their way (where shared memory has room for
+// them), and the SM's other CTAs fill its waits.
+// Warps 0 to 3 load 32 rows each, warp 4 issues the MMAs, all eight add and
+// store 32 rows x 64 columns each.
 // ---------------------------------------------------------------------------
-constexpr int EXPAND_THREADS = 416;
-__host__ __device__ constexpr int expand_stages(int rp) { return rp <= 32 ? 4 : rp <= 64 ? 3 : 2; }
+constexpr int EXPAND_THREADS = 256;
 __host__ __device__ constexpr int expand_q(int rp) { return rp * 256; }
-__host__ __device__ constexpr int expand_stage(int rp) { return TILE * 256 + expand_q(rp) + TILE * rank_bytes(rp); }
-constexpr int expand_bytes(int rp) { return expand_stages(rp) * expand_stage(rp) + 1024; }
+__host__ __device__ constexpr int expand_ahead(int rp) { return rp <= 64 ? 1 : 0; }  // units of base loaded ahead
+constexpr int expand_bytes(int rp) {
+  return (1 + expand_ahead(rp)) * TILE * 256 + expand_q(rp) + TILE * rank_bytes(rp) + 1024;
+}
 
-__global__ void __launch_bounds__(EXPAND_THREADS) k_expand(const __grid_constant__ CUtensorMap mh,
-                                                           const __grid_constant__ CUtensorMap mq,
-                                                           const __grid_constant__ CUtensorMap mb,
-                                                           const __grid_constant__ CUtensorMap my,
-                                                           const __nv_bfloat16* base, int N, int r, int rp, Plan plan,
-                                                           __nv_bfloat16* y, uint64_t limit_ns, int32_t* status) {
+__global__ void __launch_bounds__(EXPAND_THREADS, 3) k_expand(const __grid_constant__ CUtensorMap mh,
+                                                              const __grid_constant__ CUtensorMap mq,
+                                                              const __grid_constant__ CUtensorMap mb,
+                                                              const __grid_constant__ CUtensorMap my,
+                                                              const __grid_constant__ CUtensorMap mb8,
+                                                              const __grid_constant__ CUtensorMap my8,
+                                                              const __nv_bfloat16* base, int N, int r, int rp, Plan plan,
+                                                              __nv_bfloat16* y, uint64_t limit_ns, int32_t* status) {
   extern __shared__ unsigned char smem_[];
   unsigned char* smem = aligned_smem(smem_);
-  __shared__ uint64_t full[4], empty[4], acc_full[2], acc_empty[2], done;
+  __shared__ uint64_t rows_in[2], product_in, product_out;  // base's rows, h and Q in shared memory; the MMAs' end
   __shared__ int abort_, never, begin_tile, begin_chunk;
   __shared__ uint32_t tmem_;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int stages = expand_stages(rp);
-  const uint32_t ring = smem_u32(smem), stage = expand_stage(rp), q_at = TILE * 256, h_at = q_at + expand_q(rp);
+  const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31, slab = warp & 3, block = warp >> 2;
+  const int ahead = expand_ahead(rp);
+  const uint32_t at = smem_u32(smem), q_at = at + (1 + ahead) * (TILE * 256), h_at = q_at + expand_q(rp);
   if (threadIdx.x == 0) {
-    for (int i = 0; i < stages; ++i) {
-      mbar_init(&full[i], 4 * 32);
-      mbar_init(&empty[i], 8);
-    }
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(&acc_full[i], 1);
-      mbar_init(&acc_empty[i], 8);
-    }
-    mbar_init(&done, 1);
+    mbar_init(&rows_in[0], 4 * 32);
+    mbar_init(&rows_in[1], 4 * 32);
+    mbar_init(&product_in, 1);
+    mbar_init(&product_out, 1);
     abort_ = never = 0;
     fence_barrier_init();
   }
-  if (warp == 12) {
-    tmem_alloc(&tmem_, 2 * TILE);
+  if (warp == 4) {
+    tmem_alloc(&tmem_, TILE);
     tmem_relinquish();
   }
   launch_dependents();
@@ -755,179 +862,198 @@ __global__ void __launch_bounds__(EXPAND_THREADS) k_expand(const __grid_constant
   __syncthreads();
   tc_fence_after();
   const WaitGuard g{&abort_, status, limit_ns};
-  const uint32_t tmem = tmem_;
-  struct Walk {  // this CTA's units in turn
-    Tile t, next;
-    int tile, chunk;
-  } w{{}, {}, tiles, 0};
-  auto fetch = [&](int tile) { return tile < tiles ? plan.tiles[tile] : Tile{-1, 0, 0, 0}; };
-  auto more = [&] { return w.tile < tiles && (int64_t)w.t.cost * chunks + (int64_t)w.chunk * tile_cost(w.t.count) < hi; };
-  auto advance = [&] {
-    if (++w.chunk < chunks) return false;
-    w.chunk = 0;
-    w.t = w.next;
-    w.next = fetch(++w.tile + 1);
-    return true;  // another tile
+  const uint32_t tmem = uniform(tmem_);
+  const uint32_t idesc = idesc_bf16_f32(TILE, TILE) | B_MN, hrow = rp > 64 ? 128 : rank_bytes(rp);
+
+  // a tile of this CTA: its chunks up to `end`, and the warp's slab of it
+  struct Part {
+    int adapter, start, end;
+    Slab s;
   };
-  w.tile = lo < hi ? begin_tile : tiles;
-  w.chunk = begin_chunk;
-  w.t = fetch(w.tile);
-  w.next = fetch(w.tile + 1);
-  auto places = [&](const Tile& t, int slab) {  // this lane's row in a slab of the tile
-    const int at = SLAB * slab + lane;
-    return at < t.count ? plan.rows[t.start + at] : -1;
+  auto part_of = [&](int tile) {
+    Part p{-1, 0, 0, {}};
+    int row = -1;
+    if (tile < tiles) {
+      const Tile t = plan.tiles[tile];
+      const int64_t from = (int64_t)t.cost * chunks, each = tile_cost(t.count);
+      p.adapter = uniform(t.adapter);
+      p.start = uniform(t.start);
+      p.end = uniform(hi > from ? (int)min((int64_t)chunks, (hi - from + each - 1) / each) : 0);
+      const int place = SLAB * slab + lane;
+      if (place < t.count) row = plan.rows[t.start + place];
+    }
+    p.s = slab_of(row);
+    p.s.first = uniform(p.s.first);
+    p.s.count = uniform(p.s.count);
+    return p;
   };
-  int i = 0;
-  bool alive = true;
-  if (warp < 4) {
-    Slab s = slab_of(places(w.t, warp));
-    int ahead = places(w.next, warp);
-    while (more()) {
-      const int st = i % stages;
-      if (i >= stages) alive = __all_sync(0xFFFFFFFFu, mbar_wait(&empty[st], (i / stages - 1) & 1, g));
-      if (!alive) break;
-      const uint32_t at = ring + st * stage;
-      const int c0 = w.chunk * TILE;
-      const bool two = c0 + 64 < N;  // (the second block of 64 columns has some)
-      const bool product = warp == 0 && w.t.adapter >= 0;
-      const bool box = base && s.count > 0 && s.box && s.count >= MIN_BOX;
-      if (lane == 0) {
-        const uint32_t bytes = (box ? SLAB * 128 * (two ? 2 : 1) : 0) +
-                               (product ? rp * 128 * (two ? 2 : 1) + TILE * rank_bytes(rp) : 0);
-        if (bytes) mbar_expect_tx(&full[st], bytes);
-        if (box) {
-          tma_2d(at + warp * (SLAB * 128), &mb, &full[st], c0, s.first);
-          if (two) tma_2d(at + TILE * 128 + warp * (SLAB * 128), &mb, &full[st], c0 + 64, s.first);
-        }
-        if (product) {
-          tma_2d(at + h_at, &mh, &full[st], 0, w.t.start);
-          if (rp > 64) tma_2d(at + h_at + TILE * 128, &mh, &full[st], 64, w.t.start);
-          tma_3d(at + q_at, &mq, &full[st], c0, 0, w.t.adapter);
-          if (two) tma_3d(at + q_at + rp * 128, &mq, &full[st], c0 + 64, 0, w.t.adapter);
-        }
+  // the rows of base of one unit; every lane of warps 0 to 3 arrives once
+  auto load_rows = [&](const Part& p, int chunk, int buf) {
+    const int c0 = chunk * TILE;
+    const uint32_t to = at + buf * (TILE * 256) + warp * (SLAB * 128);
+    const bool two = c0 + 64 < N;
+    uint64_t* bar = &rows_in[buf];
+    if (!base || p.s.count == 0) {
+      if (elect_one()) mbar_arrive_warp(bar);
+    } else if (p.s.box) {
+      if (elect_one()) {
+        mbar_expect_tx(bar, SLAB * 128 * (two ? 2 : 1));
+        tma_2d(to, &mb, bar, c0, p.s.first);
+        if (two) tma_2d(to + TILE * 128, &mb, bar, c0 + 64, p.s.first);
+        mbar_arrive_warp(bar);
       }
-      if (base && !box && s.count > 0) {
-        const int c = lane & 15;
-        for (int l = lane >> 4; l < SLAB; l += 2) {
-          const int id = __shfl_sync(0xFFFFFFFFu, s.row, l);
-          if (id >= 0 && c0 + c * 8 < N)
-            cp16(piece(at + (c >> 3) * (TILE * 128), warp * SLAB + l, c & 7), base + (size_t)id * N + c0 + c * 8, true);
-        }
-        __syncwarp();
-        cp_arrive(&full[st]);
-      } else {
-        __syncwarp();
-        mbar_arrive(&full[st]);
+    } else {
+      // neighbours by eights as boxes, by the first lane of each eight
+      const bool near = (p.s.near >> lane) & 1;
+      if ((lane & 7) == 0 && near && p.s.row >= 0) {
+        mbar_expect_tx(bar, 8 * 128 * (two ? 2 : 1));
+        tma_2d(to + lane * 128, &mb8, bar, c0, p.s.row);
+        if (two) tma_2d(to + TILE * 128 + lane * 128, &mb8, bar, c0 + 64, p.s.row);
       }
-      ++i;
-      if (advance()) {
-        s = slab_of(ahead);
-        ahead = places(w.next, warp);
-      }
-    }
-    cp_wait<0>();
-    if (lane == 0 && abort_) settle(full, stages, i, &never);
-  } else if (warp == 12) {
-    if (lane == 0) {
-      const uint32_t idesc = idesc_bf16_f32(TILE, TILE) | B_MN, hrow = rp > 64 ? 128 : rank_bytes(rp);
-      while (more()) {
-        const int st = i % stages, acc = i & 1;
-        alive = mbar_wait(&full[st], (i / stages) & 1, g);
-        if (alive && i >= 2) alive = mbar_wait(&acc_empty[acc], (i / 2 - 1) & 1, g);
-        if (!alive) break;
-        tc_fence_after();
-        const uint32_t at = ring + st * stage;
-        if (w.t.adapter >= 0)
-          for (int k = 0; k < rp / 16; ++k)
-            umma_bf16(tmem + acc * TILE, sdesc_kmajor(at + h_at + (k >> 2) * (TILE * 128) + 32 * (k & 3), hrow),
-                      sdesc_mnmajor(at + q_at + 2048 * k, 128, rp * 128), idesc, k > 0);
-        tc_commit(&acc_full[acc]);
-        ++i;
-        advance();
-      }
-      tc_commit(&done);
-      mbar_wait(&done, 0, WaitGuard{&never, status, limit_ns});
-    }
-  } else {
-    const int slab = warp & 3, block = (warp - 4) >> 2;  // (a warp reads the tensor-memory lanes of its number modulo 4)
-    Slab s = slab_of(places(w.t, slab));
-    int ahead = places(w.next, slab);
-    int stored = -1;  // the stage whose box is on its way out
-    while (more()) {
-      const int st = i % stages, acc = i & 1, c0 = w.chunk * TILE + 64 * block;
-      alive = __all_sync(0xFFFFFFFFu, mbar_wait(&full[st], (i / stages) & 1, g) && mbar_wait(&acc_full[acc], (i / 2) & 1, g));
-      if (!alive) break;
-      tc_fence_after();
-      const uint32_t at = ring + st * stage + block * (TILE * 128) + slab * (SLAB * 128);
-      unsigned char* mine = smem + (at - ring);
-      if (s.count > 0 && c0 < N) {
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          float v[32];
-          if (w.t.adapter >= 0) {
-            tmem_ld32(tmem + acc * TILE + ((uint32_t)(32 * slab) << 16) + 64 * block + 32 * half, v);
-          } else {
-#pragma unroll
-            for (int k = 0; k < 32; ++k) v[k] = 0.0f;
-          }
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            uint4* p = reinterpret_cast<uint4*>(mine + (piece(0, lane, 4 * half + k)));
-            uint4 o = base ? *p : make_uint4(0, 0, 0, 0);
-            const float* a = v + 8 * k;
-            o.x = pack_bf16x2(bf16_lo(o.x) + a[0], bf16_hi(o.x) + a[1]);
-            o.y = pack_bf16x2(bf16_lo(o.y) + a[2], bf16_hi(o.y) + a[3]);
-            o.z = pack_bf16x2(bf16_lo(o.z) + a[4], bf16_hi(o.z) + a[5]);
-            o.w = pack_bf16x2(bf16_lo(o.w) + a[6], bf16_hi(o.w) + a[7]);
-            *p = o;
-          }
-        }
-      }
-      tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&acc_empty[acc]);
-      // the stage before this one is free once its box has been read
-      const bool box = s.box && s.count == SLAB && c0 < N;
-      if (box) {
-        fence_async_shared();
-        __syncwarp();
-        if (lane == 0) {
-          tma_store_2d(&my, at, c0, s.first);
+      if (p.s.near == 0xFFFFFFFFu) {
+        if (lane == 0) mbar_arrive_warp(bar);
+      } else {
+        const int c = lane & 15;
+        for (uint32_t m = ~p.s.near & 0x01010101u; m; m &= m - 1) {
+          const int l0 = __ffs(m) - 1 + (lane >> 4);
+#pragma unroll
+          for (int l = l0; l < l0 + 8; l += 2) {
+            const int id = __shfl_sync(0xFFFFFFFFu, p.s.row, l);
+            if (id >= 0 && c0 + c * 8 < N)
+              cp16(piece(to + (c >> 3) * (TILE * 128), l, c & 7), base + (size_t)id * N + c0 + c * 8, true);
+          }
+        }
+        cp_arrive(bar);
+      }
+    }
+    __syncwarp();
+  };
+  auto load_product = [&](const Part& p, int chunk, bool fresh) {  // warp 0
+    if (!elect_one()) return;
+    const int c0 = chunk * TILE;
+    const bool two = c0 + 64 < N;  // (the second block of 64 columns has some)
+    mbar_arrive_expect_tx(&product_in, rp * 128 * (two ? 2 : 1) + (fresh ? TILE * rank_bytes(rp) : 0));
+    if (fresh) {
+      tma_2d(h_at, &mh, &product_in, 0, p.start);
+      if (rp > 64) tma_2d(h_at + TILE * 128, &mh, &product_in, 64, p.start);
+    }
+    tma_3d(q_at, &mq, &product_in, c0, 0, p.adapter);
+    if (two) tma_3d(q_at + rp * 128, &mq, &product_in, c0 + 64, 0, p.adapter);
+  };
+
+  int tile = lo < hi ? begin_tile : tiles, chunk = begin_chunk;
+  Part now = part_of(tile), next = part_of(tile + 1);
+  bool more = tile < tiles && chunk < now.end;
+  int turn[2] = {0, 0}, products = 0, buf = 0;
+  if (more) {
+    if (warp < 4) load_rows(now, chunk, 0);
+    if (warp == 0 && now.adapter >= 0) load_product(now, chunk, true);
+    __syncwarp();
+  }
+  while (more) {
+    const bool last = chunk + 1 == now.end;  // of this tile
+    const bool product = now.adapter >= 0, another = !last || next.end > 0;
+    const int c0 = chunk * TILE, next_chunk = last ? 0 : chunk + 1;
+    if (ahead && another && warp < 4) load_rows(last ? next : now, next_chunk, buf ^ 1);
+    bool ok = true;
+    if (product) {
+      if (warp == 4) {
+        const bool in = warp_wait(&product_in, products & 1, g);
+        tc_fence_after();
+        const uint64_t h = sdesc_kmajor(h_at, hrow), q = sdesc_mnmajor(q_at, 128, rp * 128);
+        if (elect_one()) {
+          if (in)
+#pragma unroll
+            for (int k = 0; k < MAX_R / 16; ++k)
+              if (16 * k < rp) umma_bf16(tmem, h + ((k >> 2) * (TILE * 128) + 32 * (k & 3)) / 16, q + (2048 >> 4) * k, idesc, k > 0);
+          tc_commit(&product_out);
+        }
+      }
+      __syncwarp();
+      ok = wait_on(&product_out, products & 1, g);
+      ++products;
+    }
+    // (h and Q have been read: the next unit's may come)
+    ok = __all_sync(0xFFFFFFFFu, ok);
+    if (warp == 0 && ok && another && (last ? next : now).adapter >= 0) load_product(last ? next : now, next_chunk, last);
+    __syncwarp();
+    ok &= wait_on(&rows_in[buf], turn[buf] & 1, g);
+    ++turn[buf];
+    tc_fence_after();
+    const int col = c0 + 64 * block;
+    const uint32_t mine = at + buf * (TILE * 256) + block * (TILE * 128) + slab * (SLAB * 128);
+    const Slab& s = now.s;
+    if (__all_sync(0xFFFFFFFFu, ok) && s.count > 0 && col < N) {
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        float v[32];
+        if (product) {
+          tmem_ld32(tmem + ((uint32_t)(32 * slab) << 16) + 64 * block + 32 * half, v);
+        } else {
+#pragma unroll
+          for (int k = 0; k < 32; ++k) v[k] = 0.0f;
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          uint4* p = reinterpret_cast<uint4*>(smem + (piece(mine, lane, 4 * half + k) - at));
+          uint4 o = base ? *p : make_uint4(0, 0, 0, 0);
+          const float* a = v + 8 * k;
+          o.x = pack_bf16x2(bf16_lo(o.x) + a[0], bf16_hi(o.x) + a[1]);
+          o.y = pack_bf16x2(bf16_lo(o.y) + a[2], bf16_hi(o.y) + a[3]);
+          o.z = pack_bf16x2(bf16_lo(o.z) + a[4], bf16_hi(o.z) + a[5]);
+          o.w = pack_bf16x2(bf16_lo(o.w) + a[6], bf16_hi(o.w) + a[7]);
+          *p = o;
+        }
+      }
+      fence_async_shared();
+      __syncwarp();
+      if (s.whole == 0xFFFFFFFFu && s.box) {
+        if (elect_one()) {
+          tma_store_2d(&my, mine, col, s.first);
           bulk_commit();
         }
-      } else if (s.count > 0 && c0 < N) {
-        const int c = lane & 7;
-        for (int l = lane >> 3; l < SLAB; l += 4) {
+      } else if ((lane & 7) == 0 && ((s.whole >> lane) & 1)) {
+        tma_store_2d(&my8, mine + lane * 128, col, s.row);
+        bulk_commit();
+      }
+      for (uint32_t m = ~s.whole & 0x01010101u; m; m &= m - 1) {
+        const int l0 = __ffs(m) - 1 + (lane >> 3), c = lane & 7;
+#pragma unroll
+        for (int l = l0; l < l0 + 8; l += 4) {
           const int id = __shfl_sync(0xFFFFFFFFu, s.row, l);
-          if (id >= 0 && c0 + c * 8 < N)
-            *reinterpret_cast<uint4*>(y + (size_t)id * N + c0 + c * 8) = *reinterpret_cast<const uint4*>(mine + piece(0, l, c));
+          if (id >= 0 && col + c * 8 < N)
+            *reinterpret_cast<uint4*>(y + (size_t)id * N + col + c * 8) =
+                *reinterpret_cast<const uint4*>(smem + (piece(mine, l, c) - at));
         }
       }
-      __syncwarp();
-      if (lane == 0) {
-        if (stored >= 0) {
-          if (box)
-            asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
-          else
-            bulk_wait_read_all();
-          mbar_arrive(&empty[stored]);
-        }
-        if (!box) mbar_arrive(&empty[st]);
-      }
-      stored = box ? st : -1;
-      ++i;
-      if (advance()) {
-        s = slab_of(ahead);
-        ahead = places(w.next, slab);
-      }
+      bulk_wait_read_all();
     }
-    if (lane == 0) bulk_wait_read_all();
+    tc_fence_before();
+    ok = __syncthreads_and(ok);  // (the unit's rows and its accumulator are free)
+    tc_fence_after();
+    if (!ok) break;
+    chunk = next_chunk;
+    if (last) {
+      now = next;
+      next = part_of(++tile + 1);
+    }
+    more = another;
+    if (!ahead && another && warp < 4) load_rows(now, chunk, 0);
+    if (ahead) buf ^= 1;
   }
+  cp_wait<0>();
+  if (abort_ && warp == 0 && lane == 0) {
+    wait_on(&rows_in[0], turn[0] & 1, WaitGuard{&never, nullptr, 1000000});
+    wait_on(&rows_in[1], turn[1] & 1, WaitGuard{&never, nullptr, 1000000});
+    wait_on(&product_in, products & 1, WaitGuard{&never, nullptr, 1000000});
+  }
+  if (warp == 4 && products > 0) wait_on(&product_out, (products - 1) & 1, WaitGuard{&never, status, limit_ns});
   tc_fence_before();
   __syncthreads();
-  if (warp == 12) {
+  if (warp == 4) {
     tc_fence_after();
-    tmem_dealloc(tmem, 2 * TILE);
+    tmem_dealloc(tmem, TILE);
   }
 }
 
@@ -1041,7 +1167,8 @@ Plan plan_at(void* ws, int T, int G) {
 template <class... A, class... B>
 moe_status_t launch(void (*k)(A...), int ctas, int cluster, int threads, int smem, int smem_limit, bool dependent,
                     cudaStream_t stream, const B&... args) {
-  if (smem_limit && !set_smem_limit((const void*)k, smem_limit)) return MOE_ERR_CUDA;  // (one limit per kernel)
+  // (one limit per kernel)
+  if (smem_limit && (!set_smem_limit((const void*)k, smem_limit) || !prefer_shared((const void*)k))) return MOE_ERR_CUDA;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(ctas);
   cfg.blockDim = dim3(threads);
@@ -1094,9 +1221,12 @@ moe_status_t group(const int32_t* idx, int T, int G, const Plan& p, cudaStream_t
 }
 
 // CTAs per cluster that share a contraction of `blocks` stages: as many as the
-// SMs hold at once with `clusters` of them, and two stages each at least.
-int split_of(const void* kernel, int threads, int smem, int clusters, int blocks) {
-  const int slots = sm_count() * max_active_blocks(kernel, threads, smem);
+// SMs hold at once with `clusters` of them (by their shared memory, static and
+// dynamic, of which an SM has 228 KB and each CTA takes 1 KB more than it asks
+// for), and two stages each at least.
+int split_of(int smem, int clusters, int blocks) {
+  const int slots = sm_count() * (228 * 1024 / (smem + 1024));
+
   int s = slots / (clusters > 0 ? clusters : 1);
   if (s > blocks / 2) s = blocks / 2;
   return s < 1 ? 1 : s > 8 ? 8 : s;
@@ -1105,8 +1235,7 @@ int split_of(const void* kernel, int threads, int smem, int clusters, int blocks
 moe_status_t shrink(const moe_bf16* x, const moe_bf16* P, const float* scale, int T, int K, int r, int G, const Plan& p,
                     moe_bf16* h, moe_bf16* hs, const moe_bf16* other, moe_bf16* others, int32_t* st, cudaStream_t s) {
   const int rp = pad16(r), tiles = max_tiles(T, G), bytes = shrink_bytes(rp);
-  if (!set_smem_limit((const void*)k_shrink, shrink_bytes(MAX_R))) return MOE_ERR_CUDA;
-  const int split = split_of((const void*)k_shrink, SHRINK_THREADS, bytes, tiles, (K + KB - 1) / KB);
+  const int split = split_of(bytes + 1024, tiles, (K + KB - 1) / KB);
   CUtensorMap mx, mp;
   if (!map_rows(&mx, x, T, K, 64, SLAB) || !map_weight(&mp, P, G, r, K, rp)) return MOE_ERR_CUDA;
   return launch(k_shrink, tiles * split, split, SHRINK_THREADS, bytes, shrink_bytes(MAX_R), true, s, mx, mp, in(x), scale, K,
@@ -1116,11 +1245,13 @@ moe_status_t shrink(const moe_bf16* x, const moe_bf16* P, const float* scale, in
 moe_status_t wgrad(const moe_bf16* x, const moe_bf16* us, int T, int C, int r, int G, const Plan& p, moe_bf16* dP,
                    int32_t* st, cudaStream_t s) {
   const int rp = pad16(r), units = (C + TILE - 1) / TILE, bytes = wgrad_bytes(rp);
-  if (!set_smem_limit((const void*)k_wgrad, wgrad_bytes(MAX_R))) return MOE_ERR_CUDA;
-  const int split = split_of((const void*)k_wgrad, WGRAD_THREADS, bytes, units, T / KB);
+  const int split = split_of(bytes + 10 * 1024, units, T / TILE);
+
   CUtensorMap mx, mu;
-  if (!map_rows(&mx, x, T, C, 64, SLAB) || !map_rows(&mu, us, places(T, G), r, rank_cols(rp), KB)) return MOE_ERR_CUDA;
-  return launch(k_wgrad, units * split, split, WGRAD_THREADS, bytes, wgrad_bytes(MAX_R), true, s, mx, mu, in(x), C, r, rp, G,
+  if (!map_rows(&mx, x, T, C, 64, SLAB) || !map_rows(&mu, us, places(T, G), r, rank_cols(rp), TILE)) return MOE_ERR_CUDA;
+  // (not a programmatic dependent: its first clusters took places as the kernel before it left them, unevenly, and
+  // the backward of 8192 x 7168 took 154 us instead of 136)
+  return launch(k_wgrad, units * split, split, WGRAD_THREADS, bytes, wgrad_bytes(MAX_R), false, s, mx, mu, in(x), C, r, rp, G,
                 p, out(dP), g_wait_limit_ns.load(), st);
 }
 
@@ -1129,13 +1260,14 @@ moe_status_t expand(const moe_bf16* hs, const moe_bf16* Q, const moe_bf16* base,
   const int rp = pad16(r), sms = sm_count(), bytes = expand_bytes(rp);
   if (sms < 1) return MOE_ERR_CUDA;
   const int64_t units = (int64_t)max_tiles(T, G) * ((N + TILE - 1) / TILE);
-  const int grid = units < sms ? (int)units : sms;
-  CUtensorMap mh, mq, mb, my;
+  const int per_sm = 228 * 1024 / (bytes + 2048) < 3 ? 228 * 1024 / (bytes + 2048) : 3;  // (registers: three)
+  const int grid = units < sms * per_sm ? (int)units : sms * per_sm;
+  CUtensorMap mh, mq, mb, my, mb8, my8;
   if (!map_rows(&mh, hs, places(T, G), r, rank_cols(rp), TILE) || !map_weight(&mq, Q, G, r, N, rp) ||
-      !map_rows(&mb, base ? base : y, T, N, 64, SLAB) || !map_rows(&my, y, T, N, 64, SLAB))
+      !map_rows(&mb, base ? base : y, T, N, 64, SLAB) || !map_rows(&my, y, T, N, 64, SLAB) ||
+      !map_rows(&mb8, base ? base : y, T, N, 64, 8) || !map_rows(&my8, y, T, N, 64, 8))
     return MOE_ERR_CUDA;
-  constexpr int most = expand_bytes(32) > expand_bytes(MAX_R) ? expand_bytes(32) : expand_bytes(MAX_R);
-  return launch(k_expand, grid, 0, EXPAND_THREADS, bytes, most, true, s, mh, mq, mb, my, in(base), N, r, rp, p, out(y),
+  return launch(k_expand, grid, 0, EXPAND_THREADS, bytes, expand_bytes(MAX_R), true, s, mh, mq, mb, my, mb8, my8, in(base), N, r, rp, p, out(y),
                 g_wait_limit_ns.load(), st);
 }
 
