@@ -507,7 +507,7 @@ __global__ void __launch_bounds__(SHRINK_THREADS) k_shrink(const __grid_constant
 }
 
 // ---------------------------------------------------------------------------
-// k_wgrad: cluster (128 columns of X [T][C]), its CTAs share the tiles of all
+// k_wgrad: cluster (128 columns of x or dy, X [T][C]), its CTAs share the tiles of all
 // adapters: dP [G][r][C] = U^T X over each adapter's rows, U in the grouped
 // order.  An adapter's tiles that cross from one CTA's share into the next
 // ones' are summed by the whole cluster in the end.
@@ -522,11 +522,19 @@ constexpr int wgrad_bytes(int rp) { return wgrad_stages(rp) * wgrad_stage(rp) + 
 // of a step (a tile) in this CTA: the first / last of its run of one adapter; the run began before / goes on behind it
 enum { RUN_BEGINS = 1, RUN_ENDS = 2, FROM_BEFORE = 4, GOES_ON = 8 };
 
-__global__ void __launch_bounds__(WGRAD_THREADS) k_wgrad(const __grid_constant__ CUtensorMap mx,
-                                                         const __grid_constant__ CUtensorMap mu,
-                                                         const __nv_bfloat16* __restrict__ X, int C, int r, int rp, int G,
-                                                         Plan plan, __nv_bfloat16* __restrict__ dP, uint64_t limit_ns,
-                                                         int32_t* status) {
+// One of the two gradients, which share a launch: dA (x and u) and dB (dy and h).
+struct Side {
+  CUtensorMap mx, mu;
+  const __nv_bfloat16* X;
+  __nv_bfloat16* dP;
+  int C, units;  // units: 128 columns each
+};
+struct Sides {
+  Side of[2];
+};
+
+__global__ void __launch_bounds__(WGRAD_THREADS) k_wgrad(const __grid_constant__ Sides sides, int r, int rp, int G, Plan plan,
+                                                         uint64_t limit_ns, int32_t* status) {
   extern __shared__ unsigned char smem_[];
   unsigned char* smem = aligned_smem(smem_);
   __shared__ uint64_t full[3], empty[3], acc_full[2], acc_empty[2], done;
@@ -535,7 +543,13 @@ __global__ void __launch_bounds__(WGRAD_THREADS) k_wgrad(const __grid_constant__
   __shared__ int4 steps[BATCH];                        // first place, rows, adapter, flags
   __shared__ int row_of[BATCH][TILE], box_of[BATCH][4];  // rows of each step; the first one of 32 neighbours, or -1
   const uint32_t size = cluster_size(), rank = cluster_ctarank();
-  const int c0 = (int)(blockIdx.x / size) * TILE, warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
+  const int unit = (int)(blockIdx.x / size), second = unit >= sides.of[0].units ? 1 : 0;
+  const Side& side = sides.of[second];
+  const CUtensorMap &mx = side.mx, &mu = side.mu;
+  const __nv_bfloat16* const X = side.X;
+  __nv_bfloat16* const dP = side.dP;
+  const int C = side.C, c0 = (unit - (second ? sides.of[0].units : 0)) * TILE;
+  const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
   const int stages = wgrad_stages(rp);
   const uint32_t ring = smem_u32(smem), stage = wgrad_stage(rp), acc_cols = tmem_cols(rp);
   unsigned char* head = smem + stages * stage;  // float4 [rp / 4][128]: the run from before
@@ -1060,7 +1074,7 @@ __global__ void __launch_bounds__(EXPAND_THREADS, 3) k_expand(const __grid_const
 // ---------------------------------------------------------------------------
 // k_rows: few rows, one cluster per row, on the CUDA cores
 // ---------------------------------------------------------------------------
-constexpr int ROW_CTAS = 8, ROW_THREADS = 256;
+constexpr int ROW_CTAS = 8, ROW_THREADS = 256, ROW_COLS = ROW_THREADS / 2;
 
 __device__ __forceinline__ float dot8(uint4 a, uint4 b, float s) {
   const uint32_t x[4] = {a.x, a.y, a.z, a.w}, y[4] = {b.x, b.y, b.z, b.w};
@@ -1080,37 +1094,73 @@ __device__ __forceinline__ void add8(float* s, float f, uint4 q) {
   }
 }
 
-__global__ void __launch_bounds__(ROW_THREADS) k_rows(const __nv_bfloat16* __restrict__ X, const __nv_bfloat16* __restrict__ P,
+// Every CTA of a row's cluster takes an eighth of K for h and an eighth of the
+// columns for y.  A warp computes JB elements of h at a time; for y one half of
+// the threads takes the first half of the rank, the other the second, each with
+// the first AHEAD rows of Q loaded before h is known.  OCC CTAs per SM: while
+// all rows' CTAs are resident at four per SM, loads ahead shorten the chain (one
+// row of 2880 5.1 us against 5.7, 16 of 7168 6.2 against 6.6); with more rows
+// eight per SM with fewer registers are faster (128 of 7168 12.9 against 15.2).
+template <int AHEAD, int JB, int OCC>
+__global__ void __launch_bounds__(ROW_THREADS, OCC) k_rows(const __nv_bfloat16* __restrict__ X, const __nv_bfloat16* __restrict__ P,
                                                       const __nv_bfloat16* __restrict__ Q, const int32_t* __restrict__ idx,
                                                       const float* __restrict__ scale, const __nv_bfloat16* base, int K,
                                                       int N, int r, int G, __nv_bfloat16* y, __nv_bfloat16* __restrict__ h) {
   __shared__ float sums[ROW_CTAS][MAX_R];  // every CTA's sums over its part of K, from all of them
   __shared__ float hid[MAX_R];
+  __shared__ float4 other[2][ROW_COLS];
   const int row = blockIdx.x / ROW_CTAS, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_ctarank();
   const int a = idx[row];
-  const bool has = (unsigned)a < (unsigned)G;
+  const bool has = (unsigned)a < (unsigned)G;  // (of the whole cluster)
+  const int K8 = K / 8, k0 = (int)((int64_t)K8 * rank / ROW_CTAS), k1 = (int)((int64_t)K8 * (rank + 1) / ROW_CTAS);
   const int N8 = N / 8, n0 = (int)((int64_t)N8 * rank / ROW_CTAS), n1 = (int)((int64_t)N8 * (rank + 1) / ROW_CTAS);
+  const int half = threadIdx.x / ROW_COLS, t = threadIdx.x % ROW_COLS;
+  const int j0 = half ? r / 2 : 0, j1 = half ? r : r / 2;
+  const uint4* q = reinterpret_cast<const uint4*>(Q + (has ? (size_t)a * r * N : 0));
+  uint4 qa[AHEAD];
   if (has) {
-    const int K8 = K / 8, k0 = (int)((int64_t)K8 * rank / ROW_CTAS), k1 = (int)((int64_t)K8 * (rank + 1) / ROW_CTAS);
+    asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
     const uint4* x = reinterpret_cast<const uint4*>(X + (size_t)row * K);
     const uint4* p = reinterpret_cast<const uint4*>(P + (size_t)a * r * K);
-    asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
-    bool started = false;  // (the others' shared memory may be written once they have begun)
-    for (int j = warp; j < r; j += ROW_THREADS / 32) {
-      float s = 0.0f;
-      for (int k = k0 + lane; k < k1; k += 32) s = dot8(x[k], p[(size_t)j * K8 + k], s);
+    constexpr int WARPS = ROW_THREADS / 32;
+    bool begun = false;  // (the other CTAs: their shared memory may be written from then on)
+    for (int jb = warp; jb < r; jb += JB * WARPS) {
+      float s[JB];
 #pragma unroll
-      for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, d);
-      if (!started) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
-      started = true;
-      if (lane < ROW_CTAS)
-        asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(mapa_shared(smem_u32(&sums[rank][j]), lane)), "f"(s) : "memory");
+      for (int i = 0; i < JB; ++i) s[i] = 0.0f;
+#pragma unroll 2
+      for (int k = k0 + lane; k < k1; k += 32) {
+        const uint4 xv = x[k];
+        uint4 pv[JB];
+#pragma unroll
+        for (int i = 0; i < JB; ++i) pv[i] = jb + i * WARPS < r ? p[(size_t)(jb + i * WARPS) * K8 + k] : make_uint4(0, 0, 0, 0);
+#pragma unroll
+        for (int i = 0; i < JB; ++i)
+          if (jb + i * WARPS < r) s[i] = dot8(xv, pv[i], s[i]);
+      }
+      if (!begun) {
+#pragma unroll
+        for (int i = 0; i < AHEAD; ++i) qa[i] = n0 + t < n1 && j0 + i < j1 ? q[(size_t)(j0 + i) * N8 + n0 + t] : make_uint4(0, 0, 0, 0);
+      }
+#pragma unroll
+      for (int i = 0; i < JB; ++i)
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) s[i] += __shfl_xor_sync(0xFFFFFFFFu, s[i], d);
+      if (!begun) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+      begun = true;
+#pragma unroll
+      for (int i = 0; i < JB; ++i)
+        if (lane < ROW_CTAS && jb + i * WARPS < r)
+          asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(mapa_shared(smem_u32(&sums[rank][jb + i * WARPS]), lane)),
+                       "f"(s[i])
+                       : "memory");
     }
-    if (!started) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+    // (r >= 8: every warp has had an element)
     cluster_sync();
     if (threadIdx.x < r) {
       float s = 0.0f;
+#pragma unroll
       for (int c = 0; c < ROW_CTAS; ++c) s += sums[c][threadIdx.x];
       const __nv_bfloat16 v = __float2bfloat16_rn(s * scale[a]);
       hid[threadIdx.x] = __bfloat162float(v);
@@ -1120,26 +1170,53 @@ __global__ void __launch_bounds__(ROW_THREADS) k_rows(const __nv_bfloat16* __res
   } else if (h && rank == 0 && threadIdx.x < r) {
     h[(size_t)row * r + threadIdx.x] = __float2bfloat16_rn(0.0f);
   }
-  const uint4* q = reinterpret_cast<const uint4*>(Q + (has ? (size_t)a * r * N : 0));
-  for (int n = n0 + threadIdx.x; n < n1; n += ROW_THREADS) {
+  for (int nb = n0; nb < n1; nb += ROW_COLS) {
+    const int n = nb + t;
+    const bool mine = n < n1;
     float s[8];
-    const uint4 o = base ? reinterpret_cast<const uint4*>(base + (size_t)row * N)[n] : make_uint4(0, 0, 0, 0);
-    const uint32_t ow[4] = {o.x, o.y, o.z, o.w};
 #pragma unroll
     for (int i = 0; i < 8; ++i) s[i] = 0.0f;
-    if (has)
-      for (int j = 0; j < r; ++j) add8(s, hid[j], q[(size_t)j * N8 + n]);
-    uint32_t w[4];
+    if (has && mine) {
+      if (nb == n0) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) w[i] = pack_bf16x2(bf16_lo(ow[i]) + s[2 * i], bf16_hi(ow[i]) + s[2 * i + 1]);
-    reinterpret_cast<uint4*>(y + (size_t)row * N)[n] = make_uint4(w[0], w[1], w[2], w[3]);
+        for (int i = 0; i < AHEAD; ++i)
+          if (j0 + i < j1) add8(s, hid[j0 + i], qa[i]);
+      }
+#pragma unroll 8
+      for (int j = nb == n0 ? j0 + AHEAD : j0; j < j1; ++j) add8(s, hid[j], q[(size_t)j * N8 + n]);
+    }
+    if (has) {
+      if (half) {
+        other[0][t] = make_float4(s[0], s[1], s[2], s[3]);
+        other[1][t] = make_float4(s[4], s[5], s[6], s[7]);
+      }
+      __syncthreads();
+    }
+    if (!half && mine) {
+      const uint4 o = base ? reinterpret_cast<const uint4*>(base + (size_t)row * N)[n] : make_uint4(0, 0, 0, 0);
+      const uint32_t ow[4] = {o.x, o.y, o.z, o.w};
+      if (has) {
+        const float4 u = other[0][t], v = other[1][t];
+        s[0] += u.x, s[1] += u.y, s[2] += u.z, s[3] += u.w;
+        s[4] += v.x, s[5] += v.y, s[6] += v.z, s[7] += v.w;
+      }
+      uint32_t w[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) w[i] = pack_bf16x2(bf16_lo(ow[i]) + s[2 * i], bf16_hi(ow[i]) + s[2 * i + 1]);
+      reinterpret_cast<uint4*>(y + (size_t)row * N)[n] = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+    if (has) __syncthreads();
   }
 }
 
 // ---------------------------------------------------------------------------
 // Host
 // ---------------------------------------------------------------------------
-constexpr int FEW_ROWS = 64;
+// k_rows for calls of at most so many rows, and rows times rank.  It reads an adapter for each row (from L2, mostly),
+// the tiles each adapter once: at 7168 x 7168 and 64 adapters 128 rows of rank 16 take 13 us against 38, 256 rows 23
+// against 42, 64 rows of rank 64 28 against 37, 128 rows 43 against 47; with 4 adapters 256 rows of rank 16 21 against
+// 21; 512 rows of 512 x 512, rank 8, 22 against 16.
+constexpr int MOST_ROWS = 256, FEW_ROWS = 4096;
 
 size_t up256(size_t n) { return (n + 255) & ~(size_t)255; }
 int used_groups(int T, int G) { return G + 1 < T ? G + 1 : T; }             // at most, the rows without one among them
@@ -1242,17 +1319,24 @@ moe_status_t shrink(const moe_bf16* x, const moe_bf16* P, const float* scale, in
                 r, rp, p, out(h), out(hs), in(other), out(others), g_wait_limit_ns.load(), st);
 }
 
-moe_status_t wgrad(const moe_bf16* x, const moe_bf16* us, int T, int C, int r, int G, const Plan& p, moe_bf16* dP,
-                   int32_t* st, cudaStream_t s) {
-  const int rp = pad16(r), units = (C + TILE - 1) / TILE, bytes = wgrad_bytes(rp);
-  const int split = split_of(bytes + 10 * 1024, units, T / TILE);
-
-  CUtensorMap mx, mu;
-  if (!map_rows(&mx, x, T, C, 64, SLAB) || !map_rows(&mu, us, places(T, G), r, rank_cols(rp), TILE)) return MOE_ERR_CUDA;
+moe_status_t wgrad(const moe_bf16* x, const moe_bf16* us, int K, moe_bf16* dA, const moe_bf16* dy, const moe_bf16* hs, int N,
+                   moe_bf16* dB, int T, int r, int G, const Plan& p, int32_t* st, cudaStream_t s) {
+  const int rp = pad16(r), bytes = wgrad_bytes(rp);
+  Sides sides;
+  auto fill = [&](Side& d, const moe_bf16* X, const moe_bf16* U, int C, moe_bf16* dP) {
+    d.X = in(X);
+    d.dP = out(dP);
+    d.C = C;
+    d.units = (C + TILE - 1) / TILE;
+    return map_rows(&d.mx, X, T, C, 64, SLAB) && map_rows(&d.mu, U, places(T, G), r, rank_cols(rp), TILE);
+  };
+  if (!fill(sides.of[0], x, us, K, dA) || !fill(sides.of[1], dy, hs, N, dB)) return MOE_ERR_CUDA;
+  const int units = sides.of[0].units + sides.of[1].units;
+  const int split = split_of(bytes + 10 * 1024, units, max_tiles(T, G));
   // (not a programmatic dependent: its first clusters took places as the kernel before it left them, unevenly, and
   // the backward of 8192 x 7168 took 154 us instead of 136)
-  return launch(k_wgrad, units * split, split, WGRAD_THREADS, bytes, wgrad_bytes(MAX_R), false, s, mx, mu, in(x), C, r, rp, G,
-                p, out(dP), g_wait_limit_ns.load(), st);
+  return launch(k_wgrad, units * split, split, WGRAD_THREADS, bytes, wgrad_bytes(MAX_R), false, s, sides, r, rp, G, p,
+                g_wait_limit_ns.load(), st);
 }
 
 moe_status_t expand(const moe_bf16* hs, const moe_bf16* Q, const moe_bf16* base, int T, int N, int r, int G, const Plan& p,
@@ -1308,9 +1392,11 @@ extern "C" moe_status_t moe_lora_fwd(const moe_bf16* x, const moe_bf16* A, const
       overlap(y, yn, A, (size_t)G * r * K * 2) || overlap(y, yn, B, (size_t)G * r * N * 2))
     return MOE_ERR_ARG;
   const cudaStream_t s = as_stream(stream);
-  if (T <= FEW_ROWS)
-    return launch(k_rows, T * ROW_CTAS, ROW_CTAS, ROW_THREADS, 0, 0, false, s, in(x), in(A), in(B), idx, scale, in(base), K, N,
-                  r, G, out(y), out(h));
+  if (T <= MOST_ROWS && (int64_t)T * r <= FEW_ROWS) {
+    const auto k = T * ROW_CTAS <= 4 * sm_count() ? k_rows<4, 2, 4> : k_rows<1, 1, 8>;
+    return launch(k, T * ROW_CTAS, ROW_CTAS, ROW_THREADS, 0, 0, false, s, in(x), in(A), in(B), idx, scale, in(base), K, N, r, G,
+                  out(y), out(h));
+  }
   const Plan p = plan_at(ws, T, G);
   auto* hs = reinterpret_cast<moe_bf16*>(static_cast<char*>(ws) + plan_bytes(T, G));
   if (const moe_status_t e = group(idx, T, G, p, s)) return e;
@@ -1347,6 +1433,5 @@ extern "C" moe_status_t moe_lora_bwd(const moe_bf16* dy, const moe_bf16* x, cons
   if (const moe_status_t e = group(idx, T, G, p, s)) return e;
   if (const moe_status_t e = shrink(dy, B, scale, T, N, r, G, p, nullptr, us, h, hs, status, s)) return e;
   if (const moe_status_t e = expand(us, A, base, T, K, r, G, p, dx, status, s)) return e;
-  if (const moe_status_t e = wgrad(x, us, T, K, r, G, p, dA, status, s)) return e;
-  return wgrad(dy, hs, T, N, r, G, p, dB, status, s);
+  return wgrad(x, us, K, dA, dy, hs, N, dB, T, r, G, p, status, s);
 }
