@@ -28,6 +28,8 @@
 // with 8-bit ones.  One launch for all tensors: a table of (tensor, chunk),
 // built once, splits them into chunks of CHUNK elements, and the gradients'
 // addresses (they differ from step to step) come as a kernel parameter.
+#include <cmath>
+
 #include "common.cuh"
 #include "host_common.h"
 
@@ -37,7 +39,7 @@ namespace adamw {
 constexpr int THREADS = 256, PER = 8, CHUNK = 2048;  // elements per thread at a time, per chunk
 constexpr int FEW = 64, MANY = 4000;                 // gradient addresses in a launch's parameters (32,764 bytes at most)
 constexpr int BLOCK = 32;                            // elements per scale
-constexpr int MAX_PARTS = 1024;                      // CTAs of the norm's kernel
+constexpr int MAX_PARTS = 2048;                      // CTAs of the norm's kernel
 constexpr int NEAR = 8;  // fp32 steps around a turning point inside which 64 bits decide
 
 struct Entry {
@@ -49,20 +51,17 @@ struct Grads {
 };
 
 // What a step's scalars are, written once per step.
-struct Scalars {
-  double b1, a1, b2, a2, c;            // a = 1 - b
+struct Short {
   float b1h, b1l, a1h, a1l, b2f, a2f;  // a1 and a2 with c and c^2
   float step, root, lr, eps;           // lr / (1 - b1^t), 1 / sqrt(1 - b2^t)
   uint32_t key;
   int32_t skip;  // the gradients' norm is not finite
 };
+struct Scalars : Short {
+  double b1, a1, b2, a2, c;  // a = 1 - b
+};
 // the workspace: the scalars, then the norm's partial sums
 constexpr size_t PARTS_AT = 256;
-
-struct Params {
-  double b1, b2, eps, max_norm;
-  uint32_t seed;
-};
 
 __device__ __forceinline__ uint32_t mix(uint32_t x) {  // a 32-bit hash: two multiplications
   x ^= x >> 16;
@@ -100,15 +99,17 @@ __device__ __forceinline__ void load8(const float* p, int64_t n, float* v) {
     for (int i = 0; i < PER; ++i) v[i] = i < n ? p[i] : 0.0f;
   }
 }
+__device__ __forceinline__ void unpack8(uint4 q, float* v) {
+  const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    v[2 * i] = bf16_lo(w[i]);
+    v[2 * i + 1] = bf16_hi(w[i]);
+  }
+}
 __device__ __forceinline__ void load8(const __nv_bfloat16* p, int64_t n, float* v) {
   if (n >= PER && on(p, 16)) {
-    const uint4 q = *reinterpret_cast<const uint4*>(p);
-    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      v[2 * i] = bf16_lo(w[i]);
-      v[2 * i + 1] = bf16_hi(w[i]);
-    }
+    unpack8(*reinterpret_cast<const uint4*>(p), v);
   } else {
 #pragma unroll
     for (int i = 0; i < PER; ++i) v[i] = i < n ? __bfloat162float(p[i]) : 0.0f;
@@ -143,31 +144,63 @@ __device__ __forceinline__ double warp_sum(double s) {
   return s;
 }
 
-// parts[CTA] = sum of squares of its chunks.  Eight squares are added in fp32
-// (of bf16 values they are exact), these sums with their rounding errors.
+// parts[CTA] = sum of squares of its chunks, AT_ONCE of them loaded together.
+// Eight squares are added in fp32 (of bf16 values they are exact), these sums
+// with their rounding errors.
+constexpr int AT_ONCE = 2;
 template <int N>
-__global__ void __launch_bounds__(THREADS) k_adamw_norm(const __grid_constant__ Grads<N> grads,
+__global__ void __launch_bounds__(THREADS, 8) k_adamw_norm(const __grid_constant__ Grads<N> grads,
                                                         const moe_adamw_tensor_t* __restrict__ tensors,
                                                         const Entry* __restrict__ table, uint32_t chunks, int first,
                                                         double* __restrict__ parts) {
+  launch_dependents();
   float hi = 0.0f, lo = 0.0f;
-  for (uint32_t i = blockIdx.x; i < chunks; i += gridDim.x) {
-    const Entry e = table[i];
-    const moe_adamw_tensor_t& t = tensors[e.tensor];
-    const int64_t at = (int64_t)e.chunk * CHUNK + threadIdx.x * PER, n = t.n - at;
-    if (n <= 0) continue;
-    float g[PER];
-    const void* p = grads.p[e.tensor - first];
-    if (t.grad_bf16)
-      load8(static_cast<const __nv_bfloat16*>(p) + at, n, g);
-    else
-      load8(static_cast<const float*>(p) + at, n, g);
-    float q = g[0] * g[0];
+  for (uint32_t i = blockIdx.x; i < chunks; i += AT_ONCE * gridDim.x) {
+    Entry e[AT_ONCE];
+    float g[AT_ONCE][PER];
+    bool packed[AT_ONCE];  // g holds eight bf16 values in its first four words: taken apart when all loads are under way
 #pragma unroll
-    for (int j = 1; j < PER; ++j) q = fmaf(g[j], g[j], q);
-    const float s = hi + q, bb = s - hi;
-    lo += (hi - (s - bb)) + (q - bb);
-    hi = s;
+    for (int k = 0; k < AT_ONCE; ++k) e[k] = i + k * gridDim.x < chunks ? table[i + k * gridDim.x] : Entry{0xFFFFFFFFu, 0};
+#pragma unroll
+    for (int k = 0; k < AT_ONCE; ++k) {
+      int64_t n = 0, at = 0;
+      packed[k] = false;
+      if (e[k].tensor != 0xFFFFFFFFu) {
+        at = (int64_t)e[k].chunk * CHUNK + threadIdx.x * PER;
+        n = tensors[e[k].tensor].n - at;
+      }
+      if (n > 0) {
+        const void* p = grads.p[e[k].tensor - first];
+        if (tensors[e[k].tensor].grad_bf16) {
+          const auto* q = static_cast<const __nv_bfloat16*>(p) + at;
+          if (n >= PER && on(q, 16)) {
+            packed[k] = true;
+            asm volatile("ld.global.v4.f32 {%0,%1,%2,%3}, [%4];" : "=f"(g[k][0]), "=f"(g[k][1]), "=f"(g[k][2]), "=f"(g[k][3]) : "l"(q));
+          } else {
+            load8(q, n, g[k]);
+          }
+        } else {
+          load8(static_cast<const float*>(p) + at, n, g[k]);
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < PER; ++j) g[k][j] = 0.0f;
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < AT_ONCE; ++k)
+      if (packed[k])
+        unpack8(make_uint4(__float_as_uint(g[k][0]), __float_as_uint(g[k][1]), __float_as_uint(g[k][2]), __float_as_uint(g[k][3])),
+                g[k]);
+#pragma unroll
+    for (int k = 0; k < AT_ONCE; ++k) {
+      float q = g[k][0] * g[k][0];
+#pragma unroll
+      for (int j = 1; j < PER; ++j) q = fmaf(g[k][j], g[k][j], q);
+      const float s = hi + q, bb = s - hi;
+      lo += (hi - (s - bb)) + (q - bb);
+      hi = s;
+    }
   }
   // (an infinite or NaN hi stays so: its error term, NaN, is left out)
   double s = warp_sum(fabsf(hi) <= 3.4e38f ? (double)hi + (double)lo : (double)hi);
@@ -180,43 +213,58 @@ __global__ void __launch_bounds__(THREADS) k_adamw_norm(const __grid_constant__ 
   }
 }
 
-// One CTA: the norm from its parts, the step count and the step's scalars.
-__global__ void __launch_bounds__(32) k_adamw_scalars(Params p, const float* __restrict__ lr, int64_t* __restrict__ t,
-                                                      const double* __restrict__ parts, int n_parts,
-                                                      float* __restrict__ norm, Scalars* __restrict__ out) {
+// sqrt(x) and a / x to about 2^-45: an fp32 guess and one step of Newton's
+// method in 64 bits (whose own root and division take microseconds here).
+__device__ __forceinline__ double root64(double x) {
+  if (!(x > 1e-30 && x < 1e38)) return sqrt(x);
+  const double r = (double)rsqrtf((float)x), y = x * r;
+  return fma(fma(-y, y, x), 0.5 * r, y);
+}
+__device__ __forceinline__ double over64(double a, double x) {
+  if (!(x > 1e-30 && x < 1e38)) return a / x;
+  const double r = (double)(1.0f / (float)x), y = a * r;
+  return fma(fma(-y, x, a), r, y);
+}
+
+// One CTA: the norm from its parts, the step count and the step's scalars,
+// which come as they are for c = 1.
+__global__ void __launch_bounds__(256) k_adamw_scalars(Scalars o, double max_norm, double ln_b1, double ln_b2, uint32_t seed,
+                                                       const float* __restrict__ lr, int64_t* __restrict__ t,
+                                                       const double* __restrict__ parts, int n_parts,
+                                                       float* __restrict__ norm, Scalars* __restrict__ out) {
   launch_dependents();
-  double s = 0.0;
-  for (int i = threadIdx.x; i < n_parts; i += 32) s += parts[i];
-  s = sqrt(warp_sum(s));
-  if (threadIdx.x != 0) return;
-  double c = 1.0;
-  bool skip = false;
-  if (p.max_norm > 0.0) {
-    skip = !(s <= 1.7e308);
-    c = fmin(1.0, p.max_norm / (s + 1e-6));
-    if (norm) *norm = (float)s;
-  }
-  if (!skip) *t += 1;
-  const int64_t now = *t;
-  Scalars o;
-  o.b1 = p.b1;
-  o.a1 = 1.0 - p.b1;
-  o.b2 = p.b2;
-  o.a2 = 1.0 - p.b2;
-  o.c = c;
-  const double a1 = o.a1 * c;
-  o.b1h = (float)p.b1;
-  o.b1l = (float)(p.b1 - (double)o.b1h);
-  o.a1h = (float)a1;
-  o.a1l = (float)(a1 - (double)o.a1h);
-  o.b2f = (float)p.b2;
-  o.a2f = (float)(o.a2 * c * c);
+  __shared__ double warp[8];
+  const int lane = threadIdx.x & 31;
+  const int64_t now = *t + 1;
+  // 1 - b^t = -expm1(t ln b): as near as fp32 gets for every t
+  const float away1 = -expm1f((float)((double)now * ln_b1)), away2 = -expm1f((float)((double)now * ln_b2));
   o.lr = *lr;
-  o.step = (float)((double)o.lr / (1.0 - pow(p.b1, (double)now)));
-  o.root = (float)(1.0 / sqrt(1.0 - pow(p.b2, (double)now)));
-  o.eps = (float)p.eps;
-  o.key = mix(mix((uint32_t)now) ^ p.seed);
-  o.skip = skip;
+  o.step = o.lr / away1;
+  o.root = 1.0f / sqrtf(away2);
+  o.key = mix(mix((uint32_t)now) ^ seed);
+  o.skip = 0;
+  if (max_norm > 0.0) {
+    wait_for_primary();  // (of the norm's kernel)
+    double s = 0.0;
+    for (int i = threadIdx.x; i < n_parts; i += 256) s += parts[i];
+    s = warp_sum(s);
+    if (lane == 0) warp[threadIdx.x >> 5] = s;
+    __syncthreads();
+    if (threadIdx.x >= 32) return;
+    s = lane < 8 ? warp[lane] : 0.0;
+#pragma unroll
+    for (int d = 4; d > 0; d >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, d);
+    s = root64(s);
+    o.skip = !(s <= 1.7e308);
+    o.c = fmin(1.0, over64(max_norm, s + 1e-6));
+    const double a1 = o.a1 * o.c;
+    o.a1h = (float)a1;
+    o.a1l = (float)(a1 - (double)o.a1h);
+    o.a2f = (float)(o.a2 * o.c * o.c);
+    if (lane == 0 && norm) *norm = (float)s;
+  }
+  if (threadIdx.x != 0) return;
+  if (!o.skip) *t = now;
   *out = o;
 }
 
@@ -243,33 +291,37 @@ __device__ __noinline__ uint32_t code_exact(double a, uint32_t r16) {
   return (uint32_t)(ex + 6) * 8u + k;  // (a normal value's k has its leading one: 8 to 16)
 }
 
-// The code (no sign) of a >= 0 within a few fp32 steps; false where 64 bits
-// have to decide (or the value is below the normal codes).
-__device__ __forceinline__ bool code_fast(float a, uint32_t r16, uint32_t& code) {
-  const uint32_t b = __float_as_uint(a), x = b + (r16 << 4);
-  code = (x >> 20) - (120u << 3);
-  return b >= 0x3C800000u && ((x + NEAR) & 0xFFFFFu) >= 2u * NEAR;
-}
-
 // Quantises one moment of a thread's PER elements; four neighbouring threads
 // share a block.  x: the fp32 values, ex(i): the 64-bit value of element i.
 // SHIFT: which half of the random bits.
+//
+// The fp32 pattern of |x| 2^-e, less that of 2^-7 and four places up, has the
+// code of a normal value in its top byte and what lies above it in the 24 bits
+// below; 16 random bits in the upper ones carry into it.  The elements whose
+// low bits come within NEAR fp32 steps of a carry, and those below the normal
+// codes, are found together and done again one by one.
 template <bool LEAST, int SHIFT, class Exact>
-__device__ __forceinline__ uint2 quantise(const float* x, const uint32_t* bits, Exact ex, uint32_t& sbyte) {
-  uint32_t top = 0;
+__device__ __forceinline__ uint2 quantise(const float2* x, const uint32_t* bits, Exact ex, uint32_t& sbyte) {
+  float peak = 0.0f;
 #pragma unroll
-  for (int i = 0; i < PER; ++i) top = max(top, abs_bits(x[i]));
+  for (int i = 0; i < PER / 2; ++i) {
+    asm("max.NaN.f32 %0, %0, %1;" : "+f"(peak) : "f"(LEAST ? x[i].x : fabsf(x[i].x)));
+    asm("max.NaN.f32 %0, %0, %1;" : "+f"(peak) : "f"(LEAST ? x[i].y : fabsf(x[i].y)));
+  }
+  uint32_t top = __float_as_uint(peak) & 0x7FFFFFFFu;
   top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
   top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
   bool above = (top & 0x7FFFFFu) > 0x600000u;
   const bool near = (top & 0x7FFFFFu) - (0x600000u - NEAR) <= 2u * NEAR && top < 0x7F800000u;
+  auto at = [&](int i) { return i & 1 ? x[i >> 1].y : x[i >> 1].x; };
   if (__any_sync(0xFFFFFFFFu, near)) {
     // the whole group of four looks at its elements near the limit in 64 bits
     const double limit = (double)__uint_as_float((top & 0x7F800000u) | 0x600000u);
     bool over = false;
     if (near) {
+#pragma unroll
       for (int i = 0; i < PER; ++i)
-        if (abs_bits(x[i]) + 2 * NEAR >= top) over |= fabs(ex(i)) > limit;
+        if (abs_bits(at(i)) + 2 * NEAR >= top) over |= fabs(ex(i)) > limit;
     }
     const uint32_t votes = __ballot_sync(0xFFFFFFFFu, over) >> (threadIdx.x & 28);
     if (near) above = (votes & 15u) != 0;
@@ -277,37 +329,48 @@ __device__ __forceinline__ uint2 quantise(const float* x, const uint32_t* bits, 
   sbyte = scale_byte(top, above);
   if (sbyte == 0xFFu) return make_uint2(0x7F7F7F7Fu, 0x7F7F7F7Fu);
   const float inv = mx_inv_scale(sbyte);
-  uint32_t w[2] = {0, 0};
+  uint32_t y[PER], least = 0xFFFFFFFFu, close = 0xFFFFFFFFu;
 #pragma unroll
-  for (int i = 0; i < PER; ++i) {
-    const uint32_t r16 = SHIFT ? bits[i] >> 16 : bits[i] & 0xFFFFu;
-    uint32_t code;
-    if (!code_fast(fabsf(x[i]) * inv, r16, code)) {
-      if (x[i] == 0.0f) {
-        code = 0;
-      } else {
-        code = code_exact(fabs(ex(i)) * (double)inv, r16);
-        if (LEAST && code == 0) code = 1;
-      }
+  for (int i = 0; i < PER / 2; ++i) {
+    const float2 a = __fmul2_rn(x[i], make_float2(inv, inv));
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const uint32_t f = __float_as_uint(k ? a.y : a.x), mag = LEAST ? f : f & 0x7FFFFFFFu, r = bits[2 * i + k];
+      const uint32_t v = (mag - (120u << 23)) * 16u + ((SHIFT ? r >> 8 : r << 8) & 0xFFFF00u);
+      least = min(least, mag);
+      close = min(close, v * 256u + 16u * NEAR * 256u);
+      y[2 * i + k] = LEAST ? v : v | (f & 0x80000000u);
     }
-    if (!LEAST) code |= (__float_as_uint(x[i]) >> 24) & 0x80u;
-    w[i >> 2] |= code << (8 * (i & 3));
   }
-  return make_uint2(w[0], w[1]);
+  uint2 w = make_uint2(__byte_perm(__byte_perm(y[0], y[1], 0x73), __byte_perm(y[2], y[3], 0x73), 0x5410),
+                       __byte_perm(__byte_perm(y[4], y[5], 0x73), __byte_perm(y[6], y[7], 0x73), 0x5410));
+  if (least < 0x3C800000u || close < 32u * NEAR * 256u) {
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      const uint32_t mag = abs_bits(at(i) * inv), low = y[i] & 0xFFFFFFu;
+      if (mag >= 0x3C800000u && ((low + 16u * NEAR) & 0xFFFFFFu) >= 32u * NEAR) continue;
+      uint32_t code = 0;
+      if (at(i) != 0.0f) {
+        code = code_exact(fabs(ex(i)) * (double)inv, SHIFT ? bits[i] >> 16 : bits[i] & 0xFFFFu);
+        if (LEAST && code == 0) code = 1;
+        if (!LEAST) code |= (__float_as_uint(at(i)) >> 24) & 0x80u;
+      }
+      uint32_t& word = i < 4 ? w.x : w.y;
+      word = (word & ~(0xFFu << (8 * (i & 3)))) | code << (8 * (i & 3));
+    }
+  }
+  return w;
 }
 
-// m and sqrt(v) of PER elements from their codes; the block's scale is one of
+// m or sqrt(v) of PER elements from their codes; the block's scale is one of
 // the 32 elements from at on.
-__device__ __forceinline__ void decode8(const uint8_t* q, const uint8_t* s, int64_t at, float* x) {
-  const uint2 w = *reinterpret_cast<const uint2*>(q + at);
-  const float f = e8m0_value(s[at / BLOCK]);
-  const uint32_t h[4] = {w.x & 0xFFFFu, w.x >> 16, w.y & 0xFFFFu, w.y >> 16};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float2 p = e4m3x2_value(h[i]);
-    x[2 * i] = p.x * f;
-    x[2 * i + 1] = p.y * f;
-  }
+__device__ __forceinline__ void decode8(uint2 w, uint32_t sbyte, float2* x) {
+  const float f = e8m0_value(sbyte);
+  const float2 f2 = make_float2(f, f);
+  x[0] = __fmul2_rn(e4m3x2_value(w.x & 0xFFFFu), f2);
+  x[1] = __fmul2_rn(e4m3x2_value(w.x >> 16), f2);
+  x[2] = __fmul2_rn(e4m3x2_value(w.y & 0xFFFFu), f2);
+  x[3] = __fmul2_rn(e4m3x2_value(w.y >> 16), f2);
 }
 
 __device__ __forceinline__ float sqrt_hw(float x) {
@@ -315,71 +378,89 @@ __device__ __forceinline__ float sqrt_hw(float x) {
   asm("sqrt.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
+__device__ __forceinline__ float rcp_hw(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float2 both(float a) { return make_float2(a, a); }
 
 // w <- w - (lr wd w + step m / (sqrt(v) root + eps)): the quotient and the
 // root by the hardware's approximations, good to two fp32 steps; what is taken
 // off is small beside w, so that w is rounded once.
-__device__ __forceinline__ float updated(const Scalars& s, float decay, float w, float m, float root_v) {
-  return w - fmaf(s.step, __fdividef(m, fmaf(root_v, s.root, s.eps)), w * decay);
+__device__ __forceinline__ float2 updated(const Short& s, float decay, float2 w, float2 m, float2 root_v) {
+  const float2 den = __ffma2_rn(root_v, both(s.root), both(s.eps));
+  const float2 q = __fmul2_rn(m, make_float2(rcp_hw(den.x), rcp_hw(den.y)));
+  const float2 d = __ffma2_rn(q, both(s.step), __fmul2_rn(w, both(decay)));
+  return __ffma2_rn(d, both(-1.0f), w);
+}
+
+// The moments in 64 bits (calls, so that the rare path costs the usual one no registers).
+__device__ __noinline__ double exact_m(float m, float g, const Scalars* s) {
+  return __dadd_rn(__dmul_rn((double)m, s->b1), __dmul_rn(__dmul_rn((double)g, s->c), s->a1));
+}
+__device__ __noinline__ double exact_root(float root, float g, const Scalars* s) {
+  const double gc = __dmul_rn((double)g, s->c), r = (double)root;
+  return sqrt(__dadd_rn(__dmul_rn(r * r, s->b2), __dmul_rn(__dmul_rn(gc, gc), s->a2)));
 }
 
 template <bool STATE8, bool W16, class G>
-__device__ __forceinline__ void step8(const Scalars& s, const moe_adamw_tensor_t& t, const G* grad, int64_t at, int64_t n,
-                                      uint32_t key) {
-  float g[PER], w[PER], m[PER], v[PER];
+__device__ __forceinline__ void step8(const Short& s, const Scalars* all, const moe_adamw_tensor_t& t, const G* grad,
+                                      int64_t at, int64_t n, uint32_t key) {
+  float2 g[PER / 2], w[PER / 2], m[PER / 2], v[PER / 2];
   // a thread past the tensor's end works on zeros: its neighbours' block needs it in the exchange
   const bool live = n > 0;
 #pragma unroll
-  for (int i = 0; i < PER; ++i) g[i] = w[i] = m[i] = v[i] = 0.0f;
+  for (int i = 0; i < PER / 2; ++i) g[i] = w[i] = m[i] = v[i] = both(0.0f);
   float* wide = W16 ? t.master : static_cast<float*>(t.w);
   if (live) {
-    load8(grad + at, n, g);
-    load8(wide + at, n, w);
+    // (the gradient last: its bf16 values are taken apart as they come, when all other loads are under way)
     if (STATE8) {
-      decode8(static_cast<const uint8_t*>(t.m), t.m_scale, at, m);
-      decode8(static_cast<const uint8_t*>(t.v), t.v_scale, at, v);
+      const uint2 qm = *reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(t.m) + at);
+      const uint2 qv = *reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(t.v) + at);
+      const uint32_t sm = t.m_scale[at / BLOCK], sv = t.v_scale[at / BLOCK];
+      load8(wide + at, n, &w[0].x);
+      load8(grad + at, n, &g[0].x);
+      decode8(qm, sm, m);
+      decode8(qv, sv, v);
     } else {
-      load8(static_cast<const float*>(t.m) + at, n, m);
-      load8(static_cast<const float*>(t.v) + at, n, v);
+      load8(wide + at, n, &w[0].x);
+      load8(static_cast<const float*>(t.m) + at, n, &m[0].x);
+      load8(static_cast<const float*>(t.v) + at, n, &v[0].x);
+      load8(grad + at, n, &g[0].x);
     }
   }
   const float decay = s.lr * t.weight_decay;
-  float om[PER], ov[PER];
+  float2 om[PER / 2], ov[PER / 2];
 #pragma unroll
-  for (int i = 0; i < PER; ++i) {
+  for (int i = 0; i < PER / 2; ++i) {
     if (STATE8) {
       // b1 m + a1 g: the first product's error, and the low parts of both factors
-      const float p = s.b1h * m[i];
-      const float rest = fmaf(s.a1l, g[i], fmaf(s.b1l, m[i], fmaf(s.b1h, m[i], -p)));
-      om[i] = fmaf(s.a1h, g[i], p) + rest;
-      ov[i] = sqrt_hw(fmaf(s.b2f, v[i] * v[i], s.a2f * (g[i] * g[i])));
+      const float2 p = __fmul2_rn(m[i], both(s.b1h)), minus = __fmul2_rn(m[i], both(-s.b1h));
+      const float2 rest = __ffma2_rn(g[i], both(s.a1l), __ffma2_rn(m[i], both(s.b1l), __ffma2_rn(m[i], both(s.b1h), minus)));
+      om[i] = __fadd2_rn(__ffma2_rn(g[i], both(s.a1h), p), rest);
+      const float2 q = __ffma2_rn(__fmul2_rn(v[i], v[i]), both(s.b2f), __fmul2_rn(__fmul2_rn(g[i], g[i]), both(s.a2f)));
+      ov[i] = make_float2(sqrt_hw(q.x), sqrt_hw(q.y));
       w[i] = updated(s, decay, w[i], om[i], ov[i]);
     } else {
-      om[i] = fmaf(s.b1h, m[i], s.a1h * g[i]);
-      ov[i] = fmaf(s.b2f, v[i], s.a2f * (g[i] * g[i]));
-      w[i] = updated(s, decay, w[i], om[i], sqrt_hw(ov[i]));
+      om[i] = __ffma2_rn(m[i], both(s.b1h), __fmul2_rn(g[i], both(s.a1h)));
+      ov[i] = __ffma2_rn(v[i], both(s.b2f), __fmul2_rn(__fmul2_rn(g[i], g[i]), both(s.a2f)));
+      w[i] = updated(s, decay, w[i], om[i], make_float2(sqrt_hw(ov[i].x), sqrt_hw(ov[i].y)));
     }
   }
   if (live) {
-    store8(wide + at, n, w);
-    if (W16) store8(static_cast<__nv_bfloat16*>(t.w) + at, n, w);
+    store8(wide + at, n, &w[0].x);
+    if (W16) store8(static_cast<__nv_bfloat16*>(t.w) + at, n, &w[0].x);
   }
   if (STATE8) {
     uint32_t bits[PER];
-    const uint32_t k = mix(key + (uint32_t)(at >> 32));
+    const uint32_t k = mix(key + (uint32_t)(at >> 32)) + (uint32_t)at;
 #pragma unroll
-    for (int i = 0; i < PER; ++i) bits[i] = mix(k + (uint32_t)at + i);
+    for (int i = 0; i < PER; ++i) bits[i] = mix(k + i);
     uint32_t sm, sv;
-    const uint2 qm = quantise<false, 1>(
-        om, bits,
-        [&](int i) { return __dadd_rn(__dmul_rn((double)m[i], s.b1), __dmul_rn(__dmul_rn((double)g[i], s.c), s.a1)); }, sm);
-    const uint2 qv = quantise<true, 0>(
-        ov, bits,
-        [&](int i) {
-          const double gc = __dmul_rn((double)g[i], s.c), r = (double)v[i];
-          return sqrt(__dadd_rn(__dmul_rn(r * r, s.b2), __dmul_rn(__dmul_rn(gc, gc), s.a2)));
-        },
-        sv);
+    const auto of = [](const float2* x, int i) { return i & 1 ? x[i >> 1].y : x[i >> 1].x; };
+    const uint2 qm = quantise<false, 1>(om, bits, [&](int i) { return exact_m(of(m, i), of(g, i), all); }, sm);
+    const uint2 qv = quantise<true, 0>(ov, bits, [&](int i) { return exact_root(of(v, i), of(g, i), all); }, sv);
     if (live) {
       *reinterpret_cast<uint2*>(static_cast<uint8_t*>(t.m) + at) = qm;
       *reinterpret_cast<uint2*>(static_cast<uint8_t*>(t.v) + at) = qv;
@@ -389,36 +470,38 @@ __device__ __forceinline__ void step8(const Scalars& s, const moe_adamw_tensor_t
       }
     }
   } else if (live) {
-    store8(static_cast<float*>(t.m) + at, n, om);
-    store8(static_cast<float*>(t.v) + at, n, ov);
+    store8(static_cast<float*>(t.m) + at, n, &om[0].x);
+    store8(static_cast<float*>(t.v) + at, n, &ov[0].x);
   }
 }
 
 template <int N, bool STATE8>
-__global__ void __launch_bounds__(THREADS) k_adamw_step(const __grid_constant__ Grads<N> grads,
+__global__ void __launch_bounds__(THREADS, STATE8 ? 3 : 4) k_adamw_step(const __grid_constant__ Grads<N> grads,
                                                         const moe_adamw_tensor_t* __restrict__ tensors,
                                                         const Entry* __restrict__ table, uint32_t chunks, int first,
                                                         const Scalars* __restrict__ scalars) {
   wait_for_primary();
-  const Scalars s = *scalars;
+  const Short s = *scalars;
   if (s.skip) return;
   // backwards: the norm's kernel has read the last gradients last, and finds them in L2
+  Entry next = table[chunks - 1 - blockIdx.x];
   for (uint32_t i = blockIdx.x; i < chunks; i += gridDim.x) {
-    const Entry e = table[chunks - 1 - i];
+    const Entry e = next;
+    if (i + gridDim.x < chunks) next = table[chunks - 1 - i - gridDim.x];
     const moe_adamw_tensor_t t = tensors[e.tensor];
     const void* g = grads.p[e.tensor - first];
     const int64_t at = (int64_t)e.chunk * CHUNK + threadIdx.x * PER, n = t.n - at;
     const uint32_t key = mix(s.key + e.tensor);
     if (t.w_bf16) {
       if (t.grad_bf16)
-        step8<STATE8, true>(s, t, static_cast<const __nv_bfloat16*>(g), at, n, key);
+        step8<STATE8, true>(s, scalars, t, static_cast<const __nv_bfloat16*>(g), at, n, key);
       else
-        step8<STATE8, true>(s, t, static_cast<const float*>(g), at, n, key);
+        step8<STATE8, true>(s, scalars, t, static_cast<const float*>(g), at, n, key);
     } else {
       if (t.grad_bf16)
-        step8<STATE8, false>(s, t, static_cast<const __nv_bfloat16*>(g), at, n, key);
+        step8<STATE8, false>(s, scalars, t, static_cast<const __nv_bfloat16*>(g), at, n, key);
       else
-        step8<STATE8, false>(s, t, static_cast<const float*>(g), at, n, key);
+        step8<STATE8, false>(s, scalars, t, static_cast<const float*>(g), at, n, key);
     }
   }
 }
@@ -445,22 +528,18 @@ bool valid(const moe_adamw_tensor_t* t, int n, int state8) {
   return chunks < ((size_t)1 << 31);
 }
 
-template <int N, bool STATE8>
-moe_status_t launch_step(const Grads<N>& g, const moe_adamw_tensor_t* dev, const Entry* table, uint32_t chunks, int first,
-                         const Scalars* sc, bool behind_scalars, cudaStream_t stream) {
-  auto* k = k_adamw_step<N, STATE8>;
-  const int per_sm = max_active_blocks((const void*)k, THREADS, 0), sms = sm_count();
-  if (per_sm < 1 || sms < 1) return MOE_ERR_CUDA;
+template <class... A, class... B>
+moe_status_t launch(void (*k)(A...), int ctas, int threads, bool dependent, cudaStream_t stream, const B&... args) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(chunks < (uint32_t)(per_sm * sms) ? chunks : (uint32_t)(per_sm * sms));
-  cfg.blockDim = dim3(THREADS);
+  cfg.gridDim = dim3(ctas);
+  cfg.blockDim = dim3(threads);
   cfg.stream = stream;
   cudaLaunchAttribute attr;
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &attr;
-  cfg.numAttrs = behind_scalars ? 1 : 0;
-  if (cudaLaunchKernelEx(&cfg, k, g, dev, table, chunks, first, sc) != cudaSuccess) return MOE_ERR_CUDA;
+  cfg.numAttrs = dependent ? 1 : 0;
+  if (cudaLaunchKernelEx(&cfg, k, static_cast<A>(args)...) != cudaSuccess) return MOE_ERR_CUDA;
   count_launch();
   return launch_status();
 }
@@ -473,17 +552,16 @@ moe_status_t launch_group(const moe_adamw_tensor_t* dev, const Entry* table, uin
                           bool behind_scalars, cudaStream_t stream) {
   Grads<N> g;
   for (int i = 0; i < count; ++i) g.p[i] = grads[first + i];
-  if (parts) {
-    k_adamw_norm<N><<<n_parts, THREADS, 0, stream>>>(g, dev, table, chunks, first, parts);
-    count_launch();
-    return launch_status();
-  }
-  return state8 ? launch_step<N, true>(g, dev, table, chunks, first, sc, behind_scalars, stream)
-                : launch_step<N, false>(g, dev, table, chunks, first, sc, behind_scalars, stream);
+  if (parts) return launch(k_adamw_norm<N>, n_parts, THREADS, false, stream, g, dev, table, chunks, first, parts);
+  const auto k = state8 ? k_adamw_step<N, true> : k_adamw_step<N, false>;
+  const int per_sm = max_active_blocks((const void*)k, THREADS, 0), sms = sm_count();
+  if (per_sm < 1 || sms < 1) return MOE_ERR_CUDA;
+  const uint32_t most = per_sm * sms;
+  return launch(k, chunks < most ? chunks : most, THREADS, behind_scalars, stream, g, dev, table, chunks, first, sc);
 }
 
 int parts_of(uint32_t chunks) {
-  const int n = sm_count() * 6;
+  const int n = sm_count() * 8;
   const int most = n < MAX_PARTS ? n : MAX_PARTS;
   return chunks < (uint32_t)most ? (int)chunks : most;
 }
@@ -539,12 +617,26 @@ extern "C" moe_status_t moe_adamw_step(const moe_adamw_tensor_t* tensors, const 
   const auto* dev = static_cast<const moe_adamw_tensor_t*>(plan);
   const auto* table = reinterpret_cast<const Entry*>(dev + n);
   int n_parts = 0;
+  bool pass0 = false;  // the norm's last launch is right in front of the scalars'
   for (int pass = p->max_norm > 0.0 ? 0 : 1; pass < 2; ++pass) {
     if (pass == 1) {
-      const Params q = {p->beta1, p->beta2, p->eps, p->max_norm, p->seed};
-      k_adamw_scalars<<<1, 32, 0, stream>>>(q, lr, t, parts, n_parts, norm, sc);
-      count_launch();
-      if (const moe_status_t e = launch_status()) return e;
+      Scalars c1 = {};
+      c1.b1 = p->beta1;
+      c1.a1 = 1.0 - p->beta1;
+      c1.b2 = p->beta2;
+      c1.a2 = 1.0 - p->beta2;
+      c1.c = 1.0;
+      c1.b1h = (float)c1.b1;
+      c1.b1l = (float)(c1.b1 - (double)c1.b1h);
+      c1.a1h = (float)c1.a1;
+      c1.a1l = (float)(c1.a1 - (double)c1.a1h);
+      c1.b2f = (float)c1.b2;
+      c1.a2f = (float)c1.a2;
+      c1.eps = (float)p->eps;
+      const auto ln = [](double b) { return b > 0.0 ? std::log(b) : -1e9; };  // (of 0: a power of 0)
+      if (const moe_status_t e = launch(k_adamw_scalars, 1, p->max_norm > 0.0 ? 256 : 32, pass0, stream, c1, p->max_norm,
+                                        ln(p->beta1), ln(p->beta2), p->seed, lr, t, parts, n_parts, norm, sc))
+        return e;
     }
     const Entry* at = table;
     bool behind = true;  // only the launch right behind the scalars' may start before it ends
@@ -562,7 +654,7 @@ extern "C" moe_status_t moe_adamw_step(const moe_adamw_tensor_t* tensors, const 
               : launch_group<MANY>(dev, at, (uint32_t)c, grads, first, count, p->state, sc, to, np, behind, stream);
       if (e) return e;
       behind = false;
-      if (pass == 0) n_parts += np;
+      if (pass == 0) n_parts += np, pass0 = true;
       at += c;
     }
   }
