@@ -365,7 +365,8 @@ __device__ __forceinline__ uint2 quantise(const float2* x, const uint32_t* bits,
 // m or sqrt(v) of PER elements from their codes; the block's scale is one of
 // the 32 elements from at on.
 __device__ __forceinline__ void decode8(uint2 w, uint32_t sbyte, float2* x) {
-  const float f = e8m0_value(sbyte);
+  // (0 stands for 2^-127, a subnormal; 255 only beside codes that are NaN themselves)
+  const float f = __uint_as_float(max(sbyte << 23, 0x00400000u));
   const float2 f2 = make_float2(f, f);
   x[0] = __fmul2_rn(e4m3x2_value(w.x & 0xFFFFu), f2);
   x[1] = __fmul2_rn(e4m3x2_value(w.x >> 16), f2);
@@ -373,9 +374,9 @@ __device__ __forceinline__ void decode8(uint2 w, uint32_t sbyte, float2* x) {
   x[3] = __fmul2_rn(e4m3x2_value(w.y >> 16), f2);
 }
 
-__device__ __forceinline__ float sqrt_hw(float x) {
+__device__ __forceinline__ float sqrt_hw(float x) {  // (v below 2^-126, a subnormal, as 0)
   float y;
-  asm("sqrt.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+  asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
 __device__ __forceinline__ float rcp_hw(float x) {

@@ -802,7 +802,7 @@ MOE_API size_t moe_adamw_workspace_size(int n);
  * block's largest value at or below 448 2^e; a value between two codes goes up
  * if its distance above the lower one, as a fraction of theirs, and 16 random
  * bits over 65536 reach 1 together, and a sqrt(v) > 0 keeps at least the
- * smallest code.  Random bits of element i of tensor j: with the 32-bit hash
+ * smallest code (v below 2^-126 counts as 0).  Random bits of element i of tensor j: with the 32-bit hash
  * f(x): x ^= x >> 16, x *= 0x7FEB352D, x ^= x >> 15, x *= 0x846CA68B, x ^= x >> 16,
  * f(f(f(f(f(t) ^ seed) + j) + (i >> 32)) + i), high half for m and low half for
  * sqrt(v).  A block that holds NaN or an infinity becomes NaN (scale 0xFF).
