@@ -37,7 +37,8 @@ namespace moeglu {
 namespace adamw {
 
 constexpr int THREADS = 256, PER = 8, CHUNK = 2048;  // elements per thread at a time, per chunk
-constexpr int FEW = 64, MANY = 4000;                 // gradient addresses in a launch's parameters (32,764 bytes at most)
+// gradient addresses in a launch's parameters (32,764 bytes at most, each byte copied per launch)
+constexpr int FEW = 64, SOME = 512, MANY = 4000;
 constexpr int BLOCK = 32;                            // elements per scale
 constexpr int MAX_PARTS = 2048;                      // CTAs of the norm's kernel
 constexpr int NEAR = 8;  // fp32 steps around a turning point inside which 64 bits decide
@@ -652,6 +653,8 @@ extern "C" moe_status_t moe_adamw_step(const moe_adamw_tensor_t* tensors, const 
       const moe_status_t e =
           count <= FEW
               ? launch_group<FEW>(dev, at, (uint32_t)c, grads, first, count, p->state, sc, to, np, behind, stream)
+          : count <= SOME
+              ? launch_group<SOME>(dev, at, (uint32_t)c, grads, first, count, p->state, sc, to, np, behind, stream)
               : launch_group<MANY>(dev, at, (uint32_t)c, grads, first, count, p->state, sc, to, np, behind, stream);
       if (e) return e;
       behind = false;

@@ -1217,6 +1217,7 @@ __global__ void __launch_bounds__(ROW_THREADS, OCC) k_rows(const __nv_bfloat16* 
 // against 42, 64 rows of rank 64 28 against 37, 128 rows 43 against 47; with 4 adapters 256 rows of rank 16 21 against
 // 21; 512 rows of 512 x 512, rank 8, 22 against 16.
 constexpr int MOST_ROWS = 256, FEW_ROWS = 4096;
+bool few_rows(int T, int r) { return T <= MOST_ROWS && (int64_t)T * r <= FEW_ROWS; }
 
 size_t up256(size_t n) { return (n + 255) & ~(size_t)255; }
 int used_groups(int T, int G) { return G + 1 < T ? G + 1 : T; }             // at most, the rows without one among them
@@ -1371,9 +1372,12 @@ bool overlap(const void* a, size_t an, const void* b, size_t bn) {
 using namespace moeglu;
 using namespace moeglu::lora;
 
-extern "C" size_t moe_lora_workspace_size(int T, int r, int G) {
-  if (T < 0 || r <= 0 || G <= 0) return 0;
-  return plan_bytes(T, G) + 2 * sorted_bytes(T, r, G);
+extern "C" size_t moe_lora_fwd_workspace_size(int T, int r, int G) {
+  return T <= 0 || r <= 0 || G <= 0 || few_rows(T, r) ? 0 : plan_bytes(T, G) + sorted_bytes(T, r, G);
+}
+
+extern "C" size_t moe_lora_bwd_workspace_size(int T, int r, int G) {
+  return T <= 0 || r <= 0 || G <= 0 ? 0 : plan_bytes(T, G) + 2 * sorted_bytes(T, r, G);
 }
 
 extern "C" moe_status_t moe_lora_fwd(const moe_bf16* x, const moe_bf16* A, const moe_bf16* B, const int32_t* idx,
@@ -1383,7 +1387,8 @@ extern "C" moe_status_t moe_lora_fwd(const moe_bf16* x, const moe_bf16* A, const
   if (!sizes_ok(T, K, N, r, G)) return MOE_ERR_ARG;
   if (r > MAX_R || G > MAX_G) return MOE_ERR_UNSUPPORTED;
   if (T == 0) return MOE_OK;
-  if (!x || !A || !B || !idx || !scale || !y || !ws || ws_bytes < moe_lora_workspace_size(T, r, G)) return MOE_ERR_ARG;
+  const size_t need = moe_lora_fwd_workspace_size(T, r, G);
+  if (!x || !A || !B || !idx || !scale || !y || (need && !ws) || ws_bytes < need) return MOE_ERR_ARG;
   if (!aligned16(x) || !aligned16(A) || !aligned16(B) || !aligned16(base) || !aligned16(y) || !aligned16(h) ||
       (reinterpret_cast<uintptr_t>(ws) & 255u))
     return MOE_ERR_ARG;
@@ -1392,7 +1397,7 @@ extern "C" moe_status_t moe_lora_fwd(const moe_bf16* x, const moe_bf16* A, const
       overlap(y, yn, A, (size_t)G * r * K * 2) || overlap(y, yn, B, (size_t)G * r * N * 2))
     return MOE_ERR_ARG;
   const cudaStream_t s = as_stream(stream);
-  if (T <= MOST_ROWS && (int64_t)T * r <= FEW_ROWS) {
+  if (few_rows(T, r)) {
     const auto k = T * ROW_CTAS <= 4 * sm_count() ? k_rows<4, 2, 4> : k_rows<1, 1, 8>;
     return launch(k, T * ROW_CTAS, ROW_CTAS, ROW_THREADS, 0, 0, false, s, in(x), in(A), in(B), idx, scale, in(base), K, N, r, G,
                   out(y), out(h));
@@ -1418,7 +1423,8 @@ extern "C" moe_status_t moe_lora_bwd(const moe_bf16* dy, const moe_bf16* x, cons
       return MOE_ERR_CUDA;
     return MOE_OK;
   }
-  if (!dy || !x || !h || !A || !B || !idx || !scale || !dx || !ws || ws_bytes < moe_lora_workspace_size(T, r, G))
+  if (!dy || !x || !h || !A || !B || !idx || !scale || !dx || !ws ||
+      ws_bytes < moe_lora_bwd_workspace_size(T, r, G))
     return MOE_ERR_ARG;
   if (!aligned16(dy) || !aligned16(x) || !aligned16(h) || !aligned16(A) || !aligned16(B) || !aligned16(base) ||
       !aligned16(dx) || (reinterpret_cast<uintptr_t>(ws) & 255u))

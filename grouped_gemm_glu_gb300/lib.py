@@ -137,7 +137,8 @@ _SIGS = {
     "moe_dequantize_mxfp8": [P, P, SZ, P, P],
     "moe_router_fwd": [P, I, P, P, I, I, I, C.POINTER(RouterParams), P, P, P, P],
     "moe_router_bwd": [P, I, P, P, I, I, I, C.POINTER(RouterParams), P, P],
-    "moe_lora_workspace_size": ([I, I, I], SZ),
+    "moe_lora_fwd_workspace_size": ([I, I, I], SZ),
+    "moe_lora_bwd_workspace_size": ([I, I, I], SZ),
     "moe_lora_fwd": [P, P, P, P, P, P, I, I, I, I, I, P, P, P, SZ, P, P],
     "moe_lora_bwd": [P, P, P, P, P, P, P, P, I, I, I, I, I, P, P, P, P, SZ, P, P],
     "moe_adamw_plan_size": ([P, I], SZ),

@@ -801,9 +801,27 @@ def route_permute_mxfp8(xq, xs, topk_idx, topk_prob, E: int, R_cap: int, expert_
     return o
 
 
-def _lora_args(x, A, B, idx, scale):
-    """Checks an adapter call's common arguments; returns (T, K, N, r, G)."""
+def _lora_args(x, A, B, idx, scale, more=()):
+    """Checks an adapter call's arguments: the common ones, and (tensor, columns,
+    name) for more bf16 tensors with a row per row of x, None among them; columns
+    "K", "N" or "r".  Returns (T, K, N, r, G)."""
     bf = torch.bfloat16
+    try:
+        (T, K), (G, r, N) = x.shape, B.shape
+        d = x.get_device()
+        fine = (x.dtype is bf and A.dtype is bf and B.dtype is bf and idx.dtype is torch.int32 and scale.dtype is torch.float32
+                and A.shape == (G, r, K) and idx.shape == (T,) and scale.shape == (G,) and x.is_contiguous()
+                and A.is_contiguous() and B.is_contiguous() and idx.is_contiguous() and scale.is_contiguous()
+                and A.get_device() == B.get_device() == idx.get_device() == scale.get_device() == d
+                and d == torch._C._cuda_getDevice() and 0 < r <= 128 and 0 < G <= 32767 and not (r | K | N) & 7 and K > 0 and N > 0)
+        for t, c, _ in more:
+            fine = fine and (t is None or (t.dtype is bf and t.shape == (T, K if c == "K" else N if c == "N" else r)
+                                           and t.is_contiguous() and t.get_device() == d))
+    except (AttributeError, TypeError, ValueError):
+        fine = False
+    if fine:
+        return T, K, N, r, G
+    # what is wrong with them
     T, K = _need2(x, bf, "x")
     for w, what in ((A, "A"), (B, "B")):
         if _need(w, bf, None, what).dim() != 3:
@@ -812,16 +830,16 @@ def _lora_args(x, A, B, idx, scale):
     _need(A, bf, (G, r, K), "A")
     _need(idx, torch.int32, (T,), "idx")
     _need(scale, torch.float32, (G,), "scale")
-    d = x.get_device()
-    if A.get_device() != d or B.get_device() != d or idx.get_device() != d or scale.get_device() != d:
-        raise ValueError("x, A, B, idx and scale must lie on one device")
-    if d != torch.cuda.current_device():
-        raise ValueError(f"the tensors lie on cuda:{d}, which is not the current device")
+    for t, what in ((A, "A"), (B, "B"), (idx, "idx"), (scale, "scale")):
+        _on(t, t.dtype, t.shape, what, x)
+    if x.get_device() != torch.cuda.current_device():
+        raise ValueError(f"the tensors lie on {x.device}, which is not the current device")
+    for t, c, what in more:
+        if t is not None:
+            _on(t, bf, (T, K if c == "K" else N if c == "N" else r), what, x)
     if G == 0 or r == 0 or r % 8 or K % 8 or N % 8 or not K or not N:
         raise ValueError(f"r, K and N must be positive multiples of 8, got r = {r}, K = {K}, N = {N}")
-    if r > 128 or G > 32767:
-        raise ValueError(f"at most rank 128 and 32767 adapters are supported, got {r} and {G}")
-    return T, K, N, r, G
+    raise ValueError(f"at most rank 128 and 32767 adapters are supported, got {r} and {G}")
 
 
 def _on(t, dtype, shape, what, like):
@@ -838,17 +856,14 @@ def lora(x, A, B, idx, scale, base=None, out=None, with_h: bool = True, status=N
     bf16, scale [G] f32, base [T, N] bf16 the projection's output (None: zero),
     out where y goes (may be base).  Returns y [T, N] and, with_h, h [T, r] bf16,
     which lora_bwd reads."""
-    T, K, N, r, G = _lora_args(x, A, B, idx, scale)
-    bf = torch.bfloat16
-    if base is not None:
-        _on(base, bf, (T, N), "base", x)
-    y = _on(out, bf, (T, N), "out", x) if out is not None else torch.empty(T, N, dtype=bf, device=x.device)
-    h = torch.empty(T, r, dtype=bf, device=x.device) if with_h else None
-    n = _size("moe_lora_workspace_size", T, r, G)
-    ws = torch.empty(n, dtype=torch.uint8, device=x.device)
-    L.check(L.load().moe_lora_fwd(x.data_ptr(), A.data_ptr(), B.data_ptr(), idx.data_ptr(), scale.data_ptr(), _ptr(base),
-                                  T, K, N, r, G, y.data_ptr(), _ptr(h), ws.data_ptr(), n, _ptr(status), _cur(x)),
-            "moe_lora_fwd")
+    T, K, N, r, G = _lora_args(x, A, B, idx, scale, ((base, "N", "base"), (out, "N", "out")))
+    bf, dev, lib = torch.bfloat16, x.device, L.load()
+    y = out if out is not None else torch.empty(T, N, dtype=bf, device=dev)
+    h = torch.empty(T, r, dtype=bf, device=dev) if with_h else None
+    n = _size("moe_lora_fwd_workspace_size", T, r, G)
+    ws = torch.empty(n, dtype=torch.uint8, device=dev) if n else None
+    L.check(lib.moe_lora_fwd(x.data_ptr(), A.data_ptr(), B.data_ptr(), idx.data_ptr(), scale.data_ptr(), _ptr(base), T, K, N,
+                             r, G, y.data_ptr(), _ptr(h), _ptr(ws), n, _ptr(status), _cur(x)), "moe_lora_fwd")
     return {"y": y, "h": h} if with_h else {"y": y}
 
 
@@ -856,15 +871,12 @@ def lora_bwd(dy, x, h, A, B, idx, scale, base=None, out=None, status=None):
     """Backward of lora: (dx [T, K], dA [G, r, K], dB [G, r, N]) bf16 from dy
     [T, N] and the forward's x and h.  base [T, K] is the gradient that reaches x
     elsewhere, added to dx (None: zero); out where dx goes (may be base)."""
-    T, K, N, r, G = _lora_args(x, A, B, idx, scale)
-    bf = torch.bfloat16
-    _on(dy, bf, (T, N), "dy", x)
-    _on(h, bf, (T, r), "h", x)
-    if base is not None:
-        _on(base, bf, (T, K), "base", x)
-    dx = _on(out, bf, (T, K), "out", x) if out is not None else torch.empty_like(x)
+    T, K, N, r, G = _lora_args(x, A, B, idx, scale, ((dy, "N", "dy"), (h, "r", "h"), (base, "K", "base"), (out, "K", "out")))
+    if dy is None or h is None:
+        raise ValueError("dy, h: CUDA tensors are needed")
+    dx = out if out is not None else torch.empty_like(x)
     dA, dB = torch.empty_like(A), torch.empty_like(B)
-    n = _size("moe_lora_workspace_size", T, r, G)
+    n = _size("moe_lora_bwd_workspace_size", T, r, G)
     ws = torch.empty(n, dtype=torch.uint8, device=x.device)
     L.check(L.load().moe_lora_bwd(dy.data_ptr(), x.data_ptr(), h.data_ptr(), A.data_ptr(), B.data_ptr(), idx.data_ptr(),
                                   scale.data_ptr(), _ptr(base), T, K, N, r, G, dx.data_ptr(), dA.data_ptr(), dB.data_ptr(),

@@ -10,6 +10,7 @@ gradients of a captured step keep their addresses).
 """
 from __future__ import annotations
 
+import array
 import ctypes as C
 
 import torch
@@ -68,7 +69,7 @@ class AdamW:
             raise ValueError("grad_dtype: float32 or bfloat16 is needed")
         self.weights, self.state, self.max_norm = ws, state, max_norm
         self.device = dev = ws[0].device if ws else torch.device("cuda", torch.cuda.current_device())
-        self._like = [(k, w.shape) for k, w in zip(kinds, ws)]
+        self._dtypes, self._shapes = kinds, [w.shape for w in ws]
         self._at = []
         total = 0
         for w in ws:
@@ -96,11 +97,11 @@ class AdamW:
         lib = L.load()
         kind = L.MOMENTS[state]
         self._p = L.AdamwParams(betas[0], betas[1], eps, max_norm or 0.0, kind, seed & 0xFFFFFFFF)
+        self._pref = C.byref(self._p)
         host = torch.zeros(max(lib.moe_adamw_plan_size(self._rows, n), 8), dtype=u8)
         L.check(lib.moe_adamw_plan(self._rows, n, kind, host.data_ptr(), host.numel()), "moe_adamw_plan")
         self._plan = host.to(dev)
         self._ws = torch.empty(lib.moe_adamw_workspace_size(n), dtype=u8, device=dev)
-        self._grads = (C.c_void_p * max(n, 1))()
 
     def set_lr(self, lr: float):
         """The learning rate of the steps issued (or replayed) from here on."""
@@ -112,22 +113,33 @@ class AdamW:
         """One step with grads, one per weight in the weights' order, of their
         shapes and of grad_dtype, contiguous.  Returns the gradients' 2-norm before
         clipping (a float32 scalar, this object's own buffer) with max_norm, else None."""
-        like, dev = self._like, self.device
-        if len(grads) != len(like):
-            raise ValueError(f"grads: {len(like)} tensors are needed, got {len(grads)}")
-        index = dev.index
-        for i, (g, (dtype, shape)) in enumerate(zip(grads, like)):
-            if g.dtype is not dtype or g.shape != shape or not g.is_contiguous() or not g.is_cuda or g.get_device() != index:
-                raise ValueError(f"grads[{i}]: a contiguous {dtype} tensor {tuple(shape)} on {dev} is needed, got "
-                                 f"{g.dtype} {tuple(g.shape)} on {g.device}")
-        if index != torch.cuda.current_device():
-            raise ValueError(f"step: the weights lie on {dev}, which is not the current device")
-        n = len(like)
-        self._grads[:n] = [g.data_ptr() for g in grads]
-        L.check(L.load().moe_adamw_step(self._rows, self._grads, n, self._plan.data_ptr(), C.byref(self._p),
+        tensor, n, index = torch.Tensor, len(self._shapes), self.device.index
+        try:  # (whole lists at a time: a few hundred tensors are checked in some tens of microseconds)
+            fine = (len(grads) == n and [g.dtype for g in grads] == self._dtypes and [g.shape for g in grads] == self._shapes
+                    and all(map(tensor.is_contiguous, grads)) and set(map(tensor.get_device, grads)) <= {index})
+        except (AttributeError, TypeError):
+            fine = False
+        if not fine:
+            self._refuse(grads)
+        if index != torch._C._cuda_getDevice():
+            raise ValueError(f"step: the weights lie on {self.device}, which is not the current device")
+        at = array.array("Q", map(tensor.data_ptr, grads))
+        L.check(L.load().moe_adamw_step(self._rows, at.buffer_info()[0] if n else None, n, self._plan.data_ptr(), self._pref,
                                         self.lr.data_ptr(), self.t.data_ptr(), self.norm.data_ptr(), self._ws.data_ptr(),
                                         self._ws.numel(), torch._C._cuda_getCurrentRawStream(index)), "moe_adamw_step")
         return self.norm if self.max_norm is not None else None
+
+    def _refuse(self, grads):
+        """What is wrong with these gradients."""
+        if len(grads) != len(self._shapes):
+            raise ValueError(f"grads: {len(self._shapes)} tensors are needed, got {len(grads)}")
+        for i, (g, dtype, shape) in enumerate(zip(grads, self._dtypes, self._shapes)):
+            want = f"grads[{i}]: a contiguous {dtype} tensor {tuple(shape)} on {self.device} is needed"
+            if not isinstance(g, torch.Tensor):
+                raise ValueError(want)
+            if g.dtype != dtype or g.shape != shape or not g.is_contiguous() or g.get_device() != self.device.index:
+                raise ValueError(f"{want}, got {g.dtype} {tuple(g.shape)} on {g.device}")
+        raise ValueError("grads: tensors are needed")
 
     def moments(self, i: int):
         """(m, v) of weight i in its shape, float32; 8-bit states as the values they hold."""

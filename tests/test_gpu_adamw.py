@@ -133,7 +133,7 @@ def test_steps(state, wtypes, gtypes, clip, offset):
 
 
 @pytest.mark.parametrize("state", ["f32", "mxfp8"])
-@pytest.mark.parametrize("count", [65, 4001, 8100])
+@pytest.mark.parametrize("count", [65, 513, 4001, 8100])
 def test_many_tensors(state, count):
     # more than the short launch's addresses, more than one launch's
     c = Case([1 + (i * 7) % 50 for i in range(count)], (BF,), (BF,), state=state, max_norm=0.25)

@@ -15,12 +15,13 @@ def lib():
 
 
 def test_forward(lib):
-    n = lib.moe_lora_workspace_size(100, 16, 4)
-    assert n > 100 * 4 + 100 * 32
-    assert lib.moe_lora_workspace_size(-1, 16, 4) == lib.moe_lora_workspace_size(4, 0, 4) == 0
+    n = lib.moe_lora_fwd_workspace_size(1000, 16, 4)
+    assert n > 1000 * 4 + 1000 * 32
+    assert lib.moe_lora_fwd_workspace_size(-1, 16, 4) == lib.moe_lora_fwd_workspace_size(400, 0, 4) == 0
+    assert lib.moe_lora_fwd_workspace_size(1, 16, 4) == 0  # few rows need none
     P = [A + (i << 24) for i in range(9)]
 
-    def f(x=P[0], a=P[1], b=P[2], idx=P[3], scale=P[4], base=None, T=100, K=64, N=64, r=16, G=4, y=P[5], h=P[6], ws=P[7],
+    def f(x=P[0], a=P[1], b=P[2], idx=P[3], scale=P[4], base=None, T=1000, K=64, N=64, r=16, G=4, y=P[5], h=P[6], ws=P[7],
           nbytes=n):
         return lib.moe_lora_fwd(x, a, b, idx, scale, base, T, K, N, r, G, y, h, ws, nbytes, None, None)
 
@@ -35,7 +36,7 @@ def test_forward(lib):
 
 
 def test_backward(lib):
-    n = lib.moe_lora_workspace_size(100, 16, 4)
+    n = lib.moe_lora_bwd_workspace_size(100, 16, 4)
     P = [A + (i << 24) for i in range(12)]
 
     def f(dy=P[0], x=P[1], h=P[2], a=P[3], b=P[4], idx=P[5], scale=P[6], base=None, T=100, K=64, N=64, r=16, G=4, dx=P[7],
