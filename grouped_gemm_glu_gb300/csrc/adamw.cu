@@ -91,9 +91,9 @@ __device__ __forceinline__ void st_f32x8(float* p, const float* v) {
 }
 __device__ __forceinline__ bool on(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
-// n: elements left from p on (at least 1)
-__device__ __forceinline__ void load8(const float* p, int64_t n, float* v) {
-  if (n >= PER && on(p, 32)) {
+// n: elements left from p on (at least 1); whole: PER of them and aligned
+__device__ __forceinline__ void load8(const float* p, int64_t n, bool whole, float* v) {
+  if (whole) {
     ld_f32x8(p, v);
   } else {
 #pragma unroll
@@ -108,16 +108,16 @@ __device__ __forceinline__ void unpack8(uint4 q, float* v) {
     v[2 * i + 1] = bf16_hi(w[i]);
   }
 }
-__device__ __forceinline__ void load8(const __nv_bfloat16* p, int64_t n, float* v) {
-  if (n >= PER && on(p, 16)) {
+__device__ __forceinline__ void load8(const __nv_bfloat16* p, int64_t n, bool whole, float* v) {
+  if (whole) {
     unpack8(*reinterpret_cast<const uint4*>(p), v);
   } else {
 #pragma unroll
     for (int i = 0; i < PER; ++i) v[i] = i < n ? __bfloat162float(p[i]) : 0.0f;
   }
 }
-__device__ __forceinline__ void store8(float* p, int64_t n, const float* v) {
-  if (n >= PER && on(p, 32)) {
+__device__ __forceinline__ void store8(float* p, int64_t n, bool whole, const float* v) {
+  if (whole) {
     st_f32x8(p, v);
   } else {
 #pragma unroll
@@ -125,8 +125,8 @@ __device__ __forceinline__ void store8(float* p, int64_t n, const float* v) {
       if (i < n) p[i] = v[i];
   }
 }
-__device__ __forceinline__ void store8(__nv_bfloat16* p, int64_t n, const float* v) {
-  if (n >= PER && on(p, 16)) {
+__device__ __forceinline__ void store8(__nv_bfloat16* p, int64_t n, bool whole, const float* v) {
+  if (whole) {
     *reinterpret_cast<uint4*>(p) = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
                                               pack_bf16x2(v[6], v[7]));
   } else {
@@ -178,10 +178,11 @@ __global__ void __launch_bounds__(THREADS, 8) k_adamw_norm(const __grid_constant
             packed[k] = true;
             asm volatile("ld.global.v4.f32 {%0,%1,%2,%3}, [%4];" : "=f"(g[k][0]), "=f"(g[k][1]), "=f"(g[k][2]), "=f"(g[k][3]) : "l"(q));
           } else {
-            load8(q, n, g[k]);
+            load8(q, n, false, g[k]);
           }
         } else {
-          load8(static_cast<const float*>(p) + at, n, g[k]);
+          const auto* q = static_cast<const float*>(p) + at;
+          load8(q, n, n >= PER && on(q, 32), g[k]);
         }
       } else {
 #pragma unroll
@@ -272,6 +273,8 @@ __global__ void __launch_bounds__(256) k_adamw_scalars(Scalars o, double max_nor
 // ---------------------------------------------------------------------------
 // 8-bit moments
 // ---------------------------------------------------------------------------
+__device__ __forceinline__ float2 both(float a) { return make_float2(a, a); }
+
 // The scale byte e + 127 for a block whose largest magnitude has these bits:
 // 448 = 1.75 * 2^8.  `above`: the 64-bit value lies above 1.75 of its power of
 // two (asked where the fp32 one is within NEAR of it).
@@ -296,11 +299,13 @@ __device__ __noinline__ uint32_t code_exact(double a, uint32_t r16) {
 // share a block.  x: the fp32 values, ex(i): the 64-bit value of element i.
 // SHIFT: which half of the random bits.
 //
-// The fp32 pattern of |x| 2^-e, less that of 2^-7 and four places up, has the
-// code of a normal value in its top byte and what lies above it in the 24 bits
-// below; 16 random bits in the upper ones carry into it.  The elements whose
-// low bits come within NEAR fp32 steps of a carry, and those below the normal
-// codes, are found together and done again one by one.
+// The fp32 pattern of x 2^-e, four places up (its sign and the exponent's high
+// bits fall off the word) and with 8 added to the exponent (the two biases, 127
+// and 7, differ by 24 modulo the 32 that are left), has the code of a normal
+// value in its top byte and what lies above it in the 24 bits below; 16 random
+// bits in the upper ones carry into it.  The elements whose low bits come within NEAR fp32 steps of a
+// carry, and those below the normal codes, are found together and done again
+// one by one.
 template <bool LEAST, int SHIFT, class Exact>
 __device__ __forceinline__ uint2 quantise(const float2* x, const uint32_t* bits, Exact ex, uint32_t& sbyte) {
   float peak = 0.0f;
@@ -330,26 +335,28 @@ __device__ __forceinline__ uint2 quantise(const float2* x, const uint32_t* bits,
   sbyte = scale_byte(top, above);
   if (sbyte == 0xFFu) return make_uint2(0x7F7F7F7Fu, 0x7F7F7F7Fu);
   const float inv = mx_inv_scale(sbyte);
-  uint32_t y[PER], least = 0xFFFFFFFFu, close = 0xFFFFFFFFu;
+  constexpr float LOWEST = 0.015625f;  // 2^-6, the smallest normal code's value
+  uint32_t y[PER], close = 0xFFFFFFFFu;
+  float least = 1e30f;
 #pragma unroll
   for (int i = 0; i < PER / 2; ++i) {
-    const float2 a = __fmul2_rn(x[i], make_float2(inv, inv));
+    const float2 a = __fmul2_rn(x[i], both(inv));
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
-      const uint32_t f = __float_as_uint(k ? a.y : a.x), mag = LEAST ? f : f & 0x7FFFFFFFu, r = bits[2 * i + k];
-      const uint32_t v = (mag - (120u << 23)) * 16u + ((SHIFT ? r >> 8 : r << 8) & 0xFFFF00u);
-      least = min(least, mag);
+      const float f = k ? a.y : a.x;
+      const uint32_t v = __float_as_uint(f) * 16u + __byte_perm(bits[2 * i + k], 0x40u, SHIFT ? 0x4325 : 0x4105);
+      least = fminf(least, fabsf(f));
       close = min(close, v * 256u + 16u * NEAR * 256u);
-      y[2 * i + k] = LEAST ? v : v | (f & 0x80000000u);
+      y[2 * i + k] = LEAST ? v : v | (__float_as_uint(f) & 0x80000000u);
     }
   }
   uint2 w = make_uint2(__byte_perm(__byte_perm(y[0], y[1], 0x73), __byte_perm(y[2], y[3], 0x73), 0x5410),
                        __byte_perm(__byte_perm(y[4], y[5], 0x73), __byte_perm(y[6], y[7], 0x73), 0x5410));
-  if (least < 0x3C800000u || close < 32u * NEAR * 256u) {
+  if (least < LOWEST || close < 32u * NEAR * 256u) {
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
-      const uint32_t mag = abs_bits(at(i) * inv), low = y[i] & 0xFFFFFFu;
-      if (mag >= 0x3C800000u && ((low + 16u * NEAR) & 0xFFFFFFu) >= 32u * NEAR) continue;
+      const uint32_t low = y[i] & 0xFFFFFFu;
+      if (fabsf(at(i) * inv) >= LOWEST && ((low + 16u * NEAR) & 0xFFFFFFu) >= 32u * NEAR) continue;
       uint32_t code = 0;
       if (at(i) != 0.0f) {
         code = code_exact(fabs(ex(i)) * (double)inv, SHIFT ? bits[i] >> 16 : bits[i] & 0xFFFFu);
@@ -385,7 +392,6 @@ __device__ __forceinline__ float rcp_hw(float x) {
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
-__device__ __forceinline__ float2 both(float a) { return make_float2(a, a); }
 
 // w <- w - (lr wd w + step m / (sqrt(v) root + eps)): the quotient and the
 // root by the hardware's approximations, good to two fp32 steps; what is taken
@@ -412,24 +418,27 @@ __device__ __forceinline__ void step8(const Short& s, const Scalars* all, const 
   float2 g[PER / 2], w[PER / 2], m[PER / 2], v[PER / 2];
   // a thread past the tensor's end works on zeros: its neighbours' block needs it in the exchange
   const bool live = n > 0;
+  // whole vectors everywhere: one test for all of a thread's loads and stores
+  float* wide = W16 ? t.master : static_cast<float*>(t.w);
+  const bool whole = n >= PER && on(wide + at, 32) && on(grad + at, sizeof(G) * PER) && (!W16 || on(static_cast<__nv_bfloat16*>(t.w) + at, 16)) &&
+                     (STATE8 || (on(static_cast<const float*>(t.m) + at, 32) && on(static_cast<const float*>(t.v) + at, 32)));
 #pragma unroll
   for (int i = 0; i < PER / 2; ++i) g[i] = w[i] = m[i] = v[i] = both(0.0f);
-  float* wide = W16 ? t.master : static_cast<float*>(t.w);
   if (live) {
     // (the gradient last: its bf16 values are taken apart as they come, when all other loads are under way)
     if (STATE8) {
       const uint2 qm = *reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(t.m) + at);
       const uint2 qv = *reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(t.v) + at);
       const uint32_t sm = t.m_scale[at / BLOCK], sv = t.v_scale[at / BLOCK];
-      load8(wide + at, n, &w[0].x);
-      load8(grad + at, n, &g[0].x);
+      load8(wide + at, n, whole, &w[0].x);
+      load8(grad + at, n, whole, &g[0].x);
       decode8(qm, sm, m);
       decode8(qv, sv, v);
     } else {
-      load8(wide + at, n, &w[0].x);
-      load8(static_cast<const float*>(t.m) + at, n, &m[0].x);
-      load8(static_cast<const float*>(t.v) + at, n, &v[0].x);
-      load8(grad + at, n, &g[0].x);
+      load8(wide + at, n, whole, &w[0].x);
+      load8(static_cast<const float*>(t.m) + at, n, whole, &m[0].x);
+      load8(static_cast<const float*>(t.v) + at, n, whole, &v[0].x);
+      load8(grad + at, n, whole, &g[0].x);
     }
   }
   const float decay = s.lr * t.weight_decay;
@@ -451,8 +460,8 @@ __device__ __forceinline__ void step8(const Short& s, const Scalars* all, const 
     }
   }
   if (live) {
-    store8(wide + at, n, &w[0].x);
-    if (W16) store8(static_cast<__nv_bfloat16*>(t.w) + at, n, &w[0].x);
+    store8(wide + at, n, whole, &w[0].x);
+    if (W16) store8(static_cast<__nv_bfloat16*>(t.w) + at, n, whole, &w[0].x);
   }
   if (STATE8) {
     uint32_t bits[PER];
@@ -472,8 +481,8 @@ __device__ __forceinline__ void step8(const Short& s, const Scalars* all, const 
       }
     }
   } else if (live) {
-    store8(static_cast<float*>(t.m) + at, n, &om[0].x);
-    store8(static_cast<float*>(t.v) + at, n, &ov[0].x);
+    store8(static_cast<float*>(t.m) + at, n, whole, &om[0].x);
+    store8(static_cast<float*>(t.v) + at, n, whole, &ov[0].x);
   }
 }
 
