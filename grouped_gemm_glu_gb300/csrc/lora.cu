@@ -27,6 +27,12 @@
 // a contraction and add their sums through distributed shared memory, always
 // in the same order, so equal inputs give equal bits.
 // Few rows (decoding) take k_rows instead: one cluster per row, one launch.
+//
+// Measured: 8192 x 7168 with 32 adapters of rank 16, forward 73 us (grouping 6;
+// k_shrink 24, 117 MB at 4.9 TB/s, where a kernel that only loads them takes 21;
+// k_expand 43, 235 MB at 5.5 TB/s, where a plain copy takes 38 to 40); with 8 of
+// rank 32, backward 129 us (k_wgrad 50 for both gradients, 4.7 TB/s); one row
+// of 2880 5.1 us, 64 rows of 7168 with 64 adapters 8.2 us.
 #include "common.cuh"
 #include "host_common.h"
 
@@ -41,16 +47,11 @@ constexpr int ALIGN = 16;  // an adapter's first place in the grouped order: the
 constexpr int MIN_BOX = 8; // fewer neighbours than this are copied row by row
 
 struct Tile {
-  int adapter, start, count;  // -1: rows without an adapter; first place in the grouped order
-  int cost;                   // of the tiles before it (see tile_cost)
+  int adapter, start, count, pad;  // -1: rows without an adapter; first place in the grouped order
 };
-// What a unit of k_expand costs: its chain of waits more than its rows (1 + slabs took 73 us, 3 + slabs 55, 5 + slabs 49
-// and this 47 us at 8192 x 7168, rank 32, 8 adapters).
-__host__ __device__ __forceinline__ int tile_cost(int count) { return 8 + (count + SLAB - 1) / SLAB; }
-
 // Workspace: the grouped order.
 struct Plan {
-  int* sums;    // tiles with an adapter, all tiles, cost of all tiles
+  int* sums;    // tiles with an adapter, all tiles, k_expand's jobs taken
   int* first;   // [G + 2]: each adapter's first place; the rows without one; the end
   Tile* tiles;
   int* rows;    // row of each place, -1 where there is none
@@ -225,7 +226,7 @@ __device__ __forceinline__ int warp_scan(int v) {  // inclusive
 __global__ void __launch_bounds__(GROUP_THREADS) k_group(const int32_t* __restrict__ idx, int T, int G, int warps, Plan p) {
   launch_dependents();
   extern __shared__ int hist[];  // [G + 1][warps]
-  __shared__ int part[3][32], count[GROUP_THREADS], begin[GROUP_THREADS], tile_at[GROUP_THREADS], cost_at[GROUP_THREADS];
+  __shared__ int part[2][32], count[GROUP_THREADS], begin[GROUP_THREADS], tile_at[GROUP_THREADS];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, groups = G + 1;
   const int per = ((T + warps - 1) / warps + 31) & ~31;
   const int lo = min(T, warp * per), hi = warp < warps ? min(T, lo + per) : lo;
@@ -254,8 +255,8 @@ __global__ void __launch_bounds__(GROUP_THREADS) k_group(const int32_t* __restri
   });
   __syncthreads();
   // 1024 groups at a time: the rows of each before each warp's, and the sums over the groups before it (rows up to
-  // whole ALIGNs, tiles, cost)
-  int rows0 = 0, tiles0 = 0, cost0 = 0;
+  // whole ALIGNs, tiles)
+  int rows0 = 0, tiles0 = 0;
   const bool few = groups <= GROUP_THREADS;  // (then `begin` still holds every group's first place in the end)
   for (int g0 = 0; g0 < groups; g0 += GROUP_THREADS) {
     for (int g = g0 + warp; g < min(groups, g0 + GROUP_THREADS); g += GROUP_THREADS / 32) {
@@ -265,33 +266,29 @@ __global__ void __launch_bounds__(GROUP_THREADS) k_group(const int32_t* __restri
     }
     __syncthreads();
     const int g = g0 + tid, n = g < groups ? count[tid] : 0;
-    const int full = n / TILE, rest = n - full * TILE;
-    const int up = (n + ALIGN - 1) / ALIGN * ALIGN, tiles = full + (rest > 0);
-    const int cost = full * tile_cost(TILE) + (rest > 0 ? tile_cost(rest) : 0);
-    int rs = warp_scan(up), ts = warp_scan(tiles), cs = warp_scan(cost);
-    if (lane == 31) part[0][warp] = rs, part[1][warp] = ts, part[2][warp] = cs;
+    const int up = (n + ALIGN - 1) / ALIGN * ALIGN, tiles = (n + TILE - 1) / TILE;
+    int rs = warp_scan(up), ts = warp_scan(tiles);
+    if (lane == 31) part[0][warp] = rs, part[1][warp] = ts;
     __syncthreads();
-    if (warp < 3) part[warp][lane] = warp_scan(part[warp][lane]);
+    if (warp < 2) part[warp][lane] = warp_scan(part[warp][lane]);
     __syncthreads();
-    if (warp) rs += part[0][warp - 1], ts += part[1][warp - 1], cs += part[2][warp - 1];
+    if (warp) rs += part[0][warp - 1], ts += part[1][warp - 1];
     begin[tid] = rows0 + rs - up;
     tile_at[tid] = tiles0 + ts - tiles;
-    cost_at[tid] = cost0 + cs - cost;
     if (g < groups) p.first[g] = begin[tid];
     if (g == G) {
       p.first[groups] = begin[tid] + up;
       p.sums[0] = tile_at[tid];
       p.sums[1] = tile_at[tid] + tiles;
-      p.sums[2] = cost_at[tid] + cost;
+      p.sums[2] = 0;
     }
     rows0 += part[0][31];
     tiles0 += part[1][31];
-    cost0 += part[2][31];
     __syncthreads();
     for (int k = warp; k < min(groups - g0, GROUP_THREADS); k += GROUP_THREADS / 32) {
       const int c = count[k], r0 = begin[k], a = g0 + k;
       for (int i = lane; i * TILE < c; i += 32)
-        p.tiles[tile_at[k] + i] = {a < G ? a : -1, r0 + i * TILE, min(TILE, c - i * TILE), cost_at[k] + i * tile_cost(TILE)};
+        p.tiles[tile_at[k] + i] = {a < G ? a : -1, r0 + i * TILE, min(TILE, c - i * TILE), 0};
       if (c + lane < (c + ALIGN - 1) / ALIGN * ALIGN) p.rows[r0 + c + lane] = -1;
       if (!few && lane < warps) hist[a * warps + lane] += r0;
     }
@@ -814,16 +811,24 @@ __global__ void __launch_bounds__(WGRAD_THREADS) k_wgrad(const __grid_constant__
 
 // ---------------------------------------------------------------------------
 // k_expand: y = base + h Q over units of (tile, 128 columns).  Several CTAs per
-// SM, each with a stretch of neighbouring units that cost about the same
-// together.  A CTA multiplies, adds and stores one unit at a time while the
-// next one's rows of base are on their way (where shared memory has room for
-// them), and the SM's other CTAs fill its waits.
+// SM take jobs of one or two neighbouring units from a counter (a unit whose rows are
+// no neighbours takes twice as long as others, one with few rows little less:
+// fixed shares by any count left some CTAs working for twice as long as most).
+// A CTA multiplies, adds and stores one unit at a time while the next one's
+// rows of base are on their way (where shared memory has room for them), and
+// the SM's other CTAs fill its waits.
 // Warps 0 to 3 load 32 rows each, warp 4 issues the MMAs, all eight add and
 // store 32 rows x 64 columns each.
 // ---------------------------------------------------------------------------
 constexpr int EXPAND_THREADS = 256;
+// Units in a job: two share the tile's h and its rows' numbers; 8192 x 7168 with rank 16, forward, 73.1 us, one by one
+// 73.8, threes 74.5; 512 rows of 64 adapters 42.5, 46.4, 43.4.  Ones while every unit has a CTA of its own (300 x 512:
+// 12.3 us, twos 14.1).
+constexpr int expand_job(int64_t units, int ctas) { return units > ctas ? 2 : 1; }
 __host__ __device__ constexpr int expand_q(int rp) { return rp * 256; }
-__host__ __device__ constexpr int expand_ahead(int rp) { return rp <= 64 ? 1 : 0; }  // units of base loaded ahead
+// Units of base loaded ahead: where three CTAs' shared memory has room for it (ranks up to 16: the forward of 8192 x
+// 7168 77 us against 79 without; with rank 32 it would leave room for two: 46.7 us against 45.2, each with fixed shares).
+__host__ __device__ constexpr int expand_ahead(int rp) { return rp <= 16 ? 1 : 0; }
 constexpr int expand_bytes(int rp) {
   return (1 + expand_ahead(rp)) * TILE * 256 + expand_q(rp) + TILE * rank_bytes(rp) + 1024;
 }
@@ -834,12 +839,12 @@ __global__ void __launch_bounds__(EXPAND_THREADS, 3) k_expand(const __grid_const
                                                               const __grid_constant__ CUtensorMap my,
                                                               const __grid_constant__ CUtensorMap mb8,
                                                               const __grid_constant__ CUtensorMap my8,
-                                                              const __nv_bfloat16* base, int N, int r, int rp, Plan plan,
-                                                              __nv_bfloat16* y, uint64_t limit_ns, int32_t* status) {
+                                                              const __nv_bfloat16* base, int N, int r, int rp, int job,
+                                                              Plan plan, __nv_bfloat16* y, uint64_t limit_ns, int32_t* status) {
   extern __shared__ unsigned char smem_[];
   unsigned char* smem = aligned_smem(smem_);
   __shared__ uint64_t rows_in[2], product_in, product_out;  // base's rows, h and Q in shared memory; the MMAs' end
-  __shared__ int abort_, never, begin_tile, begin_chunk;
+  __shared__ int abort_, never, taken[2];  // (the jobs behind this one, by turns)
   __shared__ uint32_t tmem_;
   const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31, slab = warp & 3, block = warp >> 2;
   const int ahead = expand_ahead(rp);
@@ -858,20 +863,10 @@ __global__ void __launch_bounds__(EXPAND_THREADS, 3) k_expand(const __grid_const
   }
   launch_dependents();
   wait_for_primary();
-  // units in the order (tile, chunk); this CTA's are those whose cost begins in its share of all
-  const int chunks = (N + TILE - 1) / TILE, tiles = plan.sums[1];
-  const int64_t all = (int64_t)plan.sums[2] * chunks;
-  const int64_t lo = all * blockIdx.x / gridDim.x, hi = all * (blockIdx.x + 1) / gridDim.x;
-  for (int i = threadIdx.x; i < tiles; i += EXPAND_THREADS) {
-    const Tile t = plan.tiles[i];
-    const int64_t from = (int64_t)t.cost * chunks, each = tile_cost(t.count);
-    // (the first unit that begins at or behind lo lies in this tile, or at the start of the next)
-    if (from <= lo && lo < from + each * chunks) {
-      const int c = (int)((lo - from + each - 1) / each);
-      begin_tile = c < chunks ? i : i + 1;
-      begin_chunk = c < chunks ? c : 0;
-    }
-  }
+  const int chunks = (N + TILE - 1) / TILE, per_tile = (chunks + job - 1) / job;
+  const int64_t jobs = (int64_t)plan.sums[1] * per_tile;  // in the order (tile, columns); the first are the CTAs' numbers
+  auto take = [&] { return (int)gridDim.x + atomicAdd(plan.sums + 2, 1); };
+  if (threadIdx.x == 0) taken[0] = take();
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -879,20 +874,22 @@ __global__ void __launch_bounds__(EXPAND_THREADS, 3) k_expand(const __grid_const
   const uint32_t tmem = uniform(tmem_);
   const uint32_t idesc = idesc_bf16_f32(TILE, TILE) | B_MN, hrow = rp > 64 ? 128 : rank_bytes(rp);
 
-  // a tile of this CTA: its chunks up to `end`, and the warp's slab of it
+  // a job: its tile's adapter and place, its chunks, and the warp's slab of the tile
   struct Part {
-    int adapter, start, end;
+    int adapter, start, chunk, end;
     Slab s;
   };
-  auto part_of = [&](int tile) {
-    Part p{-1, 0, 0, {}};
+  auto part_of = [&](int number) {
+    Part p{-1, 0, 0, 0, {}};
     int row = -1;
-    if (tile < tiles) {
+    number = uniform(number);
+    if (number < jobs) {
+      const int tile = number / per_tile;
       const Tile t = plan.tiles[tile];
-      const int64_t from = (int64_t)t.cost * chunks, each = tile_cost(t.count);
       p.adapter = uniform(t.adapter);
       p.start = uniform(t.start);
-      p.end = uniform(hi > from ? (int)min((int64_t)chunks, (hi - from + each - 1) / each) : 0);
+      p.chunk = (number - tile * per_tile) * job;
+      p.end = min(p.chunk + job, chunks);
       const int place = SLAB * slab + lane;
       if (place < t.count) row = plan.rows[t.start + place];
     }
@@ -909,7 +906,7 @@ __global__ void __launch_bounds__(EXPAND_THREADS, 3) k_expand(const __grid_const
     uint64_t* bar = &rows_in[buf];
     if (!base || p.s.count == 0) {
       if (elect_one()) mbar_arrive_warp(bar);
-    } else if (p.s.box) {
+    } else if (p.s.box && p.s.count > SLAB / 2) {
       if (elect_one()) {
         mbar_expect_tx(bar, SLAB * 128 * (two ? 2 : 1));
         tma_2d(to, &mb, bar, c0, p.s.first);
@@ -956,9 +953,9 @@ __global__ void __launch_bounds__(EXPAND_THREADS, 3) k_expand(const __grid_const
     if (two) tma_3d(q_at + rp * 128, &mq, &product_in, c0 + 64, 0, p.adapter);
   };
 
-  int tile = lo < hi ? begin_tile : tiles, chunk = begin_chunk;
-  Part now = part_of(tile), next = part_of(tile + 1);
-  bool more = tile < tiles && chunk < now.end;
+  Part now = part_of(blockIdx.x), next = part_of(taken[0]);
+  int chunk = now.chunk, done = 0;  // jobs done
+  bool more = now.end > 0;
   int turn[2] = {0, 0}, products = 0, buf = 0;
   if (more) {
     if (warp < 4) load_rows(now, chunk, 0);
@@ -966,9 +963,10 @@ __global__ void __launch_bounds__(EXPAND_THREADS, 3) k_expand(const __grid_const
     __syncwarp();
   }
   while (more) {
-    const bool last = chunk + 1 == now.end;  // of this tile
+    const bool last = chunk + 1 == now.end;  // of this job
     const bool product = now.adapter >= 0, another = !last || next.end > 0;
-    const int c0 = chunk * TILE, next_chunk = last ? 0 : chunk + 1;
+    const int c0 = chunk * TILE, next_chunk = last ? next.chunk : chunk + 1;
+    if (threadIdx.x == 0 && chunk == now.chunk && next.end > 0) taken[(done + 1) & 1] = take();
     if (ahead && another && warp < 4) load_rows(last ? next : now, next_chunk, buf ^ 1);
     bool ok = true;
     if (product) {
@@ -1050,7 +1048,8 @@ __global__ void __launch_bounds__(EXPAND_THREADS, 3) k_expand(const __grid_const
     chunk = next_chunk;
     if (last) {
       now = next;
-      next = part_of(++tile + 1);
+      ++done;
+      next = now.end > 0 ? part_of(taken[done & 1]) : Part{-1, 0, 0, 0, {}};
     }
     more = another;
     if (!ahead && another && warp < 4) load_rows(now, chunk, 0);
@@ -1346,14 +1345,14 @@ moe_status_t expand(const moe_bf16* hs, const moe_bf16* Q, const moe_bf16* base,
   if (sms < 1) return MOE_ERR_CUDA;
   const int64_t units = (int64_t)max_tiles(T, G) * ((N + TILE - 1) / TILE);
   const int per_sm = 228 * 1024 / (bytes + 2048) < 3 ? 228 * 1024 / (bytes + 2048) : 3;  // (registers: three)
-  const int grid = units < sms * per_sm ? (int)units : sms * per_sm;
+  const int grid = units < sms * per_sm ? (int)units : sms * per_sm, job = expand_job(units, grid);
   CUtensorMap mh, mq, mb, my, mb8, my8;
   if (!map_rows(&mh, hs, places(T, G), r, rank_cols(rp), TILE) || !map_weight(&mq, Q, G, r, N, rp) ||
       !map_rows(&mb, base ? base : y, T, N, 64, SLAB) || !map_rows(&my, y, T, N, 64, SLAB) ||
       !map_rows(&mb8, base ? base : y, T, N, 64, 8) || !map_rows(&my8, y, T, N, 64, 8))
     return MOE_ERR_CUDA;
-  return launch(k_expand, grid, 0, EXPAND_THREADS, bytes, expand_bytes(MAX_R), true, s, mh, mq, mb, my, mb8, my8, in(base), N, r, rp, p, out(y),
-                g_wait_limit_ns.load(), st);
+  return launch(k_expand, grid, 0, EXPAND_THREADS, bytes, expand_bytes(MAX_R), true, s, mh, mq, mb, my, mb8, my8, in(base), N, r, rp, job, p,
+                out(y), g_wait_limit_ns.load(), st);
 }
 
 bool sizes_ok(int T, int K, int N, int r, int G) {
