@@ -82,7 +82,8 @@ class MoeBlock:
         """x [T, H] bf16 (the previous sublayer's output), residual [T, H] the
         stream it is added to; T is the layer's, other sizes are refused.
         adapter [T] int32: each token's adapter (-1: none; a token that
-        token_mask takes from the experts keeps its adapter).
+        token_mask takes from the experts keeps its adapter); the backward
+        reads it again.
         Returns (out [T, H], h [T, H]): the experts' output and the new stream,
         the next sublayer's x and residual.  out is the layer's own buffer: the
         next forward overwrites it."""

@@ -36,6 +36,8 @@
 #include "common.cuh"
 #include "host_common.h"
 
+#include <initializer_list>
+
 namespace moeglu {
 namespace lora {
 
@@ -1360,9 +1362,17 @@ bool sizes_ok(int T, int K, int N, int r, int G) {
          r % 8 == 0 && G > 0;
 }
 
-bool overlap(const void* a, size_t an, const void* b, size_t bn) {
-  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
-  return a && b && x < y + bn && y < x + an;
+struct Span {
+  const void* p;
+  size_t n;
+};
+bool overlaps(const Span& out, std::initializer_list<Span> others) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(out.p);
+  for (const Span& o : others) {
+    const uintptr_t y = reinterpret_cast<uintptr_t>(o.p);
+    if (out.p && o.p && x < y + o.n && y < x + out.n) return true;
+  }
+  return false;
 }
 
 }  // namespace lora
@@ -1391,9 +1401,9 @@ extern "C" moe_status_t moe_lora_fwd(const moe_bf16* x, const moe_bf16* A, const
   if (!aligned16(x) || !aligned16(A) || !aligned16(B) || !aligned16(base) || !aligned16(y) || !aligned16(h) ||
       (reinterpret_cast<uintptr_t>(ws) & 255u))
     return MOE_ERR_ARG;
-  const size_t yn = (size_t)T * N * 2;
-  if ((base != y && overlap(y, yn, base, yn)) || overlap(y, yn, x, (size_t)T * K * 2) ||
-      overlap(y, yn, A, (size_t)G * r * K * 2) || overlap(y, yn, B, (size_t)G * r * N * 2))
+  const Span sx{x, (size_t)T * K * 2}, sa{A, (size_t)G * r * K * 2}, sb{B, (size_t)G * r * N * 2}, si{idx, (size_t)T * 4},
+      sf{scale, (size_t)G * 4}, sy{y, (size_t)T * N * 2}, sh{h, (size_t)T * r * 2}, other{base == y ? nullptr : base, sy.n};
+  if (overlaps(sy, {sx, sa, sb, si, sf, sh, other}) || overlaps(sh, {sx, sa, sb, si, sf, other}))
     return MOE_ERR_ARG;
   const cudaStream_t s = as_stream(stream);
   if (few_rows(T, r)) {
@@ -1428,9 +1438,11 @@ extern "C" moe_status_t moe_lora_bwd(const moe_bf16* dy, const moe_bf16* x, cons
   if (!aligned16(dy) || !aligned16(x) || !aligned16(h) || !aligned16(A) || !aligned16(B) || !aligned16(base) ||
       !aligned16(dx) || (reinterpret_cast<uintptr_t>(ws) & 255u))
     return MOE_ERR_ARG;
-  const size_t xn = (size_t)T * K * 2, an = (size_t)G * r * K * 2, bn = (size_t)G * r * N * 2;
-  if ((base != dx && overlap(dx, xn, base, xn)) || overlap(dx, xn, x, xn) || overlap(dx, xn, dy, (size_t)T * N * 2) ||
-      overlap(dx, xn, h, (size_t)T * r * 2) || overlap(dx, xn, A, an) || overlap(dA, an, A, an) || overlap(dB, bn, B, bn))
+  const Span sx{x, (size_t)T * K * 2}, sy{dy, (size_t)T * N * 2}, sh{h, (size_t)T * r * 2}, sa{A, (size_t)G * r * K * 2},
+      sb{B, (size_t)G * r * N * 2}, si{idx, (size_t)T * 4}, sf{scale, (size_t)G * 4}, other{base == dx ? nullptr : base, sx.n},
+      odx{dx, sx.n}, oda{dA, sa.n}, odb{dB, sb.n};
+  if (overlaps(odx, {sx, sy, sh, sa, sb, si, sf, other}) ||
+      overlaps(oda, {sx, sy, sh, sa, sb, si, sf, other, odx}) || overlaps(odb, {sx, sy, sh, sa, sb, si, sf, other, odx, oda}))
     return MOE_ERR_ARG;
   const Plan p = plan_at(ws, T, G);
   auto* us = reinterpret_cast<moe_bf16*>(static_cast<char*>(ws) + plan_bytes(T, G));

@@ -31,6 +31,9 @@ class AdamW:
         keeps m and v, "mxfp8" keeps m and sqrt(v) as E4M3 codes with a scale
         per 32 elements, rounded up or down by random bits that seed starts.
         grad_dtype: one type or one per tensor (default: the weight's).
+        A weight keeps its memory for as long as this object lives: one that is
+        given another (w.data = ...) is no longer updated.  Steps of one object
+        share their state and workspace and follow one another.
 
         Flat state, one stretch per tensor from a multiple of 32 on: m and v
         (float32, or uint8 codes with scales ms and vs), master (float32, where
@@ -68,6 +71,7 @@ class AdamW:
         if any(k not in (torch.float32, torch.bfloat16) for k in kinds):
             raise ValueError("grad_dtype: float32 or bfloat16 is needed")
         self.weights, self.state, self.max_norm = ws, state, max_norm
+        self._memory = [w.detach() for w in ws]  # what the plan's addresses point at stays allocated
         self.device = dev = ws[0].device if ws else torch.device("cuda", torch.cuda.current_device())
         self._dtypes, self._shapes = kinds, [w.shape for w in ws]
         self._at = []

@@ -733,8 +733,8 @@ MOE_API size_t moe_lora_bwd_workspace_size(int T, int r, int G);
  * rows up to the largest.  Rows may come in any order of adapters.
  * K, N and r multiples of 8, K and N at most 2^20, r <= 128 and G <= 32767
  * (else MOE_ERR_UNSUPPORTED); bf16 buffers 16-byte, ws
- * (moe_lora_fwd_workspace_size bytes) 256-byte aligned; y overlaps no input but an
- * identical base.  status (nullable) receives MOE_ERR_TIMEOUT from a pipeline
+ * (moe_lora_fwd_workspace_size bytes) 256-byte aligned; y and h overlap no input
+ * (but y an identical base) nor one another.  status (nullable) receives MOE_ERR_TIMEOUT from a pipeline
  * wait that gave up.  T == 0 launches nothing. */
 MOE_API moe_status_t moe_lora_fwd(const moe_bf16* x, const moe_bf16* A, const moe_bf16* B, const int32_t* idx,
                                   const float* scale, const moe_bf16* base, int T, int K, int N, int r, int G, moe_bf16* y,
@@ -746,7 +746,8 @@ MOE_API moe_status_t moe_lora_fwd(const moe_bf16* x, const moe_bf16* A, const mo
  * base [T][K] (NULL: zero; may be dx itself) is the gradient that reaches x
  * elsewhere.  dA and dB are written whole (zero for adapters without rows) and
  * summed in fp32 in a fixed order: the same inputs give the same bits.  scale
- * carries no gradient.  ws: moe_lora_bwd_workspace_size bytes, aligned as there. */
+ * carries no gradient.  The outputs overlap no input (but dx an identical base)
+ * nor one another.  ws: moe_lora_bwd_workspace_size bytes, aligned as there. */
 MOE_API moe_status_t moe_lora_bwd(const moe_bf16* dy, const moe_bf16* x, const moe_bf16* h, const moe_bf16* A,
                                   const moe_bf16* B, const int32_t* idx, const float* scale, const moe_bf16* base, int T,
                                   int K, int N, int r, int G, moe_bf16* dx, moe_bf16* dA, moe_bf16* dB, void* ws,

@@ -350,3 +350,26 @@ def test_refusals():
             AdamW(ws, lr=1e-3)
     AdamW([], lr=1e-3).step([])
     assert ops.read_status(ops.new_status(DEV)) == L.MOE_OK
+
+
+@pytest.mark.parametrize("state", ["f32", "mxfp8"])
+@pytest.mark.parametrize("betas", [(0.0, 0.0), (0.0, 0.999), (0.9, 0.0)])
+def test_betas_of_zero(state, betas):
+    c = Case([33, 5003], (BF, F32), (BF, F32), seed=8, state=state, betas=betas, max_norm=0.5)
+    for _ in range(2):
+        was = c.before()
+        g = c.grads()
+        c.check(g, was, c.opt.step(g))
+
+
+def test_replaced_memory():
+    # the step goes on with the memory that the weight had, and leaves the new one alone
+    w = torch.ones(5000, device=DEV)
+    old = w.detach()
+    opt = AdamW([w], lr=0.5, weight_decay=0.0)
+    w.data = torch.ones(5000, device=DEV)
+    del old
+    others = [torch.ones(5000, device=DEV) for _ in range(4)]  # (would take freed memory)
+    opt.step([torch.ones(5000, device=DEV)])
+    assert bool((w == 1).all()) and all(bool((o == 1).all()) for o in others)
+    assert bool((opt._memory[0] < 1).all())

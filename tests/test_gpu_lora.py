@@ -297,6 +297,32 @@ def test_offsets_past_32_bits():
     torch.cuda.empty_cache()
 
 
+@pytest.mark.parametrize("T,r", [(76, 16), (77, 16), (256, 16), (257, 16), (128, 32), (129, 32), (256, 8)])
+def test_around_the_few_rows_rule(T, r):
+    c = Case(T, 136, 264, r, 5, "rows", seed=T)
+    _backward(c, _forward(c)["h"])
+
+
+def test_whatever_the_workspace_held():
+    c = Case(700, 264, 520, 40, 6, "runs", seed=14)
+    want = _forward(c)
+    back = ops.lora_bwd(c.dy_, c.x_, want["h"], c.A_, c.B_, c.idx_, c.scale_, base=c.xb_)
+    lib, p = L.load(), lambda t: None if t is None else t.data_ptr()
+    stream = torch.cuda.current_stream().cuda_stream
+    n, nb = lib.moe_lora_fwd_workspace_size(700, 40, 6), lib.moe_lora_bwd_workspace_size(700, 40, 6)
+    for fill in (0, 0x7F, 0xFF):
+        y, h = torch.empty_like(want["y"]), torch.empty_like(want["h"])
+        ws = torch.full((max(n, nb) + 512,), fill, dtype=torch.uint8, device=DEV)
+        assert lib.moe_lora_fwd(p(c.x_), p(c.A_), p(c.B_), p(c.idx_), p(c.scale_), p(c.yb_), 700, 264, 520, 40, 6, p(y), p(h),
+                                p(ws), n, None, stream) == L.MOE_OK
+        assert torch.equal(y, want["y"]) and torch.equal(h, want["h"]) and bool((ws[n:] == fill).all())
+        ws.fill_(fill)
+        out = [torch.empty_like(t) for t in back]
+        assert lib.moe_lora_bwd(p(c.dy_), p(c.x_), p(h), p(c.A_), p(c.B_), p(c.idx_), p(c.scale_), p(c.xb_), 700, 264, 520, 40, 6,
+                                *map(p, out), p(ws), nb, None, stream) == L.MOE_OK
+        assert all(torch.equal(a, b) for a, b in zip(out, back)) and bool((ws[nb:] == fill).all())
+
+
 def test_refusals():
     c = Case(10, 16, 24, 8, 2, "runs")
     f = lambda **k: ops.lora(**{"x": c.x_, "A": c.A_, "B": c.B_, "idx": c.idx_, "scale": c.scale_, **k})

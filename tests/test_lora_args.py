@@ -29,7 +29,8 @@ def test_forward(lib):
                dict(nbytes=n - 1), dict(T=-1), dict(T=(1 << 27) + 1), dict(K=0), dict(K=60), dict(N=12), dict(r=0),
                dict(r=4), dict(G=0), dict(K=(1 << 20) + 8), dict(x=P[0] + 8), dict(a=P[1] + 2), dict(b=P[2] + 8),
                dict(base=P[8] + 8), dict(y=P[5] + 8), dict(h=P[6] + 8), dict(ws=P[7] + 16), dict(y=P[0]), dict(y=P[1]),
-               dict(y=P[2] + 16), dict(base=P[5] + 16)):
+               dict(y=P[2] + 16), dict(base=P[5] + 16), dict(y=P[3]), dict(y=P[4]), dict(y=P[6] - 1024), dict(h=P[0]),
+               dict(h=P[3]), dict(h=P[8], base=P[8])):
         assert f(**kw) == L.MOE_ERR_ARG, kw
     assert f(r=136) == f(G=32768) == L.MOE_ERR_UNSUPPORTED
     assert f(T=0, x=None, y=None, ws=None) == L.MOE_OK
@@ -47,6 +48,7 @@ def test_backward(lib):
                dict(dx=None), dict(da=None), dict(db=None), dict(ws=None), dict(nbytes=n - 1), dict(T=-1), dict(K=4),
                dict(N=0), dict(r=12), dict(G=-1), dict(dy=P[0] + 8), dict(x=P[1] + 8), dict(h=P[2] + 8), dict(da=P[8] + 8),
                dict(dx=P[7] + 2), dict(ws=P[10] + 128), dict(dx=P[0]), dict(dx=P[1]), dict(dx=P[2]), dict(dx=P[3]),
-               dict(da=P[3]), dict(db=P[4]), dict(base=P[7] + 32)):
+               dict(da=P[3]), dict(db=P[4]), dict(base=P[7] + 32), dict(dx=P[4]), dict(dx=P[5]), dict(da=P[1]), dict(da=P[4]),
+               dict(da=P[7]), dict(db=P[0] + 64), dict(db=P[2]), dict(db=P[8]), dict(db=P[6])):
         assert f(**kw) == L.MOE_ERR_ARG, kw
     assert f(r=136) == L.MOE_ERR_UNSUPPORTED
