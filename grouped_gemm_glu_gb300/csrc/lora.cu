@@ -31,7 +31,7 @@
 // Measured: 8192 x 7168 with 32 adapters of rank 16, forward 73 us (grouping 6;
 // k_shrink 24, 117 MB at 4.9 TB/s, where a kernel that only loads them takes 21;
 // k_expand 43, 235 MB at 5.5 TB/s, where a plain copy takes 38 to 40); with 8 of
-// rank 32, backward 129 us (k_wgrad 50 for both gradients, 4.7 TB/s); one row
+// rank 32, backward 126 us (k_wgrad 50 for both gradients, 4.7 TB/s); one row
 // of 2880 5.1 us, 64 rows of 7168 with 64 adapters 8.2 us.
 #include "common.cuh"
 #include "host_common.h"
@@ -89,6 +89,15 @@ __device__ __forceinline__ void tma_2d(uint32_t dst, const CUtensorMap* m, uint6
   asm volatile(
       "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], [%2];" ::"r"(dst),
       "l"(reinterpret_cast<uint64_t>(m)), "r"(smem_u32(bar)), "r"(c0), "r"(c1)
+      : "memory");
+}
+// (of data that nothing reads again soon: they leave L2 before others)
+__device__ __forceinline__ void tma_2d_once(uint32_t dst, const CUtensorMap* m, uint64_t* bar, int32_t c0, int32_t c1) {
+  uint64_t first;
+  asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(first));
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1, {%3, %4}], [%2], %5;" ::
+          "r"(dst), "l"(reinterpret_cast<uint64_t>(m)), "r"(smem_u32(bar)), "r"(c0), "r"(c1), "l"(first)
       : "memory");
 }
 __device__ __forceinline__ void tma_3d(uint32_t dst, const CUtensorMap* m, uint64_t* bar, int32_t c0, int32_t c1, int32_t c2) {
@@ -349,7 +358,8 @@ __global__ void __launch_bounds__(SHRINK_THREADS) k_shrink(const __grid_constant
   launch_dependents();
   wait_for_primary();
   if (tile >= plan.sums[1]) return;  // (the whole cluster)
-  const Tile t = plan.tiles[tile];
+  // backwards: k_wgrad, next in the backward, begins with the first tiles and finds dy's last read rows in L2
+  const Tile t = plan.tiles[plan.sums[1] - 1 - tile];
   const int up = (t.count + ALIGN - 1) / ALIGN * ALIGN;
   if (threadIdx.x < TILE) rows[threadIdx.x] = threadIdx.x < up ? plan.rows[t.start + threadIdx.x] : -1;
   if (t.adapter < 0) {  // rows without an adapter
@@ -656,8 +666,13 @@ __global__ void __launch_bounds__(WGRAD_THREADS) k_wgrad(const __grid_constant__
         if (first >= 0) {
           if (elect_one()) {
             mbar_arrive_expect_tx(&full[st], SLAB * 128 * (two ? 2 : 1) + extra);
-            tma_2d(dst, &mx, &full[st], c0, first);
-            if (two) tma_2d(dst + TILE * 128, &mx, &full[st], c0 + 64, first);
+            if (second) {
+              tma_2d(dst, &mx, &full[st], c0, first);
+              if (two) tma_2d(dst + TILE * 128, &mx, &full[st], c0 + 64, first);
+            } else {  // (x makes room for dy, which is in L2 in part)
+              tma_2d_once(dst, &mx, &full[st], c0, first);
+              if (two) tma_2d_once(dst + TILE * 128, &mx, &full[st], c0 + 64, first);
+            }
           }
         } else if (extra) {
           if (elect_one()) mbar_expect_tx(&full[st], extra);
@@ -1335,8 +1350,7 @@ moe_status_t wgrad(const moe_bf16* x, const moe_bf16* us, int K, moe_bf16* dA, c
   if (!fill(sides.of[0], x, us, K, dA) || !fill(sides.of[1], dy, hs, N, dB)) return MOE_ERR_CUDA;
   const int units = sides.of[0].units + sides.of[1].units;
   const int split = split_of(bytes + 10 * 1024, units, max_tiles(T, G));
-  // (not a programmatic dependent: its first clusters took places as the kernel before it left them, unevenly, and
-  // the backward of 8192 x 7168 took 154 us instead of 136)
+  // (not a programmatic dependent: its first clusters took places as the kernel before it left them, unevenly)
   return launch(k_wgrad, units * split, split, WGRAD_THREADS, bytes, wgrad_bytes(MAX_R), false, s, sides, r, rp, G, p,
                 g_wait_limit_ns.load(), st);
 }
@@ -1449,6 +1463,8 @@ extern "C" moe_status_t moe_lora_bwd(const moe_bf16* dy, const moe_bf16* x, cons
   auto* hs = us + sorted_bytes(T, r, G) / 2;
   if (const moe_status_t e = group(idx, T, G, p, s)) return e;
   if (const moe_status_t e = shrink(dy, B, scale, T, N, r, G, p, nullptr, us, h, hs, status, s)) return e;
-  if (const moe_status_t e = expand(us, A, base, T, K, r, G, p, dx, status, s)) return e;
-  return wgrad(x, us, K, dA, dy, hs, N, dB, T, r, G, p, status, s);
+  // (the gradients next, while part of dy is in L2; k_expand, whose jobs any CTA takes, then fills the SMs that they leave:
+  // 8192 x 7168 with rank 32 126 us; dx before them 129)
+  if (const moe_status_t e = wgrad(x, us, K, dA, dy, hs, N, dB, T, r, G, p, status, s)) return e;
+  return expand(us, A, base, T, K, r, G, p, dx, status, s);
 }
