@@ -519,17 +519,21 @@ __global__ void __launch_bounds__(SHRINK_THREADS) k_shrink(const __grid_constant
 // k_wgrad: cluster (128 columns of x or dy, X [T][C]), its CTAs share the tiles of all
 // adapters: dP [G][r][C] = U^T X over each adapter's rows, U in the grouped
 // order.  An adapter's tiles that cross from one CTA's share into the next
-// ones' are summed by the whole cluster in the end.
+// ones' are summed by the whole cluster in the end.  A step of the ring is one
+// tile, or neighbouring small ones together (they lie side by side in the
+// grouped order), whose rows are under way at once.
 // Warps 0 to 3 load 32 rows each, 4 issues the MMAs, 5 to 8 write out; two
 // accumulators.
 // ---------------------------------------------------------------------------
-constexpr int WGRAD_THREADS = 288, BATCH = 16;  // tiles whose rows are looked up together
+constexpr int WGRAD_THREADS = 288, BATCH = 32, STEPS = 16;  // tiles looked up together, in so many steps
+constexpr int SMALL = 64;  // places: tiles of at most so many that begin in the same SMALL places share a step
 __host__ __device__ constexpr int wgrad_stages(int rp) { return rp <= 32 ? 2 : rp <= 64 ? 3 : 2; }
 __host__ __device__ constexpr int wgrad_stage(int rp) { return TILE * 256 + TILE * rank_bytes(rp); }
 constexpr int wgrad_bytes(int rp) { return wgrad_stages(rp) * wgrad_stage(rp) + 512 * rp + 1024; }
 
-// of a step (a tile) in this CTA: the first / last of its run of one adapter; the run began before / goes on behind it
-enum { RUN_BEGINS = 1, RUN_ENDS = 2, FROM_BEFORE = 4, GOES_ON = 8 };
+// of a tile in this CTA: the first / last of its run of one adapter; the run began before / goes on behind it; the first /
+// last of its step
+enum { RUN_BEGINS = 1, RUN_ENDS = 2, FROM_BEFORE = 4, GOES_ON = 8, STEP_BEGINS = 16, STEP_ENDS = 32 };
 
 // One of the two gradients, which share a launch: dA (x and u) and dB (dy and h).
 struct Side {
@@ -549,8 +553,9 @@ __global__ void __launch_bounds__(WGRAD_THREADS) k_wgrad(const __grid_constant__
   __shared__ uint64_t full[3], empty[3], acc_full[2], acc_empty[2], done;
   __shared__ int abort_, never, head_through, tail_adapter;
   __shared__ uint32_t tmem_;
-  __shared__ int4 steps[BATCH];                        // first place, rows, adapter, flags
-  __shared__ int row_of[BATCH][TILE], box_of[BATCH][4];  // rows of each step; the first one of 32 neighbours, or -1
+  __shared__ int4 part[BATCH];                           // of each tile: first place, places, adapter, flags
+  __shared__ int2 step_of[STEPS];                        // first place, places
+  __shared__ int row_of[STEPS][TILE], box_of[STEPS][4];  // rows of each step; the first one of 32 neighbours, or -1
   const uint32_t size = cluster_size(), rank = cluster_ctarank();
   const int unit = (int)(blockIdx.x / size), second = unit >= sides.of[0].units ? 1 : 0;
   const Side& side = sides.of[second];
@@ -599,37 +604,62 @@ __global__ void __launch_bounds__(WGRAD_THREADS) k_wgrad(const __grid_constant__
     if (++st == stages) st = 0, ++turn;
   };
   bool before = false, alive = true;
-  for (int b0 = lo; b0 < hi; b0 += BATCH) {
-    const int m = min(BATCH, hi - b0);
+  for (int b0 = lo, m = 0; b0 < hi; b0 += m) {
     if (b0 > lo) __syncthreads();
+    int steps;
     {
-      constexpr int WARPS = WGRAD_THREADS / 32, MORE = (BATCH + WARPS - 1) / WARPS;
-      int4 s[MORE];
-      int row[MORE][4];
+      const int ti = b0 + lane;
+      Tile t{-1, 0, 0, 0};
+      if (ti < tiles) t = plan.tiles[ti];
+      int before_it = __shfl_up_sync(0xFFFFFFFFu, t.adapter, 1), behind_it = __shfl_down_sync(0xFFFFFFFFu, t.adapter, 1);
+      if (lane == 0) before_it = ti > 0 ? plan.tiles[ti - 1].adapter : -1;
+      if (lane == 31) behind_it = ti + 1 < tiles ? plan.tiles[ti + 1].adapter : -1;
+      const int up = (t.count + ALIGN - 1) / ALIGN * ALIGN;
+      // (tiles that share a step have the same number here: together they end before TILE places from the step's first)
+      const int with = up <= SMALL ? t.start / SMALL : -1, with_last = __shfl_up_sync(0xFFFFFFFFu, with, 1);
+      const bool opens = lane == 0 || with < 0 || with != with_last;
+      uint32_t first = __ballot_sync(0xFFFFFFFFu, ti < hi && opens);
+      m = min(BATCH, hi - b0);
+      steps = __popc(first);
+      if (steps > STEPS) {  // the tiles before the step behind the last
+        uint32_t more = first;
+#pragma unroll
+        for (int k = 0; k < STEPS; ++k) more &= more - 1;
+        m = __ffs(more) - 1;
+        first ^= more;
+        steps = STEPS;
+      }
+      if (warp == 0 && lane < m) {
+        const bool begins = before_it != t.adapter, ends = behind_it != t.adapter;
+        const uint32_t behind = first >> lane >> 1;
+        part[lane] = make_int4(t.start, up, t.adapter,
+                               (begins || ti == lo ? RUN_BEGINS : 0) | (ends || ti + 1 == hi ? RUN_ENDS : 0) |
+                                   (!begins && ti == lo ? FROM_BEFORE : 0) | (!ends && ti + 1 == hi ? GOES_ON : 0) |
+                                   (opens ? STEP_BEGINS : 0) | (lane + 1 == m || (behind & 1) ? STEP_ENDS : 0));
+      }
+      constexpr int WARPS = WGRAD_THREADS / 32, MORE = (STEPS + WARPS - 1) / WARPS;
+      int from[MORE], n[MORE], row[MORE][4];
 #pragma unroll
       for (int q = 0; q < MORE; ++q) {
-        const int j = warp + q * WARPS, ti = b0 + j;
-        if (j < m) {
-          const Tile t = plan.tiles[ti];
-          const bool begins = ti == 0 || plan.tiles[ti - 1].adapter != t.adapter;
-          const bool ends = ti + 1 == tiles || plan.tiles[ti + 1].adapter != t.adapter;
-          s[q] = make_int4(t.start, t.count, t.adapter,
-                           (begins || ti == lo ? RUN_BEGINS : 0) | (ends || ti + 1 == hi ? RUN_ENDS : 0) |
-                               (!begins && ti == lo ? FROM_BEFORE : 0) | (!ends && ti + 1 == hi ? GOES_ON : 0));
-        }
+        uint32_t rest = first;
+        for (int k = warp + q * WARPS; k > 0; --k) rest &= rest - 1;
+        const int a = rest ? __ffs(rest) - 1 : 0, next = rest & (rest - 1), b = next ? __ffs(next) - 2 : m - 1;
+        from[q] = __shfl_sync(0xFFFFFFFFu, t.start, a);
+        const int end = __shfl_sync(0xFFFFFFFFu, t.start + up, b);
+        n[q] = rest ? end - from[q] : 0;
       }
 #pragma unroll
       for (int q = 0; q < MORE; ++q)
 #pragma unroll
         for (int k = 0; k < 4; ++k) {  // (all loads before the first use)
           const int l = SLAB * k + lane;
-          row[q][k] = warp + q * WARPS < m && l < s[q].y ? plan.rows[s[q].x + l] : -1;
+          row[q][k] = l < n[q] ? plan.rows[from[q] + l] : -1;
         }
 #pragma unroll
       for (int q = 0; q < MORE; ++q) {
         const int j = warp + q * WARPS;
-        if (j >= m) break;
-        if (lane == 0) steps[j] = s[q];
+        if (j >= steps) break;
+        if (lane == 0) step_of[j] = make_int2(from[q], n[q]);
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
           const int first_row = __shfl_sync(0xFFFFFFFFu, row[q][k], 0);
@@ -643,6 +673,10 @@ __global__ void __launch_bounds__(WGRAD_THREADS) k_wgrad(const __grid_constant__
     if (warp < 4) {
       const int c = lane & 7;
       const bool two = c0 + 64 < C;  // (the second block of 64 columns has some)
+      // row by row: the lane's eight columns in either block, and their place in rows 0 to 3 and 4 to 7 of eight
+      const bool left = c0 + c * 8 < C, right = c0 + 64 + c * 8 < C;
+      const __nv_bfloat16* mine = X + (left ? c0 + c * 8 : 0);
+      const uint32_t even = piece(0, lane >> 3, c), odd = piece(0, 4 + (lane >> 3), c) - 512;
       int landing = -1;              // the stage of a step whose rows are still being copied one by one
       auto landed = [&](bool behind) {  // (behind: another step's copies have been issued since)
         if (behind)
@@ -655,10 +689,10 @@ __global__ void __launch_bounds__(WGRAD_THREADS) k_wgrad(const __grid_constant__
         __syncwarp();
         landing = -1;
       };
-      int start = uniform(steps[0].x), count = uniform(steps[0].y), box = uniform(box_of[0][warp]);
-      for (int j = 0; j < m; ++j) {
+      int start = uniform(step_of[0].x), count = uniform(step_of[0].y), box = uniform(box_of[0][warp]);
+      for (int j = 0; j < steps; ++j) {
         const int from = start, now = count, first = box;
-        if (j + 1 < m) start = uniform(steps[j + 1].x), count = uniform(steps[j + 1].y), box = uniform(box_of[j + 1][warp]);
+        if (j + 1 < steps) start = uniform(step_of[j + 1].x), count = uniform(step_of[j + 1].y), box = uniform(box_of[j + 1][warp]);
         const uint32_t at = ring + st * stage, dst = at + warp * (SLAB * 128);
         if (turn > 0) alive = alive && warp_wait(&empty[st], (turn - 1) & 1, g);
         if (!alive) break;
@@ -686,14 +720,18 @@ __global__ void __launch_bounds__(WGRAD_THREADS) k_wgrad(const __grid_constant__
         __syncwarp();
         if (first < 0) {
           // row by row, with zeros where there is no row (columns past the last are products that nobody reads)
-          const int up = (now + ALIGN - 1) / ALIGN * ALIGN - SLAB * warp;  // rows of the slab that the MMAs read
-          for (int k = 0; k < 2; ++k)
+          const int up = now - SLAB * warp;  // rows of the slab that the MMAs read (a multiple of 16)
+          int id[8];
 #pragma unroll
-            for (int q = 0; q < 8; ++q) {
-              const int l = (lane >> 3) + 4 * q, id = row_of[j][SLAB * warp + l], col = c0 + 64 * k + c * 8;
-              const bool in = id >= 0 && col < C;
-              if (l < up) cp16(piece(dst + k * (TILE * 128), l, c), in ? X + (size_t)id * C + col : X, in);
-            }
+          for (int q = 0; q < 8; ++q) id[q] = row_of[j][SLAB * warp + 4 * q + (lane >> 3)];
+#pragma unroll
+          for (int q = 0; q < 8; ++q) {
+            if (4 * q >= up) break;
+            const __nv_bfloat16* src = mine + (size_t)max(id[q], 0) * C;
+            const uint32_t to = dst + (q & 1 ? odd : even) + 512 * q;
+            cp16(to, src, id[q] >= 0 && left);
+            cp16(to + TILE * 128, right ? src + 64 : src, id[q] >= 0 && right);
+          }
           cp_commit();
         }
         if (landing >= 0) landed(first < 0);
@@ -703,31 +741,36 @@ __global__ void __launch_bounds__(WGRAD_THREADS) k_wgrad(const __grid_constant__
       if (landing >= 0) landed(false);
     } else if (warp == 4) {
       const uint32_t urow = rp > 64 ? 128 : rank_bytes(rp), idesc = idesc_bf16_f32(TILE, rp) | A_MN | B_MN;
+      int from = 0;
       for (int j = 0; j < m; ++j) {
-        const int count = uniform(steps[j].y), flags = uniform(steps[j].w), acc = run & 1;
-        alive = alive && warp_wait(&full[st], turn & 1, g);
+        const int start = uniform(part[j].x), up = uniform(part[j].y), flags = uniform(part[j].w), acc = run & 1;
+        if (flags & STEP_BEGINS) {
+          from = start;
+          alive = alive && warp_wait(&full[st], turn & 1, g);
+        }
         if (alive && (flags & RUN_BEGINS) && run >= 2) alive = warp_wait(&acc_empty[acc], (run / 2 - 1) & 1, g);
         if (!alive) break;
         tc_fence_after();
-        const uint64_t x = sdesc_mnmajor(ring + st * stage, 128, TILE * 128);
-        const uint64_t u = sdesc_mnmajor(ring + st * stage + TILE * 256, urow, TILE * 128);
+        const uint32_t k0 = (start - from) / ALIGN;
+        const uint64_t x = sdesc_mnmajor(ring + st * stage, 128, TILE * 128) + (2048 >> 4) * k0;
+        const uint64_t u = sdesc_mnmajor(ring + st * stage + TILE * 256, urow, TILE * 128) + urow * k0;
         const uint32_t keep = (flags & RUN_BEGINS) ? 0u : 1u;
         if (elect_one()) {
 #pragma unroll
           for (int k = 0; k < TILE / ALIGN; ++k)
-            if (k * ALIGN < count)
+            if (k * ALIGN < up)
               umma_bf16(tmem + acc * acc_cols, x + (2048 >> 4) * k, u + urow * k, idesc, k > 0 ? 1u : keep);
-          tc_commit(&empty[st]);
+          if (flags & STEP_ENDS) tc_commit(&empty[st]);
           if (flags & RUN_ENDS) tc_commit(&acc_full[acc]);
         }
         __syncwarp();
         if (flags & RUN_ENDS) ++run;
-        next_stage();
+        if (flags & STEP_ENDS) next_stage();
       }
     } else {
       const int quad = warp & 3, l = 32 * quad + lane;  // (a warp reads the tensor-memory lanes of its number modulo 4)
       for (int j = 0; j < m && alive; ++j) {
-        const int adapter = steps[j].z, flags = steps[j].w;
+        const int adapter = part[j].z, flags = part[j].w;
         if (flags & RUN_BEGINS) before = (flags & FROM_BEFORE) != 0;
         if (!(flags & RUN_ENDS)) continue;
         const int acc = run & 1;
@@ -750,8 +793,11 @@ __global__ void __launch_bounds__(WGRAD_THREADS) k_wgrad(const __grid_constant__
           } else if (c0 + l < C) {
             __nv_bfloat16* out = dP + ((size_t)adapter * r + cc) * C + c0 + l;
 #pragma unroll
-            for (int k = 0; k < 32; ++k)
-              if (cc + k < r) out[(size_t)k * C] = __float2bfloat16_rn(v[k]);
+            for (int k = 0; k < 32; k += 8)
+              if (cc + k < r) {
+#pragma unroll
+                for (int q = 0; q < 8; ++q, out += C) *out = __float2bfloat16_rn(v[k + q]);
+              }
           }
         }
         if (l == 0) {
