@@ -883,6 +883,11 @@ __global__ void __launch_bounds__(WGRAD_THREADS) k_wgrad(const __grid_constant__
 // Warps 0 to 3 load 32 rows each, warp 4 issues the MMAs, all eight add and
 // store 32 rows x 64 columns each.
 // ---------------------------------------------------------------------------
+// two bf16 values and two fp32 ones, added and rounded
+__device__ __forceinline__ uint32_t plus(uint32_t b, float x, float y) {
+  const float2 s = __fadd2_rn(make_float2(bf16_lo(b), bf16_hi(b)), make_float2(x, y));
+  return pack_bf16x2(s.x, s.y);
+}
 constexpr int EXPAND_THREADS = 256;
 // Units in a job: two share the tile's h and its rows' numbers; 8192 x 7168 with rank 16, forward, 73.1 us, one by one
 // 73.8, threes 74.5; 512 rows of 64 adapters 42.5, 46.4, 43.4.  Ones while every unit has a CTA of its own (300 x 512:
@@ -907,7 +912,7 @@ __global__ void __launch_bounds__(EXPAND_THREADS, 3) k_expand(const __grid_const
   extern __shared__ unsigned char smem_[];
   unsigned char* smem = aligned_smem(smem_);
   __shared__ uint64_t rows_in[2], product_in, product_out;  // base's rows, h and Q in shared memory; the MMAs' end
-  __shared__ int abort_, never, taken[2];  // (the jobs behind this one, by turns)
+  __shared__ int abort_, never, taken[2];  // (the numbers of the jobs behind the next one, by turns)
   __shared__ uint32_t tmem_;
   const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31, slab = warp & 3, block = warp >> 2;
   const int ahead = expand_ahead(rp);
@@ -929,7 +934,7 @@ __global__ void __launch_bounds__(EXPAND_THREADS, 3) k_expand(const __grid_const
   const int chunks = (N + TILE - 1) / TILE, per_tile = (chunks + job - 1) / job;
   const int64_t jobs = (int64_t)plan.sums[1] * per_tile;  // in the order (tile, columns); the first are the CTAs' numbers
   auto take = [&] { return (int)gridDim.x + atomicAdd(plan.sums + 2, 1); };
-  if (threadIdx.x == 0) taken[0] = take();
+  if (threadIdx.x == 0) taken[1] = take();
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -937,26 +942,32 @@ __global__ void __launch_bounds__(EXPAND_THREADS, 3) k_expand(const __grid_const
   const uint32_t tmem = uniform(tmem_);
   const uint32_t idesc = idesc_bf16_f32(TILE, TILE) | B_MN, hrow = rp > 64 ? 128 : rank_bytes(rp);
 
-  // a job: its tile's adapter and place, its chunks, and the warp's slab of the tile
+  // a job: its tile's adapter and place, its chunks (end 0: none), and the warp's slab of the tile
   struct Part {
     int adapter, start, chunk, end;
     Slab s;
   };
-  auto part_of = [&](int number) {
-    Part p{-1, 0, 0, 0, {}};
-    int row = -1;
-    number = uniform(number);
+  // found in three steps, each with the loads of the one before
+  struct Find {
+    Tile t;
+    int chunk, row;
+  };
+  auto find_tile = [&](Find& f, int number) {
+    f.t = Tile{-1, 0, 0, 0};
+    f.chunk = -1;
     if (number < jobs) {
       const int tile = number / per_tile;
-      const Tile t = plan.tiles[tile];
-      p.adapter = uniform(t.adapter);
-      p.start = uniform(t.start);
-      p.chunk = (number - tile * per_tile) * job;
-      p.end = min(p.chunk + job, chunks);
-      const int place = SLAB * slab + lane;
-      if (place < t.count) row = plan.rows[t.start + place];
+      f.t = plan.tiles[tile];
+      f.chunk = (number - tile * per_tile) * job;
     }
-    p.s = slab_of(row);
+  };
+  auto find_row = [&](Find& f) {
+    const int place = SLAB * slab + lane;
+    f.row = place < f.t.count ? plan.rows[f.t.start + place] : -1;
+  };
+  auto part_of = [&](const Find& f) {
+    Part p{uniform(f.t.adapter), uniform(f.t.start), uniform(f.chunk), 0, slab_of(f.row)};
+    if (p.chunk >= 0) p.end = min(p.chunk + job, chunks);
     p.s.first = uniform(p.s.first);
     p.s.count = uniform(p.s.count);
     return p;
@@ -1003,7 +1014,7 @@ __global__ void __launch_bounds__(EXPAND_THREADS, 3) k_expand(const __grid_const
     }
     __syncwarp();
   };
-  auto load_product = [&](const Part& p, int chunk, bool fresh) {  // warp 0
+  auto load_product = [&](const Part& p, int chunk, bool fresh) {  // warp 6, which loads no rows
     if (!elect_one()) return;
     const int c0 = chunk * TILE;
     const bool two = c0 + 64 < N;  // (the second block of 64 columns has some)
@@ -1016,20 +1027,27 @@ __global__ void __launch_bounds__(EXPAND_THREADS, 3) k_expand(const __grid_const
     if (two) tma_3d(q_at + rp * 128, &mq, &product_in, c0 + 64, 0, p.adapter);
   };
 
-  Part now = part_of(blockIdx.x), next = part_of(taken[0]);
+  Find found, behind;
+  find_tile(behind, blockIdx.x);
+  find_tile(found, taken[1]);
+  find_row(behind);
+  find_row(found);
+  Part now = part_of(behind), next = part_of(found);
   int chunk = now.chunk, done = 0;  // jobs done
   bool more = now.end > 0;
   int turn[2] = {0, 0}, products = 0, buf = 0;
   if (more) {
     if (warp < 4) load_rows(now, chunk, 0);
-    if (warp == 0 && now.adapter >= 0) load_product(now, chunk, true);
+    if (warp == 6 && now.adapter >= 0) load_product(now, chunk, true);
     __syncwarp();
   }
   while (more) {
     const bool last = chunk + 1 == now.end;  // of this job
     const bool product = now.adapter >= 0, another = !last || next.end > 0;
     const int c0 = chunk * TILE, next_chunk = last ? next.chunk : chunk + 1;
-    if (threadIdx.x == 0 && chunk == now.chunk && next.end > 0) taken[(done + 1) & 1] = take();
+    const bool first = chunk == now.chunk;
+    if (warp == 7 && lane == 0 && first && next.end > 0) taken[done & 1] = take();
+    if (last && !first) find_tile(found, next.end > 0 ? taken[done & 1] : 0x7FFFFFFF);
     if (ahead && another && warp < 4) load_rows(last ? next : now, next_chunk, buf ^ 1);
     bool ok = true;
     if (product) {
@@ -1051,8 +1069,9 @@ __global__ void __launch_bounds__(EXPAND_THREADS, 3) k_expand(const __grid_const
     }
     // (h and Q have been read: the next unit's may come)
     ok = __all_sync(0xFFFFFFFFu, ok);
-    if (warp == 0 && ok && another && (last ? next : now).adapter >= 0) load_product(last ? next : now, next_chunk, last);
+    if (warp == 6 && ok && another && (last ? next : now).adapter >= 0) load_product(last ? next : now, next_chunk, last);
     __syncwarp();
+    if (last && !first) find_row(found);
     ok &= wait_on(&rows_in[buf], turn[buf] & 1, g);
     ++turn[buf];
     tc_fence_after();
@@ -1062,7 +1081,11 @@ __global__ void __launch_bounds__(EXPAND_THREADS, 3) k_expand(const __grid_const
     if (__all_sync(0xFFFFFFFFu, ok) && s.count > 0 && col < N) {
 #pragma unroll
       for (int half = 0; half < 2; ++half) {
+        uint4 o[4];
         float v[32];
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          o[k] = base ? *reinterpret_cast<const uint4*>(smem + (piece(mine, lane, 4 * half + k) - at)) : make_uint4(0, 0, 0, 0);
         if (product) {
           tmem_ld32(tmem + ((uint32_t)(32 * slab) << 16) + 64 * block + 32 * half, v);
         } else {
@@ -1071,14 +1094,9 @@ __global__ void __launch_bounds__(EXPAND_THREADS, 3) k_expand(const __grid_const
         }
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-          uint4* p = reinterpret_cast<uint4*>(smem + (piece(mine, lane, 4 * half + k) - at));
-          uint4 o = base ? *p : make_uint4(0, 0, 0, 0);
           const float* a = v + 8 * k;
-          o.x = pack_bf16x2(bf16_lo(o.x) + a[0], bf16_hi(o.x) + a[1]);
-          o.y = pack_bf16x2(bf16_lo(o.y) + a[2], bf16_hi(o.y) + a[3]);
-          o.z = pack_bf16x2(bf16_lo(o.z) + a[4], bf16_hi(o.z) + a[5]);
-          o.w = pack_bf16x2(bf16_lo(o.w) + a[6], bf16_hi(o.w) + a[7]);
-          *p = o;
+          o[k] = make_uint4(plus(o[k].x, a[0], a[1]), plus(o[k].y, a[2], a[3]), plus(o[k].z, a[4], a[5]), plus(o[k].w, a[6], a[7]));
+          *reinterpret_cast<uint4*>(smem + (piece(mine, lane, 4 * half + k) - at)) = o[k];
         }
       }
       fence_async_shared();
@@ -1110,9 +1128,13 @@ __global__ void __launch_bounds__(EXPAND_THREADS, 3) k_expand(const __grid_const
     if (!ok) break;
     chunk = next_chunk;
     if (last) {
+      if (first) {
+        find_tile(found, next.end > 0 ? taken[done & 1] : 0x7FFFFFFF);
+        find_row(found);
+      }
       now = next;
+      next = part_of(found);
       ++done;
-      next = now.end > 0 ? part_of(taken[done & 1]) : Part{-1, 0, 0, 0, {}};
     }
     more = another;
     if (!ahead && another && warp < 4) load_rows(now, chunk, 0);
