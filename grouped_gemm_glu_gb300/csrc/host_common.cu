@@ -82,20 +82,25 @@ bool set_smem_limit(const void* kernel, int bytes) {
   return true;
 }
 
-bool prefer_shared(const void* kernel) {
+// Sets an attribute of a kernel, once per kernel and device.
+static bool set_once(const void* kernel, cudaFuncAttribute attr, int value) {
   static std::mutex mu;
-  static std::set<std::pair<const void*, int>> done;
+  static std::set<std::tuple<const void*, int, int>> done;
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return false;
-  const auto key = std::make_pair(kernel, dev);
+  const auto key = std::make_tuple(kernel, (int)attr, dev);
   std::lock_guard<std::mutex> lock(mu);
   if (done.count(key)) return true;
-  if (cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared) !=
-      cudaSuccess)
-    return false;
+  if (cudaFuncSetAttribute(kernel, attr, value) != cudaSuccess) return false;
   done.insert(key);
   return true;
 }
+
+bool prefer_shared(const void* kernel) {
+  return set_once(kernel, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
+}
+
+bool allow_large_clusters(const void* kernel) { return set_once(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1); }
 
 static PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
   static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;

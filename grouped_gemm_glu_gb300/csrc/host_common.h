@@ -43,6 +43,9 @@ bool set_smem_limit(const void* kernel, int bytes);
 // for one; once per kernel and device; false on failure).
 bool prefer_shared(const void* kernel);
 
+// Allows clusters of up to 16 CTAs (8 by default; as above).
+bool allow_large_clusters(const void* kernel);
+
 // Encodes a tiled TMA descriptor for a row-major tensor with dims[0] the
 // contiguous dimension.  rank 2 or 3; strides_bytes has rank-1 entries.
 bool encode_tmap(CUtensorMap* map, CUtensorMapDataType dtype, int rank, const void* base,

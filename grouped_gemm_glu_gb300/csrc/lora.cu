@@ -32,7 +32,7 @@
 // k_shrink 24, 117 MB at 4.9 TB/s, where a kernel that only loads them takes 21;
 // k_expand 43, 235 MB at 5.5 TB/s, where a plain copy takes 38 to 40); with 8 of
 // rank 32, backward 126 us (k_wgrad 50 for both gradients, 4.7 TB/s); one row
-// of 2880 5.1 us, 64 rows of 7168 with 64 adapters 8.2 us.
+// of 2880 4 us, 64 rows of 7168 with 64 adapters 8.2 us.
 #include "common.cuh"
 #include "host_common.h"
 
@@ -1158,7 +1158,7 @@ __global__ void __launch_bounds__(EXPAND_THREADS, 3) k_expand(const __grid_const
 // ---------------------------------------------------------------------------
 // k_rows: few rows, one cluster per row, on the CUDA cores
 // ---------------------------------------------------------------------------
-constexpr int ROW_CTAS = 8, ROW_THREADS = 256, ROW_COLS = ROW_THREADS / 2;
+constexpr int ROW_THREADS = 256, ROW_COLS = ROW_THREADS / 2;
 
 __device__ __forceinline__ float dot8(uint4 a, uint4 b, float s) {
   const uint32_t x[4] = {a.x, a.y, a.z, a.w}, y[4] = {b.x, b.y, b.z, b.w};
@@ -1178,27 +1178,26 @@ __device__ __forceinline__ void add8(float* s, float f, uint4 q) {
   }
 }
 
-// Every CTA of a row's cluster takes an eighth of K for h and an eighth of the
-// columns for y.  A warp computes JB elements of h at a time; for y one half of
-// the threads takes the first half of the rank, the other the second, each with
-// the first AHEAD rows of Q loaded before h is known.  OCC CTAs per SM: while
-// all rows' CTAs are resident at four per SM, loads ahead shorten the chain (one
-// row of 2880 5.1 us against 5.7, 16 of 7168 6.2 against 6.6); with more rows
-// eight per SM with fewer registers are faster (128 of 7168 12.9 against 15.2).
-template <int AHEAD, int JB, int OCC>
+// Every CTA of a row's cluster takes its share of K for h and of the columns
+// for y.  A warp computes JB elements of h at a time; for y one half of the
+// threads takes the first half of the rank, the other the second, each with the
+// first AHEAD rows of Q loaded before h is known.  OCC CTAs per SM.  What bounds
+// it are the loads that few CTAs have under way, so the fewer rows, the more
+// CTAs per row and loads per thread (rows_kernel).
+template <int CTAS, int AHEAD, int JB, int OCC>
 __global__ void __launch_bounds__(ROW_THREADS, OCC) k_rows(const __nv_bfloat16* __restrict__ X, const __nv_bfloat16* __restrict__ P,
                                                       const __nv_bfloat16* __restrict__ Q, const int32_t* __restrict__ idx,
                                                       const float* __restrict__ scale, const __nv_bfloat16* base, int K,
                                                       int N, int r, int G, __nv_bfloat16* y, __nv_bfloat16* __restrict__ h) {
-  __shared__ float sums[ROW_CTAS][MAX_R];  // every CTA's sums over its part of K, from all of them
+  __shared__ float sums[CTAS][MAX_R];  // every CTA's sums over its part of K, from all of them
   __shared__ float hid[MAX_R];
   __shared__ float4 other[2][ROW_COLS];
-  const int row = blockIdx.x / ROW_CTAS, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int row = blockIdx.x / CTAS, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_ctarank();
   const int a = idx[row];
   const bool has = (unsigned)a < (unsigned)G;  // (of the whole cluster)
-  const int K8 = K / 8, k0 = (int)((int64_t)K8 * rank / ROW_CTAS), k1 = (int)((int64_t)K8 * (rank + 1) / ROW_CTAS);
-  const int N8 = N / 8, n0 = (int)((int64_t)N8 * rank / ROW_CTAS), n1 = (int)((int64_t)N8 * (rank + 1) / ROW_CTAS);
+  const int K8 = K / 8, k0 = (int)((int64_t)K8 * rank / CTAS), k1 = (int)((int64_t)K8 * (rank + 1) / CTAS);
+  const int N8 = N / 8, n0 = (int)((int64_t)N8 * rank / CTAS), n1 = (int)((int64_t)N8 * (rank + 1) / CTAS);
   const int half = threadIdx.x / ROW_COLS, t = threadIdx.x % ROW_COLS;
   const int j0 = half ? r / 2 : 0, j1 = half ? r : r / 2;
   const uint4* q = reinterpret_cast<const uint4*>(Q + (has ? (size_t)a * r * N : 0));
@@ -1235,7 +1234,7 @@ __global__ void __launch_bounds__(ROW_THREADS, OCC) k_rows(const __nv_bfloat16* 
       begun = true;
 #pragma unroll
       for (int i = 0; i < JB; ++i)
-        if (lane < ROW_CTAS && jb + i * WARPS < r)
+        if (lane < CTAS && jb + i * WARPS < r)
           asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(mapa_shared(smem_u32(&sums[rank][jb + i * WARPS]), lane)),
                        "f"(s[i])
                        : "memory");
@@ -1245,7 +1244,7 @@ __global__ void __launch_bounds__(ROW_THREADS, OCC) k_rows(const __nv_bfloat16* 
     if (threadIdx.x < r) {
       float s = 0.0f;
 #pragma unroll
-      for (int c = 0; c < ROW_CTAS; ++c) s += sums[c][threadIdx.x];
+      for (int c = 0; c < CTAS; ++c) s += sums[c][threadIdx.x];
       const __nv_bfloat16 v = __float2bfloat16_rn(s * scale[a]);
       hid[threadIdx.x] = __bfloat162float(v);
       if (h && rank == 0) h[(size_t)row * r + threadIdx.x] = v;
@@ -1303,6 +1302,23 @@ __global__ void __launch_bounds__(ROW_THREADS, OCC) k_rows(const __nv_bfloat16* 
 constexpr int MOST_ROWS = 256, FEW_ROWS = 4096;
 bool few_rows(int T, int r) { return T <= MOST_ROWS && (int64_t)T * r <= FEW_ROWS; }
 
+// k_rows for T rows of rank r, 7168 x 7168, us by CTAs per row, AHEAD, JB, OCC:
+//   rows, rank     1, 16   1, 64   1, 128   8, 64   16, 16   16, 64   32, 64   64, 16   128, 16
+//   16, 8, 2, 2    4.5     8.7     14.8     10.0    8.4      18.6     27.8     20.5     -
+//   16, 4, 4, 2    5.1     8.0     12.5     9.9     10.0     17.2     27.1     23.9     -
+//   8, 8, 4, 2     5.8     11.1    19.6     11.1    6.4      12.9     13.3     11.6     -
+//   8, 4, 2, 4     5.9     13.3    24.2     13.5    6.4      15.0     15.0     8.2      15.2
+//   8, 1, 1, 8     6.6     14.0    24.2     -       7.2      15.6     15.9     8.8      12.9
+// A GPC holds one cluster of 16 with another's CTAs beside it; clusters of 8 leave some SMs with less than two CTAs
+// (38 rows of rank 64: 8, 8, 4, 2 takes 22.9, 8, 4, 2, 4 17.2).  A rank of 16 has two elements of h per warp.
+decltype(&k_rows<8, 1, 1, 8>) rows_kernel(int T, int r, int& ctas) {
+  const int sms = sm_count();
+  ctas = T * 16 <= sms ? 16 : 8;
+  if (ctas == 16) return r <= 16 ? k_rows<16, 8, 2, 2> : k_rows<16, 4, 4, 2>;
+  if (T * 9 <= 2 * sms) return k_rows<8, 8, 4, 2>;
+  return T * 8 <= 4 * sms ? k_rows<8, 4, 2, 4> : k_rows<8, 1, 1, 8>;
+}
+
 size_t up256(size_t n) { return (n + 255) & ~(size_t)255; }
 int used_groups(int T, int G) { return G + 1 < T ? G + 1 : T; }             // at most, the rows without one among them
 int max_tiles(int T, int G) { return T / TILE + used_groups(T, G); }
@@ -1331,6 +1347,7 @@ moe_status_t launch(void (*k)(A...), int ctas, int cluster, int threads, int sme
                     cudaStream_t stream, const B&... args) {
   // (one limit per kernel)
   if (smem_limit && (!set_smem_limit((const void*)k, smem_limit) || !prefer_shared((const void*)k))) return MOE_ERR_CUDA;
+  if (cluster > 8 && !allow_large_clusters((const void*)k)) return MOE_ERR_CUDA;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(ctas);
   cfg.blockDim = dim3(threads);
@@ -1489,8 +1506,9 @@ extern "C" moe_status_t moe_lora_fwd(const moe_bf16* x, const moe_bf16* A, const
     return MOE_ERR_ARG;
   const cudaStream_t s = as_stream(stream);
   if (few_rows(T, r)) {
-    const auto k = T * ROW_CTAS <= 4 * sm_count() ? k_rows<4, 2, 4> : k_rows<1, 1, 8>;
-    return launch(k, T * ROW_CTAS, ROW_CTAS, ROW_THREADS, 0, 0, false, s, in(x), in(A), in(B), idx, scale, in(base), K, N, r, G,
+    int ctas;
+    const auto k = rows_kernel(T, r, ctas);
+    return launch(k, T * ctas, ctas, ROW_THREADS, 0, 0, false, s, in(x), in(A), in(B), idx, scale, in(base), K, N, r, G,
                   out(y), out(h));
   }
   const Plan p = plan_at(ws, T, G);

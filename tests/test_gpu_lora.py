@@ -297,7 +297,8 @@ def test_offsets_past_32_bits():
     torch.cuda.empty_cache()
 
 
-@pytest.mark.parametrize("T,r", [(76, 16), (77, 16), (256, 16), (257, 16), (128, 32), (129, 32), (256, 8)])
+@pytest.mark.parametrize("T,r", [(76, 16), (77, 16), (256, 16), (257, 16), (128, 32), (129, 32), (256, 8), (3, 128), (8, 8),
+                                 (9, 16), (9, 24), (10, 72), (32, 128), (33, 64), (34, 40)])
 def test_around_the_few_rows_rule(T, r):
     c = Case(T, 136, 264, r, 5, "rows", seed=T)
     _backward(c, _forward(c)["h"])
