@@ -31,7 +31,7 @@
 // Measured: 8192 x 7168 with 32 adapters of rank 16, forward 73 us (grouping 6;
 // k_shrink 24, 117 MB at 4.9 TB/s, where a kernel that only loads them takes 21;
 // k_expand 43, 235 MB at 5.5 TB/s, where a plain copy takes 38 to 40); with 8 of
-// rank 32, backward 126 us (k_wgrad 50 for both gradients, 4.7 TB/s); one row
+// rank 32, backward 122 us (k_wgrad 48 for both gradients, 4.9 TB/s); one row
 // of 2880 4 us, 64 rows of 7168 with 64 adapters 8.2 us.
 #include "common.cuh"
 #include "host_common.h"
@@ -889,13 +889,13 @@ __device__ __forceinline__ uint32_t plus(uint32_t b, float x, float y) {
   return pack_bf16x2(s.x, s.y);
 }
 constexpr int EXPAND_THREADS = 256;
-// Units in a job: two share the tile's h and its rows' numbers; 8192 x 7168 with rank 16, forward, 73.1 us, one by one
-// 73.8, threes 74.5; 512 rows of 64 adapters 42.5, 46.4, 43.4.  Ones while every unit has a CTA of its own (300 x 512:
-// 12.3 us, twos 14.1).
+// Units in a job: two share the tile's h and its rows' numbers; forward of 8192 x 7168 with rank 16 72.6 us, one by one
+// 73.2, threes 73.5; 4500 x 2880 x 5760 with rank 64 40.1, 40.4, 42.9; 512 rows of 64 adapters 41.3, 44.3, 42.8.  Ones
+// while every unit has a CTA of its own (300 x 512: 13.1 us, twos 14.8).
 constexpr int expand_job(int64_t units, int ctas) { return units > ctas ? 2 : 1; }
 __host__ __device__ constexpr int expand_q(int rp) { return rp * 256; }
-// Units of base loaded ahead: where three CTAs' shared memory has room for it (ranks up to 16: the forward of 8192 x
-// 7168 77 us against 79 without; with rank 32 it would leave room for two: 46.7 us against 45.2, each with fixed shares).
+// Units of base loaded ahead: where three CTAs' shared memory has room for it (ranks up to 16: 8192 x 7168 forward 73.2 us,
+// 74.0 without, backward 120 and 122; with rank 32 it would leave room for two: k_expand alone 46.7 against 45.2).
 __host__ __device__ constexpr int expand_ahead(int rp) { return rp <= 16 ? 1 : 0; }
 constexpr int expand_bytes(int rp) {
   return (1 + expand_ahead(rp)) * TILE * 256 + expand_q(rp) + TILE * rank_bytes(rp) + 1024;
@@ -1296,9 +1296,9 @@ __global__ void __launch_bounds__(ROW_THREADS, OCC) k_rows(const __nv_bfloat16* 
 // Host
 // ---------------------------------------------------------------------------
 // k_rows for calls of at most so many rows, and rows times rank.  It reads an adapter for each row (from L2, mostly),
-// the tiles each adapter once: at 7168 x 7168 and 64 adapters 128 rows of rank 16 take 13 us against 38, 256 rows 23
-// against 42, 64 rows of rank 64 28 against 37, 128 rows 43 against 47; with 4 adapters 256 rows of rank 16 21 against
-// 21; 512 rows of 512 x 512, rank 8, 22 against 16.
+// the tiles each adapter once: at 7168 x 7168 and 64 adapters 128 rows of rank 16 take 13 us against 36, 256 rows 23
+// against 39, 64 rows of rank 64 25 against 36, 128 rows 43 against 42; with few adapters 256 rows of rank 16 21 against
+// 20, one row of rank 128 12.5 against 19, 32 rows of it 30 against 30; 512 rows of 512 x 512, rank 8, 22 against 17.
 constexpr int MOST_ROWS = 256, FEW_ROWS = 4096;
 bool few_rows(int T, int r) { return T <= MOST_ROWS && (int64_t)T * r <= FEW_ROWS; }
 
