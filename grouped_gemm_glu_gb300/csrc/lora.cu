@@ -1411,10 +1411,12 @@ int split_of(int smem, int clusters, int blocks) {
   return s < 1 ? 1 : s > 8 ? 8 : s;
 }
 
+int shrink_split(int T, int K, int r, int G) { return split_of(shrink_bytes(pad16(r)) + 1024, max_tiles(T, G), (K + KB - 1) / KB); }
+
 moe_status_t shrink(const moe_bf16* x, const moe_bf16* P, const float* scale, int T, int K, int r, int G, const Plan& p,
                     moe_bf16* h, moe_bf16* hs, const moe_bf16* other, moe_bf16* others, int32_t* st, cudaStream_t s) {
   const int rp = pad16(r), tiles = max_tiles(T, G), bytes = shrink_bytes(rp);
-  const int split = split_of(bytes + 1024, tiles, (K + KB - 1) / KB);
+  const int split = shrink_split(T, K, r, G);
   CUtensorMap mx, mp;
   if (!map_rows(&mx, x, T, K, 64, SLAB) || !map_weight(&mp, P, G, r, K, rp)) return MOE_ERR_CUDA;
   return launch(k_shrink, tiles * split, split, SHRINK_THREADS, bytes, shrink_bytes(MAX_R), true, s, mx, mp, in(x), scale, K,
@@ -1434,9 +1436,14 @@ moe_status_t wgrad(const moe_bf16* x, const moe_bf16* us, int K, moe_bf16* dA, c
   };
   if (!fill(sides.of[0], x, us, K, dA) || !fill(sides.of[1], dy, hs, N, dB)) return MOE_ERR_CUDA;
   const int units = sides.of[0].units + sides.of[1].units;
-  const int split = split_of(bytes + 10 * 1024, units, max_tiles(T, G));
-  // (not a programmatic dependent: its first clusters took places as the kernel before it left them, unevenly)
-  return launch(k_wgrad, units * split, split, WGRAD_THREADS, bytes, wgrad_bytes(MAX_R), false, s, sides, r, rp, G, p,
+  // (the zeros of adapters without rows, of which there are G - T at least, take about as long as tiles: one row of 51
+  // adapters of rank 128, 2440 to 256, 27 us instead of 51)
+  const int zeros = G > T ? (int)((int64_t)(G - T) * r / MAX_R) : 0;
+  const int split = split_of(bytes + 10 * 1024, units, max_tiles(T, G) + zeros);
+  // A programmatic dependent where both kernels' CTAs find an SM each (300 x 256 x 512 backward 19.8 us, 20.6 without).  With
+  // more, its first clusters took places as k_shrink left them, unevenly (8192 x 7168 154 us, 136 without).
+  const bool dependent = max_tiles(T, G) * shrink_split(T, N, r, G) + units * split <= sm_count();
+  return launch(k_wgrad, units * split, split, WGRAD_THREADS, bytes, wgrad_bytes(MAX_R), dependent, s, sides, r, rp, G, p,
                 g_wait_limit_ns.load(), st);
 }
 
