@@ -332,6 +332,9 @@ struct Bars {
   uint32_t tmem;
 };
 // Columns of tensor memory for an accumulator of rp columns (a power of two, at least 32).
+// What of these kernels finds room on an SM together, by shared memory and
+// registers, asks for at most 448 of its 512 columns: no allocation waits for a
+// CTA of a dependent kernel, which itself waits for the kernel in front.
 __device__ __forceinline__ uint32_t tmem_cols(int rp) { return rp <= 32 ? 32 : rp <= 64 ? 64 : 128; }
 
 __device__ __forceinline__ uint2 pack4(float4 s, float f) {
