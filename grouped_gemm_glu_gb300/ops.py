@@ -855,7 +855,8 @@ def lora(x, A, B, idx, scale, base=None, out=None, with_h: bool = True, status=N
     h = scale[a] (A_a x) and y = base + B_a^T h.  A [G, r, K] and B [G, r, N]
     bf16, scale [G] f32, base [T, N] bf16 the projection's output (None: zero),
     out where y goes (may be base).  Returns y [T, N] and, with_h, h [T, r] bf16,
-    which lora_bwd reads."""
+    which lora_bwd reads.  The same call gives the same bits; a row's last bit may
+    differ with the number of rows beside it (the sums' order follows from T)."""
     T, K, N, r, G = _lora_args(x, A, B, idx, scale, ((base, "N", "base"), (out, "N", "out")))
     bf, dev, lib = torch.bfloat16, x.device, L.load()
     y = out if out is not None else torch.empty(T, N, dtype=bf, device=dev)

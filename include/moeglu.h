@@ -730,7 +730,8 @@ MOE_API size_t moe_lora_bwd_workspace_size(int T, int r, int G);
  * A [G][r][K], B [G][r][N], all bf16; scale [G] f32; base [T][N] bf16 the
  * shared projection's output (NULL: zero; may be y itself); h (nullable) is
  * kept for the backward.  Adapters of different ranks share a call with zero
- * rows up to the largest.  Rows may come in any order of adapters.
+ * rows up to the largest.  Rows may come in any order of adapters.  The same
+ * inputs give the same bits; the order of a row's sums follows from T and r.
  * K, N and r multiples of 8, K and N at most 2^20, r <= 128 and G <= 32767
  * (else MOE_ERR_UNSUPPORTED); bf16 buffers 16-byte, ws
  * (moe_lora_fwd_workspace_size bytes) 256-byte aligned; y and h overlap no input
