@@ -1113,7 +1113,8 @@ __global__ void __launch_bounds__(EXPAND_THREADS, 3) k_expand(const __grid_const
         tma_store_2d(&my8, mine + lane * 128, col, s.row);
         bulk_commit();
       }
-      for (uint32_t m = ~s.whole & 0x01010101u; m; m &= m - 1) {
+      // (eights that have rows and did not go as boxes)
+      for (uint32_t m = ~s.whole & 0x01010101u & (0xFFFFFFFFu >> (32 - s.count)); m; m &= m - 1) {
         const int l0 = __ffs(m) - 1 + (lane >> 3), c = lane & 7;
 #pragma unroll
         for (int l = l0; l < l0 + 8; l += 4) {
