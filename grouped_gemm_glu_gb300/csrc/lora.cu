@@ -321,10 +321,13 @@ __global__ void __launch_bounds__(GROUP_THREADS) k_group(const int32_t* __restri
 // k_shrink: cluster (tile), its CTAs share K.  Warps 0 to 3 load 32 rows each
 // and write out, warp 4 issues the MMAs.
 // ---------------------------------------------------------------------------
-constexpr int SHRINK_THREADS = 160, SHRINK_STAGES = 3;
+constexpr int SHRINK_THREADS = 160;
+// (4500 x 2880 x 5760 with rank 64 38.9 us, with three stages 40.2; 512 rows of 64 adapters 37.7 and 39.6; ranks 16 and 32 at
+// 8192 x 7168 within 1%; rank 128, whose stages are larger, 94.1 and 90.5)
+__host__ __device__ constexpr int shrink_stages(int rp) { return rp <= 64 ? 4 : 3; }
 __host__ __device__ constexpr int shrink_stage(int rp) { return TILE * 128 + rp * 128; }
 constexpr int shrink_bytes(int rp) {  // (the ring holds the sums in the end: 512 rp bytes)
-  return (SHRINK_STAGES * shrink_stage(rp) > 512 * rp ? SHRINK_STAGES * shrink_stage(rp) : 512 * rp) + 1024;
+  return (shrink_stages(rp) * shrink_stage(rp) > 512 * rp ? shrink_stages(rp) * shrink_stage(rp) : 512 * rp) + 1024;
 }
 struct Bars {
   uint64_t full[4], empty[4], done;
@@ -357,7 +360,7 @@ __global__ void __launch_bounds__(SHRINK_THREADS) k_shrink(const __grid_constant
   __shared__ Bars b;
   __shared__ int rows[TILE];
   const uint32_t size = cluster_size(), rank = cluster_ctarank();
-  const int tile = blockIdx.x / size, warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
+  const int tile = blockIdx.x / size, warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31, stages = shrink_stages(rp);
   launch_dependents();
   wait_for_primary();
   if (tile >= plan.sums[1]) return;  // (the whole cluster)
@@ -373,7 +376,7 @@ __global__ void __launch_bounds__(SHRINK_THREADS) k_shrink(const __grid_constant
     return;
   }
   if (threadIdx.x == 0) {
-    for (int i = 0; i < SHRINK_STAGES; ++i) {
+    for (int i = 0; i < stages; ++i) {
       mbar_init(&b.full[i], 4);
       mbar_init(&b.empty[i], 1);
     }
@@ -392,15 +395,19 @@ __global__ void __launch_bounds__(SHRINK_THREADS) k_shrink(const __grid_constant
   const uint32_t ring = smem_u32(smem), stage = shrink_stage(rp);
   const int blocks = (K + KB - 1) / KB;
   const int k0 = (int)((int64_t)blocks * rank / size), steps = (int)((int64_t)blocks * (rank + 1) / size) - k0;
+  int st = 0;  // a step's stage, and its turn of the ring
+  uint32_t turn = 0;
+  auto next_stage = [&] {
+    if (++st == stages) st = 0, ++turn;
+  };
   if (warp < 4) {
     const Slab s = slab_of(rows[threadIdx.x]);
     const uint32_t slab = warp * SLAB * 128;
     int issued = 0;
     const int adapter = uniform(t.adapter), first = uniform(s.first), count = uniform(s.count);
     if (count == 0 || (s.box && count >= MIN_BOX)) {
-      for (int i = 0; i < steps; ++i) {
-        const int st = i % SHRINK_STAGES;
-        if (i >= SHRINK_STAGES && !warp_wait(&b.empty[st], (i / SHRINK_STAGES - 1) & 1, g)) break;
+      for (int i = 0; i < steps; ++i, next_stage()) {
+        if (turn > 0 && !warp_wait(&b.empty[st], (turn - 1) & 1, g)) break;
         const uint32_t at = ring + st * stage;
         if (elect_one()) {
           mbar_arrive_expect_tx(&b.full[st], (count ? SLAB * 128 : 0) + (warp == 0 ? rp * 128 : 0));
@@ -419,11 +426,14 @@ __global__ void __launch_bounds__(SHRINK_THREADS) k_shrink(const __grid_constant
         const int row = __shfl_sync(0xFFFFFFFFu, s.row, (lane >> 3) + 4 * j);
         src[j] = row >= 0 ? X + (size_t)row * K + c * 8 : nullptr;
       }
-      constexpr int LAG = SHRINK_STAGES - 1;
-      int i = 0;
-      for (; i < steps; ++i) {
-        const int st = i % SHRINK_STAGES;
-        if (i >= SHRINK_STAGES && !warp_wait(&b.empty[st], (i / SHRINK_STAGES - 1) & 1, g)) break;
+      constexpr int LAG = 2;
+      int i = 0, landed = 0;  // the stage of the step before the last LAG ones
+      auto arrive = [&] {
+        if (lane == 0) mbar_arrive(&b.full[landed]);
+        if (++landed == stages) landed = 0;
+      };
+      for (; i < steps; ++i, next_stage()) {
+        if (turn > 0 && !warp_wait(&b.empty[st], (turn - 1) & 1, g)) break;
         const uint32_t at = ring + st * stage;
         const int k = (k0 + i) * KB;
         if (warp == 0 && elect_one()) {
@@ -441,22 +451,21 @@ __global__ void __launch_bounds__(SHRINK_THREADS) k_shrink(const __grid_constant
           cp_wait<LAG>();
           fence_async_shared();
           __syncwarp();
-          if (lane == 0) mbar_arrive(&b.full[(i - LAG) % SHRINK_STAGES]);
+          arrive();
         }
       }
       cp_wait<0>();
       fence_async_shared();
       __syncwarp();
-      if (lane == 0 && i == steps)
-        for (int k = max(0, steps - LAG); k < steps; ++k) mbar_arrive(&b.full[k % SHRINK_STAGES]);
+      if (i == steps)
+        for (int k = max(0, steps - LAG); k < steps; ++k) arrive();
     }
-    if (b.abort && lane == 0) settle(b.full, SHRINK_STAGES, issued, &b.never);
+    if (b.abort && lane == 0) settle(b.full, stages, issued, &b.never);
     __syncwarp();
   } else {
     const uint32_t idesc = idesc_bf16_f32(TILE, rp), tmem = uniform(b.tmem);
-    for (int i = 0; i < steps; ++i) {
-      const int st = i % SHRINK_STAGES;
-      if (!warp_wait(&b.full[st], (i / SHRINK_STAGES) & 1, g)) break;
+    for (int i = 0; i < steps; ++i, next_stage()) {
+      if (!warp_wait(&b.full[st], turn & 1, g)) break;
       tc_fence_after();
       const uint64_t a = sdesc_kmajor(ring + st * stage, 128), w = sdesc_kmajor(ring + st * stage + TILE * 128, 128);
       if (elect_one()) {
