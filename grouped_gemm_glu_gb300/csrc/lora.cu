@@ -6,8 +6,9 @@
 // The forward has P = A, Q = B.  The backward is the same pair with the roles
 // turned (u = bf16(s_a B_a dy), dx = base + A_a^T u), and the adapters'
 // gradients are sums over an adapter's rows, dA_a = sum u x^T, dB_a = sum h dy^T.
-// h and u are rounded to bf16 because they are tensor-core operands of the
-// products behind them; everything else is fp32 until the outputs' rounding.
+// h and u are rounded to bf16 where they are tensor-core operands of the
+// products behind them (not for few rows); everything else is fp32 until the
+// outputs' rounding.
 //
 // Memory bound: with r of 8 to 128 each element of x, base and y takes 2 r
 // operations.  Three kernels on tcgen05, all over rows grouped by adapter:
@@ -26,7 +27,8 @@
 // k_shrink and k_wgrad produce little from much: the CTAs of a cluster share
 // a contraction and add their sums through distributed shared memory, always
 // in the same order, so equal inputs give equal bits.
-// Few rows (decoding) take k_rows instead: one cluster per row, one launch.
+// Few rows (decoding) take k_rows instead: one cluster per row, one launch; in
+// the backward k_row_grads behind it.
 //
 // Measured: 8192 x 7168 with 32 adapters of rank 16, forward 73 us (grouping 6;
 // k_shrink 24, 117 MB at 4.9 TB/s, where a kernel that only loads them takes 21;
@@ -1201,7 +1203,8 @@ template <int CTAS, int AHEAD, int JB, int OCC>
 __global__ void __launch_bounds__(ROW_THREADS, OCC) k_rows(const __nv_bfloat16* __restrict__ X, const __nv_bfloat16* __restrict__ P,
                                                       const __nv_bfloat16* __restrict__ Q, const int32_t* __restrict__ idx,
                                                       const float* __restrict__ scale, const __nv_bfloat16* base, int K,
-                                                      int N, int r, int G, __nv_bfloat16* y, __nv_bfloat16* __restrict__ h) {
+                                                      int N, int r, int G, __nv_bfloat16* y, __nv_bfloat16* __restrict__ h,
+                                                      float* __restrict__ full) {
   __shared__ float sums[CTAS][MAX_R];  // every CTA's sums over its part of K, from all of them
   __shared__ float hid[MAX_R];
   __shared__ float4 other[2][ROW_COLS];
@@ -1258,9 +1261,10 @@ __global__ void __launch_bounds__(ROW_THREADS, OCC) k_rows(const __nv_bfloat16* 
       float s = 0.0f;
 #pragma unroll
       for (int c = 0; c < CTAS; ++c) s += sums[c][threadIdx.x];
-      const __nv_bfloat16 v = __float2bfloat16_rn(s * scale[a]);
-      hid[threadIdx.x] = __bfloat162float(v);
-      if (h && rank == 0) h[(size_t)row * r + threadIdx.x] = v;
+      s *= scale[a];
+      hid[threadIdx.x] = s;  // (no operand of a tensor core here: not rounded)
+      if (h && rank == 0) h[(size_t)row * r + threadIdx.x] = __float2bfloat16_rn(s);
+      if (full && rank == 0) full[(size_t)row * r + threadIdx.x] = s;
     }
     __syncthreads();
   } else if (h && rank == 0 && threadIdx.x < r) {
@@ -1306,13 +1310,74 @@ __global__ void __launch_bounds__(ROW_THREADS, OCC) k_rows(const __nv_bfloat16* 
 }
 
 // ---------------------------------------------------------------------------
+// k_row_grads: the adapters' gradients from few rows, on the CUDA cores.  CTA
+// (256 columns of x or dy, adapter); its warps take four rows of dP at a time,
+// lanes eight columns each, and go over the adapter's rows in their order.  u
+// (of k_rows) in fp32.  Bound by the writing of dA and dB, most of them zeros
+// as a rule.
+// ---------------------------------------------------------------------------
+constexpr int GRAD_THREADS = 128, GRAD_COLS = 256, GRAD_ROWS = 64, FEW_ROWS = 4096;
+
+__global__ void __launch_bounds__(GRAD_THREADS, 8) k_row_grads(const __nv_bfloat16* __restrict__ x, const float* __restrict__ u,
+                                                               const __nv_bfloat16* __restrict__ dy,
+                                                               const __nv_bfloat16* __restrict__ h,
+                                                               const int32_t* __restrict__ idx, int T, int K, int N, int r,
+                                                               __nv_bfloat16* __restrict__ dA, __nv_bfloat16* __restrict__ dB) {
+  __shared__ int rows[GRAD_ROWS], n_;
+  __shared__ float us[FEW_ROWS];  // of the adapter's rows, [n][r]
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, a = blockIdx.y, units = (K + GRAD_COLS - 1) / GRAD_COLS;
+  const bool second = (int)blockIdx.x >= units;
+  const __nv_bfloat16* X = second ? dy : x;
+  __nv_bfloat16* dP = second ? dB : dA;
+  const int C = second ? N : K, col = ((int)blockIdx.x - (second ? units : 0)) * GRAD_COLS + 8 * lane;
+  if (warp == 0) {
+    int n = 0;
+    for (int b = 0; b < T; b += 32) {
+      const bool mine = b + lane < T && idx[b + lane] == a;
+      const uint32_t m = __ballot_sync(0xFFFFFFFFu, mine);
+      if (mine) rows[n + __popc(m & ((1u << lane) - 1))] = b + lane;
+      n += __popc(m);
+    }
+    if (lane == 0) n_ = n;
+  }
+  __syncthreads();
+  wait_for_primary();
+  const int n = n_;
+  for (int i = threadIdx.x; i < n * r; i += GRAD_THREADS) {
+    const size_t at = (size_t)rows[i / r] * r + i % r;
+    us[i] = second ? __bfloat162float(h[at]) : u[at];
+  }
+  __syncthreads();
+  if (col >= C) return;
+  for (int j = 4 * warp; j < r; j += GRAD_THREADS / 8) {
+    float s[4][8] = {};
+    for (int q = 0; q < n; q += 4) {
+      uint4 v[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (q + i < n) v[i] = *reinterpret_cast<const uint4*>(X + (size_t)rows[q + i] * C + col);
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (q + i < n)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) add8(s[k], us[(q + i) * r + j + k], v[i]);
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      *reinterpret_cast<uint4*>(dP + ((size_t)a * r + j + k) * C + col) =
+          make_uint4(pack_bf16x2(s[k][0], s[k][1]), pack_bf16x2(s[k][2], s[k][3]), pack_bf16x2(s[k][4], s[k][5]),
+                     pack_bf16x2(s[k][6], s[k][7]));
+  }
+}
+
+// ---------------------------------------------------------------------------
 // Host
 // ---------------------------------------------------------------------------
 // k_rows for calls of at most so many rows, and rows times rank.  It reads an adapter for each row (from L2, mostly),
 // the tiles each adapter once: at 7168 x 7168 and 64 adapters 128 rows of rank 16 take 13 us against 36, 256 rows 23
 // against 39, 64 rows of rank 64 25 against 36, 128 rows 43 against 42; with few adapters 256 rows of rank 16 21 against
 // 20, one row of rank 128 12.5 against 19, 32 rows of it 30 against 30; 512 rows of 512 x 512, rank 8, 22 against 17.
-constexpr int MOST_ROWS = 256, FEW_ROWS = 4096;
+constexpr int MOST_ROWS = 256;
 bool few_rows(int T, int r) { return T <= MOST_ROWS && (int64_t)T * r <= FEW_ROWS; }
 
 // k_rows for T rows of rank r, 7168 x 7168, us by CTAs per row, AHEAD, JB, OCC:
@@ -1330,6 +1395,14 @@ decltype(&k_rows<8, 1, 1, 8>) rows_kernel(int T, int r, int& ctas) {
   if (ctas == 16) return r <= 16 ? k_rows<16, 8, 2, 2> : k_rows<16, 4, 4, 2>;
   if (T * 9 <= 2 * sms) return k_rows<8, 8, 4, 2>;
   return T * 8 <= 4 * sms ? k_rows<8, 4, 2, 4> : k_rows<8, 1, 1, 8>;
+}
+
+// The backward by k_rows and k_row_grads, for few rows per adapter, which a warp goes over one after the other; us, the
+// tiles behind "against": 64 rows of 7168 x 7168, 64 adapters of rank 16 16 against 50, of rank 64 57 against 90; one row
+// 7 against 22; 64 rows of 2880 x 2880, 8 adapters of rank 8 10 against 26; but 64 rows of one adapter of rank 16 23
+// against 21, of rank 64 68 against 22, of four of rank 64 37 against 28.
+bool few_grads(int T, int r, int G) {
+  return T <= GRAD_ROWS && (int64_t)T * r <= FEW_ROWS && (int64_t)T * r <= 512 * (int64_t)G;
 }
 
 size_t up256(size_t n) { return (n + 255) & ~(size_t)255; }
@@ -1356,13 +1429,13 @@ Plan plan_at(void* ws, int T, int G) {
 }
 
 template <class... A, class... B>
-moe_status_t launch(void (*k)(A...), int ctas, int cluster, int threads, int smem, int smem_limit, bool dependent,
+moe_status_t launch(void (*k)(A...), dim3 ctas, int cluster, int threads, int smem, int smem_limit, bool dependent,
                     cudaStream_t stream, const B&... args) {
   // (one limit per kernel)
   if (smem_limit && (!set_smem_limit((const void*)k, smem_limit) || !prefer_shared((const void*)k))) return MOE_ERR_CUDA;
   if (cluster > 8 && !allow_large_clusters((const void*)k)) return MOE_ERR_CUDA;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(ctas);
+  cfg.gridDim = ctas;
   cfg.blockDim = dim3(threads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
@@ -1476,6 +1549,15 @@ moe_status_t expand(const moe_bf16* hs, const moe_bf16* Q, const moe_bf16* base,
                 out(y), g_wait_limit_ns.load(), st);
 }
 
+moe_status_t rows_launch(const moe_bf16* x, const moe_bf16* P, const moe_bf16* Q, const int32_t* idx, const float* scale,
+                         const moe_bf16* base, int T, int K, int N, int r, int G, moe_bf16* y, moe_bf16* h, float* full,
+                         cudaStream_t s) {
+  int ctas;
+  const auto k = rows_kernel(T, r, ctas);
+  return launch(k, T * ctas, ctas, ROW_THREADS, 0, 0, false, s, in(x), in(P), in(Q), idx, scale, in(base), K, N, r, G, out(y),
+                out(h), full);
+}
+
 bool sizes_ok(int T, int K, int N, int r, int G) {
   return T >= 0 && T <= (1 << 27) && K > 0 && N > 0 && K % 8 == 0 && N % 8 == 0 && K <= (1 << 20) && N <= (1 << 20) && r > 0 &&
          r % 8 == 0 && G > 0;
@@ -1505,7 +1587,8 @@ extern "C" size_t moe_lora_fwd_workspace_size(int T, int r, int G) {
 }
 
 extern "C" size_t moe_lora_bwd_workspace_size(int T, int r, int G) {
-  return T <= 0 || r <= 0 || G <= 0 ? 0 : plan_bytes(T, G) + 2 * sorted_bytes(T, r, G);
+  if (T <= 0 || r <= 0 || G <= 0) return 0;
+  return few_grads(T, r, G) ? up256((size_t)T * r * 4) : plan_bytes(T, G) + 2 * sorted_bytes(T, r, G);
 }
 
 extern "C" moe_status_t moe_lora_fwd(const moe_bf16* x, const moe_bf16* A, const moe_bf16* B, const int32_t* idx,
@@ -1525,12 +1608,7 @@ extern "C" moe_status_t moe_lora_fwd(const moe_bf16* x, const moe_bf16* A, const
   if (overlaps(sy, {sx, sa, sb, si, sf, sh, other}) || overlaps(sh, {sx, sa, sb, si, sf, other}))
     return MOE_ERR_ARG;
   const cudaStream_t s = as_stream(stream);
-  if (few_rows(T, r)) {
-    int ctas;
-    const auto k = rows_kernel(T, r, ctas);
-    return launch(k, T * ctas, ctas, ROW_THREADS, 0, 0, false, s, in(x), in(A), in(B), idx, scale, in(base), K, N, r, G,
-                  out(y), out(h));
-  }
+  if (few_rows(T, r)) return rows_launch(x, A, B, idx, scale, base, T, K, N, r, G, y, h, nullptr, s);
   const Plan p = plan_at(ws, T, G);
   auto* hs = reinterpret_cast<moe_bf16*>(static_cast<char*>(ws) + plan_bytes(T, G));
   if (const moe_status_t e = group(idx, T, G, p, s)) return e;
@@ -1564,6 +1642,12 @@ extern "C" moe_status_t moe_lora_bwd(const moe_bf16* dy, const moe_bf16* x, cons
   if (overlaps(odx, {sx, sy, sh, sa, sb, si, sf, other}) ||
       overlaps(oda, {sx, sy, sh, sa, sb, si, sf, other, odx}) || overlaps(odb, {sx, sy, sh, sa, sb, si, sf, other, odx, oda}))
     return MOE_ERR_ARG;
+  if (few_grads(T, r, G)) {
+    auto* u = static_cast<float*>(ws);
+    if (const moe_status_t e = rows_launch(dy, B, A, idx, scale, base, T, N, K, r, G, dx, nullptr, u, s)) return e;
+    const dim3 grid((K + GRAD_COLS - 1) / GRAD_COLS + (N + GRAD_COLS - 1) / GRAD_COLS, G);
+    return launch(k_row_grads, grid, 0, GRAD_THREADS, 0, 0, true, s, in(x), u, in(dy), in(h), idx, T, K, N, r, out(dA), out(dB));
+  }
   const Plan p = plan_at(ws, T, G);
   auto* us = reinterpret_cast<moe_bf16*>(static_cast<char*>(ws) + plan_bytes(T, G));
   auto* hs = us + sorted_bytes(T, r, G) / 2;

@@ -726,7 +726,7 @@ MOE_API size_t moe_lora_bwd_workspace_size(int T, int r, int G);
 /* For every row t of x [T][K] with adapter a = idx[t] (int32; rows whose
  * index lies outside [0, G) have none):
  *   h = bf16(scale[a] A_a x)            [T][r], zero without an adapter
- *   y = bf16(base + B_a^T h)            [T][N], base alone without an adapter
+ *   y = bf16(base + B_a^T h)            [T][N], base alone without an adapter (for few rows from h before its rounding)
  * A [G][r][K], B [G][r][N], all bf16; scale [G] f32; base [T][N] bf16 the
  * shared projection's output (NULL: zero; may be y itself); h (nullable) is
  * kept for the backward.  Adapters of different ranks share a call with zero
@@ -742,7 +742,7 @@ MOE_API moe_status_t moe_lora_fwd(const moe_bf16* x, const moe_bf16* A, const mo
                                   moe_bf16* h, void* ws, size_t ws_bytes, int32_t* status, moe_stream_t stream);
 
 /* Backward of moe_lora_fwd for dy [T][N]; x, h, A, B, idx and scale as there:
- *   u = bf16(scale[a] B_a dy),  dx = bf16(base + A_a^T u)   [T][K]
+ *   u = bf16(scale[a] B_a dy) (few rows: not rounded),  dx = bf16(base + A_a^T u)   [T][K]
  *   dA_a = bf16(sum over a's rows of u x^T) [r][K],  dB_a = bf16(sum of h dy^T) [r][N]
  * base [T][K] (NULL: zero; may be dx itself) is the gradient that reaches x
  * elsewhere.  dA and dB are written whole (zero for adapters without rows) and

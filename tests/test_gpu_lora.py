@@ -193,6 +193,15 @@ def test_nan_and_infinities_stay_with_their_adapter_and_row(T):
     assert torch.equal(dA[others], ref[1][others])
 
 
+def test_few_rows_and_many_adapters():
+    c = Case(20, 264, 520, 16, 2500, "rows", seed=15)
+    o = _forward(c)
+    dx, dA, dB = _backward(c, o["h"])
+    unused = torch.ones(c.G, dtype=torch.bool)
+    unused[c.idx[c.idx >= 0].long()] = False
+    assert not bool(dA.cpu()[unused].any()) and not bool(dB.cpu()[unused].any())
+
+
 def test_empty_batch():
     c = Case(4, 16, 24, 8, 2, "runs")
     z = lambda n: torch.empty(0, n, dtype=BF, device=DEV)
@@ -298,7 +307,7 @@ def test_offsets_past_32_bits():
 
 
 @pytest.mark.parametrize("T,r", [(76, 16), (77, 16), (256, 16), (257, 16), (128, 32), (129, 32), (256, 8), (3, 128), (8, 8),
-                                 (9, 16), (9, 24), (10, 72), (32, 128), (33, 64), (34, 40)])
+                                 (9, 16), (9, 24), (10, 72), (32, 128), (33, 64), (34, 40), (64, 64), (64, 72), (65, 16)])
 def test_around_the_few_rows_rule(T, r):
     c = Case(T, 136, 264, r, 5, "rows", seed=T)
     _backward(c, _forward(c)["h"])
