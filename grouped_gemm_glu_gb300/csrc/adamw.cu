@@ -61,12 +61,13 @@ struct Grads {
 // What a step's scalars are, written once per step.
 struct Short {
   float b1h, b1l, a1h, a1l, b2f, a2f;  // a1 and a2 with c and c^2
+  float down;                          // a power of two that the gradients are multiplied by first
   float step, root, lr, eps;           // lr / (1 - b1^t), 1 / sqrt(1 - b2^t)
   uint32_t key;
   int32_t skip;  // the gradients' norm is not finite
 };
 struct Scalars : Short {
-  double b1, a1, b2, a2, c;  // a = 1 - b
+  double b1, a1, b2, a2, c;  // a = 1 - b; c without `down`
 };
 // the workspace: the scalars, then the norm's partial sums
 constexpr size_t PARTS_AT = 256;
@@ -266,6 +267,14 @@ __global__ void __launch_bounds__(256) k_adamw_scalars(Scalars o, double max_nor
     s = root64(s);
     o.skip = !(s <= 1.7e308);
     o.c = fmin(1.0, over64(max_norm, s + 1e-6));
+    // Gradients far larger than max_norm: c's square would leave fp32's range, although c g is an ordinary number.  The part of
+    // c below 2^-25 is a power of two of its own, which multiplies the gradients exactly.
+    const int ex = (int)((__double_as_longlong(o.c) >> 52) & 0x7FF) - 1023;
+    if (ex < -25) {
+      const int k = max(ex + 25, -126);
+      o.down = __uint_as_float((uint32_t)(k + 127) << 23);
+      o.c *= __longlong_as_double((int64_t)(1023 - k) << 52);
+    }
     const double a1 = o.a1 * o.c;
     o.a1h = (float)a1;
     o.a1l = (float)(a1 - (double)o.a1h);
@@ -447,6 +456,10 @@ __device__ __forceinline__ void step8(const Short& s, const Scalars* all, const 
       load8(static_cast<const float*>(t.v) + at, n, whole, &v[0].x);
       load8(grad + at, n, whole, &g[0].x);
     }
+  }
+  if (s.down != 1.0f) {
+#pragma unroll
+    for (int i = 0; i < PER / 2; ++i) g[i] = __fmul2_rn(g[i], both(s.down));
   }
   const float decay = s.lr * t.weight_decay;
   float2 om[PER / 2], ov[PER / 2];
@@ -644,6 +657,7 @@ extern "C" moe_status_t moe_adamw_step(const moe_adamw_tensor_t* tensors, const 
       c1.b2 = p->beta2;
       c1.a2 = 1.0 - p->beta2;
       c1.c = 1.0;
+      c1.down = 1.0f;
       c1.b1h = (float)c1.b1;
       c1.b1l = (float)(c1.b1 - (double)c1.b1h);
       c1.a1h = (float)c1.a1;

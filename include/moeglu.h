@@ -801,7 +801,9 @@ MOE_API size_t moe_adamw_workspace_size(int n);
  *   m = b1 m + (1 - b1) g',  v = b2 v + (1 - b2) g'^2
  *   w = w (1 - lr wd) - lr (m / (1 - b1^t)) / (sqrt(v / (1 - b2^t)) + eps)
  * |g| is the 2-norm over all tensors, its squares added in fp32 by eights and
- * these sums exactly (a gradient past 1.8e19 counts as infinite).  8-bit
+ * these sums exactly (sums of squares past fp32's range count as infinite: one
+ * gradient past 1.8e19, thousands past 1e17; squares below 2^-126 lose bits,
+ * those below 2^-149 count as 0).  8-bit
  * moments are written with the smallest scale 2^e (e >= -127) that keeps a
  * block's largest value at or below 448 2^e; a value between two codes goes up
  * if its distance above the lower one, as a fraction of theirs, and 16 random
