@@ -24,7 +24,8 @@ class AdamW:
     def __init__(self, weights, lr: float, betas=(0.9, 0.999), eps: float = 1e-8, weight_decay=0.01, max_norm=None,
                  state: str = "f32", grad_dtype=None, seed: int = 0):
         """weights: contiguous CUDA tensors of one device, float32 or bfloat16,
-        updated in place; a bfloat16 weight gets an f32 master here, which the
+        updated in place (parameters that require gradients too: the step is no
+        part of what autograd records); a bfloat16 weight gets an f32 master here, which the
         step updates and rounds.  weight_decay: one number, or one per tensor.
         max_norm: the gradients of a step are scaled down together to this
         2-norm; a step whose norm is not finite changes nothing.  state: "f32"
@@ -32,7 +33,7 @@ class AdamW:
         per 32 elements, rounded up or down by random bits that seed starts.
         grad_dtype: one type or one per tensor (default: the weight's).
         A weight keeps its memory for as long as this object lives: one that is
-        given another (w.data = ...) is no longer updated.  Steps of one object
+        given another (w.data = ...) is no longer updated, by a step or a load.  Steps of one object
         share their state and workspace and follow one another.
 
         Flat state, one stretch per tensor from a multiple of 32 on: m and v
@@ -88,7 +89,7 @@ class AdamW:
         self.set_lr(lr)
         size = self.m.element_size()
         self._rows = (L.AdamwTensor * max(n, 1))()
-        for row, w, at, d, k in zip(self._rows, ws, self._at, decay, kinds):
+        for row, w, at, d, k in zip(self._rows, self._memory, self._at, decay, kinds):
             narrow = w.dtype == torch.bfloat16
             if narrow:
                 self.master[at:at + w.numel()].copy_(w.view(-1))
@@ -147,7 +148,7 @@ class AdamW:
 
     def moments(self, i: int):
         """(m, v) of weight i in its shape, float32; 8-bit states as the values they hold."""
-        w, at = self.weights[i], self._at[i]
+        w, at = self._memory[i], self._at[i]
         n = w.numel()
         if self.state == "f32":
             return self.m[at:at + n].view(w.shape), self.v[at:at + n].view(w.shape)
@@ -179,6 +180,6 @@ class AdamW:
                 raise ValueError(f"{k}: {v.dtype} {tuple(v.shape)} is needed, got {d[k].dtype} {tuple(d[k].shape)}")
         for k, v in mine.items():
             v.copy_(d[k])
-        for w, at in zip(self.weights, self._at):
+        for w, at in zip(self._memory, self._at):
             if w.dtype == torch.bfloat16:
                 w.view(-1).copy_(self.master[at:at + w.numel()])
