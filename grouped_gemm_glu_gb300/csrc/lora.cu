@@ -1100,18 +1100,16 @@ __global__ void __launch_bounds__(EXPAND_THREADS, 3) k_expand(const __grid_const
 #pragma unroll
         for (int k = 0; k < 4; ++k)
           o[k] = base ? *reinterpret_cast<const uint4*>(smem + (piece(mine, lane, 4 * half + k) - at)) : make_uint4(0, 0, 0, 0);
-        if (product) {
+        if (product) {  // (base's bits otherwise: a sum would make -0 a 0 and every NaN the same)
           tmem_ld32(tmem + ((uint32_t)(32 * slab) << 16) + 64 * block + 32 * half, v);
-        } else {
 #pragma unroll
-          for (int k = 0; k < 32; ++k) v[k] = 0.0f;
+          for (int k = 0; k < 4; ++k) {
+            const float* a = v + 8 * k;
+            o[k] = make_uint4(plus(o[k].x, a[0], a[1]), plus(o[k].y, a[2], a[3]), plus(o[k].z, a[4], a[5]), plus(o[k].w, a[6], a[7]));
+          }
         }
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const float* a = v + 8 * k;
-          o[k] = make_uint4(plus(o[k].x, a[0], a[1]), plus(o[k].y, a[2], a[3]), plus(o[k].z, a[4], a[5]), plus(o[k].w, a[6], a[7]));
-          *reinterpret_cast<uint4*>(smem + (piece(mine, lane, 4 * half + k) - at)) = o[k];
-        }
+        for (int k = 0; k < 4; ++k) *reinterpret_cast<uint4*>(smem + (piece(mine, lane, 4 * half + k) - at)) = o[k];
       }
       fence_async_shared();
       __syncwarp();
@@ -1302,7 +1300,7 @@ __global__ void __launch_bounds__(ROW_THREADS, OCC) k_rows(const __nv_bfloat16* 
       }
       uint32_t w[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) w[i] = pack_bf16x2(bf16_lo(ow[i]) + s[2 * i], bf16_hi(ow[i]) + s[2 * i + 1]);
+      for (int i = 0; i < 4; ++i) w[i] = has ? pack_bf16x2(bf16_lo(ow[i]) + s[2 * i], bf16_hi(ow[i]) + s[2 * i + 1]) : ow[i];
       reinterpret_cast<uint4*>(y + (size_t)row * N)[n] = make_uint4(w[0], w[1], w[2], w[3]);
     }
     if (has) __syncthreads();
