@@ -336,10 +336,12 @@ struct Bars {
   int abort, never;  // (never raised: for the waits that go on after an abort)
   uint32_t tmem;
 };
-// Columns of tensor memory for an accumulator of rp columns (a power of two, at least 32).
-// What of these kernels finds room on an SM together, by shared memory and
-// registers, asks for at most 448 of its 512 columns: no allocation waits for a
-// CTA of a dependent kernel, which itself waits for the kernel in front.
+// Columns of tensor memory for an accumulator of rp columns (a power of two, at
+// least 32).  An allocation may wait for another CTA to give some up, and a CTA of
+// a dependent kernel (of this file or of any other) keeps what it has until the
+// kernel in front of it has ended.  So each of these kernels allocates once, and
+// lets its dependents start only behind that, in every CTA that works: whoever holds
+// tensor memory and waits does so for CTAs that have theirs.
 __device__ __forceinline__ uint32_t tmem_cols(int rp) { return rp <= 32 ? 32 : rp <= 64 ? 64 : 128; }
 
 __device__ __forceinline__ uint2 pack4(float4 s, float f) {
@@ -363,7 +365,6 @@ __global__ void __launch_bounds__(SHRINK_THREADS) k_shrink(const __grid_constant
   __shared__ int rows[TILE];
   const uint32_t size = cluster_size(), rank = cluster_ctarank();
   const int tile = blockIdx.x / size, warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31, stages = shrink_stages(rp);
-  launch_dependents();
   wait_for_primary();
   if (tile >= plan.sums[1]) return;  // (the whole cluster)
   // backwards: k_wgrad, next in the backward, begins with the first tiles and finds dy's last read rows in L2
@@ -393,6 +394,7 @@ __global__ void __launch_bounds__(SHRINK_THREADS) k_shrink(const __grid_constant
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  launch_dependents();  // (with tensor memory in hand: tmem_cols)
   const WaitGuard g{&b.abort, status, limit_ns};
   const uint32_t ring = smem_u32(smem), stage = shrink_stage(rp);
   const int blocks = (K + KB - 1) / KB;
@@ -943,7 +945,6 @@ __global__ void __launch_bounds__(EXPAND_THREADS, 3) k_expand(const __grid_const
     tmem_alloc(&tmem_, TILE);
     tmem_relinquish();
   }
-  launch_dependents();
   wait_for_primary();
   const int chunks = (N + TILE - 1) / TILE, per_tile = (chunks + job - 1) / job;
   const int64_t jobs = (int64_t)plan.sums[1] * per_tile;  // in the order (tile, columns); the first are the CTAs' numbers
@@ -952,6 +953,7 @@ __global__ void __launch_bounds__(EXPAND_THREADS, 3) k_expand(const __grid_const
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  launch_dependents();
   const WaitGuard g{&abort_, status, limit_ns};
   const uint32_t tmem = uniform(tmem_);
   const uint32_t idesc = idesc_bf16_f32(TILE, TILE) | B_MN, hrow = rp > 64 ? 128 : rank_bytes(rp);
