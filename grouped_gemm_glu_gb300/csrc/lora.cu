@@ -154,9 +154,24 @@ __device__ __forceinline__ uint32_t cluster_size() {
 // swizzle's period; 1024 bytes more are asked for).
 __device__ __forceinline__ unsigned char* aligned_smem(unsigned char* p) { return p + ((0u - smem_u32(p)) & 1023u); }
 
+// A look at a barrier that does not hold the thread back; not ready gives up.
+__device__ __noinline__ bool no_wait(uint64_t* bar, uint32_t parity, volatile int* abort, int32_t* status) {
+  uint32_t ok;
+  asm volatile("{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
+               : "=r"(ok)
+               : "r"(smem_u32(bar)), "r"(parity)
+               : "memory");
+  if (ok) return true;
+  *abort = 1;
+  set_status(status, MOE_ERR_TIMEOUT);
+  return false;
+}
 // mbar_wait for waits that mostly last a few hundred cycles: the clock and the
-// abort flag are read at every 256th look only, the first time included.
+// abort flag are read at every 256th look only, the first time included.  (A look
+// lasts until the barrier is ready or for some microseconds; the least limit,
+// 1 ns, therefore does not wait at all.)
 __device__ __forceinline__ bool wait_on(uint64_t* bar, uint32_t parity, const WaitGuard& g) {
+  if (g.limit_ns < 2) return no_wait(bar, parity, g.abort, g.status);
   uint64_t t0 = 0;
   for (uint32_t it = 1;; ++it) {
     if (mbar_test(bar, parity)) return true;
@@ -174,11 +189,25 @@ __device__ __forceinline__ bool wait_on(uint64_t* bar, uint32_t parity, const Wa
   }
 }
 
-// After an abort: gives the TMA copies of the last steps issued a millisecond
-// to land before the CTA's shared memory is given up.
-__device__ __forceinline__ void settle(uint64_t* full, int stages, int issued, int* never) {
-  for (int k = max(0, issued - stages); k < issued; ++k)
-    wait_on(&full[k % stages], (k / stages) & 1, WaitGuard{never, nullptr, 1000000});
+// The waits at a CTA's end, before it gives up its shared and its tensor memory:
+// for copies and MMAs that it has issued, whether or not it has aborted.
+constexpr uint64_t LAND_NS = 1000000;
+__device__ __forceinline__ bool land(uint64_t* bar, uint32_t parity, uint64_t limit_ns) {
+  const uint64_t t0 = globaltimer_ns();
+  while (!mbar_test(bar, parity))
+    if (globaltimer_ns() - t0 > limit_ns) return false;
+  return true;
+}
+// MMAs: their end is signalled in any case.
+__device__ __forceinline__ void land_mma(uint64_t* done, uint32_t parity, const WaitGuard& g) {
+  if (land(done, parity, g.limit_ns > LAND_NS ? g.limit_ns : LAND_NS)) return;
+  *g.abort = 1;
+  set_status(g.status, MOE_ERR_TIMEOUT);
+}
+// Copies of the last steps issued, after an abort: a stage on which another warp
+// has not arrived stays open, but a millisecond is enough for the copies.
+__device__ __forceinline__ void settle(uint64_t* full, int stages, int issued) {
+  for (int k = max(0, issued - stages); k < issued; ++k) land(&full[k % stages], (k / stages) & 1, LAND_NS);
 }
 
 // The operands of TMA and tcgen05 instructions are uniform registers.  Loops
@@ -333,7 +362,7 @@ constexpr int shrink_bytes(int rp) {  // (the ring holds the sums in the end: 51
 }
 struct Bars {
   uint64_t full[4], empty[4], done;
-  int abort, never;  // (never raised: for the waits that go on after an abort)
+  int abort;
   uint32_t tmem;
 };
 // Columns of tensor memory for an accumulator of rp columns (a power of two, at
@@ -384,7 +413,7 @@ __global__ void __launch_bounds__(SHRINK_THREADS) k_shrink(const __grid_constant
       mbar_init(&b.empty[i], 1);
     }
     mbar_init(&b.done, 1);
-    b.abort = b.never = 0;
+    b.abort = 0;
     fence_barrier_init();
   }
   if (warp == 4) {
@@ -399,7 +428,7 @@ __global__ void __launch_bounds__(SHRINK_THREADS) k_shrink(const __grid_constant
   const uint32_t ring = smem_u32(smem), stage = shrink_stage(rp);
   const int blocks = (K + KB - 1) / KB;
   const int k0 = (int)((int64_t)blocks * rank / size), steps = (int)((int64_t)blocks * (rank + 1) / size) - k0;
-  int st = 0;  // a step's stage, and its turn of the ring
+  int st = 0, issued = 0;  // a step's stage, and its turn of the ring; steps whose copies this warp has issued
   uint32_t turn = 0;
   auto next_stage = [&] {
     if (++st == stages) st = 0, ++turn;
@@ -407,7 +436,6 @@ __global__ void __launch_bounds__(SHRINK_THREADS) k_shrink(const __grid_constant
   if (warp < 4) {
     const Slab s = slab_of(rows[threadIdx.x]);
     const uint32_t slab = warp * SLAB * 128;
-    int issued = 0;
     const int adapter = uniform(t.adapter), first = uniform(s.first), count = uniform(s.count);
     if (count == 0 || (s.box && count >= MIN_BOX)) {
       for (int i = 0; i < steps; ++i, next_stage()) {
@@ -464,8 +492,6 @@ __global__ void __launch_bounds__(SHRINK_THREADS) k_shrink(const __grid_constant
       if (i == steps)
         for (int k = max(0, steps - LAG); k < steps; ++k) arrive();
     }
-    if (b.abort && lane == 0) settle(b.full, stages, issued, &b.never);
-    __syncwarp();
   } else {
     const uint32_t idesc = idesc_bf16_f32(TILE, rp), tmem = uniform(b.tmem);
     for (int i = 0; i < steps; ++i, next_stage()) {
@@ -482,10 +508,12 @@ __global__ void __launch_bounds__(SHRINK_THREADS) k_shrink(const __grid_constant
     if (elect_one()) tc_commit(&b.done);
     __syncwarp();
   }
-  if (warp == 4) wait_on(&b.done, 0, WaitGuard{&b.never, status, limit_ns});
+  if (warp == 4) land_mma(&b.done, 0, g);
   tc_fence_before();
-  __syncthreads();  // (every copy has landed and every MMA has read: the ring is free)
+  __syncthreads();  // (every copy has landed and every MMA has read: the ring is free, unless a wait gave up)
   tc_fence_after();
+  if (b.abort && lane == 0) settle(b.full, stages, issued);
+  __syncwarp();
   // the sums to shared memory, as float4 [rp / 4][128]
   if (warp < 4 && !b.abort) {
     for (int c = 0; c < rp; c += 32) {
@@ -567,7 +595,7 @@ __global__ void __launch_bounds__(WGRAD_THREADS) k_wgrad(const __grid_constant__
   extern __shared__ unsigned char smem_[];
   unsigned char* smem = aligned_smem(smem_);
   __shared__ uint64_t full[3], empty[3], acc_full[2], acc_empty[2], done;
-  __shared__ int abort_, never, head_through, tail_adapter;
+  __shared__ int abort_, head_through, tail_adapter;
   __shared__ uint32_t tmem_;
   __shared__ int4 part[BATCH];                           // of each tile: first place, places, adapter, flags
   __shared__ int2 step_of[STEPS];                        // first place, places
@@ -593,7 +621,7 @@ __global__ void __launch_bounds__(WGRAD_THREADS) k_wgrad(const __grid_constant__
       mbar_init(&acc_empty[i], 4);
     }
     mbar_init(&done, 1);
-    abort_ = never = head_through = 0;
+    abort_ = head_through = 0;
     tail_adapter = -1;
     fence_barrier_init();
   }
@@ -834,12 +862,12 @@ __global__ void __launch_bounds__(WGRAD_THREADS) k_wgrad(const __grid_constant__
   if (warp == 4) {
     if (elect_one()) tc_commit(&done);  // (the same lane is elected throughout: its commit covers all that was issued)
     __syncwarp();
-    wait_on(&done, 0, WaitGuard{&never, status, limit_ns});
-  } else if (warp < 4 && lane == 0 && abort_) {
-    settle(full, stages, i, &never);
+    land_mma(&done, 0, g);
   }
   __syncwarp();
   cluster_sync();
+  if (warp < 4 && lane == 0 && abort_) settle(full, stages, i);
+  __syncwarp();
   if (size > 1 && !abort_) {
     // the runs that cross shares: the one that begins in CTA c, its heads in the next ones up to where it ends
     int adapter[8], through[8];
@@ -928,7 +956,7 @@ __global__ void __launch_bounds__(EXPAND_THREADS, 3) k_expand(const __grid_const
   extern __shared__ unsigned char smem_[];
   unsigned char* smem = aligned_smem(smem_);
   __shared__ uint64_t rows_in[2], product_in, product_out;  // base's rows, h and Q in shared memory; the MMAs' end
-  __shared__ int abort_, never, taken[2];  // (the numbers of the jobs behind the next one, by turns)
+  __shared__ int abort_, taken[2];  // (the numbers of the jobs behind the next one, by turns)
   __shared__ uint32_t tmem_;
   const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31, slab = warp & 3, block = warp >> 2;
   const int ahead = expand_ahead(rp);
@@ -938,7 +966,7 @@ __global__ void __launch_bounds__(EXPAND_THREADS, 3) k_expand(const __grid_const
     mbar_init(&rows_in[1], 4 * 32);
     mbar_init(&product_in, 1);
     mbar_init(&product_out, 1);
-    abort_ = never = 0;
+    abort_ = 0;
     fence_barrier_init();
   }
   if (warp == 4) {
@@ -1051,10 +1079,13 @@ __global__ void __launch_bounds__(EXPAND_THREADS, 3) k_expand(const __grid_const
   Part now = part_of(behind), next = part_of(found);
   int chunk = now.chunk, done = 0;  // jobs done
   bool more = now.end > 0;
-  int turn[2] = {0, 0}, products = 0, buf = 0;
+  int products = 0, buf = 0;
+  // the parities of what has been waited for, and of what has been issued: rows by buffer, a bit each (issued by warps 0
+  // to 3); products (warp 6) and MMAs (warp 4)
+  uint32_t rows_waited = 0, rows_issued = 0, issued = 0;
   if (more) {
-    if (warp < 4) load_rows(now, chunk, 0);
-    if (warp == 6 && now.adapter >= 0) load_product(now, chunk, true);
+    if (warp < 4) load_rows(now, chunk, 0), rows_issued = 1;
+    if (warp == 6 && now.adapter >= 0) load_product(now, chunk, true), issued = 1;
     __syncwarp();
   }
   while (more) {
@@ -1064,20 +1095,20 @@ __global__ void __launch_bounds__(EXPAND_THREADS, 3) k_expand(const __grid_const
     const bool first = chunk == now.chunk;
     if (warp == 7 && lane == 0 && first && next.end > 0) taken[done & 1] = take();
     if (last && !first) find_tile(found, next.end > 0 ? taken[done & 1] : 0x7FFFFFFF);
-    if (ahead && another && warp < 4) load_rows(last ? next : now, next_chunk, buf ^ 1);
+    if (ahead && another && warp < 4) load_rows(last ? next : now, next_chunk, buf ^ 1), rows_issued ^= 2 >> buf;
     bool ok = true;
     if (product) {
       if (warp == 4) {
         const bool in = warp_wait(&product_in, products & 1, g);
         tc_fence_after();
         const uint64_t h = sdesc_kmajor(h_at, hrow), q = sdesc_mnmajor(q_at, 128, rp * 128);
-        if (elect_one()) {
-          if (in)
+        if (in && elect_one()) {  // (if not, the others' wait for the product ends by the abort flag)
 #pragma unroll
-            for (int k = 0; k < MAX_R / 16; ++k)
-              if (16 * k < rp) umma_bf16(tmem, h + ((k >> 2) * (TILE * 128) + 32 * (k & 3)) / 16, q + (2048 >> 4) * k, idesc, k > 0);
+          for (int k = 0; k < MAX_R / 16; ++k)
+            if (16 * k < rp) umma_bf16(tmem, h + ((k >> 2) * (TILE * 128) + 32 * (k & 3)) / 16, q + (2048 >> 4) * k, idesc, k > 0);
           tc_commit(&product_out);
         }
+        issued ^= in;
       }
       __syncwarp();
       ok = wait_on(&product_out, products & 1, g);
@@ -1085,11 +1116,11 @@ __global__ void __launch_bounds__(EXPAND_THREADS, 3) k_expand(const __grid_const
     }
     // (h and Q have been read: the next unit's may come)
     ok = __all_sync(0xFFFFFFFFu, ok);
-    if (warp == 6 && ok && another && (last ? next : now).adapter >= 0) load_product(last ? next : now, next_chunk, last);
+    if (warp == 6 && ok && another && (last ? next : now).adapter >= 0) load_product(last ? next : now, next_chunk, last), issued ^= 1;
     __syncwarp();
     if (last && !first) find_row(found);
-    ok &= wait_on(&rows_in[buf], turn[buf] & 1, g);
-    ++turn[buf];
+    ok &= wait_on(&rows_in[buf], (rows_waited >> buf) & 1, g);
+    rows_waited ^= 1 << buf;
     tc_fence_after();
     const int col = c0 + 64 * block;
     const uint32_t mine = at + buf * (TILE * 256) + block * (TILE * 128) + slab * (SLAB * 128);
@@ -1152,16 +1183,18 @@ __global__ void __launch_bounds__(EXPAND_THREADS, 3) k_expand(const __grid_const
       ++done;
     }
     more = another;
-    if (!ahead && another && warp < 4) load_rows(now, chunk, 0);
+    if (!ahead && another && warp < 4) load_rows(now, chunk, 0), rows_issued ^= 1;
     if (ahead) buf ^= 1;
   }
   cp_wait<0>();
-  if (abort_ && warp == 0 && lane == 0) {
-    wait_on(&rows_in[0], turn[0] & 1, WaitGuard{&never, nullptr, 1000000});
-    wait_on(&rows_in[1], turn[1] & 1, WaitGuard{&never, nullptr, 1000000});
-    wait_on(&product_in, products & 1, WaitGuard{&never, nullptr, 1000000});
+  // (the last phase issued; that of a barrier without one counts as over)
+  if (abort_ && lane == 0) {
+    if (warp == 0)
+      for (int k = 0; k < 2; ++k) land(&rows_in[k], ~(rows_issued >> k) & 1, LAND_NS);
+    if (warp == 6) land(&product_in, ~issued & 1, LAND_NS);
   }
-  if (warp == 4 && products > 0) wait_on(&product_out, (products - 1) & 1, WaitGuard{&never, status, limit_ns});
+  __syncwarp();
+  if (warp == 4) land_mma(&product_out, ~issued & 1, g);
   tc_fence_before();
   __syncthreads();
   if (warp == 4) {

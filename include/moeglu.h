@@ -827,8 +827,9 @@ MOE_API moe_status_t moe_adamw_step(const moe_adamw_tensor_t* tensors, const voi
  * for use inside a graph capture). */
 MOE_API moe_status_t moe_get_status(const int32_t* status, int32_t* host_out, moe_stream_t stream);
 
-/* Pipeline wait limit in nanoseconds for the persistent GEMMs (default 2e9);
- * after it a wait gives up, sets MOE_ERR_TIMEOUT and the kernel returns. */
+/* Pipeline wait limit in nanoseconds for the persistent GEMMs and the adapters'
+ * kernels (default 2e9); after it a wait gives up, sets MOE_ERR_TIMEOUT and the
+ * kernel returns, once its copies and MMAs under way have landed. */
 MOE_API void moe_set_wait_limit_ns(uint64_t ns);
 
 /* Self-test of the bounded wait behind every pipeline wait of the
