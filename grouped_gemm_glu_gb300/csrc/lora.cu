@@ -1,14 +1,16 @@
 // Low-rank adapters of many requests beside a projection that they share.
 //
-//   h_t = bf16(s_a P_a x_t),  y_t = bf16(base_t + Q_a^T h_t)   for row t with
-//   adapter a (P [G][r][K], Q [G][r][N]; rows without one: h = 0, y = base)
+//   h_t = s_a P_a x_t,  y_t = base_t + Q_a^T h_t   for row t with adapter a
+//   (P [G][r][K], Q [G][r][N]; rows without one: h = 0, y = base)
 //
 // The forward has P = A, Q = B.  The backward is the same pair with the roles
-// turned (u = bf16(s_a B_a dy), dx = base + A_a^T u), and the adapters'
-// gradients are sums over an adapter's rows, dA_a = sum u x^T, dB_a = sum h dy^T.
-// h and u are rounded to bf16 where they are tensor-core operands of the
-// products behind them (not for few rows); everything else is fp32 until the
-// outputs' rounding.
+// turned (u = s_a B_a dy, dx = base + A_a^T u), and the adapters' gradients are
+// sums over an adapter's rows, dA_a = sum u x^T, dB_a = sum h dy^T.  Sums are
+// fp32, outputs are rounded once.  Where h and u are tensor-core operands of the
+// products behind them they are two bf16 numbers, the value's rounding and what
+// that drops (16 bits and more: one bf16 number made y's and dA's errors a third
+// larger, and all of y's where base and product cancel); dB takes the bf16 h that
+// the caller kept.
 //
 // Memory bound: with r of 8 to 128 each element of x, base and y takes 2 r
 // operations.  Three kernels on tcgen05, all over rows grouped by adapter:
@@ -123,7 +125,7 @@ __device__ __forceinline__ uint64_t swizzle_bits(uint32_t row_bytes) {
 }
 // Operand tiles: rows of row_bytes along the contraction (kmajor) or across it
 // (mnmajor: the rows are steps of the contraction, `block` bytes between
-// blocks of 64 elements of the kept dimension).
+// blocks of the kept dimension).
 __device__ __forceinline__ uint64_t sdesc_kmajor(uint32_t saddr, uint32_t row_bytes) {
   return (uint64_t)((saddr & 0x3FFFFu) >> 4) | ((uint64_t)(row_bytes >> 1) << 32) | (1ull << 46) | swizzle_bits(row_bytes);
 }
@@ -135,6 +137,50 @@ constexpr uint32_t A_MN = 1u << 15, B_MN = 1u << 16;  // instruction descriptor:
 __device__ __forceinline__ void wait_for_primary() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
+// 32 columns of the thread's lane of tensor memory, written; and the MMA whose
+// left operand lies there (a row per lane, two elements per column).
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,"
+      "%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
+      "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
+      "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void umma_bf16_from_tmem(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, 1, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b_desc), "r"(idesc)
+      : "memory");
+}
+
+// The sum of twice 32 columns of the thread's lane.
+__device__ __forceinline__ void tmem_ld32_sum(uint32_t at, uint32_t other, float* v) {
+  uint32_t r[64];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {"
+      "%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31"
+      "}, [%64];\n tcgen05.ld.sync.aligned.32x32b.x32.b32 {"
+      "%32,%33,%34,%35,%36,%37,%38,%39,%40,%41,%42,%43,%44,%45,%46,%47,"
+      "%48,%49,%50,%51,%52,%53,%54,%55,%56,%57,%58,%59,%60,%61,%62,%63"
+      "}, [%65];\n tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+        "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+        "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31]),
+        "=r"(r[32]), "=r"(r[33]), "=r"(r[34]), "=r"(r[35]), "=r"(r[36]), "=r"(r[37]), "=r"(r[38]), "=r"(r[39]),
+        "=r"(r[40]), "=r"(r[41]), "=r"(r[42]), "=r"(r[43]), "=r"(r[44]), "=r"(r[45]), "=r"(r[46]), "=r"(r[47]),
+        "=r"(r[48]), "=r"(r[49]), "=r"(r[50]), "=r"(r[51]), "=r"(r[52]), "=r"(r[53]), "=r"(r[54]), "=r"(r[55]),
+        "=r"(r[56]), "=r"(r[57]), "=r"(r[58]), "=r"(r[59]), "=r"(r[60]), "=r"(r[61]), "=r"(r[62]), "=r"(r[63])
+      : "r"(at), "r"(other)
+      : "memory");
+#pragma unroll
+  for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]) + __uint_as_float(r[32 + i]);
+}
 __device__ __forceinline__ float4 ld_cluster(uint32_t addr) {
   float4 v;
   asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr));
@@ -373,18 +419,33 @@ struct Bars {
 // tensor memory and waits does so for CTAs that have theirs.
 __device__ __forceinline__ uint32_t tmem_cols(int rp) { return rp <= 32 ? 32 : rp <= 64 ? 64 : 128; }
 
-__device__ __forceinline__ uint2 pack4(float4 s, float f) {
-  return make_uint2(pack_bf16x2(s.x * f, s.y * f), pack_bf16x2(s.z * f, s.w * f));
+// Eight values times f as bf16, and what that drops as bf16 (nothing of an
+// infinity): together 16 bits and more.
+struct Parts {
+  uint4 hi, lo;
+};
+__device__ __forceinline__ uint32_t dropped(float x, float y, uint32_t hi) {
+  const float a = x - bf16_lo(hi), b = y - bf16_hi(hi), most = 3.3e38f;
+  return pack_bf16x2(fabsf(a) < most ? a : 0.0f, fabsf(b) < most ? b : 0.0f);
+}
+__device__ __forceinline__ Parts split8(float4 s, float4 t, float f) {
+  s = make_float4(s.x * f, s.y * f, s.z * f, s.w * f);
+  t = make_float4(t.x * f, t.y * f, t.z * f, t.w * f);
+  Parts p;
+  p.hi = make_uint4(pack_bf16x2(s.x, s.y), pack_bf16x2(s.z, s.w), pack_bf16x2(t.x, t.y), pack_bf16x2(t.z, t.w));
+  p.lo = make_uint4(dropped(s.x, s.y, p.hi.x), dropped(s.z, s.w, p.hi.y), dropped(t.x, t.y, p.hi.z), dropped(t.z, t.w, p.hi.w));
+  return p;
 }
 
 // X [T][K] (and as a tensor map, boxes of 64 columns x 32 rows), P as a map
-// of boxes 64 x rp.  h [T][r] (nullable) by row, hs in the grouped order; also
-// (other, nullable [T][r]) copied into that order as others.
+// of boxes 64 x rp.  h [T][r] (nullable) by row, hs [2][places][r] in the
+// grouped order, in two parts (split4); also (other, nullable [T][r]) copied into
+// that order as others [places][r].
 __global__ void __launch_bounds__(SHRINK_THREADS) k_shrink(const __grid_constant__ CUtensorMap mx,
                                                            const __grid_constant__ CUtensorMap mp,
                                                            const __nv_bfloat16* __restrict__ X,
                                                            const float* __restrict__ scale, int K, int r, int rp, Plan plan,
-                                                           __nv_bfloat16* __restrict__ h, __nv_bfloat16* __restrict__ hs,
+                                                           int places, __nv_bfloat16* __restrict__ h, __nv_bfloat16* __restrict__ hs,
                                                            const __nv_bfloat16* __restrict__ other,
                                                            __nv_bfloat16* __restrict__ others, uint64_t limit_ns,
                                                            int32_t* status) {
@@ -535,21 +596,34 @@ __global__ void __launch_bounds__(SHRINK_THREADS) k_shrink(const __grid_constant
   cluster_sync();
   if (!b.abort) {
     const float f = scale[t.adapter];
-    const int quads = r / 4, items = up * quads;
+    const int items = up * (r / 8);
     for (int i = threadIdx.x + rank * SHRINK_THREADS; i < items; i += SHRINK_THREADS * size) {
-      const int q = i / up, l = i - q * up;
-      const uint32_t at = ring + (q * TILE + l) * 16;
-      float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f), v[8];
+      const int q = i / up, l = i - q * up;  // (eight columns of a row)
+      const bool mine = l < t.count;
+      float4 sum[2], v[2][8];
 #pragma unroll
-      for (uint32_t c = 0; c < 8; ++c) v[c] = c < size && l < t.count ? ld_cluster(mapa_shared(at, c)) : s;
+      for (int k = 0; k < 2; ++k) {
+        sum[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
-      for (uint32_t c = 0; c < 8; ++c) s.x += v[c].x, s.y += v[c].y, s.z += v[c].z, s.w += v[c].w;
-      const uint2 o = pack4(s, l < t.count ? f : 0.0f);
-      if (h && l < t.count) *reinterpret_cast<uint2*>(h + (size_t)rows[l] * r + q * 4) = o;
-      *reinterpret_cast<uint2*>(hs + (size_t)(t.start + l) * r + q * 4) = l < t.count ? o : make_uint2(0, 0);
+        for (uint32_t c = 0; c < 8; ++c)
+          v[k][c] = c < size && mine ? ld_cluster(mapa_shared(ring + ((2 * q + k) * TILE + l) * 16, c)) : sum[k];
+      }
+#pragma unroll
+      for (int k = 0; k < 2; ++k)
+#pragma unroll
+        for (uint32_t c = 0; c < 8; ++c) {
+          sum[k].x += v[k][c].x, sum[k].y += v[k][c].y;
+          sum[k].z += v[k][c].z, sum[k].w += v[k][c].w;
+        }
+      Parts o{make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
+      if (mine) o = split8(sum[0], sum[1], f);
+      const size_t to = (size_t)(t.start + l) * r + q * 8;
+      if (h && mine) *reinterpret_cast<uint4*>(h + (size_t)rows[l] * r + q * 8) = o.hi;
+      *reinterpret_cast<uint4*>(hs + to) = o.hi;
+      *reinterpret_cast<uint4*>(hs + (size_t)places * r + to) = o.lo;
       if (other)
-        *reinterpret_cast<uint2*>(others + (size_t)(t.start + l) * r + q * 4) =
-            l < t.count ? *reinterpret_cast<const uint2*>(other + (size_t)rows[l] * r + q * 4) : make_uint2(0, 0);
+        *reinterpret_cast<uint4*>(others + to) =
+            mine ? *reinterpret_cast<const uint4*>(other + (size_t)rows[l] * r + q * 8) : make_uint4(0, 0, 0, 0);
     }
   }
   cluster_sync();  // (the other CTAs have read this one's sums)
@@ -562,18 +636,25 @@ __global__ void __launch_bounds__(SHRINK_THREADS) k_shrink(const __grid_constant
 // ---------------------------------------------------------------------------
 // k_wgrad: cluster (128 columns of x or dy, X [T][C]), its CTAs share the tiles of all
 // adapters: dP [G][r][C] = U^T X over each adapter's rows, U in the grouped
-// order.  An adapter's tiles that cross from one CTA's share into the next
-// ones' are summed by the whole cluster in the end.  A step of the ring is one
-// tile, or neighbouring small ones together (they lie side by side in the
-// grouped order), whose rows are under way at once.
+// order, u in two parts (h, which the caller gives in bf16, in one).  An adapter's
+// tiles that cross from one CTA's share into the next ones' are summed by the
+// whole cluster in the end.  A step of the ring is one tile, or neighbouring small
+// ones together (they lie side by side in the grouped order), whose rows are under
+// way at once.
+// BESIDE: u's parts are one operand of twice the columns, whose sums meet when
+// they are written out, so that an MMA reads x once for both; else two MMAs into
+// one accumulator, for runs of few rows, which writing out bounds (host rule at
+// wgrad).
 // Warps 0 to 3 load 32 rows each, 4 issues the MMAs, 5 to 8 write out; two
-// accumulators.
+// accumulators, and one for the run from before, which stays there to the end.
 // ---------------------------------------------------------------------------
 constexpr int WGRAD_THREADS = 288, BATCH = 32, STEPS = 16;  // tiles looked up together, in so many steps
 constexpr int SMALL = 64;  // places: tiles of at most so many that begin in the same SMALL places share a step
 __host__ __device__ constexpr int wgrad_stages(int rp) { return rp <= 32 ? 2 : rp <= 64 ? 3 : 2; }
-__host__ __device__ constexpr int wgrad_stage(int rp) { return TILE * 256 + TILE * rank_bytes(rp); }
-constexpr int wgrad_bytes(int rp) { return wgrad_stages(rp) * wgrad_stage(rp) + 512 * rp + 1024; }
+__host__ __device__ constexpr int wgrad_stage(int rp) { return TILE * 256 + 2 * TILE * rank_bytes(rp); }
+constexpr int wgrad_bytes(int rp) { return wgrad_stages(rp) * wgrad_stage(rp) + 1024; }
+static_assert(wgrad_stages(16) * wgrad_stage(16) >= 2 * 512 * 16 && wgrad_stages(128) * wgrad_stage(128) >= 2 * 512 * 128,
+              "two runs' sums");
 
 // of a tile in this CTA: the first / last of its run of one adapter; the run began before / goes on behind it; the first /
 // last of its step
@@ -590,11 +671,12 @@ struct Sides {
   Side of[2];
 };
 
+template <bool BESIDE>
 __global__ void __launch_bounds__(WGRAD_THREADS) k_wgrad(const __grid_constant__ Sides sides, int r, int rp, int G, Plan plan,
-                                                         uint64_t limit_ns, int32_t* status) {
+                                                         int places, uint64_t limit_ns, int32_t* status) {
   extern __shared__ unsigned char smem_[];
   unsigned char* smem = aligned_smem(smem_);
-  __shared__ uint64_t full[3], empty[3], acc_full[2], acc_empty[2], done;
+  __shared__ uint64_t full[3], empty[3], acc_full[2], acc_empty[2], done;  // (the head's accumulator has none: `done`)
   __shared__ int abort_, head_through, tail_adapter;
   __shared__ uint32_t tmem_;
   __shared__ int4 part[BATCH];                           // of each tile: first place, places, adapter, flags
@@ -609,8 +691,12 @@ __global__ void __launch_bounds__(WGRAD_THREADS) k_wgrad(const __grid_constant__
   const int C = side.C, c0 = (unit - (second ? sides.of[0].units : 0)) * TILE;
   const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
   const int stages = wgrad_stages(rp);
-  const uint32_t ring = smem_u32(smem), stage = wgrad_stage(rp), acc_cols = tmem_cols(rp);
-  unsigned char* head = smem + stages * stage;  // float4 [rp / 4][128]: the run from before
+  const uint32_t ring = smem_u32(smem), stage = wgrad_stage(rp);
+  const bool beside = BESIDE && !second;
+  const uint32_t acc_cols = BESIDE ? 2 * rank_cols(rp) : tmem_cols(rp);
+  // in the end, behind the last step, the ring holds what the cluster sums, as float4 [rp / 4][128] each: the run that goes
+  // on behind this share, and the one from before it
+  unsigned char *const tail = smem, *const head = smem + 512 * rp;
   if (threadIdx.x == 0) {
     for (int i = 0; i < stages; ++i) {
       mbar_init(&full[i], 4);
@@ -626,7 +712,7 @@ __global__ void __launch_bounds__(WGRAD_THREADS) k_wgrad(const __grid_constant__
     fence_barrier_init();
   }
   if (warp == 4) {
-    tmem_alloc(&tmem_, 2 * acc_cols);
+    tmem_alloc(&tmem_, 4 * acc_cols);
     tmem_relinquish();
   }
   tc_fence_before();
@@ -647,7 +733,32 @@ __global__ void __launch_bounds__(WGRAD_THREADS) k_wgrad(const __grid_constant__
     ++i;
     if (++st == stages) st = 0, ++turn;
   };
-  bool before = false, alive = true;
+  bool before = false, has_head = false, alive = true;
+  const int quad = warp & 3, l = 32 * quad + lane;  // (a warp reads the tensor-memory lanes of its number modulo 4)
+  auto sums = [&](int acc, int cc, float* v) {  // 32 columns of an accumulator
+    const uint32_t at = tmem + acc * acc_cols + ((uint32_t)(32 * quad) << 16) + cc;
+    if (beside && rp > 16) {
+      tmem_ld32_sum(at, at + rank_cols(rp), v);
+    } else {
+      tmem_ld32(at, v);
+      if (beside) {
+#pragma unroll
+        for (int k = 0; k < 16; ++k) v[k] += v[16 + k];
+      }
+    }
+  };
+  auto keep = [&](int acc, unsigned char* to) {
+    for (int cc = 0; cc < rp; cc += 32) {
+      float v[32];
+      sums(acc, cc, v);
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        if (cc + 4 * k < rp)
+          *reinterpret_cast<float4*>(to + (((cc >> 2) + k) * TILE + l) * 16) =
+              make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
+    }
+  };
+  const uint32_t lower = TILE * 256 + TILE * rank_bytes(rp);  // u's second part in a stage
   for (int b0 = lo, m = 0; b0 < hi; b0 += m) {
     if (b0 > lo) __syncthreads();
     int steps;
@@ -740,7 +851,7 @@ __global__ void __launch_bounds__(WGRAD_THREADS) k_wgrad(const __grid_constant__
         const uint32_t at = ring + st * stage, dst = at + warp * (SLAB * 128);
         if (turn > 0) alive = alive && warp_wait(&empty[st], (turn - 1) & 1, g);
         if (!alive) break;
-        const uint32_t extra = warp == 0 ? TILE * rank_bytes(rp) : 0;
+        const uint32_t extra = warp == 0 ? TILE * rank_bytes(rp) * (second ? 1 : 2) : 0;
         if (first >= 0) {
           if (elect_one()) {
             mbar_arrive_expect_tx(&full[st], SLAB * 128 * (two ? 2 : 1) + extra);
@@ -759,6 +870,10 @@ __global__ void __launch_bounds__(WGRAD_THREADS) k_wgrad(const __grid_constant__
           if (elect_one()) {
             tma_2d(at + TILE * 256, &mu, &full[st], 0, from);
             if (rp > 64) tma_2d(at + TILE * 256 + TILE * 128, &mu, &full[st], 64, from);
+            if (!second) {
+              tma_2d(at + lower, &mu, &full[st], 0, places + from);
+              if (rp > 64) tma_2d(at + lower + TILE * 128, &mu, &full[st], 64, places + from);
+            }
           }
         }
         __syncwarp();
@@ -784,57 +899,65 @@ __global__ void __launch_bounds__(WGRAD_THREADS) k_wgrad(const __grid_constant__
       }
       if (landing >= 0) landed(false);
     } else if (warp == 4) {
-      const uint32_t urow = rp > 64 ? 128 : rank_bytes(rp), idesc = idesc_bf16_f32(TILE, rp) | A_MN | B_MN;
+      const uint32_t urow = rp > 64 ? 128 : rank_bytes(rp);
+      const uint32_t idesc = idesc_bf16_f32(TILE, beside ? rank_cols(rp) + rp : rp) | A_MN | B_MN;
       int from = 0;
       for (int j = 0; j < m; ++j) {
-        const int start = uniform(part[j].x), up = uniform(part[j].y), flags = uniform(part[j].w), acc = run & 1;
+        const int start = uniform(part[j].x), up = uniform(part[j].y), flags = uniform(part[j].w);
         if (flags & STEP_BEGINS) {
           from = start;
           alive = alive && warp_wait(&full[st], turn & 1, g);
         }
-        if (alive && (flags & RUN_BEGINS) && run >= 2) alive = warp_wait(&acc_empty[acc], (run / 2 - 1) & 1, g);
+        if (flags & RUN_BEGINS) before = (flags & FROM_BEFORE) != 0;
+        const int acc = before ? 2 : run & 1;
+        if (alive && (flags & RUN_BEGINS) && !before && run >= 2) alive = warp_wait(&acc_empty[acc], (run / 2 - 1) & 1, g);
         if (!alive) break;
         tc_fence_after();
         const uint32_t k0 = (start - from) / ALIGN;
         const uint64_t x = sdesc_mnmajor(ring + st * stage, 128, TILE * 128) + (2048 >> 4) * k0;
-        const uint64_t u = sdesc_mnmajor(ring + st * stage + TILE * 256, urow, TILE * 128) + urow * k0;
+        const uint64_t u = sdesc_mnmajor(ring + st * stage + TILE * 256, urow, TILE * urow) + urow * k0;
         const uint32_t keep = (flags & RUN_BEGINS) ? 0u : 1u;
         if (elect_one()) {
 #pragma unroll
           for (int k = 0; k < TILE / ALIGN; ++k)
             if (k * ALIGN < up)
               umma_bf16(tmem + acc * acc_cols, x + (2048 >> 4) * k, u + urow * k, idesc, k > 0 ? 1u : keep);
+          if (!BESIDE && !second)
+#pragma unroll
+            for (int k = 0; k < TILE / ALIGN; ++k)
+              if (k * ALIGN < up)
+                umma_bf16(tmem + acc * acc_cols, x + (2048 >> 4) * k, u + (lower - TILE * 256) / 16 + urow * k, idesc, 1u);
           if (flags & STEP_ENDS) tc_commit(&empty[st]);
-          if (flags & RUN_ENDS) tc_commit(&acc_full[acc]);
+          if ((flags & RUN_ENDS) && !before) tc_commit(&acc_full[acc]);
         }
         __syncwarp();
-        if (flags & RUN_ENDS) ++run;
+        if ((flags & RUN_ENDS) && !before) ++run;
         if (flags & STEP_ENDS) next_stage();
       }
     } else {
-      const int quad = warp & 3, l = 32 * quad + lane;  // (a warp reads the tensor-memory lanes of its number modulo 4)
       for (int j = 0; j < m && alive; ++j) {
         const int adapter = part[j].z, flags = part[j].w;
         if (flags & RUN_BEGINS) before = (flags & FROM_BEFORE) != 0;
         if (!(flags & RUN_ENDS)) continue;
+        const bool goes_on = (flags & GOES_ON) != 0;
+        if (before) {  // (kept in tensor memory)
+          has_head = true;
+          if (l == 0) head_through = goes_on;
+          continue;
+        }
         const int acc = run & 1;
         alive = warp_wait(&acc_full[acc], (run / 2) & 1, g);
         if (!alive) break;
         tc_fence_after();
-        // to the gradient, or to shared memory for the cluster: head for a run from before, the ring (nothing uses it
-        // behind the last step) for one that begins here and goes on
-        const bool goes_on = (flags & GOES_ON) != 0;
-        unsigned char* keep = before ? head : goes_on ? smem : nullptr;
-        for (int cc = 0; cc < rp; cc += 32) {
+        // to the gradient, or, a run that goes on, to shared memory for the cluster
+        if (goes_on) {
+          keep(acc, tail);
+          if (l == 0) tail_adapter = adapter;
+        }
+        for (int cc = 0; cc < rp && !goes_on; cc += 32) {
           float v[32];
-          tmem_ld32(tmem + acc * acc_cols + ((uint32_t)(32 * quad) << 16) + cc, v);
-          if (keep) {
-#pragma unroll
-            for (int k = 0; k < 8; ++k)
-              if (cc + 4 * k < rp)
-                *reinterpret_cast<float4*>(keep + (((cc >> 2) + k) * TILE + l) * 16) =
-                    make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
-          } else if (c0 + l < C) {
+          sums(acc, cc, v);
+          if (c0 + l < C) {
             __nv_bfloat16* out = dP + ((size_t)adapter * r + cc) * C + c0 + l;
 #pragma unroll
             for (int k = 0; k < 32; k += 8)
@@ -843,10 +966,6 @@ __global__ void __launch_bounds__(WGRAD_THREADS) k_wgrad(const __grid_constant__
                 for (int q = 0; q < 8; ++q, out += C) *out = __float2bfloat16_rn(v[k + q]);
               }
           }
-        }
-        if (l == 0) {
-          if (before) head_through = goes_on;
-          if (!before && goes_on) tail_adapter = adapter;
         }
         tc_fence_before();
         __syncwarp();
@@ -863,6 +982,10 @@ __global__ void __launch_bounds__(WGRAD_THREADS) k_wgrad(const __grid_constant__
     if (elect_one()) tc_commit(&done);  // (the same lane is elected throughout: its commit covers all that was issued)
     __syncwarp();
     land_mma(&done, 0, g);
+  } else if (has_head) {
+    land_mma(&done, 0, g);
+    tc_fence_after();
+    keep(2, head);
   }
   __syncwarp();
   cluster_sync();
@@ -890,16 +1013,16 @@ __global__ void __launch_bounds__(WGRAD_THREADS) k_wgrad(const __grid_constant__
         }
       const int items = TILE * (r / 4);
       for (int k = threadIdx.x + rank * WGRAD_THREADS; k < items; k += WGRAD_THREADS * size) {
-        const int l = k % TILE, q = k / TILE;
-        const uint32_t at = (q * TILE + l) * 16;
+        const int column = k % TILE, q = k / TILE;
+        const uint32_t at = (q * TILE + column) * 16;
         float4 s = ld_cluster(mapa_shared(ring + at, c)), v[8];
 #pragma unroll
         for (int d = 1; d < 8; ++d)
           v[d] = (parts >> d) & 1 ? ld_cluster(mapa_shared(smem_u32(head) + at, d)) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
         for (int d = 1; d < 8; ++d) s.x += v[d].x, s.y += v[d].y, s.z += v[d].z, s.w += v[d].w;
-        if (c0 + l < C) {
-          __nv_bfloat16* out = dP + ((size_t)adapter[c] * r + 4 * q) * C + c0 + l;
+        if (c0 + column < C) {
+          __nv_bfloat16* out = dP + ((size_t)adapter[c] * r + 4 * q) * C + c0 + column;
           out[0] = __float2bfloat16_rn(s.x);
           out[(size_t)C] = __float2bfloat16_rn(s.y);
           out[(size_t)2 * C] = __float2bfloat16_rn(s.z);
@@ -912,7 +1035,7 @@ __global__ void __launch_bounds__(WGRAD_THREADS) k_wgrad(const __grid_constant__
   cluster_sync();  // (the others have read this CTA's sums)
   if (warp == 4) {
     tc_fence_after();
-    tmem_dealloc(tmem, 2 * acc_cols);
+    tmem_dealloc(tmem, 4 * acc_cols);
   }
 }
 
@@ -938,39 +1061,48 @@ constexpr int EXPAND_THREADS = 256;
 // while every unit has a CTA of its own (300 x 512: 13.1 us, twos 14.8).
 constexpr int expand_job(int64_t units, int ctas) { return units > ctas ? 2 : 1; }
 __host__ __device__ constexpr int expand_q(int rp) { return rp * 256; }
-// Units of base loaded ahead: where three CTAs' shared memory has room for it (ranks up to 16: 8192 x 7168 forward 73.2 us,
-// 74.0 without, backward 120 and 122; with rank 32 it would leave room for two: k_expand alone 46.7 against 45.2).
-__host__ __device__ constexpr int expand_ahead(int rp) { return rp <= 16 ? 1 : 0; }
+// h's second part: beside the first in shared memory up to rank 32, where three CTAs per SM have room for both; in tensor
+// memory above (two CTAs).
+__host__ __device__ constexpr bool expand_lo_in_tmem(int rp) { return rp > 32; }
+// Units of base loaded ahead: where it costs no CTA of an SM.
+__host__ __device__ constexpr int expand_ahead(int rp) { return rp > 32 && rp <= 64 ? 1 : 0; }
 constexpr int expand_bytes(int rp) {
-  return (1 + expand_ahead(rp)) * TILE * 256 + expand_q(rp) + TILE * rank_bytes(rp) + 1024;
+  return (1 + expand_ahead(rp)) * TILE * 256 + expand_q(rp) + (expand_lo_in_tmem(rp) ? 1 : 2) * TILE * rank_bytes(rp) + 1024;
+}
+constexpr int expand_most(bool lo_in_tmem) {  // for any rank of the kind
+  return !lo_in_tmem ? expand_bytes(32) : expand_bytes(64) > expand_bytes(MAX_R) ? expand_bytes(64) : expand_bytes(MAX_R);
 }
 
-__global__ void __launch_bounds__(EXPAND_THREADS, 3) k_expand(const __grid_constant__ CUtensorMap mh,
+template <bool LO_TMEM>
+__global__ void __launch_bounds__(EXPAND_THREADS, LO_TMEM ? 2 : 3) k_expand(const __grid_constant__ CUtensorMap mh,
                                                               const __grid_constant__ CUtensorMap mq,
                                                               const __grid_constant__ CUtensorMap mb,
                                                               const __grid_constant__ CUtensorMap my,
                                                               const __grid_constant__ CUtensorMap mb8,
                                                               const __grid_constant__ CUtensorMap my8,
-                                                              const __nv_bfloat16* base, int N, int r, int rp, int job,
-                                                              Plan plan, __nv_bfloat16* y, uint64_t limit_ns, int32_t* status) {
+                                                              const __nv_bfloat16* hs, const __nv_bfloat16* base, int N, int r,
+                                                              int rp, int job, Plan plan, int places, __nv_bfloat16* y,
+                                                              uint64_t limit_ns, int32_t* status) {
   extern __shared__ unsigned char smem_[];
   unsigned char* smem = aligned_smem(smem_);
-  __shared__ uint64_t rows_in[2], product_in, product_out;  // base's rows, h and Q in shared memory; the MMAs' end
+  __shared__ uint64_t rows_in[2], product_in, lo_in, product_out;  // base's rows, h and Q in place; the MMAs' end
   __shared__ int abort_, taken[2];  // (the numbers of the jobs behind the next one, by turns)
   __shared__ uint32_t tmem_;
   const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31, slab = warp & 3, block = warp >> 2;
-  const int ahead = expand_ahead(rp);
+  const int ahead = LO_TMEM ? expand_ahead(rp) : 0;
+  constexpr uint32_t tmem_columns = LO_TMEM ? 2 * TILE : TILE;
   const uint32_t at = smem_u32(smem), q_at = at + (1 + ahead) * (TILE * 256), h_at = q_at + expand_q(rp);
   if (threadIdx.x == 0) {
     mbar_init(&rows_in[0], 4 * 32);
     mbar_init(&rows_in[1], 4 * 32);
     mbar_init(&product_in, 1);
+    mbar_init(&lo_in, 4);
     mbar_init(&product_out, 1);
     abort_ = 0;
     fence_barrier_init();
   }
   if (warp == 4) {
-    tmem_alloc(&tmem_, TILE);
+    tmem_alloc(&tmem_, tmem_columns);
     tmem_relinquish();
   }
   wait_for_primary();
@@ -1062,13 +1194,37 @@ __global__ void __launch_bounds__(EXPAND_THREADS, 3) k_expand(const __grid_const
     if (!elect_one()) return;
     const int c0 = chunk * TILE;
     const bool two = c0 + 64 < N;  // (the second block of 64 columns has some)
-    mbar_arrive_expect_tx(&product_in, rp * 128 * (two ? 2 : 1) + (fresh ? TILE * rank_bytes(rp) : 0));
+    const uint32_t h_bytes = fresh ? (LO_TMEM ? 1 : 2) * TILE * rank_bytes(rp) : 0;
+    mbar_arrive_expect_tx(&product_in, rp * 128 * (two ? 2 : 1) + h_bytes);
     if (fresh) {
       tma_2d(h_at, &mh, &product_in, 0, p.start);
       if (rp > 64) tma_2d(h_at + TILE * 128, &mh, &product_in, 64, p.start);
+      if (!LO_TMEM) tma_2d(h_at + TILE * rank_bytes(rp), &mh, &product_in, 0, places + p.start);
     }
     tma_3d(q_at, &mq, &product_in, c0, 0, p.adapter);
     if (two) tma_3d(q_at + rp * 128, &mq, &product_in, c0 + 64, 0, p.adapter);
+  };
+
+  // h's second part to tensor memory, by warps 0 to 3, 64 elements at a time: read while another product is under way,
+  // stored when that is done (zeros past the rank, whose columns the product reads up to rp, and in places without a row)
+  uint4 lo[8];
+  auto read_lo = [&](const Part& p, int piece0) {
+    const uint4* src = reinterpret_cast<const uint4*>(hs + (size_t)(places + p.start + SLAB * slab + lane) * r);
+    const int pieces = p.s.row >= 0 ? r / 8 : 0;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) lo[k] = piece0 + k < pieces ? src[piece0 + k] : make_uint4(0, 0, 0, 0);
+  };
+  auto store_lo = [&](int piece0) { tmem_st32(tmem + TILE + ((uint32_t)(SLAB * slab) << 16) + 4 * piece0, &lo[0].x); };
+  auto rest_of_lo = [&](const Part& p) {
+    if (rp > 64) {
+      read_lo(p, 8);
+      store_lo(8);
+    }
+    tmem_wait_st();
+    tc_fence_before();
+    __syncwarp();
+    if (elect_one()) mbar_arrive(&lo_in);
+    __syncwarp();
   };
 
   Find found, behind;
@@ -1082,11 +1238,16 @@ __global__ void __launch_bounds__(EXPAND_THREADS, 3) k_expand(const __grid_const
   int products = 0, buf = 0;
   // the parities of what has been waited for, and of what has been issued: rows by buffer, a bit each (issued by warps 0
   // to 3); products (warp 6) and MMAs (warp 4)
-  uint32_t rows_waited = 0, rows_issued = 0, issued = 0;
+  uint32_t rows_waited = 0, rows_issued = 0, issued = 0, los = 0;  // (los: second parts that warp 4 has waited for)
   if (more) {
     if (warp < 4) load_rows(now, chunk, 0), rows_issued = 1;
     if (warp == 6 && now.adapter >= 0) load_product(now, chunk, true), issued = 1;
     __syncwarp();
+    if (LO_TMEM && warp < 4 && now.adapter >= 0) {
+      read_lo(now, 0);
+      store_lo(0);
+      rest_of_lo(now);
+    }
   }
   while (more) {
     const bool last = chunk + 1 == now.end;  // of this job
@@ -1096,16 +1257,26 @@ __global__ void __launch_bounds__(EXPAND_THREADS, 3) k_expand(const __grid_const
     if (warp == 7 && lane == 0 && first && next.end > 0) taken[done & 1] = take();
     if (last && !first) find_tile(found, next.end > 0 ? taken[done & 1] : 0x7FFFFFFF);
     if (ahead && another && warp < 4) load_rows(last ? next : now, next_chunk, buf ^ 1), rows_issued ^= 2 >> buf;
+    const bool fresh_lo = LO_TMEM && last && another && warp < 4 && next.adapter >= 0;
+    if (fresh_lo) read_lo(next, 0);
     bool ok = true;
     if (product) {
       if (warp == 4) {
-        const bool in = warp_wait(&product_in, products & 1, g);
+        bool in = warp_wait(&product_in, products & 1, g);
+        if (LO_TMEM && first) in = warp_wait(&lo_in, los++ & 1, g) && in;
         tc_fence_after();
         const uint64_t h = sdesc_kmajor(h_at, hrow), q = sdesc_mnmajor(q_at, 128, rp * 128);
         if (in && elect_one()) {  // (if not, the others' wait for the product ends by the abort flag)
 #pragma unroll
           for (int k = 0; k < MAX_R / 16; ++k)
-            if (16 * k < rp) umma_bf16(tmem, h + ((k >> 2) * (TILE * 128) + 32 * (k & 3)) / 16, q + (2048 >> 4) * k, idesc, k > 0);
+            if (16 * k < rp) {
+              const uint64_t a = h + ((k >> 2) * (TILE * 128) + 32 * (k & 3)) / 16;
+              umma_bf16(tmem, a, q + (2048 >> 4) * k, idesc, k > 0);
+              if (LO_TMEM)
+                umma_bf16_from_tmem(tmem, tmem + TILE + 8 * k, q + (2048 >> 4) * k, idesc);
+              else
+                umma_bf16(tmem, a + TILE * rank_bytes(rp) / 16, q + (2048 >> 4) * k, idesc, 1u);
+            }
           tc_commit(&product_out);
         }
         issued ^= in;
@@ -1116,8 +1287,15 @@ __global__ void __launch_bounds__(EXPAND_THREADS, 3) k_expand(const __grid_const
     }
     // (h and Q have been read: the next unit's may come)
     ok = __all_sync(0xFFFFFFFFu, ok);
-    if (warp == 6 && ok && another && (last ? next : now).adapter >= 0) load_product(last ? next : now, next_chunk, last), issued ^= 1;
+    if (warp == 6 && ok && another && (last ? next : now).adapter >= 0) {
+      load_product(last ? next : now, next_chunk, last);
+      issued ^= 1;
+    }
     __syncwarp();
+    if (fresh_lo) {
+      tc_fence_after();
+      store_lo(0);
+    }
     if (last && !first) find_row(found);
     ok &= wait_on(&rows_in[buf], (rows_waited >> buf) & 1, g);
     rows_waited ^= 1 << buf;
@@ -1184,6 +1362,7 @@ __global__ void __launch_bounds__(EXPAND_THREADS, 3) k_expand(const __grid_const
     }
     more = another;
     if (!ahead && another && warp < 4) load_rows(now, chunk, 0), rows_issued ^= 1;
+    if (fresh_lo) rest_of_lo(now);
     if (ahead) buf ^= 1;
   }
   cp_wait<0>();
@@ -1199,7 +1378,7 @@ __global__ void __launch_bounds__(EXPAND_THREADS, 3) k_expand(const __grid_const
   __syncthreads();
   if (warp == 4) {
     tc_fence_after();
-    tmem_dealloc(tmem, TILE);
+    tmem_dealloc(tmem, tmem_columns);
   }
 }
 
@@ -1539,7 +1718,7 @@ moe_status_t shrink(const moe_bf16* x, const moe_bf16* P, const float* scale, in
   CUtensorMap mx, mp;
   if (!map_rows(&mx, x, T, K, 64, SLAB) || !map_weight(&mp, P, G, r, K, rp)) return MOE_ERR_CUDA;
   return launch(k_shrink, tiles * split, split, SHRINK_THREADS, bytes, shrink_bytes(MAX_R), true, s, mx, mp, in(x), scale, K,
-                r, rp, p, out(h), out(hs), in(other), out(others), g_wait_limit_ns.load(), st);
+                r, rp, p, places(T, G), out(h), out(hs), in(other), out(others), g_wait_limit_ns.load(), st);
 }
 
 moe_status_t wgrad(const moe_bf16* x, const moe_bf16* us, int K, moe_bf16* dA, const moe_bf16* dy, const moe_bf16* hs, int N,
@@ -1551,7 +1730,7 @@ moe_status_t wgrad(const moe_bf16* x, const moe_bf16* us, int K, moe_bf16* dA, c
     d.dP = out(dP);
     d.C = C;
     d.units = (C + TILE - 1) / TILE;
-    return map_rows(&d.mx, X, T, C, 64, SLAB) && map_rows(&d.mu, U, places(T, G), r, rank_cols(rp), TILE);
+    return map_rows(&d.mx, X, T, C, 64, SLAB) && map_rows(&d.mu, U, (U == us ? 2 : 1) * places(T, G), r, rank_cols(rp), TILE);
   };
   if (!fill(sides.of[0], x, us, K, dA) || !fill(sides.of[1], dy, hs, N, dB)) return MOE_ERR_CUDA;
   const int units = sides.of[0].units + sides.of[1].units;
@@ -1562,8 +1741,10 @@ moe_status_t wgrad(const moe_bf16* x, const moe_bf16* us, int K, moe_bf16* dA, c
   // A programmatic dependent where both kernels' CTAs find an SM each (300 x 256 x 512 backward 19.8 us, 20.6 without).  With
   // more, its first clusters took places as k_shrink left them, unevenly (8192 x 7168 154 us, 136 without).
   const bool dependent = max_tiles(T, G) * shrink_split(T, N, r, G) + units * split <= sm_count();
-  return launch(k_wgrad, units * split, split, WGRAD_THREADS, bytes, wgrad_bytes(MAX_R), dependent, s, sides, r, rp, G, p,
-                g_wait_limit_ns.load(), st);
+  // (8192 x 7168 with 8 adapters of rank 64 61.8 us with BESIDE, 66.2 without; 512 rows of 64 adapters 69 and 58)
+  const bool beside = rp <= 64 && T >= 64 * (int64_t)G;
+  return launch(beside ? k_wgrad<true> : k_wgrad<false>, units * split, split, WGRAD_THREADS, bytes, wgrad_bytes(MAX_R),
+                dependent, s, sides, r, rp, G, p, places(T, G), g_wait_limit_ns.load(), st);
 }
 
 moe_status_t expand(const moe_bf16* hs, const moe_bf16* Q, const moe_bf16* base, int T, int N, int r, int G, const Plan& p,
@@ -1574,12 +1755,13 @@ moe_status_t expand(const moe_bf16* hs, const moe_bf16* Q, const moe_bf16* base,
   const int per_sm = 228 * 1024 / (bytes + 2048) < 3 ? 228 * 1024 / (bytes + 2048) : 3;  // (registers: three)
   const int grid = units < sms * per_sm ? (int)units : sms * per_sm, job = expand_job(units, grid);
   CUtensorMap mh, mq, mb, my, mb8, my8;
-  if (!map_rows(&mh, hs, places(T, G), r, rank_cols(rp), TILE) || !map_weight(&mq, Q, G, r, N, rp) ||
+  if (!map_rows(&mh, hs, 2 * places(T, G), r, rank_cols(rp), TILE) || !map_weight(&mq, Q, G, r, N, rp) ||
       !map_rows(&mb, base ? base : y, T, N, 64, SLAB) || !map_rows(&my, y, T, N, 64, SLAB) ||
       !map_rows(&mb8, base ? base : y, T, N, 64, 8) || !map_rows(&my8, y, T, N, 64, 8))
     return MOE_ERR_CUDA;
-  return launch(k_expand, grid, 0, EXPAND_THREADS, bytes, expand_bytes(MAX_R), true, s, mh, mq, mb, my, mb8, my8, in(base), N, r, rp, job, p,
-                out(y), g_wait_limit_ns.load(), st);
+  const bool lo = expand_lo_in_tmem(rp);
+  return launch(lo ? k_expand<true> : k_expand<false>, grid, 0, EXPAND_THREADS, bytes, expand_most(lo), true, s, mh, mq, mb,
+                my, mb8, my8, in(hs), in(base), N, r, rp, job, p, places(T, G), out(y), g_wait_limit_ns.load(), st);
 }
 
 moe_status_t rows_launch(const moe_bf16* x, const moe_bf16* P, const moe_bf16* Q, const int32_t* idx, const float* scale,
@@ -1616,12 +1798,12 @@ using namespace moeglu;
 using namespace moeglu::lora;
 
 extern "C" size_t moe_lora_fwd_workspace_size(int T, int r, int G) {
-  return T <= 0 || r <= 0 || G <= 0 || few_rows(T, r) ? 0 : plan_bytes(T, G) + sorted_bytes(T, r, G);
+  return T <= 0 || r <= 0 || G <= 0 || few_rows(T, r) ? 0 : plan_bytes(T, G) + sorted_bytes(T, 2 * r, G);
 }
 
 extern "C" size_t moe_lora_bwd_workspace_size(int T, int r, int G) {
   if (T <= 0 || r <= 0 || G <= 0) return 0;
-  return few_grads(T, r, G) ? up256((size_t)T * r * 4) : plan_bytes(T, G) + 2 * sorted_bytes(T, r, G);
+  return few_grads(T, r, G) ? up256((size_t)T * r * 4) : plan_bytes(T, G) + sorted_bytes(T, 2 * r, G) + sorted_bytes(T, r, G);
 }
 
 extern "C" moe_status_t moe_lora_fwd(const moe_bf16* x, const moe_bf16* A, const moe_bf16* B, const int32_t* idx,
@@ -1683,7 +1865,7 @@ extern "C" moe_status_t moe_lora_bwd(const moe_bf16* dy, const moe_bf16* x, cons
   }
   const Plan p = plan_at(ws, T, G);
   auto* us = reinterpret_cast<moe_bf16*>(static_cast<char*>(ws) + plan_bytes(T, G));
-  auto* hs = us + sorted_bytes(T, r, G) / 2;
+  auto* hs = us + sorted_bytes(T, 2 * r, G) / 2;
   if (const moe_status_t e = group(idx, T, G, p, s)) return e;
   if (const moe_status_t e = shrink(dy, B, scale, T, N, r, G, p, nullptr, us, h, hs, status, s)) return e;
   // (the gradients next, while part of dy is in L2; k_expand, whose jobs any CTA takes, then fills the SMs that they leave:

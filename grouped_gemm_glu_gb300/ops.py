@@ -855,8 +855,10 @@ def lora(x, A, B, idx, scale, base=None, out=None, with_h: bool = True, status=N
     h = scale[a] (A_a x) and y = base + B_a^T h.  A [G, r, K] and B [G, r, N]
     bf16, scale [G] f32, base [T, N] bf16 the projection's output (None: zero),
     out where y goes (may be base).  Returns y [T, N] and, with_h, h [T, r] bf16,
-    which lora_bwd reads.  The same call gives the same bits; a row's last bit may
-    differ with the number of rows beside it (the sums' order follows from T)."""
+    which lora_bwd reads.  y is formed from h with 16 bits at least, not from the
+    returned bf16 h, and rounded once.  The same call gives the same bits; with
+    another number of rows beside it a row may differ by what fp32 sums and those
+    16 bits leave (a last bit, or more where base and the product cancel)."""
     T, K, N, r, G = _lora_args(x, A, B, idx, scale, ((base, "N", "base"), (out, "N", "out")))
     bf, dev, lib = torch.bfloat16, x.device, L.load()
     y = out if out is not None else torch.empty(T, N, dtype=bf, device=dev)
@@ -871,7 +873,8 @@ def lora(x, A, B, idx, scale, base=None, out=None, with_h: bool = True, status=N
 def lora_bwd(dy, x, h, A, B, idx, scale, base=None, out=None, status=None):
     """Backward of lora: (dx [T, K], dA [G, r, K], dB [G, r, N]) bf16 from dy
     [T, N] and the forward's x and h.  base [T, K] is the gradient that reaches x
-    elsewhere, added to dx (None: zero); out where dx goes (may be base)."""
+    elsewhere, added to dx (None: zero); out where dx goes (may be base).  dA and
+    dB are those of one call, whole: adapters without rows get zeros."""
     T, K, N, r, G = _lora_args(x, A, B, idx, scale, ((dy, "N", "dy"), (h, "r", "h"), (base, "K", "base"), (out, "K", "out")))
     if dy is None or h is None:
         raise ValueError("dy, h: CUDA tensors are needed")

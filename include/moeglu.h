@@ -725,24 +725,28 @@ MOE_API size_t moe_lora_bwd_workspace_size(int T, int r, int G);
 
 /* For every row t of x [T][K] with adapter a = idx[t] (int32; rows whose
  * index lies outside [0, G) have none):
- *   h = bf16(scale[a] A_a x)            [T][r], zero without an adapter
- *   y = bf16(base + B_a^T h)            [T][N], base alone without an adapter (for few rows from h before its rounding)
+ *   h = scale[a] A_a x                  [T][r], zero without an adapter
+ *   y = bf16(base + B_a^T h)            [T][N], base's bits without an adapter
  * A [G][r][K], B [G][r][N], all bf16; scale [G] f32; base [T][N] bf16 the
  * shared projection's output (NULL: zero; may be y itself); h (nullable) is
- * kept for the backward.  Adapters of different ranks share a call with zero
- * rows up to the largest.  Rows may come in any order of adapters.  The same
- * inputs give the same bits; the order of a row's sums follows from T and r.
- * K, N and r multiples of 8, K and N at most 2^20, r <= 128 and G <= 32767
- * (else MOE_ERR_UNSUPPORTED); bf16 buffers 16-byte, ws
- * (moe_lora_fwd_workspace_size bytes) 256-byte aligned; y and h overlap no input
- * (but y an identical base) nor one another.  status (nullable) receives MOE_ERR_TIMEOUT from a pipeline
- * wait that gave up.  T == 0 launches nothing. */
+ * bf16(h), kept for the backward; y takes it with 16 bits at least.  Sums are
+ * fp32.  Adapters of different ranks share a call with zero rows up to the
+ * largest.  Rows may come in any order of adapters.  The same inputs give the
+ * same bits; the order of a row's sums follows from T and r.  What an infinity or
+ * a NaN in a row or an adapter makes infinite or NaN stays with that row and
+ * adapter (an infinity in B may come out as NaN).
+ * T at most 2^27, K, N and r multiples of 8, K and N at most 2^20 (else
+ * MOE_ERR_ARG), r <= 128 and G <= 32767 (else MOE_ERR_UNSUPPORTED); bf16 buffers
+ * 16-byte, ws (moe_lora_fwd_workspace_size bytes) 256-byte aligned; y and h
+ * overlap no input (but y an identical base) nor one another.  status (nullable)
+ * receives MOE_ERR_TIMEOUT from a pipeline wait that gave up.  T == 0 launches
+ * nothing. */
 MOE_API moe_status_t moe_lora_fwd(const moe_bf16* x, const moe_bf16* A, const moe_bf16* B, const int32_t* idx,
                                   const float* scale, const moe_bf16* base, int T, int K, int N, int r, int G, moe_bf16* y,
                                   moe_bf16* h, void* ws, size_t ws_bytes, int32_t* status, moe_stream_t stream);
 
 /* Backward of moe_lora_fwd for dy [T][N]; x, h, A, B, idx and scale as there:
- *   u = bf16(scale[a] B_a dy) (few rows: not rounded),  dx = bf16(base + A_a^T u)   [T][K]
+ *   u = scale[a] B_a dy (16 bits at least),  dx = bf16(base + A_a^T u)   [T][K]
  *   dA_a = bf16(sum over a's rows of u x^T) [r][K],  dB_a = bf16(sum of h dy^T) [r][N]
  * base [T][K] (NULL: zero; may be dx itself) is the gradient that reaches x
  * elsewhere.  dA and dB are written whole (zero for adapters without rows) and
