@@ -80,9 +80,6 @@ __device__ __forceinline__ uint32_t mix(uint32_t x) {  // a 32-bit hash: two mul
   return x ^ (x >> 16);
 }
 
-__device__ __forceinline__ void wait_for_primary() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-__device__ __forceinline__ void launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
-
 // ---------------------------------------------------------------------------
 // Loads and stores of PER consecutive elements: whole vectors where the
 // address allows, element by element at a tensor's end or off alignment.
@@ -559,22 +556,6 @@ bool valid(const moe_adamw_tensor_t* t, int n, int state8) {
   return chunks < ((size_t)1 << 31);
 }
 
-template <class... A, class... B>
-moe_status_t launch(void (*k)(A...), int ctas, int threads, bool dependent, cudaStream_t stream, const B&... args) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(ctas);
-  cfg.blockDim = dim3(threads);
-  cfg.stream = stream;
-  cudaLaunchAttribute attr;
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = dependent ? 1 : 0;
-  if (cudaLaunchKernelEx(&cfg, k, static_cast<A>(args)...) != cudaSuccess) return MOE_ERR_CUDA;
-  count_launch();
-  return launch_status();
-}
-
 // Tensors [first, first + count) as one launch each of the norm's part
 // (parts != null) or of the step.
 template <int N>
@@ -583,12 +564,12 @@ moe_status_t launch_group(const moe_adamw_tensor_t* dev, const Entry* table, uin
                           bool behind_scalars, cudaStream_t stream) {
   Grads<N> g;
   for (int i = 0; i < count; ++i) g.p[i] = grads[first + i];
-  if (parts) return launch(k_adamw_norm<N>, n_parts, THREADS, false, stream, g, dev, table, chunks, first, parts);
+  if (parts) return launch_kernel(k_adamw_norm<N>, n_parts, 0, THREADS, 0, false, stream, g, dev, table, chunks, first, parts);
   const auto k = state8 ? k_adamw_step<N, true> : k_adamw_step<N, false>;
   const int per_sm = max_active_blocks((const void*)k, THREADS, 0), sms = sm_count();
   if (per_sm < 1 || sms < 1) return MOE_ERR_CUDA;
   const uint32_t most = per_sm * sms;
-  return launch(k, chunks < most ? chunks : most, THREADS, behind_scalars, stream, g, dev, table, chunks, first, sc);
+  return launch_kernel(k, chunks < most ? chunks : most, 0, THREADS, 0, behind_scalars, stream, g, dev, table, chunks, first, sc);
 }
 
 int parts_of(uint32_t chunks) {
@@ -666,8 +647,8 @@ extern "C" moe_status_t moe_adamw_step(const moe_adamw_tensor_t* tensors, const 
       c1.a2f = (float)c1.a2;
       c1.eps = (float)p->eps;
       const auto ln = [](double b) { return b > 0.0 ? std::log(b) : -1e9; };  // (of 0: a power of 0)
-      if (const moe_status_t e = launch(k_adamw_scalars, 1, p->max_norm > 0.0 ? 256 : 32, pass0, stream, c1, p->max_norm,
-                                        ln(p->beta1), ln(p->beta2), p->seed, lr, t, parts, n_parts, norm, sc))
+      if (const moe_status_t e = launch_kernel(k_adamw_scalars, 1, 0, p->max_norm > 0.0 ? 256 : 32, 0, pass0, stream, c1,
+                                               p->max_norm, ln(p->beta1), ln(p->beta2), p->seed, lr, t, parts, n_parts, norm, sc))
         return e;
     }
     const Entry* at = table;

@@ -258,9 +258,6 @@ __device__ __forceinline__ int build_rows(const Args& a, const Rows& r) {
   return end_row;
 }
 
-__device__ __forceinline__ void launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
-__device__ __forceinline__ void wait_for_primary() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-
 __device__ __forceinline__ void warp_pair_sync(int id) { asm volatile("bar.sync %0, 64;" ::"r"(id) : "memory"); }
 
 // Whether ok holds in both warps of a pair (which both call this).

@@ -86,4 +86,34 @@ inline moe_status_t launch_status() {
   return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
+// Launches k with its arguments: in clusters of so many CTAs (0: none), as a
+// programmatic dependent of the launch in front of it or not.
+template <class... A, class... B>
+moe_status_t launch_kernel(void (*k)(A...), dim3 ctas, int cluster, int threads, int smem, bool dependent, cudaStream_t stream,
+                           const B&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = ctas;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  int n = 0;
+  if (cluster > 0) {
+    attr[n].id = cudaLaunchAttributeClusterDimension;
+    attr[n].val.clusterDim.x = cluster;
+    attr[n].val.clusterDim.y = attr[n].val.clusterDim.z = 1;
+    ++n;
+  }
+  if (dependent) {
+    attr[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[n].val.programmaticStreamSerializationAllowed = 1;
+    ++n;
+  }
+  cfg.attrs = attr;
+  cfg.numAttrs = n;
+  if (cudaLaunchKernelEx(&cfg, k, static_cast<A>(args)...) != cudaSuccess) return MOE_ERR_CUDA;
+  count_launch();
+  return launch_status();
+}
+
 }  // namespace moeglu

@@ -134,9 +134,6 @@ __device__ __forceinline__ uint64_t sdesc_mnmajor(uint32_t saddr, uint32_t row_b
 }
 constexpr uint32_t A_MN = 1u << 15, B_MN = 1u << 16;  // instruction descriptor: that operand lies across the contraction
 
-__device__ __forceinline__ void wait_for_primary() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-__device__ __forceinline__ void launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
-
 // 32 columns of the thread's lane of tensor memory, written; and the MMA whose
 // left operand lies there (a row per lane, two elements per column).
 __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t* r) {
@@ -1646,29 +1643,7 @@ moe_status_t launch(void (*k)(A...), dim3 ctas, int cluster, int threads, int sm
   // (one limit per kernel)
   if (smem_limit && (!set_smem_limit((const void*)k, smem_limit) || !prefer_shared((const void*)k))) return MOE_ERR_CUDA;
   if (cluster > 8 && !allow_large_clusters((const void*)k)) return MOE_ERR_CUDA;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = ctas;
-  cfg.blockDim = dim3(threads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[2];
-  int n = 0;
-  if (cluster > 0) {
-    attr[n].id = cudaLaunchAttributeClusterDimension;
-    attr[n].val.clusterDim.x = cluster;
-    attr[n].val.clusterDim.y = attr[n].val.clusterDim.z = 1;
-    ++n;
-  }
-  if (dependent) {
-    attr[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[n].val.programmaticStreamSerializationAllowed = 1;
-    ++n;
-  }
-  cfg.attrs = attr;
-  cfg.numAttrs = n;
-  if (cudaLaunchKernelEx(&cfg, k, static_cast<A>(args)...) != cudaSuccess) return MOE_ERR_CUDA;
-  count_launch();
-  return launch_status();
+  return launch_kernel(k, ctas, cluster, threads, smem, dependent, stream, args...);
 }
 
 using bf = __nv_bfloat16;

@@ -165,7 +165,7 @@ __device__ __forceinline__ float soft_score(const Soft& s, float x) { return exp
 // overlaps with this one up to here (programmatic dependent launch).
 __device__ __forceinline__ void flush_load(const int32_t* hist, int n, int32_t* load) {
   __syncthreads();
-  if (gridDim.x > 1) asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (gridDim.x > 1) wait_for_primary();
   for (int e = threadIdx.x; e < n; e += blockDim.x) {
     if (gridDim.x == 1)
       load[e] = hist[e];
@@ -174,7 +174,7 @@ __device__ __forceinline__ void flush_load(const int32_t* hist, int n, int32_t* 
   }
 }
 __global__ void k_router_clear(int32_t* __restrict__ load, int n) {
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  launch_dependents();
   for (int e = threadIdx.x; e < n; e += blockDim.x) load[e] = 0;
 }
 
