@@ -33,7 +33,10 @@ from .optim import AdamW
 class Adapters:
     """G low-rank adapters of rank r beside the experts: A and B [G, r, H] bf16,
     scale [G] f32 (alpha / r, often).  Adapters of lower ranks are padded with
-    zero rows.  A freshly made adapter has a zero B."""
+    zero rows.  A freshly made adapter has a zero B.  Forward and backward keep
+    them apart; an optimizer over them does not: A and B are one tensor each, so
+    that adapters without rows in a batch decay and move by their momentum as well,
+    and max_norm scales all by one norm."""
 
     def __init__(self, A, B, scale):
         bf = torch.bfloat16
@@ -141,7 +144,10 @@ class MoeBlock:
         ("adapters") or both ("all"), which update then steps; gamma and the
         bias do not decay.  The weights are updated where they are: gamma, Wr, W2,
         the adapters, and the layer's packed copies of W1 and b1 (layer.W1p,
-        layer.b1p; ops.repack_fc1(..., inverse=True) gives the plain rows)."""
+        layer.b1p; ops.repack_fc1(..., inverse=True) gives the plain rows).
+        max_norm: by the norm over this block's tensors, in a shard of the experts
+        over that shard's alone: gamma and Wr, which every shard has, would then
+        part.  Shards leave max_norm out."""
         if train not in ("all", "block", "adapters"):
             raise ValueError(f'train: "all", "block" or "adapters" is needed, got {train!r}')
         if train == "adapters" and self.adapters is None:

@@ -72,7 +72,9 @@ struct Scalars : Short {
 // the workspace: the scalars, then the norm's partial sums
 constexpr size_t PARTS_AT = 256;
 
-__device__ __forceinline__ uint32_t mix(uint32_t x) {  // a 32-bit hash: two multiplications
+// A published 32-bit hash of two multiplications (shifts and factors are those of
+// Wellons' "lowbias32"); the header states it, callers may form the bits themselves.
+__device__ __forceinline__ uint32_t mix(uint32_t x) {
   x ^= x >> 16;
   x *= 0x7FEB352Du;
   x ^= x >> 15;

@@ -1,5 +1,6 @@
-"""The weights' update: AdamW over many tensors in one launch, with moments in
-32 or in 8 bits and optional clipping by the gradients' global norm.
+"""The weights' update: AdamW over many tensors at once, with moments in 32 or
+in 8 bits and optional clipping by the gradients' global norm: two launches a
+step, three with clipping, for up to 4000 tensors.
 
   opt = AdamW(weights, lr=3e-4, weight_decay=0.1, max_norm=1.0, state="mxfp8")
   norm = opt.step(grads)
@@ -25,16 +26,25 @@ class AdamW:
                  state: str = "f32", grad_dtype=None, seed: int = 0):
         """weights: contiguous CUDA tensors of one device, float32 or bfloat16,
         updated in place (parameters that require gradients too: the step is no
-        part of what autograd records); a bfloat16 weight gets an f32 master here, which the
-        step updates and rounds.  weight_decay: one number, or one per tensor.
-        max_norm: the gradients of a step are scaled down together to this
-        2-norm; a step whose norm is not finite changes nothing.  state: "f32"
-        keeps m and v, "mxfp8" keeps m and sqrt(v) as E4M3 codes with a scale
-        per 32 elements, rounded up or down by random bits that seed starts.
-        grad_dtype: one type or one per tensor (default: the weight's).
+        part of what autograd records); a bfloat16 weight gets an f32 master here,
+        which the step updates and rounds.  weight_decay: one number, or one per
+        tensor.  max_norm: the gradients of a step are scaled down together to this
+        2-norm, which is taken over this object's tensors alone: shards of one
+        model that clip by max_norm each clip by their own norm, and what they hold
+        copies of drifts apart; a step whose norm is not finite changes nothing.
+        state: "f32" keeps m and v, "mxfp8" keeps m and sqrt(v) as E4M3 codes with a
+        scale per 32 elements, rounded up or down by random bits that seed starts:
+        right on average, but under normal gradients of a steady size the held
+        sqrt(v) spreads by 12% (b2 = 0.95) to 15% (0.999) around the 32-bit one, the
+        farthest of 65,536 elements to 0.55 and 1.8 of it.  grad_dtype: one type or one per tensor (default: the
+        weight's).
+        Every weight takes part in every step: zero gradients still decay it and
+        move it by its momentum.
         A weight keeps its memory for as long as this object lives: one that is
-        given another (w.data = ...) is no longer updated, by a step or a load.  Steps of one object
-        share their state and workspace and follow one another.
+        given another (w.data = ...) is no longer updated, by a step or a load.
+        Steps of one object share their state and workspace and follow one another.
+        Made once per set of weights: masters and addresses of a few hundred
+        tensors take some milliseconds.
 
         Flat state, one stretch per tensor from a multiple of 32 on: m and v
         (float32, or uint8 codes with scales ms and vs), master (float32, where

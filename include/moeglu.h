@@ -734,7 +734,7 @@ MOE_API size_t moe_lora_bwd_workspace_size(int T, int r, int G);
  * largest.  Rows may come in any order of adapters.  The same inputs give the
  * same bits; the order of a row's sums follows from T and r.  What an infinity or
  * a NaN in a row or an adapter makes infinite or NaN stays with that row and
- * adapter (an infinity in B may come out as NaN).
+ * adapter (an infinity in B, or in x for dA, may come out as NaN).
  * T at most 2^27, K, N and r multiples of 8, K and N at most 2^20 (else
  * MOE_ERR_ARG), r <= 128 and G <= 32767 (else MOE_ERR_UNSUPPORTED); bf16 buffers
  * 16-byte, ws (moe_lora_fwd_workspace_size bytes) 256-byte aligned; y and h
@@ -804,7 +804,7 @@ MOE_API size_t moe_adamw_workspace_size(int n);
  *   t += 1;  c = min(1, max_norm / (|g| + 1e-6)) (c = 1 without max_norm), g' = c g
  *   m = b1 m + (1 - b1) g',  v = b2 v + (1 - b2) g'^2
  *   w = w (1 - lr wd) - lr (m / (1 - b1^t)) / (sqrt(v / (1 - b2^t)) + eps)
- * |g| is the 2-norm over all tensors, its squares added in fp32 by eights and
+ * |g| is the 2-norm over this call's tensors (not over other ranks'), its squares added in fp32 by eights and
  * these sums exactly (sums of squares past fp32's range count as infinite: one
  * gradient past 1.8e19, thousands past 1e17; squares below 2^-126 lose bits,
  * those below 2^-149 count as 0).  8-bit
@@ -833,7 +833,7 @@ MOE_API moe_status_t moe_get_status(const int32_t* status, int32_t* host_out, mo
 
 /* Pipeline wait limit in nanoseconds for the persistent GEMMs and the adapters'
  * kernels (default 2e9); after it a wait gives up, sets MOE_ERR_TIMEOUT and the
- * kernel returns, once its copies and MMAs under way have landed. */
+ * kernel returns. */
 MOE_API void moe_set_wait_limit_ns(uint64_t ns);
 
 /* Self-test of the bounded wait behind every pipeline wait of the
