@@ -32,11 +32,11 @@
 // Few rows (decoding) take k_rows instead: one cluster per row, one launch; in
 // the backward k_row_grads behind it.
 //
-// Measured: 8192 x 7168 with 32 adapters of rank 16, forward 73 us (grouping 6;
-// k_shrink 24, 117 MB at 4.9 TB/s, where a kernel that only loads them takes 21;
-// k_expand 43, 235 MB at 5.5 TB/s, where a plain copy takes 38 to 40); with 8 of
-// rank 32, backward 122 us (k_wgrad 48 for both gradients, 4.9 TB/s); one row
-// of 2880 4 us, 64 rows of 7168 with 64 adapters 8.2 us.
+// Measured, calls that follow one another: 8192 x 7168 with 32 adapters of rank
+// 16, forward 73.5 us (grouping 6; k_shrink 24, 117 MB at 4.9 TB/s, where a kernel
+// that only loads them takes 21; k_expand 43, 235 MB at 5.5 TB/s, where a plain
+// copy takes 38 to 40); with 8 of rank 32, backward 123 us (k_wgrad 48 for both
+// gradients, 4.9 TB/s); one row of 2880 4 us, 64 rows of 7168 with 64 adapters 8.2.
 #include "common.cuh"
 #include "host_common.h"
 
@@ -396,8 +396,8 @@ __global__ void __launch_bounds__(GROUP_THREADS) k_group(const int32_t* __restri
 // and write out, warp 4 issues the MMAs.
 // ---------------------------------------------------------------------------
 constexpr int SHRINK_THREADS = 160;
-// (4500 x 2880 x 5760 with rank 64 38.9 us, with three stages 40.2; 512 rows of 64 adapters 37.7 and 39.6; ranks 16 and 32 at
-// 8192 x 7168 within 1%; rank 128, whose stages are larger, 94.1 and 90.5)
+// (4500 x 2880 x 5760 with rank 64 40.7 us, with three stages 41.2; 512 rows of 64 adapters of rank 16 39.0 and 41.0; ranks
+// 16 and 32 at 8192 x 7168 within 1%; rank 128, whose stages are larger, 100.0 and 95.9)
 __host__ __device__ constexpr int shrink_stages(int rp) { return rp <= 64 ? 4 : 3; }
 __host__ __device__ constexpr int shrink_stage(int rp) { return TILE * 128 + rp * 128; }
 constexpr int shrink_bytes(int rp) {  // (the ring holds the sums in the end: 512 rp bytes)
@@ -1053,15 +1053,18 @@ __device__ __forceinline__ uint32_t plus(uint32_t b, float x, float y) {
   return pack_bf16x2(s.x, s.y);
 }
 constexpr int EXPAND_THREADS = 256;
-// Units in a job: two share the tile's h and its rows' numbers; forward of 8192 x 7168 with rank 16 72.6 us, one by one
-// 73.2, threes 73.5; 4500 x 2880 x 5760 with rank 64 40.1, 40.4, 42.9; 512 rows of 64 adapters 41.3, 44.3, 42.8.  Ones
-// while every unit has a CTA of its own (300 x 512: 13.1 us, twos 14.8).
+// Units in a job: two share the tile's h and its rows' numbers; forward of 8192 x 7168 with rank 16 73.8 us, one by one
+// 75.8, threes 74.6; rank 128 95.9, 108.7, 96.3; 4500 x 2880 x 5760 with rank 64 40.7, 43.5, 39.8; 512 rows of 64 adapters
+// of rank 16 39.0, 45.8, 38.2.  Ones while every unit has a CTA of its own (300 x 512: 14.2 us, twos 15.6).
 constexpr int expand_job(int64_t units, int ctas) { return units > ctas ? 2 : 1; }
 __host__ __device__ constexpr int expand_q(int rp) { return rp * 256; }
 // h's second part: beside the first in shared memory up to rank 32, where three CTAs per SM have room for both; in tensor
-// memory above (two CTAs).
+// memory above, from where the MMA takes it (two CTAs per SM; in shared memory two and one: 4500 x 2880 x 5760 with rank 64
+// 43.5 us, so 40.7; 8192 x 7168 with rank 128 111.6 and 95.9; rank 32 in tensor memory 74.2, so 75.1, but 512 rows of 64
+// adapters 45.2 and 39.1).
 __host__ __device__ constexpr bool expand_lo_in_tmem(int rp) { return rp > 32; }
-// Units of base loaded ahead: where it costs no CTA of an SM.
+// Units of base loaded ahead: where it costs no CTA of an SM (rank 64 at 8192 x 7168 80.8 us, 85.6 without; with rank 16,
+// where it would cost the third CTA, 72.4 against 73.6, but 512 rows of 64 adapters 43.0 against 38.9).
 __host__ __device__ constexpr int expand_ahead(int rp) { return rp > 32 && rp <= 64 ? 1 : 0; }
 constexpr int expand_bytes(int rp) {
   return (1 + expand_ahead(rp)) * TILE * 256 + expand_q(rp) + (expand_lo_in_tmem(rp) ? 1 : 2) * TILE * rank_bytes(rp) + 1024;
@@ -1583,9 +1586,14 @@ __global__ void __launch_bounds__(GRAD_THREADS, 8) k_row_grads(const __nv_bfloat
 // Host
 // ---------------------------------------------------------------------------
 // k_rows for calls of at most so many rows, and rows times rank.  It reads an adapter for each row (from L2, mostly),
-// the tiles each adapter once: at 7168 x 7168 and 64 adapters 128 rows of rank 16 take 13 us against 36, 256 rows 23
-// against 39, 64 rows of rank 64 25 against 36, 128 rows 43 against 42; with few adapters 256 rows of rank 16 21 against
-// 20, one row of rank 128 12.5 against 19, 32 rows of it 30 against 30; 512 rows of 512 x 512, rank 8, 22 against 17.
+// the tiles each adapter once.  us, the tiles behind the stroke, by width (K = N), rows x rank and adapters:
+//              256 x 16, 64   256 x 16, 4   128 x 32, 64   64 x 64, 64   64 x 64, 4   32 x 128, 64   32 x 128, 4
+//   256        15 / 15        15 / 14       12 / 15        12 / 15       12 / 14      12 / 16        13 / 15
+//   1024       15 / 19        15 / 15       12 / 17        12 / 18       12 / 15      13 / 18        13 / 15
+//   2880       18 / 25        18 / 16       15 / 23        16 / 25       16 / 16      18 / 22        18 / 17
+//   7168       22 / 36        21 / 19       21 / 35        28 / 38       21 / 18      38 / 37        23 / 21
+// Above, single rows of many adapters would still be faster here (300 x 16, 64: 26 / 36 at 7168, 21 / 25 at 2880, but 18 / 15
+// at 256; 512 x 8, 64: 28 / 44, 24 / 28, 21 / 16), rows of few adapters not; how many rows an adapter has is not known here.
 constexpr int MOST_ROWS = 256;
 bool few_rows(int T, int r) { return T <= MOST_ROWS && (int64_t)T * r <= FEW_ROWS; }
 
@@ -1606,10 +1614,13 @@ decltype(&k_rows<8, 1, 1, 8>) rows_kernel(int T, int r, int& ctas) {
   return T * 8 <= 4 * sms ? k_rows<8, 4, 2, 4> : k_rows<8, 1, 1, 8>;
 }
 
-// The backward by k_rows and k_row_grads, for few rows per adapter, which a warp goes over one after the other; us, the
-// tiles behind "against": 64 rows of 7168 x 7168, 64 adapters of rank 16 16 against 50, of rank 64 57 against 90; one row
-// 7 against 22; 64 rows of 2880 x 2880, 8 adapters of rank 8 10 against 26; but 64 rows of one adapter of rank 16 23
-// against 21, of rank 64 68 against 22, of four of rank 64 37 against 28.
+// The backward by k_rows and k_row_grads, for few rows per adapter, which a warp goes over one after the other.  us as
+// above, 64 rows:
+//              rank 16, 64   rank 16, 8   rank 16, 2   rank 64, 64   rank 64, 8   rank 64, 4 (by tiles)
+//   256        9 / 25        10 / 20      15 / 19      17 / 27       21 / 22      27 / 22
+//   1024       9 / 29        10 / 21      15 / 19      18 / 41       21 / 22      27 / 22
+//   2880       12 / 35       11 / 23      16 / 21      31 / 45       26 / 25      31 / 23
+//   7168       16 / 52       13 / 29      17 / 24      56 / 90       32 / 32      37 / 27
 bool few_grads(int T, int r, int G) {
   return T <= GRAD_ROWS && (int64_t)T * r <= FEW_ROWS && (int64_t)T * r <= 512 * (int64_t)G;
 }
@@ -1713,13 +1724,10 @@ moe_status_t wgrad(const moe_bf16* x, const moe_bf16* us, int K, moe_bf16* dA, c
   // adapters of rank 128, 2440 to 256, 27 us instead of 51)
   const int zeros = G > T ? (int)((int64_t)(G - T) * r / MAX_R) : 0;
   const int split = split_of(bytes + 10 * 1024, units, max_tiles(T, G) + zeros);
-  // A programmatic dependent where both kernels' CTAs find an SM each (300 x 256 x 512 backward 19.8 us, 20.6 without).  With
-  // more, its first clusters took places as k_shrink left them, unevenly (8192 x 7168 154 us, 136 without).
-  const bool dependent = max_tiles(T, G) * shrink_split(T, N, r, G) + units * split <= sm_count();
   // (8192 x 7168 with 8 adapters of rank 64 61.8 us with BESIDE, 66.2 without; 512 rows of 64 adapters 69 and 58)
   const bool beside = rp <= 64 && T >= 64 * (int64_t)G;
   return launch(beside ? k_wgrad<true> : k_wgrad<false>, units * split, split, WGRAD_THREADS, bytes, wgrad_bytes(MAX_R),
-                dependent, s, sides, r, rp, G, p, places(T, G), g_wait_limit_ns.load(), st);
+                true, s, sides, r, rp, G, p, places(T, G), g_wait_limit_ns.load(), st);
 }
 
 moe_status_t expand(const moe_bf16* hs, const moe_bf16* Q, const moe_bf16* base, int T, int N, int r, int G, const Plan& p,
@@ -1844,7 +1852,7 @@ extern "C" moe_status_t moe_lora_bwd(const moe_bf16* dy, const moe_bf16* x, cons
   if (const moe_status_t e = group(idx, T, G, p, s)) return e;
   if (const moe_status_t e = shrink(dy, B, scale, T, N, r, G, p, nullptr, us, h, hs, status, s)) return e;
   // (the gradients next, while part of dy is in L2; k_expand, whose jobs any CTA takes, then fills the SMs that they leave:
-  // 8192 x 7168 with rank 32 126 us; dx before them 129)
+  // 8192 x 7168 with rank 32 122.7 us, rank 128 179; dx before them 122.7 and 184)
   if (const moe_status_t e = wgrad(x, us, K, dA, dy, hs, N, dB, T, r, G, p, status, s)) return e;
   return expand(us, A, base, T, K, r, G, p, dx, status, s);
 }
