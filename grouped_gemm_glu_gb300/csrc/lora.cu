@@ -33,7 +33,7 @@
 // the backward k_row_grads behind it.
 //
 // Measured, calls that follow one another: 8192 x 7168 with 32 adapters of rank
-// 16, forward 73.5 us (grouping 6; k_shrink 24, 117 MB at 4.9 TB/s, where a kernel
+// 16, forward 72 us (grouping 6; k_shrink 24, 117 MB at 4.9 TB/s, where a kernel
 // that only loads them takes 21; k_expand 43, 235 MB at 5.5 TB/s, where a plain
 // copy takes 38 to 40); with 8 of rank 32, backward 123 us (k_wgrad 48 for both
 // gradients, 4.9 TB/s); one row of 2880 4 us, 64 rows of 7168 with 64 adapters 8.2.
@@ -1055,7 +1055,7 @@ __device__ __forceinline__ uint32_t plus(uint32_t b, float x, float y) {
 constexpr int EXPAND_THREADS = 256;
 // Units in a job: two share the tile's h and its rows' numbers; forward of 8192 x 7168 with rank 16 73.8 us, one by one
 // 75.8, threes 74.6; rank 128 95.9, 108.7, 96.3; 4500 x 2880 x 5760 with rank 64 40.7, 43.5, 39.8; 512 rows of 64 adapters
-// of rank 16 39.0, 45.8, 38.2.  Ones while every unit has a CTA of its own (300 x 512: 14.2 us, twos 15.6).
+// of rank 16 39.0, 45.8, 38.2 (rank 16 without base ahead).  Ones while every unit has a CTA of its own (300 x 512: 14.2 us, twos 15.6).
 constexpr int expand_job(int64_t units, int ctas) { return units > ctas ? 2 : 1; }
 __host__ __device__ constexpr int expand_q(int rp) { return rp * 256; }
 // h's second part: beside the first in shared memory up to rank 32, where three CTAs per SM have room for both; in tensor
@@ -1063,15 +1063,14 @@ __host__ __device__ constexpr int expand_q(int rp) { return rp * 256; }
 // 43.5 us, so 40.7; 8192 x 7168 with rank 128 111.6 and 95.9; rank 32 in tensor memory 74.2, so 75.1, but 512 rows of 64
 // adapters 45.2 and 39.1).
 __host__ __device__ constexpr bool expand_lo_in_tmem(int rp) { return rp > 32; }
-// Units of base loaded ahead: where it costs no CTA of an SM (rank 64 at 8192 x 7168 80.8 us, 85.6 without; with rank 16,
-// where it would cost the third CTA, 72.4 against 73.6, but 512 rows of 64 adapters 43.0 against 38.9).
-__host__ __device__ constexpr int expand_ahead(int rp) { return rp > 32 && rp <= 64 ? 1 : 0; }
-constexpr int expand_bytes(int rp) {
-  return (1 + expand_ahead(rp)) * TILE * 256 + expand_q(rp) + (expand_lo_in_tmem(rp) ? 1 : 2) * TILE * rank_bytes(rp) + 1024;
+// Units of base loaded ahead: where it costs no CTA of an SM (rank 64 at 8192 x 7168 80.8 us, 85.6 without), and up to rank
+// 16, where it costs the third one, for adapters with many rows (8192 x 7168 72.4, 73.6 without; 512 rows of 64 adapters
+// 43.0 and 38.9).
+int expand_ahead(int rp, bool many) { return rp <= 16 ? many : rp > 32 && rp <= 64; }
+constexpr int expand_bytes(int rp, int ahead) {
+  return (1 + ahead) * TILE * 256 + expand_q(rp) + (expand_lo_in_tmem(rp) ? 1 : 2) * TILE * rank_bytes(rp) + 1024;
 }
-constexpr int expand_most(bool lo_in_tmem) {  // for any rank of the kind
-  return !lo_in_tmem ? expand_bytes(32) : expand_bytes(64) > expand_bytes(MAX_R) ? expand_bytes(64) : expand_bytes(MAX_R);
-}
+constexpr int EXPAND_MOST = expand_bytes(64, 1) > expand_bytes(MAX_R, 0) ? expand_bytes(64, 1) : expand_bytes(MAX_R, 0);
 
 template <bool LO_TMEM>
 __global__ void __launch_bounds__(EXPAND_THREADS, LO_TMEM ? 2 : 3) k_expand(const __grid_constant__ CUtensorMap mh,
@@ -1081,15 +1080,14 @@ __global__ void __launch_bounds__(EXPAND_THREADS, LO_TMEM ? 2 : 3) k_expand(cons
                                                               const __grid_constant__ CUtensorMap mb8,
                                                               const __grid_constant__ CUtensorMap my8,
                                                               const __nv_bfloat16* hs, const __nv_bfloat16* base, int N, int r,
-                                                              int rp, int job, Plan plan, int places, __nv_bfloat16* y,
-                                                              uint64_t limit_ns, int32_t* status) {
+                                                              int rp, int ahead, int job, Plan plan, int places,
+                                                              __nv_bfloat16* y, uint64_t limit_ns, int32_t* status) {
   extern __shared__ unsigned char smem_[];
   unsigned char* smem = aligned_smem(smem_);
   __shared__ uint64_t rows_in[2], product_in, lo_in, product_out;  // base's rows, h and Q in place; the MMAs' end
   __shared__ int abort_, taken[2];  // (the numbers of the jobs behind the next one, by turns)
   __shared__ uint32_t tmem_;
   const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31, slab = warp & 3, block = warp >> 2;
-  const int ahead = LO_TMEM ? expand_ahead(rp) : 0;
   constexpr uint32_t tmem_columns = LO_TMEM ? 2 * TILE : TILE;
   const uint32_t at = smem_u32(smem), q_at = at + (1 + ahead) * (TILE * 256), h_at = q_at + expand_q(rp);
   if (threadIdx.x == 0) {
@@ -1625,6 +1623,9 @@ bool few_grads(int T, int r, int G) {
   return T <= GRAD_ROWS && (int64_t)T * r <= FEW_ROWS && (int64_t)T * r <= 512 * (int64_t)G;
 }
 
+// Adapters with many rows each, on average at least.
+bool many_rows(int T, int G) { return T >= 64 * (int64_t)G; }
+
 size_t up256(size_t n) { return (n + 255) & ~(size_t)255; }
 int used_groups(int T, int G) { return G + 1 < T ? G + 1 : T; }             // at most, the rows without one among them
 int max_tiles(int T, int G) { return T / TILE + used_groups(T, G); }
@@ -1725,14 +1726,14 @@ moe_status_t wgrad(const moe_bf16* x, const moe_bf16* us, int K, moe_bf16* dA, c
   const int zeros = G > T ? (int)((int64_t)(G - T) * r / MAX_R) : 0;
   const int split = split_of(bytes + 10 * 1024, units, max_tiles(T, G) + zeros);
   // (8192 x 7168 with 8 adapters of rank 64 61.8 us with BESIDE, 66.2 without; 512 rows of 64 adapters 69 and 58)
-  const bool beside = rp <= 64 && T >= 64 * (int64_t)G;
+  const bool beside = rp <= 64 && many_rows(T, G);
   return launch(beside ? k_wgrad<true> : k_wgrad<false>, units * split, split, WGRAD_THREADS, bytes, wgrad_bytes(MAX_R),
                 true, s, sides, r, rp, G, p, places(T, G), g_wait_limit_ns.load(), st);
 }
 
 moe_status_t expand(const moe_bf16* hs, const moe_bf16* Q, const moe_bf16* base, int T, int N, int r, int G, const Plan& p,
                     moe_bf16* y, int32_t* st, cudaStream_t s) {
-  const int rp = pad16(r), sms = sm_count(), bytes = expand_bytes(rp);
+  const int rp = pad16(r), sms = sm_count(), ahead = expand_ahead(rp, many_rows(T, G)), bytes = expand_bytes(rp, ahead);
   if (sms < 1) return MOE_ERR_CUDA;
   const int64_t units = (int64_t)max_tiles(T, G) * ((N + TILE - 1) / TILE);
   const int per_sm = 228 * 1024 / (bytes + 2048) < 3 ? 228 * 1024 / (bytes + 2048) : 3;  // (registers: three)
@@ -1743,8 +1744,8 @@ moe_status_t expand(const moe_bf16* hs, const moe_bf16* Q, const moe_bf16* base,
       !map_rows(&mb8, base ? base : y, T, N, 64, 8) || !map_rows(&my8, y, T, N, 64, 8))
     return MOE_ERR_CUDA;
   const bool lo = expand_lo_in_tmem(rp);
-  return launch(lo ? k_expand<true> : k_expand<false>, grid, 0, EXPAND_THREADS, bytes, expand_most(lo), true, s, mh, mq, mb,
-                my, mb8, my8, in(hs), in(base), N, r, rp, job, p, places(T, G), out(y), g_wait_limit_ns.load(), st);
+  return launch(lo ? k_expand<true> : k_expand<false>, grid, 0, EXPAND_THREADS, bytes, EXPAND_MOST, true, s, mh, mq, mb,
+                my, mb8, my8, in(hs), in(base), N, r, rp, ahead, job, p, places(T, G), out(y), g_wait_limit_ns.load(), st);
 }
 
 moe_status_t rows_launch(const moe_bf16* x, const moe_bf16* P, const moe_bf16* Q, const int32_t* idx, const float* scale,
