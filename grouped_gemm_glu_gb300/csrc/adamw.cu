@@ -30,11 +30,11 @@
 // addresses (they differ from step to step) come as a kernel parameter.  The
 // norm and the step's scalars are kernels in front of it that it overlaps.
 //
-// Measured: 99.6 million bf16 weights in four tensors, clipped, 487 us: the
-// norm 47 (4.2 TB/s, while the step before still writes back), the step 438 (6.4
-// TB/s; a plain copy reaches 6.1).  With 8-bit moments 347 us, the step 303
-// (5.3 TB/s, with 83 instructions per element at 63% of the issue slots).
-// 95,000 weights 6.3 us.
+// Measured, a step per graph: 99.6 million bf16 weights in four tensors, clipped,
+// 483 us: the norm 47 (4.2 TB/s, while the step before still writes back), the
+// step 437 (6.4 TB/s; a plain copy reaches 6.1).  With 8-bit moments 352 us, the
+// step 303 (5.3 TB/s, with 83 instructions per element at 63% of the issue slots).
+// 95,000 weights 6.2 us.
 #include <cmath>
 
 #include "common.cuh"
