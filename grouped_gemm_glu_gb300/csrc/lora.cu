@@ -1364,6 +1364,7 @@ __global__ void __launch_bounds__(EXPAND_THREADS, LO_TMEM ? 2 : 3) k_expand(cons
     if (ahead) buf ^= 1;
   }
   cp_wait<0>();
+  if (LO_TMEM) tmem_wait_st();
   // (the last phase issued; that of a barrier without one counts as over)
   if (abort_ && lane == 0) {
     if (warp == 0)
