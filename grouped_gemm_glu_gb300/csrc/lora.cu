@@ -1055,7 +1055,8 @@ __device__ __forceinline__ uint32_t plus(uint32_t b, float x, float y) {
 constexpr int EXPAND_THREADS = 256;
 // Units in a job: two share the tile's h and its rows' numbers; forward of 8192 x 7168 with rank 16 73.8 us, one by one
 // 75.8, threes 74.6; rank 128 95.9, 108.7, 96.3; 4500 x 2880 x 5760 with rank 64 40.7, 43.5, 39.8; 512 rows of 64 adapters
-// of rank 16 39.0, 45.8, 38.2 (rank 16 without base ahead).  Ones while every unit has a CTA of its own (300 x 512: 14.2 us, twos 15.6).
+// of rank 16 39.0, 45.8, 38.2 (rank 16 without base ahead).  Ones while every unit has a CTA of its own (300 x 512: 14.2 us,
+// twos 15.6).
 constexpr int expand_job(int64_t units, int ctas) { return units > ctas ? 2 : 1; }
 __host__ __device__ constexpr int expand_q(int rp) { return rp * 256; }
 // h's second part: beside the first in shared memory up to rank 32, where three CTAs per SM have room for both; in tensor
